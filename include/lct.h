@@ -349,6 +349,40 @@ lct_status lct_adamw_step_fused(const lct_tensor *W_in, const lct_codebook *cbW,
                                 const uint16_t *d_g, const lct_adamw_params *p, const lct_tensor *W_out,
                                 const lct_tensor *M_out, const lct_tensor *V_out, void *stream);
 
+/* ---- gradients of many tensors: their global norm, and clipping -------- */
+
+typedef enum { LCT_DTYPE_BF16 = 0, LCT_DTYPE_F32 = 1 } lct_dtype;
+
+#define LCT_GRAD_WORK_BYTES 4864 /* device scratch of the two calls below */
+
+/* The global 2-norm of `count` gradients, *d_norm = sqrt(sum of g^2): the
+ * dense gradients that the fused steps take, or any other list.  (The pages
+ * have no counterpart.)  d_g, n and dtype are host arrays of `count` entries:
+ * device address (aligned to its values, so slices of a bucket are fine),
+ * values (0 is fine, the address is then not looked at) and lct_dtype, which
+ * may differ between tensors.  They are read before the call returns.
+ * d_work is LCT_GRAD_WORK_BYTES of scratch.  Partial sums are held in double
+ * and added in a fixed order: the result does not change from run to run, no
+ * square overflows or underflows, and only a norm above float's range is
+ * returned as infinity.  A NaN or an infinity among the values gives NaN or
+ * infinity.  count = 0 gives 0.
+ * Errors: LCT_ERR_INVALID_ARG (NULL or misaligned pointers, n > 2^40),
+ * LCT_ERR_UNSUPPORTED (another dtype), LCT_ERR_CUDA. */
+lct_status lct_grad_norm(const void *const *d_g, const uint64_t *n, const int32_t *dtype, uint64_t count,
+                         float *d_norm, void *d_work, void *stream);
+
+/* The same norm into *d_norm, and every gradient scaled by
+ *   c = min(1, max_norm / (norm + 1e-6))
+ * into d_out[i] (n[i] values of d_g[i]'s type, rounded once, to nearest even).
+ * d_out[i] is d_g[i] itself (in place) or apart from every gradient and every
+ * other output.  With c = 1 gradients in place are not touched.  c is NaN
+ * where the norm is NaN, and 0 where it is infinite (an infinity times 0 is
+ * NaN, a finite value 0): read *d_norm before a step to skip it.
+ * Errors: as lct_grad_norm, and LCT_ERR_INVALID_ARG for max_norm that is not
+ * positive and finite, or for overlapping tensors. */
+lct_status lct_grad_clip(const void *const *d_g, void *const *d_out, const uint64_t *n, const int32_t *dtype,
+                         uint64_t count, float max_norm, float *d_norm, void *d_work, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

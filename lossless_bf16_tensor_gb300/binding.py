@@ -33,6 +33,8 @@ LCT_MODEL_GAUSSIAN, LCT_MODEL_LAPLACE, LCT_MODEL_POWERLAW = 0, 1, 2
 LCT_LEVEL_CLEAN, LCT_LEVEL_MEDIUM, LCT_LEVEL_HIGH = 0, 1, 2
 LCT_HEADER_BYTES = 64
 LCT_STATIC_SCRATCH_BLOCKS = 16384
+LCT_DTYPE_BF16, LCT_DTYPE_F32 = 0, 1
+LCT_GRAD_WORK_BYTES = 4864
 LCT_MAGIC = 0x3154434C
 MODELS = {"gaussian": 0, "laplace": 1, "powerlaw": 2}
 LEVELS = {"CLEAN": 0, "MEDIUM": 1, "HIGH": 2}
@@ -99,7 +101,9 @@ _lib.lct_adamw_step_fused.argtypes = [ctypes.POINTER(lct_tensor), ctypes.POINTER
     ctypes.POINTER(lct_tensor), _P]
 _lib.lct_debug_wait_timeout.argtypes = [_P, _P, ctypes.c_uint64, _P]
 _lib.lct_encode_static_scratch.argtypes = [_P, ctypes.POINTER(lct_codebook), ctypes.POINTER(lct_tensor), _P]
-for _fn in ("lct_codebook_build", "lct_codebook_build_zero_atom", "lct_compressed_size", "lct_encode", "lct_decode",
+_lib.lct_grad_norm.argtypes = [_P, _P, _P, ctypes.c_uint64, _P, _P, _P]
+_lib.lct_grad_clip.argtypes = [_P, _P, _P, _P, ctypes.c_uint64, ctypes.c_float, _P, _P, _P]
+for _fn in ("lct_grad_norm", "lct_grad_clip", "lct_codebook_build", "lct_codebook_build_zero_atom", "lct_compressed_size", "lct_encode", "lct_decode",
             "lct_decode_blocks", "lct_sgd_step_fused",
             "lct_sgd_momentum_step_fused", "lct_adamw_step_fused", "lct_debug_wait_timeout",
             "lct_encode_static_scratch"):
@@ -219,6 +223,42 @@ def lct_adamw_step_fused(W_in: "CompressedTensor", cbW: lct_codebook, M_in: "Com
                                      ctypes.byref(cbM), ctypes.byref(V_in.desc), ctypes.byref(cbV), ptr,
                                      ctypes.byref(p), ctypes.byref(W_out.desc), ctypes.byref(M_out.desc),
                                      ctypes.byref(V_out.desc), _stream(stream)), "lct_adamw_step_fused")
+
+
+_GRAD_DTYPES = {torch.bfloat16: LCT_DTYPE_BF16, torch.float32: LCT_DTYPE_F32}
+
+
+class GradArrays:
+    """The host arrays of lct_grad_norm and lct_grad_clip for a list of CUDA
+    tensors (contiguous, BF16 or float32, all on one device)."""
+
+    def __init__(self, tensors, what: str = "gradients"):
+        for t in tensors:
+            if t.dtype not in _GRAD_DTYPES:
+                raise LctError(LCT_ERR_UNSUPPORTED, "%s: expected BF16 or float32, not %s" % (what, t.dtype))
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("%s: expected contiguous CUDA tensors" % what)
+        self.devices = {t.get_device() for t in tensors}
+        if len(self.devices) > 1:
+            raise ValueError("%s: expected tensors on one device" % what)
+        self.count = len(tensors)
+        self.ptr = np.array([t.data_ptr() for t in tensors], dtype=np.uint64)
+        self.n = np.array([t.numel() for t in tensors], dtype=np.uint64)
+        self.dtype = np.array([_GRAD_DTYPES[t.dtype] for t in tensors], dtype=np.int32)
+
+
+def lct_grad_norm(g: GradArrays, norm: torch.Tensor, work: torch.Tensor, stream=None) -> None:
+    _check(_lib.lct_grad_norm(g.ptr.ctypes.data, g.n.ctypes.data, g.dtype.ctypes.data, g.count, norm.data_ptr(),
+                              work.data_ptr(), _stream(stream)), "lct_grad_norm")
+
+
+def lct_grad_clip(g: GradArrays, out: GradArrays, max_norm: float, norm: torch.Tensor, work: torch.Tensor,
+                  stream=None) -> None:
+    if out.count != g.count or not np.array_equal(out.n, g.n) or not np.array_equal(out.dtype, g.dtype):
+        raise ValueError("out must match the gradients' sizes and types")
+    _check(_lib.lct_grad_clip(g.ptr.ctypes.data, out.ptr.ctypes.data, g.n.ctypes.data, g.dtype.ctypes.data, g.count,
+                              ctypes.c_float(max_norm), norm.data_ptr(), work.data_ptr(), _stream(stream)),
+           "lct_grad_clip")
 
 
 def lct_debug_wait_timeout(header: torch.Tensor, work: torch.Tensor, limit_ns: int, stream=None) -> None:

@@ -148,4 +148,19 @@ cudaError_t launch_block_offsets2(const DevTensor &t0, const DevTensor &t1, cuda
 cudaError_t launch_wait_probe(lct_header *hdr, unsigned long long *work, uint64_t wait_ns,
                               cudaStream_t s);
 
+
+// Gradients of one norm or clipping call (host arrays of device addresses).
+constexpr uint32_t kGradMaxParts = LCT_GRAD_WORK_BYTES / 8;
+struct GradArgs {
+    const void *const *src;
+    void *const *dst;  // NULL for a norm alone
+    const uint64_t *n;
+    const int32_t *dtype;
+    uint64_t count;
+    float max_norm;
+    float *norm;   // device
+    double *part;  // device, kGradMaxParts
+};
+cudaError_t launch_grads(const GradArgs &a, bool clip, cudaStream_t s);
+
 }  // namespace lct
