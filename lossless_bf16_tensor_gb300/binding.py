@@ -7,6 +7,7 @@ importing this module fails if the library has not been built
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -127,6 +128,28 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+class on_device:
+    """Makes `device` (an index, or None for the current one) the current
+    device for a block, at no cost where it already is; gives its index."""
+
+    def __init__(self, device):
+        self.device = device
+        self.before = None
+
+    def __enter__(self) -> int:
+        now = torch.cuda.current_device()
+        if self.device is None or self.device == now:
+            return now
+        torch.cuda.set_device(self.device)
+        self.before = now
+        return self.device
+
+    def __exit__(self, *exc):
+        if self.before is not None:
+            torch.cuda.set_device(self.before)
+        return False
+
+
 def _model(m) -> int:
     return MODELS[m] if isinstance(m, str) else int(m)
 
@@ -230,35 +253,40 @@ _GRAD_DTYPES = {torch.bfloat16: LCT_DTYPE_BF16, torch.float32: LCT_DTYPE_F32}
 
 class GradArrays:
     """The host arrays of lct_grad_norm and lct_grad_clip for a list of CUDA
-    tensors (contiguous, BF16 or float32, all on one device)."""
+    tensors (contiguous, BF16 or float32, all on one device), which it keeps
+    alive.  A list that stays the same from step to step can keep its arrays."""
 
     def __init__(self, tensors, what: str = "gradients"):
-        for t in tensors:
-            if t.dtype not in _GRAD_DTYPES:
-                raise LctError(LCT_ERR_UNSUPPORTED, "%s: expected BF16 or float32, not %s" % (what, t.dtype))
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError("%s: expected contiguous CUDA tensors" % what)
-        self.devices = {t.get_device() for t in tensors}
-        if len(self.devices) > 1:
-            raise ValueError("%s: expected tensors on one device" % what)
-        self.count = len(tensors)
-        self.ptr = np.array([t.data_ptr() for t in tensors], dtype=np.uint64)
-        self.n = np.array([t.numel() for t in tensors], dtype=np.uint64)
-        self.dtype = np.array([_GRAD_DTYPES[t.dtype] for t in tensors], dtype=np.int32)
+        self.tensors = ts = list(tensors)
+        devices = set(map(torch.Tensor.get_device, ts))
+        if -1 in devices or len(devices) > 1:
+            raise ValueError("%s: expected CUDA tensors on one device" % what)
+        if not all(map(torch.Tensor.is_contiguous, ts)):
+            raise ValueError("%s: expected contiguous tensors" % what)
+        try:
+            self.dtype = array.array("i", [_GRAD_DTYPES[t.dtype] for t in ts])
+        except KeyError as e:
+            raise LctError(LCT_ERR_UNSUPPORTED, "%s: expected BF16 or float32, not %s" % (what, e.args[0])) from None
+        self.device = devices.pop() if devices else None
+        self.count = len(ts)
+        self.ptr = array.array("Q", list(map(torch.Tensor.data_ptr, ts)))
+        self.n = array.array("Q", list(map(torch.Tensor.numel, ts)))
+
+    def args(self):
+        return self.n.buffer_info()[0], self.dtype.buffer_info()[0], self.count
 
 
 def lct_grad_norm(g: GradArrays, norm: torch.Tensor, work: torch.Tensor, stream=None) -> None:
-    _check(_lib.lct_grad_norm(g.ptr.ctypes.data, g.n.ctypes.data, g.dtype.ctypes.data, g.count, norm.data_ptr(),
-                              work.data_ptr(), _stream(stream)), "lct_grad_norm")
+    _check(_lib.lct_grad_norm(g.ptr.buffer_info()[0], *g.args(), norm.data_ptr(), work.data_ptr(), _stream(stream)),
+           "lct_grad_norm")
 
 
 def lct_grad_clip(g: GradArrays, out: GradArrays, max_norm: float, norm: torch.Tensor, work: torch.Tensor,
                   stream=None) -> None:
-    if out.count != g.count or not np.array_equal(out.n, g.n) or not np.array_equal(out.dtype, g.dtype):
+    if out is not g and (out.n != g.n or out.dtype != g.dtype):
         raise ValueError("out must match the gradients' sizes and types")
-    _check(_lib.lct_grad_clip(g.ptr.ctypes.data, out.ptr.ctypes.data, g.n.ctypes.data, g.dtype.ctypes.data, g.count,
-                              ctypes.c_float(max_norm), norm.data_ptr(), work.data_ptr(), _stream(stream)),
-           "lct_grad_clip")
+    _check(_lib.lct_grad_clip(g.ptr.buffer_info()[0], out.ptr.buffer_info()[0], *g.args(), max_norm, norm.data_ptr(),
+                              work.data_ptr(), _stream(stream)), "lct_grad_clip")
 
 
 def lct_debug_wait_timeout(header: torch.Tensor, work: torch.Tensor, limit_ns: int, stream=None) -> None:

@@ -10,14 +10,16 @@
 // table to the device and keeps nothing between calls.  The tensors are cut
 // into units of 256 16-byte vectors, counted from the aligned address at or
 // below a tensor's first value, and every block takes an equal contiguous
-// range of units, whatever the tensors' sizes: one binary search a block
-// finds its first tensor.
+// range of units, whatever the tensors' sizes.  The host says with which
+// tensor a block begins: a search by the block would be a chain of reads of
+// parameters that no cache holds yet.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <vector>
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -27,6 +29,8 @@ namespace dev {
 
 constexpr int kGradThreads = 256;
 constexpr int kGradUnroll = 8;  // vectors a thread holds at once
+constexpr int kGradBlocksPerSm = 4;
+constexpr int kGradCluster = 8;
 
 // One tensor of a launch.  n counts values; bit 63 says they are float32.
 struct GradEntry {
@@ -38,14 +42,15 @@ struct GradTable {
     GradEntry e[CAP];
     uint32_t first[CAP + 1];  // units before tensor i; entry `count` is their total
     uint32_t count;
+    uint16_t start[kGradMaxParts];  // the tensor that holds block i's first unit
 };
 
 constexpr unsigned long long kF32Bit = 1ull << 63;
 
 struct Span {
     unsigned long long src, dst;  // aligned down to 16 bytes
-    unsigned long long lo, hi;    // bytes of the tensor, counted from src
-    unsigned long long nvec;
+    unsigned long long hi;        // the tensor's bytes are lo..hi, counted from src
+    uint32_t lo;
     bool f32;
     bool same_phase;              // dst lies like src within a vector
 };
@@ -55,12 +60,11 @@ __device__ __forceinline__ Span span_of(const GradEntry &e)
     Span s;
     s.f32 = (e.n & kF32Bit) != 0;
     const unsigned long long n = e.n & ~kF32Bit;
-    s.lo = e.src & 15ull;
+    s.lo = static_cast<uint32_t>(e.src & 15ull);
     s.hi = s.lo + n * (s.f32 ? 4 : 2);
     s.src = e.src - s.lo;
     s.same_phase = ((e.src ^ e.dst) & 15ull) == 0;
     s.dst = e.dst - s.lo;
-    s.nvec = (s.hi + 15) / 16;
     return s;
 }
 
@@ -106,42 +110,29 @@ __device__ __forceinline__ T squares(const uint4 &v, bool f32, T acc)
     return acc;
 }
 
-// The sum of squares of a thread's vectors.  A float sum of at most 64
-// squares is within 64 * 2^-24 of them in the worst order; it is used where
-// it lies well inside float's range, and anything else (an overflow, squares
-// that underflow, infinities and NaN) is summed again in double from the
-// registers.  A sum of zeros alone stays zero.
-__device__ __forceinline__ double sum_vectors(const uint4 (&v)[kGradUnroll], bool f32)
+// The sum of squares of a thread's vectors; bit i of f32 says that vector i
+// holds float32 values.  A float sum of at most 64 squares is within 64 *
+// 2^-24 of them in the worst order; it is used where it lies well inside
+// float's range, and anything else (an overflow, squares that underflow,
+// infinities and NaN) is summed again in double from the registers.  A sum of
+// zeros alone stays zero.
+__device__ __forceinline__ double sum_vectors(const uint4 (&v)[kGradUnroll], uint32_t f32)
 {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     uint32_t any = 0;
 #pragma unroll
     for (int i = 0; i < kGradUnroll; ++i) {
-        s[i & 3] = squares<float>(v[i], f32, s[i & 3]);
+        s[i & 3] = squares<float>(v[i], (f32 >> i) & 1, s[i & 3]);
         any |= v[i].x | v[i].y | v[i].z | v[i].w;
     }
     const float t = (s[0] + s[1]) + (s[2] + s[3]);
     if (t > 0x1p-60f && t < 0x1p120f) return static_cast<double>(t);
     double d = 0.0;
-    if (any & (f32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) {
+    if (any) {
 #pragma unroll
-        for (int i = 0; i < kGradUnroll; ++i) d = squares<double>(v[i], f32, d);
+        for (int i = 0; i < kGradUnroll; ++i) d = squares<double>(v[i], (f32 >> i) & 1, d);
     }
     return d;
-}
-
-template <int CAP>
-__device__ __forceinline__ uint32_t find_entry(const GradTable<CAP> &t, uint32_t unit)
-{
-    uint32_t lo = 0, hi = t.count;  // the last i with first[i] <= unit and some units
-    while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (t.first[mid] <= unit)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
 }
 
 // Block sum of one double a thread, in a fixed order; every thread gets it.
@@ -159,32 +150,48 @@ __device__ __forceinline__ double block_sum(double v, double *sh)
     return t;
 }
 
-__device__ __forceinline__ uint32_t range_at(uint32_t units, uint32_t block, uint32_t blocks)
+__host__ __device__ __forceinline__ uint32_t range_at(uint32_t units, uint32_t block, uint32_t blocks)
 {
     return static_cast<uint32_t>(static_cast<unsigned long long>(units) * block / blocks);
 }
 
+// The sum over units lo..hi of one launch, eight at a time: eight of one
+// tensor with one set of addresses, and eight that several tensors share (a
+// list of small ones) with a set each, so that their loads are still in
+// flight together.
 template <int CAP>
 __device__ __forceinline__ double sum_units(const GradTable<CAP> &t, uint32_t lo, uint32_t hi)
 {
     double acc = 0.0;
-    uint32_t e = lo < hi ? find_entry(t, lo) : 0;
-    for (uint32_t u = lo; u < hi;) {
+    uint32_t e = t.start[blockIdx.x];
+    for (uint32_t u = lo; u < hi; u += kGradUnroll) {
+        uint4 v[kGradUnroll];
+        uint32_t f32 = 0;
         while (u >= t.first[e + 1]) ++e;
-        const Span s = span_of(t.e[e]);
-        const uint32_t end = min(hi, t.first[e + 1]), base = t.first[e];
-        for (; u < end; u += kGradUnroll) {
-            const uint32_t count = min(end - u, static_cast<uint32_t>(kGradUnroll));
-            const unsigned long long v0 = static_cast<unsigned long long>(u - base) * kGradThreads + threadIdx.x;
-            uint4 v[kGradUnroll];
+        if (u + kGradUnroll <= min(hi, t.first[e + 1])) {
+            const Span s = span_of(t.e[e]);
+            const unsigned long long v0 = static_cast<unsigned long long>(u - t.first[e]) * kGradThreads + threadIdx.x;
 #pragma unroll
             for (int i = 0; i < kGradUnroll; ++i) {
-                const unsigned long long at = v0 + static_cast<unsigned long long>(i) * kGradThreads;
-                v[i] = i < count && at < s.nvec ? load_vec(s, at) : make_uint4(0, 0, 0, 0);
+                const unsigned long long at = v0 + i * kGradThreads;
+                v[i] = at * 16 < s.hi ? load_vec(s, at) : make_uint4(0, 0, 0, 0);
             }
-            acc += sum_vectors(v, s.f32);
+            f32 = s.f32 ? 0xFFu : 0u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kGradUnroll; ++i) {
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (u + i < hi) {
+                    while (u + i >= t.first[e + 1]) ++e;
+                    const Span s = span_of(t.e[e]);
+                    const unsigned long long at =
+                        static_cast<unsigned long long>(u + i - t.first[e]) * kGradThreads + threadIdx.x;
+                    if (at * 16 < s.hi) v[i] = load_vec(s, at);
+                    f32 |= static_cast<uint32_t>(s.f32) << i;
+                }
+            }
         }
-        u = end;
+        acc += sum_vectors(v, f32);
     }
     return acc;
 }
@@ -192,10 +199,12 @@ __device__ __forceinline__ double sum_units(const GradTable<CAP> &t, uint32_t lo
 // Partial sums of one launch's tensors, one a block.  `add` is set on a later
 // launch over more tensors, which adds to the first one's partial sums.
 template <int CAP>
-__global__ void __launch_bounds__(kGradThreads) k_grad_sum(const __grid_constant__ GradTable<CAP> t, double *part,
-                                                           uint32_t add)
+__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
+    k_grad_sum(const __grid_constant__ GradTable<CAP> t, double *part, uint32_t add)
 {
     __shared__ double sh[kGradThreads / 32];
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
     const uint32_t units = t.first[t.count];
     const double acc = sum_units(t, range_at(units, blockIdx.x, gridDim.x), range_at(units, blockIdx.x + 1, gridDim.x));
     const double total = block_sum<kGradThreads>(acc, sh);
@@ -212,6 +221,7 @@ __device__ __forceinline__ double total_of(const double *part, uint32_t parts, d
 __global__ void __launch_bounds__(kGradThreads) k_grad_norm(const double *part, uint32_t parts, float *norm)
 {
     __shared__ double sh[kGradThreads / 32];
+    cudaGridDependencySynchronize();
     const double total = total_of(part, parts, sh);
     if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(total));
 }
@@ -255,7 +265,7 @@ __device__ __forceinline__ void store_vec(const Span &s, unsigned long long v, c
 {
     const unsigned long long at = v * 16;
     if (s.same_phase && at >= s.lo && at + 16 <= s.hi) {
-        *reinterpret_cast<uint4 *>(s.dst + at) = x;
+        __stcs(reinterpret_cast<uint4 *>(s.dst + at), x);  // not to push out of L2 what is still to be read
         return;
     }
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -271,49 +281,108 @@ __device__ __forceinline__ void store_vec(const Span &s, unsigned long long v, c
     }
 }
 
-// The scaling pass over units lo..hi, last unit first: what the summing pass
-// read last is what L2 still holds.
+// A step of the scaling pass: the (at most eight) units before `end`, of one
+// tensor.
+struct Step {
+    Span s;
+    unsigned long long v0;
+    uint32_t count;
+    bool skip;
+    uint4 v[kGradUnroll];
+};
+
+// The step before unit `end` of a range that begins at lo; e falls to the
+// tensor that holds unit end - 1.
 template <int CAP>
-__device__ __forceinline__ void scale_units(const GradTable<CAP> &t, uint32_t lo, uint32_t hi, const Factor &f)
+__device__ __forceinline__ void load_step(const GradTable<CAP> &t, uint32_t lo, uint32_t end, uint32_t &e, bool one, Step &p)
 {
-    uint32_t e = lo < hi ? find_entry(t, hi - 1) : 0;
+    while (t.first[e] >= end) --e;
+    p.s = span_of(t.e[e]);
+    p.skip = one && t.e[e].src == t.e[e].dst;  // nothing changes in place
+    const uint32_t base = t.first[e];
+    p.count = min(end - max(lo, base), static_cast<uint32_t>(kGradUnroll));
+    p.v0 = static_cast<unsigned long long>(end - p.count - base) * kGradThreads + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kGradUnroll; ++i) {
+        const unsigned long long at = p.v0 + i * kGradThreads;
+        if (!p.skip && i < p.count && at * 16 < p.s.hi) p.v[i] = load_vec(p.s, at);
+    }
+}
+
+__device__ __forceinline__ void store_step(const Step &p, const Factor &f)
+{
+    if (p.skip) return;
+#pragma unroll
+    for (int i = 0; i < kGradUnroll; ++i) {
+        const unsigned long long at = p.v0 + i * kGradThreads;
+        if (i < p.count && at * 16 < p.s.hi) store_vec(p.s, at, scale_vec(p.v[i], p.s.f32, f));
+    }
+}
+
+// The scaling pass over units lo..hi, last unit first: what the summing pass
+// read last is what L2 still holds.  The first step is loaded by the caller.
+template <int CAP>
+__device__ __forceinline__ void scale_units(const GradTable<CAP> &t, uint32_t lo, uint32_t hi, uint32_t e, Step &p,
+                                            const Factor &f)
+{
     for (uint32_t end = hi; end > lo;) {
-        while (t.first[e] >= end) --e;
-        const Span s = span_of(t.e[e]);
-        const uint32_t base = t.first[e], begin = max(lo, base);
-        const bool skip = f.one && t.e[e].src == t.e[e].dst;
-        while (!skip && end > begin) {
-            const uint32_t count = min(end - begin, static_cast<uint32_t>(kGradUnroll));
-            const uint32_t u = end - count;
-            const unsigned long long v0 = static_cast<unsigned long long>(u - base) * kGradThreads + threadIdx.x;
-            uint4 v[kGradUnroll];
-#pragma unroll
-            for (int i = 0; i < kGradUnroll; ++i) {
-                const unsigned long long at = v0 + static_cast<unsigned long long>(i) * kGradThreads;
-                if (i < count && at < s.nvec) v[i] = load_vec(s, at);
-            }
-#pragma unroll
-            for (int i = 0; i < kGradUnroll; ++i) {
-                const unsigned long long at = v0 + static_cast<unsigned long long>(i) * kGradThreads;
-                if (i < count && at < s.nvec) store_vec(s, at, scale_vec(v[i], s.f32, f));
-            }
-            end = u;
-        }
-        end = begin;
+        store_step(p, f);
+        end -= p.count;
+        if (end > lo) load_step(t, lo, end, e, f.one, p);
     }
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kGradThreads) k_grad_scale(const __grid_constant__ GradTable<CAP> t,
+__device__ __forceinline__ uint32_t last_entry(const GradTable<CAP> &t)
+{
+    return blockIdx.x + 1 < gridDim.x ? t.start[blockIdx.x + 1] : t.count - 1;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) k_grad_scale(const __grid_constant__ GradTable<CAP> t,
                                                              const double *part, uint32_t parts, float max_norm,
                                                              float *norm)
 {
     __shared__ double sh[kGradThreads / 32];
+    const uint32_t units = t.first[t.count];
+    const uint32_t lo = range_at(units, blockIdx.x, gridDim.x), hi = range_at(units, blockIdx.x + 1, gridDim.x);
+    // the summing pass wrote no gradient, so the first step's need not wait for it
+    uint32_t e = last_entry(t);
+    Step p;
+    if (lo < hi) load_step(t, lo, hi, e, false, p);
+    cudaGridDependencySynchronize();
     const double total = total_of(part, parts, sh);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(sqrt(total));
-    const Factor f = factor_of(total, max_norm);
+    scale_units(t, lo, hi, e, p, factor_of(total, max_norm));
+}
+
+// Norm and, for CLIP, scaling in one launch of one cluster: a few units, where
+// a second launch would cost as much as the work.
+template <int CAP, bool CLIP>
+__global__ void __launch_bounds__(kGradThreads) k_grad_cluster(const __grid_constant__ GradTable<CAP> t,
+                                                               float max_norm, float *norm)
+{
+    namespace cg = cooperative_groups;
+    __shared__ double sh[kGradThreads / 32];
+    __shared__ double mine;
+    cg::cluster_group cluster = cg::this_cluster();
     const uint32_t units = t.first[t.count];
-    scale_units(t, range_at(units, blockIdx.x, gridDim.x), range_at(units, blockIdx.x + 1, gridDim.x), f);
+    const uint32_t lo = range_at(units, blockIdx.x, gridDim.x), hi = range_at(units, blockIdx.x + 1, gridDim.x);
+    const double acc = block_sum<kGradThreads>(sum_units(t, lo, hi), sh);
+    if (threadIdx.x == 0) mine = acc;
+    cluster.sync();
+    double total = 0.0;
+#pragma unroll
+    for (int i = 0; i < kGradCluster; ++i) total += *cluster.map_shared_rank(&mine, i);
+    cluster.sync();  // no block leaves while its sum is read
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(sqrt(total));
+    if (CLIP && lo < hi) {
+        uint32_t e = last_entry(t);
+        Step p;
+        const Factor f = factor_of(total, max_norm);
+        load_step(t, lo, hi, e, f.one, p);
+        scale_units(t, lo, hi, e, p, f);
+    }
 }
 
 }  // namespace dev
@@ -323,7 +392,8 @@ namespace {
 using dev::GradEntry;
 using dev::GradTable;
 
-constexpr int kCapSmall = 64, kCapLarge = 1024;
+constexpr int kCapSmall = 64, kCapMiddle = 384, kCapLarge = 1024;
+constexpr uint32_t kClusterUnits = 64;
 
 uint64_t units_of(uint64_t src, uint64_t bytes)
 {
@@ -362,33 +432,80 @@ uint32_t grad_grid(uint32_t units)
     return std::max(1u, std::min(want, static_cast<uint32_t>(kGradMaxParts)));
 }
 
+// Says with which tensor each block of a grid begins.
+template <int CAP>
+void set_starts(GradTable<CAP> *t, uint32_t grid)
+{
+    uint32_t e = 0;
+    for (uint32_t b = 0; b < grid; ++b) {
+        const uint32_t u = dev::range_at(t->first[t->count], b, grid);
+        while (e + 1 < t->count && u >= t->first[e + 1]) ++e;
+        t->start[b] = static_cast<uint16_t>(e);
+    }
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), uint32_t grid, uint32_t cluster, bool dependent, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(dev::kGradThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    if (cluster > 1) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = cluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    } else if (dependent) {  // its blocks may start while the launch before it ends, and wait for it themselves
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int CAP>
 cudaError_t run_tables(const GradArgs &a, bool clip, cudaStream_t s)
 {
     GradTable<CAP> t;
-    uint32_t parts = 0;
+    uint32_t parts = 0, tables = 0;
     cudaError_t rc;
     uint64_t at = 0;
     do {
         at = fill_table(a, at, &t);
-        // a later launch adds to the first one's partial sums, so it has no more blocks than that
-        const uint32_t grid = parts ? parts : (at < a.count ? kGradMaxParts : grad_grid(t.first[t.count]));
-        dev::k_grad_sum<CAP><<<grid, dev::kGradThreads, 0, s>>>(t, a.part, parts ? 1u : 0u);
-        if ((rc = cudaGetLastError()) != cudaSuccess) return rc;
+        const uint32_t units = t.first[t.count];
+        if (!parts && at == a.count && units <= kClusterUnits) {
+            set_starts(&t, dev::kGradCluster);
+            return clip ? launch(dev::k_grad_cluster<CAP, true>, dev::kGradCluster, dev::kGradCluster, false, s, t,
+                                 a.max_norm, a.norm)
+                        : launch(dev::k_grad_cluster<CAP, false>, dev::kGradCluster, dev::kGradCluster, false, s, t,
+                                 a.max_norm, a.norm);
+        }
+        // a later launch adds to the first one's partial sums, so it has as many blocks as that
+        const uint32_t grid = parts ? parts : (at < a.count ? kGradMaxParts : grad_grid(units));
+        set_starts(&t, grid);
+        if ((rc = launch(dev::k_grad_sum<CAP>, grid, 1, parts != 0, s, t, a.part, parts ? 1u : 0u)) != cudaSuccess)
+            return rc;
         parts = grid;
+        ++tables;
     } while (at < a.count);
-    if (!clip) {
-        dev::k_grad_norm<<<1, dev::kGradThreads, 0, s>>>(a.part, parts, a.norm);
-        return cudaGetLastError();
-    }
+    if (!clip) return launch(dev::k_grad_norm, 1, 1, true, s, static_cast<const double *>(a.part), parts, a.norm);
     at = 0;
     bool first = true;
     do {
-        at = fill_table(a, at, &t);
-        const uint32_t grid = at < a.count || !first ? kGradMaxParts : grad_grid(t.first[t.count]);
-        dev::k_grad_scale<CAP><<<grid, dev::kGradThreads, 0, s>>>(t, a.part, parts, a.max_norm,
-                                                                  first ? a.norm : nullptr);
-        if ((rc = cudaGetLastError()) != cudaSuccess) return rc;
+        // a single table still lies in t, starts and all
+        if (tables > 1) at = fill_table(a, at, &t);
+        const uint32_t grid = tables > 1 ? kGradMaxParts : parts;
+        if (tables > 1)
+            set_starts(&t, grid);
+        else
+            at = a.count;
+        if ((rc = launch(dev::k_grad_scale<CAP>, grid, 1, first, s, t, static_cast<const double *>(a.part), parts,
+                         a.max_norm, first ? a.norm : nullptr)) != cudaSuccess)
+            return rc;
         first = false;
     } while (at < a.count);
     return cudaSuccess;
@@ -398,7 +515,8 @@ cudaError_t run_tables(const GradArgs &a, bool clip, cudaStream_t s)
 
 cudaError_t launch_grads(const GradArgs &a, bool clip, cudaStream_t s)
 {
-    return a.count <= kCapSmall ? run_tables<kCapSmall>(a, clip, s) : run_tables<kCapLarge>(a, clip, s);
+    if (a.count <= kCapSmall) return run_tables<kCapSmall>(a, clip, s);
+    return a.count <= kCapMiddle ? run_tables<kCapMiddle>(a, clip, s) : run_tables<kCapLarge>(a, clip, s);
 }
 
 namespace {

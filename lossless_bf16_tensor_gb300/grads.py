@@ -5,7 +5,9 @@ optimizer steps that take them (``lct_sgd_momentum_step_fused``,
     norm = clip_grads([p.grad for p in params], max_norm=1.0)
 
 Only orchestration lives here: the sums and the scaling run in liblct's
-kernels, on the current stream, and nothing synchronises.
+kernels, on the current stream, and nothing synchronises.  Gradients that stay
+in the same buffers from step to step may be given as one ``GradArrays``, which
+spares the collecting of their addresses.
 """
 from __future__ import annotations
 
@@ -13,20 +15,26 @@ import torch
 
 from . import binding as B
 
-
-def _scratch(g: B.GradArrays, device) -> tuple[torch.Tensor, torch.Tensor]:
-    if device is None:
-        device = torch.device("cuda", next(iter(g.devices)) if g.devices else torch.cuda.current_device())
-    work = torch.empty(B.LCT_GRAD_WORK_BYTES, dtype=torch.uint8, device=device)
-    return torch.empty((), dtype=torch.float32, device=device), work
+_SCRATCH = B.LCT_GRAD_WORK_BYTES // 4
 
 
-def grad_norm(grads, device=None) -> torch.Tensor:
+def _arrays(tensors, what: str) -> B.GradArrays:
+    return tensors if isinstance(tensors, B.GradArrays) else B.GradArrays(tensors, what)
+
+
+def _buffers(device: int) -> tuple[torch.Tensor, torch.Tensor]:
+    """The norm and the calls' scratch, from one allocation."""
+    buf = torch.empty(_SCRATCH + 4, dtype=torch.float32, device=torch.device("cuda", device))
+    return buf[_SCRATCH], buf
+
+
+def grad_norm(grads) -> torch.Tensor:
     """sqrt(sum of g^2) over every value of `grads` (contiguous BF16 or float32
-    CUDA tensors), a float32 scalar on the device.  An empty list gives 0."""
-    g = B.GradArrays(grads)
-    norm, work = _scratch(g, device)
-    with torch.cuda.device(norm.device):
+    CUDA tensors on one device), a float32 scalar there.  An empty list gives
+    0."""
+    g = _arrays(grads, "gradients")
+    with B.on_device(g.device) as device:
+        norm, work = _buffers(device)
         B.lct_grad_norm(g, norm, work)
     return norm
 
@@ -35,11 +43,11 @@ def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
     """Scale every gradient by min(1, max_norm / (norm + 1e-6)), in place or
     into `out` (tensors of the same sizes and types); returns the norm before
     clipping, a float32 scalar on the device."""
-    g = B.GradArrays(grads)
-    o = g if out is None else B.GradArrays(out, "out")
-    if o.devices != g.devices:
+    g = _arrays(grads, "gradients")
+    o = g if out is None else _arrays(out, "out")
+    if o.device != g.device:
         raise ValueError("out must be on the gradients' device")
-    norm, work = _scratch(g, None)
-    with torch.cuda.device(norm.device):
+    with B.on_device(g.device) as device:
+        norm, work = _buffers(device)
         B.lct_grad_clip(g, o, max_norm, norm, work)
     return norm
