@@ -383,6 +383,88 @@ lct_status lct_grad_norm(const void *const *d_g, const uint64_t *n, const int32_
 lct_status lct_grad_clip(const void *const *d_g, void *const *d_out, const uint64_t *n, const int32_t *dtype,
                          uint64_t count, float max_norm, float *d_norm, void *d_work, void *stream);
 
+/* ---- low-rank adapters of many requests beside a shared projection ------ */
+
+#define LCT_ADAPTER_TILE 128           /* tokens in a tile of a plan */
+#define LCT_ADAPTER_MAX_RANK 128
+#define LCT_ADAPTER_MAX 16384          /* adapters in a bank */
+#define LCT_ADAPTER_MAX_TOKENS (1 << 24)
+#define LCT_ADAPTER_MAX_COLS (1 << 20) /* columns of x and of y */
+/* rows of a plan's tile table (at least one) */
+#define LCT_ADAPTER_TILE_ROWS(tokens, adapters)                                                            \
+    ((tokens) == 0 ? 1ull                                                                                  \
+                   : ((uint64_t)(tokens) + LCT_ADAPTER_TILE - 1) / LCT_ADAPTER_TILE +                      \
+                         ((uint64_t)(adapters) + 1 < (uint64_t)(tokens) ? (uint64_t)(adapters) + 1         \
+                                                                        : (uint64_t)(tokens)))
+/* scratch of lct_adapter_backward */
+#define LCT_ADAPTER_WORK_BYTES(tokens, rank) (8ull * (tokens) * (((rank) + 15ull) / 16 * 16))
+
+/* A bank of adapters for one projection of k to n columns (caller-owned
+ * device memory, BF16, row-major): adapter a adds s_a (x A_a^T) B_a^T.  It uses
+ * the first d_ranks[a] (clamped to 0..rank) rows of A_a and columns of B_a; the
+ * others are not read.  d_ranks NULL: all of them. */
+typedef struct {
+    const uint16_t *d_a;     /* [adapters][rank][k] */
+    const uint16_t *d_b;     /* [adapters][n][rank] */
+    const float *d_scale;    /* [adapters] */
+    const int32_t *d_ranks;  /* [adapters] or NULL */
+    uint64_t adapters, rank, k, n;
+} lct_adapters;
+
+/* The grouping of a batch's tokens by adapter, from lct_adapter_plan: made
+ * once for a batch and used for every projection in it.  Every entry is
+ * trusted by the calls below (indices are the plan's own). */
+typedef struct {
+    const int32_t *d_order;  /* [tokens]: tokens in stable order of their adapter, those without one last */
+    const int32_t *d_starts; /* [adapters + 2]: where each adapter's tokens begin; without one; tokens */
+    int32_t *d_tiles;        /* [LCT_ADAPTER_TILE_ROWS][4], 16-byte aligned: adapter (-1: none), first place
+                                in the order, tokens (1..128, 0: unused row), 0; the first row's fourth
+                                value is the plan's status (an lct_status) */
+    uint64_t tokens, adapters;
+} lct_token_plan;
+
+/* Fill the three tables of a plan from each token's adapter, d_index[tokens]
+ * (-1: none).  (The pages have no counterpart.)  An index outside -1 ..
+ * adapters - 1 counts as none and latches LCT_ERR_INVALID_ARG in the plan's
+ * status.  Errors: LCT_ERR_INVALID_ARG (NULL or misaligned pointers, no
+ * adapters, overlapping tables), LCT_ERR_UNSUPPORTED (more adapters or tokens
+ * than the limits above), LCT_ERR_CUDA. */
+lct_status lct_adapter_plan(const int32_t *d_index, uint64_t tokens, uint64_t adapters, int32_t *d_order,
+                            int32_t *d_starts, int32_t *d_tiles, void *stream);
+
+/* out = y + s_a (x A_a^T) B_a^T for every token, out = y where it has no
+ * adapter: what many requests' adapters add to y, the shared projection of
+ * the same x.  x [tokens, k], y and out [tokens, n] are BF16 with rows ld_*
+ * values apart; out may be y itself.  Rows that begin at 16-byte boundaries
+ * are the fast case, others work.  The sums are float32, the narrow product is
+ * carried to the second one with 16 bits, and out is rounded once.  d_xa, if
+ * not NULL, gets x A_a^T [tokens, rank] in float32 (0 where an adapter has no
+ * such rank) for lct_adapter_backward.  A wait that ran out on the device
+ * latches LCT_ERR_TIMEOUT in the plan's status.  Errors: LCT_ERR_INVALID_ARG
+ * (NULL or misaligned pointers, strides below the widths, a plan for another
+ * number of adapters, an output that overlaps another operand),
+ * LCT_ERR_UNSUPPORTED (rank above LCT_ADAPTER_MAX_RANK or another limit),
+ * LCT_ERR_CUDA. */
+lct_status lct_adapter_forward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_x,
+                               uint64_t ld_x, const uint16_t *d_y, uint64_t ld_y, uint16_t *d_out, uint64_t ld_out,
+                               float *d_xa, void *stream);
+
+/* The gradients of lct_adapter_forward for dy, the gradient of out (which is
+ * also that of y): with d = s_a dy B_a,
+ *   dx_out = dx + d A_a        (dx: the shared projection's part; dx_out may be dx itself)
+ *   dA_a = sum over a's tokens of d^T x
+ *   dB_a = sum over a's tokens of s_a dy^T (x A_a^T)
+ * in BF16, each rounded once; gradients of unused ranks and adapters are 0.
+ * x and d_xa are the forward pass's.  d_dx_out NULL leaves dx out; d_da and
+ * d_db NULL (both) leave the bank's gradients out, and x, d_xa and d_work are
+ * then not looked at.  d_work: LCT_ADAPTER_WORK_BYTES of scratch, 16-byte
+ * aligned.  Sums over tokens are added in a fixed order.  Errors as
+ * lct_adapter_forward. */
+lct_status lct_adapter_backward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_dy,
+                                uint64_t ld_dy, const uint16_t *d_x, uint64_t ld_x, const float *d_xa,
+                                const uint16_t *d_dx, uint64_t ld_dx, uint16_t *d_dx_out, uint64_t ld_dx_out,
+                                uint16_t *d_da, uint16_t *d_db, void *d_work, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

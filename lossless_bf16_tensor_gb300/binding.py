@@ -36,6 +36,7 @@ LCT_HEADER_BYTES = 64
 LCT_STATIC_SCRATCH_BLOCKS = 16384
 LCT_DTYPE_BF16, LCT_DTYPE_F32 = 0, 1
 LCT_GRAD_WORK_BYTES = 4864
+LCT_ADAPTER_TILE, LCT_ADAPTER_MAX_RANK, LCT_ADAPTER_MAX = 128, 128, 16384
 LCT_MAGIC = 0x3154434C
 MODELS = {"gaussian": 0, "laplace": 1, "powerlaw": 2}
 LEVELS = {"CLEAN": 0, "MEDIUM": 1, "HIGH": 2}
@@ -80,6 +81,17 @@ class lct_sizes(ctypes.Structure):
                 ("status", ctypes.c_uint32), ("delta", ctypes.c_int32)]
 
 
+class lct_adapters(ctypes.Structure):
+    _fields_ = [("d_a", ctypes.c_void_p), ("d_b", ctypes.c_void_p), ("d_scale", ctypes.c_void_p),
+                ("d_ranks", ctypes.c_void_p), ("adapters", ctypes.c_uint64), ("rank", ctypes.c_uint64),
+                ("k", ctypes.c_uint64), ("n", ctypes.c_uint64)]
+
+
+class lct_token_plan(ctypes.Structure):
+    _fields_ = [("d_order", ctypes.c_void_p), ("d_starts", ctypes.c_void_p), ("d_tiles", ctypes.c_void_p),
+                ("tokens", ctypes.c_uint64), ("adapters", ctypes.c_uint64)]
+
+
 _P = ctypes.c_void_p
 _lib.lct_codebook_build.argtypes = [ctypes.c_int, ctypes.c_double, ctypes.c_double, ctypes.POINTER(lct_codebook)]
 _lib.lct_codebook_build_zero_atom.argtypes = [ctypes.c_int, ctypes.c_double, ctypes.c_double, ctypes.c_double,
@@ -104,7 +116,11 @@ _lib.lct_debug_wait_timeout.argtypes = [_P, _P, ctypes.c_uint64, _P]
 _lib.lct_encode_static_scratch.argtypes = [_P, ctypes.POINTER(lct_codebook), ctypes.POINTER(lct_tensor), _P]
 _lib.lct_grad_norm.argtypes = [_P, _P, _P, ctypes.c_uint64, _P, _P, _P]
 _lib.lct_grad_clip.argtypes = [_P, _P, _P, _P, ctypes.c_uint64, ctypes.c_float, _P, _P, _P]
-for _fn in ("lct_grad_norm", "lct_grad_clip", "lct_codebook_build", "lct_codebook_build_zero_atom", "lct_compressed_size", "lct_encode", "lct_decode",
+_U64 = ctypes.c_uint64
+_lib.lct_adapter_plan.argtypes = [_P, _U64, _U64, _P, _P, _P, _P]
+_lib.lct_adapter_forward.argtypes = [_P, _P, _P, _U64, _P, _U64, _P, _U64, _P, _P]
+_lib.lct_adapter_backward.argtypes = [_P, _P, _P, _U64, _P, _U64, _P, _P, _U64, _P, _U64, _P, _P, _P, _P]
+for _fn in ("lct_adapter_plan", "lct_adapter_forward", "lct_adapter_backward", "lct_grad_norm", "lct_grad_clip", "lct_codebook_build", "lct_codebook_build_zero_atom", "lct_compressed_size", "lct_encode", "lct_decode",
             "lct_decode_blocks", "lct_sgd_step_fused",
             "lct_sgd_momentum_step_fused", "lct_adamw_step_fused", "lct_debug_wait_timeout",
             "lct_encode_static_scratch"):
@@ -287,6 +303,43 @@ def lct_grad_clip(g: GradArrays, out: GradArrays, max_norm: float, norm: torch.T
         raise ValueError("out must match the gradients' sizes and types")
     _check(_lib.lct_grad_clip(g.ptr.buffer_info()[0], out.ptr.buffer_info()[0], *g.args(), max_norm, norm.data_ptr(),
                               work.data_ptr(), _stream(stream)), "lct_grad_clip")
+
+
+def lct_adapter_tile_rows(tokens: int, adapters: int) -> int:
+    """Rows of a plan's tile table (LCT_ADAPTER_TILE_ROWS)."""
+    return -(-tokens // LCT_ADAPTER_TILE) + min(adapters + 1, tokens) if tokens else 1
+
+
+def lct_adapter_work_bytes(tokens: int, rank: int) -> int:
+    """Scratch of lct_adapter_backward (LCT_ADAPTER_WORK_BYTES)."""
+    return 8 * tokens * ((rank + 15) // 16 * 16)
+
+
+def lct_adapter_plan(index: torch.Tensor, adapters: int, order: torch.Tensor, starts: torch.Tensor,
+                     tiles: torch.Tensor, stream=None) -> None:
+    _check(_lib.lct_adapter_plan(index.data_ptr(), index.numel(), adapters, order.data_ptr(), starts.data_ptr(),
+                                 tiles.data_ptr(), _stream(stream)), "lct_adapter_plan")
+
+
+def lct_adapter_forward(bank: lct_adapters, plan: lct_token_plan, x, y, out, xa=None, stream=None) -> None:
+    """x, y and out are 2-D BF16 tensors with unit column stride; xa is float32
+    [tokens, rank] or None."""
+    _check(_lib.lct_adapter_forward(ctypes.addressof(bank), ctypes.addressof(plan), x.data_ptr(), x.stride(0),
+                                    y.data_ptr(), y.stride(0), out.data_ptr(), out.stride(0),
+                                    None if xa is None else xa.data_ptr(), _stream(stream)), "lct_adapter_forward")
+
+
+def lct_adapter_backward(bank: lct_adapters, plan: lct_token_plan, dy, x=None, xa=None, dx=None, dx_out=None, da=None,
+                         db=None, work=None, stream=None) -> None:
+    def at(t):
+        return None if t is None else t.data_ptr()
+
+    def ld(t):
+        return 0 if t is None else t.stride(0)
+
+    _check(_lib.lct_adapter_backward(ctypes.addressof(bank), ctypes.addressof(plan), at(dy), ld(dy), at(x), ld(x),
+                                     at(xa), at(dx), ld(dx), at(dx_out), ld(dx_out), at(da), at(db), at(work),
+                                     _stream(stream)), "lct_adapter_backward")
 
 
 def lct_debug_wait_timeout(header: torch.Tensor, work: torch.Tensor, limit_ns: int, stream=None) -> None:

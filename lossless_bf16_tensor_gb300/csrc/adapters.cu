@@ -1,0 +1,1015 @@
+// Low-rank adapters of many requests beside a shared projection, for training
+// and serving.  For a token of adapter a, with A_a [R, K], B_a [N, R], s_a:
+//
+//   forward   out = y + s_a (x A_a^T) B_a^T
+//   backward  d = s_a dy B_a,  dx' = dx + d A_a,
+//             dA_a = sum d^T x,  dB_a = sum s_a dy^T (x A_a^T)
+//
+// Both directions of the tokens' part are one kernel (k_adapter): a product
+// with a narrow matrix (In W1, R columns), whose result stays on the SM, and a
+// product back to the full width added to a row that is there already.  The
+// arithmetic is 4R operations a value of x or y, which HBM delivers in 2 to 4
+// bytes: up to R = 64 HBM bounds the work, if the tensor cores take the
+// products as they come (tcgen05, accumulators in TMEM).
+//
+// Rounding: the products take the BF16 inputs as they are and add in float32;
+// the narrow result V is carried to the second product as the sum of two BF16
+// (hi + lo, 16 bits of V), so only the final value is rounded to BF16.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "../../include/lct.h"
+#include "codec_dev.cuh"
+#include "internal.h"
+
+namespace lct {
+namespace dev {
+
+constexpr int kAdThreads = 256;
+constexpr int kTileTokens = LCT_ADAPTER_TILE;
+constexpr int kChunk = 64;                        // columns of In (phase 1) or of the result (phase 2) at a time
+constexpr int kInBytes = kTileTokens * 128;       // a tile of 128 tokens by 64 BF16 columns
+constexpr uint32_t kTmemCols = 256;
+
+// ---------------------------------------------------------------- tcgen05
+
+// A row-swizzled tile: rows of 128 bytes, the 16-byte piece c of row r at
+// piece c ^ (r & 7) (the 128-byte swizzle that TMEM operands are read with).
+__device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t piece)
+{
+    return row * 128 + ((piece ^ (row & 7)) << 4);
+}
+
+// Shared-memory matrix descriptor of such a tile at a 1024-byte boundary plus
+// an offset.  Rows come in groups of eight, 1024 bytes apart; `atoms` is the
+// distance between 64-column tiles where the operand's rows run along the
+// memory's columns.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t atoms)
+{
+    return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(atoms >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction word: float32 sums of BF16 products, M = 128, N columns; an
+// operand is "across" when its rows run along the columns of its tile.
+__device__ __forceinline__ uint32_t mma_word(uint32_t n, bool a_across, bool b_across)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_across ? 1u << 15 : 0u) | (b_across ? 1u << 16 : 0u) |
+           ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t word, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+// `bar` gets one arrival when the products issued so far are done.
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc(uint32_t *at, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Eight columns of this lane's row (lane 32 w + l of the warp w of a quarter).
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&v)[8])
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ------------------------------------------------------------ tile loads
+
+__device__ __forceinline__ void async16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void store16(uint32_t dst, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 load16(uint32_t src)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(src)
+                 : "memory");
+    return v;
+}
+
+// `valid` (at most 8) BF16 values at src into a 16-byte piece, the rest zero.
+// Aligned pieces travel asynchronously; others are put together here.
+__device__ __forceinline__ void piece(uint32_t dst, const __nv_bfloat16 *src, int valid, bool aligned,
+                                      const void *anywhere)
+{
+    if (aligned) {
+        const uint32_t bytes = valid <= 0 ? 0u : static_cast<uint32_t>(min(valid, 8)) * 2;
+        async16(dst, bytes ? static_cast<const void *>(src) : anywhere, bytes);
+        return;
+    }
+    const uint16_t *p = reinterpret_cast<const uint16_t *>(src);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < valid) w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+    store16(dst, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// Eight float32 as hi + lo, each eight BF16.
+__device__ __forceinline__ void split8(const float (&v)[8], uint4 &hi, uint4 &lo)
+{
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = pack2(v[2 * i], v[2 * i + 1]);
+        // an infinite or NaN value has no remainder
+        const float a = __uint_as_float(h[i] << 16), b = __uint_as_float(h[i] & 0xFFFF0000u);
+        l[i] = pack2(isfinite(a) ? v[2 * i] - a : 0.0f, isfinite(b) ? v[2 * i + 1] - b : 0.0f);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ float peer_float(uint32_t addr, uint32_t rank)
+{
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// The rank an adapter uses, within the bank's.
+__device__ __forceinline__ int used_rank(const AdapterArgs &g, int a)
+{
+    const int r = g.ranks ? g.ranks[a] : g.rank;
+    return max(0, min(r, g.rank));
+}
+
+__device__ __forceinline__ void fail(const AdapterArgs &g)
+{
+    if (g.status) atomicCAS(reinterpret_cast<unsigned int *>(g.status), 0u, static_cast<unsigned int>(LCT_ERR_TIMEOUT));
+}
+
+// Waits for products to be done; after one wait that ran out none waits again.
+struct Waiter {
+    bool dead = false;
+    __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity)
+    {
+        if (!dead && !mbar_wait(bar, parity, kDefaultWaitNs)) dead = true;
+    }
+};
+
+// ------------------------------------------------------- the tokens' part
+
+// Shared memory: a ring of `stages` slots, each a 128 x 64 tile of In (or of
+// the row to add to) and a tile of W1 or W2; then V, hi and lo, whose space
+// first holds the block's partial sums.
+struct AdapterSmem {
+    uint32_t w_bytes, slot, v_at, v_atom, bytes;
+};
+__host__ __device__ inline AdapterSmem adapter_smem(int rank, int stages)
+{
+    AdapterSmem s;
+    const uint32_t atoms = rank > 64 ? 2 : 1;
+    s.w_bytes = atoms * 64 * 128;
+    s.slot = kInBytes + s.w_bytes;
+    s.v_at = s.slot * stages;
+    s.v_atom = kTileTokens * 128;
+    s.bytes = s.v_at + 2 * atoms * s.v_atom + 1024;  // room to start at a 1024-byte boundary
+    return s;
+}
+
+// Loads the 128 x 64 tile of `m` at columns c0.. (of `cols`).
+__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16 *m, int64_t ld, const int *tok, int count,
+                                          int c0, int cols, bool aligned)
+{
+    for (int i = threadIdx.x; i < count * 8; i += kAdThreads) {
+        const int row = i >> 3, c = i & 7, at = c0 + c * 8;
+        piece(dst + swz(row, c), m + tok[row] * ld + at, cols - at, aligned, m);
+    }
+}
+
+// Loads rows r0 .. r0 + nrows of a row-major matrix [rows, cols] with leading
+// dimension ld, columns c0 .. c0 + 8 * pieces, into 64-column tiles `atom`
+// bytes apart; what lies outside the matrix is zero.
+__device__ __forceinline__ void load_block(uint32_t dst, uint32_t atom, const __nv_bfloat16 *m, int64_t ld, int r0,
+                                           int rows, int nrows, int c0, int cols, int pieces, bool aligned)
+{
+    for (int i = threadIdx.x; i < nrows * pieces; i += kAdThreads) {
+        const int row = i / pieces, c = i - row * pieces, at = c0 + c * 8;
+        const int valid = r0 + row < rows ? cols - at : 0;
+        piece(dst + (c >> 3) * atom + swz(row, c & 7), m + (r0 + row) * ld + at, valid, aligned, m);
+    }
+}
+
+// Rows without an adapter: out = base, and nothing to keep.
+__device__ __forceinline__ void copy_rows(const AdapterArgs &g, const int *tok, int count)
+{
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    if (g.out && g.out != g.base) {
+        const bool vec = g.al_base && g.al_out;
+        const int step = vec ? 8 : 1, per = (g.nout + step - 1) / step;
+        const int64_t all = static_cast<int64_t>(count) * per;
+        for (int64_t i = rank * kAdThreads + threadIdx.x; i < all; i += size * kAdThreads) {
+            const int row = static_cast<int>(i / per), c = static_cast<int>(i - static_cast<int64_t>(row) * per) * step;
+            const __nv_bfloat16 *s = g.base + tok[row] * g.ld_base + c;
+            __nv_bfloat16 *d = g.out + tok[row] * g.ld_out + c;
+            if (vec && c + 8 <= g.nout)
+                *reinterpret_cast<uint4 *>(d) = *reinterpret_cast<const uint4 *>(s);
+            else
+                for (int j = 0; j < step && c + j < g.nout; ++j) d[j] = s[j];
+        }
+    }
+    if (g.keep)
+        for (int i = rank * kAdThreads + threadIdx.x; i < count * g.rank; i += size * kAdThreads)
+            g.keep[static_cast<int64_t>(tok[i / g.rank]) * g.rank + i % g.rank] = 0.0f;
+}
+
+// One tile of at most 128 tokens of one adapter, by one cluster.  Its blocks
+// take every c-th 64-column chunk of In for the narrow product, add up their
+// partial sums through each other's shared memory in a fixed order, and take
+// every c-th chunk of the result for the second product.  Loads run `STAGES`
+// chunks deep through both phases.
+//
+// BACK = false: In = x, W1 = A [R, K], W2 = B [N, R], V = s (x A^T).
+// BACK = true:  In = dy, W1 = B [N, R], W2 = A [R, K], V = s (dy B).
+template <bool BACK, int STAGES>
+__global__ void __launch_bounds__(kAdThreads, STAGES <= 3 ? 2 : 1) k_adapter(const __grid_constant__ AdapterArgs g)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ int tok[kTileTokens];
+    __shared__ uint64_t done[STAGES];
+    __shared__ uint32_t tmem_at;
+
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    const int4 tile = reinterpret_cast<const int4 *>(g.tiles)[blockIdx.x / size];
+    const int count = min(tile.z, kTileTokens);
+    if (count <= 0) return;
+    for (int i = threadIdx.x; i < count; i += kAdThreads) tok[i] = g.order[tile.y + i];
+    const int a = tile.x;
+    const int used = a < 0 || a >= g.adapters ? 0 : used_rank(g, a);
+    if (used == 0) {
+        __syncthreads();
+        copy_rows(g, tok, count);
+        return;
+    }
+
+    const AdapterSmem lay = adapter_smem(g.rank, STAGES);
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+    const int r16 = (used + 15) & ~15;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const __nv_bfloat16 *A = g.a + static_cast<int64_t>(a) * g.rank * g.k;
+    const __nv_bfloat16 *B = g.b + static_cast<int64_t>(a) * g.rank * g.n;
+    const float scale = g.scale[a];
+
+    if (warp == 0) tmem_alloc(&tmem_at, kTmemCols);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) mbar_init(&done[i], 1);
+        fence_mbar_init();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = tmem_at;
+
+    const int all1 = (g.nin + kChunk - 1) / kChunk, all2 = g.out ? (g.nout + kChunk - 1) / kChunk : 0;
+    const int n1 = all1 > (int)rank ? (all1 - rank + size - 1) / size : 0;
+    const int n2 = all2 > (int)rank ? (all2 - rank + size - 1) / size : 0;
+    const int n = n1 + n2;
+
+    auto load = [&](int i) {
+        const uint32_t slot = base + (i % STAGES) * lay.slot, w = slot + kInBytes;
+        if (i < n1) {
+            const int c0 = (rank + i * size) * kChunk;
+            load_rows(slot, g.in, g.ld_in, tok, count, c0, g.nin, g.al_in);
+            if (BACK)  // 64 rows of B, R columns
+                load_block(w, 64 * 128, B, g.rank, c0, g.n, kChunk, 0, used, r16 / 8, g.al_b);
+            else       // R rows of A, 64 columns
+                load_block(w, 0, A, g.k, 0, used, r16, c0, g.k, 8, g.al_a);
+        } else if (i < n) {
+            const int c0 = (rank + (i - n1) * size) * kChunk;
+            load_rows(slot, g.base, g.ld_base, tok, count, c0, g.nout, g.al_base);
+            if (BACK)
+                load_block(w, 0, A, g.k, 0, used, r16, c0, g.k, 8, g.al_a);
+            else
+                load_block(w, 64 * 128, B, g.rank, c0, g.n, kChunk, 0, used, r16 / 8, g.al_b);
+        }
+        async_commit();
+    };
+
+    Waiter waiter;
+    // Adds the product of chunk j to its tile and writes the rows out.
+    auto finish = [&](int j) {
+        const uint32_t slot = base + (j % STAGES) * lay.slot;
+        const int c0 = (rank + (j - n1) * size) * kChunk;
+        waiter.wait(&done[j % STAGES], (j / STAGES) & 1);
+        tc_after();
+        __syncwarp();
+        const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+        if ((warp & 3) * 32 < count) {
+            float v[4][8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                tmem_load8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128 + ((j - n1) & 1) * kChunk + half * 32 + q * 8, v[q]);
+            tmem_wait();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t at = slot + swz(row, half * 4 + q);
+                const uint4 y = load16(at);
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] = pack2(__uint_as_float(w[i] << 16) + v[q][2 * i],
+                                 __uint_as_float(w[i] & 0xFFFF0000u) + v[q][2 * i + 1]);
+                store16(at, make_uint4(o[0], o[1], o[2], o[3]));
+            }
+        }
+        tc_before();
+        __syncthreads();
+        // the same places that this thread loads next, so that no barrier is needed before that
+        for (int i = threadIdx.x; i < count * 8; i += kAdThreads) {
+            const int r = i >> 3, c = i & 7, at = c0 + c * 8;
+            const uint4 v = load16(slot + swz(r, c));
+            __nv_bfloat16 *o = g.out + tok[r] * g.ld_out + at;
+            if (g.al_out && at + 8 <= g.nout) {
+                *reinterpret_cast<uint4 *>(o) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (at + k < g.nout)
+                        reinterpret_cast<uint16_t *>(o)[k] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
+            }
+        }
+    };
+
+    // The block's partial sums, everyone's total, and V from it.
+    auto middle = [&]() {
+        if (n1 > 0) waiter.wait(&done[(n1 - 1) % STAGES], ((n1 - 1) / STAGES) & 1);
+        tc_after();
+        __syncwarp();
+        const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+        const uint32_t v_at = base + lay.v_at;
+        const bool rows = (warp & 3) * 32 < count;
+        const int pieces = r16 / 8;
+        if (size > 1) {
+            if (rows)
+                for (int p = half; p < pieces; p += 2) {
+                    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (n1 > 0) {
+                        tmem_load8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + p * 8, v);
+                        tmem_wait();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(v_at + ((p * 8 + i) * kTileTokens + row) * 4),
+                                     "f"(v[i])
+                                     : "memory");
+                }
+            __syncwarp();
+            cluster_sync();
+        }
+        float sum[8][8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int p = q * 2 + half;
+            if (rows && p < pieces) {
+                if (size > 1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[q][i] = 0.0f;
+                    for (uint32_t peer = 0; peer < size; ++peer)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (row < count)
+                                sum[q][i] += peer_float(v_at + ((p * 8 + i) * kTileTokens + row) * 4, peer);
+                } else {
+                    tmem_load8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + p * 8, sum[q]);
+                    tmem_wait();
+                }
+            }
+        }
+        __syncwarp();
+        if (size > 1) cluster_sync();  // everyone has read the partial sums that V's place held
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int p = q * 2 + half;
+            if (!rows || p >= pieces) continue;
+            const uint32_t at = v_at + (p >> 3) * lay.v_atom + swz(row, p & 7);
+            const uint32_t lo_at = (g.rank > 64 ? 2 : 1) * lay.v_atom;
+            const bool writes = row < count && p % size == rank;
+            if (!BACK && g.keep && writes) {
+                float *k = g.keep + static_cast<int64_t>(tok[row]) * g.rank + p * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (p * 8 + i < used) k[i] = sum[q][i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[q][i] *= scale;
+            uint4 hi, lo;
+            split8(sum[q], hi, lo);
+            store16(at, hi);
+            store16(at + lo_at, lo);
+            if (BACK && g.work && writes) {
+                // for the weights' gradients, in the plan's order: s dy B, and s (x A^T), as hi and lo
+                const int64_t line = static_cast<int64_t>(tile.y + row) * 2 * g.rank16 + p * 8;
+                *reinterpret_cast<uint4 *>(g.work + line) = hi;
+                *reinterpret_cast<uint4 *>(g.work + line + g.rank16) = lo;
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] = p * 8 + i < used
+                               ? scale * g.kept[static_cast<int64_t>(tok[row]) * g.rank + p * 8 + i]
+                               : 0.0f;
+                split8(x, hi, lo);
+                const int64_t far = static_cast<int64_t>(g.tokens) * 2 * g.rank16;
+                *reinterpret_cast<uint4 *>(g.work + far + line) = hi;
+                *reinterpret_cast<uint4 *>(g.work + far + line + g.rank16) = lo;
+            }
+        }
+        // ranks that the adapter does not use
+        if (!BACK && g.keep)
+            for (int i = rank * kAdThreads + threadIdx.x; i < count * (g.rank - used); i += size * kAdThreads)
+                g.keep[static_cast<int64_t>(tok[i / (g.rank - used)]) * g.rank + used + i % (g.rank - used)] = 0.0f;
+        fence_proxy_async();
+        tc_before();
+        __syncthreads();
+        tc_after();
+    };
+
+    for (int i = 0; i < STAGES - 1; ++i) load(i);
+    for (int i = 0; i < n; ++i) {
+        if (i == n1) middle();
+        async_wait<STAGES - 2>();
+        fence_proxy_async();
+        tc_before();
+        __syncthreads();
+        tc_after();
+        if (threadIdx.x == 0 && !waiter.dead) {
+            const uint32_t slot = base + (i % STAGES) * lay.slot, w = slot + kInBytes;
+            if (i < n1) {
+                const uint32_t word = mma_word(r16, false, BACK);
+#pragma unroll
+                for (int k = 0; k < kChunk / 16; ++k)
+                    mma(tmem, operand(slot + k * 32, 0),
+                        BACK ? operand(w + k * 16 * 128, 64 * 128) : operand(w + k * 32, 0), word, i > 0 || k > 0);
+            } else {
+                const uint32_t word = mma_word(kChunk, false, BACK);
+                const uint32_t d = tmem + 128 + ((i - n1) & 1) * kChunk, v_at = base + lay.v_at;
+                const uint32_t lo_at = (g.rank > 64 ? 2 : 1) * lay.v_atom;
+                for (int k = 0; k < r16 / 16; ++k) {
+                    const uint64_t b = BACK ? operand(w + k * 16 * 128, 0)
+                                            : operand(w + (k >> 2) * 64 * 128 + (k & 3) * 32, 0);
+                    const uint32_t v = v_at + (k >> 2) * lay.v_atom + (k & 3) * 32;
+                    mma(d, operand(v, 0), b, word, k > 0);
+                    mma(d, operand(v + lo_at, 0), b, word, true);
+                }
+            }
+            mma_commit(&done[i % STAGES]);
+        }
+        if (i > n1) finish(i - 1);
+        if (i > 0 && i + STAGES - 1 < n) waiter.wait(&done[(i - 1) % STAGES], ((i - 1) / STAGES) & 1);
+        load(i + STAGES - 1);
+    }
+    if (n == n1) middle();
+    if (n > n1) finish(n - 1);
+    async_wait<0>();
+    if (waiter.dead) fail(g);
+    tc_before();
+    __syncthreads();
+    if (warp == 0) tmem_free(tmem, kTmemCols);
+}
+
+// --------------------------------------------------- the weights' gradients
+
+// dA^T [K, R] = x^T (s dy B) and dB [N, R] = dy^T (s x A^T) of one adapter:
+// 128 columns of x or dy by one cluster, whose blocks take every c-th run of
+// 64 of the adapter's tokens; their partial sums meet in shared memory in a
+// fixed order.  The tokens are the products' inner dimension, so tiles are
+// read across: rows of a tile of x are columns of the operand.
+template <int STAGES>
+__global__ void __launch_bounds__(kAdThreads, 2) k_adapter_grad(const __grid_constant__ AdapterArgs g)
+{
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t done[STAGES];
+    __shared__ uint32_t tmem_at;
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    const int blocks_x = (g.k + 127) / 128;
+    const int which = blockIdx.y;
+    const bool is_a = which < blocks_x;
+    const int c0 = (is_a ? which : which - blocks_x) * 128;
+    const int a = blockIdx.z;
+    const int first = g.starts[a], last = g.starts[a + 1];
+    const int used = last > first ? used_rank(g, a) : 0;
+    const int cols = is_a ? g.k : g.n;
+    const __nv_bfloat16 *in = is_a ? g.x : g.in;
+    const int64_t ld = is_a ? g.ld_x : g.ld_in;
+    const bool al = is_a ? g.al_x : g.al_in;
+    const __nv_bfloat16 *v = g.work + (is_a ? 0 : static_cast<int64_t>(g.tokens) * 2 * g.rank16);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+    const uint32_t atoms = g.rank > 64 ? 2 : 1;
+    const uint32_t v_bytes = atoms * 64 * 128, slot_bytes = 2 * 64 * 128 + 2 * v_bytes;
+    const int r16 = (used + 15) & ~15;
+    const int all = (last - first + 63) / 64;
+    const int n = used && all > (int)rank ? (all - rank + size - 1) / size : 0;
+    uint32_t tmem = 0;
+    Waiter waiter;
+    if (used) {
+        if (warp == 0) tmem_alloc(&tmem_at, 128);
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < STAGES; ++i) mbar_init(&done[i], 1);
+            fence_mbar_init();
+        }
+        tc_before();
+        __syncthreads();
+        tc_after();
+        tmem = tmem_at;
+
+        auto load = [&](int i) {
+            if (i < n) {
+                const uint32_t slot = base + (i % STAGES) * slot_bytes;
+                const int t0 = first + (rank + i * size) * 64;
+                for (int j = threadIdx.x; j < 64 * 16; j += kAdThreads) {
+                    const int row = j >> 4, c = j & 15, at = c0 + c * 8;
+                    const bool there = t0 + row < last;
+                    const int64_t t = there ? g.order[t0 + row] : 0;
+                    piece(slot + (c >> 3) * 64 * 128 + swz(row, c & 7), in + t * ld + at, there ? cols - at : 0, al, in);
+                }
+                const int pieces = r16 / 8;
+                for (int j = threadIdx.x; j < 64 * 2 * pieces; j += kAdThreads) {
+                    const int row = j / (2 * pieces), q = j - row * 2 * pieces, lo = q >= pieces, c = q - lo * pieces;
+                    const uint32_t dst = slot + 2 * 64 * 128 + lo * v_bytes + (c >> 3) * 64 * 128 + swz(row, c & 7);
+                    piece(dst, v + (static_cast<int64_t>(t0 + row) * 2 + lo) * g.rank16 + c * 8, t0 + row < last ? 8 : 0,
+                          true, v);
+                }
+            }
+            async_commit();
+        };
+        for (int i = 0; i < STAGES - 1; ++i) load(i);
+        for (int i = 0; i < n; ++i) {
+            async_wait<STAGES - 2>();
+            fence_proxy_async();
+            tc_before();
+            __syncthreads();
+            tc_after();
+            if (threadIdx.x == 0 && !waiter.dead) {
+                const uint32_t slot = base + (i % STAGES) * slot_bytes, w = slot + 2 * 64 * 128;
+                const uint32_t word = mma_word(r16, true, true);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t m = operand(slot + k * 16 * 128, 64 * 128);
+                    mma(tmem, m, operand(w + k * 16 * 128, 64 * 128), word, i > 0 || k > 0);
+                    mma(tmem, m, operand(w + v_bytes + k * 16 * 128, 64 * 128), word, true);
+                }
+                mma_commit(&done[i % STAGES]);
+            }
+            if (i > 0 && i + STAGES - 1 < n) waiter.wait(&done[(i - 1) % STAGES], ((i - 1) / STAGES) & 1);
+            load(i + STAGES - 1);
+        }
+        if (n > 0) waiter.wait(&done[(n - 1) % STAGES], ((n - 1) / STAGES) & 1);
+        async_wait<0>();
+        tc_after();
+        __syncthreads();
+    }
+
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    if (used) {
+        for (int p = half; p < r16 / 8; p += 2) {
+            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (n > 0) {
+                tmem_load8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + p * 8, x);
+                tmem_wait();
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((p * 8 + i) * 128 + row) * 4), "f"(x[i]) : "memory");
+        }
+        tc_before();
+    }
+    __syncwarp();
+    cluster_sync();
+    // this block's share of the ranks
+    for (int i = rank * 2 + half; i < g.rank; i += 2 * size) {
+        float s = 0.0f;
+        if (i < used)
+            for (uint32_t peer = 0; peer < size; ++peer) s += peer_float(base + (i * 128 + row) * 4, peer);
+        if (c0 + row < cols) {
+            if (is_a)
+                g.da[(static_cast<int64_t>(a) * g.rank + i) * g.k + c0 + row] = __float2bfloat16_rn(s);
+            else
+                g.db[(static_cast<int64_t>(a) * g.n + c0 + row) * g.rank + i] = __float2bfloat16_rn(s);
+        }
+    }
+    if (waiter.dead) fail(g);
+    __syncwarp();
+    cluster_sync();
+    if (used && warp == 0) tmem_free(tmem, 128);
+}
+
+// -------------------------------------------------------------- the plan
+
+// The tokens in stable order of their adapter.  Each warp counts a contiguous
+// share of the tokens, one column of shared counters an adapter; a scan over
+// adapters and warps turns the counts into places, and each warp deals its
+// tokens out.  Lanes with the same adapter find each other by a match.
+__global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ PlanArgs g)
+{
+    extern __shared__ int counts[];  // [adapters + 1][warps]
+    __shared__ int part[32], tile_part[32];
+    __shared__ int bad;
+    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int groups = g.adapters + 1;
+    if (threadIdx.x == 0) bad = 0;
+    for (int i = threadIdx.x; i < groups * warps; i += blockDim.x) counts[i] = 0;
+    __syncthreads();
+    const int share = ((g.tokens + warps - 1) / warps + 31) & ~31;
+    const int lo = min(g.tokens, warp * share), hi = min(g.tokens, lo + share);
+    auto group_of = [&](int t) {
+        const int a = g.index[t];
+        if (a >= g.adapters || a < -1) bad = 1;
+        return a < 0 || a >= g.adapters ? g.adapters : a;
+    };
+    for (int t0 = lo; t0 < hi; t0 += 32) {
+        const bool there = t0 + lane < hi;
+        const int a = there ? group_of(t0 + lane) : -1;
+        const unsigned same = __match_any_sync(kFull, a);
+        if (there && lane == __ffs(same) - 1) counts[a * warps + warp] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // exclusive places over (adapter, warp), and tiles over adapters: each thread takes a run of adapters
+    const int run = (groups + blockDim.x - 1) / blockDim.x;
+    const int a0 = min(groups, static_cast<int>(threadIdx.x) * run), a1 = min(groups, a0 + run);
+    int sum = 0, tiles = 0;
+    for (int a = a0; a < a1; ++a) {
+        int c = 0;
+        for (int w = 0; w < warps; ++w) c += counts[a * warps + w];
+        sum += c;
+        tiles += (c + kTileTokens - 1) / kTileTokens;
+    }
+    int before = sum, tiles_before = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, before, o), y = __shfl_up_sync(kFull, tiles_before, o);
+        if (lane >= o) before += x, tiles_before += y;
+    }
+    if (lane == 31) part[warp] = before, tile_part[warp] = tiles_before;
+    __syncthreads();
+    int all_tiles = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) before += part[w], tiles_before += tile_part[w];
+        all_tiles += tile_part[w];
+    }
+    before -= sum;
+    tiles_before -= tiles;
+    int4 *table = reinterpret_cast<int4 *>(g.tiles);
+    for (int a = a0; a < a1; ++a) {
+        const int first = before;
+        g.starts[a] = first;
+        for (int w = 0; w < warps; ++w) {
+            const int c = counts[a * warps + w];
+            counts[a * warps + w] = before;
+            before += c;
+        }
+        for (int t = first; t < before; t += kTileTokens) {
+            const int flag = tiles_before == 0 && bad ? LCT_ERR_INVALID_ARG : 0;
+            table[tiles_before++] = make_int4(a == g.adapters ? -1 : a, t, min(kTileTokens, before - t), flag);
+        }
+    }
+    if (threadIdx.x == 0) g.starts[groups] = g.tokens;
+    for (int i = all_tiles + threadIdx.x; i < g.rows; i += blockDim.x) table[i] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    for (int t0 = lo; t0 < hi; t0 += 32) {
+        const bool there = t0 + lane < hi;
+        const int a = there ? group_of(t0 + lane) : -1;
+        const unsigned same = __match_any_sync(kFull, a);
+        int at = 0;
+        if (there) at = counts[a * warps + warp];
+        __syncwarp();
+        if (there) {
+            g.order[at + __popc(same & ((1u << lane) - 1))] = t0 + lane;
+            if (lane == __ffs(same) - 1) counts[a * warps + warp] = at + __popc(same);
+        }
+        __syncwarp();
+    }
+}
+
+}  // namespace dev
+
+namespace {
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, uint32_t threads, uint32_t smem, uint32_t cluster, cudaStream_t s,
+                   A... args)
+{
+    cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (rc != cudaSuccess) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Blocks of a cluster: enough that the tiles fill the GPU twice over, as far
+// as there are chunks to share out.
+uint32_t cluster_for(uint64_t tiles, uint64_t chunks)
+{
+    uint32_t c = 1;
+    while (c < 8 && tiles * c < 304 && 2ull * c <= chunks) c *= 2;
+    return c;
+}
+
+constexpr int kStages = 3;
+
+}  // namespace
+
+cudaError_t launch_adapter(const AdapterArgs &a, bool back, cudaStream_t s)
+{
+    const uint64_t chunks = (std::max(a.nin, a.out ? a.nout : 0) + 63) / 64;
+    const uint32_t c = cluster_for((a.tokens + 127) / 128 + std::min(a.adapters, a.tokens), chunks);
+    const uint32_t smem = dev::adapter_smem(a.rank, kStages).bytes;
+    const dim3 grid(c * a.rows);
+    return back ? launch(dev::k_adapter<true, kStages>, grid, dev::kAdThreads, smem, c, s, a)
+                : launch(dev::k_adapter<false, kStages>, grid, dev::kAdThreads, smem, c, s, a);
+}
+
+cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s)
+{
+    const uint32_t cols = (a.k + 127) / 128 + (a.n + 127) / 128;
+    const uint32_t c = cluster_for(static_cast<uint64_t>(cols) * a.adapters, (a.tokens + 63) / 64);
+    const uint32_t atoms = a.rank > 64 ? 2 : 1;
+    const uint32_t smem = 3 * (2 * 64 * 128 + 2 * atoms * 64 * 128) + 1024;
+    return launch(dev::k_adapter_grad<3>, dim3(c, cols, a.adapters), dev::kAdThreads, smem, c, s, a);
+}
+
+cudaError_t launch_adapter_plan(const PlanArgs &a, cudaStream_t s)
+{
+    // as many warps as the counters leave room for
+    uint32_t warps = 32;
+    while (warps > 1 && (a.adapters + 1ull) * warps * 4 > 200 * 1024) warps /= 2;
+    return launch(dev::k_adapter_plan, dim3(1), warps * 32, (a.adapters + 1) * warps * 4, 1, s, a);
+}
+
+namespace {
+
+bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool al(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// A matrix of BF16 rows in memory.
+struct Rows {
+    const void *p;
+    uint64_t ld, cols, rows;
+};
+bool rows_ok(const Rows &m) { return m.p && al(m.p, 2) && m.ld >= m.cols && m.ld <= kMaxN; }
+bool rows_al(const Rows &m) { return al16(m.p) && (m.ld % 8 == 0 || m.rows == 1); }
+
+// Whether two matrices share no value: apart in memory, or column slices of
+// rows with one stride that do not meet.
+bool rows_apart(const Rows &x, const Rows &y)
+{
+    if (!x.rows || !y.rows) return true;
+    const uint64_t xl = reinterpret_cast<uint64_t>(x.p), yl = reinterpret_cast<uint64_t>(y.p);
+    const uint64_t xh = xl + 2 * ((x.rows - 1) * x.ld + x.cols), yh = yl + 2 * ((y.rows - 1) * y.ld + y.cols);
+    if (xh <= yl || yh <= xl) return true;
+    if (x.ld != y.ld || ((xl ^ yl) & 1)) return false;
+    const uint64_t d = yl >= xl ? ((yl - xl) / 2) % x.ld : (x.ld - ((xl - yl) / 2) % x.ld) % x.ld;
+    return d >= x.cols && d + y.cols <= x.ld;
+}
+bool same_rows(const Rows &x, const Rows &y) { return x.p == y.p && x.ld == y.ld; }
+
+bool bytes_apart(const Rows &x, const void *p, uint64_t bytes)
+{
+    if (!x.rows || !p || !bytes) return true;
+    const uint64_t xl = reinterpret_cast<uint64_t>(x.p), pl = reinterpret_cast<uint64_t>(p);
+    return xl + 2 * ((x.rows - 1) * x.ld + x.cols) <= pl || pl + bytes <= xl;
+}
+bool bytes_apart(const void *x, uint64_t xn, const void *p, uint64_t n)
+{
+    const uint64_t xl = reinterpret_cast<uint64_t>(x), pl = reinterpret_cast<uint64_t>(p);
+    return !x || !p || !xn || !n || xl + xn <= pl || pl + n <= xl;
+}
+
+lct_status check_bank(const lct_adapters *b, const lct_token_plan *p, AdapterArgs *g)
+{
+    if (!b || !p) return LCT_ERR_INVALID_ARG;
+    if (b->adapters == 0 || b->rank == 0 || b->k == 0 || b->n == 0 || p->adapters != b->adapters)
+        return LCT_ERR_INVALID_ARG;
+    if (b->rank > LCT_ADAPTER_MAX_RANK || b->adapters > LCT_ADAPTER_MAX || p->tokens > LCT_ADAPTER_MAX_TOKENS ||
+        b->k > LCT_ADAPTER_MAX_COLS || b->n > LCT_ADAPTER_MAX_COLS)
+        return LCT_ERR_UNSUPPORTED;
+    if (!b->d_a || !b->d_b || !b->d_scale || !al(b->d_a, 2) || !al(b->d_b, 2) || !al(b->d_scale, 4) ||
+        !al(b->d_ranks, 4))
+        return LCT_ERR_INVALID_ARG;
+    if (!p->d_order || !p->d_starts || !p->d_tiles || !al(p->d_order, 4) || !al(p->d_starts, 4) || !al16(p->d_tiles))
+        return LCT_ERR_INVALID_ARG;
+    *g = AdapterArgs{};
+    g->a = reinterpret_cast<const __nv_bfloat16 *>(b->d_a);
+    g->b = reinterpret_cast<const __nv_bfloat16 *>(b->d_b);
+    g->scale = b->d_scale;
+    g->ranks = b->d_ranks;
+    g->adapters = static_cast<int>(b->adapters);
+    g->rank = static_cast<int>(b->rank);
+    g->rank16 = (g->rank + 15) & ~15;
+    g->k = static_cast<int>(b->k);
+    g->n = static_cast<int>(b->n);
+    g->al_a = al16(b->d_a) && g->k % 8 == 0;
+    g->al_b = al16(b->d_b) && g->rank % 8 == 0;
+    g->tokens = static_cast<int>(p->tokens);
+    g->order = p->d_order;
+    g->starts = p->d_starts;
+    g->tiles = p->d_tiles;
+    g->rows = static_cast<int>(LCT_ADAPTER_TILE_ROWS(p->tokens, p->adapters));
+    g->status = p->d_tiles + 3;
+    return LCT_OK;
+}
+
+// Whether a written region leaves the bank and the plan alone.
+bool apart_from_bank(const Rows &m, const AdapterArgs &g)
+{
+    const uint64_t ab = 2ull * g.adapters * g.rank * g.k, bb = 2ull * g.adapters * g.rank * g.n;
+    return bytes_apart(m, g.a, ab) && bytes_apart(m, g.b, bb) && bytes_apart(m, g.scale, 4ull * g.adapters) &&
+           bytes_apart(m, g.ranks, 4ull * g.adapters) && bytes_apart(m, g.order, 4ull * g.tokens) &&
+           bytes_apart(m, g.starts, 4ull * (g.adapters + 2)) && bytes_apart(m, g.tiles, 16ull * g.rows);
+}
+Rows flat(const void *p, uint64_t bytes) { return Rows{p, bytes / 2, bytes / 2, p && bytes ? 1ull : 0ull}; }
+
+}  // namespace
+}  // namespace lct
+
+using namespace lct;
+
+extern "C" lct_status lct_adapter_plan(const int32_t *d_index, uint64_t tokens, uint64_t adapters, int32_t *d_order,
+                                       int32_t *d_starts, int32_t *d_tiles, void *stream)
+{
+    if (adapters == 0) return LCT_ERR_INVALID_ARG;
+    if (adapters > LCT_ADAPTER_MAX || tokens > LCT_ADAPTER_MAX_TOKENS) return LCT_ERR_UNSUPPORTED;
+    if (!d_starts || !d_tiles || !al(d_starts, 4) || !al16(d_tiles)) return LCT_ERR_INVALID_ARG;
+    if (tokens && (!d_index || !d_order || !al(d_index, 4) || !al(d_order, 4))) return LCT_ERR_INVALID_ARG;
+    PlanArgs g;
+    g.index = d_index;
+    g.order = d_order;
+    g.starts = d_starts;
+    g.tiles = d_tiles;
+    g.tokens = static_cast<int>(tokens);
+    g.adapters = static_cast<int>(adapters);
+    g.rows = static_cast<int>(LCT_ADAPTER_TILE_ROWS(tokens, adapters));
+    const void *out[3] = {d_order, d_starts, d_tiles};
+    const uint64_t len[3] = {4 * tokens, 4 * (adapters + 2), 16ull * g.rows};
+    for (int i = 0; i < 3; ++i) {
+        if (!bytes_apart(out[i], len[i], d_index, 4 * tokens)) return LCT_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 3; ++j)
+            if (!bytes_apart(out[i], len[i], out[j], len[j])) return LCT_ERR_INVALID_ARG;
+    }
+    return launch_adapter_plan(g, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
+}
+
+extern "C" lct_status lct_adapter_forward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_x,
+                                          uint64_t ld_x, const uint16_t *d_y, uint64_t ld_y, uint16_t *d_out,
+                                          uint64_t ld_out, float *d_xa, void *stream)
+{
+    AdapterArgs g;
+    const lct_status rc = check_bank(bank, plan, &g);
+    if (rc != LCT_OK) return rc;
+    if (plan->tokens == 0) return LCT_OK;
+    const uint64_t t = plan->tokens;
+    const Rows x{d_x, ld_x, bank->k, t}, y{d_y, ld_y, bank->n, t}, out{d_out, ld_out, bank->n, t};
+    if (!rows_ok(x) || !rows_ok(y) || !rows_ok(out) || !al(d_xa, 4)) return LCT_ERR_INVALID_ARG;
+    if (!rows_apart(out, x) || (!same_rows(out, y) && !rows_apart(out, y)) || !apart_from_bank(out, g))
+        return LCT_ERR_INVALID_ARG;
+    const uint64_t kept = d_xa ? 4 * t * bank->rank : 0;
+    if (!bytes_apart(x, d_xa, kept) || !bytes_apart(y, d_xa, kept) || !bytes_apart(out, d_xa, kept) ||
+        !apart_from_bank(flat(d_xa, kept), g))
+        return LCT_ERR_INVALID_ARG;
+    g.in = reinterpret_cast<const __nv_bfloat16 *>(d_x);
+    g.ld_in = static_cast<int64_t>(ld_x);
+    g.nin = g.k;
+    g.al_in = rows_al(x);
+    g.base = reinterpret_cast<const __nv_bfloat16 *>(d_y);
+    g.ld_base = static_cast<int64_t>(ld_y);
+    g.al_base = rows_al(y);
+    g.out = reinterpret_cast<__nv_bfloat16 *>(d_out);
+    g.ld_out = static_cast<int64_t>(ld_out);
+    g.al_out = rows_al(out);
+    g.nout = g.n;
+    g.keep = d_xa;
+    return launch_adapter(g, false, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
+}
+
+extern "C" lct_status lct_adapter_backward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_dy,
+                                           uint64_t ld_dy, const uint16_t *d_x, uint64_t ld_x, const float *d_xa,
+                                           const uint16_t *d_dx, uint64_t ld_dx, uint16_t *d_dx_out, uint64_t ld_dx_out,
+                                           uint16_t *d_da, uint16_t *d_db, void *d_work, void *stream)
+{
+    AdapterArgs g;
+    const lct_status rc = check_bank(bank, plan, &g);
+    if (rc != LCT_OK) return rc;
+    const uint64_t t = plan->tokens;
+    const uint64_t abytes = 2ull * bank->adapters * bank->rank * bank->k;
+    const uint64_t bbytes = 2ull * bank->adapters * bank->rank * bank->n;
+    if (!d_da != !d_db || (!d_da && !d_dx_out) || !al(d_da, 2) || !al(d_db, 2)) return LCT_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (t == 0) {
+        if (!d_da) return LCT_OK;
+        return cudaMemsetAsync(d_da, 0, abytes, s) == cudaSuccess && cudaMemsetAsync(d_db, 0, bbytes, s) == cudaSuccess
+                   ? LCT_OK
+                   : LCT_ERR_CUDA;
+    }
+    const uint64_t kept = 4 * t * bank->rank, work = LCT_ADAPTER_WORK_BYTES(t, bank->rank);
+    const Rows dy{d_dy, ld_dy, bank->n, t}, x{d_x, ld_x, bank->k, d_da ? t : 0};
+    const Rows dx{d_dx, ld_dx, bank->k, d_dx_out ? t : 0}, out{d_dx_out, ld_dx_out, bank->k, d_dx_out ? t : 0};
+    if (!rows_ok(dy) || (d_dx_out && (!rows_ok(dx) || !rows_ok(out)))) return LCT_ERR_INVALID_ARG;
+    if (d_da && (!rows_ok(x) || !d_xa || !al(d_xa, 4) || !d_work || !al16(d_work))) return LCT_ERR_INVALID_ARG;
+    const Rows written[4] = {out, flat(d_da, d_da ? abytes : 0), flat(d_db, d_db ? bbytes : 0),
+                             flat(d_work, d_da ? work : 0)};
+    for (int i = 0; i < 4; ++i) {
+        if (!written[i].rows) continue;
+        if (!rows_apart(written[i], dy) || !rows_apart(written[i], x) || !apart_from_bank(written[i], g) ||
+            (d_da && !bytes_apart(written[i], d_xa, kept)))
+            return LCT_ERR_INVALID_ARG;
+        if (!(i == 0 && same_rows(out, dx)) && !rows_apart(written[i], dx)) return LCT_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 4; ++j)
+            if (!rows_apart(written[i], written[j])) return LCT_ERR_INVALID_ARG;
+    }
+    g.in = reinterpret_cast<const __nv_bfloat16 *>(d_dy);
+    g.ld_in = static_cast<int64_t>(ld_dy);
+    g.nin = g.n;
+    g.al_in = rows_al(dy);
+    if (d_dx_out) {
+        g.base = reinterpret_cast<const __nv_bfloat16 *>(d_dx);
+        g.ld_base = static_cast<int64_t>(ld_dx);
+        g.al_base = rows_al(dx);
+        g.out = reinterpret_cast<__nv_bfloat16 *>(d_dx_out);
+        g.ld_out = static_cast<int64_t>(ld_dx_out);
+        g.al_out = rows_al(out);
+    }
+    g.nout = g.k;
+    if (d_da) {
+        g.x = reinterpret_cast<const __nv_bfloat16 *>(d_x);
+        g.ld_x = static_cast<int64_t>(ld_x);
+        g.al_x = rows_al(x);
+        g.kept = d_xa;
+        g.work = static_cast<__nv_bfloat16 *>(d_work);
+        g.da = reinterpret_cast<__nv_bfloat16 *>(d_da);
+        g.db = reinterpret_cast<__nv_bfloat16 *>(d_db);
+    }
+    if (launch_adapter(g, true, s) != cudaSuccess) return LCT_ERR_CUDA;
+    if (d_da && launch_adapter_grad(g, s) != cudaSuccess) return LCT_ERR_CUDA;
+    return LCT_OK;
+}

@@ -4,6 +4,7 @@
 
 #include <cstdint>
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/lct.h"
@@ -162,5 +163,33 @@ struct GradArgs {
     double *part;  // device, kGradMaxParts
 };
 cudaError_t launch_grads(const GradArgs &a, bool clip, cudaStream_t s);
+
+// The adapters' kernels.  `in` is x and `base`, `out` are y and the result
+// (backward: dy, dx and the new dx).
+struct AdapterArgs {
+    const __nv_bfloat16 *a, *b;  // [adapters, rank, k], [adapters, n, rank]
+    const float *scale;
+    const int32_t *ranks;        // or NULL
+    const int32_t *order, *starts;
+    int32_t *tiles, *status;
+    const __nv_bfloat16 *in, *base;
+    __nv_bfloat16 *out;          // or NULL: no rows are wanted
+    const __nv_bfloat16 *x;      // backward: the forward pass's x
+    const float *kept;           // backward: its x A^T, [tokens, rank]
+    float *keep;                 // forward: where to put that, or NULL
+    __nv_bfloat16 *work;         // backward: s dy B and s x A^T as hi and lo, [2][tokens][2][rank16]
+    __nv_bfloat16 *da, *db;
+    int64_t ld_in, ld_base, ld_out, ld_x;
+    int32_t adapters, rank, rank16, k, n, nin, nout, tokens, rows;
+    bool al_a, al_b, al_in, al_base, al_out, al_x;  // rows begin at 16-byte boundaries
+};
+struct PlanArgs {
+    const int32_t *index;
+    int32_t *order, *starts, *tiles;
+    int32_t tokens, adapters, rows;
+};
+cudaError_t launch_adapter(const AdapterArgs &a, bool back, cudaStream_t s);
+cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s);
+cudaError_t launch_adapter_plan(const PlanArgs &a, cudaStream_t s);
 
 }  // namespace lct
