@@ -15,7 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
-from .matmul import compressed_linear
+from .matmul import compressed_linear, compressed_linear_input_grad
 
 
 def _need(ok: bool, what: str) -> None:
@@ -148,3 +148,35 @@ def adapter_grads(dy: torch.Tensor, x: torch.Tensor, xa: torch.Tensor, bank: Ada
     with B.on_device(bank.device.index):
         B.lct_adapter_backward(bank.desc, plan.desc, dym, xm, xa, dxm, om, da, db, work)
     return (None if dx is None else out), da, db
+
+
+class _AdapterLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, a, b, bank, plan, w, cb):
+        y = compressed_linear(x, w, cb, bank.n, bank.k)
+        out, xa = adapter_apply(x, bank, plan, y, out=y, keep=True)
+        ctx.save_for_backward(x, xa)
+        ctx.rest = (bank, plan, w, cb)
+        return out
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, xa = ctx.saved_tensors
+        bank, plan, w, cb = ctx.rest
+        dy = dy.contiguous()
+        dx = compressed_linear_input_grad(dy, w, cb, bank.n, bank.k) if ctx.needs_input_grad[0] else None
+        dx, da, db = adapter_grads(dy, x, xa, bank, plan, dx, out=dx)
+        return dx, da, db, None, None, None, None
+
+
+def adapter_linear(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_codebook, bank: AdapterBank,
+                   plan: AdapterPlan) -> torch.Tensor:
+    """y = x W^T + s_a (x A_a^T) B_a^T for a compressed frozen W [n, k] and each
+    token's own adapter; x [..., k] BF16 on CUDA.  Differentiable in x and in
+    the bank's a and b (leaves such as ``torch.nn.Parameter``); the weight is
+    decoded again for the gradient of x.  What it saves for backward goes
+    through ``compressed_activations`` like any other saved tensor."""
+    if torch.is_grad_enabled() and (x.requires_grad or bank.a.requires_grad or bank.b.requires_grad):
+        return _AdapterLinear.apply(x, bank.a, bank.b, bank, plan, w, cb)
+    y = compressed_linear(x, w, cb, bank.n, bank.k)
+    return adapter_apply(x, bank, plan, y, out=y)

@@ -857,7 +857,7 @@ lct_status check_bank(const lct_adapters *b, const lct_token_plan *p, AdapterArg
     if (!b->d_a || !b->d_b || !b->d_scale || !al(b->d_a, 2) || !al(b->d_b, 2) || !al(b->d_scale, 4) ||
         !al(b->d_ranks, 4))
         return LCT_ERR_INVALID_ARG;
-    if (!p->d_order || !p->d_starts || !p->d_tiles || !al(p->d_order, 4) || !al(p->d_starts, 4) || !al16(p->d_tiles))
+    if ((p->tokens && !p->d_order) || !p->d_starts || !p->d_tiles || !al(p->d_order, 4) || !al(p->d_starts, 4) || !al16(p->d_tiles))
         return LCT_ERR_INVALID_ARG;
     *g = AdapterArgs{};
     g->a = reinterpret_cast<const __nv_bfloat16 *>(b->d_a);

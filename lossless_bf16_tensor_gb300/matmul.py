@@ -103,3 +103,17 @@ def compressed_linear(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_codebook
     # every decode on the side stream finished before the main stream's last
     # GEMM, so the buffers (allocated on the main stream) can be freed as usual
     return yt.t().contiguous().reshape(*x.shape[:-1], out_features)
+
+
+def compressed_linear_input_grad(dy: torch.Tensor, w: B.CompressedTensor, cb: B.lct_codebook, out_features: int,
+                                 in_features: int) -> torch.Tensor:
+    """dx = dy @ W, the gradient of ``compressed_linear`` with respect to x: W
+    is decoded again and is dense for the length of this product."""
+    if w.n != out_features * in_features:
+        raise ValueError("weight size does not match its shape")
+    if dy.dtype != torch.bfloat16 or not dy.is_cuda or dy.shape[-1] != out_features:
+        raise ValueError("dy must be a CUDA BF16 tensor [..., out_features]")
+    dense = torch.empty(w.n, dtype=torch.bfloat16, device=dy.device)
+    B.lct_decode(w, cb, dense.view(torch.int16), torch.cuda.current_stream(dy.device))
+    return torch.mm(dy.reshape(-1, out_features), dense.view(out_features, in_features)).reshape(
+        *dy.shape[:-1], in_features)
