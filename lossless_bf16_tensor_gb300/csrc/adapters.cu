@@ -32,6 +32,7 @@ constexpr int kTileTokens = LCT_ADAPTER_TILE;
 constexpr int kChunk = 64;                        // columns of In (phase 1) or of the result (phase 2) at a time
 constexpr int kInBytes = kTileTokens * 128;       // a tile of 128 tokens by 64 BF16 columns
 constexpr uint32_t kTmemCols = 256;
+constexpr int kAdStages = 3;
 
 // ---------------------------------------------------------------- tcgen05
 
@@ -176,6 +177,29 @@ __device__ __forceinline__ uint32_t cluster_size()
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank)
+{
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ float4 peer_float4(uint32_t at)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void peer_store16(uint32_t at, uint4 v)
+{
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+// Writes before it, of this block's or of a peer's memory, are seen by products after it.
+__device__ __forceinline__ void fence_proxy_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
 __device__ __forceinline__ float peer_float(uint32_t addr, uint32_t rank)
 {
     uint32_t at;
@@ -226,27 +250,45 @@ __host__ __device__ inline AdapterSmem adapter_smem(int rank, int stages)
     return s;
 }
 
-// Loads the 128 x 64 tile of `m` at columns c0.. (of `cols`).
-__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16 *m, int64_t ld, const int *tok, int count,
-                                          int c0, int cols, bool aligned)
+// Where a thread's pieces lie in a tile of 128-byte rows: 8 threads a row, 32
+// rows at a time, so that its rows are 32 apart and its place in them is one.
+struct Place {
+    int row, col;    // its first row, and its first column of the 64
+    uint32_t at;     // byte offset of its first piece
+};
+__device__ __forceinline__ Place my_place()
 {
-    for (int i = threadIdx.x; i < count * 8; i += kAdThreads) {
-        const int row = i >> 3, c = i & 7, at = c0 + c * 8;
-        piece(dst + swz(row, c), m + tok[row] * ld + at, cols - at, aligned, m);
-    }
+    Place p;
+    p.row = threadIdx.x >> 3;
+    p.col = (threadIdx.x & 7) * 8;
+    p.at = swz(p.row, threadIdx.x & 7);
+    return p;
 }
 
-// Loads rows r0 .. r0 + nrows of a row-major matrix [rows, cols] with leading
-// dimension ld, columns c0 .. c0 + 8 * pieces, into 64-column tiles `atom`
-// bytes apart; what lies outside the matrix is zero.
-__device__ __forceinline__ void load_block(uint32_t dst, uint32_t atom, const __nv_bfloat16 *m, int64_t ld, int r0,
-                                           int rows, int nrows, int c0, int cols, int pieces, bool aligned)
+// Loads the 128 x 64 tile of `m` at columns c0.. (of `cols`), rows t[].
+__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16 *m, int64_t ld, const Place &p,
+                                          const int (&t)[4], int count, int c0, int cols, bool aligned)
 {
-    for (int i = threadIdx.x; i < nrows * pieces; i += kAdThreads) {
-        const int row = i / pieces, c = i - row * pieces, at = c0 + c * 8;
-        const int valid = r0 + row < rows ? cols - at : 0;
-        piece(dst + (c >> 3) * atom + swz(row, c & 7), m + (r0 + row) * ld + at, valid, aligned, m);
-    }
+    const int valid = cols - c0 - p.col;
+    const __nv_bfloat16 *at = m + c0 + p.col;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (p.row + 32 * q < count) piece(dst + p.at + q * 4096, at + t[q] * ld, valid, aligned, m);
+}
+
+// Loads rows r0 .. r0 + nrows (at most 128) of a row-major matrix [rows, cols]
+// with leading dimension ld, columns c0 .. c0 + 64; what lies outside the
+// matrix is zero.  `width` columns of the tile are looked at.
+__device__ __forceinline__ void load_block(uint32_t dst, const __nv_bfloat16 *m, int64_t ld, const Place &p, int r0,
+                                           int rows, int nrows, int c0, int cols, int width, bool aligned)
+{
+    if (p.col >= width) return;
+    const int valid = cols - c0 - p.col;
+    const __nv_bfloat16 *at = m + static_cast<int64_t>(r0 + p.row) * ld + c0 + p.col;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (p.row + 32 * q < nrows)
+            piece(dst + p.at + q * 4096, at + 32 * q * ld, r0 + p.row + 32 * q < rows ? valid : 0, aligned, m);
 }
 
 // Rows without an adapter: out = base, and nothing to keep.
@@ -280,9 +322,11 @@ __device__ __forceinline__ void copy_rows(const AdapterArgs &g, const int *tok, 
 //
 // BACK = false: In = x, W1 = A [R, K], W2 = B [N, R], V = s (x A^T).
 // BACK = true:  In = dy, W1 = B [N, R], W2 = A [R, K], V = s (dy B).
-template <bool BACK, int STAGES>
-__global__ void __launch_bounds__(kAdThreads, STAGES <= 3 ? 2 : 1) k_adapter(const __grid_constant__ AdapterArgs g)
+template <bool BACK, int RANK>
+__global__ void __launch_bounds__(kAdThreads, RANK <= 64 ? 2 : 1) k_adapter(const __grid_constant__ AdapterArgs g)
 {
+    constexpr int STAGES = kAdStages;
+    constexpr int UNITS = RANK / 16;  // a warp's share of V's units, at most
     extern __shared__ uint8_t raw[];
     __shared__ int tok[kTileTokens];
     __shared__ uint64_t done[STAGES];
@@ -324,22 +368,35 @@ __global__ void __launch_bounds__(kAdThreads, STAGES <= 3 ? 2 : 1) k_adapter(con
     const int n2 = all2 > (int)rank ? (all2 - rank + size - 1) / size : 0;
     const int n = n1 + n2;
 
+    const Place my = my_place();
+    int t[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) t[q] = my.row + 32 * q < count ? tok[my.row + 32 * q] : 0;
+
+    auto load_w = [&](uint32_t w, bool r_rows, const __nv_bfloat16 *m, int ld, int c0, int cols, bool aligned) {
+        if (r_rows) {  // A: R rows, 64 columns
+            load_block(w, m, ld, my, 0, used, r16, c0, cols, kChunk, aligned);
+        } else {       // B: 64 rows, R columns
+            load_block(w, m, ld, my, c0, cols, kChunk, 0, used, r16, aligned);
+            if (r16 > 64) load_block(w + 64 * 128, m, ld, my, c0, cols, kChunk, 64, used, r16 - 64, aligned);
+        }
+    };
     auto load = [&](int i) {
         const uint32_t slot = base + (i % STAGES) * lay.slot, w = slot + kInBytes;
         if (i < n1) {
             const int c0 = (rank + i * size) * kChunk;
-            load_rows(slot, g.in, g.ld_in, tok, count, c0, g.nin, g.al_in);
-            if (BACK)  // 64 rows of B, R columns
-                load_block(w, 64 * 128, B, g.rank, c0, g.n, kChunk, 0, used, r16 / 8, g.al_b);
-            else       // R rows of A, 64 columns
-                load_block(w, 0, A, g.k, 0, used, r16, c0, g.k, 8, g.al_a);
+            load_rows(slot, g.in, g.ld_in, my, t, count, c0, g.nin, g.al_in);
+            if (BACK)
+                load_w(w, false, B, g.rank, c0, g.n, g.al_b);
+            else
+                load_w(w, true, A, g.k, c0, g.k, g.al_a);
         } else if (i < n) {
             const int c0 = (rank + (i - n1) * size) * kChunk;
-            load_rows(slot, g.base, g.ld_base, tok, count, c0, g.nout, g.al_base);
+            load_rows(slot, g.base, g.ld_base, my, t, count, c0, g.nout, g.al_base);
             if (BACK)
-                load_block(w, 0, A, g.k, 0, used, r16, c0, g.k, 8, g.al_a);
+                load_w(w, true, A, g.k, c0, g.k, g.al_a);
             else
-                load_block(w, 64 * 128, B, g.rank, c0, g.n, kChunk, 0, used, r16 / 8, g.al_b);
+                load_w(w, false, B, g.rank, c0, g.n, g.al_b);
         }
         async_commit();
     };
@@ -375,10 +432,12 @@ __global__ void __launch_bounds__(kAdThreads, STAGES <= 3 ? 2 : 1) k_adapter(con
         tc_before();
         __syncthreads();
         // the same places that this thread loads next, so that no barrier is needed before that
-        for (int i = threadIdx.x; i < count * 8; i += kAdThreads) {
-            const int r = i >> 3, c = i & 7, at = c0 + c * 8;
-            const uint4 v = load16(slot + swz(r, c));
-            __nv_bfloat16 *o = g.out + tok[r] * g.ld_out + at;
+        const int at = c0 + my.col;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (my.row + 32 * q >= count) break;
+            const uint4 v = load16(slot + my.at + q * 4096);
+            __nv_bfloat16 *o = g.out + t[q] * g.ld_out + at;
             if (g.al_out && at + 8 <= g.nout) {
                 *reinterpret_cast<uint4 *>(o) = v;
             } else {
@@ -391,60 +450,69 @@ __global__ void __launch_bounds__(kAdThreads, STAGES <= 3 ? 2 : 1) k_adapter(con
         }
     };
 
-    // The block's partial sums, everyone's total, and V from it.
+    // V from the blocks' partial sums.  A unit is 8 of its columns for 32 rows,
+    // one row a lane; the cluster's blocks share the units out, and each one
+    // adds up its units' partial sums, block by block, and hands the result to
+    // every block.
     auto middle = [&]() {
         if (n1 > 0) waiter.wait(&done[(n1 - 1) % STAGES], ((n1 - 1) / STAGES) & 1);
         tc_after();
         __syncwarp();
-        const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-        const uint32_t v_at = base + lay.v_at;
-        const bool rows = (warp & 3) * 32 < count;
-        const int pieces = r16 / 8;
+        const uint32_t v_at = base + lay.v_at, lo_at = (g.rank > 64 ? 2 : 1) * lay.v_atom;
+        const int pieces = r16 / 8, quarter = warp & 3, half = warp >> 2;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        float sum[UNITS][8];
+        int piece_of[UNITS];
         if (size > 1) {
-            if (rows)
+            if (quarter * 32 < count)
                 for (int p = half; p < pieces; p += 2) {
                     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                     if (n1 > 0) {
-                        tmem_load8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + p * 8, v);
+                        tmem_load8(lanes + p * 8, v);
                         tmem_wait();
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(v_at + ((p * 8 + i) * kTileTokens + row) * 4),
-                                     "f"(v[i])
-                                     : "memory");
+                    const uint32_t at = v_at + (p * 2 * kTileTokens + quarter * 32 + lane) * 16;
+                    store16(at, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                           __float_as_uint(v[3])));
+                    store16(at + kTileTokens * 16, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
+                                                              __float_as_uint(v[6]), __float_as_uint(v[7])));
                 }
             __syncwarp();
             cluster_sync();
         }
-        float sum[8][8];
+        const int groups = (count + 31) / 32;  // of 32 rows
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int p = q * 2 + half;
-            if (rows && p < pieces) {
-                if (size > 1) {
+        for (int q = 0; q < UNITS; ++q) {
+            piece_of[q] = -1;
+            if (size > 1) {
+                // unit u is piece u / groups of rows u % groups
+                const int u = static_cast<int>(rank) + static_cast<int>(size) * (warp + 8 * q);
+                if (u >= pieces * groups) continue;
+                piece_of[q] = u / groups * 4 + u % groups;
+                const uint32_t at = v_at + (u / groups * 2 * kTileTokens + u % groups * 32 + lane) * 16;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sum[q][i] = 0.0f;
-                    for (uint32_t peer = 0; peer < size; ++peer)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (row < count)
-                                sum[q][i] += peer_float(v_at + ((p * 8 + i) * kTileTokens + row) * 4, peer);
-                } else {
-                    tmem_load8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + p * 8, sum[q]);
-                    tmem_wait();
+                for (int i = 0; i < 8; ++i) sum[q][i] = 0.0f;
+                for (uint32_t peer = 0; peer < size; ++peer) {
+                    const uint32_t there = peer_addr(at, peer);
+                    const float4 x = peer_float4(there), y = peer_float4(there + kTileTokens * 16);
+                    sum[q][0] += x.x, sum[q][1] += x.y, sum[q][2] += x.z, sum[q][3] += x.w;
+                    sum[q][4] += y.x, sum[q][5] += y.y, sum[q][6] += y.z, sum[q][7] += y.w;
                 }
+            } else if (half + 2 * q < pieces && quarter < groups) {
+                piece_of[q] = (half + 2 * q) * 4 + quarter;
+                tmem_load8(lanes + (half + 2 * q) * 8, sum[q]);
+                tmem_wait();
             }
         }
-        __syncwarp();
-        if (size > 1) cluster_sync();  // everyone has read the partial sums that V's place held
+        if (size > 1) {
+            __syncwarp();
+            cluster_sync();  // everyone has read the partial sums that V's place held
+        }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int p = q * 2 + half;
-            if (!rows || p >= pieces) continue;
-            const uint32_t at = v_at + (p >> 3) * lay.v_atom + swz(row, p & 7);
-            const uint32_t lo_at = (g.rank > 64 ? 2 : 1) * lay.v_atom;
-            const bool writes = row < count && p % size == rank;
+        for (int q = 0; q < UNITS; ++q) {
+            if (piece_of[q] < 0) continue;
+            const int p = piece_of[q] >> 2, row = (piece_of[q] & 3) * 32 + lane;
+            const bool writes = row < count;
             if (!BACK && g.keep && writes) {
                 float *k = g.keep + static_cast<int64_t>(tok[row]) * g.rank + p * 8;
 #pragma unroll
@@ -455,8 +523,17 @@ __global__ void __launch_bounds__(kAdThreads, STAGES <= 3 ? 2 : 1) k_adapter(con
             for (int i = 0; i < 8; ++i) sum[q][i] *= scale;
             uint4 hi, lo;
             split8(sum[q], hi, lo);
-            store16(at, hi);
-            store16(at + lo_at, lo);
+            const uint32_t at = v_at + (p >> 3) * lay.v_atom + swz(row, p & 7);
+            if (size > 1) {
+                for (uint32_t peer = 0; peer < size; ++peer) {
+                    const uint32_t there = peer_addr(at, peer);
+                    peer_store16(there, hi);
+                    peer_store16(there + lo_at, lo);
+                }
+            } else {
+                store16(at, hi);
+                store16(at + lo_at, lo);
+            }
             if (BACK && g.work && writes) {
                 // for the weights' gradients, in the plan's order: s dy B, and s (x A^T), as hi and lo
                 const int64_t line = static_cast<int64_t>(tile.y + row) * 2 * g.rank16 + p * 8;
@@ -478,9 +555,14 @@ __global__ void __launch_bounds__(kAdThreads, STAGES <= 3 ? 2 : 1) k_adapter(con
         if (!BACK && g.keep)
             for (int i = rank * kAdThreads + threadIdx.x; i < count * (g.rank - used); i += size * kAdThreads)
                 g.keep[static_cast<int64_t>(tok[i / (g.rank - used)]) * g.rank + used + i % (g.rank - used)] = 0.0f;
-        fence_proxy_async();
+        fence_proxy_all();
         tc_before();
-        __syncthreads();
+        __syncwarp();
+        if (size > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        fence_proxy_all();
         tc_after();
     };
 
@@ -574,23 +656,37 @@ __global__ void __launch_bounds__(kAdThreads, 2) k_adapter_grad(const __grid_con
         tc_after();
         tmem = tmem_at;
 
+        // 16 threads a row of 128 columns, or of V's hi and lo; 16 rows at a time
+        const int my_row = threadIdx.x >> 4, my_c = threadIdx.x & 15;
+        const uint32_t my_at = (my_c >> 3) * 64 * 128 + swz(my_row, my_c & 7);
+        int tok[4];  // the rows of the chunk that is loaded next, fetched one chunk early
+        auto next_tokens = [&](int i) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int at = first + (rank + i * size) * 64 + my_row + 16 * q;
+                tok[q] = at < last ? g.order[at] : 0;
+            }
+        };
+        next_tokens(0);
         auto load = [&](int i) {
             if (i < n) {
                 const uint32_t slot = base + (i % STAGES) * slot_bytes;
-                const int t0 = first + (rank + i * size) * 64;
-                for (int j = threadIdx.x; j < 64 * 16; j += kAdThreads) {
-                    const int row = j >> 4, c = j & 15, at = c0 + c * 8;
-                    const bool there = t0 + row < last;
-                    const int64_t t = there ? g.order[t0 + row] : 0;
-                    piece(slot + (c >> 3) * 64 * 128 + swz(row, c & 7), in + t * ld + at, there ? cols - at : 0, al, in);
+                const int t0 = first + (rank + i * size) * 64 + my_row;
+                const int at = c0 + my_c * 8;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const bool there = t0 + 16 * q < last;
+                    piece(slot + my_at + q * 2048, in + tok[q] * ld + at, there ? cols - at : 0, al, in);
                 }
-                const int pieces = r16 / 8;
-                for (int j = threadIdx.x; j < 64 * 2 * pieces; j += kAdThreads) {
-                    const int row = j / (2 * pieces), q = j - row * 2 * pieces, lo = q >= pieces, c = q - lo * pieces;
-                    const uint32_t dst = slot + 2 * 64 * 128 + lo * v_bytes + (c >> 3) * 64 * 128 + swz(row, c & 7);
-                    piece(dst, v + (static_cast<int64_t>(t0 + row) * 2 + lo) * g.rank16 + c * 8, t0 + row < last ? 8 : 0,
-                          true, v);
-                }
+                const __nv_bfloat16 *from = v + (static_cast<int64_t>(t0) * 2 + (my_c >> 3)) * g.rank16 + (my_c & 7) * 8;
+                const uint32_t to = slot + 2 * 64 * 128 + (my_c >> 3) * v_bytes + swz(my_row, my_c & 7);
+                for (int c = 0; c < r16; c += 64)
+                    if (c + (my_c & 7) * 8 < r16)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            piece(to + c * 128 + q * 2048, from + c + 32 * q * static_cast<int64_t>(g.rank16),
+                                  t0 + 16 * q < last ? 8 : 0, true, v);
+                next_tokens(i + 1);
             }
             async_commit();
         };
@@ -767,27 +863,32 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, uint32_t threads, uint32_t s
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Blocks of a cluster: enough that the tiles fill the GPU twice over, as far
-// as there are chunks to share out.
+// Blocks of a cluster: as many as keep the grid within what the GPU holds at
+// once, two blocks on each SM, and as there are chunks to share out.
 uint32_t cluster_for(uint64_t tiles, uint64_t chunks)
 {
     uint32_t c = 1;
-    while (c < 8 && tiles * c < 304 && 2ull * c <= chunks) c *= 2;
+    while (c < 8 && tiles * c * 2 <= 304 && 2ull * c <= chunks) c *= 2;
     return c;
 }
 
-constexpr int kStages = 3;
+template <bool BACK>
+cudaError_t launch_tokens(const AdapterArgs &a, uint32_t c, cudaStream_t s)
+{
+    const uint32_t smem = dev::adapter_smem(a.rank, dev::kAdStages).bytes;
+    const dim3 grid(c * a.rows);
+    return a.rank <= 64 ? launch(dev::k_adapter<BACK, 64>, grid, dev::kAdThreads, smem, c, s, a)
+                        : launch(dev::k_adapter<BACK, 128>, grid, dev::kAdThreads, smem, c, s, a);
+}
 
 }  // namespace
 
 cudaError_t launch_adapter(const AdapterArgs &a, bool back, cudaStream_t s)
 {
     const uint64_t chunks = (std::max(a.nin, a.out ? a.nout : 0) + 63) / 64;
-    const uint32_t c = cluster_for((a.tokens + 127) / 128 + std::min(a.adapters, a.tokens), chunks);
-    const uint32_t smem = dev::adapter_smem(a.rank, kStages).bytes;
-    const dim3 grid(c * a.rows);
-    return back ? launch(dev::k_adapter<true, kStages>, grid, dev::kAdThreads, smem, c, s, a)
-                : launch(dev::k_adapter<false, kStages>, grid, dev::kAdThreads, smem, c, s, a);
+    // half of the adapters' last tiles are empty ones at a guess
+    const uint32_t c = cluster_for(a.tokens / 128 + (std::min(a.adapters, a.tokens) + 1) / 2, chunks);
+    return back ? launch_tokens<true>(a, c, s) : launch_tokens<false>(a, c, s);
 }
 
 cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s)
