@@ -156,6 +156,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
+// What rounding v to the BF16 whose bits (as float32) are `kept` left out; an
+// infinite or NaN value has no remainder.
+__device__ __forceinline__ float rest(float v, uint32_t kept)
+{
+    const float h = __uint_as_float(kept);
+    return isfinite(h) ? v - h : 0.0f;
+}
+
 // Eight float32 as hi + lo, each eight BF16.
 __device__ __forceinline__ void split8(const float (&v)[8], uint4 &hi, uint4 &lo)
 {
@@ -163,9 +171,7 @@ __device__ __forceinline__ void split8(const float (&v)[8], uint4 &hi, uint4 &lo
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         h[i] = pack2(v[2 * i], v[2 * i + 1]);
-        // an infinite or NaN value has no remainder
-        const float a = __uint_as_float(h[i] << 16), b = __uint_as_float(h[i] & 0xFFFF0000u);
-        l[i] = pack2(isfinite(a) ? v[2 * i] - a : 0.0f, isfinite(b) ? v[2 * i + 1] - b : 0.0f);
+        l[i] = pack2(rest(v[2 * i], h[i] << 16), rest(v[2 * i + 1], h[i] & 0xFFFF0000u));
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);
@@ -197,6 +203,13 @@ __device__ __forceinline__ void peer_store16(uint32_t at, uint4 v)
     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
+// The two halves of a meeting of the cluster.
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Writes before it, of this block's or of a peer's memory, are seen by products after it.
 __device__ __forceinline__ void fence_proxy_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
@@ -609,6 +622,224 @@ __global__ void __launch_bounds__(kAdThreads, RANK <= 64 ? 2 : 1) k_adapter(cons
     if (warp == 0) tmem_free(tmem, kTmemCols);
 }
 
+// ------------------------------------------------ the forward of few tokens
+
+// Where requests bring a token each, an adapter has a handful of rows, and
+// what counts is how early its weights are asked for.  Here a cluster takes a
+// tile as before, but 16 rows at a time, by warp-wide 16 x 8 products (a tile
+// of 128 rows would be empty), in chunks of 128 columns that are all in flight
+// at once at the usual sizes: one round trip to memory, one meeting of the
+// cluster.  A tile of more than 16 rows makes more passes, its weights then
+// coming from L2.
+constexpr int kFewRows = 16, kFewCols = 128;
+
+template <int RT>
+struct Few {
+    static constexpr int kStages = RT == 16 ? 8 : RT == 32 ? 6 : 4;
+    static constexpr int kWBytes = RT * kFewCols * 2, kSlot = kWBytes + kFewRows * kFewCols * 2;
+    static constexpr int kSplitR = RT / 16, kSplitK = 8 / kSplitR;  // warps over R, and over a chunk's columns
+    static constexpr int kPart = kStages * kSlot;                    // [kSplitK][16][RT] float32
+    static constexpr int kSum = kPart + kSplitK * kFewRows * RT * 4; // [16][RT] float32
+    static constexpr int kV = kSum + kFewRows * RT * 4;              // hi, lo: [16][RT] BF16
+    static constexpr int kBytes = kV + 2 * kFewRows * RT * 2;
+};
+
+// 16-byte piece c of row r in rows of `pieces` pieces, so that eight rows'
+// pieces of one column lie in eight different 16-byte banks.
+template <int PIECES>
+__device__ __forceinline__ uint32_t few_at(int r, int c)
+{
+    const int x = PIECES >= 8 ? r & 7 : PIECES == 4 ? (r >> 1) & 3 : (r >> 2) & 1;
+    return (r * PIECES + (c ^ x)) * 16;
+}
+
+__device__ __forceinline__ void ldm4(uint32_t at, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int RT>
+__global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constant__ AdapterArgs g)
+{
+    using F = Few<RT>;
+    constexpr int S = F::kStages;
+    extern __shared__ __align__(128) uint8_t raw[];
+    __shared__ int tok[kTileTokens];
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    const int4 tile = reinterpret_cast<const int4 *>(g.tiles)[blockIdx.x / size];
+    const int count = min(tile.z, kTileTokens);
+    if (count <= 0) return;
+    for (int i = threadIdx.x; i < count; i += kAdThreads) tok[i] = g.order[tile.y + i];
+    const int a = tile.x;
+    const int used = a < 0 || a >= g.adapters ? 0 : used_rank(g, a);
+    __syncthreads();
+    if (used == 0) {
+        copy_rows(g, tok, count);
+        return;
+    }
+    const uint32_t base = smem_addr(raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const __nv_bfloat16 *A = g.a + static_cast<int64_t>(a) * g.rank * g.k;
+    const __nv_bfloat16 *B = g.b + static_cast<int64_t>(a) * g.rank * g.n;
+    const float scale = g.scale[a];
+    const int all1 = (g.nin + kFewCols - 1) / kFewCols, all2 = (g.nout + kFewCols - 1) / kFewCols;
+    const int n1 = all1 > (int)rank ? (all1 - rank + size - 1) / size : 0;
+    const int n2 = all2 > (int)rank ? (all2 - rank + size - 1) / size : 0;
+    const int n = n1 + n2;
+    // a thread's piece of a row tile
+    const int row = threadIdx.x >> 4, c16 = threadIdx.x & 15;
+    // a warp's part of the narrow product: 16 ranks from r0, and the 16-column steps k0, k0 + kSplitK ..
+    const int r0 = warp % F::kSplitR * 16, k0 = warp / F::kSplitR;
+
+    for (int first = 0; first < count; first += kFewRows) {
+        const int rows = min(kFewRows, count - first);
+        const int64_t t = row < rows ? tok[first + row] : 0;
+        auto load = [&](int i) {
+            const uint32_t slot = base + (i % S) * F::kSlot, tile_at = slot + F::kWBytes;
+            if (i < n1) {
+                const int c0 = (rank + i * size) * kFewCols, at = c0 + c16 * 8;
+                if (row < rows)
+                    piece(tile_at + few_at<16>(row, c16), g.in + t * g.ld_in + at, g.nin - at, g.al_in, g.in);
+#pragma unroll
+                for (int q = 0; q < RT / 16; ++q) {
+                    const int r = row + 16 * q;
+                    piece(slot + few_at<16>(r, c16), A + static_cast<int64_t>(r) * g.k + at, r < used ? g.k - at : 0,
+                          g.al_a, A);
+                }
+            } else if (i < n) {
+                const int c0 = (rank + (i - n1) * size) * kFewCols, at = c0 + c16 * 8;
+                if (row < rows)
+                    piece(tile_at + few_at<16>(row, c16), g.base + t * g.ld_base + at, g.nout - at, g.al_base, g.base);
+#pragma unroll
+                for (int q = 0; q < RT / 16; ++q) {
+                    constexpr int P = RT / 8;
+                    const int id = threadIdx.x + q * kAdThreads, r = id / P, c = id % P;
+                    piece(slot + few_at<P>(r, c), B + static_cast<int64_t>(c0 + r) * g.rank + c * 8,
+                          c0 + r < g.n ? used - c * 8 : 0, g.al_b, B);
+                }
+            }
+            async_commit();
+        };
+        for (int i = 0; i < S - 1; ++i) load(i);
+
+        // the narrow product
+        float acc[2][4] = {};
+        for (int i = 0; i < n1; ++i) {
+            async_wait<S - 2>();
+            __syncthreads();
+            load(i + S - 1);  // into the slot of chunk i - 1, which every warp has done with
+            const uint32_t slot = base + (i % S) * F::kSlot, tile_at = slot + F::kWBytes;
+#pragma unroll
+            for (int k = k0; k < 8; k += F::kSplitK) {
+                uint32_t x[4], w[4];
+                ldm4(tile_at + few_at<16>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4)), x);
+                ldm4(slot + few_at<16>(r0 + (lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1)), w);
+                mma16(acc[0], x, w[0], w[1]);
+                mma16(acc[1], x, w[2], w[3]);
+            }
+        }
+        // the block's sums, over its warps in their order
+        float *part = reinterpret_cast<float *>(raw + F::kPart), *sum = reinterpret_cast<float *>(raw + F::kSum);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                part[(k0 * kFewRows + lane / 4 + (j >> 1) * 8) * RT + r0 + h * 8 + (lane & 3) * 2 + (j & 1)] = acc[h][j];
+        __syncthreads();
+        for (int e = threadIdx.x; e < kFewRows * RT; e += kAdThreads) {
+            float v = 0.0f;
+#pragma unroll
+            for (int q = 0; q < F::kSplitK; ++q) v += part[q * kFewRows * RT + e];
+            sum[e] = v;
+        }
+        __syncwarp();
+        if (size > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        // everyone's, over the blocks in their order; V as hi and lo
+        for (int e = threadIdx.x; e < kFewRows * RT / 4; e += kAdThreads) {
+            const int r = e / (RT / 4), c = e % (RT / 4) * 4;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < rows) {
+                for (uint32_t peer = 0; peer < size; ++peer) {
+                    const float4 x = peer_float4(peer_addr(smem_addr(sum + e * 4), peer));
+                    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+                }
+                if (g.keep && e % size == rank) {
+                    const float k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)  // zero where the adapter has no such rank
+                        if (c + j < g.rank) g.keep[static_cast<int64_t>(tok[first + r]) * g.rank + c + j] = k[j];
+                }
+            }
+            v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+            const uint2 hi = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+            const uint2 lo = make_uint2(pack2(rest(v.x, hi.x << 16), rest(v.y, hi.x & 0xFFFF0000u)),
+                                        pack2(rest(v.z, hi.y << 16), rest(v.w, hi.y & 0xFFFF0000u)));
+            uint8_t *at = raw + F::kV + few_at<RT / 8>(r, c / 8) + (c & 4) * 2;
+            *reinterpret_cast<uint2 *>(at) = hi;
+            *reinterpret_cast<uint2 *>(at + kFewRows * RT * 2) = lo;
+        }
+        __syncwarp();
+        if (size > 1) cluster_arrive();  // the sums have been read
+        __syncthreads();
+
+        // the product back to the full width
+        for (int i = n1; i < n; ++i) {
+            async_wait<S - 2>();
+            __syncthreads();
+            load(i + S - 1);
+            const uint32_t slot = base + (i % S) * F::kSlot;
+            float d[2][4] = {};
+#pragma unroll
+            for (int k = 0; k < RT / 16; ++k) {
+                uint32_t hi[4], lo[4], w[4];
+                const uint32_t v = base + F::kV + few_at<RT / 8>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4));
+                ldm4(v, hi);
+                ldm4(v + kFewRows * RT * 2, lo);
+                ldm4(slot + few_at<RT / 8>(warp * 16 + (lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1)), w);
+                mma16(d[0], hi, w[0], w[1]);
+                mma16(d[0], lo, w[0], w[1]);
+                mma16(d[1], hi, w[2], w[3]);
+                mma16(d[1], lo, w[2], w[3]);
+            }
+            const int c0 = (rank + (i - n1) * size) * kFewCols;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // rows lane / 4 and 8 on, columns 2 (lane % 4) and 8 on
+                const int r = lane / 4 + (j & 1) * 8, h = j >> 1, col = warp * 16 + h * 8 + (lane & 3) * 2;
+                if (r >= rows || c0 + col >= g.nout) continue;
+                const uint32_t y = *reinterpret_cast<const uint32_t *>(raw + (slot - base) + F::kWBytes +
+                                                                       few_at<16>(r, col >> 3) + (col & 7) * 2);
+                const uint32_t o = pack2(__uint_as_float(y << 16) + d[h][(j & 1) * 2],
+                                         __uint_as_float(y & 0xFFFF0000u) + d[h][(j & 1) * 2 + 1]);
+                uint16_t *at = reinterpret_cast<uint16_t *>(g.out) + tok[first + r] * g.ld_out + c0 + col;
+                if (g.al_out && c0 + col + 1 < g.nout) {
+                    *reinterpret_cast<uint32_t *>(at) = o;
+                } else {
+                    at[0] = static_cast<uint16_t>(o);
+                    if (c0 + col + 1 < g.nout) at[1] = static_cast<uint16_t>(o >> 16);
+                }
+            }
+        }
+        async_wait<0>();
+        __syncwarp();
+        if (size > 1) cluster_wait();  // no block changes its sums, or leaves, before everyone has read them
+        __syncthreads();
+    }
+}
+
 // --------------------------------------------------- the weights' gradients
 
 // dA^T [K, R] = x^T (s dy B) and dB [N, R] = dy^T (s x A^T) of one adapter:
@@ -881,10 +1112,26 @@ cudaError_t launch_tokens(const AdapterArgs &a, uint32_t c, cudaStream_t s)
                         : launch(dev::k_adapter<BACK, 128>, grid, dev::kAdThreads, smem, c, s, a);
 }
 
+// The forward of few tokens: at most 16 an adapter on average.
+template <int RT>
+cudaError_t launch_few(const AdapterArgs &a, uint32_t c, cudaStream_t s)
+{
+    return launch(dev::k_adapter_few<RT>, dim3(c * a.rows), dev::kAdThreads, dev::Few<RT>::kBytes, c, s, a);
+}
+
 }  // namespace
 
 cudaError_t launch_adapter(const AdapterArgs &a, bool back, cudaStream_t s)
 {
+    if (!back && a.tokens <= 16ll * std::min(a.adapters, a.tokens)) {
+        const uint64_t few = (std::max(a.nin, a.nout) + dev::kFewCols - 1) / dev::kFewCols;
+        uint32_t c = 1;
+        while (c < 8 && a.rows * c * 2ull <= 608 && 2ull * c <= few) c *= 2;
+        return a.rank <= 16   ? launch_few<16>(a, c, s)
+               : a.rank <= 32 ? launch_few<32>(a, c, s)
+               : a.rank <= 64 ? launch_few<64>(a, c, s)
+                              : launch_few<128>(a, c, s);
+    }
     const uint64_t chunks = (std::max(a.nin, a.out ? a.nout : 0) + 63) / 64;
     // half of the adapters' last tiles are empty ones at a guess
     const uint32_t c = cluster_for(a.tokens / 128 + (std::min(a.adapters, a.tokens) + 1) / 2, chunks);
