@@ -18,9 +18,7 @@ from . import binding as B
 from .matmul import compressed_linear, compressed_linear_input_grad
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+_BF16 = torch.bfloat16
 
 
 class AdapterBank:
@@ -30,41 +28,47 @@ class AdapterBank:
     on one CUDA device; the tensors stay the caller's, and their values may
     change between calls."""
 
+    __slots__ = ("a", "b", "scale", "ranks", "adapters", "rank", "k", "n", "device", "desc")
+
     def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, ranks: torch.Tensor | None = None):
-        _need(a.dim() == 3 and b.dim() == 3 and b.shape[0] == a.shape[0] and b.shape[2] == a.shape[1],
-              "expected a [adapters, R, k] and b [adapters, n, R]")
-        _need(a.dtype == torch.bfloat16 and b.dtype == torch.bfloat16, "a and b must be BF16")
-        _need(scale.dtype == torch.float32 and scale.shape == a.shape[:1], "scale must be float32 [adapters]")
-        _need(ranks is None or (ranks.dtype == torch.int32 and ranks.shape == a.shape[:1]),
-              "ranks must be int32 [adapters]")
-        for t in (a, b, scale, ranks):
-            _need(t is None or (t.is_cuda and t.is_contiguous() and t.device == a.device),
-                  "the bank's tensors must be contiguous, on one CUDA device")
-        self.a, self.b, self.scale, self.ranks = a, b, scale, ranks
+        if a.dim() != 3 or b.dim() != 3:
+            raise ValueError("expected a [adapters, R, k] and b [adapters, n, R]")
         self.adapters, self.rank, self.k = a.shape
-        self.n = b.shape[1]
-        self.device = a.device
+        adapters, self.n, rank = b.shape
+        if adapters != self.adapters or rank != self.rank:
+            raise ValueError("expected a [adapters, R, k] and b [adapters, n, R]")
+        if a.dtype is not _BF16 or b.dtype is not _BF16:
+            raise ValueError("a and b must be BF16")
+        if scale.dtype is not torch.float32 or scale.shape != (adapters,):
+            raise ValueError("scale must be float32 [adapters]")
+        self.device = device = a.get_device()
+        if device < 0 or b.get_device() != device or scale.get_device() != device or not a.is_contiguous() \
+                or not b.is_contiguous() or not scale.is_contiguous():
+            raise ValueError("the bank's tensors must be contiguous, on one CUDA device")
+        if ranks is not None and (ranks.dtype is not torch.int32 or ranks.shape != (adapters,)
+                                  or not ranks.is_contiguous() or ranks.get_device() != device):
+            raise ValueError("ranks must be contiguous int32 [adapters] on the bank's device")
+        self.a, self.b, self.scale, self.ranks = a, b, scale, ranks
         self.desc = B.lct_adapters(a.data_ptr(), b.data_ptr(), scale.data_ptr(),
-                                   None if ranks is None else ranks.data_ptr(), self.adapters, self.rank, self.k,
-                                   self.n)
+                                   None if ranks is None else ranks.data_ptr(), adapters, rank, self.k, self.n)
 
 
 class AdapterPlan:
     """A batch's tokens grouped by adapter, as ``adapter_plan`` makes it:
     order [tokens], starts [adapters + 2] and tiles [rows, 4], all int32."""
 
+    __slots__ = ("order", "starts", "tiles", "tokens", "adapters", "device", "desc")
+
     def __init__(self, order: torch.Tensor, starts: torch.Tensor, tiles: torch.Tensor):
-        self.tokens, self.adapters = order.numel(), starts.numel() - 2
-        _need(tiles.dim() == 2 and tiles.shape[1] == 4 and self.adapters > 0
-              and tiles.shape[0] == B.lct_adapter_tile_rows(self.tokens, self.adapters),
-              "the tables do not belong to one plan")
+        self.tokens, self.adapters = tokens, adapters = order.numel(), starts.numel() - 2
+        if adapters <= 0 or tiles.shape != (B.lct_adapter_tile_rows(tokens, adapters), 4):
+            raise ValueError("the tables do not belong to one plan")
+        self.device = device = tiles.get_device()
         for t in (order, starts, tiles):
-            _need(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.device == tiles.device,
-                  "the plan's tables must be contiguous int32, on one CUDA device")
+            if t.dtype is not torch.int32 or t.get_device() != device or device < 0 or not t.is_contiguous():
+                raise ValueError("the plan's tables must be contiguous int32, on one CUDA device")
         self.order, self.starts, self.tiles = order, starts, tiles
-        self.device = tiles.device
-        self.desc = B.lct_token_plan(order.data_ptr(), starts.data_ptr(), tiles.data_ptr(), self.tokens,
-                                     self.adapters)
+        self.desc = B.lct_token_plan(order.data_ptr(), starts.data_ptr(), tiles.data_ptr(), tokens, adapters)
 
     def status(self) -> int:
         """The plan's latched status (0 is fine); synchronises."""
@@ -74,37 +78,43 @@ class AdapterPlan:
 def adapter_plan(index: torch.Tensor, adapters: int) -> AdapterPlan:
     """Group a batch's tokens by adapter; index is each token's adapter (int32,
     any shape, flattened), -1 for none."""
-    _need(index.dtype == torch.int32 and index.is_cuda and index.is_contiguous(),
-          "index must be a contiguous int32 CUDA tensor")
+    if index.dtype is not torch.int32 or not index.is_cuda or not index.is_contiguous():
+        raise ValueError("index must be a contiguous int32 CUDA tensor")
     tokens, adapters = index.numel(), int(adapters)
     if not 0 < adapters <= B.LCT_ADAPTER_MAX:
         raise B.LctError(B.LCT_ERR_UNSUPPORTED if adapters > 0 else B.LCT_ERR_INVALID_ARG, "adapter_plan")
     rows = B.lct_adapter_tile_rows(tokens, adapters)
-    # one allocation: the tile table first, which has to be aligned
-    buf = torch.empty(4 * rows + tokens + adapters + 2, dtype=torch.int32, device=index.device)
-    tiles, order, starts = buf.split([4 * rows, tokens, adapters + 2])
-    plan = AdapterPlan(order, starts, tiles.view(rows, 4))
-    with B.on_device(index.device.index):
-        B.lct_adapter_plan(index, adapters, order, starts, plan.tiles)
+    device = index.device
+    tiles = torch.empty((rows, 4), dtype=torch.int32, device=device)
+    order = torch.empty(tokens, dtype=torch.int32, device=device)
+    starts = torch.empty(adapters + 2, dtype=torch.int32, device=device)
+    plan = AdapterPlan(order, starts, tiles)
+    d = plan.desc
+    B.lct_adapter_plan(index, adapters, d.d_order, d.d_starts, d.d_tiles)
     return plan
 
 
-def _rows(t: torch.Tensor, cols: int, tokens: int, device: torch.device, what: str) -> torch.Tensor:
-    """t [..., cols] as a matrix of `tokens` rows."""
-    if t.dtype != torch.bfloat16 or t.device != device or t.shape[-1:] != (cols,) or t.numel() != tokens * cols:
-        raise ValueError("%s: expected a BF16 tensor of %d rows of %d on %s" % (what, tokens, cols, device))
-    m = t if t.dim() == 2 else t.view(tokens, cols)
-    if m.stride(1) != 1 and cols > 1:
-        raise ValueError("%s: values of a row must lie side by side" % what)
-    if m.stride(0) < cols:  # the stride of a single row means nothing
-        _need(tokens <= 1, "%s: rows must not overlap" % what)
-        m = m.as_strided((tokens, cols), (cols, 1))
-    return m
+def _rows(t: torch.Tensor, cols: int, tokens: int, device: int, what: str) -> tuple[int, int]:
+    """t [..., cols] as a matrix of `tokens` rows: (address, row stride)."""
+    if t.dtype is not _BF16 or t.get_device() != device or t.shape[-1:] != (cols,) or t.numel() != tokens * cols:
+        raise ValueError("%s: expected a BF16 tensor of %d rows of %d on CUDA device %d" % (what, tokens, cols, device))
+    if t.dim() != 2:
+        t = t.view(tokens, cols)
+    ld, one = t.stride()
+    if tokens <= 1:  # the stride of a single row means nothing
+        ld = cols
+    if (one != 1 and cols > 1) or ld < cols:
+        raise ValueError("%s: values of a row must lie side by side, and rows must not overlap" % what)
+    return t.data_ptr(), ld
 
 
 def _match(bank: AdapterBank, plan: AdapterPlan) -> None:
-    _need(plan.adapters == bank.adapters and plan.device == bank.device,
-          "the plan must be for the bank's adapters, on its device")
+    if plan.adapters != bank.adapters or plan.device != bank.device:
+        raise ValueError("the plan must be for the bank's adapters, on its device")
+
+
+def _new(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=_BF16, device=t.device)
 
 
 def adapter_apply(x: torch.Tensor, bank: AdapterBank, plan: AdapterPlan, y: torch.Tensor,
@@ -114,14 +124,13 @@ def adapter_apply(x: torch.Tensor, bank: AdapterBank, plan: AdapterPlan, y: torc
     may be y itself; by default it is a new tensor.  With `keep`, returns (out,
     xa): xa = x A_a^T, float32 [tokens, R], is what ``adapter_grads`` needs."""
     _match(bank, plan)
-    tokens = plan.tokens
-    xm, ym = _rows(x, bank.k, tokens, bank.device, "x"), _rows(y, bank.n, tokens, bank.device, "y")
+    tokens, device = plan.tokens, bank.device
+    xm, ym = _rows(x, bank.k, tokens, device, "x"), _rows(y, bank.n, tokens, device, "y")
     if out is None:
-        out = torch.empty(y.shape, dtype=torch.bfloat16, device=bank.device)
-    om = _rows(out, bank.n, tokens, bank.device, "out")
-    xa = torch.empty(tokens, bank.rank, dtype=torch.float32, device=bank.device) if keep else None
-    with B.on_device(bank.device.index):
-        B.lct_adapter_forward(bank.desc, plan.desc, xm, ym, om, xa)
+        out = _new(y)
+    om = _rows(out, bank.n, tokens, device, "out")
+    xa = torch.empty((tokens, bank.rank), dtype=torch.float32, device=x.device) if keep else None
+    B.lct_adapter_forward(bank.desc, plan.desc, device, xm, ym, om, xa.data_ptr() if keep else None)
     return (out, xa) if keep else out
 
 
@@ -132,21 +141,21 @@ def adapter_grads(dy: torch.Tensor, x: torch.Tensor, xa: torch.Tensor, bank: Ada
     adapters' part is added, into `out` (may be dx itself) or a new tensor; None
     where no gradient of x is wanted, and dx' is then None."""
     _match(bank, plan)
-    tokens = plan.tokens
-    dym, xm = _rows(dy, bank.n, tokens, bank.device, "dy"), _rows(x, bank.k, tokens, bank.device, "x")
-    if xa.dtype != torch.float32 or xa.shape != (tokens, bank.rank) or not xa.is_contiguous() \
-            or xa.device != bank.device:
+    tokens, device = plan.tokens, bank.device
+    dym, xm = _rows(dy, bank.n, tokens, device, "dy"), _rows(x, bank.k, tokens, device, "x")
+    if xa.dtype is not torch.float32 or xa.shape != (tokens, bank.rank) or not xa.is_contiguous() \
+            or xa.get_device() != device:
         raise ValueError("xa: expected contiguous float32 [tokens, R] on the bank's device")
-    dxm = om = None
+    dxm = om = (None, 0)
     if dx is not None:
-        dxm = _rows(dx, bank.k, tokens, bank.device, "dx")
+        dxm = _rows(dx, bank.k, tokens, device, "dx")
         if out is None:
-            out = torch.empty(dx.shape, dtype=torch.bfloat16, device=bank.device)
-        om = _rows(out, bank.k, tokens, bank.device, "out")
+            out = _new(dx)
+        om = _rows(out, bank.k, tokens, device, "out")
     da, db = torch.empty_like(bank.a), torch.empty_like(bank.b)
-    work = torch.empty(B.lct_adapter_work_bytes(tokens, bank.rank), dtype=torch.uint8, device=bank.device)
-    with B.on_device(bank.device.index):
-        B.lct_adapter_backward(bank.desc, plan.desc, dym, xm, xa, dxm, om, da, db, work)
+    work = torch.empty(B.lct_adapter_work_bytes(tokens, bank.rank), dtype=torch.uint8, device=x.device)
+    B.lct_adapter_backward(bank.desc, plan.desc, device, dym, xm, xa.data_ptr(), dxm, om, da.data_ptr(),
+                           db.data_ptr(), work.data_ptr())
     return (None if dx is None else out), da, db
 
 

@@ -144,26 +144,20 @@ def _stream(stream) -> int:
     return int(stream)
 
 
-class on_device:
-    """Makes `device` (an index, or None for the current one) the current
-    device for a block, at no cost where it already is; gives its index."""
-
-    def __init__(self, device):
-        self.device = device
-        self.before = None
-
-    def __enter__(self) -> int:
-        now = torch.cuda.current_device()
-        if self.device is None or self.device == now:
-            return now
-        torch.cuda.set_device(self.device)
-        self.before = now
-        return self.device
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            torch.cuda.set_device(self.before)
-        return False
+def _call(fn, what: str, device: int, *args, stream=None) -> None:
+    """fn(*args, stream) with `device` (an index) current, on its current
+    stream by default; a failure raises."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        stream = _stream(stream)
+    if torch._C._cuda_getDevice() == device:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc:
+        raise LctError(rc, what)
 
 
 def _model(m) -> int:
@@ -273,18 +267,18 @@ class GradArrays:
     alive.  A list that stays the same from step to step can keep its arrays."""
 
     def __init__(self, tensors, what: str = "gradients"):
-        self.tensors = ts = list(tensors)
+        self.tensors = ts = tensors if isinstance(tensors, (list, tuple)) else list(tensors)
+        self.count = len(ts)
+        try:
+            self.dtype = array.array("i", [_GRAD_DTYPES[t.dtype] for t in ts])
+        except KeyError as e:
+            raise LctError(LCT_ERR_UNSUPPORTED, "%s: expected BF16 or float32, not %s" % (what, e.args[0])) from None
         devices = set(map(torch.Tensor.get_device, ts))
         if -1 in devices or len(devices) > 1:
             raise ValueError("%s: expected CUDA tensors on one device" % what)
         if not all(map(torch.Tensor.is_contiguous, ts)):
             raise ValueError("%s: expected contiguous tensors" % what)
-        try:
-            self.dtype = array.array("i", [_GRAD_DTYPES[t.dtype] for t in ts])
-        except KeyError as e:
-            raise LctError(LCT_ERR_UNSUPPORTED, "%s: expected BF16 or float32, not %s" % (what, e.args[0])) from None
-        self.device = devices.pop() if devices else None
-        self.count = len(ts)
+        self.device = devices.pop() if devices else torch.cuda.current_device()
         self.ptr = array.array("Q", list(map(torch.Tensor.data_ptr, ts)))
         self.n = array.array("Q", list(map(torch.Tensor.numel, ts)))
 
@@ -293,16 +287,16 @@ class GradArrays:
 
 
 def lct_grad_norm(g: GradArrays, norm: torch.Tensor, work: torch.Tensor, stream=None) -> None:
-    _check(_lib.lct_grad_norm(g.ptr.buffer_info()[0], *g.args(), norm.data_ptr(), work.data_ptr(), _stream(stream)),
-           "lct_grad_norm")
+    _call(_lib.lct_grad_norm, "lct_grad_norm", g.device, g.ptr.buffer_info()[0], *g.args(), norm.data_ptr(),
+          work.data_ptr(), stream=stream)
 
 
 def lct_grad_clip(g: GradArrays, out: GradArrays, max_norm: float, norm: torch.Tensor, work: torch.Tensor,
                   stream=None) -> None:
-    if out is not g and (out.n != g.n or out.dtype != g.dtype):
-        raise ValueError("out must match the gradients' sizes and types")
-    _check(_lib.lct_grad_clip(g.ptr.buffer_info()[0], out.ptr.buffer_info()[0], *g.args(), max_norm, norm.data_ptr(),
-                              work.data_ptr(), _stream(stream)), "lct_grad_clip")
+    if out is not g and (out.n != g.n or out.dtype != g.dtype or (g.count and out.device != g.device)):
+        raise ValueError("out must match the gradients' sizes, types and device")
+    _call(_lib.lct_grad_clip, "lct_grad_clip", g.device, g.ptr.buffer_info()[0], out.ptr.buffer_info()[0], *g.args(),
+          max_norm, norm.data_ptr(), work.data_ptr(), stream=stream)
 
 
 def lct_adapter_tile_rows(tokens: int, adapters: int) -> int:
@@ -315,31 +309,25 @@ def lct_adapter_work_bytes(tokens: int, rank: int) -> int:
     return 8 * tokens * ((rank + 15) // 16 * 16)
 
 
-def lct_adapter_plan(index: torch.Tensor, adapters: int, order: torch.Tensor, starts: torch.Tensor,
-                     tiles: torch.Tensor, stream=None) -> None:
-    _check(_lib.lct_adapter_plan(index.data_ptr(), index.numel(), adapters, order.data_ptr(), starts.data_ptr(),
-                                 tiles.data_ptr(), _stream(stream)), "lct_adapter_plan")
+def lct_adapter_plan(index: torch.Tensor, adapters: int, order: int, starts: int, tiles: int, stream=None) -> None:
+    """order, starts and tiles are device addresses."""
+    _call(_lib.lct_adapter_plan, "lct_adapter_plan", index.get_device(), index.data_ptr(), index.numel(), adapters,
+          order, starts, tiles, stream=stream)
 
 
-def lct_adapter_forward(bank: lct_adapters, plan: lct_token_plan, x, y, out, xa=None, stream=None) -> None:
-    """x, y and out are 2-D BF16 tensors with unit column stride; xa is float32
-    [tokens, rank] or None."""
-    _check(_lib.lct_adapter_forward(ctypes.addressof(bank), ctypes.addressof(plan), x.data_ptr(), x.stride(0),
-                                    y.data_ptr(), y.stride(0), out.data_ptr(), out.stride(0),
-                                    None if xa is None else xa.data_ptr(), _stream(stream)), "lct_adapter_forward")
+def lct_adapter_forward(bank: lct_adapters, plan: lct_token_plan, device: int, x, y, out, xa=None,
+                        stream=None) -> None:
+    """x, y and out are (device address, row stride) of BF16 matrices; xa is a
+    device address or None."""
+    _call(_lib.lct_adapter_forward, "lct_adapter_forward", device, ctypes.addressof(bank), ctypes.addressof(plan),
+          *x, *y, *out, xa, stream=stream)
 
 
-def lct_adapter_backward(bank: lct_adapters, plan: lct_token_plan, dy, x=None, xa=None, dx=None, dx_out=None, da=None,
-                         db=None, work=None, stream=None) -> None:
-    def at(t):
-        return None if t is None else t.data_ptr()
-
-    def ld(t):
-        return 0 if t is None else t.stride(0)
-
-    _check(_lib.lct_adapter_backward(ctypes.addressof(bank), ctypes.addressof(plan), at(dy), ld(dy), at(x), ld(x),
-                                     at(xa), at(dx), ld(dx), at(dx_out), ld(dx_out), at(da), at(db), at(work),
-                                     _stream(stream)), "lct_adapter_backward")
+def lct_adapter_backward(bank: lct_adapters, plan: lct_token_plan, device: int, dy, x=(None, 0), xa=None,
+                         dx=(None, 0), dx_out=(None, 0), da=None, db=None, work=None, stream=None) -> None:
+    """Matrices and addresses as in lct_adapter_forward; None leaves one out."""
+    _call(_lib.lct_adapter_backward, "lct_adapter_backward", device, ctypes.addressof(bank), ctypes.addressof(plan),
+          *dy, *x, xa, *dx, *dx_out, da, db, work, stream=stream)
 
 
 def lct_debug_wait_timeout(header: torch.Tensor, work: torch.Tensor, limit_ns: int, stream=None) -> None:

@@ -522,33 +522,32 @@ cudaError_t launch_grads(const GradArgs &a, bool clip, cudaStream_t s)
 namespace {
 
 // No output may touch another output, and none may touch a gradient but its
-// own, in place.
+// own, in place.  Buckets come in the order of their addresses, so sorting is
+// mostly a look that finds them sorted.
 bool grads_apart(const GradArgs &a)
 {
     struct R {
         uintptr_t lo, hi;
-        uint64_t tensor;
-        int kind;  // 0 gradient, 1 output, 2 both (in place)
     };
-    std::vector<R> r;
-    r.reserve(2 * a.count);
+    std::vector<R> out, in;  // outputs (with the gradients in place), and the other gradients
+    out.reserve(a.count);
     for (uint64_t i = 0; i < a.count; ++i) {
         if (!a.n[i]) continue;
         const uint64_t bytes = a.n[i] * (a.dtype[i] == LCT_DTYPE_F32 ? 4 : 2);
         const uintptr_t g = reinterpret_cast<uintptr_t>(a.src[i]), o = reinterpret_cast<uintptr_t>(a.dst[i]);
-        if (g == o)
-            r.push_back({g, g + bytes, i, 2});
-        else {
-            r.push_back({g, g + bytes, i, 0});
-            r.push_back({o, o + bytes, i, 1});
-        }
+        out.push_back({o, o + bytes});
+        if (g != o) in.push_back({g, g + bytes});
     }
-    std::sort(r.begin(), r.end(), [](const R &x, const R &y) { return x.lo < y.lo; });
-    uintptr_t any_hi = 0, out_hi = 0;  // furthest end of any range, and of an output, so far
-    for (const R &x : r) {
-        if (x.kind ? x.lo < any_hi : x.lo < out_hi) return false;
-        any_hi = std::max(any_hi, x.hi);
-        if (x.kind) out_hi = std::max(out_hi, x.hi);
+    const auto less = [](const R &x, const R &y) { return x.lo < y.lo; };
+    for (auto *v : {&out, &in})
+        if (!std::is_sorted(v->begin(), v->end(), less)) std::sort(v->begin(), v->end(), less);
+    for (size_t i = 1; i < out.size(); ++i)
+        if (out[i].lo < out[i - 1].hi) return false;
+    // gradients may overlap one another, so each is held against the outputs on its own
+    size_t k = 0;
+    for (const R &x : in) {
+        while (k < out.size() && out[k].hi <= x.lo) ++k;
+        if (k < out.size() && out[k].lo < x.hi) return false;
     }
     return true;
 }

@@ -22,9 +22,10 @@ def _arrays(tensors, what: str) -> B.GradArrays:
     return tensors if isinstance(tensors, B.GradArrays) else B.GradArrays(tensors, what)
 
 
-def _buffers(device: int) -> tuple[torch.Tensor, torch.Tensor]:
+def _buffers(g: B.GradArrays) -> tuple[torch.Tensor, torch.Tensor]:
     """The norm and the calls' scratch, from one allocation."""
-    buf = torch.empty(_SCRATCH + 4, dtype=torch.float32, device=torch.device("cuda", device))
+    device = g.tensors[0].device if g.count else torch.device("cuda", g.device)
+    buf = torch.empty(_SCRATCH + 4, dtype=torch.float32, device=device)
     return buf[_SCRATCH], buf
 
 
@@ -33,9 +34,8 @@ def grad_norm(grads) -> torch.Tensor:
     CUDA tensors on one device), a float32 scalar there.  An empty list gives
     0."""
     g = _arrays(grads, "gradients")
-    with B.on_device(g.device) as device:
-        norm, work = _buffers(device)
-        B.lct_grad_norm(g, norm, work)
+    norm, work = _buffers(g)
+    B.lct_grad_norm(g, norm, work)
     return norm
 
 
@@ -45,9 +45,6 @@ def clip_grads(grads, max_norm: float, out=None) -> torch.Tensor:
     clipping, a float32 scalar on the device."""
     g = _arrays(grads, "gradients")
     o = g if out is None else _arrays(out, "out")
-    if o.device != g.device:
-        raise ValueError("out must be on the gradients' device")
-    with B.on_device(g.device) as device:
-        norm, work = _buffers(device)
-        B.lct_grad_clip(g, o, max_norm, norm, work)
+    norm, work = _buffers(g)
+    B.lct_grad_clip(g, o, max_norm, norm, work)
     return norm
