@@ -31,8 +31,6 @@ constexpr int kAdThreads = 256;
 constexpr int kTileTokens = LCT_ADAPTER_TILE;
 constexpr int kChunk = 64;                        // columns of In (phase 1) or of the result (phase 2) at a time
 constexpr int kInBytes = kTileTokens * 128;       // a tile of 128 tokens by 64 BF16 columns
-constexpr uint32_t kTmemCols = 256;
-constexpr int kAdStages = 3;
 
 // ---------------------------------------------------------------- tcgen05
 
@@ -132,22 +130,43 @@ __device__ __forceinline__ uint4 load16(uint32_t src)
     return v;
 }
 
-// `valid` (at most 8) BF16 values at src into a 16-byte piece, the rest zero.
-// Aligned pieces travel asynchronously; others are put together here.
+// `valid` (at most 8) BF16 values at src, at any address, the rest zero.
+__device__ __forceinline__ uint4 gather8(const __nv_bfloat16 *src, int valid)
+{
+    const uint16_t *p = reinterpret_cast<const uint16_t *>(src);
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (valid >= 8) {
+        if (reinterpret_cast<uintptr_t>(p) & 2) {
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(p + 1);
+            const uint32_t h = p[0], a = q[0], b = q[1], c = q[2], t = p[7];
+            w[0] = h | a << 16;
+            w[1] = __funnelshift_r(a, b, 16);
+            w[2] = __funnelshift_r(b, c, 16);
+            w[3] = c >> 16 | t << 16;
+        } else {
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = q[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+            if (i < valid) w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The same into a 16-byte piece of shared memory: asynchronously where the
+// address allows it.
 __device__ __forceinline__ void piece(uint32_t dst, const __nv_bfloat16 *src, int valid, bool aligned,
                                       const void *anywhere)
 {
     if (aligned) {
         const uint32_t bytes = valid <= 0 ? 0u : static_cast<uint32_t>(min(valid, 8)) * 2;
         async16(dst, bytes ? static_cast<const void *>(src) : anywhere, bytes);
-        return;
+    } else {
+        store16(dst, gather8(src, valid));
     }
-    const uint16_t *p = reinterpret_cast<const uint16_t *>(src);
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < valid) w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
-    store16(dst, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b)
@@ -234,74 +253,528 @@ __device__ __forceinline__ void fail(const AdapterArgs &g)
     if (g.status) atomicCAS(reinterpret_cast<unsigned int *>(g.status), 0u, static_cast<unsigned int>(LCT_ERR_TIMEOUT));
 }
 
-// Waits for products to be done; after one wait that ran out none waits again.
+// Waits at a barrier, bounded by the SM's clock (a wait is a second or two
+// long at the most; reading %globaltimer once in every wait that does not pass
+// at once costs microseconds each).  After one wait that ran out, none waits
+// again.
+constexpr long long kWaitClocks = 2000000000ll;
 struct Waiter {
     bool dead = false;
+    template <typename Try>
+    __device__ __forceinline__ void until(Try ready)
+    {
+        if (dead || ready()) return;
+        const long long t0 = clock64();
+        while (!ready())
+            if (clock64() - t0 > kWaitClocks) {
+                dead = true;
+                return;
+            }
+    }
     __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity)
     {
-        if (!dead && !mbar_wait(bar, parity, kDefaultWaitNs)) dead = true;
+        until([&] { return mbar_try(bar, parity); });
     }
 };
 
+// A meeting of the cluster's eight result warps: each warp arrives at every
+// block's barrier, and waits at its own.
+__device__ __forceinline__ void arrive_cluster(uint64_t *bar, uint32_t size, int lane)
+{
+    __syncwarp();
+    if (lane < static_cast<int>(size)) {
+        const uint32_t there = peer_addr(smem_addr(bar), lane);
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(there) : "memory");
+    }
+}
+__device__ __forceinline__ bool try_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void wait_cluster(Waiter &w, uint64_t *bar, uint32_t parity)
+{
+    w.until([&] { return try_cluster(bar, parity); });
+}
+
+// The result warps alone.
+__device__ __forceinline__ void out_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+__device__ __forceinline__ uint16_t load2(uint32_t at)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// t[j / 4] of a thread's rows, without an index into registers.
+__device__ __forceinline__ int row_token(const int (&t)[8], int j)
+{
+    int v = t[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        if (j >> 2 == i) v = t[i];
+    return v;
+}
+
 // ------------------------------------------------------- the tokens' part
 
-// Shared memory: a ring of `stages` slots, each a 128 x 64 tile of In (or of
-// the row to add to) and a tile of W1 or W2; then V, hi and lo, whose space
-// first holds the block's partial sums.
-struct AdapterSmem {
-    uint32_t w_bytes, slot, v_at, v_atom, bytes;
+// Warps by what they do: eight turn sums into results, one issues the
+// products, four load.  They meet at mbarriers only, so that a load never
+// waits for a result to be written.
+constexpr int kOutWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 4;
+constexpr int kTokThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kSums = 4;  // tiles of sums of the second product in TMEM, beside the narrow one's
+constexpr uint32_t kTmemCols = 512;
+
+// Shared memory: a ring of slots, each a 128 x 64 tile of In (or of the row to
+// add to) and a tile of W1 or W2; then V, hi and lo, whose space first holds
+// the block's partial sums.  It takes the whole SM.
+template <int RANK>
+struct Tok {
+    static constexpr int kAtoms = RANK / 64;
+    static constexpr uint32_t kWBytes = kAtoms * 64 * 128, kSlot = kInBytes + kWBytes;
+    static constexpr uint32_t kVAtom = kTileTokens * 128, kVLo = kAtoms * kVAtom;
+    static constexpr int kStages = RANK <= 64 ? 8 : 5;
+    static constexpr int kLag = kStages - 3;  // loads in flight before a chunk is said to be there
+    static constexpr uint32_t kVAt = kStages * kSlot;
+    static constexpr uint32_t kBytes = kVAt + 2 * kVLo + 1024;  // room to start at a 1024-byte boundary
+    static constexpr int kUnits = RANK / 16;  // a warp's share of V's units, at most
 };
-__host__ __device__ inline AdapterSmem adapter_smem(int rank, int stages)
-{
-    AdapterSmem s;
-    const uint32_t atoms = rank > 64 ? 2 : 1;
-    s.w_bytes = atoms * 64 * 128;
-    s.slot = kInBytes + s.w_bytes;
-    s.v_at = s.slot * stages;
-    s.v_atom = kTileTokens * 128;
-    s.bytes = s.v_at + 2 * atoms * s.v_atom + 1024;  // room to start at a 1024-byte boundary
-    return s;
-}
 
-// Where a thread's pieces lie in a tile of 128-byte rows: 8 threads a row, 32
-// rows at a time, so that its rows are 32 apart and its place in them is one.
-struct Place {
-    int row, col;    // its first row, and its first column of the 64
-    uint32_t at;     // byte offset of its first piece
+// One row of the plan's table, as a cluster's blocks share it.
+struct TileWork {
+    int a, first, count;  // count 0: no more tiles
+    int used, r16;
+    int n1, n2;           // this block's chunks of the two products
 };
-__device__ __forceinline__ Place my_place()
+__device__ __forceinline__ TileWork tile_work(const AdapterArgs &g, int i, uint32_t rank, uint32_t size)
 {
-    Place p;
-    p.row = threadIdx.x >> 3;
-    p.col = (threadIdx.x & 7) * 8;
-    p.at = swz(p.row, threadIdx.x & 7);
-    return p;
+    TileWork w = {};
+    if (i >= g.rows) return w;
+    const int4 t = reinterpret_cast<const int4 *>(g.tiles)[i];
+    w.a = t.x;
+    w.first = t.y;
+    w.count = min(t.z, kTileTokens);
+    w.used = t.x < 0 || t.x >= g.adapters || w.count <= 0 ? 0 : used_rank(g, t.x);
+    w.r16 = (w.used + 15) & ~15;
+    const int all1 = w.used ? (g.nin + kChunk - 1) / kChunk : 0;
+    // rows without an adapter are copied, in place there is nothing to do
+    const int all2 = g.out && (w.used || g.out != g.base) ? (g.nout + kChunk - 1) / kChunk : 0;
+    w.n1 = all1 > static_cast<int>(rank) ? (all1 - rank + size - 1) / size : 0;
+    w.n2 = all2 > static_cast<int>(rank) ? (all2 - rank + size - 1) / size : 0;
+    return w;
 }
 
-// Loads the 128 x 64 tile of `m` at columns c0.. (of `cols`), rows t[].
-__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16 *m, int64_t ld, const Place &p,
-                                          const int (&t)[4], int count, int c0, int cols, bool aligned)
+// N 16-byte pieces, 2048 bytes apart in the tile: src(q) and how many of its
+// values are there.  Pieces that do not travel asynchronously are all fetched
+// before the first is stored.
+template <int N, typename Src, typename Valid>
+__device__ __forceinline__ void pieces(uint32_t dst, bool aligned, const void *anywhere, Src src, Valid valid)
 {
-    const int valid = cols - c0 - p.col;
-    const __nv_bfloat16 *at = m + c0 + p.col;
+    if (aligned) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        if (p.row + 32 * q < count) piece(dst + p.at + q * 4096, at + t[q] * ld, valid, aligned, m);
+        for (int q = 0; q < N; ++q) {
+            const int v = valid(q);
+            const uint32_t bytes = v <= 0 ? 0u : static_cast<uint32_t>(min(v, 8)) * 2;
+            async16(dst + q * 2048, bytes ? static_cast<const void *>(src(q)) : anywhere, bytes);
+        }
+    } else {
+        uint4 x[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q) x[q] = gather8(src(q), valid(q));
+#pragma unroll
+        for (int q = 0; q < N; ++q) store16(dst + q * 2048, x[q]);
+    }
 }
 
-// Loads rows r0 .. r0 + nrows (at most 128) of a row-major matrix [rows, cols]
-// with leading dimension ld, columns c0 .. c0 + 64; what lies outside the
-// matrix is zero.  `width` columns of the tile are looked at.
-__device__ __forceinline__ void load_block(uint32_t dst, const __nv_bfloat16 *m, int64_t ld, const Place &p, int r0,
-                                           int rows, int nrows, int c0, int cols, int width, bool aligned)
+// Tiles of at most 128 tokens of one adapter, by clusters that take tiles in
+// turn.  A cluster's blocks take every c-th 64-column chunk of In for the
+// narrow product, add up their partial sums through each other's shared memory
+// in a fixed order, and take every c-th chunk of the result for the second
+// product.  Loads run on through both products and into the next tile.
+//
+// BACK = false: In = x, W1 = A [R, K], W2 = B [N, R], V = s (x A^T).
+// BACK = true:  In = dy, W1 = B [N, R], W2 = A [R, K], V = s (dy B).
+template <bool BACK, int RANK>
+__global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constant__ AdapterArgs g)
 {
-    if (p.col >= width) return;
-    const int valid = cols - c0 - p.col;
-    const __nv_bfloat16 *at = m + static_cast<int64_t>(r0 + p.row) * ld + c0 + p.col;
+    using T = Tok<RANK>;
+    constexpr int S = T::kStages;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[S], done[S], out_free[S], narrow, sum_free[kSums], meet[3];
+    __shared__ uint32_t tmem_at;
+
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    const int clusters = gridDim.x / size, first_tile = blockIdx.x / size;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u, v_at = base + T::kVAt;
+
+    if (warp == 0) tmem_alloc(&tmem_at, kTmemCols);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], kLoadWarps);
+            mbar_init(&done[i], 1);
+            mbar_init(&out_free[i], 4);
+        }
+        mbar_init(&narrow, 1);
+        for (int i = 0; i < kSums; ++i) mbar_init(&sum_free[i], 4);
+        for (int i = 0; i < 3; ++i) mbar_init(&meet[i], kOutWarps * size);
+        fence_mbar_init();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (size > 1) cluster_sync();
+    const uint32_t tmem = tmem_at;
+    Waiter waiter;
+
+    if (warp >= kLoadWarp) {
+        // ------------------------------------------------------------ loads
+        const int id = threadIdx.x - 32 * kLoadWarp;
+        const int row0 = id >> 3, col = (id & 7) * 8;  // 8 threads a row of 64 columns, 16 rows at a time
+        const uint32_t at = swz(row0, id & 7);
+        uint32_t second = 0, out_parity = 0;  // bit s: slot s last held a chunk of the second product; its next phase
+        int i = 0;
+        auto rows = [&](uint32_t dst, const __nv_bfloat16 *m, int64_t ld, const int (&t)[8], int count, int c0, int cols,
+                        bool aligned) {
+            const __nv_bfloat16 *from = m + c0 + col;
+            const int valid = cols - c0 - col;
+            // rows past the tile's tokens stay as they are: they reach only themselves
+            if (count > 64)
+                pieces<8>(dst + at, aligned, m, [&](int q) { return from + t[q] * ld; },
+                          [&](int q) { return row0 + 16 * q < count ? valid : 0; });
+            else if (count > 16)
+                pieces<4>(dst + at, aligned, m, [&](int q) { return from + t[q] * ld; },
+                          [&](int q) { return row0 + 16 * q < count ? valid : 0; });
+            else
+                pieces<1>(dst + at, aligned, m, [&](int q) { return from + t[q] * ld; },
+                          [&](int q) { return row0 + 16 * q < count ? valid : 0; });
+        };
+        for (int tile = first_tile;; tile += clusters) {
+            const TileWork w = tile_work(g, tile, rank, size);
+            if (w.count <= 0) break;
+            int t[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        if (p.row + 32 * q < nrows)
-            piece(dst + p.at + q * 4096, at + 32 * q * ld, r0 + p.row + 32 * q < rows ? valid : 0, aligned, m);
+            for (int q = 0; q < 8; ++q) t[q] = row0 + 16 * q < w.count ? g.order[w.first + row0 + 16 * q] : 0;
+            const __nv_bfloat16 *A = g.a + static_cast<int64_t>(w.a) * g.rank * g.k;
+            const __nv_bfloat16 *B = g.b + static_cast<int64_t>(w.a) * g.rank * g.n;
+            for (int k = 0; k < w.n1 + w.n2; ++k, ++i) {
+                const int s = i % S;
+                if (i >= S) {
+                    if (second >> s & 1) {
+                        waiter.wait(&out_free[s], out_parity >> s & 1);
+                        out_parity ^= 1u << s;
+                    } else {
+                        waiter.wait(&done[s], (i / S - 1) & 1);
+                    }
+                }
+                const uint32_t slot = base + s * T::kSlot, wt = slot + kInBytes;
+                const bool two = k >= w.n1;
+                const int c0 = (rank + (two ? k - w.n1 : k) * size) * kChunk;
+                if (two)
+                    rows(slot, g.base, g.ld_base, t, w.count, c0, g.nout, g.al_base);
+                else
+                    rows(slot, g.in, g.ld_in, t, w.count, c0, g.nin, g.al_in);
+                second = (second & ~(1u << s)) | (static_cast<uint32_t>(two) << s);
+                if (!w.used) {
+                    // nothing to multiply with
+                } else if (two == BACK) {  // A: R rows, 64 columns
+                    const __nv_bfloat16 *from = A + static_cast<int64_t>(row0) * g.k + c0 + col;
+                    const int valid = g.k - c0 - col;
+#pragma unroll
+                    for (int h = 0; h < T::kAtoms * 4; h += 4) {  // 64 rows at a time
+                        if (16 * h >= w.r16) break;
+                        pieces<4>(wt + at + h * 2048, g.al_a, A,
+                                  [&](int q) { return from + static_cast<int64_t>(16 * (q + h)) * g.k; },
+                                  [&](int q) { return row0 + 16 * (q + h) < w.used ? valid : 0; });
+                    }
+                } else {  // B: 64 rows, R columns
+                    const __nv_bfloat16 *from = B + static_cast<int64_t>(c0 + row0) * g.rank + col;
+#pragma unroll
+                    for (int h = 0; h < T::kAtoms; ++h) {
+                        if (col + 64 * h >= w.r16) break;
+                        pieces<4>(wt + at + h * 64 * 128, g.al_b, B,
+                                  [&](int q) { return from + 64 * h + static_cast<int64_t>(16 * q) * g.rank; },
+                                  [&](int q) { return c0 + row0 + 16 * q < g.n ? w.used - col - 64 * h : 0; });
+                    }
+                }
+                async_commit();
+                if (i >= T::kLag) {  // the chunk kLag back has landed
+                    async_wait<T::kLag>();
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[(i - T::kLag) % S]);
+                }
+            }
+        }
+        async_wait<0>();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0)
+            for (int j = max(0, i - T::kLag); j < i; ++j) mbar_arrive(&full[j % S]);
+    } else if (warp == kMmaWarp) {
+        // --------------------------------------------------------- products
+        int i = 0, q = 0, tiles = 0;  // chunks, chunks of second products, tiles with a product
+        uint64_t *last = nullptr;
+        for (int tile = first_tile;; tile += clusters) {
+            const TileWork w = tile_work(g, tile, rank, size);
+            if (w.count <= 0) break;
+            const uint32_t word1 = mma_word(w.r16, false, BACK), word2 = mma_word(kChunk, false, BACK);
+            for (int k = 0; k < w.n1 + w.n2; ++k, ++i) {
+                const int s = i % S;
+                const uint32_t slot = base + s * T::kSlot, wt = slot + kInBytes;
+                waiter.wait(&full[s], (i / S) & 1);
+                if (k < w.n1) {
+                    tc_after();
+                    if (lane == 0 && !waiter.dead) {
+#pragma unroll
+                        for (int j = 0; j < kChunk / 16; ++j)
+                            mma(tmem, operand(slot + j * 32, 0),
+                                BACK ? operand(wt + j * 16 * 128, 64 * 128) : operand(wt + j * 32, 0), word1,
+                                k > 0 || j > 0);
+                        mma_commit(&done[s]);
+                        if (k == w.n1 - 1) mma_commit(&narrow);
+                    }
+                } else {
+                    if (k == w.n1 && w.used) {
+                        wait_cluster(waiter, &meet[2], tiles & 1);  // V is there
+                        fence_proxy_all();
+                    }
+                    if (q >= kSums) waiter.wait(&sum_free[q % kSums], (q / kSums - 1) & 1);
+                    tc_after();
+                    if (lane == 0 && !waiter.dead) {
+                        const uint32_t d = tmem + 128 + q % kSums * kChunk;
+                        for (int j = 0; j < w.r16 / 16; ++j) {
+                            const uint64_t b = BACK ? operand(wt + j * 16 * 128, 0)
+                                                    : operand(wt + (j >> 2) * 64 * 128 + (j & 3) * 32, 0);
+                            const uint32_t v = v_at + (j >> 2) * T::kVAtom + (j & 3) * 32;
+                            mma(d, operand(v, 0), b, word2, j > 0);
+                            mma(d, operand(v + T::kVLo, 0), b, word2, true);
+                        }
+                        mma_commit(&done[s]);
+                    }
+                    ++q;
+                }
+                __syncwarp();
+                last = &done[s];
+            }
+            if (w.used) {
+                // a block without a chunk of the second product still has to see its V's phase
+                if (w.n2 == 0) wait_cluster(waiter, &meet[2], tiles & 1);
+                ++tiles;
+            }
+        }
+        if (last) waiter.wait(last, ((i - 1) / S) & 1);
+    } else {
+        // ---------------------------------------------------------- results
+        const int quarter = warp & 3, half = warp >> 2;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        int i = 0, q = 0, tiles = 0;
+        for (int tile = first_tile;; tile += clusters) {
+            const TileWork w = tile_work(g, tile, rank, size);
+            if (w.count <= 0) break;
+            // ranks that the adapter does not use
+            if (!BACK && g.keep)
+                for (int e = rank * 32 * kOutWarps + threadIdx.x; e < w.count * (g.rank - w.used);
+                     e += size * 32 * kOutWarps) {
+                    const int r = e / (g.rank - w.used), c = w.used + e - r * (g.rank - w.used);
+                    g.keep[static_cast<int64_t>(g.order[w.first + r]) * g.rank + c] = 0.0f;
+                }
+            int t[8];  // the rows that this thread writes: 8 threads a row
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = quarter * 32 + j * 4 + lane / 8;
+                t[j] = r < w.count ? g.order[w.first + r] : 0;
+            }
+            if (w.used) {
+                // V from the blocks' partial sums.  A unit is 8 of its columns for 32 rows, one row a lane; the
+                // cluster's blocks share the units out, and each one adds up its units' partial sums, block by
+                // block, and hands the result to every block.
+                const int npieces = w.r16 / 8, groups = (w.count + 31) / 32;  // groups of 32 rows
+                const float scale = g.scale[w.a];
+                out_warps_sync();  // the last tile's second product has been waited for
+                if (w.n1 > 0) waiter.wait(&narrow, tiles & 1);
+                tc_after();
+                __syncwarp();
+                float sum[T::kUnits][8];
+                int unit[T::kUnits];
+                if (size > 1) {
+                    if (quarter < groups)
+                        for (int p = half; p < npieces; p += 2) {
+                            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                            if (w.n1 > 0) {
+                                tmem_load8(lanes + p * 8, v);
+                                tmem_wait();
+                            }
+                            const uint32_t to = v_at + (p * 2 * kTileTokens + quarter * 32 + lane) * 16;
+                            store16(to, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                   __float_as_uint(v[3])));
+                            store16(to + kTileTokens * 16,
+                                    make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                                               __float_as_uint(v[7])));
+                        }
+                    arrive_cluster(&meet[0], size, lane);
+                    wait_cluster(waiter, &meet[0], tiles & 1);
+                }
+#pragma unroll
+                for (int u = 0; u < T::kUnits; ++u) {
+                    unit[u] = -1;
+                    if (size > 1) {
+                        const int e = static_cast<int>(rank) + static_cast<int>(size) * (warp + kOutWarps * u);
+                        if (e >= npieces * groups) continue;
+                        const int p = e / groups, gr = e - p * groups;
+                        unit[u] = p * 4 + gr;
+                        const uint32_t from = v_at + (p * 2 * kTileTokens + gr * 32 + lane) * 16;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sum[u][j] = 0.0f;
+                        for (uint32_t peer = 0; peer < size; ++peer) {
+                            const uint32_t there = peer_addr(from, peer);
+                            const float4 x = peer_float4(there), y = peer_float4(there + kTileTokens * 16);
+                            sum[u][0] += x.x, sum[u][1] += x.y, sum[u][2] += x.z, sum[u][3] += x.w;
+                            sum[u][4] += y.x, sum[u][5] += y.y, sum[u][6] += y.z, sum[u][7] += y.w;
+                        }
+                    } else if (half + 2 * u < npieces && quarter < groups) {
+                        unit[u] = (half + 2 * u) * 4 + quarter;
+                        tmem_load8(lanes + (half + 2 * u) * 8, sum[u]);
+                        tmem_wait();
+                    }
+                }
+                if (size > 1) {  // everyone has read the partial sums that V's place held
+                    arrive_cluster(&meet[1], size, lane);
+                    wait_cluster(waiter, &meet[1], tiles & 1);
+                }
+#pragma unroll
+                for (int u = 0; u < T::kUnits; ++u) {
+                    if (unit[u] < 0) continue;
+                    const int p = unit[u] >> 2, row = (unit[u] & 3) * 32 + lane;
+                    const bool writes = row < w.count;
+                    const int64_t token = writes && (BACK ? g.work != nullptr : g.keep != nullptr)
+                                              ? g.order[w.first + row] : 0;
+                    if (!BACK && g.keep && writes) {
+                        float *k = g.keep + token * g.rank + p * 8;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (p * 8 + j < w.used) k[j] = sum[u][j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[u][j] *= scale;
+                    uint4 hi, lo;
+                    split8(sum[u], hi, lo);
+                    const uint32_t to = v_at + (p >> 3) * T::kVAtom + swz(row, p & 7);
+                    if (size > 1) {
+                        for (uint32_t peer = 0; peer < size; ++peer) {
+                            const uint32_t there = peer_addr(to, peer);
+                            peer_store16(there, hi);
+                            peer_store16(there + T::kVLo, lo);
+                        }
+                    } else {
+                        store16(to, hi);
+                        store16(to + T::kVLo, lo);
+                    }
+                    if (BACK && g.work && writes) {
+                        // for the weights' gradients, in the plan's order: s dy B, and s (x A^T), as hi and lo
+                        const int64_t line = static_cast<int64_t>(w.first + row) * 2 * g.rank16 + p * 8;
+                        *reinterpret_cast<uint4 *>(g.work + line) = hi;
+                        *reinterpret_cast<uint4 *>(g.work + line + g.rank16) = lo;
+                        float x[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            x[j] = p * 8 + j < w.used ? scale * g.kept[token * g.rank + p * 8 + j] : 0.0f;
+                        split8(x, hi, lo);
+                        const int64_t far = static_cast<int64_t>(g.tokens) * 2 * g.rank16;
+                        *reinterpret_cast<uint4 *>(g.work + far + line) = hi;
+                        *reinterpret_cast<uint4 *>(g.work + far + line + g.rank16) = lo;
+                    }
+                }
+                fence_proxy_all();
+                tc_before();
+                arrive_cluster(&meet[2], size, lane);
+                ++tiles;
+            }
+            i += w.n1;
+            // Adds the second product's sums to the rows and writes them out, every other chunk.
+            for (int k = 0; k < w.n2; ++k, ++i, ++q) {
+                if ((q & 1) != half) continue;
+                const int s = i % S, c0 = (rank + k * size) * kChunk;
+                const uint32_t slot = base + s * T::kSlot;
+                waiter.wait(&full[s], (i / S) & 1);
+                waiter.wait(&done[s], (i / S) & 1);
+                tc_after();
+                __syncwarp();
+                if (quarter * 32 < w.count && w.used) {
+                    const int row = quarter * 32 + lane;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v[4][8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) tmem_load8(lanes + 128 + q % kSums * kChunk + h * 32 + j * 8, v[j]);
+                        tmem_wait();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t at = slot + swz(row, h * 4 + j);
+                            const uint4 y = load16(at);
+                            const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+                            uint32_t o[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                o[e] = pack2(__uint_as_float(x[e] << 16) + v[j][2 * e],
+                                             __uint_as_float(x[e] & 0xFFFF0000u) + v[j][2 * e + 1]);
+                            store16(at, make_uint4(o[0], o[1], o[2], o[3]));
+                        }
+                    }
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sum_free[q % kSums]);
+                if (g.al_out) {
+                    const int at = c0 + (lane & 7) * 8;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int row = quarter * 32 + j * 4 + lane / 8;
+                        if (row >= w.count || at >= g.nout) break;
+                        const uint4 v = load16(slot + swz(row, lane & 7));
+                        __nv_bfloat16 *o = g.out + t[j] * g.ld_out + at;
+                        if (at + 8 <= g.nout) {
+                            *reinterpret_cast<uint4 *>(o) = v;
+                        } else {
+                            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (at + e < g.nout)
+                                    reinterpret_cast<uint16_t *>(o)[e] =
+                                        static_cast<uint16_t>(x[e / 2] >> (16 * (e & 1)));
+                        }
+                    }
+                } else {
+                    // rows at any address: a warp writes one row's 64 values at a time, two a lane
+                    for (int j = 0; j < 32 && quarter * 32 + j < w.count; ++j) {
+                        const int row = quarter * 32 + j, at = c0 + lane;
+                        uint16_t *o = reinterpret_cast<uint16_t *>(g.out) +
+                                      static_cast<int64_t>(__shfl_sync(kFull, row_token(t, j), (j & 3) * 8)) * g.ld_out;
+                        const uint32_t from = slot + swz(row, lane >> 3) + (lane & 7) * 2;
+                        const uint32_t far = slot + swz(row, 4 + (lane >> 3)) + (lane & 7) * 2;
+                        if (at < g.nout) o[at] = load2(from);
+                        if (at + 32 < g.nout) o[at + 32] = load2(far);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&out_free[s]);
+            }
+        }
+    }
+    if (waiter.dead) fail(g);
+    tc_before();
+    __syncthreads();
+    if (size > 1) cluster_sync();  // no block leaves while a peer may still reach its memory
+    if (warp == 0) tmem_free(tmem, kTmemCols);
 }
 
 // Rows without an adapter: out = base, and nothing to keep.
@@ -325,301 +798,6 @@ __device__ __forceinline__ void copy_rows(const AdapterArgs &g, const int *tok, 
     if (g.keep)
         for (int i = rank * kAdThreads + threadIdx.x; i < count * g.rank; i += size * kAdThreads)
             g.keep[static_cast<int64_t>(tok[i / g.rank]) * g.rank + i % g.rank] = 0.0f;
-}
-
-// One tile of at most 128 tokens of one adapter, by one cluster.  Its blocks
-// take every c-th 64-column chunk of In for the narrow product, add up their
-// partial sums through each other's shared memory in a fixed order, and take
-// every c-th chunk of the result for the second product.  Loads run `STAGES`
-// chunks deep through both phases.
-//
-// BACK = false: In = x, W1 = A [R, K], W2 = B [N, R], V = s (x A^T).
-// BACK = true:  In = dy, W1 = B [N, R], W2 = A [R, K], V = s (dy B).
-template <bool BACK, int RANK>
-__global__ void __launch_bounds__(kAdThreads, RANK <= 64 ? 2 : 1) k_adapter(const __grid_constant__ AdapterArgs g)
-{
-    constexpr int STAGES = kAdStages;
-    constexpr int UNITS = RANK / 16;  // a warp's share of V's units, at most
-    extern __shared__ uint8_t raw[];
-    __shared__ int tok[kTileTokens];
-    __shared__ uint64_t done[STAGES];
-    __shared__ uint32_t tmem_at;
-
-    const uint32_t rank = cluster_rank(), size = cluster_size();
-    const int4 tile = reinterpret_cast<const int4 *>(g.tiles)[blockIdx.x / size];
-    const int count = min(tile.z, kTileTokens);
-    if (count <= 0) return;
-    for (int i = threadIdx.x; i < count; i += kAdThreads) tok[i] = g.order[tile.y + i];
-    const int a = tile.x;
-    const int used = a < 0 || a >= g.adapters ? 0 : used_rank(g, a);
-    if (used == 0) {
-        __syncthreads();
-        copy_rows(g, tok, count);
-        return;
-    }
-
-    const AdapterSmem lay = adapter_smem(g.rank, STAGES);
-    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-    const int r16 = (used + 15) & ~15;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    const __nv_bfloat16 *A = g.a + static_cast<int64_t>(a) * g.rank * g.k;
-    const __nv_bfloat16 *B = g.b + static_cast<int64_t>(a) * g.rank * g.n;
-    const float scale = g.scale[a];
-
-    if (warp == 0) tmem_alloc(&tmem_at, kTmemCols);
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) mbar_init(&done[i], 1);
-        fence_mbar_init();
-    }
-    tc_before();
-    __syncthreads();
-    tc_after();
-    const uint32_t tmem = tmem_at;
-
-    const int all1 = (g.nin + kChunk - 1) / kChunk, all2 = g.out ? (g.nout + kChunk - 1) / kChunk : 0;
-    const int n1 = all1 > (int)rank ? (all1 - rank + size - 1) / size : 0;
-    const int n2 = all2 > (int)rank ? (all2 - rank + size - 1) / size : 0;
-    const int n = n1 + n2;
-
-    const Place my = my_place();
-    int t[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) t[q] = my.row + 32 * q < count ? tok[my.row + 32 * q] : 0;
-
-    auto load_w = [&](uint32_t w, bool r_rows, const __nv_bfloat16 *m, int ld, int c0, int cols, bool aligned) {
-        if (r_rows) {  // A: R rows, 64 columns
-            load_block(w, m, ld, my, 0, used, r16, c0, cols, kChunk, aligned);
-        } else {       // B: 64 rows, R columns
-            load_block(w, m, ld, my, c0, cols, kChunk, 0, used, r16, aligned);
-            if (r16 > 64) load_block(w + 64 * 128, m, ld, my, c0, cols, kChunk, 64, used, r16 - 64, aligned);
-        }
-    };
-    auto load = [&](int i) {
-        const uint32_t slot = base + (i % STAGES) * lay.slot, w = slot + kInBytes;
-        if (i < n1) {
-            const int c0 = (rank + i * size) * kChunk;
-            load_rows(slot, g.in, g.ld_in, my, t, count, c0, g.nin, g.al_in);
-            if (BACK)
-                load_w(w, false, B, g.rank, c0, g.n, g.al_b);
-            else
-                load_w(w, true, A, g.k, c0, g.k, g.al_a);
-        } else if (i < n) {
-            const int c0 = (rank + (i - n1) * size) * kChunk;
-            load_rows(slot, g.base, g.ld_base, my, t, count, c0, g.nout, g.al_base);
-            if (BACK)
-                load_w(w, true, A, g.k, c0, g.k, g.al_a);
-            else
-                load_w(w, false, B, g.rank, c0, g.n, g.al_b);
-        }
-        async_commit();
-    };
-
-    Waiter waiter;
-    // Adds the product of chunk j to its tile and writes the rows out.
-    auto finish = [&](int j) {
-        const uint32_t slot = base + (j % STAGES) * lay.slot;
-        const int c0 = (rank + (j - n1) * size) * kChunk;
-        waiter.wait(&done[j % STAGES], (j / STAGES) & 1);
-        tc_after();
-        __syncwarp();
-        const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-        if ((warp & 3) * 32 < count) {
-            float v[4][8];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                tmem_load8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128 + ((j - n1) & 1) * kChunk + half * 32 + q * 8, v[q]);
-            tmem_wait();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t at = slot + swz(row, half * 4 + q);
-                const uint4 y = load16(at);
-                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[i] = pack2(__uint_as_float(w[i] << 16) + v[q][2 * i],
-                                 __uint_as_float(w[i] & 0xFFFF0000u) + v[q][2 * i + 1]);
-                store16(at, make_uint4(o[0], o[1], o[2], o[3]));
-            }
-        }
-        tc_before();
-        __syncthreads();
-        // the same places that this thread loads next, so that no barrier is needed before that
-        const int at = c0 + my.col;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (my.row + 32 * q >= count) break;
-            const uint4 v = load16(slot + my.at + q * 4096);
-            __nv_bfloat16 *o = g.out + t[q] * g.ld_out + at;
-            if (g.al_out && at + 8 <= g.nout) {
-                *reinterpret_cast<uint4 *>(o) = v;
-            } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (at + k < g.nout)
-                        reinterpret_cast<uint16_t *>(o)[k] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
-            }
-        }
-    };
-
-    // V from the blocks' partial sums.  A unit is 8 of its columns for 32 rows,
-    // one row a lane; the cluster's blocks share the units out, and each one
-    // adds up its units' partial sums, block by block, and hands the result to
-    // every block.
-    auto middle = [&]() {
-        if (n1 > 0) waiter.wait(&done[(n1 - 1) % STAGES], ((n1 - 1) / STAGES) & 1);
-        tc_after();
-        __syncwarp();
-        const uint32_t v_at = base + lay.v_at, lo_at = (g.rank > 64 ? 2 : 1) * lay.v_atom;
-        const int pieces = r16 / 8, quarter = warp & 3, half = warp >> 2;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        float sum[UNITS][8];
-        int piece_of[UNITS];
-        if (size > 1) {
-            if (quarter * 32 < count)
-                for (int p = half; p < pieces; p += 2) {
-                    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (n1 > 0) {
-                        tmem_load8(lanes + p * 8, v);
-                        tmem_wait();
-                    }
-                    const uint32_t at = v_at + (p * 2 * kTileTokens + quarter * 32 + lane) * 16;
-                    store16(at, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                           __float_as_uint(v[3])));
-                    store16(at + kTileTokens * 16, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
-                                                              __float_as_uint(v[6]), __float_as_uint(v[7])));
-                }
-            __syncwarp();
-            cluster_sync();
-        }
-        const int groups = (count + 31) / 32;  // of 32 rows
-#pragma unroll
-        for (int q = 0; q < UNITS; ++q) {
-            piece_of[q] = -1;
-            if (size > 1) {
-                // unit u is piece u / groups of rows u % groups
-                const int u = static_cast<int>(rank) + static_cast<int>(size) * (warp + 8 * q);
-                if (u >= pieces * groups) continue;
-                piece_of[q] = u / groups * 4 + u % groups;
-                const uint32_t at = v_at + (u / groups * 2 * kTileTokens + u % groups * 32 + lane) * 16;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[q][i] = 0.0f;
-                for (uint32_t peer = 0; peer < size; ++peer) {
-                    const uint32_t there = peer_addr(at, peer);
-                    const float4 x = peer_float4(there), y = peer_float4(there + kTileTokens * 16);
-                    sum[q][0] += x.x, sum[q][1] += x.y, sum[q][2] += x.z, sum[q][3] += x.w;
-                    sum[q][4] += y.x, sum[q][5] += y.y, sum[q][6] += y.z, sum[q][7] += y.w;
-                }
-            } else if (half + 2 * q < pieces && quarter < groups) {
-                piece_of[q] = (half + 2 * q) * 4 + quarter;
-                tmem_load8(lanes + (half + 2 * q) * 8, sum[q]);
-                tmem_wait();
-            }
-        }
-        if (size > 1) {
-            __syncwarp();
-            cluster_sync();  // everyone has read the partial sums that V's place held
-        }
-#pragma unroll
-        for (int q = 0; q < UNITS; ++q) {
-            if (piece_of[q] < 0) continue;
-            const int p = piece_of[q] >> 2, row = (piece_of[q] & 3) * 32 + lane;
-            const bool writes = row < count;
-            if (!BACK && g.keep && writes) {
-                float *k = g.keep + static_cast<int64_t>(tok[row]) * g.rank + p * 8;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (p * 8 + i < used) k[i] = sum[q][i];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[q][i] *= scale;
-            uint4 hi, lo;
-            split8(sum[q], hi, lo);
-            const uint32_t at = v_at + (p >> 3) * lay.v_atom + swz(row, p & 7);
-            if (size > 1) {
-                for (uint32_t peer = 0; peer < size; ++peer) {
-                    const uint32_t there = peer_addr(at, peer);
-                    peer_store16(there, hi);
-                    peer_store16(there + lo_at, lo);
-                }
-            } else {
-                store16(at, hi);
-                store16(at + lo_at, lo);
-            }
-            if (BACK && g.work && writes) {
-                // for the weights' gradients, in the plan's order: s dy B, and s (x A^T), as hi and lo
-                const int64_t line = static_cast<int64_t>(tile.y + row) * 2 * g.rank16 + p * 8;
-                *reinterpret_cast<uint4 *>(g.work + line) = hi;
-                *reinterpret_cast<uint4 *>(g.work + line + g.rank16) = lo;
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    x[i] = p * 8 + i < used
-                               ? scale * g.kept[static_cast<int64_t>(tok[row]) * g.rank + p * 8 + i]
-                               : 0.0f;
-                split8(x, hi, lo);
-                const int64_t far = static_cast<int64_t>(g.tokens) * 2 * g.rank16;
-                *reinterpret_cast<uint4 *>(g.work + far + line) = hi;
-                *reinterpret_cast<uint4 *>(g.work + far + line + g.rank16) = lo;
-            }
-        }
-        // ranks that the adapter does not use
-        if (!BACK && g.keep)
-            for (int i = rank * kAdThreads + threadIdx.x; i < count * (g.rank - used); i += size * kAdThreads)
-                g.keep[static_cast<int64_t>(tok[i / (g.rank - used)]) * g.rank + used + i % (g.rank - used)] = 0.0f;
-        fence_proxy_all();
-        tc_before();
-        __syncwarp();
-        if (size > 1)
-            cluster_sync();
-        else
-            __syncthreads();
-        fence_proxy_all();
-        tc_after();
-    };
-
-    for (int i = 0; i < STAGES - 1; ++i) load(i);
-    for (int i = 0; i < n; ++i) {
-        if (i == n1) middle();
-        async_wait<STAGES - 2>();
-        fence_proxy_async();
-        tc_before();
-        __syncthreads();
-        tc_after();
-        if (threadIdx.x == 0 && !waiter.dead) {
-            const uint32_t slot = base + (i % STAGES) * lay.slot, w = slot + kInBytes;
-            if (i < n1) {
-                const uint32_t word = mma_word(r16, false, BACK);
-#pragma unroll
-                for (int k = 0; k < kChunk / 16; ++k)
-                    mma(tmem, operand(slot + k * 32, 0),
-                        BACK ? operand(w + k * 16 * 128, 64 * 128) : operand(w + k * 32, 0), word, i > 0 || k > 0);
-            } else {
-                const uint32_t word = mma_word(kChunk, false, BACK);
-                const uint32_t d = tmem + 128 + ((i - n1) & 1) * kChunk, v_at = base + lay.v_at;
-                const uint32_t lo_at = (g.rank > 64 ? 2 : 1) * lay.v_atom;
-                for (int k = 0; k < r16 / 16; ++k) {
-                    const uint64_t b = BACK ? operand(w + k * 16 * 128, 0)
-                                            : operand(w + (k >> 2) * 64 * 128 + (k & 3) * 32, 0);
-                    const uint32_t v = v_at + (k >> 2) * lay.v_atom + (k & 3) * 32;
-                    mma(d, operand(v, 0), b, word, k > 0);
-                    mma(d, operand(v + lo_at, 0), b, word, true);
-                }
-            }
-            mma_commit(&done[i % STAGES]);
-        }
-        if (i > n1) finish(i - 1);
-        if (i > 0 && i + STAGES - 1 < n) waiter.wait(&done[(i - 1) % STAGES], ((i - 1) / STAGES) & 1);
-        load(i + STAGES - 1);
-    }
-    if (n == n1) middle();
-    if (n > n1) finish(n - 1);
-    async_wait<0>();
-    if (waiter.dead) fail(g);
-    tc_before();
-    __syncthreads();
-    if (warp == 0) tmem_free(tmem, kTmemCols);
 }
 
 // ------------------------------------------------ the forward of few tokens
@@ -1103,13 +1281,56 @@ uint32_t cluster_for(uint64_t tiles, uint64_t chunks)
     return c;
 }
 
-template <bool BACK>
-cudaError_t launch_tokens(const AdapterArgs &a, uint32_t c, cudaStream_t s)
+// How many clusters of a size the GPU holds at once (0: none, or an error).
+template <typename... P>
+uint32_t clusters_at_once(void (*kernel)(P...), uint32_t threads, uint32_t smem, uint32_t cluster)
 {
-    const uint32_t smem = dev::adapter_smem(a.rank, dev::kAdStages).bytes;
-    const dim3 grid(c * a.rows);
-    return a.rank <= 64 ? launch(dev::k_adapter<BACK, 64>, grid, dev::kAdThreads, smem, c, s, a)
-                        : launch(dev::k_adapter<BACK, 128>, grid, dev::kAdThreads, smem, c, s, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    return n > 0 ? static_cast<uint32_t>(n) : 0;
+}
+
+// Clusters take tiles in turn, one block on an SM.  Larger clusters end a
+// tile sooner, but fewer of them fit (36 of four and 15 of eight on 152 SMs),
+// and a turn has a part that no cluster shortens (filling the ring, the
+// meetings), which measures like about 12 chunks: the size with the least
+// turns x (chunks of a turn + 12) is taken, a chunk of the second product
+// counting twice for what it writes.
+template <bool BACK, int RANK>
+cudaError_t launch_tokens_at(const AdapterArgs &a, cudaStream_t s)
+{
+    const auto kernel = dev::k_adapter<BACK, RANK>;
+    constexpr uint32_t smem = dev::Tok<RANK>::kBytes;
+    const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (rc != cudaSuccess) return rc;
+    const uint64_t n1 = (a.nin + 63) / 64, n2 = a.out ? (a.nout + 63) / 64 : 0;
+    // half of the adapters' last tiles are empty ones at a guess
+    const uint64_t tiles = std::max(1, a.tokens / 128 + (std::min(a.adapters, a.tokens) + 1) / 2);
+    uint64_t best = ~0ull;
+    uint32_t c = 0, fit = 0;
+    for (uint32_t d = 1; d <= 8 && d <= std::max(n1, n2); ++d) {
+        const uint32_t f = clusters_at_once(kernel, dev::kTokThreads, smem, d);
+        if (!f) continue;
+        const uint64_t cost = (tiles + f - 1) / f * ((n1 + d - 1) / d + 2 * ((n2 + d - 1) / d) + 12);
+        if (cost < best) best = cost, c = d, fit = f;
+    }
+    if (!c) return cudaErrorInvalidConfiguration;
+    return launch(kernel, dim3(c * std::min(static_cast<uint32_t>(a.rows), fit)), dev::kTokThreads, smem, c, s, a);
+}
+template <bool BACK>
+cudaError_t launch_tokens(const AdapterArgs &a, cudaStream_t s)
+{
+    return a.rank <= 64 ? launch_tokens_at<BACK, 64>(a, s) : launch_tokens_at<BACK, 128>(a, s);
 }
 
 // The forward of few tokens: at most 16 an adapter on average.
@@ -1132,10 +1353,7 @@ cudaError_t launch_adapter(const AdapterArgs &a, bool back, cudaStream_t s)
                : a.rank <= 64 ? launch_few<64>(a, c, s)
                               : launch_few<128>(a, c, s);
     }
-    const uint64_t chunks = (std::max(a.nin, a.out ? a.nout : 0) + 63) / 64;
-    // half of the adapters' last tiles are empty ones at a guess
-    const uint32_t c = cluster_for(a.tokens / 128 + (std::min(a.adapters, a.tokens) + 1) / 2, chunks);
-    return back ? launch_tokens<true>(a, c, s) : launch_tokens<false>(a, c, s);
+    return back ? launch_tokens<true>(a, s) : launch_tokens<false>(a, s);
 }
 
 cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s)
