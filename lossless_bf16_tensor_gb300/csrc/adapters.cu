@@ -253,27 +253,31 @@ __device__ __forceinline__ void fail(const AdapterArgs &g)
     if (g.status) atomicCAS(reinterpret_cast<unsigned int *>(g.status), 0u, static_cast<unsigned int>(LCT_ERR_TIMEOUT));
 }
 
-// Waits at a barrier, bounded by the SM's clock (a wait is a second or two
-// long at the most; reading %globaltimer once in every wait that does not pass
-// at once costs microseconds each).  After one wait that ran out, none waits
-// again.
-constexpr long long kWaitClocks = 2000000000ll;
+// Waits at a barrier for a limited number of tries (each of which the hardware
+// holds for a while, so that it is seconds in all, where a wait that passes
+// takes microseconds).  After one wait that ran out, none waits again.
+constexpr uint32_t kWaitTries = 1u << 23;
+__device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 struct Waiter {
     bool dead = false;
-    template <typename Try>
-    __device__ __forceinline__ void until(Try ready)
-    {
-        if (dead || ready()) return;
-        const long long t0 = clock64();
-        while (!ready())
-            if (clock64() - t0 > kWaitClocks) {
-                dead = true;
-                return;
-            }
-    }
     __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity)
     {
-        until([&] { return mbar_try(bar, parity); });
+        const uint32_t at = smem_addr(bar);
+        uint32_t left = dead ? 0 : kWaitTries;
+#pragma unroll 1
+        while (left && !try_cluster(at, parity)) --left;
+        dead = left == 0;
     }
 };
 
@@ -287,25 +291,27 @@ __device__ __forceinline__ void arrive_cluster(uint64_t *bar, uint32_t size, int
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(there) : "memory");
     }
 }
-__device__ __forceinline__ bool try_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ void wait_cluster(Waiter &w, uint64_t *bar, uint32_t parity)
-{
-    w.until([&] { return try_cluster(bar, parity); });
-}
-
 // The result warps alone.
 __device__ __forceinline__ void out_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Warps by what they do: eight turn sums into results, one issues the
+// products, eight load.  They meet at mbarriers only, so that a load never
+// waits for a result to be written.
+constexpr int kOutWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 8;
+constexpr int kTokThreads = 32 * (kLoadWarp + kLoadWarps);
+
+// A load warp's share of a chunk is there: when its asynchronous copies have
+// landed (an arrival of every thread), and for pieces that it stored itself
+// (one a warp).  It does not wait for them, and the fence that lets products
+// read what ordinary stores and copies wrote is the product warp's: before a
+// load warp's arrival that fence would wait for every copy in flight.
+constexpr uint32_t kFullArrivals = kLoadWarps * 33;
+__device__ __forceinline__ void arrive_full(uint64_t *bar, int lane)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
 
 __device__ __forceinline__ uint16_t load2(uint32_t at)
 {
@@ -314,23 +320,8 @@ __device__ __forceinline__ uint16_t load2(uint32_t at)
     return v;
 }
 
-// t[j / 4] of a thread's rows, without an index into registers.
-__device__ __forceinline__ int row_token(const int (&t)[8], int j)
-{
-    int v = t[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i)
-        if (j >> 2 == i) v = t[i];
-    return v;
-}
-
 // ------------------------------------------------------- the tokens' part
 
-// Warps by what they do: eight turn sums into results, one issues the
-// products, four load.  They meet at mbarriers only, so that a load never
-// waits for a result to be written.
-constexpr int kOutWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 4;
-constexpr int kTokThreads = 32 * (kLoadWarp + kLoadWarps);
 constexpr int kSums = 4;  // tiles of sums of the second product in TMEM, beside the narrow one's
 constexpr uint32_t kTmemCols = 512;
 
@@ -343,10 +334,9 @@ struct Tok {
     static constexpr uint32_t kWBytes = kAtoms * 64 * 128, kSlot = kInBytes + kWBytes;
     static constexpr uint32_t kVAtom = kTileTokens * 128, kVLo = kAtoms * kVAtom;
     static constexpr int kStages = RANK <= 64 ? 8 : 5;
-    static constexpr int kLag = kStages - 3;  // loads in flight before a chunk is said to be there
     static constexpr uint32_t kVAt = kStages * kSlot;
     static constexpr uint32_t kBytes = kVAt + 2 * kVLo + 1024;  // room to start at a 1024-byte boundary
-    static constexpr int kUnits = RANK / 16;  // a warp's share of V's units, at most
+    static constexpr int kUnits = RANK / 32;  // a warp's share of V's units in a cluster of two, at most
 };
 
 // One row of the plan's table, as a cluster's blocks share it.
@@ -373,26 +363,44 @@ __device__ __forceinline__ TileWork tile_work(const AdapterArgs &g, int i, uint3
     return w;
 }
 
-// N 16-byte pieces, 2048 bytes apart in the tile: src(q) and how many of its
-// values are there.  Pieces that do not travel asynchronously are all fetched
-// before the first is stored.
-template <int N, typename Src, typename Valid>
-__device__ __forceinline__ void pieces(uint32_t dst, bool aligned, const void *anywhere, Src src, Valid valid)
+// The first N of a thread's row addresses.
+template <int N, int M>
+__device__ __forceinline__ const __nv_bfloat16 *const (&first_of(const __nv_bfloat16 *const (&p)[M]))[N]
 {
-    if (aligned) {
+    return reinterpret_cast<const __nv_bfloat16 *const (&)[N]>(p);
+}
+
+// N 16-byte pieces, 32 rows apart, from p[] on: `valid` of a row's eight values
+// are there, and rows from `rows` on are empty.  Pieces that do not travel
+// asynchronously are all fetched before the first is stored.  (A copy of no
+// bytes reads nothing, whatever its address.)
+template <bool FAST, int N>
+__device__ __forceinline__ void pieces(uint32_t dst, const __nv_bfloat16 *const (&p)[N], int64_t plus, int valid,
+                                       int rows, bool aligned)
+{
+    if (FAST || aligned) {
+        const uint32_t bytes = valid <= 0 ? 0u : static_cast<uint32_t>(min(valid, 8)) * 2;
 #pragma unroll
-        for (int q = 0; q < N; ++q) {
-            const int v = valid(q);
-            const uint32_t bytes = v <= 0 ? 0u : static_cast<uint32_t>(min(v, 8)) * 2;
-            async16(dst + q * 2048, bytes ? static_cast<const void *>(src(q)) : anywhere, bytes);
-        }
+        for (int q = 0; q < N; ++q) async16(dst + q * 4096, p[q] + plus, 32 * q < rows ? bytes : 0u);
     } else {
         uint4 x[N];
 #pragma unroll
-        for (int q = 0; q < N; ++q) x[q] = gather8(src(q), valid(q));
+        for (int q = 0; q < N; ++q) x[q] = gather8(p[q] + plus, 32 * q < rows ? valid : 0);
 #pragma unroll
-        for (int q = 0; q < N; ++q) store16(dst + q * 2048, x[q]);
+        for (int q = 0; q < N; ++q) store16(dst + q * 4096, x[q]);
     }
+}
+// The first 32, 64 or 128 rows of four pieces, whichever holds `rows`.
+template <bool FAST, int N>
+__device__ __forceinline__ void pieces_of(int rows, uint32_t dst, const __nv_bfloat16 *const (&p)[N], int64_t plus,
+                                          int valid, int left, bool aligned)
+{
+    if (N > 2 && rows > 64)
+        pieces<FAST>(dst, p, plus, valid, left, aligned);
+    else if (rows > 32)
+        pieces<FAST>(dst, first_of<2>(p), plus, valid, left, aligned);
+    else
+        pieces<FAST>(dst, first_of<1>(p), plus, valid, left, aligned);
 }
 
 // Tiles of at most 128 tokens of one adapter, by clusters that take tiles in
@@ -403,7 +411,8 @@ __device__ __forceinline__ void pieces(uint32_t dst, bool aligned, const void *a
 //
 // BACK = false: In = x, W1 = A [R, K], W2 = B [N, R], V = s (x A^T).
 // BACK = true:  In = dy, W1 = B [N, R], W2 = A [R, K], V = s (dy B).
-template <bool BACK, int RANK>
+// FAST: every row begins at a 16-byte boundary.
+template <bool BACK, int RANK, bool FAST>
 __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constant__ AdapterArgs g)
 {
     using T = Tok<RANK>;
@@ -420,7 +429,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
     if (warp == 0) tmem_alloc(&tmem_at, kTmemCols);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], kLoadWarps);
+            mbar_init(&full[i], kFullArrivals);
             mbar_init(&done[i], 1);
             mbar_init(&out_free[i], 4);
         }
@@ -439,136 +448,127 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
     if (warp >= kLoadWarp) {
         // ------------------------------------------------------------ loads
         const int id = threadIdx.x - 32 * kLoadWarp;
-        const int row0 = id >> 3, col = (id & 7) * 8;  // 8 threads a row of 64 columns, 16 rows at a time
+        const int row0 = id >> 3, col = (id & 7) * 8;  // 8 threads a row of 64 columns, 32 rows at a time
         const uint32_t at = swz(row0, id & 7);
         uint32_t second = 0, out_parity = 0;  // bit s: slot s last held a chunk of the second product; its next phase
-        int i = 0;
-        auto rows = [&](uint32_t dst, const __nv_bfloat16 *m, int64_t ld, const int (&t)[8], int count, int c0, int cols,
-                        bool aligned) {
-            const __nv_bfloat16 *from = m + c0 + col;
-            const int valid = cols - c0 - col;
-            // rows past the tile's tokens stay as they are: they reach only themselves
-            if (count > 64)
-                pieces<8>(dst + at, aligned, m, [&](int q) { return from + t[q] * ld; },
-                          [&](int q) { return row0 + 16 * q < count ? valid : 0; });
-            else if (count > 16)
-                pieces<4>(dst + at, aligned, m, [&](int q) { return from + t[q] * ld; },
-                          [&](int q) { return row0 + 16 * q < count ? valid : 0; });
-            else
-                pieces<1>(dst + at, aligned, m, [&](int q) { return from + t[q] * ld; },
-                          [&](int q) { return row0 + 16 * q < count ? valid : 0; });
-        };
+        int i = 0, s = 0;
         for (int tile = first_tile;; tile += clusters) {
             const TileWork w = tile_work(g, tile, rank, size);
             if (w.count <= 0) break;
-            int t[8];
+            // this thread's piece of each of its rows, at its first chunk
+            const int start = rank * kChunk + col;
+            const __nv_bfloat16 *in[4], *add[4], *ra[T::kAtoms * 2], *rb[2];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) t[q] = row0 + 16 * q < w.count ? g.order[w.first + row0 + 16 * q] : 0;
-            const __nv_bfloat16 *A = g.a + static_cast<int64_t>(w.a) * g.rank * g.k;
-            const __nv_bfloat16 *B = g.b + static_cast<int64_t>(w.a) * g.rank * g.n;
-            for (int k = 0; k < w.n1 + w.n2; ++k, ++i) {
-                const int s = i % S;
-                if (i >= S) {
-                    if (second >> s & 1) {
-                        waiter.wait(&out_free[s], out_parity >> s & 1);
-                        out_parity ^= 1u << s;
-                    } else {
-                        waiter.wait(&done[s], (i / S - 1) & 1);
-                    }
-                }
-                const uint32_t slot = base + s * T::kSlot, wt = slot + kInBytes;
-                const bool two = k >= w.n1;
-                const int c0 = (rank + (two ? k - w.n1 : k) * size) * kChunk;
-                if (two)
-                    rows(slot, g.base, g.ld_base, t, w.count, c0, g.nout, g.al_base);
-                else
-                    rows(slot, g.in, g.ld_in, t, w.count, c0, g.nin, g.al_in);
-                second = (second & ~(1u << s)) | (static_cast<uint32_t>(two) << s);
-                if (!w.used) {
-                    // nothing to multiply with
-                } else if (two == BACK) {  // A: R rows, 64 columns
-                    const __nv_bfloat16 *from = A + static_cast<int64_t>(row0) * g.k + c0 + col;
-                    const int valid = g.k - c0 - col;
+            for (int q = 0; q < 4; ++q) {
+                const int64_t t = row0 + 32 * q < w.count ? g.order[w.first + row0 + 32 * q] : 0;
+                in[q] = g.in + t * g.ld_in + start;
+                add[q] = g.base + t * g.ld_base + start;
+            }
 #pragma unroll
-                    for (int h = 0; h < T::kAtoms * 4; h += 4) {  // 64 rows at a time
-                        if (16 * h >= w.r16) break;
-                        pieces<4>(wt + at + h * 2048, g.al_a, A,
-                                  [&](int q) { return from + static_cast<int64_t>(16 * (q + h)) * g.k; },
-                                  [&](int q) { return row0 + 16 * (q + h) < w.used ? valid : 0; });
-                    }
-                } else {  // B: 64 rows, R columns
-                    const __nv_bfloat16 *from = B + static_cast<int64_t>(c0 + row0) * g.rank + col;
+            for (int q = 0; q < T::kAtoms * 2; ++q)
+                ra[q] = g.a + (static_cast<int64_t>(w.a) * g.rank + row0 + 32 * q) * g.k + start;
 #pragma unroll
-                    for (int h = 0; h < T::kAtoms; ++h) {
-                        if (col + 64 * h >= w.r16) break;
-                        pieces<4>(wt + at + h * 64 * 128, g.al_b, B,
-                                  [&](int q) { return from + 64 * h + static_cast<int64_t>(16 * q) * g.rank; },
-                                  [&](int q) { return c0 + row0 + 16 * q < g.n ? w.used - col - 64 * h : 0; });
-                    }
+            for (int q = 0; q < 2; ++q)
+                rb[q] = g.b + (static_cast<int64_t>(w.a) * g.n + rank * kChunk + row0 + 32 * q) * g.rank + col;
+            const int left = w.count - row0;  // rows from this thread's first one on
+            auto slot_free = [&]() {
+                if (i < S) return;
+                if (second >> s & 1) {
+                    waiter.wait(&out_free[s], out_parity >> s & 1);
+                    out_parity ^= 1u << s;
+                } else {
+                    waiter.wait(&done[s], (i / S - 1) & 1);
                 }
-                async_commit();
-                if (i >= T::kLag) {  // the chunk kLag back has landed
-                    async_wait<T::kLag>();
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[(i - T::kLag) % S]);
-                }
+            };
+            // A: R rows, 64 columns; B: 64 rows, R columns
+            auto load_a = [&](uint32_t to, int step) {
+                const int valid = g.k - start - step, rows = w.used - row0;
+                if (row0 < w.r16) pieces_of<FAST>(w.r16, to + at, ra, step, valid, rows, g.al_a);
+            };
+            auto load_b = [&](uint32_t to, int step) {
+                const int rows = g.n - (start - col) - step - row0;
+                const int64_t plus = static_cast<int64_t>(step) * g.rank;
+#pragma unroll
+                for (int h = 0; h < T::kAtoms; ++h)
+                    if (col + 64 * h < w.r16)
+                        pieces<FAST>(to + at + h * 64 * 128, rb, plus + 64 * h, w.used - col - 64 * h, rows, g.al_b);
+            };
+            // rows past the tile's tokens stay as they are, by 32: they reach only themselves
+            const int stride = static_cast<int>(size) * kChunk;
+            int step = 0;  // columns from the first chunk
+            for (int k = 0; k < w.n1; ++k, ++i, s = s + 1 == S ? 0 : s + 1, step += stride) {
+                slot_free();
+                const uint32_t slot = base + s * T::kSlot;
+                pieces_of<FAST>(w.count, slot + at, in, step, g.nin - start - step, left, g.al_in);
+                BACK ? load_b(slot + kInBytes, step) : load_a(slot + kInBytes, step);
+                second &= ~(1u << s);
+                arrive_full(&full[s], lane);
+            }
+            step = 0;
+            for (int k = 0; k < w.n2; ++k, ++i, s = s + 1 == S ? 0 : s + 1, step += stride) {
+                slot_free();
+                const uint32_t slot = base + s * T::kSlot;
+                pieces_of<FAST>(w.count, slot + at, add, step, g.nout - start - step, left, g.al_base);
+                if (w.used) BACK ? load_a(slot + kInBytes, step) : load_b(slot + kInBytes, step);
+                second |= 1u << s;
+                arrive_full(&full[s], lane);
             }
         }
         async_wait<0>();
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0)
-            for (int j = max(0, i - T::kLag); j < i; ++j) mbar_arrive(&full[j % S]);
     } else if (warp == kMmaWarp) {
         // --------------------------------------------------------- products
-        int i = 0, q = 0, tiles = 0;  // chunks, chunks of second products, tiles with a product
+        int i = 0, s = 0, q = 0, tiles = 0;  // chunks and their slot, chunks of second products, tiles with a product
         uint64_t *last = nullptr;
+        // descriptors of slot 0's tiles and of V; sixteenths of a byte offset add to them
+        const uint64_t in0 = operand(base, 0), v0 = operand(v_at, 0);
+        const uint64_t along0 = operand(base + kInBytes, 0), across0 = operand(base + kInBytes, 64 * 128);
         for (int tile = first_tile;; tile += clusters) {
             const TileWork w = tile_work(g, tile, rank, size);
             if (w.count <= 0) break;
             const uint32_t word1 = mma_word(w.r16, false, BACK), word2 = mma_word(kChunk, false, BACK);
-            for (int k = 0; k < w.n1 + w.n2; ++k, ++i) {
-                const int s = i % S;
-                const uint32_t slot = base + s * T::kSlot, wt = slot + kInBytes;
+            for (int k = 0; k < w.n1; ++k, ++i, s = s + 1 == S ? 0 : s + 1) {
                 waiter.wait(&full[s], (i / S) & 1);
-                if (k < w.n1) {
-                    tc_after();
-                    if (lane == 0 && !waiter.dead) {
+                fence_proxy_async();
+                tc_after();
+                if (lane == 0 && !waiter.dead) {
+                    const uint64_t x = in0 + s * (T::kSlot >> 4), m = (BACK ? across0 : along0) + s * (T::kSlot >> 4);
 #pragma unroll
-                        for (int j = 0; j < kChunk / 16; ++j)
-                            mma(tmem, operand(slot + j * 32, 0),
-                                BACK ? operand(wt + j * 16 * 128, 64 * 128) : operand(wt + j * 32, 0), word1,
-                                k > 0 || j > 0);
-                        mma_commit(&done[s]);
-                        if (k == w.n1 - 1) mma_commit(&narrow);
+                    for (int j = 0; j < kChunk / 16; ++j)
+                        mma(tmem, x + j * 2, m + j * (BACK ? 128 : 2), word1, k > 0 || j > 0);
+                    mma_commit(&done[s]);
+                    if (k == w.n1 - 1) mma_commit(&narrow);
+                }
+                __syncwarp();
+                last = &done[s];
+            }
+            for (int k = 0; k < w.n2; ++k, ++i, s = s + 1 == S ? 0 : s + 1, ++q) {
+                waiter.wait(&full[s], (i / S) & 1);
+                if (k == 0 && w.used) {
+                    waiter.wait(&meet[2], tiles & 1);  // V is there
+                    fence_proxy_all();
+                }
+                if (q >= kSums) waiter.wait(&sum_free[q % kSums], (q / kSums - 1) & 1);
+                fence_proxy_async();
+                tc_after();
+                if (lane == 0 && !waiter.dead) {
+                    const uint32_t d = tmem + 128 + q % kSums * kChunk;
+                    const uint64_t m = (BACK ? across0 : along0) + s * (T::kSlot >> 4);
+#pragma unroll
+                    for (int j = 0; j < RANK / 16; ++j) {
+                        if (j * 16 >= w.r16) break;
+                        const uint64_t v = v0 + (j >> 2) * (T::kVAtom >> 4) + (j & 3) * 2;
+                        const uint64_t b = m + (BACK ? j * 128 : (j >> 2) * 512 + (j & 3) * 2);
+                        mma(d, v, b, word2, j > 0);
+                        mma(d, v + (T::kVLo >> 4), b, word2, true);
                     }
-                } else {
-                    if (k == w.n1 && w.used) {
-                        wait_cluster(waiter, &meet[2], tiles & 1);  // V is there
-                        fence_proxy_all();
-                    }
-                    if (q >= kSums) waiter.wait(&sum_free[q % kSums], (q / kSums - 1) & 1);
-                    tc_after();
-                    if (lane == 0 && !waiter.dead) {
-                        const uint32_t d = tmem + 128 + q % kSums * kChunk;
-                        for (int j = 0; j < w.r16 / 16; ++j) {
-                            const uint64_t b = BACK ? operand(wt + j * 16 * 128, 0)
-                                                    : operand(wt + (j >> 2) * 64 * 128 + (j & 3) * 32, 0);
-                            const uint32_t v = v_at + (j >> 2) * T::kVAtom + (j & 3) * 32;
-                            mma(d, operand(v, 0), b, word2, j > 0);
-                            mma(d, operand(v + T::kVLo, 0), b, word2, true);
-                        }
-                        mma_commit(&done[s]);
-                    }
-                    ++q;
+                    mma_commit(&done[s]);
                 }
                 __syncwarp();
                 last = &done[s];
             }
             if (w.used) {
                 // a block without a chunk of the second product still has to see its V's phase
-                if (w.n2 == 0) wait_cluster(waiter, &meet[2], tiles & 1);
+                if (w.n2 == 0) waiter.wait(&meet[2], tiles & 1);
                 ++tiles;
             }
         }
@@ -606,6 +606,46 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                 __syncwarp();
                 float sum[T::kUnits][8];
                 int unit[T::kUnits];
+                auto emit = [&](float (&x)[8], int p, int gr) {
+                    const int row = gr * 32 + lane;
+                    const bool writes = row < w.count;
+                    const int64_t token = writes && (BACK ? g.work != nullptr : g.keep != nullptr)
+                                              ? g.order[w.first + row] : 0;
+                    if (!BACK && g.keep && writes) {
+                        float *k = g.keep + token * g.rank + p * 8;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (p * 8 + j < w.used) k[j] = x[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] *= scale;
+                    uint4 hi, lo;
+                    split8(x, hi, lo);
+                    const uint32_t to = v_at + (p >> 3) * T::kVAtom + swz(row, p & 7);
+                    for (uint32_t peer = 0; peer < size; ++peer) {
+                        const uint32_t there = size > 1 ? peer_addr(to, peer) : 0;
+                        if (size > 1) {
+                            peer_store16(there, hi);
+                            peer_store16(there + T::kVLo, lo);
+                        } else {
+                            store16(to, hi);
+                            store16(to + T::kVLo, lo);
+                        }
+                    }
+                    if (BACK && g.work && writes) {
+                        // for the weights' gradients, in the plan's order: s dy B, and s (x A^T), as hi and lo
+                        const int64_t line = static_cast<int64_t>(w.first + row) * 2 * g.rank16 + p * 8;
+                        *reinterpret_cast<uint4 *>(g.work + line) = hi;
+                        *reinterpret_cast<uint4 *>(g.work + line + g.rank16) = lo;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            x[j] = p * 8 + j < w.used ? scale * g.kept[token * g.rank + p * 8 + j] : 0.0f;
+                        split8(x, hi, lo);
+                        const int64_t far = static_cast<int64_t>(g.tokens) * 2 * g.rank16;
+                        *reinterpret_cast<uint4 *>(g.work + far + line) = hi;
+                        *reinterpret_cast<uint4 *>(g.work + far + line + g.rank16) = lo;
+                    }
+                };
                 if (size > 1) {
                     if (quarter < groups)
                         for (int p = half; p < npieces; p += 2) {
@@ -622,13 +662,13 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                                                __float_as_uint(v[7])));
                         }
                     arrive_cluster(&meet[0], size, lane);
-                    wait_cluster(waiter, &meet[0], tiles & 1);
+                    waiter.wait(&meet[0], tiles & 1);
                 }
+                if (size > 1) {
 #pragma unroll
-                for (int u = 0; u < T::kUnits; ++u) {
-                    unit[u] = -1;
-                    if (size > 1) {
+                    for (int u = 0; u < T::kUnits; ++u) {
                         const int e = static_cast<int>(rank) + static_cast<int>(size) * (warp + kOutWarps * u);
+                        unit[u] = -1;
                         if (e >= npieces * groups) continue;
                         const int p = e / groups, gr = e - p * groups;
                         unit[u] = p * 4 + gr;
@@ -641,57 +681,18 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                             sum[u][0] += x.x, sum[u][1] += x.y, sum[u][2] += x.z, sum[u][3] += x.w;
                             sum[u][4] += y.x, sum[u][5] += y.y, sum[u][6] += y.z, sum[u][7] += y.w;
                         }
-                    } else if (half + 2 * u < npieces && quarter < groups) {
-                        unit[u] = (half + 2 * u) * 4 + quarter;
-                        tmem_load8(lanes + (half + 2 * u) * 8, sum[u]);
-                        tmem_wait();
                     }
-                }
-                if (size > 1) {  // everyone has read the partial sums that V's place held
+                    // everyone has read the partial sums that V's place held
                     arrive_cluster(&meet[1], size, lane);
-                    wait_cluster(waiter, &meet[1], tiles & 1);
-                }
+                    waiter.wait(&meet[1], tiles & 1);
 #pragma unroll
-                for (int u = 0; u < T::kUnits; ++u) {
-                    if (unit[u] < 0) continue;
-                    const int p = unit[u] >> 2, row = (unit[u] & 3) * 32 + lane;
-                    const bool writes = row < w.count;
-                    const int64_t token = writes && (BACK ? g.work != nullptr : g.keep != nullptr)
-                                              ? g.order[w.first + row] : 0;
-                    if (!BACK && g.keep && writes) {
-                        float *k = g.keep + token * g.rank + p * 8;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (p * 8 + j < w.used) k[j] = sum[u][j];
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[u][j] *= scale;
-                    uint4 hi, lo;
-                    split8(sum[u], hi, lo);
-                    const uint32_t to = v_at + (p >> 3) * T::kVAtom + swz(row, p & 7);
-                    if (size > 1) {
-                        for (uint32_t peer = 0; peer < size; ++peer) {
-                            const uint32_t there = peer_addr(to, peer);
-                            peer_store16(there, hi);
-                            peer_store16(there + T::kVLo, lo);
-                        }
-                    } else {
-                        store16(to, hi);
-                        store16(to + T::kVLo, lo);
-                    }
-                    if (BACK && g.work && writes) {
-                        // for the weights' gradients, in the plan's order: s dy B, and s (x A^T), as hi and lo
-                        const int64_t line = static_cast<int64_t>(w.first + row) * 2 * g.rank16 + p * 8;
-                        *reinterpret_cast<uint4 *>(g.work + line) = hi;
-                        *reinterpret_cast<uint4 *>(g.work + line + g.rank16) = lo;
-                        float x[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            x[j] = p * 8 + j < w.used ? scale * g.kept[token * g.rank + p * 8 + j] : 0.0f;
-                        split8(x, hi, lo);
-                        const int64_t far = static_cast<int64_t>(g.tokens) * 2 * g.rank16;
-                        *reinterpret_cast<uint4 *>(g.work + far + line) = hi;
-                        *reinterpret_cast<uint4 *>(g.work + far + line + g.rank16) = lo;
+                    for (int u = 0; u < T::kUnits; ++u)
+                        if (unit[u] >= 0) emit(sum[u], unit[u] >> 2, unit[u] & 3);
+                } else if (quarter < groups) {
+                    for (int p = half; p < npieces; p += 2) {
+                        tmem_load8(lanes + p * 8, sum[0]);
+                        tmem_wait();
+                        emit(sum[0], p, quarter);
                     }
                 }
                 fence_proxy_all();
@@ -734,7 +735,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                 tc_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sum_free[q % kSums]);
-                if (g.al_out) {
+                if (FAST || g.al_out) {
                     const int at = c0 + (lane & 7) * 8;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -758,7 +759,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                     for (int j = 0; j < 32 && quarter * 32 + j < w.count; ++j) {
                         const int row = quarter * 32 + j, at = c0 + lane;
                         uint16_t *o = reinterpret_cast<uint16_t *>(g.out) +
-                                      static_cast<int64_t>(__shfl_sync(kFull, row_token(t, j), (j & 3) * 8)) * g.ld_out;
+                                      static_cast<int64_t>(g.order[w.first + row]) * g.ld_out;
                         const uint32_t from = slot + swz(row, lane >> 3) + (lane & 7) * 2;
                         const uint32_t far = slot + swz(row, 4 + (lane >> 3)) + (lane & 7) * 2;
                         if (at < g.nout) o[at] = load2(from);
@@ -1306,10 +1307,10 @@ uint32_t clusters_at_once(void (*kernel)(P...), uint32_t threads, uint32_t smem,
 // meetings), which measures like about 12 chunks: the size with the least
 // turns x (chunks of a turn + 12) is taken, a chunk of the second product
 // counting twice for what it writes.
-template <bool BACK, int RANK>
+template <bool BACK, int RANK, bool FAST>
 cudaError_t launch_tokens_at(const AdapterArgs &a, cudaStream_t s)
 {
-    const auto kernel = dev::k_adapter<BACK, RANK>;
+    const auto kernel = dev::k_adapter<BACK, RANK, FAST>;
     constexpr uint32_t smem = dev::Tok<RANK>::kBytes;
     const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (rc != cudaSuccess) return rc;
@@ -1330,7 +1331,9 @@ cudaError_t launch_tokens_at(const AdapterArgs &a, cudaStream_t s)
 template <bool BACK>
 cudaError_t launch_tokens(const AdapterArgs &a, cudaStream_t s)
 {
-    return a.rank <= 64 ? launch_tokens_at<BACK, 64>(a, s) : launch_tokens_at<BACK, 128>(a, s);
+    const bool fast = a.al_in && a.al_a && a.al_b && (!a.out || (a.al_base && a.al_out));
+    if (a.rank <= 64) return fast ? launch_tokens_at<BACK, 64, true>(a, s) : launch_tokens_at<BACK, 64, false>(a, s);
+    return fast ? launch_tokens_at<BACK, 128, true>(a, s) : launch_tokens_at<BACK, 128, false>(a, s);
 }
 
 // The forward of few tokens: at most 16 an adapter on average.
