@@ -68,6 +68,18 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         : "memory");
 }
 
+// One thread of the warp, as the compiler knows: products take their operands
+// from uniform registers, which a plain `lane == 0` makes it build thread by
+// thread (650 cycles for four products, where this takes 100).
+__device__ __forceinline__ bool elect()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // `bar` gets one arrival when the products issued so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
@@ -271,12 +283,29 @@ __device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity)
 }
 struct Waiter {
     bool dead = false;
-    __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity)
+    __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity)  // for this block's own warps
     {
-        const uint32_t at = smem_addr(bar);
         uint32_t left = dead ? 0 : kWaitTries;
 #pragma unroll 1
-        while (left && !try_cluster(at, parity)) --left;
+        while (left && !mbar_try(bar, parity)) --left;
+        dead = left == 0;
+    }
+    __device__ __forceinline__ void wait_both(uint64_t *a, uint32_t a_parity, uint64_t *b, uint32_t b_parity)
+    {
+        uint32_t left = dead ? 0 : kWaitTries;
+#pragma unroll 1
+        while (left) {
+            const bool x = mbar_try(a, a_parity), y = mbar_try(b, b_parity);
+            if (x && y) break;
+            --left;
+        }
+        dead = left == 0;
+    }
+    __device__ __forceinline__ void wait_cluster(uint64_t *bar, uint32_t parity)  // for the cluster's
+    {
+        uint32_t left = dead ? 0 : kWaitTries;
+#pragma unroll 1
+        while (left && !try_cluster(smem_addr(bar), parity)) --left;
         dead = left == 0;
     }
 };
@@ -291,6 +320,9 @@ __device__ __forceinline__ void arrive_cluster(uint64_t *bar, uint32_t size, int
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(there) : "memory");
     }
 }
+// Four result warps that share chunks.
+__device__ __forceinline__ void set_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(2 + half)); }
+
 // The result warps alone.
 __device__ __forceinline__ void out_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -298,6 +330,7 @@ __device__ __forceinline__ void out_warps_sync() { asm volatile("bar.sync 1, 256
 // products, eight load.  They meet at mbarriers only, so that a load never
 // waits for a result to be written.
 constexpr int kOutWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 8;
+constexpr int kLoadGroup = 4;  // warps that load one chunk; the groups take chunks in turn
 constexpr int kTokThreads = 32 * (kLoadWarp + kLoadWarps);
 
 // A load warp's share of a chunk is there: when its asynchronous copies have
@@ -305,7 +338,7 @@ constexpr int kTokThreads = 32 * (kLoadWarp + kLoadWarps);
 // (one a warp).  It does not wait for them, and the fence that lets products
 // read what ordinary stores and copies wrote is the product warp's: before a
 // load warp's arrival that fence would wait for every copy in flight.
-constexpr uint32_t kFullArrivals = kLoadWarps * 33;
+constexpr uint32_t kFullArrivals = kLoadGroup * 33;
 __device__ __forceinline__ void arrive_full(uint64_t *bar, int lane)
 {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -363,44 +396,28 @@ __device__ __forceinline__ TileWork tile_work(const AdapterArgs &g, int i, uint3
     return w;
 }
 
-// The first N of a thread's row addresses.
-template <int N, int M>
-__device__ __forceinline__ const __nv_bfloat16 *const (&first_of(const __nv_bfloat16 *const (&p)[M]))[N]
-{
-    return reinterpret_cast<const __nv_bfloat16 *const (&)[N]>(p);
-}
-
-// N 16-byte pieces, 32 rows apart, from p[] on: `valid` of a row's eight values
-// are there, and rows from `rows` on are empty.  Pieces that do not travel
-// asynchronously are all fetched before the first is stored.  (A copy of no
-// bytes reads nothing, whatever its address.)
-template <bool FAST, int N>
-__device__ __forceinline__ void pieces(uint32_t dst, const __nv_bfloat16 *const (&p)[N], int64_t plus, int valid,
-                                       int rows, bool aligned)
+// N 16-byte pieces, 16 rows apart, from src(0) on: `valid` of a row's eight
+// values are there, and rows from `rows` on are empty.  Pieces that do not
+// travel asynchronously are fetched four at a time before they are stored.
+// (A copy of no bytes reads nothing, whatever its address.)
+template <bool FAST, int N, typename Src>
+__device__ __forceinline__ void pieces(uint32_t dst, Src src, int valid, int rows, bool aligned)
 {
     if (FAST || aligned) {
         const uint32_t bytes = valid <= 0 ? 0u : static_cast<uint32_t>(min(valid, 8)) * 2;
 #pragma unroll
-        for (int q = 0; q < N; ++q) async16(dst + q * 4096, p[q] + plus, 32 * q < rows ? bytes : 0u);
+        for (int q = 0; q < N; ++q) async16(dst + q * 2048, src(q), 16 * q < rows ? bytes : 0u);
     } else {
-        uint4 x[N];
+        constexpr int M = N < 4 ? N : 4;
 #pragma unroll
-        for (int q = 0; q < N; ++q) x[q] = gather8(p[q] + plus, 32 * q < rows ? valid : 0);
+        for (int h = 0; h < N; h += M) {
+            uint4 x[M];
 #pragma unroll
-        for (int q = 0; q < N; ++q) store16(dst + q * 4096, x[q]);
+            for (int q = 0; q < M; ++q) x[q] = gather8(src(h + q), 16 * (h + q) < rows ? valid : 0);
+#pragma unroll
+            for (int q = 0; q < M; ++q) store16(dst + (h + q) * 2048, x[q]);
+        }
     }
-}
-// The first 32, 64 or 128 rows of four pieces, whichever holds `rows`.
-template <bool FAST, int N>
-__device__ __forceinline__ void pieces_of(int rows, uint32_t dst, const __nv_bfloat16 *const (&p)[N], int64_t plus,
-                                          int valid, int left, bool aligned)
-{
-    if (N > 2 && rows > 64)
-        pieces<FAST>(dst, p, plus, valid, left, aligned);
-    else if (rows > 32)
-        pieces<FAST>(dst, first_of<2>(p), plus, valid, left, aligned);
-    else
-        pieces<FAST>(dst, first_of<1>(p), plus, valid, left, aligned);
 }
 
 // Tiles of at most 128 tokens of one adapter, by clusters that take tiles in
@@ -418,7 +435,9 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
     using T = Tok<RANK>;
     constexpr int S = T::kStages;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[S], done[S], out_free[S], narrow, sum_free[kSums], meet[3];
+    // a slot is full, and free again; the narrow product, and a tile of sums of the second one, is there, the latter
+    // free again; the cluster's meetings
+    __shared__ uint64_t full[S], freed[S], narrow, summed[kSums], sum_free[kSums], meet[3];
     __shared__ uint32_t tmem_at;
 
     const uint32_t rank = cluster_rank(), size = cluster_size();
@@ -430,11 +449,13 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], kFullArrivals);
-            mbar_init(&done[i], 1);
-            mbar_init(&out_free[i], 4);
+            mbar_init(&freed[i], 1);
         }
         mbar_init(&narrow, 1);
-        for (int i = 0; i < kSums; ++i) mbar_init(&sum_free[i], 4);
+        for (int i = 0; i < kSums; ++i) {
+            mbar_init(&summed[i], 1);
+            mbar_init(&sum_free[i], 4);
+        }
         for (int i = 0; i < 3; ++i) mbar_init(&meet[i], kOutWarps * size);
         fence_mbar_init();
     }
@@ -447,78 +468,78 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
 
     if (warp >= kLoadWarp) {
         // ------------------------------------------------------------ loads
-        const int id = threadIdx.x - 32 * kLoadWarp;
-        const int row0 = id >> 3, col = (id & 7) * 8;  // 8 threads a row of 64 columns, 32 rows at a time
+        const int group = (warp - kLoadWarp) / kLoadGroup, id = (threadIdx.x - 32 * kLoadWarp) & 127;
+        const int row0 = id >> 3, col = (id & 7) * 8;  // 8 threads a row of 64 columns, 16 rows at a time
         const uint32_t at = swz(row0, id & 7);
-        uint32_t second = 0, out_parity = 0;  // bit s: slot s last held a chunk of the second product; its next phase
         int i = 0, s = 0;
+        auto next = [&]() {
+            ++i;
+            s = s + 1 == S ? 0 : s + 1;
+        };
         for (int tile = first_tile;; tile += clusters) {
             const TileWork w = tile_work(g, tile, rank, size);
             if (w.count <= 0) break;
-            // this thread's piece of each of its rows, at its first chunk
-            const int start = rank * kChunk + col;
-            const __nv_bfloat16 *in[4], *add[4], *ra[T::kAtoms * 2], *rb[2];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t t = row0 + 32 * q < w.count ? g.order[w.first + row0 + 32 * q] : 0;
-                in[q] = g.in + t * g.ld_in + start;
-                add[q] = g.base + t * g.ld_base + start;
-            }
-#pragma unroll
-            for (int q = 0; q < T::kAtoms * 2; ++q)
-                ra[q] = g.a + (static_cast<int64_t>(w.a) * g.rank + row0 + 32 * q) * g.k + start;
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                rb[q] = g.b + (static_cast<int64_t>(w.a) * g.n + rank * kChunk + row0 + 32 * q) * g.rank + col;
+            const int start = rank * kChunk + col, stride = static_cast<int>(size) * kChunk;
             const int left = w.count - row0;  // rows from this thread's first one on
-            auto slot_free = [&]() {
-                if (i < S) return;
-                if (second >> s & 1) {
-                    waiter.wait(&out_free[s], out_parity >> s & 1);
-                    out_parity ^= 1u << s;
-                } else {
-                    waiter.wait(&done[s], (i / S - 1) & 1);
-                }
-            };
+            int t[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) t[q] = 16 * q < left ? g.order[w.first + row0 + 16 * q] : 0;
             // A: R rows, 64 columns; B: 64 rows, R columns
+            const __nv_bfloat16 *A = g.a + (static_cast<int64_t>(w.a) * g.rank + row0) * g.k + start;
+            const __nv_bfloat16 *B = g.b + (static_cast<int64_t>(w.a) * g.n + rank * kChunk + row0) * g.rank + col;
             auto load_a = [&](uint32_t to, int step) {
                 const int valid = g.k - start - step, rows = w.used - row0;
-                if (row0 < w.r16) pieces_of<FAST>(w.r16, to + at, ra, step, valid, rows, g.al_a);
+                const int64_t down = static_cast<int64_t>(16) * g.k;
+                if (RANK > 64 && w.r16 > 64)
+                    pieces<FAST, RANK / 16>(to + at, [&](int q) { return A + step + q * down; }, valid, rows, g.al_a);
+                else if (w.r16 > 32)
+                    pieces<FAST, 4>(to + at, [&](int q) { return A + step + q * down; }, valid, rows, g.al_a);
+                else if (w.r16 > 16)
+                    pieces<FAST, 2>(to + at, [&](int q) { return A + step + q * down; }, valid, rows, g.al_a);
+                else
+                    pieces<FAST, 1>(to + at, [&](int q) { return A + step + q * down; }, valid, rows, g.al_a);
             };
             auto load_b = [&](uint32_t to, int step) {
                 const int rows = g.n - (start - col) - step - row0;
-                const int64_t plus = static_cast<int64_t>(step) * g.rank;
+                const int64_t down = static_cast<int64_t>(16) * g.rank;
+                const __nv_bfloat16 *from = B + static_cast<int64_t>(step) * g.rank;
 #pragma unroll
                 for (int h = 0; h < T::kAtoms; ++h)
                     if (col + 64 * h < w.r16)
-                        pieces<FAST>(to + at + h * 64 * 128, rb, plus + 64 * h, w.used - col - 64 * h, rows, g.al_b);
+                        pieces<FAST, 4>(to + at + h * 64 * 128, [&](int q) { return from + 64 * h + q * down; },
+                                        w.used - col - 64 * h, rows, g.al_b);
             };
-            // rows past the tile's tokens stay as they are, by 32: they reach only themselves
-            const int stride = static_cast<int>(size) * kChunk;
-            int step = 0;  // columns from the first chunk
-            for (int k = 0; k < w.n1; ++k, ++i, s = s + 1 == S ? 0 : s + 1, step += stride) {
-                slot_free();
-                const uint32_t slot = base + s * T::kSlot;
-                pieces_of<FAST>(w.count, slot + at, in, step, g.nin - start - step, left, g.al_in);
-                BACK ? load_b(slot + kInBytes, step) : load_a(slot + kInBytes, step);
-                second &= ~(1u << s);
-                arrive_full(&full[s], lane);
-            }
-            step = 0;
-            for (int k = 0; k < w.n2; ++k, ++i, s = s + 1 == S ? 0 : s + 1, step += stride) {
-                slot_free();
-                const uint32_t slot = base + s * T::kSlot;
-                pieces_of<FAST>(w.count, slot + at, add, step, g.nout - start - step, left, g.al_base);
-                if (w.used) BACK ? load_a(slot + kInBytes, step) : load_b(slot + kInBytes, step);
-                second |= 1u << s;
-                arrive_full(&full[s], lane);
-            }
+            // the rows of In or of what is added to; rows past the tile's tokens stay as they are, by 16 at the
+            // least: they reach only themselves
+            auto product = [&](const __nv_bfloat16 *m, int64_t ld, bool al, int cols, int chunks, bool two) {
+                const __nv_bfloat16 *p[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) p[q] = m + t[q] * ld + start;
+                int step = 0;  // columns from the first chunk
+                for (int k = 0; k < chunks; ++k, next(), step += stride) {
+                    if ((i & 1) != group) continue;
+                    if (i >= S) waiter.wait(&freed[s], (i / S - 1) & 1);
+                    const uint32_t slot = base + s * T::kSlot;
+                    const int valid = cols - start - step;
+                    if (w.count > 64)
+                        pieces<FAST, 8>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
+                    else if (w.count > 32)
+                        pieces<FAST, 4>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
+                    else if (w.count > 16)
+                        pieces<FAST, 2>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
+                    else
+                        pieces<FAST, 1>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
+                    if (w.used) two == BACK ? load_a(slot + kInBytes, step) : load_b(slot + kInBytes, step);
+                    arrive_full(&full[s], lane);
+                }
+            };
+            product(g.in, g.ld_in, g.al_in, g.nin, w.n1, false);
+            product(g.base, g.ld_base, g.al_base, g.nout, w.n2, true);
         }
         async_wait<0>();
     } else if (warp == kMmaWarp) {
         // --------------------------------------------------------- products
         int i = 0, s = 0, q = 0, tiles = 0;  // chunks and their slot, chunks of second products, tiles with a product
-        uint64_t *last = nullptr;
         // descriptors of slot 0's tiles and of V; sixteenths of a byte offset add to them
         const uint64_t in0 = operand(base, 0), v0 = operand(v_at, 0);
         const uint64_t along0 = operand(base + kInBytes, 0), across0 = operand(base + kInBytes, 64 * 128);
@@ -530,27 +551,26 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                 waiter.wait(&full[s], (i / S) & 1);
                 fence_proxy_async();
                 tc_after();
-                if (lane == 0 && !waiter.dead) {
+                if (elect() && !waiter.dead) {
                     const uint64_t x = in0 + s * (T::kSlot >> 4), m = (BACK ? across0 : along0) + s * (T::kSlot >> 4);
 #pragma unroll
                     for (int j = 0; j < kChunk / 16; ++j)
                         mma(tmem, x + j * 2, m + j * (BACK ? 128 : 2), word1, k > 0 || j > 0);
-                    mma_commit(&done[s]);
+                    mma_commit(&freed[s]);
                     if (k == w.n1 - 1) mma_commit(&narrow);
                 }
                 __syncwarp();
-                last = &done[s];
             }
             for (int k = 0; k < w.n2; ++k, ++i, s = s + 1 == S ? 0 : s + 1, ++q) {
                 waiter.wait(&full[s], (i / S) & 1);
                 if (k == 0 && w.used) {
-                    waiter.wait(&meet[2], tiles & 1);  // V is there
+                    waiter.wait_cluster(&meet[2], tiles & 1);  // V is there
                     fence_proxy_all();
                 }
                 if (q >= kSums) waiter.wait(&sum_free[q % kSums], (q / kSums - 1) & 1);
                 fence_proxy_async();
                 tc_after();
-                if (lane == 0 && !waiter.dead) {
+                if (elect() && !waiter.dead) {
                     const uint32_t d = tmem + 128 + q % kSums * kChunk;
                     const uint64_t m = (BACK ? across0 : along0) + s * (T::kSlot >> 4);
 #pragma unroll
@@ -561,18 +581,16 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                         mma(d, v, b, word2, j > 0);
                         mma(d, v + (T::kVLo >> 4), b, word2, true);
                     }
-                    mma_commit(&done[s]);
+                    mma_commit(&summed[q % kSums]);
                 }
                 __syncwarp();
-                last = &done[s];
             }
             if (w.used) {
                 // a block without a chunk of the second product still has to see its V's phase
-                if (w.n2 == 0) waiter.wait(&meet[2], tiles & 1);
+                if (w.n2 == 0) waiter.wait_cluster(&meet[2], tiles & 1);
                 ++tiles;
             }
         }
-        if (last) waiter.wait(last, ((i - 1) / S) & 1);
     } else {
         // ---------------------------------------------------------- results
         const int quarter = warp & 3, half = warp >> 2;
@@ -662,7 +680,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                                                __float_as_uint(v[7])));
                         }
                     arrive_cluster(&meet[0], size, lane);
-                    waiter.wait(&meet[0], tiles & 1);
+                    waiter.wait_cluster(&meet[0], tiles & 1);
                 }
                 if (size > 1) {
 #pragma unroll
@@ -684,7 +702,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                     }
                     // everyone has read the partial sums that V's place held
                     arrive_cluster(&meet[1], size, lane);
-                    waiter.wait(&meet[1], tiles & 1);
+                    waiter.wait_cluster(&meet[1], tiles & 1);
 #pragma unroll
                     for (int u = 0; u < T::kUnits; ++u)
                         if (unit[u] >= 0) emit(sum[u], unit[u] >> 2, unit[u] & 3);
@@ -702,12 +720,16 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
             }
             i += w.n1;
             // Adds the second product's sums to the rows and writes them out, every other chunk.
+            __nv_bfloat16 *o[8];
+            const int mine = rank * kChunk + (lane & 7) * 8;  // the column of this thread's pieces in its first chunk
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = g.out + t[j] * g.ld_out + mine;
+            const int rows_left = w.count - quarter * 32 - lane / 8;  // of the rows it writes, four apart
             for (int k = 0; k < w.n2; ++k, ++i, ++q) {
                 if ((q & 1) != half) continue;
-                const int s = i % S, c0 = (rank + k * size) * kChunk;
+                const int s = i % S, step = k * static_cast<int>(size) * kChunk;
                 const uint32_t slot = base + s * T::kSlot;
-                waiter.wait(&full[s], (i / S) & 1);
-                waiter.wait(&done[s], (i / S) & 1);
+                waiter.wait_both(&full[s], (i / S) & 1, &summed[q % kSums], (q / kSums) & 1);
                 tc_after();
                 __syncwarp();
                 if (quarter * 32 < w.count && w.used) {
@@ -723,12 +745,12 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                             const uint32_t at = slot + swz(row, h * 4 + j);
                             const uint4 y = load16(at);
                             const uint32_t x[4] = {y.x, y.y, y.z, y.w};
-                            uint32_t o[4];
+                            uint32_t r[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                o[e] = pack2(__uint_as_float(x[e] << 16) + v[j][2 * e],
+                                r[e] = pack2(__uint_as_float(x[e] << 16) + v[j][2 * e],
                                              __uint_as_float(x[e] & 0xFFFF0000u) + v[j][2 * e + 1]);
-                            store16(at, make_uint4(o[0], o[1], o[2], o[3]));
+                            store16(at, make_uint4(r[0], r[1], r[2], r[3]));
                         }
                     }
                 }
@@ -736,38 +758,39 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sum_free[q % kSums]);
                 if (FAST || g.al_out) {
-                    const int at = c0 + (lane & 7) * 8;
+                    const int there = g.nout - mine - step;
+                    uint4 v[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int row = quarter * 32 + j * 4 + lane / 8;
-                        if (row >= w.count || at >= g.nout) break;
-                        const uint4 v = load16(slot + swz(row, lane & 7));
-                        __nv_bfloat16 *o = g.out + t[j] * g.ld_out + at;
-                        if (at + 8 <= g.nout) {
-                            *reinterpret_cast<uint4 *>(o) = v;
-                        } else {
-                            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    for (int j = 0; j < 8; ++j) v[j] = load16(slot + swz(quarter * 32 + j * 4 + lane / 8, lane & 7));
+                    if (there >= 8) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (at + e < g.nout)
-                                    reinterpret_cast<uint16_t *>(o)[e] =
+                        for (int j = 0; j < 8; ++j)
+                            if (4 * j < rows_left) *reinterpret_cast<uint4 *>(o[j] + step) = v[j];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                            for (int e = 0; e < 7; ++e)
+                                if (4 * j < rows_left && e < there)
+                                    reinterpret_cast<uint16_t *>(o[j] + step)[e] =
                                         static_cast<uint16_t>(x[e / 2] >> (16 * (e & 1)));
                         }
                     }
                 } else {
                     // rows at any address: a warp writes one row's 64 values at a time, two a lane
                     for (int j = 0; j < 32 && quarter * 32 + j < w.count; ++j) {
-                        const int row = quarter * 32 + j, at = c0 + lane;
-                        uint16_t *o = reinterpret_cast<uint16_t *>(g.out) +
-                                      static_cast<int64_t>(g.order[w.first + row]) * g.ld_out;
-                        const uint32_t from = slot + swz(row, lane >> 3) + (lane & 7) * 2;
+                        const int row = quarter * 32 + j, at = rank * kChunk + step + lane;
+                        uint16_t *to = reinterpret_cast<uint16_t *>(g.out) +
+                                       static_cast<int64_t>(g.order[w.first + row]) * g.ld_out;
+                        const uint32_t near = slot + swz(row, lane >> 3) + (lane & 7) * 2;
                         const uint32_t far = slot + swz(row, 4 + (lane >> 3)) + (lane & 7) * 2;
-                        if (at < g.nout) o[at] = load2(from);
-                        if (at + 32 < g.nout) o[at + 32] = load2(far);
+                        if (at < g.nout) to[at] = load2(near);
+                        if (at + 32 < g.nout) to[at + 32] = load2(far);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&out_free[s]);
+                set_sync(half);
+                if ((threadIdx.x & 127) == 0) mbar_arrive(&freed[s]);
             }
         }
     }
