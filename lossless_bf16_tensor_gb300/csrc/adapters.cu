@@ -244,11 +244,9 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // Writes before it, of this block's or of a peer's memory, are seen by products after it.
 __device__ __forceinline__ void fence_proxy_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-__device__ __forceinline__ float peer_float(uint32_t addr, uint32_t rank)
+__device__ __forceinline__ float peer_float(uint32_t at)
 {
-    uint32_t at;
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
     return v;
 }
@@ -366,7 +364,8 @@ struct Tok {
     static constexpr int kAtoms = RANK / 64;
     static constexpr uint32_t kWBytes = kAtoms * 64 * 128, kSlot = kInBytes + kWBytes;
     static constexpr uint32_t kVAtom = kTileTokens * 128, kVLo = kAtoms * kVAtom;
-    static constexpr int kStages = RANK <= 64 ? 8 : 5;
+    static constexpr int kStages = RANK <= 64 ? 8 : 4;
+    static_assert(kStages % 2 == 0, "a slot belongs to one load group, which sees each of its phases");
     static constexpr uint32_t kVAt = kStages * kSlot;
     static constexpr uint32_t kBytes = kVAt + 2 * kVLo + 1024;  // room to start at a 1024-byte boundary
     static constexpr int kUnits = RANK / 32;  // a warp's share of V's units in a cluster of two, at most
@@ -1045,143 +1044,189 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
 // --------------------------------------------------- the weights' gradients
 
 // dA^T [K, R] = x^T (s dy B) and dB [N, R] = dy^T (s x A^T) of one adapter:
-// 128 columns of x or dy by one cluster, whose blocks take every c-th run of
+// 256 columns of x or dy by one cluster, whose blocks take every c-th run of
 // 64 of the adapter's tokens; their partial sums meet in shared memory in a
 // fixed order.  The tokens are the products' inner dimension, so tiles are
-// read across: rows of a tile of x are columns of the operand.
-template <int STAGES>
-__global__ void __launch_bounds__(kAdThreads, 2) k_adapter_grad(const __grid_constant__ AdapterArgs g)
+// read across: rows of a tile of x are columns of the operand.  256 columns,
+// because every block of columns reads V again: 16 KB at R = 64 for 32 KB of x.
+constexpr int kGradCols = 256, kGradTokens = 64;
+constexpr int kGradLoadWarps = 8;  // which write the results at the end
+constexpr int kGradAdThreads = 32 * (kGradLoadWarps + 1);
+constexpr uint32_t kGradTmemCols = 256;
+
+template <int RANK, int STAGES>
+struct Grad {
+    static constexpr int kAtoms = RANK / 64;
+    // two load groups take slots in turn, and slots come free in order: of two or more, a group that waits for a
+    // slot's last chunk has seen the one before it go
+    static_assert(STAGES >= 2, "");
+    static constexpr uint32_t kTile = kGradTokens * 128;  // 64 tokens by 64 columns
+    static constexpr uint32_t kIn = kGradCols / 64 * kTile, kV = kAtoms * kTile, kSlot = kIn + 2 * kV;
+    static constexpr uint32_t kSums = RANK * kGradCols * 4;
+    static constexpr uint32_t kBytes = (STAGES * kSlot > kSums ? STAGES * kSlot : kSums) + 1024;
+};
+
+template <int RANK, int STAGES>
+__global__ void __launch_bounds__(kGradAdThreads) k_adapter_grad(const __grid_constant__ AdapterArgs g)
 {
+    using T = Grad<RANK, STAGES>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t done[STAGES];
+    __shared__ uint64_t full[STAGES], freed[STAGES], all_done;
     __shared__ uint32_t tmem_at;
     const uint32_t rank = cluster_rank(), size = cluster_size();
-    const int blocks_x = (g.k + 127) / 128;
-    const int which = blockIdx.y;
-    const bool is_a = which < blocks_x;
-    const int c0 = (is_a ? which : which - blocks_x) * 128;
+    const int blocks_x = (g.k + kGradCols - 1) / kGradCols;
+    const bool is_a = static_cast<int>(blockIdx.y) < blocks_x;
+    const int c0 = (is_a ? blockIdx.y : blockIdx.y - blocks_x) * kGradCols;
     const int a = blockIdx.z;
     const int first = g.starts[a], last = g.starts[a + 1];
-    const int used = last > first ? used_rank(g, a) : 0;
+    const int used = last > first ? used_rank(g, a) : 0, r16 = (used + 15) & ~15;
     const int cols = is_a ? g.k : g.n;
-    const __nv_bfloat16 *in = is_a ? g.x : g.in;
-    const int64_t ld = is_a ? g.ld_x : g.ld_in;
-    const bool al = is_a ? g.al_x : g.al_in;
-    const __nv_bfloat16 *v = g.work + (is_a ? 0 : static_cast<int64_t>(g.tokens) * 2 * g.rank16);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-    const uint32_t atoms = g.rank > 64 ? 2 : 1;
-    const uint32_t v_bytes = atoms * 64 * 128, slot_bytes = 2 * 64 * 128 + 2 * v_bytes;
-    const int r16 = (used + 15) & ~15;
-    const int all = (last - first + 63) / 64;
-    const int n = used && all > (int)rank ? (all - rank + size - 1) / size : 0;
+    const int all = (last - first + kGradTokens - 1) / kGradTokens;
+    const int n = used && all > static_cast<int>(rank) ? (all - rank + size - 1) / size : 0;
     uint32_t tmem = 0;
     Waiter waiter;
     if (used) {
-        if (warp == 0) tmem_alloc(&tmem_at, 128);
+        if (warp == 0) tmem_alloc(&tmem_at, kGradTmemCols);
         if (threadIdx.x == 0) {
-            for (int i = 0; i < STAGES; ++i) mbar_init(&done[i], 1);
+            for (int i = 0; i < STAGES; ++i) {
+                mbar_init(&full[i], kLoadGroup * 33);
+                mbar_init(&freed[i], 1);
+            }
+            mbar_init(&all_done, 1);
             fence_mbar_init();
         }
         tc_before();
         __syncthreads();
         tc_after();
         tmem = tmem_at;
-
-        // 16 threads a row of 128 columns, or of V's hi and lo; 16 rows at a time
-        const int my_row = threadIdx.x >> 4, my_c = threadIdx.x & 15;
-        const uint32_t my_at = (my_c >> 3) * 64 * 128 + swz(my_row, my_c & 7);
-        int tok[4];  // the rows of the chunk that is loaded next, fetched one chunk early
-        auto next_tokens = [&](int i) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int at = first + (rank + i * size) * 64 + my_row + 16 * q;
-                tok[q] = at < last ? g.order[at] : 0;
-            }
-        };
-        next_tokens(0);
-        auto load = [&](int i) {
-            if (i < n) {
-                const uint32_t slot = base + (i % STAGES) * slot_bytes;
-                const int t0 = first + (rank + i * size) * 64 + my_row;
-                const int at = c0 + my_c * 8;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const bool there = t0 + 16 * q < last;
-                    piece(slot + my_at + q * 2048, in + tok[q] * ld + at, there ? cols - at : 0, al, in);
+        if (warp < kGradLoadWarps) {
+            // Two groups of four warps take chunks in turn.  A warp loads 512 bytes of one token at a time.
+            const __nv_bfloat16 *in = is_a ? g.x : g.in;
+            const int64_t ld = is_a ? g.ld_x : g.ld_in;
+            const bool al = is_a ? g.al_x : g.al_in;
+            const __nv_bfloat16 *v = g.work + (is_a ? 0 : static_cast<int64_t>(g.tokens) * 2 * g.rank16);
+            const int group = warp / kLoadGroup, id = threadIdx.x & 127, w4 = id >> 5;
+            const int at = c0 + lane * 8, valid = cols - at;
+            const uint32_t tile = (lane >> 3) * T::kTile;
+            // V: 16 threads a token, eight of them its hi part
+            const int v_row = id >> 4, v_lo = (id >> 3) & 1, v_c = id & 7;
+            auto fetch = [&](int i) {  // the tokens of a chunk, one a lane
+                const int t = first + (static_cast<int>(rank) + i * static_cast<int>(size)) * kGradTokens + w4 + 4 * lane;
+                return i < n && lane < 16 && t < last ? g.order[t] : 0;
+            };
+            int token = fetch(group);
+            for (int i = group; i < n; i += 2) {
+                const int s = i % STAGES;
+                const uint32_t slot = base + s * T::kSlot;
+                const int t0 = first + (static_cast<int>(rank) + i * static_cast<int>(size)) * kGradTokens;
+                const int left = last - t0;  // tokens from this chunk's first one on; the rest of it is zero
+                if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
+#pragma unroll 4
+                for (int q = 0; q < 16; ++q) {
+                    const int64_t t = __shfl_sync(kFull, token, q);
+                    piece(slot + tile + swz(w4 + 4 * q, lane & 7), in + t * ld + at, w4 + 4 * q < left ? valid : 0, al,
+                          in);
                 }
-                const __nv_bfloat16 *from = v + (static_cast<int64_t>(t0) * 2 + (my_c >> 3)) * g.rank16 + (my_c & 7) * 8;
-                const uint32_t to = slot + 2 * 64 * 128 + (my_c >> 3) * v_bytes + swz(my_row, my_c & 7);
-                for (int c = 0; c < r16; c += 64)
-                    if (c + (my_c & 7) * 8 < r16)
+                for (int c = v_c * 8; c < r16; c += 64) {
+                    const __nv_bfloat16 *from = v + (static_cast<int64_t>(t0 + v_row) * 2 + v_lo) * g.rank16 + c;
+                    const uint32_t to = slot + T::kIn + v_lo * T::kV + (c >> 6) * T::kTile + swz(v_row, v_c);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            piece(to + c * 128 + q * 2048, from + c + 32 * q * static_cast<int64_t>(g.rank16),
-                                  t0 + 16 * q < last ? 8 : 0, true, v);
-                next_tokens(i + 1);
-            }
-            async_commit();
-        };
-        for (int i = 0; i < STAGES - 1; ++i) load(i);
-        for (int i = 0; i < n; ++i) {
-            async_wait<STAGES - 2>();
-            fence_proxy_async();
-            tc_before();
-            __syncthreads();
-            tc_after();
-            if (threadIdx.x == 0 && !waiter.dead) {
-                const uint32_t slot = base + (i % STAGES) * slot_bytes, w = slot + 2 * 64 * 128;
-                const uint32_t word = mma_word(r16, true, true);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint64_t m = operand(slot + k * 16 * 128, 64 * 128);
-                    mma(tmem, m, operand(w + k * 16 * 128, 64 * 128), word, i > 0 || k > 0);
-                    mma(tmem, m, operand(w + v_bytes + k * 16 * 128, 64 * 128), word, true);
+                    for (int q = 0; q < 8; ++q)
+                        async16(to + q * 1024, v_row + 8 * q < left ? from + q * 16 * g.rank16 : v,
+                                v_row + 8 * q < left ? 16 : 0);
                 }
-                mma_commit(&done[i % STAGES]);
+                arrive_full(&full[s], lane);
+                token = fetch(i + 2);
             }
-            if (i > 0 && i + STAGES - 1 < n) waiter.wait(&done[(i - 1) % STAGES], ((i - 1) / STAGES) & 1);
-            load(i + STAGES - 1);
+            async_wait<0>();
+            if (n > 0) waiter.wait(&all_done, 0);
+        } else {
+            const uint32_t word = mma_word(r16, true, true);
+            const uint64_t in0 = operand(base, T::kTile), v0 = operand(base + T::kIn, T::kTile);
+            const bool two = c0 + 128 < cols;
+            for (int i = 0; i < n; ++i) {
+                const int s = i % STAGES;
+                waiter.wait(&full[s], (i / STAGES) & 1);
+                fence_proxy_async();
+                tc_after();
+                if (elect() && !waiter.dead) {
+                    const uint64_t x = in0 + s * (T::kSlot >> 4), v = v0 + s * (T::kSlot >> 4);
+#pragma unroll
+                    for (int k = 0; k < kGradTokens / 16; ++k) {
+                        mma(tmem, x + k * 128, v + k * 128, word, i > 0 || k > 0);
+                        mma(tmem, x + k * 128, v + (T::kV >> 4) + k * 128, word, true);
+                        if (two) {
+                            mma(tmem + 128, x + (2 * T::kTile >> 4) + k * 128, v + k * 128, word, i > 0 || k > 0);
+                            mma(tmem + 128, x + (2 * T::kTile >> 4) + k * 128, v + (T::kV >> 4) + k * 128, word, true);
+                        }
+                    }
+                    mma_commit(&freed[s]);
+                    if (i == n - 1) mma_commit(&all_done);
+                }
+                __syncwarp();
+            }
+            if (n > 0) waiter.wait(&all_done, 0);
         }
-        if (n > 0) waiter.wait(&done[(n - 1) % STAGES], ((n - 1) / STAGES) & 1);
-        async_wait<0>();
         tc_after();
         __syncthreads();
-    }
-
-    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-    if (used) {
-        for (int p = half; p < r16 / 8; p += 2) {
-            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (n > 0) {
-                tmem_load8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + p * 8, x);
-                tmem_wait();
-            }
+        // the block's sums: [rank][column]
+        if (warp < kGradLoadWarps) {
+            const int quarter = warp & 3, half = warp >> 2, col = half * 128 + quarter * 32 + lane;
+            const uint32_t lanes = tmem + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+            if (c0 + half * 128 < cols)
+                for (int p = 0; p < r16 / 8; ++p) {
+                    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (n > 0) {
+                        tmem_load8(lanes + p * 8, x);
+                        tmem_wait();
+                    }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((p * 8 + i) * 128 + row) * 4), "f"(x[i]) : "memory");
+                    for (int j = 0; j < 8; ++j)
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((p * 8 + j) * kGradCols + col) * 4),
+                                     "f"(x[j])
+                                     : "memory");
+                }
         }
         tc_before();
     }
     __syncwarp();
     cluster_sync();
-    // this block's share of the ranks
-    for (int i = rank * 2 + half; i < g.rank; i += 2 * size) {
-        float s = 0.0f;
-        if (i < used)
-            for (uint32_t peer = 0; peer < size; ++peer) s += peer_float(base + (i * 128 + row) * 4, peer);
-        if (c0 + row < cols) {
-            if (is_a)
-                g.da[(static_cast<int64_t>(a) * g.rank + i) * g.k + c0 + row] = __float2bfloat16_rn(s);
-            else
-                g.db[(static_cast<int64_t>(a) * g.n + c0 + row) * g.rank + i] = __float2bfloat16_rn(s);
+    // Everyone's, eight ranks of a column at a time, by the blocks in turn.
+    const int col = threadIdx.x;
+    if (col < kGradCols && c0 + col < cols)
+        for (int p = rank; p * 8 < g.rank; p += size) {
+            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (p * 8 < used)  // sums beyond the used ranks, up to the next 16, are zero
+                for (uint32_t peer = 0; peer < size; ++peer) {
+                    const uint32_t there = peer_addr(base + (p * 8 * kGradCols + col) * 4, peer);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] += peer_float(there + j * kGradCols * 4);
+                }
+            if (is_a) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (p * 8 + j < g.rank)
+                        g.da[(static_cast<int64_t>(a) * g.rank + p * 8 + j) * g.k + c0 + col] =
+                            __float2bfloat16_rn(p * 8 + j < used ? x[j] : 0.0f);
+            } else {
+                __nv_bfloat16 *to = g.db + (static_cast<int64_t>(a) * g.n + c0 + col) * g.rank + p * 8;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = p * 8 + j < used ? x[j] : 0.0f;
+                if (g.al_db)
+                    *reinterpret_cast<uint4 *>(to) =
+                        make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+                else
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (p * 8 + j < g.rank) to[j] = __float2bfloat16_rn(x[j]);
+            }
         }
-    }
     if (waiter.dead) fail(g);
     __syncwarp();
     cluster_sync();
-    if (used && warp == 0) tmem_free(tmem, 128);
+    if (used && warp == 0) tmem_free(tmem, kGradTmemCols);
 }
 
 // -------------------------------------------------------------- the plan
@@ -1296,15 +1341,6 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, uint32_t threads, uint32_t s
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Blocks of a cluster: as many as keep the grid within what the GPU holds at
-// once, two blocks on each SM, and as there are chunks to share out.
-uint32_t cluster_for(uint64_t tiles, uint64_t chunks)
-{
-    uint32_t c = 1;
-    while (c < 8 && tiles * c * 2 <= 304 && 2ull * c <= chunks) c *= 2;
-    return c;
-}
-
 // How many clusters of a size the GPU holds at once (0: none, or an error).
 template <typename... P>
 uint32_t clusters_at_once(void (*kernel)(P...), uint32_t threads, uint32_t smem, uint32_t cluster)
@@ -1382,13 +1418,41 @@ cudaError_t launch_adapter(const AdapterArgs &a, bool back, cudaStream_t s)
     return back ? launch_tokens<true>(a, s) : launch_tokens<false>(a, s);
 }
 
+namespace {
+
+// As for the tokens' part; a turn's fixed part measures like about 8 chunks.
+// Where an adapter has a chunk or two, the ring is short, so that two blocks
+// share an SM.
+template <int RANK, int STAGES>
+cudaError_t launch_grad_at(const AdapterArgs &a, uint64_t blocks, uint64_t chunks, cudaStream_t s)
+{
+    const auto kernel = dev::k_adapter_grad<RANK, STAGES>;
+    constexpr uint32_t smem = dev::Grad<RANK, STAGES>::kBytes;
+    const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (rc != cudaSuccess) return rc;
+    uint64_t best = ~0ull;
+    uint32_t c = 0;
+    for (uint32_t d = 1; d <= 8 && d <= chunks; ++d) {
+        const uint32_t f = clusters_at_once(kernel, dev::kGradAdThreads, smem, d);
+        if (!f) continue;
+        const uint64_t cost = (blocks + f - 1) / f * ((chunks + d - 1) / d + 8);
+        if (cost < best) best = cost, c = d;
+    }
+    if (!c) return cudaErrorInvalidConfiguration;
+    const uint32_t cols = (a.k + dev::kGradCols - 1) / dev::kGradCols + (a.n + dev::kGradCols - 1) / dev::kGradCols;
+    return launch(kernel, dim3(c, cols, a.adapters), dev::kGradAdThreads, smem, c, s, a);
+}
+
+}  // namespace
+
 cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s)
 {
-    const uint32_t cols = (a.k + 127) / 128 + (a.n + 127) / 128;
-    const uint32_t c = cluster_for(static_cast<uint64_t>(cols) * a.adapters, (a.tokens + 63) / 64);
-    const uint32_t atoms = a.rank > 64 ? 2 : 1;
-    const uint32_t smem = 3 * (2 * 64 * 128 + 2 * atoms * 64 * 128) + 1024;
-    return launch(dev::k_adapter_grad<3>, dim3(c, cols, a.adapters), dev::kAdThreads, smem, c, s, a);
+    const uint64_t busy = std::min(a.adapters, a.tokens);
+    const uint64_t chunks = (a.tokens / busy + dev::kGradTokens - 1) / dev::kGradTokens;
+    const uint64_t blocks = ((a.k + dev::kGradCols - 1) / dev::kGradCols + (a.n + dev::kGradCols - 1) / dev::kGradCols) * busy;
+    if (chunks <= 2)
+        return a.rank <= 64 ? launch_grad_at<64, 2>(a, blocks, chunks, s) : launch_grad_at<128, 2>(a, blocks, chunks, s);
+    return a.rank <= 64 ? launch_grad_at<64, 4>(a, blocks, chunks, s) : launch_grad_at<128, 3>(a, blocks, chunks, s);
 }
 
 cudaError_t launch_adapter_plan(const PlanArgs &a, cudaStream_t s)
@@ -1600,6 +1664,7 @@ extern "C" lct_status lct_adapter_backward(const lct_adapters *bank, const lct_t
         g.work = static_cast<__nv_bfloat16 *>(d_work);
         g.da = reinterpret_cast<__nv_bfloat16 *>(d_da);
         g.db = reinterpret_cast<__nv_bfloat16 *>(d_db);
+        g.al_db = al16(d_db) && g.rank % 8 == 0;
     }
     if (launch_adapter(g, true, s) != cudaSuccess) return LCT_ERR_CUDA;
     if (d_da && launch_adapter_grad(g, s) != cudaSuccess) return LCT_ERR_CUDA;
