@@ -1066,7 +1066,8 @@ struct Grad {
     static constexpr uint32_t kBytes = (STAGES * kSlot > kSums ? STAGES * kSlot : kSums) + 1024;
 };
 
-template <int RANK, int STAGES>
+// FAST: every row begins at a 16-byte boundary.
+template <int RANK, int STAGES, bool FAST>
 __global__ void __launch_bounds__(kGradAdThreads) k_adapter_grad(const __grid_constant__ AdapterArgs g)
 {
     using T = Grad<RANK, STAGES>;
@@ -1105,13 +1106,17 @@ __global__ void __launch_bounds__(kGradAdThreads) k_adapter_grad(const __grid_co
             // Two groups of four warps take chunks in turn.  A warp loads 512 bytes of one token at a time.
             const __nv_bfloat16 *in = is_a ? g.x : g.in;
             const int64_t ld = is_a ? g.ld_x : g.ld_in;
-            const bool al = is_a ? g.al_x : g.al_in;
             const __nv_bfloat16 *v = g.work + (is_a ? 0 : static_cast<int64_t>(g.tokens) * 2 * g.rank16);
             const int group = warp / kLoadGroup, id = threadIdx.x & 127, w4 = id >> 5;
             const int at = c0 + lane * 8, valid = cols - at;
-            const uint32_t tile = (lane >> 3) * T::kTile;
+            const uint32_t bytes = valid <= 0 ? 0u : static_cast<uint32_t>(min(valid, 8)) * 2;
+            const __nv_bfloat16 *from = in + at;
+            // its tokens lie four rows apart, so in two places of the eight that the swizzle has
+            const uint32_t even = (lane >> 3) * T::kTile + swz(w4, lane & 7);
+            const uint32_t odd = (lane >> 3) * T::kTile + swz(w4 + 4, lane & 7);
             // V: 16 threads a token, eight of them its hi part
             const int v_row = id >> 4, v_lo = (id >> 3) & 1, v_c = id & 7;
+            const uint32_t v_to = T::kIn + v_lo * T::kV + swz(v_row, v_c);
             auto fetch = [&](int i) {  // the tokens of a chunk, one a lane
                 const int t = first + (static_cast<int>(rank) + i * static_cast<int>(size)) * kGradTokens + w4 + 4 * lane;
                 return i < n && lane < 16 && t < last ? g.order[t] : 0;
@@ -1123,19 +1128,39 @@ __global__ void __launch_bounds__(kGradAdThreads) k_adapter_grad(const __grid_co
                 const int t0 = first + (static_cast<int>(rank) + i * static_cast<int>(size)) * kGradTokens;
                 const int left = last - t0;  // tokens from this chunk's first one on; the rest of it is zero
                 if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
-#pragma unroll 4
-                for (int q = 0; q < 16; ++q) {
-                    const int64_t t = __shfl_sync(kFull, token, q);
-                    piece(slot + tile + swz(w4 + 4 * q, lane & 7), in + t * ld + at, w4 + 4 * q < left ? valid : 0, al,
-                          in);
-                }
-                for (int c = v_c * 8; c < r16; c += 64) {
-                    const __nv_bfloat16 *from = v + (static_cast<int64_t>(t0 + v_row) * 2 + v_lo) * g.rank16 + c;
-                    const uint32_t to = slot + T::kIn + v_lo * T::kV + (c >> 6) * T::kTile + swz(v_row, v_c);
+                if (FAST && left >= kGradTokens) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        async16(to + q * 1024, v_row + 8 * q < left ? from + q * 16 * g.rank16 : v,
-                                v_row + 8 * q < left ? 16 : 0);
+                    for (int q = 0; q < 16; ++q)
+                        async16(slot + (q & 1 ? odd : even) + q / 2 * 1024,
+                                from + static_cast<int64_t>(__shfl_sync(kFull, token, q)) * ld, bytes);
+                    for (int c = v_c * 8; c < r16; c += 64) {
+                        const __nv_bfloat16 *p = v + (static_cast<int64_t>(t0 + v_row) * 2 + v_lo) * g.rank16 + c;
+                        const uint32_t to = slot + v_to + (c >> 6) * T::kTile;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) async16(to + q * 1024, p + q * 16 * g.rank16, 16);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int h = 0; h < 16; h += 4) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int64_t t = __shfl_sync(kFull, token, h + q);
+                            x[q] = gather8(from + t * ld, w4 + 4 * (h + q) < left ? valid : 0);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            store16(slot + (q & 1 ? odd : even) + (h + q) / 2 * 1024, x[q]);
+                    }
+                    for (int c = v_c * 8; c < r16; c += 64) {
+                        const __nv_bfloat16 *p = v + (static_cast<int64_t>(t0 + v_row) * 2 + v_lo) * g.rank16 + c;
+                        const uint32_t to = slot + v_to + (c >> 6) * T::kTile;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const bool there = v_row + 8 * q < left;
+                            async16(to + q * 1024, there ? p + q * 16 * g.rank16 : v, there ? 16 : 0);
+                        }
+                    }
                 }
                 arrive_full(&full[s], lane);
                 token = fetch(i + 2);
@@ -1423,10 +1448,10 @@ namespace {
 // As for the tokens' part; a turn's fixed part measures like about 8 chunks.
 // Where an adapter has a chunk or two, the ring is short, so that two blocks
 // share an SM.
-template <int RANK, int STAGES>
+template <int RANK, int STAGES, bool FAST>
 cudaError_t launch_grad_at(const AdapterArgs &a, uint64_t blocks, uint64_t chunks, cudaStream_t s)
 {
-    const auto kernel = dev::k_adapter_grad<RANK, STAGES>;
+    const auto kernel = dev::k_adapter_grad<RANK, STAGES, FAST>;
     constexpr uint32_t smem = dev::Grad<RANK, STAGES>::kBytes;
     const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (rc != cudaSuccess) return rc;
@@ -1443,6 +1468,13 @@ cudaError_t launch_grad_at(const AdapterArgs &a, uint64_t blocks, uint64_t chunk
     return launch(kernel, dim3(c, cols, a.adapters), dev::kGradAdThreads, smem, c, s, a);
 }
 
+template <int RANK, int STAGES>
+cudaError_t launch_grad(const AdapterArgs &a, bool fast, uint64_t blocks, uint64_t chunks, cudaStream_t s)
+{
+    return fast ? launch_grad_at<RANK, STAGES, true>(a, blocks, chunks, s)
+                : launch_grad_at<RANK, STAGES, false>(a, blocks, chunks, s);
+}
+
 }  // namespace
 
 cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s)
@@ -1450,9 +1482,10 @@ cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s)
     const uint64_t busy = std::min(a.adapters, a.tokens);
     const uint64_t chunks = (a.tokens / busy + dev::kGradTokens - 1) / dev::kGradTokens;
     const uint64_t blocks = ((a.k + dev::kGradCols - 1) / dev::kGradCols + (a.n + dev::kGradCols - 1) / dev::kGradCols) * busy;
-    if (chunks <= 2)
-        return a.rank <= 64 ? launch_grad_at<64, 2>(a, blocks, chunks, s) : launch_grad_at<128, 2>(a, blocks, chunks, s);
-    return a.rank <= 64 ? launch_grad_at<64, 4>(a, blocks, chunks, s) : launch_grad_at<128, 3>(a, blocks, chunks, s);
+    const bool fast = a.al_x && a.al_in, few = chunks <= 2;
+    if (a.rank <= 64)
+        return few ? launch_grad<64, 2>(a, fast, blocks, chunks, s) : launch_grad<64, 4>(a, fast, blocks, chunks, s);
+    return few ? launch_grad<128, 2>(a, fast, blocks, chunks, s) : launch_grad<128, 3>(a, fast, blocks, chunks, s);
 }
 
 cudaError_t launch_adapter_plan(const PlanArgs &a, cudaStream_t s)
