@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "../../include/lct.h"
@@ -25,6 +26,15 @@
 #include "internal.h"
 
 namespace lct {
+
+// Boxes of the matrices that the kernels read.
+struct TokenMaps {
+    CUtensorMap in, base, a, b;
+};
+struct GradMaps {
+    CUtensorMap x, dy, d, v;
+};
+
 namespace dev {
 
 constexpr int kAdThreads = 256;
@@ -263,10 +273,10 @@ __device__ __forceinline__ void fail(const AdapterArgs &g)
     if (g.status) atomicCAS(reinterpret_cast<unsigned int *>(g.status), 0u, static_cast<unsigned int>(LCT_ERR_TIMEOUT));
 }
 
-// Waits at a barrier for a limited number of tries (each of which the hardware
-// holds for a while, so that it is seconds in all, where a wait that passes
-// takes microseconds).  After one wait that ran out, none waits again.
-constexpr uint32_t kWaitTries = 1u << 23;
+// Waits at a barrier, for at most about a second by the SM's clock (a wait
+// that passes takes microseconds).  After one wait that ran out, none waits
+// again.
+constexpr uint32_t kWaitClocks = 1800000000u;
 __device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -281,30 +291,32 @@ __device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity)
 }
 struct Waiter {
     bool dead = false;
+    template <typename Ready>
+    __device__ __forceinline__ void until(Ready ready)
+    {
+        if (dead || ready()) return;
+        const uint32_t t0 = static_cast<uint32_t>(clock());
+#pragma unroll 1
+        while (!ready())
+            if (static_cast<uint32_t>(clock()) - t0 > kWaitClocks) {
+                dead = true;
+                break;
+            }
+    }
     __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity)  // for this block's own warps
     {
-        uint32_t left = dead ? 0 : kWaitTries;
-#pragma unroll 1
-        while (left && !mbar_try(bar, parity)) --left;
-        dead = left == 0;
+        until([&] { return mbar_try(bar, parity); });
     }
     __device__ __forceinline__ void wait_both(uint64_t *a, uint32_t a_parity, uint64_t *b, uint32_t b_parity)
     {
-        uint32_t left = dead ? 0 : kWaitTries;
-#pragma unroll 1
-        while (left) {
+        until([&] {
             const bool x = mbar_try(a, a_parity), y = mbar_try(b, b_parity);
-            if (x && y) break;
-            --left;
-        }
-        dead = left == 0;
+            return x && y;
+        });
     }
     __device__ __forceinline__ void wait_cluster(uint64_t *bar, uint32_t parity)  // for the cluster's
     {
-        uint32_t left = dead ? 0 : kWaitTries;
-#pragma unroll 1
-        while (left && !try_cluster(smem_addr(bar), parity)) --left;
-        dead = left == 0;
+        until([&] { return try_cluster(smem_addr(bar), parity); });
     }
 };
 
@@ -325,9 +337,9 @@ __device__ __forceinline__ void set_sync(int half) { asm volatile("bar.sync %0, 
 __device__ __forceinline__ void out_warps_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // Warps by what they do: eight turn sums into results, one issues the
-// products, eight load.  They meet at mbarriers only, so that a load never
+// products, one loads boxes (TMA) and eight load what no box holds.  They meet at mbarriers only, so that a load never
 // waits for a result to be written.
-constexpr int kOutWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 8;
+constexpr int kOutWarps = 8, kMmaWarp = 8, kBoxWarp = 9, kLoadWarp = 10, kLoadWarps = 8;
 constexpr int kLoadGroup = 4;  // warps that load one chunk; the groups take chunks in turn
 constexpr int kTokThreads = 32 * (kLoadWarp + kLoadWarps);
 
@@ -349,6 +361,50 @@ __device__ __forceinline__ uint16_t load2(uint32_t at)
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
     return v;
+}
+
+// A box of a row-major matrix into a row-swizzled tile, and one of a stack of
+// matrices; what lies outside is zero.  x is a multiple of 64.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, int x, int y, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(m), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void arrive_many(uint64_t *bar, uint32_t count)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+
+// Boxes are 32 rows high.  Bit i of the result: rows 32 i .. of a tile are not
+// consecutive tokens, so that no box holds them; `y` is the first token of the
+// group of 32 that lane 8 i belongs to.  (A box with rows past the tile's
+// tokens brings others', which reach only themselves.)
+constexpr int kBoxRows = 32;
+__device__ __forceinline__ uint32_t scattered(const int32_t *order, int first, int count, int lane, int &y)
+{
+    int t[4];
+    bool in_line = true;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = lane * 4 + j < count ? order[first + lane * 4 + j] : 0;
+    y = __shfl_sync(kFull, t[0], lane & ~7);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) in_line = in_line && (lane * 4 + j >= count || t[j] == y + (lane & 7) * 4 + j);
+    const uint32_t bad = __ballot_sync(kFull, !in_line);
+    uint32_t groups = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) groups |= (bad >> (8 * i) & 0xFF ? 1u : 0u) << i;
+    return groups;
 }
 
 // ------------------------------------------------------- the tokens' part
@@ -427,9 +483,12 @@ __device__ __forceinline__ void pieces(uint32_t dst, Src src, int valid, int row
 //
 // BACK = false: In = x, W1 = A [R, K], W2 = B [N, R], V = s (x A^T).
 // BACK = true:  In = dy, W1 = B [N, R], W2 = A [R, K], V = s (dy B).
-// FAST: every row begins at a 16-byte boundary.
+// FAST: every row begins at a 16-byte boundary.  Then runs of 32 consecutive
+// tokens, and the weights where g.boxes_w says so (a rank that is a multiple of
+// 16, which all adapters use), come as boxes.
 template <bool BACK, int RANK, bool FAST>
-__global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constant__ AdapterArgs g)
+__global__ void __launch_bounds__(kTokThreads, 1)
+    k_adapter(const __grid_constant__ AdapterArgs g, const __grid_constant__ TokenMaps maps)
 {
     using T = Tok<RANK>;
     constexpr int S = T::kStages;
@@ -447,7 +506,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
     if (warp == 0) tmem_alloc(&tmem_at, kTmemCols);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], kFullArrivals);
+            mbar_init(&full[i], kFullArrivals + 1);
             mbar_init(&freed[i], 1);
         }
         mbar_init(&narrow, 1);
@@ -480,6 +539,9 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
             if (w.count <= 0) break;
             const int start = rank * kChunk + col, stride = static_cast<int>(size) * kChunk;
             const int left = w.count - row0;  // rows from this thread's first one on
+            int y;
+            const uint32_t loose = FAST ? scattered(g.order, w.first, w.count, lane, y) : 0xFu;
+            const bool boxes_w = FAST && g.boxes_w;
             int t[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) t[q] = 16 * q < left ? g.order[w.first + row0 + 16 * q] : 0;
@@ -520,15 +582,18 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                     if (i >= S) waiter.wait(&freed[s], (i / S - 1) & 1);
                     const uint32_t slot = base + s * T::kSlot;
                     const int valid = cols - start - step;
-                    if (w.count > 64)
-                        pieces<FAST, 8>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
-                    else if (w.count > 32)
-                        pieces<FAST, 4>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
-                    else if (w.count > 16)
+                    if (FAST && loose == 0 && (boxes_w || !w.used)) continue;  // boxes hold all of it
+                    if (!FAST && w.count <= 32)
                         pieces<FAST, 2>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
+                    else if (!FAST)
+                        pieces<FAST, 8>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
                     else
-                        pieces<FAST, 1>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
-                    if (w.used) two == BACK ? load_a(slot + kInBytes, step) : load_b(slot + kInBytes, step);
+#pragma unroll
+                        for (int q = 0; q < 8; q += 2)
+                            if (loose >> q / 2 & 1)
+                                pieces<FAST, 2>(slot + at + q * 2048, [&](int e) { return p[q + e] + step; }, valid,
+                                                left - 16 * q, al);
+                    if (w.used && !boxes_w) two == BACK ? load_a(slot + kInBytes, step) : load_b(slot + kInBytes, step);
                     arrive_full(&full[s], lane);
                 }
             };
@@ -536,6 +601,56 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
             product(g.base, g.ld_base, g.al_base, g.nout, w.n2, true);
         }
         async_wait<0>();
+    } else if (warp == kBoxWarp) {
+        // ------------------------------------------------------------ boxes
+        int i = 0, s = 0;
+        for (int tile = first_tile;; tile += clusters) {
+            const TileWork w = tile_work(g, tile, rank, size);
+            if (w.count <= 0) break;
+            int mine = 0, y[4];
+            const uint32_t loose = FAST ? scattered(g.order, w.first, w.count, lane, mine) : 0xFu;
+            uint32_t groups = 0, bytes = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[j] = __shfl_sync(kFull, mine, 8 * j);
+                if (j * kBoxRows < w.count && !(loose >> j & 1)) groups |= 1u << j, bytes += kBoxRows * 128;
+            }
+            const bool weights = FAST && g.boxes_w && w.used, alone = FAST && loose == 0 && (weights || !w.used);
+            // the weights' boxes: A, R rows of 64 columns; B, 64 rows of R columns
+            const uint32_t a_bytes = weights ? g.rank * 128 : 0, b_bytes = weights ? T::kWBytes : 0;
+            auto product = [&](const CUtensorMap *m, int chunks, bool two) {
+                int c0 = rank * kChunk;
+                for (int k = 0; k < chunks; ++k, ++i, s = s + 1 == S ? 0 : s + 1, c0 += size * kChunk) {
+                    if (i >= S) waiter.wait(&freed[s], (i / S - 1) & 1);
+                    if (elect()) {
+                        const uint32_t slot = base + s * T::kSlot;
+                        const uint32_t due = bytes + (two == BACK ? a_bytes : b_bytes);
+                        if (due)
+                            mbar_expect_tx(&full[s], due);
+                        else
+                            mbar_arrive(&full[s]);
+                        if (alone) arrive_many(&full[s], kFullArrivals);
+                        if (FAST) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (groups >> j & 1) load_box(slot + j * kBoxRows * 128, m, c0, y[j], &full[s]);
+                            if (weights) {
+                                if (two == BACK) {
+                                    load_box(slot + kInBytes, &maps.a, c0, 0, w.a, &full[s]);
+                                } else {
+#pragma unroll
+                                    for (int h = 0; h < T::kAtoms; ++h)
+                                        load_box(slot + kInBytes + h * 64 * 128, &maps.b, 64 * h, c0, w.a, &full[s]);
+                                }
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            };
+            product(&maps.in, w.n1, false);
+            product(&maps.base, w.n2, true);
+        }
     } else if (warp == kMmaWarp) {
         // --------------------------------------------------------- products
         int i = 0, s = 0, q = 0, tiles = 0;  // chunks and their slot, chunks of second products, tiles with a product
@@ -788,6 +903,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) k_adapter(const __grid_constan
                         if (at + 32 < g.nout) to[at + 32] = load2(far);
                     }
                 }
+                fence_proxy_async();  // the slot's next chunk may be a box
                 set_sync(half);
                 if ((threadIdx.x & 127) == 0) mbar_arrive(&freed[s]);
             }
@@ -1051,7 +1167,8 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
 // because every block of columns reads V again: 16 KB at R = 64 for 32 KB of x.
 constexpr int kGradCols = 256, kGradTokens = 64;
 constexpr int kGradLoadWarps = 8;  // which write the results at the end
-constexpr int kGradAdThreads = 32 * (kGradLoadWarps + 1);
+constexpr int kGradMmaWarp = kGradLoadWarps, kGradBoxWarp = kGradMmaWarp + 1;
+constexpr int kGradAdThreads = 32 * (kGradBoxWarp + 1);
 constexpr uint32_t kGradTmemCols = 256;
 
 template <int RANK, int STAGES>
@@ -1066,9 +1183,29 @@ struct Grad {
     static constexpr uint32_t kBytes = (STAGES * kSlot > kSums ? STAGES * kSlot : kSums) + 1024;
 };
 
-// FAST: every row begins at a 16-byte boundary.
+// The tokens of a chunk of 64, two a lane, and whether they are two runs of 32
+// consecutive ones.
+struct ChunkTokens {
+    int near, far;
+    bool runs;
+};
+__device__ __forceinline__ ChunkTokens chunk_tokens(const int32_t *order, int at, int last, bool there, int lane)
+{
+    ChunkTokens c = {0, 0, false};
+    if (!there) return c;
+    if (at + lane < last) c.near = order[at + lane];
+    if (at + 32 + lane < last) c.far = order[at + 32 + lane];
+    const int near0 = __shfl_sync(kFull, c.near, 0), far0 = __shfl_sync(kFull, c.far, 0);
+    const int in_line = __all_sync(kFull, c.near == near0 + lane && c.far == far0 + lane);
+    c.runs = in_line && at + kGradTokens <= last;
+    return c;
+}
+
+// FAST: every row begins at a 16-byte boundary.  Then a chunk of 64 tokens that
+// are two runs of 32 comes as boxes.
 template <int RANK, int STAGES, bool FAST>
-__global__ void __launch_bounds__(kGradAdThreads) k_adapter_grad(const __grid_constant__ AdapterArgs g)
+__global__ void __launch_bounds__(kGradAdThreads)
+    k_adapter_grad(const __grid_constant__ AdapterArgs g, const __grid_constant__ GradMaps maps)
 {
     using T = Grad<RANK, STAGES>;
     extern __shared__ uint8_t raw[];
@@ -1092,7 +1229,7 @@ __global__ void __launch_bounds__(kGradAdThreads) k_adapter_grad(const __grid_co
         if (warp == 0) tmem_alloc(&tmem_at, kGradTmemCols);
         if (threadIdx.x == 0) {
             for (int i = 0; i < STAGES; ++i) {
-                mbar_init(&full[i], kLoadGroup * 33);
+                mbar_init(&full[i], kFullArrivals);
                 mbar_init(&freed[i], 1);
             }
             mbar_init(&all_done, 1);
@@ -1102,6 +1239,9 @@ __global__ void __launch_bounds__(kGradAdThreads) k_adapter_grad(const __grid_co
         __syncthreads();
         tc_after();
         tmem = tmem_at;
+        auto chunk_at = [&](int i) {
+            return first + (static_cast<int>(rank) + i * static_cast<int>(size)) * kGradTokens;
+        };
         if (warp < kGradLoadWarps) {
             // Two groups of four warps take chunks in turn.  A warp loads 512 bytes of one token at a time.
             const __nv_bfloat16 *in = is_a ? g.x : g.in;
@@ -1117,22 +1257,22 @@ __global__ void __launch_bounds__(kGradAdThreads) k_adapter_grad(const __grid_co
             // V: 16 threads a token, eight of them its hi part
             const int v_row = id >> 4, v_lo = (id >> 3) & 1, v_c = id & 7;
             const uint32_t v_to = T::kIn + v_lo * T::kV + swz(v_row, v_c);
-            auto fetch = [&](int i) {  // the tokens of a chunk, one a lane
-                const int t = first + (static_cast<int>(rank) + i * static_cast<int>(size)) * kGradTokens + w4 + 4 * lane;
-                return i < n && lane < 16 && t < last ? g.order[t] : 0;
-            };
-            int token = fetch(group);
+            ChunkTokens tokens = chunk_tokens(g.order, chunk_at(group), last, group < n, lane);
             for (int i = group; i < n; i += 2) {
                 const int s = i % STAGES;
                 const uint32_t slot = base + s * T::kSlot;
-                const int t0 = first + (static_cast<int>(rank) + i * static_cast<int>(size)) * kGradTokens;
+                const int t0 = chunk_at(i);
                 const int left = last - t0;  // tokens from this chunk's first one on; the rest of it is zero
+                const ChunkTokens now = tokens;
+                tokens = chunk_tokens(g.order, chunk_at(i + 2), last, i + 2 < n, lane);
                 if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
+                if (FAST && now.runs) continue;  // boxes hold it
+                auto token = [&](int row) { return __shfl_sync(kFull, row < 32 ? now.near : now.far, row & 31); };
                 if (FAST && left >= kGradTokens) {
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         async16(slot + (q & 1 ? odd : even) + q / 2 * 1024,
-                                from + static_cast<int64_t>(__shfl_sync(kFull, token, q)) * ld, bytes);
+                                from + static_cast<int64_t>(token(w4 + 4 * q)) * ld, bytes);
                     for (int c = v_c * 8; c < r16; c += 64) {
                         const __nv_bfloat16 *p = v + (static_cast<int64_t>(t0 + v_row) * 2 + v_lo) * g.rank16 + c;
                         const uint32_t to = slot + v_to + (c >> 6) * T::kTile;
@@ -1145,7 +1285,7 @@ __global__ void __launch_bounds__(kGradAdThreads) k_adapter_grad(const __grid_co
                         uint4 x[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const int64_t t = __shfl_sync(kFull, token, h + q);
+                            const int64_t t = token(w4 + 4 * (h + q));
                             x[q] = gather8(from + t * ld, w4 + 4 * (h + q) < left ? valid : 0);
                         }
 #pragma unroll
@@ -1163,9 +1303,34 @@ __global__ void __launch_bounds__(kGradAdThreads) k_adapter_grad(const __grid_co
                     }
                 }
                 arrive_full(&full[s], lane);
-                token = fetch(i + 2);
             }
             async_wait<0>();
+            if (n > 0) waiter.wait(&all_done, 0);
+        } else if (warp == kGradBoxWarp) {
+            ChunkTokens tokens = chunk_tokens(g.order, chunk_at(0), last, FAST && n > 0, lane);
+            for (int i = 0; FAST && i < n; ++i) {
+                const int s = i % STAGES;
+                const ChunkTokens now = tokens;
+                tokens = chunk_tokens(g.order, chunk_at(i + 1), last, i + 1 < n, lane);
+                if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
+                const int y[2] = {__shfl_sync(kFull, now.near, 0), __shfl_sync(kFull, now.far, 0)};
+                if (now.runs && elect()) {
+                    const uint32_t slot = base + s * T::kSlot;
+                    const CUtensorMap *m = is_a ? &maps.x : &maps.dy, *v = is_a ? &maps.d : &maps.v;
+                    mbar_expect_tx(&full[s], T::kSlot);
+                    arrive_many(&full[s], kFullArrivals - 1);
+#pragma unroll
+                    for (int j = 0; j < kGradCols / 64; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            load_box(slot + j * T::kTile + h * kBoxRows * 128, m, c0 + 64 * j, y[h], &full[s]);
+#pragma unroll
+                    for (int j = 0; j < 2 * T::kAtoms; ++j)
+                        load_box(slot + T::kIn + j * T::kTile, v, (j >= T::kAtoms) * g.rank16 + j % T::kAtoms * 64,
+                                 chunk_at(i), &full[s]);
+                }
+                __syncwarp();
+            }
             if (n > 0) waiter.wait(&all_done, 0);
         } else {
             const uint32_t word = mma_word(r16, true, true);
@@ -1366,6 +1531,35 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, uint32_t threads, uint32_t s
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// A box map of [planes][rows][cols] BF16 (planes 0: a plain matrix) for boxes
+// of 64 columns by `box` rows in the 128-byte swizzle.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+bool box_map(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t planes, uint32_t box)
+{
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    if (rows == 1) ld = (cols + 7) / 8 * 8;  // the stride of a single row means nothing, but has to be one
+    const cuuint64_t dims[3] = {cols, rows, planes}, strides[2] = {2 * ld, 2 * ld * rows};
+    const cuuint32_t size[3] = {64, box, 1}, step[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, const_cast<void *>(p), dims, strides, size, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // How many clusters of a size the GPU holds at once (0: none, or an error).
 template <typename... P>
 uint32_t clusters_at_once(void (*kernel)(P...), uint32_t threads, uint32_t smem, uint32_t cluster)
@@ -1392,8 +1586,19 @@ uint32_t clusters_at_once(void (*kernel)(P...), uint32_t threads, uint32_t smem,
 // turns x (chunks of a turn + 12) is taken, a chunk of the second product
 // counting twice for what it writes.
 template <bool BACK, int RANK, bool FAST>
-cudaError_t launch_tokens_at(const AdapterArgs &a, cudaStream_t s)
+cudaError_t launch_tokens_at(const AdapterArgs &args, cudaStream_t s)
 {
+    AdapterArgs a = args;
+    TokenMaps maps = {};
+    if (FAST) {
+        bool ok = box_map(&maps.in, a.in, a.nin, a.tokens, a.ld_in, 0, dev::kBoxRows);
+        if (ok && a.out) ok = box_map(&maps.base, a.base, a.nout, a.tokens, a.ld_base, 0, dev::kBoxRows);
+        a.boxes_w = !a.ranks && a.rank % 16 == 0;
+        if (ok && a.boxes_w)
+            ok = box_map(&maps.a, a.a, a.k, a.rank, a.k, a.adapters, a.rank) &&
+                 box_map(&maps.b, a.b, a.rank, a.n, a.rank, a.adapters, 64);
+        if (!ok) return cudaErrorInvalidValue;
+    }
     const auto kernel = dev::k_adapter<BACK, RANK, FAST>;
     constexpr uint32_t smem = dev::Tok<RANK>::kBytes;
     const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1410,7 +1615,7 @@ cudaError_t launch_tokens_at(const AdapterArgs &a, cudaStream_t s)
         if (cost < best) best = cost, c = d, fit = f;
     }
     if (!c) return cudaErrorInvalidConfiguration;
-    return launch(kernel, dim3(c * std::min(static_cast<uint32_t>(a.rows), fit)), dev::kTokThreads, smem, c, s, a);
+    return launch(kernel, dim3(c * std::min(static_cast<uint32_t>(a.rows), fit)), dev::kTokThreads, smem, c, s, a, maps);
 }
 template <bool BACK>
 cudaError_t launch_tokens(const AdapterArgs &a, cudaStream_t s)
@@ -1465,7 +1670,14 @@ cudaError_t launch_grad_at(const AdapterArgs &a, uint64_t blocks, uint64_t chunk
     }
     if (!c) return cudaErrorInvalidConfiguration;
     const uint32_t cols = (a.k + dev::kGradCols - 1) / dev::kGradCols + (a.n + dev::kGradCols - 1) / dev::kGradCols;
-    return launch(kernel, dim3(c, cols, a.adapters), dev::kGradAdThreads, smem, c, s, a);
+    GradMaps maps = {};
+    const uint64_t half = static_cast<uint64_t>(a.tokens) * 2 * a.rank16;
+    if (FAST && (!box_map(&maps.x, a.x, a.k, a.tokens, a.ld_x, 0, dev::kBoxRows) ||
+                 !box_map(&maps.dy, a.in, a.n, a.tokens, a.ld_in, 0, dev::kBoxRows) ||
+                 !box_map(&maps.d, a.work, 2 * a.rank16, a.tokens, 2 * a.rank16, 0, dev::kGradTokens) ||
+                 !box_map(&maps.v, a.work + half, 2 * a.rank16, a.tokens, 2 * a.rank16, 0, dev::kGradTokens)))
+        return cudaErrorInvalidValue;
+    return launch(kernel, dim3(c, cols, a.adapters), dev::kGradAdThreads, smem, c, s, a, maps);
 }
 
 template <int RANK, int STAGES>
@@ -1507,7 +1719,7 @@ struct Rows {
     uint64_t ld, cols, rows;
 };
 bool rows_ok(const Rows &m) { return m.p && al(m.p, 2) && m.ld >= m.cols && m.ld <= kMaxN; }
-bool rows_al(const Rows &m) { return al16(m.p) && (m.ld % 8 == 0 || m.rows == 1); }
+bool rows_al(const Rows &m) { return al16(m.p) && ((m.ld % 8 == 0 && m.ld < 1ull << 38) || m.rows == 1); }
 
 // Whether two matrices share no value: apart in memory, or column slices of
 // rows with one stride that do not meet.
