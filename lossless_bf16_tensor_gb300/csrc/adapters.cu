@@ -348,7 +348,16 @@ constexpr int kTokThreads = 32 * (kLoadWarp + kLoadWarps);
 // (one a warp).  It does not wait for them, and the fence that lets products
 // read what ordinary stores and copies wrote is the product warp's: before a
 // load warp's arrival that fence would wait for every copy in flight.
-constexpr uint32_t kFullArrivals = kLoadGroup * 33;
+//
+// Every load warp arrives for every chunk that is its group's, loads or not,
+// and so does the box warp: a warp that fell two of a slot's turns behind would
+// take its barrier's phase for another one.
+constexpr uint32_t kFullArrivals = kLoadGroup * 33 + 1;
+__device__ __forceinline__ void arrive_idle(uint64_t *bar, int lane)
+{
+    if (lane == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 33;" ::"r"(smem_addr(bar)) : "memory");
+}
 __device__ __forceinline__ void arrive_full(uint64_t *bar, int lane)
 {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -381,11 +390,6 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, int
         "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
 }
-__device__ __forceinline__ void arrive_many(uint64_t *bar, uint32_t count)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
-}
-
 // Boxes are 32 rows high.  Bit i of the result: rows 32 i .. of a tile are not
 // consecutive tokens, so that no box holds them; `y` is the first token of the
 // group of 32 that lane 8 i belongs to.  (A box with rows past the tile's
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     if (warp == 0) tmem_alloc(&tmem_at, kTmemCols);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], kFullArrivals + 1);
+            mbar_init(&full[i], kFullArrivals);
             mbar_init(&freed[i], 1);
         }
         mbar_init(&narrow, 1);
@@ -582,7 +586,10 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                     if (i >= S) waiter.wait(&freed[s], (i / S - 1) & 1);
                     const uint32_t slot = base + s * T::kSlot;
                     const int valid = cols - start - step;
-                    if (FAST && loose == 0 && (boxes_w || !w.used)) continue;  // boxes hold all of it
+                    if (FAST && loose == 0 && (boxes_w || !w.used)) {  // boxes hold all of it
+                        arrive_idle(&full[s], lane);
+                        continue;
+                    }
                     if (!FAST && w.count <= 32)
                         pieces<FAST, 2>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
                     else if (!FAST)
@@ -615,7 +622,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 y[j] = __shfl_sync(kFull, mine, 8 * j);
                 if (j * kBoxRows < w.count && !(loose >> j & 1)) groups |= 1u << j, bytes += kBoxRows * 128;
             }
-            const bool weights = FAST && g.boxes_w && w.used, alone = FAST && loose == 0 && (weights || !w.used);
+            const bool weights = FAST && g.boxes_w && w.used;
             // the weights' boxes: A, R rows of 64 columns; B, 64 rows of R columns
             const uint32_t a_bytes = weights ? g.rank * 128 : 0, b_bytes = weights ? T::kWBytes : 0;
             auto product = [&](const CUtensorMap *m, int chunks, bool two) {
@@ -629,7 +636,6 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                             mbar_expect_tx(&full[s], due);
                         else
                             mbar_arrive(&full[s]);
-                        if (alone) arrive_many(&full[s], kFullArrivals);
                         if (FAST) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
@@ -1165,6 +1171,11 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
 // fixed order.  The tokens are the products' inner dimension, so tiles are
 // read across: rows of a tile of x are columns of the operand.  256 columns,
 // because every block of columns reads V again: 16 KB at R = 64 for 32 KB of x.
+//
+// The products' rows are V's columns, up to R = 64 its hi part's and below
+// them its lo part's, and their 256 columns x's: 12 KB of operands for what
+// four products with x's 128 columns as rows would read 24 KB for, which is
+// what bounded them (57 cycles each, where 256 x 128 x 16 takes 128).
 constexpr int kGradCols = 256, kGradTokens = 64;
 constexpr int kGradLoadWarps = 8;  // which write the results at the end
 constexpr int kGradMmaWarp = kGradLoadWarps, kGradBoxWarp = kGradMmaWarp + 1;
@@ -1179,7 +1190,8 @@ struct Grad {
     static_assert(STAGES >= 2, "");
     static constexpr uint32_t kTile = kGradTokens * 128;  // 64 tokens by 64 columns
     static constexpr uint32_t kIn = kGradCols / 64 * kTile, kV = kAtoms * kTile, kSlot = kIn + 2 * kV;
-    static constexpr uint32_t kSums = RANK * kGradCols * 4;
+    static constexpr uint32_t kSumRow = (RANK + 1) * 4;  // one column's sums, an odd number of words
+    static constexpr uint32_t kSums = kGradCols * kSumRow;
     static constexpr uint32_t kBytes = (STAGES * kSlot > kSums ? STAGES * kSlot : kSums) + 1024;
 };
 
@@ -1221,6 +1233,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
     const int cols = is_a ? g.k : g.n;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+    float *sums = reinterpret_cast<float *>(raw + (base - smem_addr(raw)));
     const int all = (last - first + kGradTokens - 1) / kGradTokens;
     const int n = used && all > static_cast<int>(rank) ? (all - rank + size - 1) / size : 0;
     uint32_t tmem = 0;
@@ -1266,7 +1279,10 @@ __global__ void __launch_bounds__(kGradAdThreads)
                 const ChunkTokens now = tokens;
                 tokens = chunk_tokens(g.order, chunk_at(i + 2), last, i + 2 < n, lane);
                 if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
-                if (FAST && now.runs) continue;  // boxes hold it
+                if (FAST && now.runs) {  // boxes hold it
+                    arrive_idle(&full[s], lane);
+                    continue;
+                }
                 auto token = [&](int row) { return __shfl_sync(kFull, row < 32 ? now.near : now.far, row & 31); };
                 if (FAST && left >= kGradTokens) {
 #pragma unroll
@@ -1308,17 +1324,19 @@ __global__ void __launch_bounds__(kGradAdThreads)
             if (n > 0) waiter.wait(&all_done, 0);
         } else if (warp == kGradBoxWarp) {
             ChunkTokens tokens = chunk_tokens(g.order, chunk_at(0), last, FAST && n > 0, lane);
-            for (int i = 0; FAST && i < n; ++i) {
+            for (int i = 0; i < n; ++i) {
                 const int s = i % STAGES;
                 const ChunkTokens now = tokens;
-                tokens = chunk_tokens(g.order, chunk_at(i + 1), last, i + 1 < n, lane);
+                tokens = chunk_tokens(g.order, chunk_at(i + 1), last, FAST && i + 1 < n, lane);
                 if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
                 const int y[2] = {__shfl_sync(kFull, now.near, 0), __shfl_sync(kFull, now.far, 0)};
-                if (now.runs && elect()) {
+                if (!elect()) {
+                } else if (!now.runs) {
+                    mbar_arrive(&full[s]);
+                } else {
                     const uint32_t slot = base + s * T::kSlot;
                     const CUtensorMap *m = is_a ? &maps.x : &maps.dy, *v = is_a ? &maps.d : &maps.v;
                     mbar_expect_tx(&full[s], T::kSlot);
-                    arrive_many(&full[s], kFullArrivals - 1);
 #pragma unroll
                     for (int j = 0; j < kGradCols / 64; ++j)
 #pragma unroll
@@ -1333,9 +1351,8 @@ __global__ void __launch_bounds__(kGradAdThreads)
             }
             if (n > 0) waiter.wait(&all_done, 0);
         } else {
-            const uint32_t word = mma_word(r16, true, true);
+            const uint32_t word = mma_word(min(kGradCols, (cols - c0 + 15) & ~15), true, true);
             const uint64_t in0 = operand(base, T::kTile), v0 = operand(base + T::kIn, T::kTile);
-            const bool two = c0 + 128 < cols;
             for (int i = 0; i < n; ++i) {
                 const int s = i % STAGES;
                 waiter.wait(&full[s], (i / STAGES) & 1);
@@ -1345,12 +1362,8 @@ __global__ void __launch_bounds__(kGradAdThreads)
                     const uint64_t x = in0 + s * (T::kSlot >> 4), v = v0 + s * (T::kSlot >> 4);
 #pragma unroll
                     for (int k = 0; k < kGradTokens / 16; ++k) {
-                        mma(tmem, x + k * 128, v + k * 128, word, i > 0 || k > 0);
-                        mma(tmem, x + k * 128, v + (T::kV >> 4) + k * 128, word, true);
-                        if (two) {
-                            mma(tmem + 128, x + (2 * T::kTile >> 4) + k * 128, v + k * 128, word, i > 0 || k > 0);
-                            mma(tmem + 128, x + (2 * T::kTile >> 4) + k * 128, v + (T::kV >> 4) + k * 128, word, true);
-                        }
+                        mma(tmem, v + k * 128, x + k * 128, word, i > 0 || k > 0);
+                        if (RANK > 64) mma(tmem, v + (T::kV >> 4) + k * 128, x + k * 128, word, true);
                     }
                     mma_commit(&freed[s]);
                     if (i == n - 1) mma_commit(&all_done);
@@ -1361,23 +1374,27 @@ __global__ void __launch_bounds__(kGradAdThreads)
         }
         tc_after();
         __syncthreads();
-        // the block's sums: [rank][column]
-        if (warp < kGradLoadWarps) {
-            const int quarter = warp & 3, half = warp >> 2, col = half * 128 + quarter * 32 + lane;
-            const uint32_t lanes = tmem + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
-            if (c0 + half * 128 < cols)
-                for (int p = 0; p < r16 / 8; ++p) {
+        // The block's sums, [column][rank]: lanes hold ranks, those of the upper half the lo part's (added last).
+        const int quarter = warp & 3, half = warp >> 2;
+        const bool lo = RANK <= 64 && quarter >= 2;
+        const int r = (RANK <= 64 ? quarter & 1 : quarter) * 32 + lane;
+        const uint32_t lanes = tmem + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+        const int end = min(128, cols - c0 - half * 128);
+        for (int turn = 0; turn < (RANK <= 64 ? 2 : 1); ++turn) {
+            if (warp < kGradLoadWarps && lo == (RANK <= 64 && turn == 0) && r - lane < r16)
+                for (int c = 0; c < end; c += 8) {
                     float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                     if (n > 0) {
-                        tmem_load8(lanes + p * 8, x);
+                        tmem_load8(lanes + c, x);
                         tmem_wait();
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((p * 8 + j) * kGradCols + col) * 4),
-                                     "f"(x[j])
-                                     : "memory");
+                    for (int j = 0; j < 8; ++j) {
+                        float *to = sums + (half * 128 + c + j) * (RANK + 1) + r;
+                        *to = RANK <= 64 && turn ? *to + x[j] : x[j];
+                    }
                 }
+            __syncthreads();
         }
         tc_before();
     }
@@ -1390,9 +1407,9 @@ __global__ void __launch_bounds__(kGradAdThreads)
             float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (p * 8 < used)  // sums beyond the used ranks, up to the next 16, are zero
                 for (uint32_t peer = 0; peer < size; ++peer) {
-                    const uint32_t there = peer_addr(base + (p * 8 * kGradCols + col) * 4, peer);
+                    const uint32_t there = peer_addr(base + col * T::kSumRow + p * 32, peer);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] += peer_float(there + j * kGradCols * 4);
+                    for (int j = 0; j < 8; ++j) x[j] += peer_float(there + j * 4);
                 }
             if (is_a) {
 #pragma unroll
