@@ -390,6 +390,11 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, int
         "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
 }
+__device__ __forceinline__ void fetch_map(const CUtensorMap *m)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
 // Boxes are 32 rows high.  Bit i of the result: rows 32 i .. of a tile are not
 // consecutive tokens, so that no box holds them; `y` is the first token of the
 // group of 32 that lane 8 i belongs to.  (A box with rows past the tile's
@@ -508,6 +513,14 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u, v_at = base + T::kVAt;
 
     if (warp == 0) tmem_alloc(&tmem_at, kTmemCols);
+    if (FAST && warp == kBoxWarp && lane == 0) {
+        fetch_map(&maps.in);
+        if (g.out) fetch_map(&maps.base);
+        if (g.boxes_w) {
+            fetch_map(&maps.a);
+            fetch_map(&maps.b);
+        }
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], kFullArrivals);
@@ -1190,8 +1203,8 @@ struct Grad {
     static_assert(STAGES >= 2, "");
     static constexpr uint32_t kTile = kGradTokens * 128;  // 64 tokens by 64 columns
     static constexpr uint32_t kIn = kGradCols / 64 * kTile, kV = kAtoms * kTile, kSlot = kIn + 2 * kV;
-    static constexpr uint32_t kSumRow = (RANK + 1) * 4;  // one column's sums, an odd number of words
-    static constexpr uint32_t kSums = kGradCols * kSumRow;
+    static constexpr uint32_t kSumRow = (kGradCols + 1) * 4;  // one rank's sums, an odd number of words
+    static constexpr uint32_t kSums = RANK * kSumRow;
     static constexpr uint32_t kBytes = (STAGES * kSlot > kSums ? STAGES * kSlot : kSums) + 1024;
 };
 
@@ -1240,6 +1253,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
     Waiter waiter;
     if (used) {
         if (warp == 0) tmem_alloc(&tmem_at, kGradTmemCols);
+        if (FAST && warp == kGradBoxWarp && lane < 2) fetch_map(is_a ? (lane ? &maps.d : &maps.x) : (lane ? &maps.v : &maps.dy));
         if (threadIdx.x == 0) {
             for (int i = 0; i < STAGES; ++i) {
                 mbar_init(&full[i], kFullArrivals);
@@ -1374,7 +1388,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
         }
         tc_after();
         __syncthreads();
-        // The block's sums, [column][rank]: lanes hold ranks, those of the upper half the lo part's (added last).
+        // The block's sums, [rank][column]: lanes hold ranks, those of the upper half the lo part's (added last).
         const int quarter = warp & 3, half = warp >> 2;
         const bool lo = RANK <= 64 && quarter >= 2;
         const int r = (RANK <= 64 ? quarter & 1 : quarter) * 32 + lane;
@@ -1390,7 +1404,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        float *to = sums + (half * 128 + c + j) * (RANK + 1) + r;
+                        float *to = sums + r * (kGradCols + 1) + half * 128 + c + j;
                         *to = RANK <= 64 && turn ? *to + x[j] : x[j];
                     }
                 }
@@ -1407,9 +1421,9 @@ __global__ void __launch_bounds__(kGradAdThreads)
             float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (p * 8 < used)  // sums beyond the used ranks, up to the next 16, are zero
                 for (uint32_t peer = 0; peer < size; ++peer) {
-                    const uint32_t there = peer_addr(base + col * T::kSumRow + p * 32, peer);
+                    const uint32_t there = peer_addr(base + p * 8 * T::kSumRow + col * 4, peer);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] += peer_float(there + j * 4);
+                    for (int j = 0; j < 8; ++j) x[j] += peer_float(there + j * T::kSumRow);
                 }
             if (is_a) {
 #pragma unroll
