@@ -20,9 +20,7 @@ and raises if the library is not built; nothing falls back to the CPU.
 _BINDING_NAMES = {"lct_codebook_build", "lct_codebook_build_zero_atom", "lct_encode", "lct_decode",
                   "lct_decode_blocks", "lct_sgd_step_fused", "lct_sgd_momentum_step_fused",
                   "lct_adamw_step_fused", "lct_encode_static_scratch", "lct_compressed_size",
-                  "lct_debug_wait_timeout", "lct_grad_norm", "lct_grad_clip", "GradArrays",
-                  "lct_adapters", "lct_token_plan", "lct_adapter_plan", "lct_adapter_forward",
-                  "lct_adapter_backward", "CompressedTensor", "LctError", "library"}
+                  "lct_debug_wait_timeout", "CompressedTensor", "LctError", "library"}
 
 
 def __getattr__(name):

@@ -7,7 +7,6 @@ importing this module fails if the library has not been built
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import os
 
@@ -34,9 +33,6 @@ LCT_MODEL_GAUSSIAN, LCT_MODEL_LAPLACE, LCT_MODEL_POWERLAW = 0, 1, 2
 LCT_LEVEL_CLEAN, LCT_LEVEL_MEDIUM, LCT_LEVEL_HIGH = 0, 1, 2
 LCT_HEADER_BYTES = 64
 LCT_STATIC_SCRATCH_BLOCKS = 16384
-LCT_DTYPE_BF16, LCT_DTYPE_F32 = 0, 1
-LCT_GRAD_WORK_BYTES = 4864
-LCT_ADAPTER_TILE, LCT_ADAPTER_MAX_RANK, LCT_ADAPTER_MAX = 128, 128, 16384
 LCT_MAGIC = 0x3154434C
 MODELS = {"gaussian": 0, "laplace": 1, "powerlaw": 2}
 LEVELS = {"CLEAN": 0, "MEDIUM": 1, "HIGH": 2}
@@ -81,17 +77,6 @@ class lct_sizes(ctypes.Structure):
                 ("status", ctypes.c_uint32), ("delta", ctypes.c_int32)]
 
 
-class lct_adapters(ctypes.Structure):
-    _fields_ = [("d_a", ctypes.c_void_p), ("d_b", ctypes.c_void_p), ("d_scale", ctypes.c_void_p),
-                ("d_ranks", ctypes.c_void_p), ("adapters", ctypes.c_uint64), ("rank", ctypes.c_uint64),
-                ("k", ctypes.c_uint64), ("n", ctypes.c_uint64)]
-
-
-class lct_token_plan(ctypes.Structure):
-    _fields_ = [("d_order", ctypes.c_void_p), ("d_starts", ctypes.c_void_p), ("d_tiles", ctypes.c_void_p),
-                ("tokens", ctypes.c_uint64), ("adapters", ctypes.c_uint64)]
-
-
 _P = ctypes.c_void_p
 _lib.lct_codebook_build.argtypes = [ctypes.c_int, ctypes.c_double, ctypes.c_double, ctypes.POINTER(lct_codebook)]
 _lib.lct_codebook_build_zero_atom.argtypes = [ctypes.c_int, ctypes.c_double, ctypes.c_double, ctypes.c_double,
@@ -114,13 +99,7 @@ _lib.lct_adamw_step_fused.argtypes = [ctypes.POINTER(lct_tensor), ctypes.POINTER
     ctypes.POINTER(lct_tensor), _P]
 _lib.lct_debug_wait_timeout.argtypes = [_P, _P, ctypes.c_uint64, _P]
 _lib.lct_encode_static_scratch.argtypes = [_P, ctypes.POINTER(lct_codebook), ctypes.POINTER(lct_tensor), _P]
-_lib.lct_grad_norm.argtypes = [_P, _P, _P, ctypes.c_uint64, _P, _P, _P]
-_lib.lct_grad_clip.argtypes = [_P, _P, _P, _P, ctypes.c_uint64, ctypes.c_float, _P, _P, _P]
-_U64 = ctypes.c_uint64
-_lib.lct_adapter_plan.argtypes = [_P, _U64, _U64, _P, _P, _P, _P]
-_lib.lct_adapter_forward.argtypes = [_P, _P, _P, _U64, _P, _U64, _P, _U64, _P, _P]
-_lib.lct_adapter_backward.argtypes = [_P, _P, _P, _U64, _P, _U64, _P, _P, _U64, _P, _U64, _P, _P, _P, _P]
-for _fn in ("lct_adapter_plan", "lct_adapter_forward", "lct_adapter_backward", "lct_grad_norm", "lct_grad_clip", "lct_codebook_build", "lct_codebook_build_zero_atom", "lct_compressed_size", "lct_encode", "lct_decode",
+for _fn in ("lct_codebook_build", "lct_codebook_build_zero_atom", "lct_compressed_size", "lct_encode", "lct_decode",
             "lct_decode_blocks", "lct_sgd_step_fused",
             "lct_sgd_momentum_step_fused", "lct_adamw_step_fused", "lct_debug_wait_timeout",
             "lct_encode_static_scratch"):
@@ -142,22 +121,6 @@ def _stream(stream) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
-
-
-def _call(fn, what: str, device: int, *args, stream=None) -> None:
-    """fn(*args, stream) with `device` (an index) current, on its current
-    stream by default; a failure raises."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
-    else:
-        stream = _stream(stream)
-    if torch._C._cuda_getDevice() == device:
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream)
-    if rc:
-        raise LctError(rc, what)
 
 
 def _model(m) -> int:
@@ -256,78 +219,6 @@ def lct_adamw_step_fused(W_in: "CompressedTensor", cbW: lct_codebook, M_in: "Com
                                      ctypes.byref(cbM), ctypes.byref(V_in.desc), ctypes.byref(cbV), ptr,
                                      ctypes.byref(p), ctypes.byref(W_out.desc), ctypes.byref(M_out.desc),
                                      ctypes.byref(V_out.desc), _stream(stream)), "lct_adamw_step_fused")
-
-
-_GRAD_DTYPES = {torch.bfloat16: LCT_DTYPE_BF16, torch.float32: LCT_DTYPE_F32}
-
-
-class GradArrays:
-    """The host arrays of lct_grad_norm and lct_grad_clip for a list of CUDA
-    tensors (contiguous, BF16 or float32, all on one device), which it keeps
-    alive.  A list that stays the same from step to step can keep its arrays."""
-
-    def __init__(self, tensors, what: str = "gradients"):
-        self.tensors = ts = tensors if isinstance(tensors, (list, tuple)) else list(tensors)
-        self.count = len(ts)
-        try:
-            self.dtype = array.array("i", [_GRAD_DTYPES[t.dtype] for t in ts])
-        except KeyError as e:
-            raise LctError(LCT_ERR_UNSUPPORTED, "%s: expected BF16 or float32, not %s" % (what, e.args[0])) from None
-        devices = set(map(torch.Tensor.get_device, ts))
-        if -1 in devices or len(devices) > 1:
-            raise ValueError("%s: expected CUDA tensors on one device" % what)
-        if not all(map(torch.Tensor.is_contiguous, ts)):
-            raise ValueError("%s: expected contiguous tensors" % what)
-        self.device = devices.pop() if devices else torch.cuda.current_device()
-        self.ptr = array.array("Q", list(map(torch.Tensor.data_ptr, ts)))
-        self.n = array.array("Q", list(map(torch.Tensor.numel, ts)))
-
-    def args(self):
-        return self.n.buffer_info()[0], self.dtype.buffer_info()[0], self.count
-
-
-def lct_grad_norm(g: GradArrays, norm: torch.Tensor, work: torch.Tensor, stream=None) -> None:
-    _call(_lib.lct_grad_norm, "lct_grad_norm", g.device, g.ptr.buffer_info()[0], *g.args(), norm.data_ptr(),
-          work.data_ptr(), stream=stream)
-
-
-def lct_grad_clip(g: GradArrays, out: GradArrays, max_norm: float, norm: torch.Tensor, work: torch.Tensor,
-                  stream=None) -> None:
-    if out is not g and (out.n != g.n or out.dtype != g.dtype or (g.count and out.device != g.device)):
-        raise ValueError("out must match the gradients' sizes, types and device")
-    _call(_lib.lct_grad_clip, "lct_grad_clip", g.device, g.ptr.buffer_info()[0], out.ptr.buffer_info()[0], *g.args(),
-          max_norm, norm.data_ptr(), work.data_ptr(), stream=stream)
-
-
-def lct_adapter_tile_rows(tokens: int, adapters: int) -> int:
-    """Rows of a plan's tile table (LCT_ADAPTER_TILE_ROWS)."""
-    return -(-tokens // LCT_ADAPTER_TILE) + min(adapters + 1, tokens) if tokens else 1
-
-
-def lct_adapter_work_bytes(tokens: int, rank: int) -> int:
-    """Scratch of lct_adapter_backward (LCT_ADAPTER_WORK_BYTES)."""
-    return 8 * tokens * ((rank + 15) // 16 * 16)
-
-
-def lct_adapter_plan(index: torch.Tensor, adapters: int, order: int, starts: int, tiles: int, stream=None) -> None:
-    """order, starts and tiles are device addresses."""
-    _call(_lib.lct_adapter_plan, "lct_adapter_plan", index.get_device(), index.data_ptr(), index.numel(), adapters,
-          order, starts, tiles, stream=stream)
-
-
-def lct_adapter_forward(bank: lct_adapters, plan: lct_token_plan, device: int, x, y, out, xa=None,
-                        stream=None) -> None:
-    """x, y and out are (device address, row stride) of BF16 matrices; xa is a
-    device address or None."""
-    _call(_lib.lct_adapter_forward, "lct_adapter_forward", device, ctypes.addressof(bank), ctypes.addressof(plan),
-          *x, *y, *out, xa, stream=stream)
-
-
-def lct_adapter_backward(bank: lct_adapters, plan: lct_token_plan, device: int, dy, x=(None, 0), xa=None,
-                         dx=(None, 0), dx_out=(None, 0), da=None, db=None, work=None, stream=None) -> None:
-    """Matrices and addresses as in lct_adapter_forward; None leaves one out."""
-    _call(_lib.lct_adapter_backward, "lct_adapter_backward", device, ctypes.addressof(bank), ctypes.addressof(plan),
-          *dy, *x, xa, *dx, *dx_out, da, db, work, stream=stream)
 
 
 def lct_debug_wait_timeout(header: torch.Tensor, work: torch.Tensor, limit_ns: int, stream=None) -> None:

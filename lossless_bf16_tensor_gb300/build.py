@@ -1,8 +1,10 @@
-"""Build liblct.so (the C-ABI library) for sm_103a with nvcc, in-tree.
+"""Build liblct.so (the C-ABI library) for sm_103a with nvcc, and _calls.so (the
+Python entry points of its gradient and adapter calls) with the C++ compiler,
+in-tree.
 
 Each translation unit is compiled in parallel, then linked into one shared
-library beside this file.  The result is rebuilt only when a source or header
-is newer than it.  No GPU is needed to build.
+library beside this file.  The results are rebuilt only when a source or header
+is newer than them.  No GPU is needed to build.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -18,6 +21,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "liblct.so")
+CALLS_SRC = os.path.join(HERE, "calls", "calls.cpp")
+CALLS = os.path.join(HERE, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-ffp-contract=off",
@@ -76,6 +81,32 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_calls(force: bool = False) -> str:
+    """_calls.so, linked against liblct.so beside it and the installed torch."""
+    deps = [CALLS_SRC, LIB, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(CALLS) and all(os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
+        return CALLS
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_path("include"), os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    tmpdir = tempfile.mkdtemp(prefix="lct_build_", dir=HERE)
+    try:
+        out = os.path.join(tmpdir, "_calls.so")
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", CALLS_SRC, "-o", out,
+               "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+        cmd += ["-I" + p for p in include] + ["-L" + os.path.join(root, "lib"), "-L" + HERE]
+        cmd += ["-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-l:liblct.so", "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("building _calls.so failed:\n%s%s" % (r.stdout, r.stderr))
+        os.replace(out, CALLS)
+    finally:
+        shutil.rmtree(tmpdir, ignore_errors=True)
+    return CALLS
+
+
 if __name__ == "__main__":  # pragma: no cover
     import sys
     print(build_library(force="--force" in sys.argv, verbose=True))
+    print(build_calls(force="--force" in sys.argv))

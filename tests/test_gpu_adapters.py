@@ -114,7 +114,7 @@ def plan_of(index, n):
     starts = [sum(g < a for g in group) for a in range(n + 2)]
     tiles = [[a if a < n else -1, f, min(128, starts[a + 1] - f), 0] for a in range(n + 1)
              for f in range(starts[a], starts[a + 1], 128)]
-    rows = B.lct_adapter_tile_rows(len(index), n)
+    rows = -(-len(index) // 128) + min(n + 1, len(index)) if index else 1
     assert len(tiles) <= rows
     return order, starts, tiles + [[0, 0, 0, 0]] * (rows - len(tiles))
 
