@@ -353,7 +353,7 @@ lct_status lct_adamw_step_fused(const lct_tensor *W_in, const lct_codebook *cbW,
 
 typedef enum { LCT_DTYPE_BF16 = 0, LCT_DTYPE_F32 = 1 } lct_dtype;
 
-#define LCT_GRAD_WORK_BYTES 4864 /* device scratch of the two calls below */
+#define LCT_GRAD_WORK_BYTES 4896 /* device scratch of the two calls below */
 
 /* The global 2-norm of `count` gradients, *d_norm = sqrt(sum of g^2): the
  * dense gradients that the fused steps take, or any other list.  (The pages

@@ -17,6 +17,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 #include <vector>
 
 #include <cooperative_groups.h>
@@ -52,7 +53,7 @@ struct Span {
     unsigned long long hi;        // the tensor's bytes are lo..hi, counted from src
     uint32_t lo;
     bool f32;
-    bool same_phase;              // dst lies like src within a vector
+    bool same_phase, in_place;    // dst lies like src within a vector, or is src
 };
 
 __device__ __forceinline__ Span span_of(const GradEntry &e)
@@ -64,16 +65,17 @@ __device__ __forceinline__ Span span_of(const GradEntry &e)
     s.hi = s.lo + n * (s.f32 ? 4 : 2);
     s.src = e.src - s.lo;
     s.same_phase = ((e.src ^ e.dst) & 15ull) == 0;
+    s.in_place = e.src == e.dst;
     s.dst = e.dst - s.lo;
     return s;
 }
 
-// Vector v of a tensor; a vector at the tensor's first or last bytes is put
-// together from its own values, the rest of it zero.
-__device__ __forceinline__ uint4 load_vec(const Span &s, unsigned long long v)
+// The vector at byte `at` of a tensor; one at the tensor's first or last bytes
+// is put together from its own values, the rest of it zero.
+template <bool WHOLE>
+__device__ __forceinline__ uint4 load_vec(const Span &s, unsigned long long at)
 {
-    const unsigned long long at = v * 16;
-    if (at >= s.lo && at + 16 <= s.hi) return *reinterpret_cast<const uint4 *>(s.src + at);
+    if (WHOLE || (at >= s.lo && at + 16 <= s.hi)) return *reinterpret_cast<const uint4 *>(s.src + at);
     uint32_t w[4] = {0, 0, 0, 0};
     if (s.f32) {
 #pragma unroll
@@ -135,18 +137,21 @@ __device__ __forceinline__ double sum_vectors(const uint4 (&v)[kGradUnroll], uin
     return d;
 }
 
-// Block sum of one double a thread, in a fixed order; every thread gets it.
-template <int THREADS>
+// Block sum of one double a thread, in a fixed order; the first warp gets it.
+// A double addition takes a warp 16 cycles of a pipe that the SM has one of, so
+// that one warp adds, and little: with eight warps adding and taking roots each
+// block took 6 us for what is 0.3 us of work.
 __device__ __forceinline__ double block_sum(double v, double *sh)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x / 32] = v;
+    sh[threadIdx.x] = v;
     __syncthreads();
     double t = 0.0;
+    if (threadIdx.x < 32) {
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) t += sh[i];
-    __syncthreads();
+        for (int i = 0; i < kGradThreads / 32; ++i) t += sh[i * 32 + threadIdx.x];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    }
     return t;
 }
 
@@ -155,42 +160,66 @@ __host__ __device__ __forceinline__ uint32_t range_at(uint32_t units, uint32_t b
     return static_cast<uint32_t>(static_cast<unsigned long long>(units) * block / blocks);
 }
 
-// The sum over units lo..hi of one launch, eight at a time: eight of one
-// tensor with one set of addresses, and eight that several tensors share (a
-// list of small ones) with a set each, so that their loads are still in
-// flight together.
+// The tensor that holds a unit: the last one that begins at it or before.
+template <int CAP>
+__device__ __forceinline__ uint32_t find_entry(const GradTable<CAP> &t, uint32_t unit)
+{
+    uint32_t lo = 0, hi = t.count;
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (t.first[mid] <= unit)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Calls `with(i, span, byte, whole)` for this thread's vector of each of up to
+// eight units u0..u1 of a launch that is there, e being the tensor of u0; byte
+// is the vector's place in the span.  Eight units inside one tensor, whose
+// vectors are all whole, are the case that is to be fast (`whole` is then true
+// at compile time: with the checks of a tensor's edges in it, the scaling pass
+// took 85 instructions a vector, which is what bounded it).  Units that several
+// tensors share (a list of small ones) have an address each, so that their
+// loads are in flight together.
+template <int CAP, typename With>
+__device__ __forceinline__ void each_unit(const GradTable<CAP> &t, uint32_t u0, uint32_t u1, uint32_t e, With with)
+{
+    const Span s = span_of(t.e[e]);
+    const unsigned long long b0 = static_cast<unsigned long long>(u0 - t.first[e]) * (kGradThreads * 16);
+    if (u0 + kGradUnroll <= min(u1, t.first[e + 1]) && b0 >= s.lo && b0 + kGradUnroll * kGradThreads * 16 <= s.hi) {
+#pragma unroll
+        for (int i = 0; i < kGradUnroll; ++i)
+            with(i, s, b0 + threadIdx.x * 16 + i * (kGradThreads * 16), std::true_type{});
+    } else {
+#pragma unroll
+        for (int i = 0; i < kGradUnroll; ++i) {
+            if (u0 + i >= u1) continue;
+            while (u0 + i >= t.first[e + 1]) ++e;
+            const Span edge = span_of(t.e[e]);
+            const unsigned long long at =
+                (static_cast<unsigned long long>(u0 + i - t.first[e]) * kGradThreads + threadIdx.x) * 16;
+            if (at < edge.hi) with(i, edge, at, std::false_type{});
+        }
+    }
+}
+
 template <int CAP>
 __device__ __forceinline__ double sum_units(const GradTable<CAP> &t, uint32_t lo, uint32_t hi)
 {
     double acc = 0.0;
     uint32_t e = t.start[blockIdx.x];
     for (uint32_t u = lo; u < hi; u += kGradUnroll) {
+        while (u >= t.first[e + 1]) ++e;
         uint4 v[kGradUnroll];
         uint32_t f32 = 0;
-        while (u >= t.first[e + 1]) ++e;
-        if (u + kGradUnroll <= min(hi, t.first[e + 1])) {
-            const Span s = span_of(t.e[e]);
-            const unsigned long long v0 = static_cast<unsigned long long>(u - t.first[e]) * kGradThreads + threadIdx.x;
 #pragma unroll
-            for (int i = 0; i < kGradUnroll; ++i) {
-                const unsigned long long at = v0 + i * kGradThreads;
-                v[i] = at * 16 < s.hi ? load_vec(s, at) : make_uint4(0, 0, 0, 0);
-            }
-            f32 = s.f32 ? 0xFFu : 0u;
-        } else {
-#pragma unroll
-            for (int i = 0; i < kGradUnroll; ++i) {
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (u + i < hi) {
-                    while (u + i >= t.first[e + 1]) ++e;
-                    const Span s = span_of(t.e[e]);
-                    const unsigned long long at =
-                        static_cast<unsigned long long>(u + i - t.first[e]) * kGradThreads + threadIdx.x;
-                    if (at * 16 < s.hi) v[i] = load_vec(s, at);
-                    f32 |= static_cast<uint32_t>(s.f32) << i;
-                }
-            }
-        }
+        for (int i = 0; i < kGradUnroll; ++i) v[i] = make_uint4(0, 0, 0, 0);
+        each_unit(t, u, hi, e, [&](int i, const Span &s, unsigned long long at, auto whole) {
+            v[i] = load_vec<whole.value>(s, at);
+            f32 |= static_cast<uint32_t>(s.f32) << i;
+        });
         acc += sum_vectors(v, f32);
     }
     return acc;
@@ -202,47 +231,78 @@ template <int CAP>
 __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
     k_grad_sum(const __grid_constant__ GradTable<CAP> t, double *part, uint32_t add)
 {
-    __shared__ double sh[kGradThreads / 32];
+    __shared__ double sh[kGradThreads];
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
     const uint32_t units = t.first[t.count];
     const double acc = sum_units(t, range_at(units, blockIdx.x, gridDim.x), range_at(units, blockIdx.x + 1, gridDim.x));
-    const double total = block_sum<kGradThreads>(acc, sh);
+    const double total = block_sum(acc, sh);
     if (threadIdx.x == 0) part[blockIdx.x] = (add ? part[blockIdx.x] : 0.0) + total;
 }
 
-__device__ __forceinline__ double total_of(const double *part, uint32_t parts, double *sh)
+// The total of all partial sums, in the first warp.
+__device__ __forceinline__ double total_of(const double *part, uint32_t parts)
 {
-    double a = 0.0;
-    for (uint32_t i = threadIdx.x; i < parts; i += kGradThreads) a += part[i];
-    return block_sum<kGradThreads>(a, sh);
+    double t = 0.0;
+    for (uint32_t i = threadIdx.x; i < parts; i += 32) t += part[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    return t;
 }
 
-__global__ void __launch_bounds__(kGradThreads) k_grad_norm(const double *part, uint32_t parts, float *norm)
+// The root of a total as root * 2^exp with root in [1, 2), in float: the
+// total's exponent made even, its fraction rounded to float (2^-24) and the
+// root of that (2^-24 again).  Zero, infinity and NaN pass with exp = 0.
+struct Root {
+    float root;
+    int exp;
+};
+__device__ __forceinline__ Root root_of(double total)
 {
-    __shared__ double sh[kGradThreads / 32];
-    cudaGridDependencySynchronize();
-    const double total = total_of(part, parts, sh);
-    if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(total));
+    if (!(total > 0.0 && total < __longlong_as_double(0x7FF0000000000000ll)))
+        return {static_cast<float>(total), 0};
+    // sums of squares of float32 values are normal doubles
+    const long long bits = __double_as_longlong(total);
+    const int e = static_cast<int>(bits >> 52) - 1023, odd = e & 1;
+    const double m = __longlong_as_double((bits & 0x000FFFFFFFFFFFFFll) | (static_cast<long long>(1023 + odd) << 52));
+    return {sqrtf(static_cast<float>(m)), (e - odd) / 2};
 }
+__device__ __forceinline__ float norm_of(const Root &r) { return r.exp > 127 ? INFINITY : ldexpf(r.root, r.exp); }
 
-// g' = (g * pre) * mul.  The factor is taken in double from the double norm,
-// so a norm above float's range still clips; a factor too small for a normal
-// float is split in two.
+// g' = (g * pre) * mul.  A norm above float's range still clips, and a factor
+// too small for a normal float is split in two.
 struct Factor {
     float pre, mul;
     bool one;
 };
 
-__device__ __forceinline__ Factor factor_of(double total, float max_norm)
+__device__ __forceinline__ Factor factor_of(const Root &r, float max_norm)
 {
-    double c = static_cast<double>(max_norm) / (sqrt(total) + 1e-6);
-    if (c > 1.0) c = 1.0;  // NaN stays
-    Factor f;
-    f.one = c == 1.0;
-    f.pre = c < 0x1p-100 ? 0x1p-64f : 1.0f;
-    f.mul = static_cast<float>(c < 0x1p-100 ? c * 0x1p64 : c);
+    Factor f = {1.0f, 0.0f, false};
+    if (r.exp > 100) {  // 1e-6 beside 2^100 is nothing; the factor is max_norm / root * 2^-exp
+        const float c = max_norm / r.root;
+        f.pre = 0x1p-64f;
+        f.mul = ldexpf(c, 64 - r.exp);
+    } else {
+        const float c = max_norm / (norm_of(r) + 1e-6f);
+        f.mul = c > 1.0f ? 1.0f : c;  // NaN stays
+        f.one = f.mul == 1.0f;
+    }
     return f;
+}
+
+// The norm, and where `factor` is given that too.
+__global__ void __launch_bounds__(32) k_grad_norm(const double *part, uint32_t parts, float *norm, float max_norm,
+                                                  Factor *factor)
+{
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
+    const double total = total_of(part, parts);
+    if (threadIdx.x == 0) {
+        const Root r = root_of(total);
+        *norm = norm_of(r);
+        if (factor) *factor = factor_of(r, max_norm);
+    }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -254,17 +314,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 __device__ __forceinline__ uint4 scale_vec(const uint4 &v, bool f32, const Factor &f)
 {
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (f.pre == 1.0f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = f32 ? __float_as_uint((__uint_as_float(w[i]) * f.pre) * f.mul)
-                   : pack_bf16((bf_lo(w[i]) * f.pre) * f.mul, (bf_hi(w[i]) * f.pre) * f.mul);
+        for (int i = 0; i < 4; ++i)
+            w[i] = f32 ? __float_as_uint(__uint_as_float(w[i]) * f.mul)
+                       : pack_bf16(bf_lo(w[i]) * f.mul, bf_hi(w[i]) * f.mul);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = f32 ? __float_as_uint((__uint_as_float(w[i]) * f.pre) * f.mul)
+                       : pack_bf16((bf_lo(w[i]) * f.pre) * f.mul, (bf_hi(w[i]) * f.pre) * f.mul);
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void store_vec(const Span &s, unsigned long long v, const uint4 &x)
+template <bool WHOLE>
+__device__ __forceinline__ void store_vec(const Span &s, unsigned long long at, const uint4 &x)
 {
-    const unsigned long long at = v * 16;
-    if (s.same_phase && at >= s.lo && at + 16 <= s.hi) {
+    if (s.same_phase && (WHOLE || (at >= s.lo && at + 16 <= s.hi))) {
         __stcs(reinterpret_cast<uint4 *>(s.dst + at), x);  // not to push out of L2 what is still to be read
         return;
     }
@@ -281,79 +348,45 @@ __device__ __forceinline__ void store_vec(const Span &s, unsigned long long v, c
     }
 }
 
-// A step of the scaling pass: the (at most eight) units before `end`, of one
-// tensor.
-struct Step {
-    Span s;
-    unsigned long long v0;
-    uint32_t count;
-    bool skip;
-    uint4 v[kGradUnroll];
-};
-
-// The step before unit `end` of a range that begins at lo; e falls to the
-// tensor that holds unit end - 1.
+// Scales units u0..u1 (at most eight), which v holds.
 template <int CAP>
-__device__ __forceinline__ void load_step(const GradTable<CAP> &t, uint32_t lo, uint32_t end, uint32_t &e, bool one, Step &p)
+__device__ __forceinline__ void load_units(const GradTable<CAP> &t, uint32_t u0, uint32_t u1, uint32_t e, bool one,
+                                           uint4 (&v)[kGradUnroll])
 {
-    while (t.first[e] >= end) --e;
-    p.s = span_of(t.e[e]);
-    p.skip = one && t.e[e].src == t.e[e].dst;  // nothing changes in place
-    const uint32_t base = t.first[e];
-    p.count = min(end - max(lo, base), static_cast<uint32_t>(kGradUnroll));
-    p.v0 = static_cast<unsigned long long>(end - p.count - base) * kGradThreads + threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < kGradUnroll; ++i) {
-        const unsigned long long at = p.v0 + i * kGradThreads;
-        if (!p.skip && i < p.count && at * 16 < p.s.hi) p.v[i] = load_vec(p.s, at);
-    }
+    each_unit(t, u0, u1, e, [&](int i, const Span &s, unsigned long long at, auto whole) {
+        if (!(one && s.in_place)) v[i] = load_vec<whole.value>(s, at);
+    });
+}
+template <int CAP>
+__device__ __forceinline__ void scale_units(const GradTable<CAP> &t, uint32_t u0, uint32_t u1, uint32_t e,
+                                            const uint4 (&v)[kGradUnroll], const Factor &f)
+{
+    each_unit(t, u0, u1, e, [&](int i, const Span &s, unsigned long long at, auto whole) {
+        if (f.one && s.in_place) return;  // a factor of 1 changes nothing
+        store_vec<whole.value>(s, at, scale_vec(v[i], s.f32, f));
+    });
 }
 
-__device__ __forceinline__ void store_step(const Step &p, const Factor &f)
-{
-    if (p.skip) return;
-#pragma unroll
-    for (int i = 0; i < kGradUnroll; ++i) {
-        const unsigned long long at = p.v0 + i * kGradThreads;
-        if (i < p.count && at * 16 < p.s.hi) store_vec(p.s, at, scale_vec(p.v[i], p.s.f32, f));
-    }
-}
-
-// The scaling pass over units lo..hi, last unit first: what the summing pass
-// read last is what L2 still holds.  The first step is loaded by the caller.
+// The scaling pass, a block for every eight units, last unit first: what the
+// summing pass read last is what L2 still holds.  Many short blocks, as each
+// one first loads all it has and then stores it: blocks that stay and step
+// through their share fall into step with each other, and DRAM then turns
+// between reading and writing (181 instead of 152 us for 162 million values).
 template <int CAP>
-__device__ __forceinline__ void scale_units(const GradTable<CAP> &t, uint32_t lo, uint32_t hi, uint32_t e, Step &p,
-                                            const Factor &f)
+__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
+    k_grad_scale(const __grid_constant__ GradTable<CAP> t, const Factor *factor)
 {
-    for (uint32_t end = hi; end > lo;) {
-        store_step(p, f);
-        end -= p.count;
-        if (end > lo) load_step(t, lo, end, e, f.one, p);
-    }
-}
-
-template <int CAP>
-__device__ __forceinline__ uint32_t last_entry(const GradTable<CAP> &t)
-{
-    return blockIdx.x + 1 < gridDim.x ? t.start[blockIdx.x + 1] : t.count - 1;
-}
-
-template <int CAP>
-__global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm) k_grad_scale(const __grid_constant__ GradTable<CAP> t,
-                                                             const double *part, uint32_t parts, float max_norm,
-                                                             float *norm)
-{
-    __shared__ double sh[kGradThreads / 32];
     const uint32_t units = t.first[t.count];
-    const uint32_t lo = range_at(units, blockIdx.x, gridDim.x), hi = range_at(units, blockIdx.x + 1, gridDim.x);
-    // the summing pass wrote no gradient, so the first step's need not wait for it
-    uint32_t e = last_entry(t);
-    Step p;
-    if (lo < hi) load_step(t, lo, hi, e, false, p);
+    const uint32_t u0 = (gridDim.x - 1 - blockIdx.x) * kGradUnroll, u1 = min(units, u0 + kGradUnroll);
+    const uint32_t e = find_entry(t, u0);
+    uint4 v[kGradUnroll];
+    // the first blocks start while the factor is computed, and load meanwhile: nobody writes gradients there
+    const bool early = blockIdx.x < kGradMaxParts;
+    if (early) load_units(t, u0, u1, e, false, v);
     cudaGridDependencySynchronize();
-    const double total = total_of(part, parts, sh);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(sqrt(total));
-    scale_units(t, lo, hi, e, p, factor_of(total, max_norm));
+    const Factor f = *factor;
+    if (!early) load_units(t, u0, u1, e, f.one, v);
+    scale_units(t, u0, u1, e, v, f);
 }
 
 // Norm and, for CLIP, scaling in one launch of one cluster: a few units, where
@@ -363,25 +396,34 @@ __global__ void __launch_bounds__(kGradThreads) k_grad_cluster(const __grid_cons
                                                                float max_norm, float *norm)
 {
     namespace cg = cooperative_groups;
-    __shared__ double sh[kGradThreads / 32];
+    __shared__ double sh[kGradThreads];
     __shared__ double mine;
+    __shared__ Factor shared;
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t units = t.first[t.count];
     const uint32_t lo = range_at(units, blockIdx.x, gridDim.x), hi = range_at(units, blockIdx.x + 1, gridDim.x);
-    const double acc = block_sum<kGradThreads>(sum_units(t, lo, hi), sh);
+    const double acc = block_sum(sum_units(t, lo, hi), sh);
     if (threadIdx.x == 0) mine = acc;
     cluster.sync();
-    double total = 0.0;
+    if (threadIdx.x < 32) {
+        double total = threadIdx.x < kGradCluster ? *cluster.map_shared_rank(&mine, threadIdx.x) : 0.0;
 #pragma unroll
-    for (int i = 0; i < kGradCluster; ++i) total += *cluster.map_shared_rank(&mine, i);
+        for (int o = kGradCluster / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+        if (threadIdx.x == 0) {
+            const Root r = root_of(total);
+            if (blockIdx.x == 0) *norm = norm_of(r);
+            if (CLIP) shared = factor_of(r, max_norm);
+        }
+    }
     cluster.sync();  // no block leaves while its sum is read
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(sqrt(total));
-    if (CLIP && lo < hi) {
-        uint32_t e = last_entry(t);
-        Step p;
-        const Factor f = factor_of(total, max_norm);
-        load_step(t, lo, hi, e, f.one, p);
-        scale_units(t, lo, hi, e, p, f);
+    if (CLIP) {
+        const Factor f = shared;
+        for (uint32_t u = lo; u < hi; u += kGradUnroll) {
+            const uint32_t e = find_entry(t, u);
+            uint4 v[kGradUnroll];
+            load_units(t, u, hi, e, f.one, v);
+            scale_units(t, u, hi, e, v, f);
+        }
     }
 }
 
@@ -445,11 +487,12 @@ void set_starts(GradTable<CAP> *t, uint32_t grid)
 }
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), uint32_t grid, uint32_t cluster, bool dependent, cudaStream_t s, A... args)
+cudaError_t launch(void (*kernel)(P...), uint32_t grid, uint32_t threads, uint32_t cluster, bool dependent,
+                   cudaStream_t s, A... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(dev::kGradThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     if (cluster > 1) {
@@ -479,35 +522,35 @@ cudaError_t run_tables(const GradArgs &a, bool clip, cudaStream_t s)
         const uint32_t units = t.first[t.count];
         if (!parts && at == a.count && units <= kClusterUnits) {
             set_starts(&t, dev::kGradCluster);
-            return clip ? launch(dev::k_grad_cluster<CAP, true>, dev::kGradCluster, dev::kGradCluster, false, s, t,
+            return clip ? launch(dev::k_grad_cluster<CAP, true>, dev::kGradCluster, dev::kGradThreads, dev::kGradCluster, false, s, t,
                                  a.max_norm, a.norm)
-                        : launch(dev::k_grad_cluster<CAP, false>, dev::kGradCluster, dev::kGradCluster, false, s, t,
+                        : launch(dev::k_grad_cluster<CAP, false>, dev::kGradCluster, dev::kGradThreads, dev::kGradCluster, false, s, t,
                                  a.max_norm, a.norm);
         }
         // a later launch adds to the first one's partial sums, so it has as many blocks as that
         const uint32_t grid = parts ? parts : (at < a.count ? kGradMaxParts : grad_grid(units));
         set_starts(&t, grid);
-        if ((rc = launch(dev::k_grad_sum<CAP>, grid, 1, parts != 0, s, t, a.part, parts ? 1u : 0u)) != cudaSuccess)
+        if ((rc = launch(dev::k_grad_sum<CAP>, grid, dev::kGradThreads, 1, parts != 0, s, t, a.part, parts ? 1u : 0u)) != cudaSuccess)
             return rc;
         parts = grid;
         ++tables;
     } while (at < a.count);
-    if (!clip) return launch(dev::k_grad_norm, 1, 1, true, s, static_cast<const double *>(a.part), parts, a.norm);
+    dev::Factor *factor = clip ? reinterpret_cast<dev::Factor *>(a.part + kGradMaxParts) : nullptr;
+    rc = launch(dev::k_grad_norm, 1, 32, 1, true, s, static_cast<const double *>(a.part), parts, a.norm, a.max_norm,
+                factor);
+    if (!clip || rc != cudaSuccess) return rc;
     at = 0;
-    bool first = true;
-    do {
-        // a single table still lies in t, starts and all
-        if (tables > 1) at = fill_table(a, at, &t);
-        const uint32_t grid = tables > 1 ? kGradMaxParts : parts;
+    for (bool first = true; first || at < a.count; first = false) {
         if (tables > 1)
-            set_starts(&t, grid);
+            at = fill_table(a, at, &t);
         else
-            at = a.count;
-        if ((rc = launch(dev::k_grad_scale<CAP>, grid, 1, first, s, t, static_cast<const double *>(a.part), parts,
-                         a.max_norm, first ? a.norm : nullptr)) != cudaSuccess)
-            return rc;
-        first = false;
-    } while (at < a.count);
+            at = a.count;  // a single table still lies in t
+        const uint32_t units = t.first[t.count];
+        if (!units) continue;
+        rc = launch(dev::k_grad_scale<CAP>, (units + dev::kGradUnroll - 1) / dev::kGradUnroll, dev::kGradThreads, 1, first,
+                    s, t, static_cast<const dev::Factor *>(factor));
+        if (rc != cudaSuccess) return rc;
+    }
     return cudaSuccess;
 }
 

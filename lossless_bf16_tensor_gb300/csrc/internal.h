@@ -151,7 +151,8 @@ cudaError_t launch_wait_probe(lct_header *hdr, unsigned long long *work, uint64_
 
 
 // Gradients of one norm or clipping call (host arrays of device addresses).
-constexpr uint32_t kGradMaxParts = LCT_GRAD_WORK_BYTES / 8;
+constexpr uint32_t kGradMaxParts = 608;  // partial sums, a double each; the clipping factor behind them
+static_assert(8 * kGradMaxParts + 32 <= LCT_GRAD_WORK_BYTES, "");
 struct GradArgs {
     const void *const *src;
     void *const *dst;  // NULL for a norm alone
@@ -160,7 +161,7 @@ struct GradArgs {
     uint64_t count;
     float max_norm;
     float *norm;   // device
-    double *part;  // device, kGradMaxParts
+    double *part;  // device, LCT_GRAD_WORK_BYTES
 };
 cudaError_t launch_grads(const GradArgs &a, bool clip, cudaStream_t s);
 
