@@ -152,30 +152,37 @@ __device__ __forceinline__ uint4 load16(uint32_t src)
     return v;
 }
 
-// `valid` (at most 8) BF16 values at src, at any address, the rest zero.
-__device__ __forceinline__ uint4 gather8(const __nv_bfloat16 *src, int valid)
+// Eight BF16 values at any address, of which `valid` are there (the rest zero),
+// in two steps, so that many are fetched before the first is waited for.  Six of
+// them lie in three aligned words, from the first value on that begins one; the
+// other two are read alone.
+struct Eight {
+    uint32_t a, b, c, h, t;
+    bool odd, part;
+};
+__device__ __forceinline__ Eight fetch8(const __nv_bfloat16 *src, int valid)
 {
     const uint16_t *p = reinterpret_cast<const uint16_t *>(src);
-    uint32_t w[4] = {0, 0, 0, 0};
+    Eight e = {0, 0, 0, 0, 0, (reinterpret_cast<uintptr_t>(p) & 2) != 0, valid < 8};
     if (valid >= 8) {
-        if (reinterpret_cast<uintptr_t>(p) & 2) {
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(p + 1);
-            const uint32_t h = p[0], a = q[0], b = q[1], c = q[2], t = p[7];
-            w[0] = h | a << 16;
-            w[1] = __funnelshift_r(a, b, 16);
-            w[2] = __funnelshift_r(b, c, 16);
-            w[3] = c >> 16 | t << 16;
-        } else {
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = q[i];
-        }
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(p + e.odd);
+        e.a = q[0], e.b = q[1], e.c = q[2];
+        e.h = p[e.odd ? 0 : 6], e.t = p[7];
     } else {
+        uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 7; ++i)
             if (i < valid) w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+        e.a = w[0], e.b = w[1], e.c = w[2], e.h = w[3];
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return e;
+}
+__device__ __forceinline__ uint4 join8(const Eight &e)
+{
+    if (e.part) return make_uint4(e.a, e.b, e.c, e.h);
+    if (!e.odd) return make_uint4(e.a, e.b, e.c, e.h | e.t << 16);
+    return make_uint4(e.h | e.a << 16, __funnelshift_r(e.a, e.b, 16), __funnelshift_r(e.b, e.c, 16),
+                      e.c >> 16 | e.t << 16);
 }
 
 // The same into a 16-byte piece of shared memory: asynchronously where the
@@ -187,7 +194,7 @@ __device__ __forceinline__ void piece(uint32_t dst, const __nv_bfloat16 *src, in
         const uint32_t bytes = valid <= 0 ? 0u : static_cast<uint32_t>(min(valid, 8)) * 2;
         async16(dst, bytes ? static_cast<const void *>(src) : anywhere, bytes);
     } else {
-        store16(dst, gather8(src, valid));
+        store16(dst, join8(fetch8(src, valid)));
     }
 }
 
@@ -462,7 +469,7 @@ __device__ __forceinline__ TileWork tile_work(const AdapterArgs &g, int i, uint3
 
 // N 16-byte pieces, 16 rows apart, from src(0) on: `valid` of a row's eight
 // values are there, and rows from `rows` on are empty.  Pieces that do not
-// travel asynchronously are fetched four at a time before they are stored.
+// travel asynchronously are all fetched before the first is stored.
 // (A copy of no bytes reads nothing, whatever its address.)
 template <bool FAST, int N, typename Src>
 __device__ __forceinline__ void pieces(uint32_t dst, Src src, int valid, int rows, bool aligned)
@@ -472,14 +479,14 @@ __device__ __forceinline__ void pieces(uint32_t dst, Src src, int valid, int row
 #pragma unroll
         for (int q = 0; q < N; ++q) async16(dst + q * 2048, src(q), 16 * q < rows ? bytes : 0u);
     } else {
-        constexpr int M = N < 4 ? N : 4;
+        constexpr int M = N < 8 ? N : 8;
 #pragma unroll
         for (int h = 0; h < N; h += M) {
-            uint4 x[M];
+            Eight x[M];
 #pragma unroll
-            for (int q = 0; q < M; ++q) x[q] = gather8(src(h + q), 16 * (h + q) < rows ? valid : 0);
+            for (int q = 0; q < M; ++q) x[q] = fetch8(src(h + q), 16 * (h + q) < rows ? valid : 0);
 #pragma unroll
-            for (int q = 0; q < M; ++q) store16(dst + (h + q) * 2048, x[q]);
+            for (int q = 0; q < M; ++q) store16(dst + (h + q) * 2048, join8(x[q]));
         }
     }
 }
@@ -511,6 +518,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     const int clusters = gridDim.x / size, first_tile = blockIdx.x / size;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u, v_at = base + T::kVAt;
+    const TileWork first_work = tile_work(g, first_tile, rank, size);  // on its way while the block sets itself up
 
     if (warp == 0) tmem_alloc(&tmem_at, kTmemCols);
     if (FAST && warp == kBoxWarp && lane == 0) {
@@ -537,7 +545,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    if (size > 1) cluster_sync();
+    // barriers are there for the peers; who reaches out to theirs waits for that first
+    if (size > 1) cluster_arrive();
     const uint32_t tmem = tmem_at;
     Waiter waiter;
 
@@ -552,7 +561,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
             s = s + 1 == S ? 0 : s + 1;
         };
         for (int tile = first_tile;; tile += clusters) {
-            const TileWork w = tile_work(g, tile, rank, size);
+            const TileWork w = tile == first_tile ? first_work : tile_work(g, tile, rank, size);
             if (w.count <= 0) break;
             const int start = rank * kChunk + col, stride = static_cast<int>(size) * kChunk;
             const int left = w.count - row0;  // rows from this thread's first one on
@@ -625,7 +634,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         // ------------------------------------------------------------ boxes
         int i = 0, s = 0;
         for (int tile = first_tile;; tile += clusters) {
-            const TileWork w = tile_work(g, tile, rank, size);
+            const TileWork w = tile == first_tile ? first_work : tile_work(g, tile, rank, size);
             if (w.count <= 0) break;
             int mine = 0, y[4];
             const uint32_t loose = FAST ? scattered(g.order, w.first, w.count, lane, mine) : 0xFu;
@@ -677,7 +686,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         const uint64_t in0 = operand(base, 0), v0 = operand(v_at, 0);
         const uint64_t along0 = operand(base + kInBytes, 0), across0 = operand(base + kInBytes, 64 * 128);
         for (int tile = first_tile;; tile += clusters) {
-            const TileWork w = tile_work(g, tile, rank, size);
+            const TileWork w = tile == first_tile ? first_work : tile_work(g, tile, rank, size);
             if (w.count <= 0) break;
             const uint32_t word1 = mma_word(w.r16, false, BACK), word2 = mma_word(kChunk, false, BACK);
             for (int k = 0; k < w.n1; ++k, ++i, s = s + 1 == S ? 0 : s + 1) {
@@ -729,8 +738,9 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         int i = 0, q = 0, tiles = 0;
+        if (size > 1) cluster_wait();
         for (int tile = first_tile;; tile += clusters) {
-            const TileWork w = tile_work(g, tile, rank, size);
+            const TileWork w = tile == first_tile ? first_work : tile_work(g, tile, rank, size);
             if (w.count <= 0) break;
             // ranks that the adapter does not use
             if (!BACK && g.keep)
@@ -739,6 +749,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                     const int r = e / (g.rank - w.used), c = w.used + e - r * (g.rank - w.used);
                     g.keep[static_cast<int64_t>(g.order[w.first + r]) * g.rank + c] = 0.0f;
                 }
+            int my_token = 0;  // of row lane
+            if (!FAST && quarter * 32 + lane < w.count) my_token = g.order[w.first + quarter * 32 + lane];
             int t[8];  // the rows that this thread writes: 8 threads a row
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -826,11 +838,23 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                         const uint32_t from = v_at + (p * 2 * kTileTokens + gr * 32 + lane) * 16;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) sum[u][j] = 0.0f;
-                        for (uint32_t peer = 0; peer < size; ++peer) {
-                            const uint32_t there = peer_addr(from, peer);
-                            const float4 x = peer_float4(there), y = peer_float4(there + kTileTokens * 16);
-                            sum[u][0] += x.x, sum[u][1] += x.y, sum[u][2] += x.z, sum[u][3] += x.w;
-                            sum[u][4] += y.x, sum[u][5] += y.y, sum[u][6] += y.z, sum[u][7] += y.w;
+                        // four blocks' at a time, so that their reads are in flight together
+                        for (uint32_t peer = 0; peer < size; peer += 4) {
+                            float4 x[4], y[4];
+#pragma unroll
+                            for (uint32_t j = 0; j < 4; ++j) {
+                                x[j] = y[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                if (peer + j < size) {
+                                    const uint32_t there = peer_addr(from, peer + j);
+                                    x[j] = peer_float4(there);
+                                    y[j] = peer_float4(there + kTileTokens * 16);
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                sum[u][0] += x[j].x, sum[u][1] += x[j].y, sum[u][2] += x[j].z, sum[u][3] += x[j].w;
+                                sum[u][4] += y[j].x, sum[u][5] += y[j].y, sum[u][6] += y[j].z, sum[u][7] += y[j].w;
+                            }
                         }
                     }
                     // everyone has read the partial sums that V's place held
@@ -912,14 +936,23 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                     }
                 } else {
                     // rows at any address: a warp writes one row's 64 values at a time, two a lane
-                    for (int j = 0; j < 32 && quarter * 32 + j < w.count; ++j) {
-                        const int row = quarter * 32 + j, at = rank * kChunk + step + lane;
-                        uint16_t *to = reinterpret_cast<uint16_t *>(g.out) +
-                                       static_cast<int64_t>(g.order[w.first + row]) * g.ld_out;
-                        const uint32_t near = slot + swz(row, lane >> 3) + (lane & 7) * 2;
-                        const uint32_t far = slot + swz(row, 4 + (lane >> 3)) + (lane & 7) * 2;
-                        if (at < g.nout) to[at] = load2(near);
-                        if (at + 32 < g.nout) to[at + 32] = load2(far);
+                    const int at = rank * kChunk + step + lane;
+                    for (int j = 0; j < 32 && quarter * 32 + j < w.count; j += 8) {
+                        uint16_t near[8], far[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int row = quarter * 32 + j + e;
+                            near[e] = load2(slot + swz(row, lane >> 3) + (lane & 7) * 2);
+                            far[e] = load2(slot + swz(row, 4 + (lane >> 3)) + (lane & 7) * 2);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int64_t token = __shfl_sync(kFull, my_token, j + e);
+                            uint16_t *to = reinterpret_cast<uint16_t *>(g.out) + token * g.ld_out + at;
+                            const bool there = quarter * 32 + j + e < w.count;
+                            if (there && at < g.nout) to[0] = near[e];
+                            if (there && at + 32 < g.nout) to[32] = far[e];
+                        }
                     }
                 }
                 fence_proxy_async();  // the slot's next chunk may be a box
@@ -929,6 +962,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
         }
     }
     if (waiter.dead) fail(g);
+    __syncwarp();
+    if (size > 1 && warp >= kOutWarps) cluster_wait();
     tc_before();
     __syncthreads();
     if (size > 1) cluster_sync();  // no block leaves while a peer may still reach its memory
@@ -1312,15 +1347,15 @@ __global__ void __launch_bounds__(kGradAdThreads)
                 } else {
 #pragma unroll 1
                     for (int h = 0; h < 16; h += 4) {
-                        uint4 x[4];
+                        Eight x[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const int64_t t = token(w4 + 4 * (h + q));
-                            x[q] = gather8(from + t * ld, w4 + 4 * (h + q) < left ? valid : 0);
+                            x[q] = fetch8(from + t * ld, w4 + 4 * (h + q) < left ? valid : 0);
                         }
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            store16(slot + (q & 1 ? odd : even) + (h + q) / 2 * 1024, x[q]);
+                            store16(slot + (q & 1 ? odd : even) + (h + q) / 2 * 1024, join8(x[q]));
                     }
                     for (int c = v_c * 8; c < r16; c += 64) {
                         const __nv_bfloat16 *p = v + (static_cast<int64_t>(t0 + v_row) * 2 + v_lo) * g.rank16 + c;
@@ -1453,32 +1488,54 @@ __global__ void __launch_bounds__(kGradAdThreads)
 // -------------------------------------------------------------- the plan
 
 // The tokens in stable order of their adapter.  Each warp counts a contiguous
-// share of the tokens, one column of shared counters an adapter; a scan over
+// share of the tokens, one row of shared counters an adapter; a scan over
 // adapters and warps turns the counts into places, and each warp deals its
-// tokens out.  Lanes with the same adapter find each other by a match.
+// tokens out.  Lanes with the same adapter find each other by a match.  One
+// block: a plan is made once for a batch, and what it costs is latency, so
+// tokens are fetched eight rounds at a time, and a short batch has few warps.
+constexpr int kPlanRounds = 8;
+// The lanes with this lane's value; runs of one adapter need no match.
+__device__ __forceinline__ unsigned same_adapter(int a)
+{
+    const int first = __shfl_sync(kFull, a, 0);
+    return __all_sync(kFull, a == first) ? kFull : __match_any_sync(kFull, a);
+}
 __global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ PlanArgs g)
 {
-    extern __shared__ int counts[];  // [adapters + 1][warps]
+    extern __shared__ int counts[];  // [adapters + 1][warps, and one more to spread the banks]
     __shared__ int part[32], tile_part[32];
     __shared__ int bad;
-    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x & 31, pitch = warps + 1;
     const int groups = g.adapters + 1;
-    if (threadIdx.x == 0) bad = 0;
-    for (int i = threadIdx.x; i < groups * warps; i += blockDim.x) counts[i] = 0;
-    __syncthreads();
     const int share = ((g.tokens + warps - 1) / warps + 31) & ~31;
     const int lo = min(g.tokens, warp * share), hi = min(g.tokens, lo + share);
-    auto group_of = [&](int t) {
-        const int a = g.index[t];
-        if (a >= g.adapters || a < -1) bad = 1;
-        return a < 0 || a >= g.adapters ? g.adapters : a;
+    // a round's adapters, -1 past the end; those outside the bank are as none
+    auto fetch = [&](int t0, int (&a)[kPlanRounds]) {
+#pragma unroll
+        for (int i = 0; i < kPlanRounds; ++i) {
+            const int t = t0 + 32 * i + lane;
+            a[i] = t < hi ? g.index[t] : -2;
+        }
+#pragma unroll
+        for (int i = 0; i < kPlanRounds; ++i) {
+            const bool there = t0 + 32 * i + lane < hi;
+            if (there && (a[i] >= g.adapters || a[i] < -1)) bad = 1;
+            a[i] = !there ? -1 : a[i] < 0 || a[i] >= g.adapters ? g.adapters : a[i];
+        }
     };
-    for (int t0 = lo; t0 < hi; t0 += 32) {
-        const bool there = t0 + lane < hi;
-        const int a = there ? group_of(t0 + lane) : -1;
-        const unsigned same = __match_any_sync(kFull, a);
-        if (there && lane == __ffs(same) - 1) counts[a * warps + warp] += __popc(same);
-        __syncwarp();
+    int mine[kPlanRounds];
+    if (threadIdx.x == 0) bad = 0;
+    for (int i = threadIdx.x; i < groups * pitch; i += blockDim.x) counts[i] = 0;
+    __syncthreads();
+    for (int t0 = lo; t0 < hi; t0 += 32 * kPlanRounds) {
+        fetch(t0, mine);
+#pragma unroll
+        for (int i = 0; i < kPlanRounds; ++i) {
+            if (t0 + 32 * i >= hi) break;
+            const unsigned same = same_adapter(mine[i]);
+            if (mine[i] >= 0 && lane == __ffs(same) - 1) counts[mine[i] * pitch + warp] += __popc(same);
+            __syncwarp();
+        }
     }
     __syncthreads();
     // exclusive places over (adapter, warp), and tiles over adapters: each thread takes a run of adapters
@@ -1487,7 +1544,7 @@ __global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ P
     int sum = 0, tiles = 0;
     for (int a = a0; a < a1; ++a) {
         int c = 0;
-        for (int w = 0; w < warps; ++w) c += counts[a * warps + w];
+        for (int w = 0; w < warps; ++w) c += counts[a * pitch + w];
         sum += c;
         tiles += (c + kTileTokens - 1) / kTileTokens;
     }
@@ -1511,8 +1568,8 @@ __global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ P
         const int first = before;
         g.starts[a] = first;
         for (int w = 0; w < warps; ++w) {
-            const int c = counts[a * warps + w];
-            counts[a * warps + w] = before;
+            const int c = counts[a * pitch + w];
+            counts[a * pitch + w] = before;
             before += c;
         }
         for (int t = first; t < before; t += kTileTokens) {
@@ -1523,18 +1580,21 @@ __global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ P
     if (threadIdx.x == 0) g.starts[groups] = g.tokens;
     for (int i = all_tiles + threadIdx.x; i < g.rows; i += blockDim.x) table[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    for (int t0 = lo; t0 < hi; t0 += 32) {
-        const bool there = t0 + lane < hi;
-        const int a = there ? group_of(t0 + lane) : -1;
-        const unsigned same = __match_any_sync(kFull, a);
-        int at = 0;
-        if (there) at = counts[a * warps + warp];
-        __syncwarp();
-        if (there) {
-            g.order[at + __popc(same & ((1u << lane) - 1))] = t0 + lane;
-            if (lane == __ffs(same) - 1) counts[a * warps + warp] = at + __popc(same);
+    for (int t0 = lo; t0 < hi; t0 += 32 * kPlanRounds) {
+        if (hi - lo > 32 * kPlanRounds) fetch(t0, mine);  // a shorter share is still there
+#pragma unroll
+        for (int i = 0; i < kPlanRounds; ++i) {
+            if (t0 + 32 * i >= hi) break;
+            const unsigned same = same_adapter(mine[i]);
+            int at = 0;
+            if (mine[i] >= 0) at = counts[mine[i] * pitch + warp];
+            __syncwarp();
+            if (mine[i] >= 0) {
+                g.order[at + __popc(same & ((1u << lane) - 1))] = t0 + 32 * i + lane;
+                if (lane == __ffs(same) - 1) counts[mine[i] * pitch + warp] = at + __popc(same);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     }
 }
 
@@ -1733,10 +1793,12 @@ cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s)
 
 cudaError_t launch_adapter_plan(const PlanArgs &a, cudaStream_t s)
 {
-    // as many warps as the counters leave room for
-    uint32_t warps = 32;
-    while (warps > 1 && (a.adapters + 1ull) * warps * 4 > 200 * 1024) warps /= 2;
-    return launch(dev::k_adapter_plan, dim3(1), warps * 32, (a.adapters + 1) * warps * 4, 1, s, a);
+    // a round of a warp for 32 tokens, as far as the counters leave room
+    uint32_t warps = 1;
+    while (warps < 32 && warps * 32 * dev::kPlanRounds / 4 < static_cast<uint32_t>(a.tokens) &&
+           (a.adapters + 1ull) * (2 * warps + 1) * 4 <= 200 * 1024)
+        warps *= 2;
+    return launch(dev::k_adapter_plan, dim3(1), warps * 32, (a.adapters + 1) * (warps + 1) * 4, 1, s, a);
 }
 
 namespace {
