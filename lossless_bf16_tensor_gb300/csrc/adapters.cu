@@ -187,12 +187,11 @@ __device__ __forceinline__ uint4 join8(const Eight &e)
 
 // The same into a 16-byte piece of shared memory: asynchronously where the
 // address allows it.
-__device__ __forceinline__ void piece(uint32_t dst, const __nv_bfloat16 *src, int valid, bool aligned,
-                                      const void *anywhere)
+template <bool FAST>
+__device__ __forceinline__ void piece(uint32_t dst, const __nv_bfloat16 *src, int valid, bool aligned)
 {
-    if (aligned) {
-        const uint32_t bytes = valid <= 0 ? 0u : static_cast<uint32_t>(min(valid, 8)) * 2;
-        async16(dst, bytes ? static_cast<const void *>(src) : anywhere, bytes);
+    if (FAST || aligned) {
+        async16(dst, src, valid <= 0 ? 0u : static_cast<uint32_t>(min(valid, 8)) * 2);
     } else {
         store16(dst, join8(fetch8(src, valid)));
     }
@@ -1006,7 +1005,7 @@ constexpr int kFewRows = 16, kFewCols = 128;
 
 template <int RT>
 struct Few {
-    static constexpr int kStages = RT == 16 ? 8 : RT == 32 ? 6 : 4;
+    static constexpr int kStages = RT <= 32 ? 8 : 4;
     static constexpr int kWBytes = RT * kFewCols * 2, kSlot = kWBytes + kFewRows * kFewCols * 2;
     static constexpr int kSplitR = RT / 16, kSplitK = 8 / kSplitR;  // warps over R, and over a chunk's columns
     static constexpr int kPart = kStages * kSlot;                    // [kSplitK][16][RT] float32
@@ -1040,7 +1039,9 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int RT>
+// FAST: every row begins at a 16-byte boundary.  (Its code is a third of the
+// other's, and a launch of a few microseconds is fetching most of it.)
+template <int RT, bool FAST>
 __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constant__ AdapterArgs g)
 {
     using F = Few<RT>;
@@ -1054,8 +1055,8 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
     for (int i = threadIdx.x; i < count; i += kAdThreads) tok[i] = g.order[tile.y + i];
     const int a = tile.x;
     const int used = a < 0 || a >= g.adapters ? 0 : used_rank(g, a);
-    __syncthreads();
     if (used == 0) {
+        __syncthreads();
         copy_rows(g, tok, count);
         return;
     }
@@ -1063,7 +1064,6 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const __nv_bfloat16 *A = g.a + static_cast<int64_t>(a) * g.rank * g.k;
     const __nv_bfloat16 *B = g.b + static_cast<int64_t>(a) * g.rank * g.n;
-    const float scale = g.scale[a];
     const int all1 = (g.nin + kFewCols - 1) / kFewCols, all2 = (g.nout + kFewCols - 1) / kFewCols;
     const int n1 = all1 > (int)rank ? (all1 - rank + size - 1) / size : 0;
     const int n2 = all2 > (int)rank ? (all2 - rank + size - 1) / size : 0;
@@ -1073,43 +1073,70 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
     // a warp's part of the narrow product: 16 ranks from r0, and the 16-column steps k0, k0 + kSplitK ..
     const int r0 = warp % F::kSplitR * 16, k0 = warp / F::kSplitR;
 
+    // chunk i's weights into its slot
+    auto load_w = [&](int i) {
+        const uint32_t slot = base + (i % S) * F::kSlot;
+        if (i < n1) {
+            const int at = (rank + i * size) * kFewCols + c16 * 8;
+#pragma unroll
+            for (int q = 0; q < RT / 16; ++q) {
+                const int r = row + 16 * q;
+                piece<FAST>(slot + few_at<16>(r, c16), A + static_cast<int64_t>(r) * g.k + at, r < used ? g.k - at : 0,
+                            g.al_a);
+            }
+        } else if (i < n) {
+            const int c0 = (rank + (i - n1) * size) * kFewCols;
+#pragma unroll
+            for (int q = 0; q < RT / 16; ++q) {
+                constexpr int P = RT / 8;
+                const int id = threadIdx.x + q * kAdThreads, r = id / P, c = id % P;
+                piece<FAST>(slot + few_at<P>(r, c), B + static_cast<int64_t>(c0 + r) * g.rank + c * 8,
+                            c0 + r < g.n ? used - c * 8 : 0, g.al_b);
+            }
+        }
+    };
+    // Where every chunk has a slot of its own, as at the usual sizes, all of them are asked for at once, the weights
+    // before the tokens are known, and nothing but the cluster's meeting is waited for on the way.
+    const bool at_once = n <= S && count <= kFewRows;
+    const int ahead = at_once ? S : S - 1;
+    const float scale = g.scale[a];
+
     for (int first = 0; first < count; first += kFewRows) {
+#pragma unroll 1
+        for (int i = 0; i < ahead; ++i) load_w(i);
+        if (first == 0) __syncthreads();  // the tokens are there
         const int rows = min(kFewRows, count - first);
         const int64_t t = row < rows ? tok[first + row] : 0;
-        auto load = [&](int i) {
-            const uint32_t slot = base + (i % S) * F::kSlot, tile_at = slot + F::kWBytes;
-            if (i < n1) {
-                const int c0 = (rank + i * size) * kFewCols, at = c0 + c16 * 8;
-                if (row < rows)
-                    piece(tile_at + few_at<16>(row, c16), g.in + t * g.ld_in + at, g.nin - at, g.al_in, g.in);
-#pragma unroll
-                for (int q = 0; q < RT / 16; ++q) {
-                    const int r = row + 16 * q;
-                    piece(slot + few_at<16>(r, c16), A + static_cast<int64_t>(r) * g.k + at, r < used ? g.k - at : 0,
-                          g.al_a, A);
-                }
-            } else if (i < n) {
-                const int c0 = (rank + (i - n1) * size) * kFewCols, at = c0 + c16 * 8;
-                if (row < rows)
-                    piece(tile_at + few_at<16>(row, c16), g.base + t * g.ld_base + at, g.nout - at, g.al_base, g.base);
-#pragma unroll
-                for (int q = 0; q < RT / 16; ++q) {
-                    constexpr int P = RT / 8;
-                    const int id = threadIdx.x + q * kAdThreads, r = id / P, c = id % P;
-                    piece(slot + few_at<P>(r, c), B + static_cast<int64_t>(c0 + r) * g.rank + c * 8,
-                          c0 + r < g.n ? used - c * 8 : 0, g.al_b, B);
-                }
+        auto load_rows = [&](int i) {
+            if (row < rows && i < n) {
+                const bool two = i >= n1;
+                const int at = (rank + (two ? i - n1 : i) * size) * kFewCols + c16 * 8;
+                piece<FAST>(base + (i % S) * F::kSlot + F::kWBytes + few_at<16>(row, c16),
+                            (two ? g.base + t * g.ld_base : g.in + t * g.ld_in) + at, (two ? g.nout : g.nin) - at,
+                            two ? g.al_base : g.al_in);
             }
             async_commit();
         };
-        for (int i = 0; i < S - 1; ++i) load(i);
+#pragma unroll 1
+        for (int i = 0; i < ahead; ++i) load_rows(i);
+        // chunk i is there; every warp has read its slot's last one, so the next one can come
+        auto chunk = [&](int i) {
+            if (at_once && i > 0) return;
+            if (at_once)
+                async_wait<0>();
+            else
+                async_wait<S - 2>();
+            __syncthreads();
+            if (at_once) return;
+            load_w(i + S - 1);
+            load_rows(i + S - 1);
+        };
 
         // the narrow product
         float acc[2][4] = {};
+#pragma unroll 1
         for (int i = 0; i < n1; ++i) {
-            async_wait<S - 2>();
-            __syncthreads();
-            load(i + S - 1);  // into the slot of chunk i - 1, which every warp has done with
+            chunk(i);
             const uint32_t slot = base + (i % S) * F::kSlot, tile_at = slot + F::kWBytes;
 #pragma unroll
             for (int k = k0; k < 8; k += F::kSplitK) {
@@ -1168,10 +1195,9 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
         __syncthreads();
 
         // the product back to the full width
+#pragma unroll 1
         for (int i = n1; i < n; ++i) {
-            async_wait<S - 2>();
-            __syncthreads();
-            load(i + S - 1);
+            chunk(i);
             const uint32_t slot = base + (i % S) * F::kSlot;
             float d[2][4] = {};
 #pragma unroll
@@ -1196,7 +1222,7 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
                 const uint32_t o = pack2(__uint_as_float(y << 16) + d[h][(j & 1) * 2],
                                          __uint_as_float(y & 0xFFFF0000u) + d[h][(j & 1) * 2 + 1]);
                 uint16_t *at = reinterpret_cast<uint16_t *>(g.out) + tok[first + r] * g.ld_out + c0 + col;
-                if (g.al_out && c0 + col + 1 < g.nout) {
+                if ((FAST || g.al_out) && c0 + col + 1 < g.nout) {
                     *reinterpret_cast<uint32_t *>(at) = o;
                 } else {
                     at[0] = static_cast<uint16_t>(o);
@@ -1720,7 +1746,9 @@ cudaError_t launch_tokens(const AdapterArgs &a, cudaStream_t s)
 template <int RT>
 cudaError_t launch_few(const AdapterArgs &a, uint32_t c, cudaStream_t s)
 {
-    return launch(dev::k_adapter_few<RT>, dim3(c * a.rows), dev::kAdThreads, dev::Few<RT>::kBytes, c, s, a);
+    const bool fast = a.al_in && a.al_a && a.al_b && a.al_base && a.al_out;
+    return launch(fast ? dev::k_adapter_few<RT, true> : dev::k_adapter_few<RT, false>, dim3(c * a.rows),
+                  dev::kAdThreads, dev::Few<RT>::kBytes, c, s, a);
 }
 
 }  // namespace
