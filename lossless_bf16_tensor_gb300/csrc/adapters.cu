@@ -1359,39 +1359,30 @@ __global__ void __launch_bounds__(kGradAdThreads)
                     continue;
                 }
                 auto token = [&](int row) { return __shfl_sync(kFull, row < 32 ? now.near : now.far, row & 31); };
-                if (FAST && left >= kGradTokens) {
+                if (FAST) {
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
                         async16(slot + (q & 1 ? odd : even) + q / 2 * 1024,
-                                from + static_cast<int64_t>(token(w4 + 4 * q)) * ld, bytes);
-                    for (int c = v_c * 8; c < r16; c += 64) {
-                        const __nv_bfloat16 *p = v + (static_cast<int64_t>(t0 + v_row) * 2 + v_lo) * g.rank16 + c;
-                        const uint32_t to = slot + v_to + (c >> 6) * T::kTile;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) async16(to + q * 1024, p + q * 16 * g.rank16, 16);
-                    }
+                                from + static_cast<int64_t>(token(w4 + 4 * q)) * ld, w4 + 4 * q < left ? bytes : 0u);
                 } else {
 #pragma unroll 1
-                    for (int h = 0; h < 16; h += 4) {
-                        Eight x[4];
+                    for (int h = 0; h < 16; h += 8) {
+                        Eight x[8];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int64_t t = token(w4 + 4 * (h + q));
-                            x[q] = fetch8(from + t * ld, w4 + 4 * (h + q) < left ? valid : 0);
-                        }
+                        for (int q = 0; q < 8; ++q)
+                            x[q] = fetch8(from + static_cast<int64_t>(token(w4 + 4 * (h + q))) * ld,
+                                          w4 + 4 * (h + q) < left ? valid : 0);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
+                        for (int q = 0; q < 8; ++q)
                             store16(slot + (q & 1 ? odd : even) + (h + q) / 2 * 1024, join8(x[q]));
                     }
-                    for (int c = v_c * 8; c < r16; c += 64) {
-                        const __nv_bfloat16 *p = v + (static_cast<int64_t>(t0 + v_row) * 2 + v_lo) * g.rank16 + c;
-                        const uint32_t to = slot + v_to + (c >> 6) * T::kTile;
+                }
+                for (int c = v_c * 8; c < r16; c += 64) {
+                    const __nv_bfloat16 *p = v + (static_cast<int64_t>(t0 + v_row) * 2 + v_lo) * g.rank16 + c;
+                    const uint32_t to = slot + v_to + (c >> 6) * T::kTile;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const bool there = v_row + 8 * q < left;
-                            async16(to + q * 1024, there ? p + q * 16 * g.rank16 : v, there ? 16 : 0);
-                        }
-                    }
+                    for (int q = 0; q < 8; ++q)
+                        async16(to + q * 1024, p + q * 16 * g.rank16, v_row + 8 * q < left ? 16 : 0);
                 }
                 arrive_full(&full[s], lane);
             }
