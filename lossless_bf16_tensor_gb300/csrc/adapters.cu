@@ -766,8 +766,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 if (w.n1 > 0) waiter.wait(&narrow, tiles & 1);
                 tc_after();
                 __syncwarp();
-                float sum[T::kUnits][8];
-                int unit[T::kUnits];
+                float sum[T::kUnits][8] = {};
                 auto emit = [&](float (&x)[8], int p, int gr) {
                     const int row = gr * 32 + lane;
                     const bool writes = row < w.count;
@@ -827,17 +826,15 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                     waiter.wait_cluster(&meet[0], tiles & 1);
                 }
                 if (size > 1) {
-#pragma unroll
+#pragma unroll 1
                     for (int u = 0; u < T::kUnits; ++u) {
                         const int e = static_cast<int>(rank) + static_cast<int>(size) * (warp + kOutWarps * u);
-                        unit[u] = -1;
-                        if (e >= npieces * groups) continue;
+                        if (e >= npieces * groups) break;
                         const int p = e / groups, gr = e - p * groups;
-                        unit[u] = p * 4 + gr;
                         const uint32_t from = v_at + (p * 2 * kTileTokens + gr * 32 + lane) * 16;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) sum[u][j] = 0.0f;
+                        float one[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                         // four blocks' at a time, so that their reads are in flight together
+#pragma unroll 1
                         for (uint32_t peer = 0; peer < size; peer += 4) {
                             float4 x[4], y[4];
 #pragma unroll
@@ -851,23 +848,40 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                             }
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                sum[u][0] += x[j].x, sum[u][1] += x[j].y, sum[u][2] += x[j].z, sum[u][3] += x[j].w;
-                                sum[u][4] += y[j].x, sum[u][5] += y[j].y, sum[u][6] += y[j].z, sum[u][7] += y[j].w;
+                                one[0] += x[j].x, one[1] += x[j].y, one[2] += x[j].z, one[3] += x[j].w;
+                                one[4] += y[j].x, one[5] += y[j].y, one[6] += y[j].z, one[7] += y[j].w;
                             }
                         }
+#pragma unroll
+                        for (int k = 0; k < T::kUnits; ++k)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (k == u) sum[k][j] = one[j];
                     }
                     // everyone has read the partial sums that V's place held
                     arrive_cluster(&meet[1], size, lane);
                     waiter.wait_cluster(&meet[1], tiles & 1);
+                }
+                // loops of one copy each: this runs once a tile, and fetching its code is most of what it takes
+#pragma unroll 1
+                for (int u = 0; u < (size > 1 ? T::kUnits : npieces / 2); ++u) {
+                    float one[8];
+                    int p = half + 2 * u, gr = quarter;
+                    if (size > 1) {
+                        const int e = static_cast<int>(rank) + static_cast<int>(size) * (warp + kOutWarps * u);
+                        if (e >= npieces * groups) break;
+                        p = e / groups, gr = e - p * groups;
 #pragma unroll
-                    for (int u = 0; u < T::kUnits; ++u)
-                        if (unit[u] >= 0) emit(sum[u], unit[u] >> 2, unit[u] & 3);
-                } else if (quarter < groups) {
-                    for (int p = half; p < npieces; p += 2) {
-                        tmem_load8(lanes + p * 8, sum[0]);
+                        for (int k = 0; k < T::kUnits; ++k)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (k == u) one[j] = sum[k][j];
+                    } else {
+                        if (quarter >= groups) break;
+                        tmem_load8(lanes + p * 8, one);
                         tmem_wait();
-                        emit(sum[0], p, quarter);
                     }
+                    emit(one, p, gr);
                 }
                 fence_proxy_all();
                 tc_before();
