@@ -1523,8 +1523,9 @@ __global__ void __launch_bounds__(kGradAdThreads)
 // adapters and warps turns the counts into places, and each warp deals its
 // tokens out.  Lanes with the same adapter find each other by a match.  One
 // block: a plan is made once for a batch, and what it costs is latency, so
-// tokens are fetched eight rounds at a time, and a short batch has few warps.
-constexpr int kPlanRounds = 8;
+// tokens are fetched sixteen rounds at a time (up to 16,384 tokens once, for both
+// passes), and a short batch has few warps.
+constexpr int kPlanRounds = 16;
 // The lanes with this lane's value; runs of one adapter need no match.
 __device__ __forceinline__ unsigned same_adapter(int a)
 {
@@ -1826,9 +1827,9 @@ cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s)
 
 cudaError_t launch_adapter_plan(const PlanArgs &a, cudaStream_t s)
 {
-    // a round of a warp for 32 tokens, as far as the counters leave room
+    // two rounds of 32 tokens a warp, as far as the counters leave room for warps
     uint32_t warps = 1;
-    while (warps < 32 && warps * 32 * dev::kPlanRounds / 4 < static_cast<uint32_t>(a.tokens) &&
+    while (warps < 32 && warps * 64 < static_cast<uint32_t>(a.tokens) &&
            (a.adapters + 1ull) * (2 * warps + 1) * 4 <= 200 * 1024)
         warps *= 2;
     return launch(dev::k_adapter_plan, dim3(1), warps * 32, (a.adapters + 1) * (warps + 1) * 4, 1, s, a);
