@@ -611,6 +611,30 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                         arrive_idle(&full[s], lane);
                         continue;
                     }
+                    if (!FAST && !al && w.count <= 64 && w.used && w.r16 <= 64 && !(two == BACK ? g.al_a : g.al_b)) {
+                        // rows and weights at any address: one round trip to memory for both
+                        Eight x[4], y[4];
+                        const bool a_rows = two == BACK;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            x[q] = fetch8(p[q] + step, 16 * q < left ? valid : 0);
+                            const int r = row0 + 16 * q;
+                            if (a_rows)
+                                y[q] = fetch8(A + step + static_cast<int64_t>(16 * q) * g.k,
+                                              r < w.used ? g.k - start - step : 0);
+                            else
+                                y[q] = fetch8(B + static_cast<int64_t>(step + 16 * q) * g.rank,
+                                              (start - col) + step + r < g.n ? w.used - col : 0);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (16 * q < left) store16(slot + at + q * 2048, join8(x[q]));
+                            if (a_rows ? row0 + 16 * q < w.r16 : col < w.r16)
+                                store16(slot + kInBytes + at + q * 2048, join8(y[q]));
+                        }
+                        arrive_full(&full[s], lane);
+                        continue;
+                    }
                     if (!FAST && w.count <= 32)
                         pieces<FAST, 2>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
                     else if (!FAST)
@@ -1301,6 +1325,32 @@ __device__ __forceinline__ ChunkTokens chunk_tokens(const int32_t *order, int at
     return c;
 }
 
+// The z-th adapter that has tokens, or -1, by a whole block: the rows of the
+// plan's table that begin an adapter, counted in order.
+__device__ __forceinline__ int busy_adapter(const AdapterArgs &g, int z)
+{
+    __shared__ int found, counts[kGradAdThreads / 32];
+    if (threadIdx.x == 0) found = -1;
+    int seen = 0;
+    for (int r0 = 0; r0 < g.rows && seen <= z; r0 += kGradAdThreads) {
+        const int i = r0 + threadIdx.x;
+        const int4 t = i < g.rows ? reinterpret_cast<const int4 *>(g.tiles)[i] : make_int4(-1, 0, 0, 0);
+        const bool begins = t.z > 0 && t.x >= 0 && t.x < g.adapters && t.y == g.starts[t.x];
+        const uint32_t lanes = __ballot_sync(kFull, begins);
+        __syncthreads();  // the last round's counts have been read
+        if ((threadIdx.x & 31) == 0) counts[threadIdx.x / 32] = __popc(lanes);
+        __syncthreads();
+        int before = seen;
+        for (int w = 0; w < kGradAdThreads / 32; ++w) {
+            if (w < static_cast<int>(threadIdx.x / 32)) before += counts[w];
+            seen += counts[w];
+        }
+        if (begins && before + __popc(lanes & ((1u << (threadIdx.x & 31)) - 1)) == z) found = t.x;
+    }
+    __syncthreads();
+    return found;
+}
+
 // FAST: every row begins at a 16-byte boundary.  Then a chunk of 64 tokens that
 // are two runs of 32 comes as boxes.
 template <int RANK, int STAGES, bool FAST>
@@ -1315,7 +1365,9 @@ __global__ void __launch_bounds__(kGradAdThreads)
     const int blocks_x = (g.k + kGradCols - 1) / kGradCols;
     const bool is_a = static_cast<int>(blockIdx.y) < blocks_x;
     const int c0 = (is_a ? blockIdx.y : blockIdx.y - blocks_x) * kGradCols;
-    const int a = blockIdx.z;
+    // more adapters than tokens: the gradients are zero already, and only adapters with tokens get blocks
+    const int a = g.sparse ? busy_adapter(g, blockIdx.z) : blockIdx.z;
+    if (a < 0) return;
     const int first = g.starts[a], last = g.starts[a + 1];
     const int used = last > first ? used_rank(g, a) : 0, r16 = (used + 15) & ~15;
     const int cols = is_a ? g.k : g.n;
@@ -1727,8 +1779,9 @@ cudaError_t launch_tokens_at(const AdapterArgs &args, cudaStream_t s)
     const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (rc != cudaSuccess) return rc;
     const uint64_t n1 = (a.nin + 63) / 64, n2 = a.out ? (a.nout + 63) / 64 : 0;
-    // half of the adapters' last tiles are empty ones at a guess
-    const uint64_t tiles = std::max(1, a.tokens / 128 + (std::min(a.adapters, a.tokens) + 1) / 2);
+    // an adapter's last tile is half full at a guess, and with few tokens an adapter it is the only one
+    const uint64_t busy = std::min(a.adapters, a.tokens);
+    const uint64_t tiles = std::max(a.tokens / 128 + (busy + 1) / 2, busy + a.tokens / 256);
     uint64_t best = ~0ull;
     uint32_t c = 0, fit = 0;
     for (uint32_t d = 1; d <= 8 && d <= std::max(n1, n2); ++d) {
@@ -1802,7 +1855,7 @@ cudaError_t launch_grad_at(const AdapterArgs &a, uint64_t blocks, uint64_t chunk
                  !box_map(&maps.d, a.work, 2 * a.rank16, a.tokens, 2 * a.rank16, 0, dev::kGradTokens) ||
                  !box_map(&maps.v, a.work + half, 2 * a.rank16, a.tokens, 2 * a.rank16, 0, dev::kGradTokens)))
         return cudaErrorInvalidValue;
-    return launch(kernel, dim3(c, cols, a.adapters), dev::kGradAdThreads, smem, c, s, a, maps);
+    return launch(kernel, dim3(c, cols, a.sparse ? a.tokens : a.adapters), dev::kGradAdThreads, smem, c, s, a, maps);
 }
 
 template <int RANK, int STAGES>
@@ -2038,6 +2091,10 @@ extern "C" lct_status lct_adapter_backward(const lct_adapters *bank, const lct_t
         g.db = reinterpret_cast<__nv_bfloat16 *>(d_db);
         g.al_db = al16(d_db) && g.rank % 8 == 0;
     }
+    g.sparse = plan->tokens < bank->adapters;
+    if (d_da && g.sparse && (cudaMemsetAsync(d_da, 0, abytes, s) != cudaSuccess ||
+                             cudaMemsetAsync(d_db, 0, bbytes, s) != cudaSuccess))
+        return LCT_ERR_CUDA;
     if (launch_adapter(g, true, s) != cudaSuccess) return LCT_ERR_CUDA;
     if (d_da && launch_adapter_grad(g, s) != cudaSuccess) return LCT_ERR_CUDA;
     return LCT_OK;
