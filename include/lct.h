@@ -412,8 +412,10 @@ typedef struct {
 } lct_adapters;
 
 /* The grouping of a batch's tokens by adapter, from lct_adapter_plan: made
- * once for a batch and used for every projection in it.  Every entry is
- * trusted by the calls below (indices are the plan's own). */
+ * once for a batch and used for every projection in it.  Entries are checked
+ * against `tokens` and `adapters` where they are used: tables that are not a
+ * plan's reach nothing out of bounds, latch LCT_ERR_CORRUPT in the plan's
+ * status where that shows, and give unspecified results. */
 typedef struct {
     const int32_t *d_order;  /* [tokens]: tokens in stable order of their adapter, those without one last */
     const int32_t *d_starts; /* [adapters + 2]: where each adapter's tokens begin; without one; tokens */

@@ -274,9 +274,31 @@ __device__ __forceinline__ int used_rank(const AdapterArgs &g, int a)
     return max(0, min(r, g.rank));
 }
 
-__device__ __forceinline__ void fail(const AdapterArgs &g)
+// Latches an error in the plan.
+__device__ __forceinline__ void fail(const AdapterArgs &g, int code)
 {
-    if (g.status) atomicCAS(reinterpret_cast<unsigned int *>(g.status), 0u, static_cast<unsigned int>(LCT_ERR_TIMEOUT));
+    atomicCAS(reinterpret_cast<unsigned int *>(g.status), 0u, static_cast<unsigned int>(code));
+}
+
+// Place i of the order (i < tokens), and a row of the tile table: one that is
+// not a plan's reaches nothing out of bounds.
+__device__ __forceinline__ int checked_token(const AdapterArgs &g, int t)
+{
+    if (static_cast<uint32_t>(t) < static_cast<uint32_t>(g.tokens)) return t;
+    fail(g, LCT_ERR_CORRUPT);
+    return 0;
+}
+__device__ __forceinline__ int token_at(const AdapterArgs &g, int i) { return checked_token(g, g.order[i]); }
+__device__ __forceinline__ int4 tile_at(const AdapterArgs &g, int i)
+{
+    int4 t = reinterpret_cast<const int4 *>(g.tiles)[i];
+    if (t.z <= 0) {
+        t.z = 0;
+    } else if (t.z > kTileTokens || t.y < 0 || t.y > g.tokens - t.z) {
+        fail(g, LCT_ERR_CORRUPT);
+        t.z = 0;
+    }
+    return t;
 }
 
 // Waits at a barrier, for at most about a second by the SM's clock (a wait
@@ -406,12 +428,12 @@ __device__ __forceinline__ void fetch_map(const CUtensorMap *m)
 // group of 32 that lane 8 i belongs to.  (A box with rows past the tile's
 // tokens brings others', which reach only themselves.)
 constexpr int kBoxRows = 32;
-__device__ __forceinline__ uint32_t scattered(const int32_t *order, int first, int count, int lane, int &y)
+__device__ __forceinline__ uint32_t scattered(const AdapterArgs &g, int first, int count, int lane, int &y)
 {
     int t[4];
     bool in_line = true;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) t[j] = lane * 4 + j < count ? order[first + lane * 4 + j] : 0;
+    for (int j = 0; j < 4; ++j) t[j] = lane * 4 + j < count ? token_at(g, first + lane * 4 + j) : 0;
     y = __shfl_sync(kFull, t[0], lane & ~7);
 #pragma unroll
     for (int j = 0; j < 4; ++j) in_line = in_line && (lane * 4 + j >= count || t[j] == y + (lane & 7) * 4 + j);
@@ -452,10 +474,10 @@ __device__ __forceinline__ TileWork tile_work(const AdapterArgs &g, int i, uint3
 {
     TileWork w = {};
     if (i >= g.rows) return w;
-    const int4 t = reinterpret_cast<const int4 *>(g.tiles)[i];
+    const int4 t = tile_at(g, i);
     w.a = t.x;
     w.first = t.y;
-    w.count = min(t.z, kTileTokens);
+    w.count = t.z;
     w.used = t.x < 0 || t.x >= g.adapters || w.count <= 0 ? 0 : used_rank(g, t.x);
     w.r16 = (w.used + 15) & ~15;
     const int all1 = w.used ? (g.nin + kChunk - 1) / kChunk : 0;
@@ -565,11 +587,11 @@ __global__ void __launch_bounds__(kTokThreads, 1)
             const int start = rank * kChunk + col, stride = static_cast<int>(size) * kChunk;
             const int left = w.count - row0;  // rows from this thread's first one on
             int y;
-            const uint32_t loose = FAST ? scattered(g.order, w.first, w.count, lane, y) : 0xFu;
+            const uint32_t loose = FAST ? scattered(g, w.first, w.count, lane, y) : 0xFu;
             const bool boxes_w = FAST && g.boxes_w;
             int t[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) t[q] = 16 * q < left ? g.order[w.first + row0 + 16 * q] : 0;
+            for (int q = 0; q < 8; ++q) t[q] = 16 * q < left ? token_at(g, w.first + row0 + 16 * q) : 0;
             // A: R rows, 64 columns; B: 64 rows, R columns
             const __nv_bfloat16 *A = g.a + (static_cast<int64_t>(w.a) * g.rank + row0) * g.k + start;
             const __nv_bfloat16 *B = g.b + (static_cast<int64_t>(w.a) * g.n + rank * kChunk + row0) * g.rank + col;
@@ -660,7 +682,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
             const TileWork w = tile == first_tile ? first_work : tile_work(g, tile, rank, size);
             if (w.count <= 0) break;
             int mine = 0, y[4];
-            const uint32_t loose = FAST ? scattered(g.order, w.first, w.count, lane, mine) : 0xFu;
+            const uint32_t loose = FAST ? scattered(g, w.first, w.count, lane, mine) : 0xFu;
             uint32_t groups = 0, bytes = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -770,15 +792,15 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 for (int e = rank * 32 * kOutWarps + threadIdx.x; e < w.count * (g.rank - w.used);
                      e += size * 32 * kOutWarps) {
                     const int r = e / (g.rank - w.used), c = w.used + e - r * (g.rank - w.used);
-                    g.keep[static_cast<int64_t>(g.order[w.first + r]) * g.rank + c] = 0.0f;
+                    g.keep[static_cast<int64_t>(token_at(g, w.first + r)) * g.rank + c] = 0.0f;
                 }
             int my_token = 0;  // of row lane
-            if (!FAST && quarter * 32 + lane < w.count) my_token = g.order[w.first + quarter * 32 + lane];
+            if (!FAST && quarter * 32 + lane < w.count) my_token = token_at(g, w.first + quarter * 32 + lane);
             int t[8];  // the rows that this thread writes: 8 threads a row
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int r = quarter * 32 + j * 4 + lane / 8;
-                t[j] = r < w.count ? g.order[w.first + r] : 0;
+                t[j] = r < w.count ? token_at(g, w.first + r) : 0;
             }
             if (w.used) {
                 // V from the blocks' partial sums.  A unit is 8 of its columns for 32 rows, one row a lane; the
@@ -795,7 +817,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                     const int row = gr * 32 + lane;
                     const bool writes = row < w.count;
                     const int64_t token = writes && (BACK ? g.work != nullptr : g.keep != nullptr)
-                                              ? g.order[w.first + row] : 0;
+                                              ? token_at(g, w.first + row) : 0;
                     if (!BACK && g.keep && writes) {
                         float *k = g.keep + token * g.rank + p * 8;
 #pragma unroll
@@ -998,7 +1020,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
             }
         }
     }
-    if (waiter.dead) fail(g);
+    if (waiter.dead) fail(g, LCT_ERR_TIMEOUT);
     __syncwarp();
     if (size > 1 && warp >= kOutWarps) cluster_wait();
     tc_before();
@@ -1087,10 +1109,10 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
     extern __shared__ __align__(128) uint8_t raw[];
     __shared__ int tok[kTileTokens];
     const uint32_t rank = cluster_rank(), size = cluster_size();
-    const int4 tile = reinterpret_cast<const int4 *>(g.tiles)[blockIdx.x / size];
-    const int count = min(tile.z, kTileTokens);
+    const int4 tile = tile_at(g, blockIdx.x / size);
+    const int count = tile.z;
     if (count <= 0) return;
-    for (int i = threadIdx.x; i < count; i += kAdThreads) tok[i] = g.order[tile.y + i];
+    for (int i = threadIdx.x; i < count; i += kAdThreads) tok[i] = token_at(g, tile.y + i);
     const int a = tile.x;
     const int used = a < 0 || a >= g.adapters ? 0 : used_rank(g, a);
     if (used == 0) {
@@ -1313,15 +1335,15 @@ struct ChunkTokens {
     int near, far;
     bool runs;
 };
-__device__ __forceinline__ ChunkTokens chunk_tokens(const int32_t *order, int at, int last, bool there, int lane)
+__device__ __forceinline__ ChunkTokens chunk_tokens(const AdapterArgs &g, int at, int last, bool there, int lane)
 {
     ChunkTokens c = {0, 0, false};
     if (!there) return c;
-    if (at + lane < last) c.near = order[at + lane];
-    if (at + 32 + lane < last) c.far = order[at + 32 + lane];
+    if (at + lane < last) c.near = g.order[at + lane];
+    if (at + 32 + lane < last) c.far = g.order[at + 32 + lane];
     const int near0 = __shfl_sync(kFull, c.near, 0), far0 = __shfl_sync(kFull, c.far, 0);
     const int in_line = __all_sync(kFull, c.near == near0 + lane && c.far == far0 + lane);
-    c.runs = in_line && at + kGradTokens <= last;
+    c.runs = in_line && at + kGradTokens <= last;  // (a box outside the matrix is zero)
     return c;
 }
 
@@ -1334,7 +1356,7 @@ __device__ __forceinline__ int busy_adapter(const AdapterArgs &g, int z)
     int seen = 0;
     for (int r0 = 0; r0 < g.rows && seen <= z; r0 += kGradAdThreads) {
         const int i = r0 + threadIdx.x;
-        const int4 t = i < g.rows ? reinterpret_cast<const int4 *>(g.tiles)[i] : make_int4(-1, 0, 0, 0);
+        const int4 t = i < g.rows ? tile_at(g, i) : make_int4(-1, 0, 0, 0);
         const bool begins = t.z > 0 && t.x >= 0 && t.x < g.adapters && t.y == g.starts[t.x];
         const uint32_t lanes = __ballot_sync(kFull, begins);
         __syncthreads();  // the last round's counts have been read
@@ -1368,7 +1390,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
     // more adapters than tokens: the gradients are zero already, and only adapters with tokens get blocks
     const int a = g.sparse ? busy_adapter(g, blockIdx.z) : blockIdx.z;
     if (a < 0) return;
-    const int first = g.starts[a], last = g.starts[a + 1];
+    const int first = max(0, min(g.starts[a], g.tokens)), last = max(first, min(g.starts[a + 1], g.tokens));
     const int used = last > first ? used_rank(g, a) : 0, r16 = (used + 15) & ~15;
     const int cols = is_a ? g.k : g.n;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -1411,19 +1433,21 @@ __global__ void __launch_bounds__(kGradAdThreads)
             // V: 16 threads a token, eight of them its hi part
             const int v_row = id >> 4, v_lo = (id >> 3) & 1, v_c = id & 7;
             const uint32_t v_to = T::kIn + v_lo * T::kV + swz(v_row, v_c);
-            ChunkTokens tokens = chunk_tokens(g.order, chunk_at(group), last, group < n, lane);
+            ChunkTokens tokens = chunk_tokens(g, chunk_at(group), last, group < n, lane);
             for (int i = group; i < n; i += 2) {
                 const int s = i % STAGES;
                 const uint32_t slot = base + s * T::kSlot;
                 const int t0 = chunk_at(i);
                 const int left = last - t0;  // tokens from this chunk's first one on; the rest of it is zero
-                const ChunkTokens now = tokens;
-                tokens = chunk_tokens(g.order, chunk_at(i + 2), last, i + 2 < n, lane);
+                ChunkTokens now = tokens;
+                tokens = chunk_tokens(g, chunk_at(i + 2), last, i + 2 < n, lane);
                 if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
                 if (FAST && now.runs) {  // boxes hold it
                     arrive_idle(&full[s], lane);
                     continue;
                 }
+                now.near = checked_token(g, now.near);
+                now.far = checked_token(g, now.far);
                 auto token = [&](int row) { return __shfl_sync(kFull, row < 32 ? now.near : now.far, row & 31); };
                 if (FAST) {
 #pragma unroll
@@ -1455,11 +1479,11 @@ __global__ void __launch_bounds__(kGradAdThreads)
             async_wait<0>();
             if (n > 0) waiter.wait(&all_done, 0);
         } else if (warp == kGradBoxWarp) {
-            ChunkTokens tokens = chunk_tokens(g.order, chunk_at(0), last, FAST && n > 0, lane);
+            ChunkTokens tokens = chunk_tokens(g, chunk_at(0), last, FAST && n > 0, lane);
             for (int i = 0; i < n; ++i) {
                 const int s = i % STAGES;
                 const ChunkTokens now = tokens;
-                tokens = chunk_tokens(g.order, chunk_at(i + 1), last, FAST && i + 1 < n, lane);
+                tokens = chunk_tokens(g, chunk_at(i + 1), last, FAST && i + 1 < n, lane);
                 if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
                 const int y[2] = {__shfl_sync(kFull, now.near, 0), __shfl_sync(kFull, now.far, 0)};
                 if (!elect()) {
@@ -1562,7 +1586,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
                         if (p * 8 + j < g.rank) to[j] = __float2bfloat16_rn(x[j]);
             }
         }
-    if (waiter.dead) fail(g);
+    if (waiter.dead) fail(g, LCT_ERR_TIMEOUT);
     __syncwarp();
     cluster_sync();
     if (used && warp == 0) tmem_free(tmem, kGradTmemCols);

@@ -492,3 +492,49 @@ def test_refusals():
             adapter_grads(**{**dict(dy=c.dy, x=c.x, xa=xa, bank=c.bank, plan=c.plan, dx=c.dx), **kw})
     with pytest.raises(B.LctError):
         adapter_grads(c.dy, c.x, xa, c.bank, c.plan, c.dx, out=c.x)
+
+
+@pytest.mark.parametrize("what", ["order", "tiles", "starts"])
+@pytest.mark.parametrize("t,n", [(40, 40), (300, 2)])
+def test_tables_that_are_not_a_plan(what, t, n):
+    """Entries out of range reach nothing; the plan says so where it shows."""
+    c = Case(t, n, 16, 128, 128, index=[i % n for i in range(t)], seed=17)
+    _, xa = adapter_apply(c.x, c.bank, c.plan, c.y, keep=True)
+    bad = AdapterPlan(c.plan.order.clone(), c.plan.starts.clone(), c.plan.tiles.clone())
+    if what == "order":
+        bad.order[3::7] = 2 ** 31 - 1
+        bad.order[5::7] = -4
+    elif what == "tiles":
+        bad.tiles[1, 1] = t - 1
+        bad.tiles[1, 2] = 100_000
+    else:
+        bad.starts[1] = -5
+        bad.starts[2:] = 2 ** 30
+    out = adapter_apply(c.x, c.bank, bad, c.y)
+    grads = adapter_grads(c.dy, c.x, xa, c.bank, bad, c.dx)
+    torch.cuda.synchronize()
+    assert out.shape == c.y.shape and grads[0].shape == c.dx.shape
+    if what != "starts":
+        assert bad.status() == B.LCT_ERR_CORRUPT
+    check_forward(c, adapter_apply(c.x, c.bank, c.plan, c.y))
+    assert c.plan.status() == 0
+
+
+@pytest.mark.parametrize("t,n", [(1, 9), (3, 200), (30, 31), (90, 700), (400, 1000)])
+def test_more_adapters_than_tokens(t, n):
+    rng = random.Random(t)
+    both(Case(t, n, 8, 128, 136, seed=t, index=[rng.choice([-1, 0, n - 1, rng.randint(0, n - 1)]) for _ in range(t)]))
+
+
+@pytest.mark.parametrize("r", [16, 40, 80])
+@pytest.mark.parametrize("k,m", [(512, 768), (1000, 264)])
+def test_runs_of_consecutive_tokens(r, k, m):
+    """Runs longer and shorter than the boxes that they are loaded by."""
+    index = [0] * 200 + [1] * 33 + [-1] * 70 + [0] * 95 + [2] * 1 + [1] * 300 + [0] * 7 + [2] * 128 + [-1] * 3
+    both(Case(len(index), 3, r, k, m, seed=r + k, index=index))
+
+
+def test_many_tiles_a_block():
+    """More tiles than blocks fit on the GPU: blocks go on to further ones."""
+    both(Case(30_000, 2, 8, 64, 72, seed=18, index=[(i // 70) % 2 for i in range(30_000)]))
+    both(Case(26_000, 3, 72, 72, 64, seed=19, index=[i % 4 - 1 for i in range(26_000)]))
