@@ -1597,11 +1597,12 @@ __global__ void __launch_bounds__(kGradAdThreads)
 // The tokens in stable order of their adapter.  Each warp counts a contiguous
 // share of the tokens, one row of shared counters an adapter; a scan over
 // adapters and warps turns the counts into places, and each warp deals its
-// tokens out.  Lanes with the same adapter find each other by a match.  One
-// block: a plan is made once for a batch, and what it costs is latency, so
-// tokens are fetched sixteen rounds at a time (up to 16,384 tokens once, for both
+// tokens out.  Lanes with the same adapter find each other by a match.  A plan
+// is made once for a batch, and what it costs is latency: one block, or for a
+// long batch (where one SM would be issuing instructions for 10 us) a cluster
+// of eight, which read each other's totals; tokens are fetched sixteen rounds at a time (up to 16,384 tokens once, for both
 // passes), and a short batch has few warps.
-constexpr int kPlanRounds = 16;
+constexpr int kPlanRounds = 16, kPlanBlocks = 8;
 // The lanes with this lane's value; runs of one adapter need no match.
 __device__ __forceinline__ unsigned same_adapter(int a)
 {
@@ -1610,13 +1611,15 @@ __device__ __forceinline__ unsigned same_adapter(int a)
 }
 __global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ PlanArgs g)
 {
-    extern __shared__ int counts[];  // [adapters + 1][warps, and one more to spread the banks]
+    extern __shared__ int counts[];  // [adapters + 1][warps, and the block's total (which also spreads the banks)]
     __shared__ int part[32], tile_part[32];
     __shared__ int bad;
     const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x & 31, pitch = warps + 1;
+    const int block = cluster_rank(), blocks = cluster_size();
     const int groups = g.adapters + 1;
-    const int share = ((g.tokens + warps - 1) / warps + 31) & ~31;
-    const int lo = min(g.tokens, warp * share), hi = min(g.tokens, lo + share);
+    const int share = ((g.tokens + warps * blocks - 1) / (warps * blocks) + 31) & ~31;
+    const int lo = min(static_cast<int64_t>(g.tokens), static_cast<int64_t>(block * warps + warp) * share);
+    const int hi = min(g.tokens, lo + share);
     // a round's adapters, -1 past the end; those outside the bank are as none
     auto fetch = [&](int t0, int (&a)[kPlanRounds]) {
 #pragma unroll
@@ -1646,13 +1649,38 @@ __global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ P
         }
     }
     __syncthreads();
-    // exclusive places over (adapter, warp), and tiles over adapters: each thread takes a run of adapters
+    // exclusive places over (adapter, block, warp), and tiles over adapters: each thread takes a run of adapters
     const int run = (groups + blockDim.x - 1) / blockDim.x;
     const int a0 = min(groups, static_cast<int>(threadIdx.x) * run), a1 = min(groups, a0 + run);
-    int sum = 0, tiles = 0;
     for (int a = a0; a < a1; ++a) {
         int c = 0;
         for (int w = 0; w < warps; ++w) c += counts[a * pitch + w];
+        counts[a * pitch + warps] = c;
+    }
+    __syncwarp();
+    if (blocks > 1) cluster_sync();
+    // an adapter's tokens in all blocks, and in those before this one
+    auto totals = [&](int a, int &earlier) {
+        int all = 0;
+        earlier = 0;
+#pragma unroll
+        for (int p = 0; p < kPlanBlocks; ++p) {
+            const int c = p >= blocks  ? 0
+                          : blocks > 1 ? static_cast<int>(ld_peer_shared(&counts[a * pitch + warps], p))
+                                       : counts[a * pitch + warps];
+            all += c;
+            if (p < block) earlier += c;
+        }
+        return all;
+    };
+    bool any_bad = bad;
+    if (blocks > 1) {
+        any_bad = false;
+        for (int p = 0; p < blocks; ++p) any_bad = any_bad || ld_peer_shared(&bad, p);
+    }
+    int sum = 0, tiles = 0, earlier;
+    for (int a = a0; a < a1; ++a) {
+        const int c = totals(a, earlier);
         sum += c;
         tiles += (c + kTileTokens - 1) / kTileTokens;
     }
@@ -1674,19 +1702,25 @@ __global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ P
     int4 *table = reinterpret_cast<int4 *>(g.tiles);
     for (int a = a0; a < a1; ++a) {
         const int first = before;
-        g.starts[a] = first;
+        before += totals(a, earlier);
+        int place = first + earlier;
         for (int w = 0; w < warps; ++w) {
             const int c = counts[a * pitch + w];
-            counts[a * pitch + w] = before;
-            before += c;
+            counts[a * pitch + w] = place;
+            place += c;
         }
+        if (block == 0) g.starts[a] = first;
         for (int t = first; t < before; t += kTileTokens) {
-            const int flag = tiles_before == 0 && bad ? LCT_ERR_INVALID_ARG : 0;
-            table[tiles_before++] = make_int4(a == g.adapters ? -1 : a, t, min(kTileTokens, before - t), flag);
+            const int flag = tiles_before == 0 && any_bad ? LCT_ERR_INVALID_ARG : 0;
+            if (block == 0) table[tiles_before] = make_int4(a == g.adapters ? -1 : a, t, min(kTileTokens, before - t), flag);
+            ++tiles_before;
         }
     }
-    if (threadIdx.x == 0) g.starts[groups] = g.tokens;
-    for (int i = all_tiles + threadIdx.x; i < g.rows; i += blockDim.x) table[i] = make_int4(0, 0, 0, 0);
+    __syncwarp();
+    if (blocks > 1) cluster_arrive();  // the totals have been read
+    if (block == 0 && threadIdx.x == 0) g.starts[groups] = g.tokens;
+    for (int i = all_tiles + block * blockDim.x + threadIdx.x; i < g.rows; i += blocks * blockDim.x)
+        table[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
     for (int t0 = lo; t0 < hi; t0 += 32 * kPlanRounds) {
         if (hi - lo > 32 * kPlanRounds) fetch(t0, mine);  // a shorter share is still there
@@ -1704,6 +1738,8 @@ __global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ P
             __syncwarp();
         }
     }
+    __syncwarp();
+    if (blocks > 1) cluster_wait();  // no block leaves before its totals have been read
 }
 
 }  // namespace dev
@@ -1904,12 +1940,13 @@ cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s)
 
 cudaError_t launch_adapter_plan(const PlanArgs &a, cudaStream_t s)
 {
+    const uint32_t blocks = a.tokens > 4096 ? dev::kPlanBlocks : 1;
     // two rounds of 32 tokens a warp, as far as the counters leave room for warps
     uint32_t warps = 1;
-    while (warps < 32 && warps * 64 < static_cast<uint32_t>(a.tokens) &&
+    while (warps < 32 && warps * blocks * 64 < static_cast<uint32_t>(a.tokens) &&
            (a.adapters + 1ull) * (2 * warps + 1) * 4 <= 200 * 1024)
         warps *= 2;
-    return launch(dev::k_adapter_plan, dim3(1), warps * 32, (a.adapters + 1) * (warps + 1) * 4, 1, s, a);
+    return launch(dev::k_adapter_plan, dim3(blocks), warps * 32, (a.adapters + 1) * (warps + 1) * 4, blocks, s, a);
 }
 
 namespace {

@@ -240,16 +240,6 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
     if (threadIdx.x == 0) part[blockIdx.x] = (add ? part[blockIdx.x] : 0.0) + total;
 }
 
-// The total of all partial sums, in the first warp.
-__device__ __forceinline__ double total_of(const double *part, uint32_t parts)
-{
-    double t = 0.0;
-    for (uint32_t i = threadIdx.x; i < parts; i += 32) t += part[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    return t;
-}
-
 // The root of a total as root * 2^exp with root in [1, 2), in float: the
 // total's exponent made even, its fraction rounded to float (2^-24) and the
 // root of that (2^-24 again).  Zero, infinity and NaN pass with exp = 0.
@@ -291,13 +281,24 @@ __device__ __forceinline__ Factor factor_of(const Root &r, float max_norm)
     return f;
 }
 
-// The norm, and where `factor` is given that too.
-__global__ void __launch_bounds__(32) k_grad_norm(const double *part, uint32_t parts, float *norm, float max_norm,
-                                                  Factor *factor)
+// The norm, and where `factor` is given that too, from all partial sums (which
+// a thread reads at once: one warp that read them one after another took 6 us).
+__global__ void __launch_bounds__(kGradThreads)
+    k_grad_norm(const double *part, uint32_t parts, float *norm, float max_norm, Factor *factor)
 {
+    constexpr int kEach = (kGradMaxParts + kGradThreads - 1) / kGradThreads;
+    __shared__ double sh[kGradThreads];
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
-    const double total = total_of(part, parts);
+    double p[kEach], mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const uint32_t at = threadIdx.x + i * kGradThreads;
+        p[i] = at < parts ? part[at] : 0.0;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) mine += p[i];
+    const double total = block_sum(mine, sh);
     if (threadIdx.x == 0) {
         const Root r = root_of(total);
         *norm = norm_of(r);
@@ -536,7 +537,7 @@ cudaError_t run_tables(const GradArgs &a, bool clip, cudaStream_t s)
         ++tables;
     } while (at < a.count);
     dev::Factor *factor = clip ? reinterpret_cast<dev::Factor *>(a.part + kGradMaxParts) : nullptr;
-    rc = launch(dev::k_grad_norm, 1, 32, 1, true, s, static_cast<const double *>(a.part), parts, a.norm, a.max_norm,
+    rc = launch(dev::k_grad_norm, 1, dev::kGradThreads, 1, true, s, static_cast<const double *>(a.part), parts, a.norm, a.max_norm,
                 factor);
     if (!clip || rc != cudaSuccess) return rc;
     at = 0;

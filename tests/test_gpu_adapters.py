@@ -121,7 +121,8 @@ def plan_of(index, n):
 
 @pytest.mark.parametrize("t,n,runs", [(1, 1, False), (1, 500, False), (31, 3, False), (33, 3, True), (128, 1, True),
                                       (129, 1, True), (1000, 7, False), (1024, 1025, False), (5000, 64, True),
-                                      (20_011, 3, False), (3000, 16_384, False), (700, 2047, True)])
+                                      (20_011, 3, False), (3000, 16_384, False), (700, 2047, True), (4096, 9, True),
+                                      (4097, 9, True), (40_000, 5, True), (150_001, 40, False), (9000, 16_384, False)])
 def test_plan(t, n, runs):
     rng = random.Random(t * n)
     index = []
