@@ -539,6 +539,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
     const int clusters = gridDim.x / size, first_tile = blockIdx.x / size;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u, v_at = base + T::kVAt;
+    if (BACK) pdl_launch_dependents();  // the weights' gradients may set themselves up
     const TileWork first_work = tile_work(g, first_tile, rank, size);  // on its way while the block sets itself up
 
     if (warp == 0) tmem_alloc(&tmem_at, kTmemCols);
@@ -1415,6 +1416,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
         __syncthreads();
         tc_after();
         tmem = tmem_at;
+        pdl_wait();  // V is the tokens' kernel's
         auto chunk_at = [&](int i) {
             return first + (static_cast<int>(rank) + i * static_cast<int>(size)) * kGradTokens;
         };
@@ -1746,7 +1748,7 @@ __global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ P
 
 namespace {
 
-template <typename... P, typename... A>
+template <bool DEPENDENT = false, typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), dim3 grid, uint32_t threads, uint32_t smem, uint32_t cluster, cudaStream_t s,
                    A... args)
 {
@@ -1757,12 +1759,14 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, uint32_t threads, uint32_t s
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = DEPENDENT ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1915,7 +1919,7 @@ cudaError_t launch_grad_at(const AdapterArgs &a, uint64_t blocks, uint64_t chunk
                  !box_map(&maps.d, a.work, 2 * a.rank16, a.tokens, 2 * a.rank16, 0, dev::kGradTokens) ||
                  !box_map(&maps.v, a.work + half, 2 * a.rank16, a.tokens, 2 * a.rank16, 0, dev::kGradTokens)))
         return cudaErrorInvalidValue;
-    return launch(kernel, dim3(c, cols, a.sparse ? a.tokens : a.adapters), dev::kGradAdThreads, smem, c, s, a, maps);
+    return launch<true>(kernel, dim3(c, cols, a.sparse ? a.tokens : a.adapters), dev::kGradAdThreads, smem, c, s, a, maps);
 }
 
 template <int RANK, int STAGES>
