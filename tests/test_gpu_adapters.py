@@ -172,6 +172,13 @@ def test_batches(t, n, r, k, m):
     both(Case(t, n, r, k, m, seed=t + n))
 
 
+@pytest.mark.parametrize("r", [3, 16, 31, 64, 128])
+@pytest.mark.parametrize("t,n,k,m", [(17, 1, 128, 128), (32, 1, 4096, 4096), (25, 2, 1000, 136), (31, 3, 201, 1031),
+                                     (32, 3, 8192, 64), (29, 1, 64, 8192)])
+def test_a_batch_of_a_few_adapters(t, n, r, k, m):
+    both(Case(t, n, r, k, m, seed=t + r))
+
+
 def test_ranks_of_their_own_and_unused_values_are_not_read():
     c = Case(400, 6, 40, 256, 320, ranks=[0, 1, 16, 17, 40, 100], seed=1)
     for i, u in enumerate((0, 1, 16, 17)):
