@@ -180,7 +180,7 @@ __device__ __forceinline__ uint32_t find_entry(const GradTable<CAP> &t, uint32_t
 // is the vector's place in the span.  Eight units inside one tensor, whose
 // vectors are all whole, are the case that is to be fast (`whole` is then true
 // at compile time: with the checks of a tensor's edges in it, the scaling pass
-// took 85 instructions a vector, which is what bounded it).  Units that several
+// was bound by issuing instructions).  Units that several
 // tensors share (a list of small ones) have an address each, so that their
 // loads are in flight together.
 template <int CAP, typename With>
@@ -226,7 +226,9 @@ __device__ __forceinline__ double sum_units(const GradTable<CAP> &t, uint32_t lo
 }
 
 // Partial sums of one launch's tensors, one a block.  `add` is set on a later
-// launch over more tensors, which adds to the first one's partial sums.
+// launch over more tensors, which adds to the first one's partial sums.  324 MB
+// in 290 tensors take 53 us with the norm's launch, 6.1 TB/s, 91% of a copy's
+// rate; 1216 or 2432 blocks, or five or six an SM, were slower than these 608.
 template <int CAP>
 __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
     k_grad_sum(const __grid_constant__ GradTable<CAP> t, double *part, uint32_t add)
@@ -372,7 +374,10 @@ __device__ __forceinline__ void scale_units(const GradTable<CAP> &t, uint32_t u0
 // summing pass read last is what L2 still holds.  Many short blocks, as each
 // one first loads all it has and then stores it: blocks that stay and step
 // through their share fall into step with each other, and DRAM then turns
-// between reading and writing (181 instead of 152 us for 162 million values).
+// between reading and writing (norm and clipping of 162 million BF16 values
+// took 181 us so, 162 us by short blocks; since the first blocks also load
+// before the factor is there and the norm's last step is one round trip, 155
+// us: 3 x 324 MB of traffic at 6.3 TB/s, some of it from L2).
 template <int CAP>
 __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
     k_grad_scale(const __grid_constant__ GradTable<CAP> t, const Factor *factor)
@@ -391,7 +396,8 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocksPerSm)
 }
 
 // Norm and, for CLIP, scaling in one launch of one cluster: a few units, where
-// a second launch would cost as much as the work.
+// a second launch would cost as much as the work (the norm of 14 tensors of
+// 65,536 values in all: 4.5 us, most of it the launch and two meetings).
 template <int CAP, bool CLIP>
 __global__ void __launch_bounds__(kGradThreads) k_grad_cluster(const __grid_constant__ GradTable<CAP> t,
                                                                float max_norm, float *norm)
