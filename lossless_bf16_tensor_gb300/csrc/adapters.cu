@@ -197,6 +197,37 @@ __device__ __forceinline__ void piece(uint32_t dst, const __nv_bfloat16 *src, in
     }
 }
 
+// Rows at any address.  PIECES 16-byte pieces of a row are copied from the
+// aligned address at or below its first value (the piece that holds that value
+// lies in the tensor's allocation with all of its bytes), asynchronously like
+// aligned ones, and moved down by the row's `skip` values when they are there.
+// The last piece may need a part of one more, which goes to `extra`.  This is
+// one piece's copy, from its aligned address; `valid` of the row's values are
+// there, the rest is zero.
+__device__ __forceinline__ uint32_t skip_of(const __nv_bfloat16 *row)
+{
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) >> 1) & 7;
+}
+template <int PIECES>
+__device__ __forceinline__ void raw_piece(uint32_t dst, uint32_t extra, const __nv_bfloat16 *from, uint32_t skip,
+                                          int piece, int valid)
+{
+    const int left = valid <= 0 ? 0 : min(valid, 8 * PIECES) + static_cast<int>(skip) - 8 * piece;
+    async16(dst, from, 2 * max(0, min(left, 8)));
+    if (piece == PIECES - 1 && skip) async16(extra, from + 8, 2 * max(0, left - 8));
+}
+// The eight values from the skip-th on of two pieces.
+__device__ __forceinline__ uint4 move_down(const uint4 &x, const uint4 &y, uint32_t skip)
+{
+    const bool four = skip & 4, two = skip & 2;
+    const uint32_t a0 = four ? x.z : x.x, a1 = four ? x.w : x.y, a2 = four ? y.x : x.z, a3 = four ? y.y : x.w,
+                   a4 = four ? y.z : y.x, a5 = four ? y.w : y.y;
+    const uint32_t b0 = two ? a1 : a0, b1 = two ? a2 : a1, b2 = two ? a3 : a2, b3 = two ? a4 : a3, b4 = two ? a5 : a4;
+    const uint32_t odd = (skip & 1) * 16;
+    return make_uint4(__funnelshift_r(b0, b1, odd), __funnelshift_r(b1, b2, odd), __funnelshift_r(b2, b3, odd),
+                      __funnelshift_r(b3, b4, odd));
+}
+
 __device__ __forceinline__ uint32_t pack2(float a, float b)
 {
     const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
@@ -451,16 +482,19 @@ constexpr uint32_t kTmemCols = 512;
 
 // Shared memory: a ring of slots, each a 128 x 64 tile of In (or of the row to
 // add to) and a tile of W1 or W2; then V, hi and lo, whose space first holds
-// the block's partial sums.  It takes the whole SM.
-template <int RANK>
+// the block's partial sums.  It takes the whole SM.  Without boxes a slot has
+// room beside it for the pieces that rows at any address end in.
+template <int RANK, bool FAST>
 struct Tok {
     static constexpr int kAtoms = RANK / 64;
     static constexpr uint32_t kWBytes = kAtoms * 64 * 128, kSlot = kInBytes + kWBytes;
     static constexpr uint32_t kVAtom = kTileTokens * 128, kVLo = kAtoms * kVAtom;
-    static constexpr int kStages = RANK <= 64 ? 8 : 4;
+    static constexpr int kStages = RANK > 64 ? 4 : FAST ? 8 : 6;
     static_assert(kStages % 2 == 0, "a slot belongs to one load group, which sees each of its phases");
     static constexpr uint32_t kVAt = kStages * kSlot;
-    static constexpr uint32_t kBytes = kVAt + 2 * kVLo + 1024;  // room to start at a 1024-byte boundary
+    static constexpr uint32_t kExtraAt = kVAt + 2 * kVLo, kExtraW = kTileTokens * 16;
+    static constexpr uint32_t kExtra = FAST ? 0 : kExtraW + RANK * 16;
+    static constexpr uint32_t kBytes = kExtraAt + kStages * kExtra + 1024;  // room to start at a 1024-byte boundary
     static constexpr int kUnits = RANK / 32;  // a warp's share of V's units in a cluster of two, at most
 };
 
@@ -489,25 +523,40 @@ __device__ __forceinline__ TileWork tile_work(const AdapterArgs &g, int i, uint3
 }
 
 // N 16-byte pieces, 16 rows apart, from src(0) on: `valid` of a row's eight
-// values are there, and rows from `rows` on are empty.  Pieces that do not
-// travel asynchronously are all fetched before the first is stored.
-// (A copy of no bytes reads nothing, whatever its address.)
-template <bool FAST, int N, typename Src>
-__device__ __forceinline__ void pieces(uint32_t dst, Src src, int valid, int rows, bool aligned)
+// values are there, and rows from `rows` on are empty.  (A copy of no bytes
+// reads nothing, whatever its address.)
+template <int N, typename Src>
+__device__ __forceinline__ void pieces(uint32_t dst, Src src, int valid, int rows)
 {
-    if (FAST || aligned) {
-        const uint32_t bytes = valid <= 0 ? 0u : static_cast<uint32_t>(min(valid, 8)) * 2;
+    const uint32_t bytes = valid <= 0 ? 0u : static_cast<uint32_t>(min(valid, 8)) * 2;
 #pragma unroll
-        for (int q = 0; q < N; ++q) async16(dst + q * 2048, src(q), 16 * q < rows ? bytes : 0u);
-    } else {
-        constexpr int M = N < 8 ? N : 8;
+    for (int q = 0; q < N; ++q) async16(dst + q * 2048, src(q), 16 * q < rows ? bytes : 0u);
+}
+
+// A chunk whose pieces are on their way: its slot, and of each of a thread's
+// rows, 16 apart, the values to skip (four bits each), In's and the weights'.
+struct Late {
+    uint32_t rows, weights;
+    int slot;
+};
+// Moves a thread's pieces of one tile down, once its warp's copies are there.
+template <int N>
+__device__ __forceinline__ void move_rows(uint32_t tile, uint32_t next, uint32_t next_step, uint32_t skips)
+{
+    if (!__any_sync(kFull, skips != 0)) return;
+#pragma unroll 1
+    for (int h = 0; h < N; h += 4, skips >>= 16, tile += 4 * 2048, next += 4 * next_step) {
+        uint4 x[4], y[4];
 #pragma unroll
-        for (int h = 0; h < N; h += M) {
-            Eight x[M];
+        for (int q = 0; q < 4; ++q) {
+            x[q] = load16(tile + q * 2048);
+            y[q] = load16(next + q * next_step);
+        }
+        __syncwarp();  // a row's threads have all read it
 #pragma unroll
-            for (int q = 0; q < M; ++q) x[q] = fetch8(src(h + q), 16 * (h + q) < rows ? valid : 0);
-#pragma unroll
-            for (int q = 0; q < M; ++q) store16(dst + (h + q) * 2048, join8(x[q]));
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t skip = skips >> 4 * q & 7;
+            if (skip) store16(tile + q * 2048, move_down(x[q], y[q], skip));
         }
     }
 }
@@ -528,14 +577,21 @@ __device__ __forceinline__ void pieces(uint32_t dst, Src src, int valid, int row
 //
 // Forward of 8192 tokens of 16 adapters in runs, rank 64, 4096 to 8192 columns:
 // 67 us for 361 MB (5.4 TB/s, 80% of a copy's rate), the tensor pipe busy 15%
-// of the time.  777 scattered tokens of five adapters at odd widths (1001 to
-// 2047), which are copied through registers: 20 us, which is the time of the
-// few dependent steps of a tile (plan, chunks, meeting, second product).
+// of the time.
+//
+// Rows at any address come as aligned pieces too, and the load warps move them
+// down in shared memory when they are there; a chunk later, so that a group has
+// two on their way (three would wait for slots: 244 instead of 205 us at the
+// time).  16,384 tokens, rank 64, 4095 to 4097 columns: 159 us forward (rows
+// read through registers 435 us; aligned rows 76 us): the results' warps, which
+// move rows up to the output's alignment, bound it.  777 scattered tokens of
+// five adapters from 1001 to 2047 columns: 20 us, the few dependent steps of a
+// tile (plan, chunks, meeting, second product).
 template <bool BACK, int RANK, bool FAST>
 __global__ void __launch_bounds__(kTokThreads, 1)
     k_adapter(const __grid_constant__ AdapterArgs g, const __grid_constant__ TokenMaps maps)
 {
-    using T = Tok<RANK>;
+    using T = Tok<RANK, FAST>;
     constexpr int S = T::kStages;
     extern __shared__ uint8_t raw[];
     // a slot is full, and free again; the narrow product, and a tile of sums of the second one, is there, the latter
@@ -590,6 +646,20 @@ __global__ void __launch_bounds__(kTokThreads, 1)
             ++i;
             s = s + 1 == S ? 0 : s + 1;
         };
+        // rows at any address: the last chunk whose pieces are to be moved when they are there, if any
+        Late late = {};
+        bool flying = false;
+        const uint32_t extra0 = base + T::kExtraAt + row0 * 16;
+        auto settle = [&](const Late &c) {
+            const uint32_t slot = base + c.slot * T::kSlot, extra = extra0 + c.slot * T::kExtra;
+            const bool end = (id & 7) == 7;
+            const uint32_t next = swz(row0, (id + 1) & 7);
+            move_rows<8>(slot + at, end ? extra : slot + next, end ? 256 : 2048, c.rows);
+            move_rows<RANK / 16>(slot + kInBytes + at, end ? extra + T::kExtraW : slot + kInBytes + next,
+                                 end ? 256 : 2048, c.weights);
+            __syncwarp();
+            arrive_idle(&full[c.slot], lane);
+        };
         for (int tile = first_tile;; tile += clusters) {
             const TileWork w = tile == first_tile ? first_work : tile_work(g, tile, rank, size);
             if (w.count <= 0) break;
@@ -608,13 +678,13 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 const int valid = g.k - start - step, rows = w.used - row0;
                 const int64_t down = static_cast<int64_t>(16) * g.k;
                 if (RANK > 64 && w.r16 > 64)
-                    pieces<FAST, RANK / 16>(to + at, [&](int q) { return A + step + q * down; }, valid, rows, g.al_a);
+                    pieces<RANK / 16>(to + at, [&](int q) { return A + step + q * down; }, valid, rows);
                 else if (w.r16 > 32)
-                    pieces<FAST, 4>(to + at, [&](int q) { return A + step + q * down; }, valid, rows, g.al_a);
+                    pieces<4>(to + at, [&](int q) { return A + step + q * down; }, valid, rows);
                 else if (w.r16 > 16)
-                    pieces<FAST, 2>(to + at, [&](int q) { return A + step + q * down; }, valid, rows, g.al_a);
+                    pieces<2>(to + at, [&](int q) { return A + step + q * down; }, valid, rows);
                 else
-                    pieces<FAST, 1>(to + at, [&](int q) { return A + step + q * down; }, valid, rows, g.al_a);
+                    pieces<1>(to + at, [&](int q) { return A + step + q * down; }, valid, rows);
             };
             auto load_b = [&](uint32_t to, int step) {
                 const int rows = g.n - (start - col) - step - row0;
@@ -623,67 +693,120 @@ __global__ void __launch_bounds__(kTokThreads, 1)
 #pragma unroll
                 for (int h = 0; h < T::kAtoms; ++h)
                     if (col + 64 * h < w.r16)
-                        pieces<FAST, 4>(to + at + h * 64 * 128, [&](int q) { return from + 64 * h + q * down; },
-                                        w.used - col - 64 * h, rows, g.al_b);
+                        pieces<4>(to + at + h * 64 * 128, [&](int q) { return from + 64 * h + q * down; },
+                                  w.used - col - 64 * h, rows);
             };
             // the rows of In or of what is added to; rows past the tile's tokens stay as they are, by 16 at the
             // least: they reach only themselves
-            auto product = [&](const __nv_bfloat16 *m, int64_t ld, bool al, int cols, int chunks, bool two) {
-                const __nv_bfloat16 *p[8];
+            // at any address: the values to skip, which no step changes (64 columns, and 64 rows, are 128 bytes or
+            // a multiple), four bits a row, and the pieces' aligned addresses
+            const int piece = id & 7;
+            uint32_t skips_a = 0, skips_b = 0;
+            if (!FAST) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) p[q] = m + t[q] * ld + start;
+                for (int q = 0; q < RANK / 16; ++q) {
+                    if (row0 + 16 * q < w.used) skips_a |= skip_of(A - col + static_cast<int64_t>(16 * q) * g.k) << 4 * q;
+                    if (q / 4 * 64 < w.used)
+                        skips_b |= skip_of(B - col + static_cast<int64_t>(q % 4 * 16) * g.rank + q / 4 * 64) << 4 * q;
+                }
+            }
+            auto product = [&](const __nv_bfloat16 *m, int64_t ld, int cols, int chunks, bool two) {
+                const __nv_bfloat16 *p[8];
+                uint32_t skips = 0;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    p[q] = m + t[q] * ld + start;
+                    if (!FAST) {
+                        const uint32_t skip = skip_of(p[q] - col);
+                        p[q] -= skip;
+                        if (16 * q < left) skips |= skip << 4 * q;
+                    }
+                }
                 int step = 0;  // columns from the first chunk
                 for (int k = 0; k < chunks; ++k, next(), step += stride) {
                     if ((i & 1) != group) continue;
                     if (i >= S) waiter.wait(&freed[s], (i / S - 1) & 1);
                     const uint32_t slot = base + s * T::kSlot;
-                    const int valid = cols - start - step;
-                    if (FAST && loose == 0 && (boxes_w || !w.used)) {  // boxes hold all of it
-                        arrive_idle(&full[s], lane);
-                        continue;
-                    }
-                    if (!FAST && !al && w.count <= 64 && w.used && w.r16 <= 64 && !(two == BACK ? g.al_a : g.al_b)) {
-                        // rows and weights at any address: one round trip to memory for both
-                        Eight x[4], y[4];
-                        const bool a_rows = two == BACK;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            x[q] = fetch8(p[q] + step, 16 * q < left ? valid : 0);
-                            const int r = row0 + 16 * q;
-                            if (a_rows)
-                                y[q] = fetch8(A + step + static_cast<int64_t>(16 * q) * g.k,
-                                              r < w.used ? g.k - start - step : 0);
-                            else
-                                y[q] = fetch8(B + static_cast<int64_t>(step + 16 * q) * g.rank,
-                                              (start - col) + step + r < g.n ? w.used - col : 0);
+                    if (FAST) {
+                        if (loose == 0 && (boxes_w || !w.used)) {  // boxes hold all of it
+                            arrive_idle(&full[s], lane);
+                            continue;
                         }
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (16 * q < left) store16(slot + at + q * 2048, join8(x[q]));
-                            if (a_rows ? row0 + 16 * q < w.r16 : col < w.r16)
-                                store16(slot + kInBytes + at + q * 2048, join8(y[q]));
+                        for (int q = 0; q < 8; q += 2)
+                            if (loose >> q / 2 & 1)
+                                pieces<2>(slot + at + q * 2048, [&](int e) { return p[q + e] + step; },
+                                          cols - start - step, left - 16 * q);
+                        if (w.used && !boxes_w)
+                            two == BACK ? load_a(slot + kInBytes, step) : load_b(slot + kInBytes, step);
+                        arrive_full(&full[s], lane);
+                        continue;
+                    }
+                    const uint32_t extra = extra0 + s * T::kExtra, extra_w = extra + T::kExtraW;
+                    const int here = start - col + step;  // the chunk's first column
+                    if (cols - here >= kChunk) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (16 * q < w.count) async16(slot + at + q * 2048, p[q] + step, 16 * q < left ? 16 : 0);
+                        if (piece == 7 && skips)
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                if (skips >> 4 * q & 7)
+                                    async16(extra + q * 256, p[q] + step + 8, 2 * (skips >> 4 * q & 7));
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            if (16 * q < w.count)
+                                raw_piece<8>(slot + at + q * 2048, extra + q * 256, p[q] + step, skips >> 4 * q & 7, piece,
+                                             16 * q < left ? cols - here : 0);
+                    }
+                    const uint32_t to = slot + kInBytes + at;
+                    uint32_t skips_w = two == BACK ? skips_a : skips_b;
+                    if (two == BACK) {
+                        const __nv_bfloat16 *from = A + step;
+                        const int64_t down = static_cast<int64_t>(16) * g.k;
+#pragma unroll 2
+                        for (int q = 0; 16 * q < w.r16; ++q, from += down) {
+                            const uint32_t skip = skips_w >> 4 * q & 7;
+                            raw_piece<8>(to + q * 2048, extra_w + q * 256, from - skip, skip, piece,
+                                         row0 + 16 * q < w.used ? g.k - here : 0);
+                        }
+                    } else {
+                        const __nv_bfloat16 *from = B + static_cast<int64_t>(step) * g.rank;
+                        const int64_t down = static_cast<int64_t>(16) * g.rank;
+#pragma unroll 2
+                        for (int q = 0; q / 4 * 64 < w.r16; ++q) {
+                            const uint32_t skip = skips_w >> 4 * q & 7;
+                            raw_piece<8>(to + q * 2048, extra_w + q * 256, from + q % 4 * down + q / 4 * 64 - skip, skip,
+                                         piece, here + row0 + q % 4 * 16 < g.n ? w.used - q / 4 * 64 : 0);
+                        }
+                    }
+                    if (!__any_sync(kFull, (skips | skips_w) != 0)) {
+                        if (flying) {
+                            async_wait<0>();
+                            __syncwarp();
+                            settle(late);
+                            flying = false;
                         }
                         arrive_full(&full[s], lane);
                         continue;
                     }
-                    if (!FAST && w.count <= 32)
-                        pieces<FAST, 2>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
-                    else if (!FAST)
-                        pieces<FAST, 8>(slot + at, [&](int q) { return p[q] + step; }, valid, left, al);
-                    else
-#pragma unroll
-                        for (int q = 0; q < 8; q += 2)
-                            if (loose >> q / 2 & 1)
-                                pieces<FAST, 2>(slot + at + q * 2048, [&](int e) { return p[q + e] + step; }, valid,
-                                                left - 16 * q, al);
-                    if (w.used && !boxes_w) two == BACK ? load_a(slot + kInBytes, step) : load_b(slot + kInBytes, step);
-                    arrive_full(&full[s], lane);
+                    async_commit();
+                    if (flying) {
+                        async_wait<1>();
+                        __syncwarp();
+                        settle(late);
+                    }
+                    flying = true;
+                    late = {skips, skips_w, s};
                 }
             };
-            product(g.in, g.ld_in, g.al_in, g.nin, w.n1, false);
-            product(g.base, g.ld_base, g.al_base, g.nout, w.n2, true);
+            product(g.in, g.ld_in, g.nin, w.n1, false);
+            product(g.base, g.ld_base, g.nout, w.n2, true);
         }
         async_wait<0>();
+        __syncwarp();
+        if (flying) settle(late);
     } else if (warp == kBoxWarp) {
         // ------------------------------------------------------------ boxes
         int i = 0, s = 0;
@@ -803,8 +926,6 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                     const int r = e / (g.rank - w.used), c = w.used + e - r * (g.rank - w.used);
                     g.keep[static_cast<int64_t>(token_at(g, w.first + r)) * g.rank + c] = 0.0f;
                 }
-            int my_token = 0;  // of row lane
-            if (!FAST && quarter * 32 + lane < w.count) my_token = token_at(g, w.first + quarter * 32 + lane);
             int t[8];  // the rows that this thread writes: 8 threads a row
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -1003,23 +1124,41 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                         }
                     }
                 } else {
-                    // rows at any address: a warp writes one row's 64 values at a time, two a lane
-                    const int at = rank * kChunk + step + lane;
-                    for (int j = 0; j < 32 && quarter * 32 + j < w.count; j += 8) {
-                        uint16_t near[8], far[8];
+                    // rows at any address: eight threads write a row's seven whole pieces, and one each of the eight
+                    // values that are left at its two ends; four rows' at a time, without a branch inside
+                    const int c = lane & 7, here = mine - c * 8 + step;
+                    const bool whole = g.nout - here >= kChunk;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int row = quarter * 32 + j + e;
-                            near[e] = load2(slot + swz(row, lane >> 3) + (lane & 7) * 2);
-                            far[e] = load2(slot + swz(row, 4 + (lane >> 3)) + (lane & 7) * 2);
+                    for (int j0 = 0; j0 < 8; j0 += 4) {
+                        uint4 x[4], y[4];
+                        uint16_t one[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t row = quarter * 32 + (j0 + j) * 4 + lane / 8;
+                            const int skip = skip_of(o[j0 + j]), e = c < 8 - skip ? c : 56 + c;
+                            x[j] = load16(slot + swz(row, skip ? (c + 7) & 7 : c));
+                            y[j] = load16(slot + swz(row, c));
+                            one[j] = load2(slot + swz(row, e >> 3) + (e & 7) * 2);
                         }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int64_t token = __shfl_sync(kFull, my_token, j + e);
-                            uint16_t *to = reinterpret_cast<uint16_t *>(g.out) + token * g.ld_out + at;
-                            const bool there = quarter * 32 + j + e < w.count;
-                            if (there && at < g.nout) to[0] = near[e];
-                            if (there && at + 32 < g.nout) to[32] = far[e];
+                        for (int j = 0; j < 4; ++j) {
+                            const int skip = skip_of(o[j0 + j]), e = c < 8 - skip ? c : 56 + c;
+                            const bool mine_too = 4 * (j0 + j) < rows_left;
+                            __nv_bfloat16 *to = o[j0 + j] + step;
+                            const uint4 v = move_down(x[j], y[j], 8 - skip);  // (moved by eight it is x)
+                            if (mine_too && skip && here + e < g.nout)
+                                reinterpret_cast<uint16_t *>(to)[e - c * 8] = one[j];
+                            if (whole) {
+                                if (mine_too && (!skip || c)) *reinterpret_cast<uint4 *>(to - skip) = v;
+                            } else if (mine_too && (!skip || c)) {
+                                const int there = g.nout - here - c * 8 + skip;
+                                const uint32_t z[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    if (e < there)
+                                        reinterpret_cast<uint16_t *>(to - skip)[e] =
+                                            static_cast<uint16_t>(z[e / 2] >> (16 * (e & 1)));
+                            }
                         }
                     }
                 }
@@ -1363,7 +1502,7 @@ constexpr int kGradMmaWarp = kGradLoadWarps, kGradBoxWarp = kGradMmaWarp + 1;
 constexpr int kGradAdThreads = 32 * (kGradBoxWarp + 1);
 constexpr uint32_t kGradTmemCols = 256;
 
-template <int RANK, int STAGES>
+template <int RANK, int STAGES, bool FAST>
 struct Grad {
     static constexpr int kAtoms = RANK / 64;
     // two load groups take slots in turn, and slots come free in order: of two or more, a group that waits for a
@@ -1373,7 +1512,9 @@ struct Grad {
     static constexpr uint32_t kIn = kGradCols / 64 * kTile, kV = kAtoms * kTile, kSlot = kIn + 2 * kV;
     static constexpr uint32_t kSumRow = (kGradCols + 1) * 4;  // one rank's sums, an odd number of words
     static constexpr uint32_t kSums = RANK * kSumRow;
-    static constexpr uint32_t kBytes = (STAGES * kSlot > kSums ? STAGES * kSlot : kSums) + 1024;
+    static constexpr uint32_t kExtraAt = STAGES * kSlot, kExtra = FAST ? 0 : kGradTokens * 16;  // as in Tok
+    static constexpr uint32_t kRing = STAGES * (kSlot + kExtra);
+    static constexpr uint32_t kBytes = (kRing > kSums ? kRing : kSums) + 1024;
 };
 
 // The tokens of a chunk of 64, two a lane, and whether they are two runs of 32
@@ -1426,7 +1567,7 @@ template <int RANK, int STAGES, bool FAST>
 __global__ void __launch_bounds__(kGradAdThreads)
     k_adapter_grad(const __grid_constant__ AdapterArgs g, const __grid_constant__ GradMaps maps)
 {
-    using T = Grad<RANK, STAGES>;
+    using T = Grad<RANK, STAGES, FAST>;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[STAGES], freed[STAGES], all_done;
     __shared__ uint32_t tmem_at;
@@ -1481,10 +1622,41 @@ __global__ void __launch_bounds__(kGradAdThreads)
             // V: 16 threads a token, eight of them its hi part
             const int v_row = id >> 4, v_lo = (id >> 3) & 1, v_c = id & 7;
             const uint32_t v_to = T::kIn + v_lo * T::kV + swz(v_row, v_c);
+            // at any address: the last chunk whose pieces are to be moved when they are there, if any, and the values to
+            // skip in each of its tokens' rows, four bits each
+            uint64_t late = 0;
+            int late_slot = -1;
+            auto settle = [&]() {
+                const uint32_t slot = base + late_slot * T::kSlot;
+                const int next = lane + 1, tile = (next >> 3) * T::kTile;
+                const uint32_t extra = base + T::kExtraAt + late_slot * T::kExtra + w4 * 16;
+                uint32_t far0 = lane == 31 ? extra : slot + tile + swz(w4, next & 7);
+                uint32_t far1 = lane == 31 ? extra + 64 : slot + tile + swz(w4 + 4, next & 7);
+                const uint32_t down = lane == 31 ? 128 : 1024;
+#pragma unroll 1
+                for (int h = 0; h < 16; h += 4, far0 += 2 * down, far1 += 2 * down, late >>= 16) {
+                    uint4 x[4], y[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        x[q] = load16(slot + (q & 1 ? odd : even) + (h + q) / 2 * 1024);
+                        y[q] = load16((q & 1 ? far1 : far0) + q / 2 * down);
+                    }
+                    __syncwarp();  // a row's threads have all read it
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t skip = static_cast<uint32_t>(late >> 4 * q) & 7;
+                        if (skip) store16(slot + (q & 1 ? odd : even) + (h + q) / 2 * 1024, move_down(x[q], y[q], skip));
+                    }
+                }
+                __syncwarp();
+                arrive_idle(&full[late_slot], lane);
+                late_slot = -1;
+            };
             ChunkTokens tokens = chunk_tokens(g, chunk_at(group), last, group < n, lane);
             for (int i = group; i < n; i += 2) {
                 const int s = i % STAGES;
                 const uint32_t slot = base + s * T::kSlot;
+                uint64_t skips = 0;
                 const int t0 = chunk_at(i);
                 const int left = last - t0;  // tokens from this chunk's first one on; the rest of it is zero
                 ChunkTokens now = tokens;
@@ -1503,16 +1675,14 @@ __global__ void __launch_bounds__(kGradAdThreads)
                         async16(slot + (q & 1 ? odd : even) + q / 2 * 1024,
                                 from + static_cast<int64_t>(token(w4 + 4 * q)) * ld, w4 + 4 * q < left ? bytes : 0u);
                 } else {
-#pragma unroll 1
-                    for (int h = 0; h < 16; h += 8) {
-                        Eight x[8];
+                    const uint32_t extra = base + T::kExtraAt + s * T::kExtra + w4 * 16;
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            x[q] = fetch8(from + static_cast<int64_t>(token(w4 + 4 * (h + q))) * ld,
-                                          w4 + 4 * (h + q) < left ? valid : 0);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            store16(slot + (q & 1 ? odd : even) + (h + q) / 2 * 1024, join8(x[q]));
+                    for (int q = 0; q < 16; ++q) {
+                        const __nv_bfloat16 *line = in + static_cast<int64_t>(token(w4 + 4 * q)) * ld + c0;
+                        const uint32_t skip = w4 + 4 * q < left ? skip_of(line) : 0;
+                        raw_piece<32>(slot + (q & 1 ? odd : even) + q / 2 * 1024, extra + q * 64,
+                                      line - skip + lane * 8, skip, lane, w4 + 4 * q < left ? cols - c0 : 0);
+                        skips |= static_cast<uint64_t>(skip) << 4 * q;
                     }
                 }
                 for (int c = v_c * 8; c < r16; c += 64) {
@@ -1522,9 +1692,27 @@ __global__ void __launch_bounds__(kGradAdThreads)
                     for (int q = 0; q < 8; ++q)
                         async16(to + q * 1024, p + q * 16 * g.rank16, v_row + 8 * q < left ? 16 : 0);
                 }
-                arrive_full(&full[s], lane);
+                if (FAST) {
+                    arrive_full(&full[s], lane);
+                    continue;
+                }
+                async_commit();
+                if (late_slot >= 0) {
+                    async_wait<1>();
+                    __syncwarp();
+                    settle();
+                }
+                late = skips;
+                late_slot = s;
+                if (STAGES == 2) {  // the group's only slot
+                    async_wait<0>();
+                    __syncwarp();
+                    settle();
+                }
             }
             async_wait<0>();
+            __syncwarp();
+            if (late_slot >= 0) settle();
             if (n > 0) waiter.wait(&all_done, 0);
         } else if (warp == kGradBoxWarp) {
             ChunkTokens tokens = chunk_tokens(g, chunk_at(0), last, FAST && n > 0, lane);
@@ -1887,7 +2075,7 @@ cudaError_t launch_tokens_at(const AdapterArgs &args, cudaStream_t s)
         if (!ok) return cudaErrorInvalidValue;
     }
     const auto kernel = dev::k_adapter<BACK, RANK, FAST>;
-    constexpr uint32_t smem = dev::Tok<RANK>::kBytes;
+    constexpr uint32_t smem = dev::Tok<RANK, FAST>::kBytes;
     const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (rc != cudaSuccess) return rc;
     const uint64_t n1 = (a.nin + 63) / 64, n2 = a.out ? (a.nout + 63) / 64 : 0;
@@ -1952,7 +2140,7 @@ template <int RANK, int STAGES, bool FAST>
 cudaError_t launch_grad_at(const AdapterArgs &a, uint64_t blocks, uint64_t chunks, cudaStream_t s)
 {
     const auto kernel = dev::k_adapter_grad<RANK, STAGES, FAST>;
-    constexpr uint32_t smem = dev::Grad<RANK, STAGES>::kBytes;
+    constexpr uint32_t smem = dev::Grad<RANK, STAGES, FAST>::kBytes;
     const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (rc != cudaSuccess) return rc;
     uint64_t best = ~0ull;
