@@ -438,10 +438,11 @@ lct_status lct_adapter_plan(const int32_t *d_index, uint64_t tokens, uint64_t ad
  * adapter: what many requests' adapters add to y, the shared projection of
  * the same x.  x [tokens, k], y and out [tokens, n] are BF16 with rows ld_*
  * values apart; out may be y itself.  Rows that begin at 16-byte boundaries
- * are the fast case, others work.  The sums are float32, the narrow product is
- * carried to the second one with 16 bits, and out is rounded once.  d_xa, if
- * not NULL, gets x A_a^T [tokens, rank] in float32 (0 where an adapter has no
- * such rank) for lct_adapter_backward.  A wait that ran out on the device
+ * are the fast case; of others whole aligned 16-byte pieces are fetched, what
+ * lies before a row's first value among it.  The sums are float32, the narrow
+ * product is carried to the second one with 16 bits, and out is rounded once.
+ * d_xa, if not NULL, gets x A_a^T [tokens, rank] in float32 (0 where an adapter
+ * has no such rank) for lct_adapter_backward.  A wait that ran out on the device
  * latches LCT_ERR_TIMEOUT in the plan's status.  Errors: LCT_ERR_INVALID_ARG
  * (NULL or misaligned pointers, strides below the widths, a plan for another
  * number of adapters, an output that overlaps another operand),

@@ -1,7 +1,8 @@
 """Lossless BF16 tensor compression on GB300 (sm_103a): LCT's exponent-Huffman
 codec, the fused compressed SGD / SGD-with-momentum / AdamW steps, and the
 pieces built on them for training (saved activations kept compressed,
-a linear layer whose weight is decoded tile by tile).
+a linear layer whose weight is decoded tile by tile, low-rank adapters beside
+it, the norm and clipping of gradients).
 
 The work happens in ``liblct.so`` (CUDA kernels behind a C ABI, declared in
 ``include/lct.h``); ``binding`` is its thin ctypes binding, re-exported here:
@@ -12,8 +13,8 @@ The work happens in ``liblct.so`` (CUDA kernels behind a C ABI, declared in
                                             lct_adamw_step_fused, lct_compressed_size,
                                             CompressedTensor)
 
-``activations.compressed_activations`` and ``matmul.compressed_linear`` are
-imported from their modules.  The binding is loaded on first attribute access
+``activations.compressed_activations``, ``matmul.compressed_linear``, and what
+``adapters`` and ``grads`` hold are imported from their modules.  The binding is loaded on first attribute access
 and raises if the library is not built; nothing falls back to the CPU.
 """
 
