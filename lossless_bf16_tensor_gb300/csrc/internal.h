@@ -182,9 +182,9 @@ struct AdapterArgs {
     __nv_bfloat16 *da, *db;
     int64_t ld_in, ld_base, ld_out, ld_x;
     int32_t adapters, rank, rank16, k, n, nin, nout, tokens, rows;
-    bool al_a, al_b, al_in, al_base, al_out, al_x, al_db;
+    bool al_a, al_b, al_in, al_base, al_out, al_x, al_db;  // rows begin at 16-byte boundaries
     bool sparse;                                            // backward: more adapters than tokens
-    bool boxes_w;                                           // set by the launcher  // rows begin at 16-byte boundaries
+    bool boxes_w;                                           // the weights come as boxes: set by the launcher
 };
 struct PlanArgs {
     const int32_t *index;

@@ -245,6 +245,23 @@ def test_slices_of_one_buffer():
     assert torch.equal(x, c.x) and torch.equal(y, c.y)
 
 
+@pytest.mark.parametrize("t,n,r,k,m", [(300, 2, 64, 1001, 2047), (500, 3, 128, 513, 257), (260, 2, 33, 2050, 1026),
+                                       (20, 9, 7, 131, 129), (1500, 1, 16, 4097, 65), (400, 2, 100, 64, 1031)])
+def test_slices_and_in_place_at_odd_widths(t, n, r, k, m):
+    """Rows of x, y, dy and dx one after another in one buffer: pieces that hold the end of one and the start of the
+    next; the results in place."""
+    c = Case(t, n, r, k, m, seed=k)
+    buf = torch.cat([c.x, c.y, c.dy, c.dx], 1).contiguous()
+    x, y, dy, dx = buf.split([k, m, m, k], 1)
+    _, xa = adapter_apply(x, c.bank, c.plan, y, out=y, keep=True)
+    check_forward(c, y, xa)
+    assert torch.equal(x, c.x) and torch.equal(dy, c.dy) and torch.equal(dx, c.dx)
+    new, da, db = adapter_grads(dy, x, xa, c.bank, c.plan, dx, out=dx)
+    check_backward(c, (dx, da, db))
+    assert new is dx and torch.equal(x, c.x) and torch.equal(dy, c.dy)
+    check_forward(c, y)
+
+
 def test_in_place_and_more_dimensions():
     c = Case(60, 2, 16, 128, 192, seed=5)
     want, xa = adapter_apply(c.x, c.bank, c.plan, c.y, keep=True)
