@@ -2059,7 +2059,14 @@ uint32_t clusters_at_once(void (*kernel)(P...), uint32_t threads, uint32_t smem,
 // and a turn has a part that no cluster shortens (filling the ring, the
 // meetings), which measures like about 12 chunks: the size with the least
 // turns x (chunks of a turn + 12) is taken, a chunk of the second product
-// counting twice for what it writes.
+// counting twice for what it writes.  Clusters of 12 and 16, of which 8 and 7
+// fit, are for 4096 columns and more, ranks up to 64 and batches whose tiles all
+// fit at once, whatever the plan holds: 512 tokens of one adapter, rank 16, 8192
+// columns take 24.0 us by eight, 18.2 by 16.  Their meetings take longer, the
+// more so the higher the rank (500 tokens, rank 64, 1024 columns: 13.8 and 15.8
+// us; 128 tokens, rank 128, 4096 columns: 24.1 and 26.8), and a second turn
+// costs most (1000 tokens of two adapters, 1024 to 4096 columns: 16.5 us by
+// eight, 24.3 by 12).
 template <bool BACK, int RANK, bool FAST>
 cudaError_t launch_tokens_at(const AdapterArgs &args, cudaStream_t s)
 {
@@ -2076,7 +2083,7 @@ cudaError_t launch_tokens_at(const AdapterArgs &args, cudaStream_t s)
     }
     const auto kernel = dev::k_adapter<BACK, RANK, FAST>;
     constexpr uint32_t smem = dev::Tok<RANK, FAST>::kBytes;
-    const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (rc != cudaSuccess) return rc;
     const uint64_t n1 = (a.nin + 63) / 64, n2 = a.out ? (a.nout + 63) / 64 : 0;
     // an adapter's last tile is half full at a guess, and with few tokens an adapter it is the only one
@@ -2084,9 +2091,14 @@ cudaError_t launch_tokens_at(const AdapterArgs &args, cudaStream_t s)
     const uint64_t tiles = std::max(a.tokens / 128 + (busy + 1) / 2, busy + a.tokens / 256);
     uint64_t best = ~0ull;
     uint32_t c = 0, fit = 0;
-    for (uint32_t d = 1; d <= 8 && d <= std::max(n1, n2); ++d) {
+    const bool wide = RANK <= 64 && std::max(n1, n2) >= 64 && a.rows <= 152 / 12;
+    if (wide) {
+        rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (rc != cudaSuccess) return rc;
+    }
+    for (uint32_t d = 1; d <= (wide ? 16u : 8u) && d <= std::max(n1, n2); d += d < 8 ? 1 : 4) {
         const uint32_t f = clusters_at_once(kernel, dev::kTokThreads, smem, d);
-        if (!f) continue;
+        if (!f || (d > 8 && a.rows > static_cast<int32_t>(f))) continue;
         const uint64_t cost = (tiles + f - 1) / f * ((n1 + d - 1) / d + 2 * ((n2 + d - 1) / d) + 12);
         if (cost < best) best = cost, c = d, fit = f;
     }

@@ -179,6 +179,13 @@ def test_a_batch_of_a_few_adapters(t, n, r, k, m):
     both(Case(t, n, r, k, m, seed=t + r))
 
 
+@pytest.mark.parametrize("t,n,r,k,m", [(128, 1, 16, 4096, 4096), (300, 3, 64, 8192, 256), (33, 1, 5, 200, 4160),
+                                       (500, 1, 64, 4097, 8191), (700, 1, 33, 4096, 1000), (200, 2, 64, 64, 8192)])
+def test_wide_batches_of_few_tiles(t, n, r, k, m):
+    """One or a few tiles, which the largest clusters share."""
+    both(Case(t, n, r, k, m, seed=t + r))
+
+
 def test_ranks_of_their_own_and_unused_values_are_not_read():
     c = Case(400, 6, 40, 256, 320, ranks=[0, 1, 16, 17, 40, 100], seed=1)
     for i, u in enumerate((0, 1, 16, 17)):
