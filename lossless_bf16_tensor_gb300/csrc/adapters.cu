@@ -2050,7 +2050,10 @@ uint32_t clusters_at_once(void (*kernel)(P...), uint32_t threads, uint32_t smem,
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // a size that does not fit is no error of the caller's
+        return 0;
+    }
     return n > 0 ? static_cast<uint32_t>(n) : 0;
 }
 
@@ -2091,6 +2094,7 @@ cudaError_t launch_tokens_at(const AdapterArgs &args, cudaStream_t s)
     const uint64_t tiles = std::max(a.tokens / 128 + (busy + 1) / 2, busy + a.tokens / 256);
     uint64_t best = ~0ull;
     uint32_t c = 0, fit = 0;
+    // (more rows than the smaller of them has clusters: not asked)
     const bool wide = RANK <= 64 && std::max(n1, n2) >= 64 && a.rows <= 152 / 12;
     if (wide) {
         rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
