@@ -1577,7 +1577,12 @@ __global__ void __launch_bounds__(kGradAdThreads)
     const int c0 = (is_a ? blockIdx.y : blockIdx.y - blocks_x) * kGradCols;
     // more adapters than tokens: the gradients are zero already, and only adapters with tokens get blocks
     const int a = g.sparse ? busy_adapter(g, blockIdx.z) : blockIdx.z;
-    if (a < 0) return;
+    // every block waits for the tokens' kernel, with work or without: what follows in the stream is ordered behind this
+    // grid, and a grid in which nobody waits may end before the one it depends on
+    if (a < 0) {
+        pdl_wait();
+        return;
+    }
     const int first = max(0, min(g.starts[a], g.tokens)), last = max(first, min(g.starts[a + 1], g.tokens));
     const int used = last > first ? used_rank(g, a) : 0, r16 = (used + 15) & ~15;
     const int cols = is_a ? g.k : g.n;
@@ -1789,6 +1794,8 @@ __global__ void __launch_bounds__(kGradAdThreads)
             __syncthreads();
         }
         tc_before();
+    } else {
+        pdl_wait();
     }
     __syncwarp();
     cluster_sync();
