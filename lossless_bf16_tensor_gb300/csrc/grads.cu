@@ -261,8 +261,11 @@ __device__ __forceinline__ Root root_of(double total)
 }
 __device__ __forceinline__ float norm_of(const Root &r) { return r.exp > 127 ? INFINITY : ldexpf(r.root, r.exp); }
 
-// g' = (g * pre) * mul.  A norm above float's range still clips, and a factor
-// too small for a normal float is split in two.
+// g' = (g * pre) * mul.  pre is a power of two, 1 unless the factor lies below
+// float's normal range: then mul is the smallest normal power of two times the
+// factor's fraction, so that no bit of the factor is lost and only the last
+// product rounds (g * pre is exact wherever that product is not zero).  A
+// factor below 2^-274, whose results lie below 2^-146, gives zeros.
 struct Factor {
     float pre, mul;
     bool one;
@@ -271,15 +274,20 @@ struct Factor {
 __device__ __forceinline__ Factor factor_of(const Root &r, float max_norm)
 {
     Factor f = {1.0f, 0.0f, false};
-    if (r.exp > 100) {  // 1e-6 beside 2^100 is nothing; the factor is max_norm / root * 2^-exp
-        const float c = max_norm / r.root;
-        f.pre = 0x1p-64f;
-        f.mul = ldexpf(c, 64 - r.exp);
-    } else {
-        const float c = max_norm / (norm_of(r) + 1e-6f);
-        f.mul = c > 1.0f ? 1.0f : c;  // NaN stays
+    const float n = norm_of(r) + 1e-6f;
+    const float c = max_norm / n;
+    // a norm above float's range (r.exp > 127, beside which 1e-6 is nothing) lies above every max_norm
+    if (r.exp <= 127 && !(c < 0x1p-126f && n < INFINITY)) {
+        f.mul = c > 1.0f ? 1.0f : c;  // NaN stays; an infinite norm gives 0
         f.one = f.mul == 1.0f;
+        return f;
     }
+    int en = r.exp, em, ec;
+    const float root = r.exp > 127 ? r.root : frexpf(n, &en);
+    const float m = frexpf(frexpf(max_norm, &em) / root, &ec);
+    const int e = ec + em - en;  // the factor is m * 2^e, m in [0.5, 1)
+    f.pre = e < -125 ? ldexpf(1.0f, e + 125) : 1.0f;
+    f.mul = ldexpf(m, max(e, -125));
     return f;
 }
 
