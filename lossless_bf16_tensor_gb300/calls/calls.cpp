@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <cstdint>
+#include <optional>
 #include <vector>
 
 #include <ATen/core/Tensor.h>
@@ -60,46 +61,52 @@ void *stream_of(int device) { return c10::cuda::getCurrentCUDAStream(static_cast
 
 // ---------------------------------------------------------------- gradients
 
+// A reference.
+struct Held {
+    PyObject *o;
+    explicit Held(PyObject *p) : o(p) {}
+    Held(const Held &) = delete;
+    Held &operator=(const Held &) = delete;
+    ~Held() { Py_XDECREF(o); }
+};
+
+// A list's tensors.  They are held until the call has been enqueued: an iterable
+// may make its tensors as it goes, and nobody else holds those; let go of
+// earlier, their memory could become the call's own scratch.
 struct Grads {
+    Held seq;
     std::vector<const void *> ptr;
     std::vector<uint64_t> n;
     std::vector<int32_t> dtype;
     int device = -1;
+
+    explicit Grads(PyObject *list);
 };
 
-Grads grads_of(PyObject *list)
+Grads::Grads(PyObject *list) : seq(PySequence_Fast(list, "expected a sequence of tensors"))
 {
-    Grads g;
-    PyObject *seq = PySequence_Fast(list, "expected a sequence of tensors");
-    if (!seq) throw Raised{};
-    try {
-        const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq);
-        g.ptr.reserve(count);
-        g.n.reserve(count);
-        g.dtype.reserve(count);
-        for (Py_ssize_t i = 0; i < count; ++i) {
-            const at::Tensor &t = tensor(PySequence_Fast_GET_ITEM(seq, i), "expected tensors");
-            need(t.is_cuda() && t.is_contiguous(), "expected contiguous CUDA tensors");
-            need(g.device < 0 || t.get_device() == g.device, "expected tensors on one device");
-            g.device = t.get_device();
-            if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)
-                check(LCT_ERR_UNSUPPORTED, "gradients other than BF16 and float32");
-            g.dtype.push_back(t.scalar_type() == at::kFloat ? LCT_DTYPE_F32 : LCT_DTYPE_BF16);
-            g.ptr.push_back(t.data_ptr());
-            g.n.push_back(static_cast<uint64_t>(t.numel()));
-        }
-    } catch (...) {
-        Py_DECREF(seq);
-        throw;
+    if (!seq.o) throw Raised{};
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq.o);
+    ptr.reserve(count);
+    n.reserve(count);
+    dtype.reserve(count);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        const at::Tensor &t = tensor(PySequence_Fast_GET_ITEM(seq.o, i), "expected tensors");
+        need(t.is_cuda() && t.is_contiguous(), "expected contiguous CUDA tensors");
+        need(device < 0 || t.get_device() == device, "expected tensors on one device");
+        device = t.get_device();
+        if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)
+            check(LCT_ERR_UNSUPPORTED, "gradients other than BF16 and float32");
+        dtype.push_back(t.scalar_type() == at::kFloat ? LCT_DTYPE_F32 : LCT_DTYPE_BF16);
+        ptr.push_back(t.data_ptr());
+        n.push_back(static_cast<uint64_t>(t.numel()));
     }
-    Py_DECREF(seq);
-    return g;
 }
 
 // (grads) -> norm
 PyObject *grad_norm(PyObject *const *a)
 {
-    Grads g = grads_of(a[0]);
+    Grads g(a[0]);
     if (g.device < 0) g.device = c10::cuda::current_device();
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(g.device));
     at::Tensor norm = make({}, at::kFloat, g.device), work = make({LCT_GRAD_WORK_BYTES}, at::kByte, g.device);
@@ -112,16 +119,16 @@ PyObject *grad_norm(PyObject *const *a)
 // (grads, max_norm, out or None) -> norm
 PyObject *clip_grads(PyObject *const *a)
 {
-    Grads g = grads_of(a[0]);
+    Grads g(a[0]);
     const double max_norm = PyFloat_AsDouble(a[1]);
     if (PyErr_Occurred()) throw Raised{};
-    Grads other;
+    std::optional<Grads> other;
     if (a[2] != Py_None) {
-        other = grads_of(a[2]);
-        need(other.n == g.n && other.dtype == g.dtype && other.device == g.device,
+        other.emplace(a[2]);
+        need(other->n == g.n && other->dtype == g.dtype && other->device == g.device,
              "out must match the gradients' sizes, types and device");
     }
-    const Grads &out = a[2] == Py_None ? g : other;
+    const Grads &out = other ? *other : g;
     if (g.device < 0) g.device = c10::cuda::current_device();
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(g.device));
     at::Tensor norm = make({}, at::kFloat, g.device), work = make({LCT_GRAD_WORK_BYTES}, at::kByte, g.device);
