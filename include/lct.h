@@ -366,8 +366,9 @@ typedef enum { LCT_DTYPE_BF16 = 0, LCT_DTYPE_F32 = 1 } lct_dtype;
  * square overflows or underflows, and only a norm above float's range is
  * returned as infinity.  A NaN or an infinity among the values gives NaN or
  * infinity.  count = 0 gives 0.
- * Errors: LCT_ERR_INVALID_ARG (NULL or misaligned pointers, n > 2^40),
- * LCT_ERR_UNSUPPORTED (another dtype), LCT_ERR_CUDA. */
+ * Errors: LCT_ERR_INVALID_ARG (NULL or misaligned pointers, n > 2^40, d_norm
+ * or d_work over one another or over a gradient), LCT_ERR_UNSUPPORTED
+ * (another dtype), LCT_ERR_CUDA. */
 lct_status lct_grad_norm(const void *const *d_g, const uint64_t *n, const int32_t *dtype, uint64_t count,
                          float *d_norm, void *d_work, void *stream);
 
@@ -379,7 +380,8 @@ lct_status lct_grad_norm(const void *const *d_g, const uint64_t *n, const int32_
  * where the norm is NaN, and 0 where it is infinite (an infinity times 0 is
  * NaN, a finite value 0): read *d_norm before a step to skip it.
  * Errors: as lct_grad_norm, and LCT_ERR_INVALID_ARG for max_norm that is not
- * positive and finite, or for overlapping tensors. */
+ * positive and finite, or for overlapping tensors (d_norm and d_work among
+ * them). */
 lct_status lct_grad_clip(const void *const *d_g, void *const *d_out, const uint64_t *n, const int32_t *dtype,
                          uint64_t count, float max_norm, float *d_norm, void *d_work, void *stream);
 

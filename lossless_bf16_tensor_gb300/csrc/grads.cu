@@ -610,10 +610,18 @@ bool grads_apart(const GradArgs &a)
     return true;
 }
 
+// Whether n bytes at p and m bytes at q share none.
+bool apart(const void *p, uint64_t n, const void *q, uint64_t m)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    return x + n <= y || y + m <= x;
+}
+
 lct_status check_grads(GradArgs *a, bool clip)
 {
     if (!a->norm || (reinterpret_cast<uintptr_t>(a->norm) & 3u)) return LCT_ERR_INVALID_ARG;
     if (!a->part || (reinterpret_cast<uintptr_t>(a->part) & 15u)) return LCT_ERR_INVALID_ARG;
+    if (!apart(a->norm, 4, a->part, LCT_GRAD_WORK_BYTES)) return LCT_ERR_INVALID_ARG;
     if (a->count && (!a->src || !a->n || !a->dtype || (clip && !a->dst))) return LCT_ERR_INVALID_ARG;
     for (uint64_t i = 0; i < a->count; ++i) {
         if (a->dtype[i] != LCT_DTYPE_BF16 && a->dtype[i] != LCT_DTYPE_F32) return LCT_ERR_UNSUPPORTED;
@@ -622,6 +630,11 @@ lct_status check_grads(GradArgs *a, bool clip)
         const uintptr_t mask = a->dtype[i] == LCT_DTYPE_F32 ? 3u : 1u;
         if (!a->src[i] || (reinterpret_cast<uintptr_t>(a->src[i]) & mask)) return LCT_ERR_INVALID_ARG;
         if (clip && (!a->dst[i] || (reinterpret_cast<uintptr_t>(a->dst[i]) & mask))) return LCT_ERR_INVALID_ARG;
+        // the norm and the scratch are written while gradients are still read
+        const uint64_t bytes = a->n[i] * (mask + 1);
+        for (const void *p : {a->src[i], clip ? static_cast<const void *>(a->dst[i]) : a->src[i]})
+            if (!apart(p, bytes, a->norm, 4) || !apart(p, bytes, a->part, LCT_GRAD_WORK_BYTES))
+                return LCT_ERR_INVALID_ARG;
     }
     return LCT_OK;
 }
