@@ -954,8 +954,9 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                         for (int j = 0; j < 8; ++j)
                             if (p * 8 + j < w.used) k[j] = x[j];
                     }
+                    // the ranks from `used` to the next 16 are products with zeros: zero, whatever In holds
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] *= scale;
+                    for (int j = 0; j < 8; ++j) x[j] = p * 8 + j < w.used ? x[j] * scale : 0.0f;
                     uint4 hi, lo;
                     split8(x, hi, lo);
                     const uint32_t to = v_at + (p >> 3) * T::kVAtom + swz(row, p & 7);
@@ -1412,10 +1413,13 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
                     const float k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j)  // zero where the adapter has no such rank
-                        if (c + j < g.rank) g.keep[static_cast<int64_t>(tok[first + r]) * g.rank + c + j] = k[j];
+                        if (c + j < g.rank)
+                            g.keep[static_cast<int64_t>(tok[first + r]) * g.rank + c + j] = c + j < used ? k[j] : 0.0f;
                 }
             }
-            v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+            // ranks from `used` on are products with zeros: zero, whatever In holds
+            v.x = c < used ? v.x * scale : 0.0f, v.y = c + 1 < used ? v.y * scale : 0.0f;
+            v.z = c + 2 < used ? v.z * scale : 0.0f, v.w = c + 3 < used ? v.w * scale : 0.0f;
             const uint2 hi = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
             const uint2 lo = make_uint2(pack2(rest(v.x, hi.x << 16), rest(v.y, hi.x & 0xFFFF0000u)),
                                         pack2(rest(v.z, hi.y << 16), rest(v.w, hi.y & 0xFFFF0000u)));
