@@ -1504,11 +1504,12 @@ constexpr int kGradCols = 256, kGradTokens = 64;
 constexpr int kGradLoadWarps = 8;  // which write the results at the end
 constexpr int kGradMmaWarp = kGradLoadWarps, kGradBoxWarp = kGradMmaWarp + 1;
 constexpr int kGradAdThreads = 32 * (kGradBoxWarp + 1);
-constexpr uint32_t kGradTmemCols = 256;
 
 template <int RANK, int STAGES, bool FAST>
 struct Grad {
     static constexpr int kAtoms = RANK / 64;
+    // V's hi and lo parts have sums of their own, in lanes of their own or, above R = 64, in columns of their own
+    static constexpr uint32_t kTmemCols = RANK <= 64 ? 256 : 512;
     // two load groups take slots in turn, and slots come free in order: of two or more, a group that waits for a
     // slot's last chunk has seen the one before it go
     static_assert(STAGES >= 2, "");
@@ -1520,6 +1521,9 @@ struct Grad {
     static constexpr uint32_t kRing = STAGES * (kSlot + kExtra);
     static constexpr uint32_t kBytes = (kRing > kSums ? kRing : kSums) + 1024;
 };
+// Blocks that take an SM's whole TMEM share it with no block that takes TMEM too (1 KB of each block's shared memory is
+// the system's), so that none waits for another's.
+static_assert(Grad<64, 2, true>::kBytes + Grad<128, 2, true>::kBytes + 2048 >= 228 * 1024, "");
 
 // The tokens of a chunk of 64, two a lane, and whether they are two runs of 32
 // consecutive ones.
@@ -1598,7 +1602,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
     uint32_t tmem = 0;
     Waiter waiter;
     if (used) {
-        if (warp == 0) tmem_alloc(&tmem_at, kGradTmemCols);
+        if (warp == 0) tmem_alloc(&tmem_at, T::kTmemCols);
         if (FAST && warp == kGradBoxWarp && lane < 2) fetch_map(is_a ? (lane ? &maps.d : &maps.x) : (lane ? &maps.v : &maps.dy));
         if (threadIdx.x == 0) {
             for (int i = 0; i < STAGES; ++i) {
@@ -1764,7 +1768,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
 #pragma unroll
                     for (int k = 0; k < kGradTokens / 16; ++k) {
                         mma(tmem, v + k * 128, x + k * 128, word, i > 0 || k > 0);
-                        if (RANK > 64) mma(tmem, v + (T::kV >> 4) + k * 128, x + k * 128, word, true);
+                        if (RANK > 64) mma(tmem + 256, v + (T::kV >> 4) + k * 128, x + k * 128, word, i > 0 || k > 0);
                     }
                     mma_commit(&freed[s]);
                     if (i == n - 1) mma_commit(&all_done);
@@ -1775,7 +1779,9 @@ __global__ void __launch_bounds__(kGradAdThreads)
         }
         tc_after();
         __syncthreads();
-        // The block's sums, [rank][column]: lanes hold ranks, those of the upper half the lo part's (added last).
+        // The block's sums, [rank][column]: lanes hold ranks, up to R = 64 those of the upper half the lo part's (which
+        // come first).  The two are added where hi's sum is finite: beside an infinity in x or dy, hi and lo of opposite
+        // signs would give NaN.
         const int quarter = warp & 3, half = warp >> 2;
         const bool lo = RANK <= 64 && quarter >= 2;
         const int r = (RANK <= 64 ? quarter & 1 : quarter) * 32 + lane;
@@ -1784,15 +1790,19 @@ __global__ void __launch_bounds__(kGradAdThreads)
         for (int turn = 0; turn < (RANK <= 64 ? 2 : 1); ++turn) {
             if (warp < kGradLoadWarps && lo == (RANK <= 64 && turn == 0) && r - lane < r16)
                 for (int c = 0; c < end; c += 8) {
-                    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                     if (n > 0) {
                         tmem_load8(lanes + c, x);
+                        if (RANK > 64) tmem_load8(lanes + 256 + c, y);
                         tmem_wait();
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         float *to = sums + r * (kGradCols + 1) + half * 128 + c + j;
-                        *to = RANK <= 64 && turn ? *to + x[j] : x[j];
+                        if (RANK <= 64)
+                            *to = turn == 1 && isfinite(x[j]) ? *to + x[j] : x[j];
+                        else
+                            *to = isfinite(x[j]) ? x[j] + y[j] : x[j];
                     }
                 }
             __syncthreads();
@@ -1836,7 +1846,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
     if (waiter.dead) fail(g, LCT_ERR_TIMEOUT);
     __syncwarp();
     cluster_sync();
-    if (used && warp == 0) tmem_free(tmem, kGradTmemCols);
+    if (used && warp == 0) tmem_free(tmem, T::kTmemCols);
 }
 
 // -------------------------------------------------------------- the plan

@@ -73,3 +73,26 @@ def test_an_infinite_scale():
         out = adapter_apply(c.x.abs_(), c.bank, c.plan, c.y)
         same(out, c.exact()[0], c.k + 2 * c.r)
         assert bool(out[c.index == 0].isinf().all()) and bool(out[c.index != 0].isfinite().all())
+
+
+@pytest.mark.parametrize("k,m", [(256, 136), (201, 131)])
+@pytest.mark.parametrize("r,ranks", RANKS, ids=[str(r) if q is None else "own" for r, q in RANKS])
+@pytest.mark.parametrize("t,n", SHAPES)
+def test_infinities_against_finite_values_in_the_banks_gradients(t, n, r, ranks, k, m):
+    """da where x is infinite, db where dy is: the finite factor is carried in two parts, which may have opposite
+    signs.  (One adapter has both kinds of tokens where the batch is large enough.)"""
+    c = case(t, n, r, k, m, ranks and ranks[:n], seed=r + 1)
+    _, xa = adapter_apply(c.x, c.bank, c.plan, c.y, keep=True)
+    rows = (c.index >= 0).nonzero()[:, 0]
+    c.x[rows[0], 3], c.x[rows[-1], k - 1] = math.inf, -math.inf
+    c.dy[rows[len(rows) // 2], 11] = math.inf
+    _, da, db = adapter_grads(c.dy, c.x, xa, c.bank, c.plan, c.dx)
+    want = c.exact(back=True)
+    same(da, want[1], c.m + 2 * c.t)
+    # x's infinities came after the forward pass: db is that of the x of then
+    c.x[rows[0], 3], c.x[rows[-1], k - 1] = 0.5, 0.25
+    _, xa = adapter_apply(c.x, c.bank, c.plan, c.y, keep=True)
+    _, da, db = adapter_grads(c.dy, c.x, xa, c.bank, c.plan, c.dx)
+    want = c.exact(back=True)
+    same(da, want[1], c.m + 2 * c.t)
+    same(db, want[2], c.k + 2 * c.t)
