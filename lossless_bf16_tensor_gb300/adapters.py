@@ -13,6 +13,7 @@ current stream, and nothing synchronises.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 from .calls import calls
@@ -84,6 +85,7 @@ class _AdapterLinear(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable  # the gradients' own gradients are not there: asking for them raises
     def backward(ctx, dy):
         x, xa = ctx.saved_tensors
         bank, plan, w, cb = ctx.rest
@@ -96,7 +98,7 @@ class _AdapterLinear(torch.autograd.Function):
 def adapter_linear(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_codebook, bank: AdapterBank,
                    plan: AdapterPlan) -> torch.Tensor:
     """y = x W^T + s_a (x A_a^T) B_a^T for a compressed frozen W [n, k] and each
-    token's own adapter; x [..., k] BF16 on CUDA.  Differentiable in x and in
+    token's own adapter; x [..., k] BF16 on CUDA.  Differentiable (once) in x and in
     the bank's a and b (leaves such as ``torch.nn.Parameter``); the weight is
     decoded again for the gradient of x.  What it saves for backward goes
     through ``compressed_activations`` like any other saved tensor."""
