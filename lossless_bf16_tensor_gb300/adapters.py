@@ -75,23 +75,39 @@ def adapter_grads(dy: torch.Tensor, x: torch.Tensor, xa: torch.Tensor, bank: Ada
                                dx, out)
 
 
+_OPERANDS = ("the bank's a", "the bank's b", "the bank's scale", "the bank's ranks", "the plan's order",
+             "the plan's starts", "the plan's tiles")
+
+
+def _versions(tensors):
+    return [None if t is None or t.is_inference() else t._version for t in tensors]
+
+
 class _AdapterLinear(torch.autograd.Function):
+    # The bank and the plan are long-lived operands, not activations: they stay out of save_for_backward, whose hooks
+    # (compressed_activations) would copy a plain tensor and skip the check of a parameter's version.  Backward makes
+    # that check itself.
     @staticmethod
     def forward(ctx, x, a, b, bank, plan, w, cb):
         y = compressed_linear(x, w, cb, bank.n, bank.k)
-        out, xa = adapter_apply(x, bank, plan, y, out=y, keep=True)
+        operands = (a, b, bank.scale, bank.ranks, plan.order, plan.starts, plan.tiles)
+        out, xa = calls.adapter_apply(*operands, x, y, y, True)
         ctx.save_for_backward(x, xa)
-        ctx.rest = (bank, plan, w, cb)
+        ctx.rest = (operands, _versions(operands), w, cb, bank.n, bank.k)
         return out
 
     @staticmethod
     @once_differentiable  # the gradients' own gradients are not there: asking for them raises
     def backward(ctx, dy):
         x, xa = ctx.saved_tensors
-        bank, plan, w, cb = ctx.rest
+        operands, versions, w, cb, n, k = ctx.rest
+        for name, then, now in zip(_OPERANDS, versions, _versions(operands)):
+            if then != now:
+                raise RuntimeError("adapter_linear: %s was modified in place between forward and backward "
+                                   "(version %s, now %s)" % (name, then, now))
         dy = dy.contiguous()
-        dx = compressed_linear_input_grad(dy, w, cb, bank.n, bank.k) if ctx.needs_input_grad[0] else None
-        dx, da, db = adapter_grads(dy, x, xa, bank, plan, dx, out=dx)
+        dx = compressed_linear_input_grad(dy, w, cb, n, k) if ctx.needs_input_grad[0] else None
+        dx, da, db = calls.adapter_grads(*operands, dy, x, xa, dx, dx)
         return dx, da, db, None, None, None, None
 
 
@@ -101,7 +117,9 @@ def adapter_linear(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_codebook, b
     token's own adapter; x [..., k] BF16 on CUDA.  Differentiable (once) in x and in
     the bank's a and b (leaves such as ``torch.nn.Parameter``); the weight is
     decoded again for the gradient of x.  What it saves for backward goes
-    through ``compressed_activations`` like any other saved tensor."""
+    through ``compressed_activations`` like any other saved tensor; the bank
+    and the plan are used as they are, and backward raises if one of them was
+    modified in place since."""
     if torch.is_grad_enabled() and (x.requires_grad or bank.a.requires_grad or bank.b.requires_grad):
         return _AdapterLinear.apply(x, bank.a, bank.b, bank, plan, w, cb)
     y = compressed_linear(x, w, cb, bank.n, bank.k)

@@ -3,6 +3,8 @@ of giving a gradient that is wrong or not there."""
 import pytest
 import torch
 
+from lossless_bf16_tensor_gb300 import binding as B
+from lossless_bf16_tensor_gb300.activations import compressed_activations
 from lossless_bf16_tensor_gb300.adapters import AdapterBank, adapter_linear
 from test_gpu_adapters import Case, compressed_weight
 
@@ -30,3 +32,55 @@ def test_second_derivatives_raise(weight):
     (gx,) = torch.autograd.grad(y.float().square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError):
         gx.float().square().sum().backward()
+
+
+@pytest.mark.parametrize("hooks", [False, True], ids=["plain", "compressed"])
+@pytest.mark.parametrize("what", ["a", "b", "scale", "ranks", "order", "starts", "tiles"])
+def test_operands_modified_before_backward_raise(weight, what, hooks):
+    w, cb, _ = weight
+    c, x, bank = leaves(seed=1, t=600)
+    bank = AdapterBank(bank.a, bank.b, bank.scale, torch.full((3,), 12, dtype=torch.int32, device="cuda"))
+    saved = compressed_activations(B.lct_codebook_build("gaussian", 1.0))
+    if hooks:
+        with saved:
+            y = adapter_linear(x * 1.0, w, cb, bank, c.plan)
+    else:
+        y = adapter_linear(x * 1.0, w, cb, bank, c.plan)
+    loss = y.float().square().sum()
+    loss.backward(retain_graph=True)
+    first = [v.grad.clone() for v in (x, bank.a, bank.b)]
+    x.grad = bank.a.grad = bank.b.grad = None
+    loss.backward(retain_graph=True)  # nothing was modified: the same again
+    assert all(torch.equal(v.grad, g) for v, g in zip((x, bank.a, bank.b), first))
+    operand = getattr(bank, what, None)
+    with torch.no_grad():
+        (operand if operand is not None else getattr(c.plan, what)).add_(0)
+    with pytest.raises(RuntimeError, match=what):
+        loss.backward()
+
+
+def test_a_bank_with_other_tensors_before_backward(weight):
+    """A bank that is given other tensors afterwards changes nothing for a forward pass that was made."""
+    w, cb, _ = weight
+    c, x, bank = leaves(seed=2)
+    adapter_linear(x, w, cb, bank, c.plan).float().square().sum().backward()
+    want = x.grad.clone(), bank.a.grad.clone()
+    x.grad = bank.a.grad = None
+    loss = adapter_linear(x, w, cb, bank, c.plan).float().square().sum()
+    a, bank.a = bank.a, torch.nn.Parameter(torch.zeros_like(bank.a))
+    loss.backward()
+    assert torch.equal(x.grad, want[0]) and torch.equal(a.grad, want[1]) and bank.a.grad is None
+
+
+def test_operands_made_in_inference_mode(weight):
+    """They have no versions; a frozen bank of such tensors still gives x its gradient."""
+    w, cb, _ = weight
+    c = Case(200, 3, 16, K, N, seed=3)
+    with torch.inference_mode():
+        frozen = AdapterBank(c.a.clone(), c.b.clone(), c.scale.clone())
+    grads = []
+    for bank in (c.bank, frozen):
+        x = c.x.clone().requires_grad_(True)
+        adapter_linear(x, w, cb, bank, c.plan).float().square().sum().backward()
+        grads.append(x.grad)
+    assert torch.equal(*grads)
