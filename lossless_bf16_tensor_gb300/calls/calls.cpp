@@ -57,6 +57,13 @@ at::Tensor make(at::IntArrayRef shape, at::ScalarType type, int device)
     return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, device));
 }
 
+// A call wrote into a caller's tensor: autograd's check of tensors that it saved has to notice.  (Tensors made in
+// inference mode have no version.)
+void wrote(const at::Tensor &t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 void *stream_of(int device) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream(); }
 
 // ---------------------------------------------------------------- gradients
@@ -136,6 +143,8 @@ PyObject *clip_grads(PyObject *const *a)
                         g.n.data(), g.dtype.data(), g.ptr.size(), static_cast<float>(max_norm),
                         static_cast<float *>(norm.data_ptr()), work.data_ptr(), stream_of(g.device)),
           "lct_grad_clip");
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(out.seq.o); ++i)
+        wrote(tensor(PySequence_Fast_GET_ITEM(out.seq.o, i), "expected tensors"));
     return THPVariable_Wrap(norm);
 }
 
@@ -314,6 +323,7 @@ PyObject *adapter_apply(PyObject *const *a)
     check(lct_adapter_forward(&bank, &plan, xr.p, xr.ld, yr.p, yr.ld, outr.p, outr.ld,
                               keep ? static_cast<float *>(xa.data_ptr()) : nullptr, stream_of(device)),
           "lct_adapter_forward");
+    if (a[9] != Py_None) wrote(out);
     PyObject *res = a[9] == Py_None ? THPVariable_Wrap(fresh) : Py_NewRef(a[9]);
     return keep ? tuple_of({res, THPVariable_Wrap(xa)}) : res;
 }
@@ -351,6 +361,7 @@ PyObject *adapter_grads(PyObject *const *a)
                                dx.ld, out.p, out.ld, static_cast<uint16_t *>(da.data_ptr()),
                                static_cast<uint16_t *>(db.data_ptr()), work.data_ptr(), stream_of(device)),
           "lct_adapter_backward");
+    if (wants && !makes) wrote(tensor(a[11], "out must be a tensor or None"));
     PyObject *first = !wants ? Py_NewRef(Py_None) : makes ? THPVariable_Wrap(fresh) : Py_NewRef(a[11]);
     return tuple_of({first, THPVariable_Wrap(da), THPVariable_Wrap(db)});
 }

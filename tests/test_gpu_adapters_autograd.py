@@ -5,7 +5,8 @@ import torch
 
 from lossless_bf16_tensor_gb300 import binding as B
 from lossless_bf16_tensor_gb300.activations import compressed_activations
-from lossless_bf16_tensor_gb300.adapters import AdapterBank, adapter_linear
+from lossless_bf16_tensor_gb300.adapters import AdapterBank, adapter_apply, adapter_grads, adapter_linear
+from lossless_bf16_tensor_gb300.grads import clip_grads, grad_norm
 from test_gpu_adapters import Case, compressed_weight
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +85,57 @@ def test_operands_made_in_inference_mode(weight):
         adapter_linear(x, w, cb, bank, c.plan).float().square().sum().backward()
         grads.append(x.grad)
     assert torch.equal(*grads)
+
+
+def test_what_is_written_in_place_gets_another_version():
+    c = Case(50, 2, 8, 64, 72, seed=4)
+    y, dx = c.y.clone(), c.dx.clone()
+    _, xa = adapter_apply(c.x, c.bank, c.plan, y, out=y, keep=True)
+    adapter_grads(c.dy, c.x, xa, c.bank, c.plan, dx, out=dx)
+    assert (y._version, dx._version) == (1, 1)
+    gs = [v.clone() for v in (c.x, c.y)]
+    out = [torch.empty_like(g) for g in gs]
+    clip_grads(gs, 1.0, out=out)
+    assert [g._version for g in gs] == [0, 0] and [o._version for o in out] == [1, 1]
+    clip_grads(gs, 1.0)
+    assert [g._version for g in gs] == [1, 1]
+    flat = torch.zeros(100, device="cuda")
+    clip_grads([flat[:40], flat[40:]], 1.0)  # views share their base's version
+    assert flat._version == 2
+    grad_norm(gs)
+    adapter_grads(c.dy, c.x, xa, c.bank, c.plan, dx)
+    assert [v._version for v in (*gs, c.x, c.y, c.dy, dx, xa, c.a, c.b)] == [1, 1, 0, 0, 0, 1, 0, 0, 0]
+
+
+def test_a_saved_tensor_that_is_written_over_is_noticed():
+    c = Case(50, 2, 8, 64, 72, seed=5)
+
+    def loss(v):
+        v = v.clone().requires_grad_(True) * 1.0
+        return v, v.square().sum()
+
+    for write in (lambda v: adapter_apply(c.x, c.bank, c.plan, c.y, out=v),
+                  lambda v: adapter_apply(c.x, c.bank, c.plan, v, out=v),
+                  lambda v: clip_grads([v], 1.0)):
+        v, s = loss(c.y)
+        with torch.no_grad():
+            write(v)
+        with pytest.raises(RuntimeError):
+            s.backward()
+
+
+def test_tensors_made_in_inference_mode_are_written():
+    c = Case(50, 2, 8, 64, 72, seed=6)
+    want = adapter_apply(c.x, c.bank, c.plan, c.y)
+    with torch.inference_mode():
+        y, g = c.y.clone(), c.dy.clone()
+        adapter_apply(c.x, c.bank, c.plan, y, out=y)
+    assert torch.equal(y, want)
+    z = c.y.clone()
+    with torch.inference_mode():
+        adapter_apply(c.x, c.bank, c.plan, z, out=z)
+    assert torch.equal(z, want)
+    with torch.no_grad():
+        clip_grads([g], 1e-3)
+        adapter_apply(c.x, c.bank, c.plan, y, out=y)
+    assert abs(float(g.double().norm()) - 1e-3) < 1e-5
