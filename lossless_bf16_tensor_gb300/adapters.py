@@ -60,7 +60,9 @@ def adapter_apply(x: torch.Tensor, bank: AdapterBank, plan: AdapterPlan, y: torc
     """out = y + s_a (x A_a^T) B_a^T for every token (out = y for tokens without
     an adapter); x [..., k], y and out [..., n], BF16, rows at any stride.  out
     may be y itself; by default it is a new tensor.  With `keep`, returns (out,
-    xa): xa = x A_a^T, float32 [tokens, R], is what ``adapter_grads`` needs."""
+    xa): xa = x A_a^T, float32 [tokens, R], is what ``adapter_grads`` needs.
+    Autograd does not see this call: it raises where an operand requires a
+    gradient and gradients are enabled (``adapter_linear`` gives them)."""
     return calls.adapter_apply(bank.a, bank.b, bank.scale, bank.ranks, plan.order, plan.starts, plan.tiles, x, y, out,
                                bool(keep))
 
@@ -120,6 +122,8 @@ def adapter_linear(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_codebook, b
     through ``compressed_activations`` like any other saved tensor; the bank
     and the plan are used as they are, and backward raises if one of them was
     modified in place since."""
+    if torch.is_grad_enabled() and bank.scale.requires_grad:
+        raise RuntimeError("adapter_linear gives no gradient for the bank's scale, but it requires one")
     if torch.is_grad_enabled() and (x.requires_grad or bank.a.requires_grad or bank.b.requires_grad):
         return _AdapterLinear.apply(x, bank.a, bank.b, bank, plan, w, cb)
     y = compressed_linear(x, w, cb, bank.n, bank.k)

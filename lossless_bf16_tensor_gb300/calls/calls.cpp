@@ -12,6 +12,7 @@
 #include <vector>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -318,6 +319,13 @@ PyObject *adapter_apply(PyObject *const *a)
     if (a[9] == Py_None) fresh = make(y.sizes(), at::kBFloat16, device);
     const at::Tensor &out = a[9] == Py_None ? fresh : tensor(a[9], "out must be a tensor or None");
     const Rows outr = rows_of(out, bank.n, plan.tokens, device, "out");
+    if (at::GradMode::is_enabled())
+        for (const at::Tensor *t : {&x, &y, &out, &tensor(a[0], "a"), &tensor(a[1], "b"), &tensor(a[2], "scale")})
+            if (t->requires_grad()) {
+                PyErr_SetString(PyExc_RuntimeError, "adapter_apply gives no gradients, but an operand requires one: use "
+                                                    "adapter_linear, or call it under torch.no_grad()");
+                throw Raised{};
+            }
     at::Tensor xa;
     if (keep) xa = make({static_cast<int64_t>(plan.tokens), static_cast<int64_t>(bank.rank)}, at::kFloat, device);
     check(lct_adapter_forward(&bank, &plan, xr.p, xr.ld, yr.p, yr.ld, outr.p, outr.ld,

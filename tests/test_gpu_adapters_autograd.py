@@ -139,3 +139,33 @@ def test_tensors_made_in_inference_mode_are_written():
         clip_grads([g], 1e-3)
         adapter_apply(c.x, c.bank, c.plan, y, out=y)
     assert abs(float(g.double().norm()) - 1e-3) < 1e-5
+
+
+def test_gradients_that_are_not_there_raise(weight):
+    w, cb, _ = weight
+    c = Case(50, 2, 8, K, N, seed=7)
+    want = adapter_apply(c.x, c.bank, c.plan, c.y)
+
+    def grad(v):
+        return v.clone().requires_grad_(True)
+
+    ok = dict(x=c.x, bank=c.bank, plan=c.plan, y=c.y)
+    for kw in (dict(x=grad(c.x)), dict(y=grad(c.y)), dict(out=grad(c.y)),
+               dict(bank=AdapterBank(torch.nn.Parameter(c.a), c.b, c.scale)),
+               dict(bank=AdapterBank(c.a, torch.nn.Parameter(c.b), c.scale)),
+               dict(bank=AdapterBank(c.a, c.b, grad(c.scale)))):
+        with pytest.raises(RuntimeError, match="adapter_linear"):
+            adapter_apply(**{**ok, **kw})
+        with torch.no_grad():
+            assert torch.equal(adapter_apply(**{**ok, **kw}), want)
+        with torch.inference_mode():
+            assert torch.equal(adapter_apply(**{**ok, **kw}), want)
+    learnt = AdapterBank(c.a, c.b, grad(c.scale))
+    with pytest.raises(RuntimeError, match="scale"):
+        adapter_linear(c.x, w, cb, learnt, c.plan)
+    with torch.no_grad():
+        assert adapter_linear(c.x, w, cb, learnt, c.plan).shape == (50, N)
+    # the gradients' own call is for those who make them by hand
+    _, xa = adapter_apply(c.x, c.bank, c.plan, c.y, keep=True)
+    bank = AdapterBank(torch.nn.Parameter(c.a), torch.nn.Parameter(c.b), c.scale)
+    assert adapter_grads(c.dy, c.x, xa, bank, c.plan, c.dx)[1].shape == c.a.shape
