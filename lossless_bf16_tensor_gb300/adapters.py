@@ -81,6 +81,13 @@ _OPERANDS = ("the bank's a", "the bank's b", "the bank's scale", "the bank's ran
              "the plan's starts", "the plan's tiles")
 
 
+def _rows(x, k):
+    """x [..., k] as a matrix whose rows the kernels can read: a copy where its leading dimensions make no single row
+    index, or a row's values do not lie side by side."""
+    rows = x.reshape(-1, k)
+    return rows if rows.stride(1) == 1 and rows.stride(0) >= k else rows.contiguous()
+
+
 def _versions(tensors):
     return [None if t is None or t.is_inference() else t._version for t in tensors]
 
@@ -93,6 +100,7 @@ class _AdapterLinear(torch.autograd.Function):
     def forward(ctx, x, a, b, bank, plan, w, cb):
         y = compressed_linear(x, w, cb, bank.n, bank.k)
         operands = (a, b, bank.scale, bank.ranks, plan.order, plan.starts, plan.tiles)
+        x = _rows(x, bank.k)
         out, xa = calls.adapter_apply(*operands, x, y, y, True)
         ctx.save_for_backward(x, xa)
         ctx.rest = (operands, _versions(operands), w, cb, bank.n, bank.k)
@@ -116,7 +124,7 @@ class _AdapterLinear(torch.autograd.Function):
 def adapter_linear(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_codebook, bank: AdapterBank,
                    plan: AdapterPlan) -> torch.Tensor:
     """y = x W^T + s_a (x A_a^T) B_a^T for a compressed frozen W [n, k] and each
-    token's own adapter; x [..., k] BF16 on CUDA.  Differentiable (once) in x and in
+    token's own adapter; x [..., k] BF16 on CUDA, at any strides.  Differentiable (once) in x and in
     the bank's a and b (leaves such as ``torch.nn.Parameter``); the weight is
     decoded again for the gradient of x.  What it saves for backward goes
     through ``compressed_activations`` like any other saved tensor; the bank
@@ -127,4 +135,4 @@ def adapter_linear(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_codebook, b
     if torch.is_grad_enabled() and (x.requires_grad or bank.a.requires_grad or bank.b.requires_grad):
         return _AdapterLinear.apply(x, bank.a, bank.b, bank, plan, w, cb)
     y = compressed_linear(x, w, cb, bank.n, bank.k)
-    return adapter_apply(x, bank, plan, y, out=y)
+    return adapter_apply(_rows(x, bank.k), bank, plan, y, out=y)

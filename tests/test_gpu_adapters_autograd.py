@@ -5,7 +5,7 @@ import torch
 
 from lossless_bf16_tensor_gb300 import binding as B
 from lossless_bf16_tensor_gb300.activations import compressed_activations
-from lossless_bf16_tensor_gb300.adapters import AdapterBank, adapter_apply, adapter_grads, adapter_linear
+from lossless_bf16_tensor_gb300.adapters import AdapterBank, adapter_apply, adapter_grads, adapter_linear, adapter_plan
 from lossless_bf16_tensor_gb300.grads import clip_grads, grad_norm
 from test_gpu_adapters import Case, compressed_weight
 
@@ -169,3 +169,35 @@ def test_gradients_that_are_not_there_raise(weight):
     _, xa = adapter_apply(c.x, c.bank, c.plan, c.y, keep=True)
     bank = AdapterBank(torch.nn.Parameter(c.a), torch.nn.Parameter(c.b), c.scale)
     assert adapter_grads(c.dy, c.x, xa, bank, c.plan, c.dx)[1].shape == c.a.shape
+
+
+@pytest.mark.parametrize("layout", ["permuted", "expanded row", "expanded batch", "columns", "strided", "one token"])
+def test_x_at_any_strides(weight, layout):
+    """As compressed_linear takes it: the same results and gradients as for a contiguous copy."""
+    w, cb, _ = weight
+    c = Case(60, 2, 8, K, N, seed=8)
+    base = c.x
+
+    def views(v):
+        return {"permuted": lambda: v.view(3, 20, K).transpose(0, 1),
+                "expanded row": lambda: v[:1].expand(60, K),
+                "expanded batch": lambda: v.view(3, 20, K)[:, :1].expand(3, 20, K),
+                "columns": lambda: v.view(K, 60).t(),
+                "strided": lambda: torch.cat([v, v], 1)[:, 8:8 + K],
+                "one token": lambda: v[7:8, :]}[layout]()
+
+    plan = c.plan if layout != "one token" else adapter_plan(c.index[7:8], 2)
+    results = []
+    for copy in (False, True):
+        leaf = base.clone().requires_grad_(True)
+        a, b = torch.nn.Parameter(c.a.clone()), torch.nn.Parameter(c.b.clone())
+        x = views(leaf)
+        x = x.contiguous() if copy else x
+        bank = AdapterBank(a, b, c.scale)
+        y = adapter_linear(x, w, cb, bank, plan)
+        assert y.shape == (*x.shape[:-1], N)
+        y.float().square().sum().backward()
+        with torch.no_grad():
+            assert torch.equal(adapter_linear(x, w, cb, bank, plan), y)
+        results.append((y.detach(), leaf.grad, a.grad, b.grad))
+    assert all(torch.equal(p, q) for p, q in zip(*results))
