@@ -4,7 +4,8 @@
  * The codec's writers place each block's overflow bytes with a single-pass
  * scan in which a block waits for earlier blocks to publish their counts.
  * Every such wait is bounded; these hooks let a test watch a wait run out on
- * the GPU without faulting or hanging it.
+ * the GPU without faulting or hanging it.  The adapters' kernels have warps that
+ * wait for each other's loads and products; two more hooks are for those.
  */
 #ifndef LCT_DEBUG_H
 #define LCT_DEBUG_H
@@ -29,6 +30,20 @@ extern "C" {
  * Errors: LCT_ERR_INVALID_ARG for NULL/misaligned pointers or a limit out of
  * range, LCT_ERR_CUDA for a launch failure. */
 lct_status lct_debug_wait_timeout(void *d_header, void *d_work, uint64_t limit_ns, void *stream);
+
+/* lct_adapter_forward and lct_adapter_backward with kernels (the tiles' and the
+ * bank's gradients', whatever the batch) whose product warps do nothing: every
+ * wait for a product runs out, after about a second in each kernel.  Results
+ * are unspecified; LCT_ERR_TIMEOUT is latched in the plan's status, the kernels
+ * return normally and the CUDA context stays usable.  Errors as for those. */
+lct_status lct_debug_adapter_forward_timeout(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_x,
+                                             uint64_t ld_x, const uint16_t *d_y, uint64_t ld_y, uint16_t *d_out,
+                                             uint64_t ld_out, float *d_xa, void *stream);
+lct_status lct_debug_adapter_backward_timeout(const lct_adapters *bank, const lct_token_plan *plan,
+                                              const uint16_t *d_dy, uint64_t ld_dy, const uint16_t *d_x, uint64_t ld_x,
+                                              const float *d_xa, const uint16_t *d_dx, uint64_t ld_dx,
+                                              uint16_t *d_dx_out, uint64_t ld_dx_out, uint16_t *d_da, uint16_t *d_db,
+                                              void *d_work, void *stream);
 
 #ifdef __cplusplus
 }

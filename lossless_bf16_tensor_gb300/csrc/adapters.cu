@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 
 #include "../../include/lct.h"
+#include "../../include/lct_debug.h"
 #include "codec_dev.cuh"
 #include "internal.h"
 
@@ -333,8 +334,9 @@ __device__ __forceinline__ int4 tile_at(const AdapterArgs &g, int i)
 }
 
 // Waits at a barrier, for at most about a second by the SM's clock (a wait
-// that passes takes microseconds).  After one wait that ran out, none waits
-// again.
+// that passes takes microseconds).  A warp waits as a whole.  After a wait that
+// ran out it waits no more and tells nobody anything, and a warp that loads or
+// multiplies stops: what it started last has had that second to end.
 constexpr uint32_t kWaitClocks = 1800000000u;
 __device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity)
 {
@@ -353,11 +355,11 @@ struct Waiter {
     template <typename Ready>
     __device__ __forceinline__ void until(Ready ready)
     {
-        if (dead || ready()) return;
+        if (dead || __all_sync(kFull, ready())) return;
         const uint32_t t0 = static_cast<uint32_t>(clock());
 #pragma unroll 1
-        while (!ready())
-            if (static_cast<uint32_t>(clock()) - t0 > kWaitClocks) {
+        while (!__all_sync(kFull, ready()))
+            if (__any_sync(kFull, static_cast<uint32_t>(clock()) - t0 > kWaitClocks)) {
                 dead = true;
                 break;
             }
@@ -726,6 +728,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 for (int k = 0; k < chunks; ++k, next(), step += stride) {
                     if ((i & 1) != group) continue;
                     if (i >= S) waiter.wait(&freed[s], (i / S - 1) & 1);
+                    if (waiter.dead) return;
                     const uint32_t slot = base + s * T::kSlot;
                     if (FAST) {
                         if (loose == 0 && (boxes_w || !w.used)) {  // boxes hold all of it
@@ -802,7 +805,8 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 }
             };
             product(g.in, g.ld_in, g.nin, w.n1, false);
-            product(g.base, g.ld_base, g.nout, w.n2, true);
+            if (!waiter.dead) product(g.base, g.ld_base, g.nout, w.n2, true);
+            if (waiter.dead) break;
         }
         async_wait<0>();
         __syncwarp();
@@ -828,6 +832,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 int c0 = rank * kChunk;
                 for (int k = 0; k < chunks; ++k, ++i, s = s + 1 == S ? 0 : s + 1, c0 += size * kChunk) {
                     if (i >= S) waiter.wait(&freed[s], (i / S - 1) & 1);
+                    if (waiter.dead) return;
                     if (elect()) {
                         const uint32_t slot = base + s * T::kSlot;
                         const uint32_t due = bytes + (two == BACK ? a_bytes : b_bytes);
@@ -854,15 +859,20 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 }
             };
             product(&maps.in, w.n1, false);
-            product(&maps.base, w.n2, true);
+            if (!waiter.dead) product(&maps.base, w.n2, true);
+            if (waiter.dead) break;
         }
+        // the block does not end before its boxes are there
+        for (int c = max(0, i - S); c < i; ++c) waiter.wait(&full[c % S], (c / S) & 1);
     } else if (warp == kMmaWarp) {
         // --------------------------------------------------------- products
         int i = 0, s = 0, q = 0, tiles = 0;  // chunks and their slot, chunks of second products, tiles with a product
+        uint64_t *last = nullptr;            // what says that the last products are done
+        uint32_t last_parity = 0;
         // descriptors of slot 0's tiles and of V; sixteenths of a byte offset add to them
         const uint64_t in0 = operand(base, 0), v0 = operand(v_at, 0);
         const uint64_t along0 = operand(base + kInBytes, 0), across0 = operand(base + kInBytes, 64 * 128);
-        for (int tile = first_tile;; tile += clusters) {
+        for (int tile = first_tile; !g.stalled; tile += clusters) {
             const TileWork w = tile == first_tile ? first_work : tile_work(g, tile, rank, size);
             if (w.count <= 0) break;
             const uint32_t word1 = mma_word(w.r16, false, BACK), word2 = mma_word(kChunk, false, BACK);
@@ -880,6 +890,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 }
                 __syncwarp();
             }
+            if (w.n1 > 0) last = &narrow, last_parity = tiles & 1;
             for (int k = 0; k < w.n2; ++k, ++i, s = s + 1 == S ? 0 : s + 1, ++q) {
                 waiter.wait(&full[s], (i / S) & 1);
                 if (k == 0 && w.used) {
@@ -903,6 +914,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                     mma_commit(&summed[q % kSums]);
                 }
                 __syncwarp();
+                last = &summed[q % kSums], last_parity = (q / kSums) & 1;
             }
             if (w.used) {
                 // a block without a chunk of the second product still has to see its V's phase
@@ -910,6 +922,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 ++tiles;
             }
         }
+        if (last) waiter.wait(last, last_parity);
     } else {
         // ---------------------------------------------------------- results
         const int quarter = warp & 3, half = warp >> 2;
@@ -999,7 +1012,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                                     make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
                                                __float_as_uint(v[7])));
                         }
-                    arrive_cluster(&meet[0], size, lane);
+                    if (!waiter.dead) arrive_cluster(&meet[0], size, lane);
                     waiter.wait_cluster(&meet[0], tiles & 1);
                 }
                 if (size > 1) {
@@ -1036,7 +1049,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                                 if (k == u) sum[k][j] = one[j];
                     }
                     // everyone has read the partial sums that V's place held
-                    arrive_cluster(&meet[1], size, lane);
+                    if (!waiter.dead) arrive_cluster(&meet[1], size, lane);
                     waiter.wait_cluster(&meet[1], tiles & 1);
                 }
                 // loops of one copy each: this runs once a tile, and fetching its code is most of what it takes
@@ -1062,7 +1075,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 }
                 fence_proxy_all();
                 tc_before();
-                arrive_cluster(&meet[2], size, lane);
+                if (!waiter.dead) arrive_cluster(&meet[2], size, lane);
                 ++tiles;
             }
             i += w.n1;
@@ -1103,7 +1116,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sum_free[q % kSums]);
+                if (lane == 0 && !waiter.dead) mbar_arrive(&sum_free[q % kSums]);
                 if (FAST || g.al_out) {
                     const int there = g.nout - mine - step;
                     uint4 v[8];
@@ -1165,7 +1178,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 }
                 fence_proxy_async();  // the slot's next chunk may be a box
                 set_sync(half);
-                if ((threadIdx.x & 127) == 0) mbar_arrive(&freed[s]);
+                if ((threadIdx.x & 127) == 0 && !waiter.dead) mbar_arrive(&freed[s]);
             }
         }
     }
@@ -1675,6 +1688,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
                 ChunkTokens now = tokens;
                 tokens = chunk_tokens(g, chunk_at(i + 2), last, i + 2 < n, lane);
                 if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
+                if (waiter.dead) break;
                 if (FAST && now.runs) {  // boxes hold it
                     arrive_idle(&full[s], lane);
                     continue;
@@ -1734,6 +1748,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
                 const ChunkTokens now = tokens;
                 tokens = chunk_tokens(g, chunk_at(i + 1), last, FAST && i + 1 < n, lane);
                 if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
+                if (waiter.dead) break;
                 const int y[2] = {__shfl_sync(kFull, now.near, 0), __shfl_sync(kFull, now.far, 0)};
                 if (!elect()) {
                 } else if (!now.runs) {
@@ -1758,7 +1773,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
         } else {
             const uint32_t word = mma_word(min(kGradCols, (cols - c0 + 15) & ~15), true, true);
             const uint64_t in0 = operand(base, T::kTile), v0 = operand(base + T::kIn, T::kTile);
-            for (int i = 0; i < n; ++i) {
+            for (int i = 0; i < n && !g.stalled; ++i) {
                 const int s = i % STAGES;
                 waiter.wait(&full[s], (i / STAGES) & 1);
                 fence_proxy_async();
@@ -2163,6 +2178,7 @@ cudaError_t launch_few(const AdapterArgs &a, cudaStream_t s)
 cudaError_t launch_adapter(const AdapterArgs &a, bool back, cudaStream_t s)
 {
     const int64_t busy = std::min(a.adapters, a.tokens);
+    if (a.stalled) return back ? launch_tokens<true>(a, s) : launch_tokens<false>(a, s);
     if (!back && a.tokens > 16 && a.tokens <= 32 && a.tokens > 8 * busy) return launch_few<32>(a, s);
     if (!back && a.tokens <= 16 * busy) return launch_few<16>(a, s);
     return back ? launch_tokens<true>(a, s) : launch_tokens<false>(a, s);
@@ -2344,9 +2360,11 @@ extern "C" lct_status lct_adapter_plan(const int32_t *d_index, uint64_t tokens, 
     return launch_adapter_plan(g, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
 }
 
-extern "C" lct_status lct_adapter_forward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_x,
-                                          uint64_t ld_x, const uint16_t *d_y, uint64_t ld_y, uint16_t *d_out,
-                                          uint64_t ld_out, float *d_xa, void *stream)
+namespace {
+
+lct_status forward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_x, uint64_t ld_x,
+                   const uint16_t *d_y, uint64_t ld_y, uint16_t *d_out, uint64_t ld_out, float *d_xa, bool stalled,
+                   void *stream)
 {
     AdapterArgs g;
     const lct_status rc = check_bank(bank, plan, &g);
@@ -2373,13 +2391,14 @@ extern "C" lct_status lct_adapter_forward(const lct_adapters *bank, const lct_to
     g.al_out = rows_al(out);
     g.nout = g.n;
     g.keep = d_xa;
+    g.stalled = stalled;
     return launch_adapter(g, false, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
 }
 
-extern "C" lct_status lct_adapter_backward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_dy,
-                                           uint64_t ld_dy, const uint16_t *d_x, uint64_t ld_x, const float *d_xa,
-                                           const uint16_t *d_dx, uint64_t ld_dx, uint16_t *d_dx_out, uint64_t ld_dx_out,
-                                           uint16_t *d_da, uint16_t *d_db, void *d_work, void *stream)
+lct_status backward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_dy, uint64_t ld_dy,
+                    const uint16_t *d_x, uint64_t ld_x, const float *d_xa, const uint16_t *d_dx, uint64_t ld_dx,
+                    uint16_t *d_dx_out, uint64_t ld_dx_out, uint16_t *d_da, uint16_t *d_db, void *d_work, bool stalled,
+                    void *stream)
 {
     AdapterArgs g;
     const lct_status rc = check_bank(bank, plan, &g);
@@ -2435,10 +2454,47 @@ extern "C" lct_status lct_adapter_backward(const lct_adapters *bank, const lct_t
         g.al_db = al16(d_db) && g.rank % 8 == 0;
     }
     g.sparse = plan->tokens < bank->adapters;
+    g.stalled = stalled;
     if (d_da && g.sparse && (cudaMemsetAsync(d_da, 0, abytes, s) != cudaSuccess ||
                              cudaMemsetAsync(d_db, 0, bbytes, s) != cudaSuccess))
         return LCT_ERR_CUDA;
     if (launch_adapter(g, true, s) != cudaSuccess) return LCT_ERR_CUDA;
     if (d_da && launch_adapter_grad(g, s) != cudaSuccess) return LCT_ERR_CUDA;
     return LCT_OK;
+}
+
+}  // namespace
+
+extern "C" lct_status lct_adapter_forward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_x,
+                                          uint64_t ld_x, const uint16_t *d_y, uint64_t ld_y, uint16_t *d_out,
+                                          uint64_t ld_out, float *d_xa, void *stream)
+{
+    return forward(bank, plan, d_x, ld_x, d_y, ld_y, d_out, ld_out, d_xa, false, stream);
+}
+
+extern "C" lct_status lct_adapter_backward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_dy,
+                                           uint64_t ld_dy, const uint16_t *d_x, uint64_t ld_x, const float *d_xa,
+                                           const uint16_t *d_dx, uint64_t ld_dx, uint16_t *d_dx_out, uint64_t ld_dx_out,
+                                           uint16_t *d_da, uint16_t *d_db, void *d_work, void *stream)
+{
+    return backward(bank, plan, d_dy, ld_dy, d_x, ld_x, d_xa, d_dx, ld_dx, d_dx_out, ld_dx_out, d_da, d_db, d_work, false,
+                    stream);
+}
+
+extern "C" lct_status lct_debug_adapter_forward_timeout(const lct_adapters *bank, const lct_token_plan *plan,
+                                                        const uint16_t *d_x, uint64_t ld_x, const uint16_t *d_y,
+                                                        uint64_t ld_y, uint16_t *d_out, uint64_t ld_out, float *d_xa,
+                                                        void *stream)
+{
+    return forward(bank, plan, d_x, ld_x, d_y, ld_y, d_out, ld_out, d_xa, true, stream);
+}
+
+extern "C" lct_status lct_debug_adapter_backward_timeout(const lct_adapters *bank, const lct_token_plan *plan,
+                                                         const uint16_t *d_dy, uint64_t ld_dy, const uint16_t *d_x,
+                                                         uint64_t ld_x, const float *d_xa, const uint16_t *d_dx,
+                                                         uint64_t ld_dx, uint16_t *d_dx_out, uint64_t ld_dx_out,
+                                                         uint16_t *d_da, uint16_t *d_db, void *d_work, void *stream)
+{
+    return backward(bank, plan, d_dy, ld_dy, d_x, ld_x, d_xa, d_dx, ld_dx, d_dx_out, ld_dx_out, d_da, d_db, d_work, true,
+                    stream);
 }

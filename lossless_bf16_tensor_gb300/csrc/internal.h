@@ -185,6 +185,7 @@ struct AdapterArgs {
     bool al_a, al_b, al_in, al_base, al_out, al_x, al_db;  // rows begin at 16-byte boundaries
     bool sparse;                                            // backward: more adapters than tokens
     bool boxes_w;                                           // the weights come as boxes: set by the launcher
+    bool stalled;                                           // a test: no products are made, so that waits run out
 };
 struct PlanArgs {
     const int32_t *index;
