@@ -334,9 +334,9 @@ __device__ __forceinline__ int4 tile_at(const AdapterArgs &g, int i)
 }
 
 // Waits at a barrier, for at most about a second by the SM's clock (a wait
-// that passes takes microseconds).  A warp waits as a whole.  After a wait that
-// ran out it waits no more and tells nobody anything, and a warp that loads or
-// multiplies stops: what it started last has had that second to end.
+// that passes takes microseconds).  After a wait that ran out a thread waits no
+// more and tells nobody anything, and it starts no box and no product: what it
+// started last has had that second to end.
 constexpr uint32_t kWaitClocks = 1800000000u;
 __device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity)
 {
@@ -355,11 +355,11 @@ struct Waiter {
     template <typename Ready>
     __device__ __forceinline__ void until(Ready ready)
     {
-        if (dead || __all_sync(kFull, ready())) return;
+        if (dead || ready()) return;
         const uint32_t t0 = static_cast<uint32_t>(clock());
 #pragma unroll 1
-        while (!__all_sync(kFull, ready()))
-            if (__any_sync(kFull, static_cast<uint32_t>(clock()) - t0 > kWaitClocks)) {
+        while (!ready())
+            if (static_cast<uint32_t>(clock()) - t0 > kWaitClocks) {
                 dead = true;
                 break;
             }
@@ -383,10 +383,10 @@ struct Waiter {
 
 // A meeting of the cluster's eight result warps: each warp arrives at every
 // block's barrier, and waits at its own.
-__device__ __forceinline__ void arrive_cluster(uint64_t *bar, uint32_t size, int lane)
+__device__ __forceinline__ void arrive_cluster(uint64_t *bar, uint32_t size, int lane, const Waiter &waiter)
 {
     __syncwarp();
-    if (lane < static_cast<int>(size)) {
+    if (lane < static_cast<int>(size) && !waiter.dead) {
         const uint32_t there = peer_addr(smem_addr(bar), lane);
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(there) : "memory");
     }
@@ -414,16 +414,17 @@ constexpr int kTokThreads = 32 * (kLoadWarp + kLoadWarps);
 // and so does the box warp: a warp that fell two of a slot's turns behind would
 // take its barrier's phase for another one.
 constexpr uint32_t kFullArrivals = kLoadGroup * 33 + 1;
-__device__ __forceinline__ void arrive_idle(uint64_t *bar, int lane)
+__device__ __forceinline__ void arrive_idle(uint64_t *bar, int lane, const Waiter &waiter)
 {
-    if (lane == 0)
+    if (lane == 0 && !waiter.dead)
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 33;" ::"r"(smem_addr(bar)) : "memory");
 }
-__device__ __forceinline__ void arrive_full(uint64_t *bar, int lane)
+__device__ __forceinline__ void arrive_full(uint64_t *bar, int lane, const Waiter &waiter)
 {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+    if (!waiter.dead)
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
+    if (lane == 0 && !waiter.dead) mbar_arrive(bar);
 }
 
 __device__ __forceinline__ uint16_t load2(uint32_t at)
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
             move_rows<RANK / 16>(slot + kInBytes + at, end ? extra + T::kExtraW : slot + kInBytes + next,
                                  end ? 256 : 2048, c.weights);
             __syncwarp();
-            arrive_idle(&full[c.slot], lane);
+            arrive_idle(&full[c.slot], lane, waiter);
         };
         for (int tile = first_tile;; tile += clusters) {
             const TileWork w = tile == first_tile ? first_work : tile_work(g, tile, rank, size);
@@ -728,11 +729,10 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 for (int k = 0; k < chunks; ++k, next(), step += stride) {
                     if ((i & 1) != group) continue;
                     if (i >= S) waiter.wait(&freed[s], (i / S - 1) & 1);
-                    if (waiter.dead) return;
                     const uint32_t slot = base + s * T::kSlot;
                     if (FAST) {
                         if (loose == 0 && (boxes_w || !w.used)) {  // boxes hold all of it
-                            arrive_idle(&full[s], lane);
+                            arrive_idle(&full[s], lane, waiter);
                             continue;
                         }
 #pragma unroll
@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                                           cols - start - step, left - 16 * q);
                         if (w.used && !boxes_w)
                             two == BACK ? load_a(slot + kInBytes, step) : load_b(slot + kInBytes, step);
-                        arrive_full(&full[s], lane);
+                        arrive_full(&full[s], lane, waiter);
                         continue;
                     }
                     const uint32_t extra = extra0 + s * T::kExtra, extra_w = extra + T::kExtraW;
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                             settle(late);
                             flying = false;
                         }
-                        arrive_full(&full[s], lane);
+                        arrive_full(&full[s], lane, waiter);
                         continue;
                     }
                     async_commit();
@@ -805,8 +805,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 }
             };
             product(g.in, g.ld_in, g.nin, w.n1, false);
-            if (!waiter.dead) product(g.base, g.ld_base, g.nout, w.n2, true);
-            if (waiter.dead) break;
+            product(g.base, g.ld_base, g.nout, w.n2, true);
         }
         async_wait<0>();
         __syncwarp();
@@ -832,8 +831,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 int c0 = rank * kChunk;
                 for (int k = 0; k < chunks; ++k, ++i, s = s + 1 == S ? 0 : s + 1, c0 += size * kChunk) {
                     if (i >= S) waiter.wait(&freed[s], (i / S - 1) & 1);
-                    if (waiter.dead) return;
-                    if (elect()) {
+                    if (elect() && !waiter.dead) {
                         const uint32_t slot = base + s * T::kSlot;
                         const uint32_t due = bytes + (two == BACK ? a_bytes : b_bytes);
                         if (due)
@@ -859,8 +857,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 }
             };
             product(&maps.in, w.n1, false);
-            if (!waiter.dead) product(&maps.base, w.n2, true);
-            if (waiter.dead) break;
+            product(&maps.base, w.n2, true);
         }
         // the block does not end before its boxes are there
         for (int c = max(0, i - S); c < i; ++c) waiter.wait(&full[c % S], (c / S) & 1);
@@ -967,9 +964,11 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                         for (int j = 0; j < 8; ++j)
                             if (p * 8 + j < w.used) k[j] = x[j];
                     }
-                    // the ranks from `used` to the next 16 are products with zeros: zero, whatever In holds
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = p * 8 + j < w.used ? x[j] * scale : 0.0f;
+                    for (int j = 0; j < 8; ++j) x[j] *= scale;
+                    if (p * 8 + 8 > w.used)  // the ranks up to the next 16 are products with zeros: zero, whatever In holds
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = p * 8 + j < w.used ? x[j] : 0.0f;
                     uint4 hi, lo;
                     split8(x, hi, lo);
                     const uint32_t to = v_at + (p >> 3) * T::kVAtom + swz(row, p & 7);
@@ -1012,7 +1011,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                                     make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
                                                __float_as_uint(v[7])));
                         }
-                    if (!waiter.dead) arrive_cluster(&meet[0], size, lane);
+                    arrive_cluster(&meet[0], size, lane, waiter);
                     waiter.wait_cluster(&meet[0], tiles & 1);
                 }
                 if (size > 1) {
@@ -1049,7 +1048,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                                 if (k == u) sum[k][j] = one[j];
                     }
                     // everyone has read the partial sums that V's place held
-                    if (!waiter.dead) arrive_cluster(&meet[1], size, lane);
+                    arrive_cluster(&meet[1], size, lane, waiter);
                     waiter.wait_cluster(&meet[1], tiles & 1);
                 }
                 // loops of one copy each: this runs once a tile, and fetching its code is most of what it takes
@@ -1075,7 +1074,7 @@ __global__ void __launch_bounds__(kTokThreads, 1)
                 }
                 fence_proxy_all();
                 tc_before();
-                if (!waiter.dead) arrive_cluster(&meet[2], size, lane);
+                arrive_cluster(&meet[2], size, lane, waiter);
                 ++tiles;
             }
             i += w.n1;
@@ -1333,7 +1332,12 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
     // before the tokens are known, and nothing but the cluster's meeting is waited for on the way.
     const bool at_once = n <= S && count <= ROWS;
     const int ahead = at_once ? S : S - 1;
+    // the scale at a thread's four ranks of V, 0 where the adapter has no such rank
+    static_assert(kAdThreads % (RT / 4) == 0, "");
     const float scale = g.scale[a];
+    float scales[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) scales[j] = static_cast<int>(threadIdx.x) % (RT / 4) * 4 + j < used ? scale : 0.0f;
 
     for (int first = 0; first < count; first += ROWS) {
 #pragma unroll 1
@@ -1404,7 +1408,7 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
             float v = 0.0f;
 #pragma unroll
             for (int q = 0; q < F::kSplitK; ++q) v += part[q * ROWS * RT + e];
-            sum[e] = v;
+            sum[e] = e % RT < used ? v : 0.0f;  // the others are products with zeros: zero, whatever In holds
         }
         __syncwarp();
         if (size > 1)
@@ -1426,13 +1430,10 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
                     const float k[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j)  // zero where the adapter has no such rank
-                        if (c + j < g.rank)
-                            g.keep[static_cast<int64_t>(tok[first + r]) * g.rank + c + j] = c + j < used ? k[j] : 0.0f;
+                        if (c + j < g.rank) g.keep[static_cast<int64_t>(tok[first + r]) * g.rank + c + j] = k[j];
                 }
             }
-            // ranks from `used` on are products with zeros: zero, whatever In holds
-            v.x = c < used ? v.x * scale : 0.0f, v.y = c + 1 < used ? v.y * scale : 0.0f;
-            v.z = c + 2 < used ? v.z * scale : 0.0f, v.w = c + 3 < used ? v.w * scale : 0.0f;
+            v.x *= scales[0], v.y *= scales[1], v.z *= scales[2], v.w *= scales[3];
             const uint2 hi = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
             const uint2 lo = make_uint2(pack2(rest(v.x, hi.x << 16), rest(v.y, hi.x & 0xFFFF0000u)),
                                         pack2(rest(v.z, hi.y << 16), rest(v.w, hi.y & 0xFFFF0000u)));
@@ -1675,7 +1676,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
                     }
                 }
                 __syncwarp();
-                arrive_idle(&full[late_slot], lane);
+                arrive_idle(&full[late_slot], lane, waiter);
                 late_slot = -1;
             };
             ChunkTokens tokens = chunk_tokens(g, chunk_at(group), last, group < n, lane);
@@ -1688,9 +1689,8 @@ __global__ void __launch_bounds__(kGradAdThreads)
                 ChunkTokens now = tokens;
                 tokens = chunk_tokens(g, chunk_at(i + 2), last, i + 2 < n, lane);
                 if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
-                if (waiter.dead) break;
                 if (FAST && now.runs) {  // boxes hold it
-                    arrive_idle(&full[s], lane);
+                    arrive_idle(&full[s], lane, waiter);
                     continue;
                 }
                 now.near = checked_token(g, now.near);
@@ -1720,7 +1720,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
                         async16(to + q * 1024, p + q * 16 * g.rank16, v_row + 8 * q < left ? 16 : 0);
                 }
                 if (FAST) {
-                    arrive_full(&full[s], lane);
+                    arrive_full(&full[s], lane, waiter);
                     continue;
                 }
                 async_commit();
@@ -1748,9 +1748,8 @@ __global__ void __launch_bounds__(kGradAdThreads)
                 const ChunkTokens now = tokens;
                 tokens = chunk_tokens(g, chunk_at(i + 1), last, FAST && i + 1 < n, lane);
                 if (i >= STAGES) waiter.wait(&freed[s], (i / STAGES - 1) & 1);
-                if (waiter.dead) break;
                 const int y[2] = {__shfl_sync(kFull, now.near, 0), __shfl_sync(kFull, now.far, 0)};
-                if (!elect()) {
+                if (!elect() || waiter.dead) {
                 } else if (!now.runs) {
                     mbar_arrive(&full[s]);
                 } else {
@@ -1795,13 +1794,14 @@ __global__ void __launch_bounds__(kGradAdThreads)
         tc_after();
         __syncthreads();
         // The block's sums, [rank][column]: lanes hold ranks, up to R = 64 those of the upper half the lo part's (which
-        // come first).  The two are added where hi's sum is finite: beside an infinity in x or dy, hi and lo of opposite
-        // signs would give NaN.
+        // come first).  Beside an infinity in x or dy, hi and lo of opposite signs would give NaN: lo's sums are taken as
+        // finite (they are, where hi's are), so that hi's decide.
         const int quarter = warp & 3, half = warp >> 2;
         const bool lo = RANK <= 64 && quarter >= 2;
         const int r = (RANK <= 64 ? quarter & 1 : quarter) * 32 + lane;
         const uint32_t lanes = tmem + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
         const int end = min(128, cols - c0 - half * 128);
+        const auto finite = [](float v) { return fmaxf(fminf(v, 0x1.fffffep127f), -0x1.fffffep127f); };
         for (int turn = 0; turn < (RANK <= 64 ? 2 : 1); ++turn) {
             if (warp < kGradLoadWarps && lo == (RANK <= 64 && turn == 0) && r - lane < r16)
                 for (int c = 0; c < end; c += 8) {
@@ -1814,10 +1814,7 @@ __global__ void __launch_bounds__(kGradAdThreads)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         float *to = sums + r * (kGradCols + 1) + half * 128 + c + j;
-                        if (RANK <= 64)
-                            *to = turn == 1 && isfinite(x[j]) ? *to + x[j] : x[j];
-                        else
-                            *to = isfinite(x[j]) ? x[j] + y[j] : x[j];
+                        *to = RANK > 64 ? x[j] + finite(y[j]) : turn ? *to + x[j] : finite(x[j]);
                     }
                 }
             __syncthreads();
