@@ -376,9 +376,10 @@ lct_status lct_grad_norm(const void *const *d_g, const uint64_t *n, const int32_
  *   c = min(1, max_norm / (norm + 1e-6))
  * into d_out[i] (n[i] values of d_g[i]'s type, rounded once, to nearest even).
  * d_out[i] is d_g[i] itself (in place) or apart from every gradient and every
- * other output.  With c = 1 gradients in place are not touched.  c is NaN
- * where the norm is NaN, and 0 where it is infinite (an infinity times 0 is
- * NaN, a finite value 0): read *d_norm before a step to skip it.
+ * other output.  With c = 1 gradients in place are not touched.  A norm above
+ * float's range, which *d_norm gives as infinity, still clips to max_norm.  c
+ * is NaN where a gradient is NaN, and 0 where one is infinite (an infinity
+ * times 0 is NaN, a finite value 0): read *d_norm before a step to skip it.
  * Errors: as lct_grad_norm, and LCT_ERR_INVALID_ARG for max_norm that is not
  * positive and finite, or for overlapping tensors (d_norm and d_work among
  * them). */
@@ -444,12 +445,15 @@ lct_status lct_adapter_plan(const int32_t *d_index, uint64_t tokens, uint64_t ad
  * lies before a row's first value among it.  The sums are float32, the narrow
  * product is carried to the second one with 16 bits, and out is rounded once.
  * d_xa, if not NULL, gets x A_a^T [tokens, rank] in float32 (0 where an adapter
- * has no such rank) for lct_adapter_backward.  A wait that ran out on the device
- * latches LCT_ERR_TIMEOUT in the plan's status.  Errors: LCT_ERR_INVALID_ARG
- * (NULL or misaligned pointers, strides below the widths, a plan for another
- * number of adapters, an output that overlaps another operand),
- * LCT_ERR_UNSUPPORTED (rank above LCT_ADAPTER_MAX_RANK or another limit),
- * LCT_ERR_CUDA. */
+ * has no such rank) for lct_adapter_backward.  Infinities and NaN in x stay in
+ * their rows and follow the formula, whatever ranks an adapter leaves unused;
+ * an infinite B_a (backward, for dx_out: A_a) may give NaN where the formula
+ * gives an infinity, as the narrow product's two parts may have opposite signs.
+ * A wait that ran out on the device latches LCT_ERR_TIMEOUT in the plan's
+ * status.  Errors: LCT_ERR_INVALID_ARG (NULL or misaligned pointers, strides
+ * below the widths, a plan for another number of adapters, an output that
+ * overlaps another operand), LCT_ERR_UNSUPPORTED (rank above
+ * LCT_ADAPTER_MAX_RANK or another limit), LCT_ERR_CUDA. */
 lct_status lct_adapter_forward(const lct_adapters *bank, const lct_token_plan *plan, const uint16_t *d_x,
                                uint64_t ld_x, const uint16_t *d_y, uint64_t ld_y, uint16_t *d_out, uint64_t ld_out,
                                float *d_xa, void *stream);

@@ -435,7 +435,8 @@ __device__ __forceinline__ uint16_t load2(uint32_t at)
 }
 
 // A box of a row-major matrix into a row-swizzled tile, and one of a stack of
-// matrices; what lies outside is zero.  x is a multiple of 64.
+// matrices; what lies outside is zero.  x is a multiple of 16 (32 bytes): of 64,
+// but for the lo part of V.
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *m, int x, int y, uint64_t *bar)
 {
     asm volatile(
@@ -1229,9 +1230,9 @@ __device__ __forceinline__ void copy_rows(const AdapterArgs &g, const int *tok, 
 // larger batches were no faster than the tile kernel (64 tokens of one adapter
 // 15.6 and 15.2 us, 512 of eight 21.6 and 16.1 us).
 //
-// One token at rank 16 and 4096 columns takes 6.7 us, of which about 2 us is an
+// One token at rank 16 and 4096 columns takes 7.0 us, of which about 2 us is an
 // empty launch's and the rest two dependent trips to memory (plan, then data)
-// and the cluster's meeting; 64 tokens of 64 adapters 8.6 us, floor 2.8 us.
+// and the cluster's meeting; 64 tokens of 64 adapters 8.9 us, floor 2.8 us.
 constexpr int kFewCols = 128;
 
 template <int RT, int ROWS>
@@ -1507,7 +1508,7 @@ __global__ void __launch_bounds__(kAdThreads) k_adapter_few(const __grid_constan
 // (5.4 TB/s, 81% of a copy's rate), tensor pipe busy 28% of the time; reading
 // the tokens from the last one on, for what L2 still holds of dy, changed
 // nothing.  2048 tokens of four adapters, R = 32, 1024 to 4096: the two launches
-// of the backward pass take 30 us, each a chain of set-up, one trip to memory a
+// of the backward pass take 31 us, each a chain of set-up, one trip to memory a
 // turn and a meeting, against 4.8 us for the bytes.
 //
 // The products' rows are V's columns, up to R = 64 its hi part's and below
