@@ -474,6 +474,99 @@ lct_status lct_adapter_backward(const lct_adapters *bank, const lct_token_plan *
                                 const uint16_t *d_dx, uint64_t ld_dx, uint16_t *d_dx_out, uint64_t ld_dx_out,
                                 uint16_t *d_da, uint16_t *d_db, void *d_work, void *stream);
 
+/* ---- the vocabulary's two ends: the lookup, and the loss ----------------- */
+
+#define LCT_VOCAB_MAX (1 << 24)          /* rows of the vocabulary's matrix */
+#define LCT_VOCAB_MAX_COLS (1 << 16)
+#define LCT_VOCAB_MAX_TOKENS (1 << 24)
+#define LCT_EMBEDDING_CHUNK 32           /* sorted tokens that one block adds */
+/* scratch of lct_embedding_grad */
+#define LCT_EMBEDDING_WORK_BYTES(tokens, vocab, cols)                                                      \
+    (16ull + 64ull * (((uint64_t)(tokens) + 3) / 4) + 16ull * (((uint64_t)(vocab) + 3) / 4) +              \
+     8ull * (((uint64_t)(tokens) + LCT_EMBEDDING_CHUNK - 1) / LCT_EMBEDDING_CHUNK) * (uint64_t)(cols))
+
+/* A batch's ids: a row of the vocabulary's matrix for each token.  A negative
+ * id is none (padding, a token without a target). */
+typedef struct {
+    const void *d_ids; /* [tokens], int32 or (wide) int64 */
+    int32_t wide;      /* 0 or 1 */
+    uint64_t tokens, vocab;
+} lct_ids;
+
+/* out_i = scale * table[id_i] for every token, rounded once; a row of zeros for
+ * a token without an id, and of NaN for an id of vocab or more.  (The pages have
+ * no counterpart.)  d_table holds rows `first` .. first + rows of the matrix
+ * [vocab, cols], ld_table values apart, of `dtype`, which is out's too; tokens
+ * of other rows are left as they are, so that a compressed matrix can be decoded
+ * and looked up a piece at a time.  Rows at 16-byte boundaries are the fast
+ * case.  Errors: LCT_ERR_INVALID_ARG (NULL or misaligned pointers, strides
+ * below cols, rows outside the vocabulary, out over another operand),
+ * LCT_ERR_UNSUPPORTED (another dtype, a size above the limits), LCT_ERR_CUDA. */
+lct_status lct_embedding(const lct_ids *ids, const void *d_table, uint64_t ld_table, int32_t dtype, uint64_t first,
+                         uint64_t rows, uint64_t cols, float scale, void *d_out, uint64_t ld_out, void *stream);
+
+/* The gradient of lct_embedding for dy [tokens, cols], the gradient of its out:
+ *   out_v = base_v + scale * sum of dy_i over the tokens with id_i = v
+ * for every v of the vocabulary: the dense gradient that the fused steps take
+ * (with ld_out = cols).  base may be NULL (zero) or out itself, whose rows
+ * without tokens are then not touched: a matrix that is also the loss's
+ * projection adds the lookup's gradient to that one's.  Sums are float32, added
+ * in an order that depends on the ids alone (the same bits every time), and
+ * rounded once.  Ids outside the vocabulary add nothing.  d_work:
+ * LCT_EMBEDDING_WORK_BYTES of scratch, 16-byte aligned.  Errors as
+ * lct_embedding. */
+lct_status lct_embedding_grad(const lct_ids *ids, const void *d_dy, uint64_t ld_dy, int32_t dtype, uint64_t cols,
+                              float scale, const void *d_base, uint64_t ld_base, void *d_out, uint64_t ld_out,
+                              void *d_work, void *stream);
+
+/* What lct_loss_work_bytes is asked for. */
+#define LCT_LOSS_BACKWARD 1
+#define LCT_LOSS_WEIGHT 2    /* backward: with the weight's gradient */
+#define LCT_LOSS_UNALIGNED 4 /* a row of x or of the weight does not begin at a 16-byte boundary */
+
+/* Bytes of scratch (256-byte aligned) of the two calls below for pieces of at
+ * most `rows` rows of the vocabulary: one piece (rows = vocab), or several. */
+uint64_t lct_loss_work_bytes(uint64_t tokens, uint64_t vocab, uint64_t cols, uint64_t rows, int32_t flags);
+
+/* The cross entropy of a projection onto the vocabulary, which keeps no logits:
+ *   lse_i = log sum over v of exp(x_i W_v),   loss_i = lse_i - x_i W_{t_i}
+ * in float32.  (The pages have no counterpart.)  x [tokens, cols] and W are
+ * BF16; products add in float32.  A token without a target (t_i < 0) has loss 0;
+ * a target of vocab or more gives NaN, and so does an infinite logit.
+ * d_w holds rows `first` .. first + rows of W [vocab, cols].  The whole W can be
+ * given in one call (first 0, rows = vocab), or in pieces, in order, with the
+ * same batch, results and d_work: what they have in common lives there from call
+ * to call.  d_loss and d_lse are written by the last piece's call.
+ * d_total, if not NULL, gets three floats: the sum of the losses, their mean over
+ * the tokens with a target, and 1 over the number of those (no token: sum and
+ * mean 0).  Rows at 16-byte boundaries are the fast case; others are copied to
+ * such in d_work first.  A wait that ran out on the device makes every loss NaN
+ * and leaves LCT_ERR_TIMEOUT in d_work's first word.  Errors:
+ * LCT_ERR_INVALID_ARG (NULL or misaligned pointers, strides below cols, a piece
+ * outside the vocabulary, too little scratch, an output over another operand),
+ * LCT_ERR_UNSUPPORTED (a size above the limits), LCT_ERR_CUDA. */
+lct_status lct_loss_forward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,
+                            const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows, float *d_loss,
+                            float *d_lse, float *d_total, void *d_work, uint64_t work_bytes, void *stream);
+
+/* The gradients of lct_loss_forward: with c_i = d_dloss[i * dloss_stride] *
+ * *d_scale (dloss_stride 0 or 1; d_scale NULL: 1), the gradient of loss_i, and
+ *   g_iv = c_i (exp(x_i W_v - lse_i) - [v = t_i]),
+ *   dx = g W  [tokens, cols],   dW = g^T x  (this piece's rows; d_dw NULL: left out)
+ * in BF16.  Logits are computed again, g is held in BF16 for a bounded part of
+ * the vocabulary at a time but for its targets' entries, which go into both
+ * results in float32.  A token without a target has dx 0 and adds nothing to
+ * dW, whatever its x holds; one with an impossible target has dx NaN and adds
+ * nothing.  Pieces as in the forward pass (d_dw NULL for all or none); d_dx is
+ * written by the last one's call.  Sums are added in an order that depends on the
+ * targets alone: the same bits every time.  A wait that ran out makes dx NaN.
+ * Errors as lct_loss_forward. */
+lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,
+                             const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows, const float *d_loss,
+                             const float *d_lse, const float *d_dloss, uint64_t dloss_stride, const float *d_scale,
+                             uint16_t *d_dx, uint64_t ld_dx, uint16_t *d_dw, uint64_t ld_dw, void *d_work,
+                             uint64_t work_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

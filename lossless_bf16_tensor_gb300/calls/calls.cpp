@@ -1,4 +1,4 @@
-// Python entry points of the gradient and adapter calls: tensors in, checks,
+// Python entry points of the gradient, adapter and vocabulary calls: tensors in, checks,
 // allocation of the results from torch's caching allocator, and one call of the
 // C ABI on the current stream.  They are here and not in Python because a
 // decode step calls them hundreds of times: what ctypes and Python take for one
@@ -211,14 +211,16 @@ struct Rows {
 };
 
 // t [..., cols] as a matrix of `tokens` rows
-Rows rows_of(const at::Tensor &t, uint64_t cols, uint64_t tokens, int device, const char *what)
+Rows rows_of(const at::Tensor &t, uint64_t cols, uint64_t tokens, int device, const char *what,
+             at::ScalarType type = at::kBFloat16)
 {
     const auto sizes = t.sizes(), strides = t.strides();
     const int64_t d = t.dim();
-    if (t.scalar_type() != at::kBFloat16 || !t.is_cuda() || t.get_device() != device || d < 1 ||
+    if (t.scalar_type() != type || !t.is_cuda() || t.get_device() != device || d < 1 ||
         static_cast<uint64_t>(sizes[d - 1]) != cols || static_cast<uint64_t>(t.numel()) != tokens * cols) {
-        PyErr_Format(PyExc_ValueError, "%s: expected a BF16 tensor of %llu rows of %llu on CUDA device %d", what,
-                     static_cast<unsigned long long>(tokens), static_cast<unsigned long long>(cols), device);
+        PyErr_Format(PyExc_ValueError, "%s: expected a %s tensor of %llu rows of %llu on CUDA device %d", what,
+                     type == at::kFloat ? "float32" : "BF16", static_cast<unsigned long long>(tokens),
+                     static_cast<unsigned long long>(cols), device);
         throw Raised{};
     }
     // leading dimensions that make one row index: each one's stride is the next one's times its size
@@ -374,6 +376,261 @@ PyObject *adapter_grads(PyObject *const *a)
     return tuple_of({first, THPVariable_Wrap(da), THPVariable_Wrap(db)});
 }
 
+// ------------------------------------------------------ the vocabulary's ends
+
+// ids of any shape, flattened
+lct_ids ids_of(const at::Tensor &t, uint64_t vocab, const char *what)
+{
+    if (!t.is_cuda() || !t.is_contiguous() || (t.scalar_type() != at::kInt && t.scalar_type() != at::kLong)) {
+        PyErr_Format(PyExc_ValueError, "%s: expected a contiguous int32 or int64 CUDA tensor", what);
+        throw Raised{};
+    }
+    lct_ids i{};
+    i.d_ids = t.data_ptr();
+    i.wide = t.scalar_type() == at::kLong;
+    i.tokens = static_cast<uint64_t>(t.numel());
+    i.vocab = vocab;
+    return i;
+}
+lct_dtype dtype_of(const at::Tensor &t, const char *what)
+{
+    if (t.scalar_type() != at::kFloat && t.scalar_type() != at::kBFloat16) check(LCT_ERR_UNSUPPORTED, what);
+    return t.scalar_type() == at::kFloat ? LCT_DTYPE_F32 : LCT_DTYPE_BF16;
+}
+uint64_t number(PyObject *o)
+{
+    const long long v = PyLong_AsLongLong(o);
+    if (PyErr_Occurred()) throw Raised{};
+    need(v >= 0, "expected a number that is not negative");
+    return static_cast<uint64_t>(v);
+}
+double real(PyObject *o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (PyErr_Occurred()) throw Raised{};
+    return v;
+}
+void no_gradient(std::initializer_list<const at::Tensor *> operands, const char *what)
+{
+    if (!at::GradMode::is_enabled()) return;
+    for (const at::Tensor *t : operands)
+        if (t->requires_grad()) {
+            PyErr_Format(PyExc_RuntimeError,
+                         "%s gives no gradients, but an operand requires one: call it under torch.no_grad()", what);
+            throw Raised{};
+        }
+}
+
+// (ids, table, first, vocab, scale, out or None) -> out; the table's rows are `first` .. of vocab (0: all of them)
+PyObject *embedding(PyObject *const *a)
+{
+    const at::Tensor &idt = tensor(a[0], "tokens must be a tensor"), &table = tensor(a[1], "table must be a tensor");
+    need(table.dim() == 2 && table.is_cuda(), "table must be a CUDA tensor [rows, columns]");
+    const lct_dtype dtype = dtype_of(table, "tables other than BF16 and float32");
+    const uint64_t rows = static_cast<uint64_t>(table.size(0)), cols = static_cast<uint64_t>(table.size(1));
+    const uint64_t first = number(a[2]), vocab = number(a[3]);
+    const lct_ids ids = ids_of(idt, vocab ? vocab : rows, "tokens");
+    const int device = table.get_device();
+    need(idt.get_device() == device, "tokens and table must be on one device");
+    const Rows tr = rows_of(table, cols, rows, device, "table", table.scalar_type());
+    const float scale = static_cast<float>(real(a[4]));
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
+    at::Tensor fresh;
+    if (a[5] == Py_None) {
+        std::vector<int64_t> shape(idt.sizes().begin(), idt.sizes().end());
+        shape.push_back(static_cast<int64_t>(cols));
+        fresh = make(shape, table.scalar_type(), device);
+    }
+    const at::Tensor &out = a[5] == Py_None ? fresh : tensor(a[5], "out must be a tensor or None");
+    no_gradient({&table, &out}, "embedding into out");
+    const Rows outr = rows_of(out, cols, ids.tokens, device, "out", table.scalar_type());
+    check(lct_embedding(&ids, tr.p, tr.ld, dtype, first, rows, cols, scale, outr.p, outr.ld, stream_of(device)),
+          "lct_embedding");
+    if (a[5] == Py_None) return THPVariable_Wrap(fresh);
+    wrote(out);
+    return Py_NewRef(a[5]);
+}
+
+// (dy, ids, rows, scale, base or None, out or None) -> out
+PyObject *embedding_grad(PyObject *const *a)
+{
+    const at::Tensor &dy = tensor(a[0], "dy must be a tensor"), &idt = tensor(a[1], "tokens must be a tensor");
+    const uint64_t vocab = number(a[2]);
+    const lct_ids ids = ids_of(idt, vocab, "tokens");
+    need(dy.is_cuda() && dy.dim() >= 1 && idt.get_device() == dy.get_device(), "dy and tokens must be on one CUDA device");
+    const lct_dtype dtype = dtype_of(dy, "gradients other than BF16 and float32");
+    const int device = dy.get_device();
+    const uint64_t cols = static_cast<uint64_t>(dy.size(dy.dim() - 1));
+    const Rows dyr = rows_of(dy, cols, ids.tokens, device, "dy", dy.scalar_type());
+    const float scale = static_cast<float>(real(a[3]));
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
+    Rows base;
+    if (a[4] != Py_None)
+        base = rows_of(tensor(a[4], "base must be a tensor or None"), cols, vocab, device, "base", dy.scalar_type());
+    at::Tensor fresh;
+    if (a[5] == Py_None) fresh = make({static_cast<int64_t>(vocab), static_cast<int64_t>(cols)}, dy.scalar_type(), device);
+    const at::Tensor &out = a[5] == Py_None ? fresh : tensor(a[5], "out must be a tensor or None");
+    no_gradient({&dy, &out}, "embedding_grad");
+    const Rows outr = rows_of(out, cols, vocab, device, "out", dy.scalar_type());
+    at::Tensor work = make({static_cast<int64_t>(LCT_EMBEDDING_WORK_BYTES(ids.tokens, vocab, cols))}, at::kByte, device);
+    check(lct_embedding_grad(&ids, dyr.p, dyr.ld, dtype, cols, scale, base.p, base.ld, outr.p, outr.ld, work.data_ptr(),
+                             stream_of(device)),
+          "lct_embedding_grad");
+    if (a[5] == Py_None) return THPVariable_Wrap(fresh);
+    wrote(out);
+    return Py_NewRef(a[5]);
+}
+
+// What a call of the loss works on: x [..., cols], a piece of the weight [rows, cols] that begins at `first` of `vocab`
+// rows (0: it is all of it), targets.
+struct LossOperands {
+    lct_ids ids;
+    Rows x, w;
+    uint64_t cols, first, rows;
+    int device;
+    bool unaligned;
+};
+LossOperands loss_operands(const at::Tensor &x, const at::Tensor &w, const at::Tensor &targets, PyObject *first,
+                           PyObject *vocab)
+{
+    LossOperands o{};
+    need(w.dim() == 2 && w.is_cuda(), "weight must be a CUDA tensor [vocabulary, columns]");
+    if (w.scalar_type() != at::kBFloat16 || x.scalar_type() != at::kBFloat16)
+        check(LCT_ERR_UNSUPPORTED, "x and weights other than BF16");
+    o.rows = static_cast<uint64_t>(w.size(0));
+    o.cols = static_cast<uint64_t>(w.size(1));
+    o.first = number(first);
+    const uint64_t all = number(vocab);
+    o.device = w.get_device();
+    o.ids = ids_of(targets, all ? all : o.rows, "targets");
+    need(targets.get_device() == o.device, "targets and weight must be on one device");
+    o.w = rows_of(w, o.cols, o.rows, o.device, "weight");
+    o.x = rows_of(x, o.cols, o.ids.tokens, o.device, "x");
+    const auto odd = [](const Rows &r, uint64_t n) {
+        return n && (reinterpret_cast<uintptr_t>(r.p) % 16 || (r.ld % 8 && n > 1));
+    };
+    o.unaligned = odd(o.x, o.ids.tokens) || odd(o.w, o.rows);
+    return o;
+}
+const at::Tensor &floats(PyObject *o, uint64_t n, int device, const char *what)
+{
+    const at::Tensor &t = tensor(o, what);
+    if (t.scalar_type() != at::kFloat || !t.is_cuda() || t.get_device() != device || !t.is_contiguous() ||
+        static_cast<uint64_t>(t.numel()) != n) {
+        PyErr_Format(PyExc_ValueError, "%s: expected contiguous float32, %llu values on CUDA device %d", what,
+                     static_cast<unsigned long long>(n), device);
+        throw Raised{};
+    }
+    return t;
+}
+
+// (x, weight, targets, total) -> (loss, lse) or (loss, lse, total)
+PyObject *cross_entropy(PyObject *const *a)
+{
+    const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
+    const at::Tensor &targets = tensor(a[2], "targets must be a tensor");
+    const Held zero(PyLong_FromLong(0));
+    const LossOperands o = loss_operands(x, w, targets, zero.o, zero.o);
+    no_gradient({&x, &w}, "cross_entropy");
+    const bool totals = a[3] == Py_True;
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(o.device));
+    at::Tensor loss = make(targets.sizes(), at::kFloat, o.device), lse = make(targets.sizes(), at::kFloat, o.device), total;
+    if (totals) total = make({3}, at::kFloat, o.device);
+    const uint64_t bytes =
+        lct_loss_work_bytes(o.ids.tokens, o.ids.vocab, o.cols, o.rows, o.unaligned ? LCT_LOSS_UNALIGNED : 0);
+    at::Tensor work = make({static_cast<int64_t>(bytes)}, at::kByte, o.device);
+    check(lct_loss_forward(&o.ids, o.x.p, o.x.ld, o.cols, o.w.p, o.w.ld, 0, o.rows, static_cast<float *>(loss.data_ptr()),
+                           static_cast<float *>(lse.data_ptr()), totals ? static_cast<float *>(total.data_ptr()) : nullptr,
+                           work.data_ptr(), bytes, stream_of(o.device)),
+          "lct_loss_forward");
+    if (!totals) return tuple_of({THPVariable_Wrap(loss), THPVariable_Wrap(lse)});
+    return tuple_of({THPVariable_Wrap(loss), THPVariable_Wrap(lse), THPVariable_Wrap(total)});
+}
+
+// (x, piece, first, vocab, targets, loss, lse, total or None, work) -> None
+PyObject *cross_entropy_piece(PyObject *const *a)
+{
+    const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
+    const LossOperands o = loss_operands(x, w, tensor(a[4], "targets must be a tensor"), a[2], a[3]);
+    const at::Tensor &loss = floats(a[5], o.ids.tokens, o.device, "loss"), &lse = floats(a[6], o.ids.tokens, o.device, "lse");
+    float *total = a[7] == Py_None ? nullptr : static_cast<float *>(floats(a[7], 3, o.device, "total").data_ptr());
+    const at::Tensor &work = tensor(a[8], "work must be a tensor");
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(o.device));
+    check(lct_loss_forward(&o.ids, o.x.p, o.x.ld, o.cols, o.w.p, o.w.ld, o.first, o.rows,
+                           static_cast<float *>(loss.data_ptr()), static_cast<float *>(lse.data_ptr()), total,
+                           work.data_ptr(), static_cast<uint64_t>(work.numel()), stream_of(o.device)),
+          "lct_loss_forward");
+    Py_RETURN_NONE;
+}
+
+struct Upstream {
+    const float *dloss, *scale;
+    uint64_t stride;
+};
+// dloss: a value a token, or one for all; scale: a value that all are multiplied by, or None
+Upstream upstream_of(PyObject *dloss, PyObject *scale, uint64_t tokens, int device)
+{
+    Upstream u{};
+    const at::Tensor &t = tensor(dloss, "dloss must be a tensor");
+    u.stride = t.numel() == 1 && tokens != 1 ? 0 : 1;
+    u.dloss = static_cast<const float *>(floats(dloss, u.stride ? tokens : 1, device, "dloss").data_ptr());
+    if (scale != Py_None) u.scale = static_cast<const float *>(floats(scale, 1, device, "scale").data_ptr());
+    return u;
+}
+
+// (x, weight, targets, loss, lse, dloss, scale or None, weight_grad) -> (dx, dw or None)
+PyObject *cross_entropy_grads(PyObject *const *a)
+{
+    const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
+    const Held zero(PyLong_FromLong(0));
+    const LossOperands o = loss_operands(x, w, tensor(a[2], "targets must be a tensor"), zero.o, zero.o);
+    const at::Tensor &loss = floats(a[3], o.ids.tokens, o.device, "loss"), &lse = floats(a[4], o.ids.tokens, o.device, "lse");
+    const Upstream u = upstream_of(a[5], a[6], o.ids.tokens, o.device);
+    no_gradient({&x, &w, &loss, &lse}, "cross_entropy_grads");
+    const bool weight = a[7] == Py_True;
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(o.device));
+    at::Tensor dx = make(x.sizes(), at::kBFloat16, o.device), dw;
+    if (weight) dw = make(w.sizes(), at::kBFloat16, o.device);
+    const uint64_t bytes = lct_loss_work_bytes(
+        o.ids.tokens, o.ids.vocab, o.cols, o.rows,
+        LCT_LOSS_BACKWARD | (weight ? LCT_LOSS_WEIGHT : 0) | (o.unaligned ? LCT_LOSS_UNALIGNED : 0));
+    at::Tensor work = make({static_cast<int64_t>(bytes)}, at::kByte, o.device);
+    check(lct_loss_backward(&o.ids, o.x.p, o.x.ld, o.cols, o.w.p, o.w.ld, 0, o.rows,
+                            static_cast<const float *>(loss.data_ptr()), static_cast<const float *>(lse.data_ptr()), u.dloss,
+                            u.stride, u.scale, static_cast<uint16_t *>(dx.data_ptr()), o.cols,
+                            weight ? static_cast<uint16_t *>(dw.data_ptr()) : nullptr, o.cols, work.data_ptr(), bytes,
+                            stream_of(o.device)),
+          "lct_loss_backward");
+    return tuple_of({THPVariable_Wrap(dx), weight ? THPVariable_Wrap(dw) : Py_NewRef(Py_None)});
+}
+
+// (x, piece, first, vocab, targets, loss, lse, dloss, scale or None, dx, dw's piece or None, work) -> None
+PyObject *cross_entropy_grads_piece(PyObject *const *a)
+{
+    const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
+    const LossOperands o = loss_operands(x, w, tensor(a[4], "targets must be a tensor"), a[2], a[3]);
+    const at::Tensor &loss = floats(a[5], o.ids.tokens, o.device, "loss"), &lse = floats(a[6], o.ids.tokens, o.device, "lse");
+    const Upstream u = upstream_of(a[7], a[8], o.ids.tokens, o.device);
+    const Rows dx = rows_of(tensor(a[9], "dx must be a tensor"), o.cols, o.ids.tokens, o.device, "dx");
+    Rows dw;
+    if (a[10] != Py_None) dw = rows_of(tensor(a[10], "dw must be a tensor or None"), o.cols, o.rows, o.device, "dw");
+    const at::Tensor &work = tensor(a[11], "work must be a tensor");
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(o.device));
+    check(lct_loss_backward(&o.ids, o.x.p, o.x.ld, o.cols, o.w.p, o.w.ld, o.first, o.rows,
+                            static_cast<const float *>(loss.data_ptr()), static_cast<const float *>(lse.data_ptr()), u.dloss,
+                            u.stride, u.scale, dx.p, dx.ld, dw.p, dw.ld, work.data_ptr(),
+                            static_cast<uint64_t>(work.numel()), stream_of(o.device)),
+          "lct_loss_backward");
+    Py_RETURN_NONE;
+}
+
+// (tokens, vocab, cols, rows, flags) -> bytes
+PyObject *loss_work_bytes(PyObject *const *a)
+{
+    return PyLong_FromUnsignedLongLong(lct_loss_work_bytes(number(a[0]), number(a[1]), number(a[2]), number(a[3]),
+                                                           static_cast<int32_t>(number(a[4]))));
+}
+
 // (LctError)
 PyObject *set_error(PyObject *const *a)
 {
@@ -411,6 +668,13 @@ PyMethodDef methods[] = {method<grad_norm, 1>("grad_norm"),
                          method<adapter_plan, 2>("adapter_plan"),
                          method<adapter_apply, 11>("adapter_apply"),
                          method<adapter_grads, 12>("adapter_grads"),
+                         method<embedding, 6>("embedding"),
+                         method<embedding_grad, 6>("embedding_grad"),
+                         method<cross_entropy, 4>("cross_entropy"),
+                         method<cross_entropy_piece, 9>("cross_entropy_piece"),
+                         method<cross_entropy_grads, 8>("cross_entropy_grads"),
+                         method<cross_entropy_grads_piece, 12>("cross_entropy_grads_piece"),
+                         method<loss_work_bytes, 5>("loss_work_bytes"),
                          method<set_error, 1>("set_error"),
                          {nullptr, nullptr, 0, nullptr}};
 

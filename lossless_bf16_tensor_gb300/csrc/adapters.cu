@@ -1838,28 +1838,6 @@ __global__ void __launch_bounds__(1024) k_adapter_plan(const __grid_constant__ P
 
 namespace {
 
-// How many clusters of a size the GPU holds at once (0: none, or an error).
-template <typename... P>
-uint32_t clusters_at_once(void (*kernel)(P...), uint32_t threads, uint32_t smem, uint32_t cluster)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(cluster);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();  // a size that does not fit is no error of the caller's
-        return 0;
-    }
-    return n > 0 ? static_cast<uint32_t>(n) : 0;
-}
-
 // Clusters take tiles in turn, one block on an SM.  Larger clusters end a
 // tile sooner, but fewer of them fit (36 of four and 15 of eight on 152 SMs),
 // and a turn has a part that no cluster shortens (filling the ring, the

@@ -1,0 +1,487 @@
+// The lookup of tokens' rows in a table, and its gradient.
+//
+//   lookup    out_i = f E[t_i]                         (0 for t_i < 0)
+//   gradient  dE_v = dE0_v + f sum over t_i = v of dy_i
+//
+// Both move rows and compute next to nothing: HBM bounds them.  The gradient
+// reads dy once, in the order of the ids (a stable radix sort of the batch's ids
+// comes first), and writes every row of dE once: sums are held in float32
+// registers, in the tokens' order, so that no atomics are needed and the same
+// inputs give the same bits.  Frequent ids would make one block add thousands of
+// rows; so the sorted tokens are cut into chunks of 32 whatever their ids, and
+// the partial sums of an id that crosses chunks are added by a second kernel.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "../../include/lct.h"
+#include "codec_dev.cuh"
+#include "internal.h"
+#include "rows_dev.cuh"
+#include "tensor_dev.cuh"
+
+namespace lct {
+namespace dev {
+
+// --------------------------------------------------------- sorting the ids
+
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBlocks = 8;
+
+// Stable radix sort of the ids by one cluster: least digit first, a warp
+// counting and placing 32 consecutive ids at a time.  Ids outside 0 .. vocab - 1
+// become `vocab` and end up behind the others.  Then first[v], where v's ids
+// begin (-1: none), and the number of ids that are there.
+__global__ void __launch_bounds__(kSortThreads) k_sort_ids(const __grid_constant__ SortArgs g)
+{
+    extern __shared__ uint32_t counts[];  // [warps][digits], then the block's totals [digits]
+    __shared__ uint32_t part[kSortWarps];
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int digits = 1 << g.bits;
+    uint32_t *total = counts + kSortWarps * digits;
+    uint32_t *mine = counts + warp * digits;
+    const int share = (g.tokens + static_cast<int>(size) * kSortThreads - 1) / (static_cast<int>(size) * kSortThreads) * 32;
+    const int64_t lo = static_cast<int64_t>(rank * kSortWarps + warp) * share;
+    const int64_t hi = min(lo + share, static_cast<int64_t>(g.tokens));
+    pdl_wait();
+    if (g.clear && rank == 0 && threadIdx.x < 2) g.clear[threadIdx.x] = 0;
+    if (g.first)
+        for (int v = rank * kSortThreads + threadIdx.x; v < g.vocab; v += size * kSortThreads) g.first[v] = -1;
+    for (int pass = 0; pass < g.passes; ++pass) {
+        const int to = (g.passes - 1 - pass) & 1, shift = pass * g.bits;
+        auto key_at = [&](int64_t i) -> int {
+            if (i >= hi) return -1;
+            if (pass) return __ldcg(&g.key[to ^ 1][i]);
+            const int64_t id = id_at(g.ids, g.wide, i);
+            return id < 0 || id >= g.vocab ? g.vocab : static_cast<int>(id);
+        };
+        for (int d = lane; d < digits; d += 32) mine[d] = 0;
+        __syncwarp();
+        for (int64_t i = lo + lane; i - lane < hi; i += 32) {
+            const int key = key_at(i);
+            const int d = key < 0 ? -1 : key >> shift & (digits - 1);
+            const uint32_t same = __match_any_sync(kFull, d);
+            if (d >= 0 && lane == __ffs(same) - 1) mine[d] += __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        // each warp's place within the block's ids of a digit
+        for (int d = threadIdx.x; d < digits; d += kSortThreads) {
+            uint32_t sum = 0;
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = counts[w * digits + d];
+                counts[w * digits + d] = sum;
+                sum += c;
+            }
+            total[d] = sum;
+        }
+        cluster_sync();
+        // where the block's ids of a digit go: behind all smaller digits, and this digit's of earlier blocks
+        uint32_t before = 0, all = 0;
+        if (static_cast<int>(threadIdx.x) < digits)
+            for (uint32_t r = 0; r < size; ++r) {
+                const uint32_t c = ld_peer_shared(&total[threadIdx.x], r);
+                if (r < rank) before += c;
+                all += c;
+            }
+        uint32_t sum = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(kFull, sum, o);
+            if (lane >= o) sum += x;
+        }
+        if (lane == 31) part[warp] = sum;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) before += part[w];
+        cluster_sync();  // the totals have been read, and take the places
+        if (static_cast<int>(threadIdx.x) < digits) total[threadIdx.x] = before + sum - all;
+        __syncthreads();
+        for (int64_t i = lo + lane; i - lane < hi; i += 32) {
+            const int key = key_at(i);
+            const int token = pass && i < hi ? __ldcg(&g.order[to ^ 1][i]) : static_cast<int>(i);
+            const int d = key < 0 ? -1 : key >> shift & (digits - 1);
+            const uint32_t same = __match_any_sync(kFull, d);
+            uint32_t at = 0;
+            if (d >= 0) at = mine[d];
+            __syncwarp();
+            if (d >= 0) {
+                const uint32_t place = total[d] + at + __popc(same & ((1u << lane) - 1));
+                g.key[to][place] = key;
+                g.order[to][place] = token;
+                if (lane == __ffs(same) - 1) mine[d] = at + __popc(same);
+            }
+            __syncwarp();
+        }
+        cluster_sync();
+    }
+    for (int64_t i = lo + lane; i < hi; i += 32) {
+        const int key = __ldcg(&g.key[0][i]), last = i ? __ldcg(&g.key[0][i - 1]) : -1;
+        if (key != last) {
+            if (key < g.vocab) {
+                if (g.first) g.first[key] = static_cast<int>(i);
+            } else {
+                *g.count = static_cast<int>(i);
+            }
+        }
+        if (i == g.tokens - 1 && key < g.vocab) *g.count = g.tokens;
+    }
+    if (g.tokens == 0 && rank == 0 && threadIdx.x == 0) *g.count = 0;
+}
+
+// ------------------------------------------------------------------ lookup
+
+// ROWS rows a block at a time: their ids are one trip to memory, the rows
+// themselves the next, and all are asked for before the first is written.
+template <typename T, bool AL, int ROWS>
+__global__ void __launch_bounds__(kRowThreads) k_embedding(const __grid_constant__ LookupArgs g)
+{
+    const int slab = blockIdx.y;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * ROWS;
+    Piece<T, AL> p[ROWS];
+    int64_t id[ROWS];
+    pdl_wait();
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) id[r] = i0 + r < g.tokens ? id_at(g.ids, g.wide, i0 + r) : -1;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t at = id[r] - g.row0;
+        if (at >= 0 && at < g.rows) {
+            p[r].load(static_cast<const T *>(g.table) + at * g.ld_table, slab, g.cols);
+        } else {
+            const T fill = from_float<T>(id[r] < 0 ? 0.0f : __int_as_float(0x7FC00000));
+#pragma unroll
+            for (int e = 0; e < RowPiece<T, AL>::kVec; ++e) p[r].v[e] = fill;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t at = id[r] - g.row0;
+        const bool there = at >= 0 && at < g.rows;
+        if (i0 + r >= g.tokens || (!there && id[r] >= 0 && id[r] < g.vocab)) continue;  // another piece's row
+        if (there && g.scale != 1.0f) {
+#pragma unroll
+            for (int e = 0; e < RowPiece<T, AL>::kVec; ++e) p[r].v[e] = from_float<T>(to_float(p[r].v[e]) * g.scale);
+        }
+        p[r].store(static_cast<T *>(g.out) + (i0 + r) * g.ld_out, slab, g.cols);
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+
+constexpr int kSegTokens = LCT_EMBEDDING_CHUNK;
+constexpr int kSegAhead = 8;  // rows asked for at a time
+
+// A finished row: scaled, added to its base, rounded once.  Compact sums
+// (float32, unscaled) go to the row of the id's first token instead.
+template <typename T, bool AL>
+__device__ __forceinline__ void finish_row(const SegmentArgs &g, int key, int first, int slab,
+                                           const float (&acc)[RowPiece<T, AL>::kVec])
+{
+    using P = RowPiece<T, AL>;
+    if (g.compact) {
+        float *row = static_cast<float *>(g.out) + first * g.ld_out;
+#pragma unroll
+        for (int e = 0; e < P::kVec; ++e)
+            if (P::col(slab, e) < g.cols) row[P::col(slab, e)] = acc[e];
+        return;
+    }
+    Piece<T, AL> p;
+    if (g.base) p.load(static_cast<const T *>(g.base) + key * g.ld_base, slab, g.cols);
+#pragma unroll
+    for (int e = 0; e < P::kVec; ++e)
+        p.v[e] = from_float<T>(g.base ? fmaf(g.scale, acc[e], to_float(p.v[e])) : g.scale * acc[e]);
+    p.store(static_cast<T *>(g.out) + key * g.ld_out, slab, g.cols);
+}
+
+// Partial sums of an id that crosses chunks, [chunk][2][cols]: of one that began
+// earlier (0), of one that begins here and goes on (1).
+__device__ __forceinline__ float *partial(const SegmentArgs &g, int64_t chunk, int which)
+{
+    return g.part + (chunk * 2 + which) * g.cols;
+}
+
+// Rows without tokens: zero, or their base.
+template <typename T, bool AL>
+__device__ __forceinline__ void fill_rows(const SegmentArgs &g, int64_t block)
+{
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    const int64_t r0 = block * g.fill_rows, r1 = min(r0 + g.fill_rows, static_cast<int64_t>(g.vocab));
+    for (int64_t r = r0 + threadIdx.x / 32; r < r1; r += warps) {
+        if (g.first[r] >= 0) continue;
+        T *row = static_cast<T *>(g.out) + r * g.ld_out;
+        const T *base = g.base ? static_cast<const T *>(g.base) + r * g.ld_base : nullptr;
+        // whole 16-byte pieces between the row's ends, where both rows have them
+        const uint32_t skip = (reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T);
+        constexpr int kPer = 16 / sizeof(T);
+        int a = AL || !skip ? 0 : kPer - static_cast<int>(skip), n = 0;
+        if (AL || !base || ((reinterpret_cast<uintptr_t>(base) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0)
+            n = max(0, g.cols - a) / kPer;
+        if (n == 0) a = 0;
+        for (int c = lane; c < a; c += 32) row[c] = base ? base[c] : from_float<T>(0.0f);
+        uint4 *q = reinterpret_cast<uint4 *>(row + a);
+        const uint4 *b = reinterpret_cast<const uint4 *>(base + a);
+#pragma unroll 4
+        for (int c = lane; c < n; c += 32) q[c] = base ? __ldg(b + c) : make_uint4(0, 0, 0, 0);
+        for (int c = a + n * kPer + lane; c < g.cols; c += 32) row[c] = base ? base[c] : from_float<T>(0.0f);
+    }
+}
+
+// Chunks of sorted tokens by the first blocks, rows without tokens by the rest.
+template <typename T, bool AL>
+__global__ void __launch_bounds__(kRowThreads) k_segments(const __grid_constant__ SegmentArgs g)
+{
+    using P = RowPiece<T, AL>;
+    __shared__ int keys[kSegTokens], tokens[kSegTokens];
+    __shared__ float coefs[kSegTokens];
+    pdl_wait();
+    if (blockIdx.x >= g.chunks * g.slabs) {
+        fill_rows<T, AL>(g, blockIdx.x - g.chunks * g.slabs);
+        return;
+    }
+    const int64_t chunk = blockIdx.x / g.slabs;
+    const int slab = blockIdx.x % g.slabs;
+    const int64_t i0 = chunk * kSegTokens;
+    const int n = static_cast<int>(min(static_cast<int64_t>(kSegTokens), *g.count - i0));
+    if (n <= 0) return;
+    for (int j = threadIdx.x; j < n; j += blockDim.x) {
+        keys[j] = g.key[i0 + j];
+        tokens[j] = g.order ? g.order[i0 + j] : static_cast<int>(i0 + j);
+        coefs[j] = g.coef ? g.coef[i0 + j] : 1.0f;
+    }
+    __syncthreads();
+    const bool goes_on = i0 + n < *g.count && g.key[i0 + n] == keys[n - 1];
+    int64_t began = i0 > 0 && g.key[i0 - 1] == keys[0] ? -1 : i0;  // where the id's tokens begin (-1: in an earlier chunk)
+    float acc[P::kVec];
+#pragma unroll
+    for (int e = 0; e < P::kVec; ++e) acc[e] = 0.0f;
+    for (int j0 = 0; j0 < n; j0 += kSegAhead) {
+        Piece<T, AL> p[kSegAhead];
+#pragma unroll
+        for (int j = 0; j < kSegAhead; ++j)
+            if (j0 + j < n) p[j].load(static_cast<const T *>(g.src) + tokens[j0 + j] * g.ld_src, slab, g.cols);
+#pragma unroll
+        for (int j = 0; j < kSegAhead; ++j) {
+            const int at = j0 + j;
+            if (at >= n) break;
+            const float f = coefs[at];
+#pragma unroll
+            for (int e = 0; e < P::kVec; ++e) acc[e] = fmaf(f, to_float(p[j].v[e]), acc[e]);
+            if (at + 1 < n && keys[at + 1] == keys[at]) continue;
+            if (began < 0 || (at == n - 1 && goes_on)) {
+                float *to = partial(g, chunk, began < 0 ? 0 : 1);
+#pragma unroll
+                for (int e = 0; e < P::kVec; ++e)
+                    if (P::col(slab, e) < g.cols) to[P::col(slab, e)] = acc[e];
+            } else {
+                finish_row<T, AL>(g, keys[at], static_cast<int>(began), slab, acc);
+            }
+            began = i0 + at + 1;
+#pragma unroll
+            for (int e = 0; e < P::kVec; ++e) acc[e] = 0.0f;
+        }
+    }
+}
+
+// Ids that cross chunks: the block of the chunk where one begins adds its parts.
+template <typename T, bool AL>
+__global__ void __launch_bounds__(kRowThreads) k_segment_ends(const __grid_constant__ SegmentArgs g)
+{
+    using P = RowPiece<T, AL>;
+    pdl_wait();
+    const int64_t chunk = blockIdx.x / g.slabs, i0 = chunk * kSegTokens, next = i0 + kSegTokens, count = *g.count;
+    const int slab = blockIdx.x % g.slabs, lane = threadIdx.x & 31;
+    if (next >= count) return;
+    const int key = g.key[next - 1];
+    if (g.key[next] != key || (i0 > 0 && g.key[i0] == key && g.key[i0 - 1] == key)) return;
+    // the chunks that the id goes on in
+    int64_t more = 0;
+    for (;; more += 32) {
+        const int64_t at = next + (more + lane) * kSegTokens;
+        const uint32_t same = __ballot_sync(kFull, at < count && g.key[at] == key);
+        if (same != kFull) {
+            more += __ffs(~same) - 1;
+            break;
+        }
+    }
+    float acc[P::kVec];
+    const float *from = partial(g, chunk, 1);
+#pragma unroll
+    for (int e = 0; e < P::kVec; ++e) acc[e] = P::col(slab, e) < g.cols ? from[P::col(slab, e)] : 0.0f;
+#pragma unroll 4
+    for (int64_t c = 1; c <= more; ++c) {
+        from = partial(g, chunk + c, 0);
+#pragma unroll
+        for (int e = 0; e < P::kVec; ++e)
+            if (P::col(slab, e) < g.cols) acc[e] += from[P::col(slab, e)];
+    }
+    const int first = g.compact ? g.first[key] : 0;
+    finish_row<T, AL>(g, key, first, slab, acc);
+}
+
+}  // namespace dev
+
+// ------------------------------------------------------------------ launches
+
+cudaError_t launch_sort_ids(SortArgs g, cudaStream_t s)
+{
+    int need = 1;
+    while (need < 31 && g.vocab >> need) ++need;  // bits of `vocab`, the largest key
+    g.passes = (need + 8) / 9;
+    g.bits = (need + g.passes - 1) / g.passes;
+    const uint32_t smem = (dev::kSortWarps + 1) * (4u << g.bits);
+    return launch<true>(dev::k_sort_ids, dim3(g.tokens > 4096 ? dev::kSortBlocks : 1), dev::kSortThreads, smem,
+                        g.tokens > 4096 ? dev::kSortBlocks : 1, s, g);
+}
+
+namespace {
+
+template <typename T, bool AL>
+cudaError_t lookup(const LookupArgs &g, cudaStream_t s)
+{
+    uint32_t threads, slabs;
+    row_shape(g.cols, dev::RowPiece<T, AL>::kVec, &threads, &slabs);
+    if (g.tokens * static_cast<uint64_t>(slabs) <= 152 * 8)
+        return launch<true>(dev::k_embedding<T, AL, 1>, dim3(static_cast<uint32_t>(g.tokens), slabs), threads, 0, 1, s, g);
+    return launch<true>(dev::k_embedding<T, AL, 4>, dim3(static_cast<uint32_t>((g.tokens + 3) / 4), slabs), threads, 0, 1, s,
+                        g);
+}
+
+template <typename T, bool AL>
+cudaError_t segments(SegmentArgs g, bool fill, cudaStream_t s)
+{
+    uint32_t threads;
+    row_shape(g.cols, dev::RowPiece<T, AL>::kVec, &threads, &g.slabs);
+    g.chunks = (static_cast<uint32_t>(g.tokens) + dev::kSegTokens - 1) / dev::kSegTokens;
+    // a fill block's rows: about 64 KB
+    g.fill_rows = static_cast<int32_t>(std::max<uint64_t>(threads / 32, 65536 / (sizeof(T) * static_cast<uint64_t>(g.cols))));
+    const uint32_t fills = fill ? (static_cast<uint32_t>(g.vocab) + g.fill_rows - 1) / g.fill_rows : 0;
+    cudaError_t rc = cudaSuccess;
+    if (g.chunks * g.slabs + fills)
+        rc = launch<true>(dev::k_segments<T, AL>, dim3(g.chunks * g.slabs + fills), threads, 0, 1, s, g);
+    if (rc == cudaSuccess && g.chunks > 1)
+        rc = launch<true>(dev::k_segment_ends<T, AL>, dim3((g.chunks - 1) * g.slabs), threads, 0, 1, s, g);
+    return rc;
+}
+
+}  // namespace
+
+cudaError_t launch_segments(const SegmentArgs &g, bool wide, bool aligned, bool fill, cudaStream_t s)
+{
+    if (wide) return aligned ? segments<float, true>(g, fill, s) : segments<float, false>(g, fill, s);
+    return aligned ? segments<__nv_bfloat16, true>(g, fill, s) : segments<__nv_bfloat16, false>(g, fill, s);
+}
+
+cudaError_t launch_lookup(const LookupArgs &g, bool wide, bool aligned, cudaStream_t s)
+{
+    if (wide) return aligned ? lookup<float, true>(g, s) : lookup<float, false>(g, s);
+    return aligned ? lookup<__nv_bfloat16, true>(g, s) : lookup<__nv_bfloat16, false>(g, s);
+}
+
+lct_status check_ids(const lct_ids *ids)
+{
+    if (!ids || ids->vocab == 0) return LCT_ERR_INVALID_ARG;
+    if (ids->tokens > LCT_VOCAB_MAX_TOKENS || ids->vocab > LCT_VOCAB_MAX) return LCT_ERR_UNSUPPORTED;
+    if (ids->wide != 0 && ids->wide != 1) return LCT_ERR_INVALID_ARG;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(ids->d_ids);
+    if (ids->tokens && (!at || at % (ids->wide ? 8 : 4))) return LCT_ERR_INVALID_ARG;
+    return LCT_OK;
+}
+
+namespace {
+
+uint64_t value_bytes(int32_t dtype) { return dtype == LCT_DTYPE_F32 ? 4 : 2; }
+
+}  // namespace
+}  // namespace lct
+
+using namespace lct;
+
+extern "C" lct_status lct_embedding(const lct_ids *ids, const void *d_table, uint64_t ld_table, int32_t dtype,
+                                    uint64_t first, uint64_t rows, uint64_t cols, float scale, void *d_out,
+                                    uint64_t ld_out, void *stream)
+{
+    const lct_status rc = check_ids(ids);
+    if (rc != LCT_OK) return rc;
+    if (dtype != LCT_DTYPE_BF16 && dtype != LCT_DTYPE_F32) return LCT_ERR_UNSUPPORTED;
+    if (cols == 0 || first > ids->vocab || rows > ids->vocab - first) return LCT_ERR_INVALID_ARG;
+    if (cols > LCT_VOCAB_MAX_COLS) return LCT_ERR_UNSUPPORTED;
+    if (ids->tokens == 0) return LCT_OK;
+    const uint64_t size = value_bytes(dtype);
+    const Matrix table{d_table, ld_table, cols, rows, size}, out{d_out, ld_out, cols, ids->tokens, size};
+    if (!matrix_ok(table) || !matrix_ok(out)) return LCT_ERR_INVALID_ARG;
+    if (!apart(out, table) || !apart(out, ids->d_ids, ids->tokens * (ids->wide ? 8 : 4))) return LCT_ERR_INVALID_ARG;
+    LookupArgs g;
+    g.ids = ids->d_ids;
+    g.wide = ids->wide;
+    g.table = d_table;
+    g.out = d_out;
+    g.ld_table = static_cast<int64_t>(ld_table);
+    g.ld_out = static_cast<int64_t>(ld_out);
+    g.row0 = static_cast<int64_t>(first);
+    g.rows = static_cast<int64_t>(rows);
+    g.vocab = static_cast<int64_t>(ids->vocab);
+    g.tokens = static_cast<int64_t>(ids->tokens);
+    g.cols = static_cast<int32_t>(cols);
+    g.scale = scale;
+    return launch_lookup(g, dtype == LCT_DTYPE_F32, matrix_al(table) && matrix_al(out) && cols * size % 16 == 0,
+                         static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? LCT_OK
+               : LCT_ERR_CUDA;
+}
+
+extern "C" lct_status lct_embedding_grad(const lct_ids *ids, const void *d_dy, uint64_t ld_dy, int32_t dtype,
+                                         uint64_t cols, float scale, const void *d_base, uint64_t ld_base, void *d_out,
+                                         uint64_t ld_out, void *d_work, void *stream)
+{
+    const lct_status rc = check_ids(ids);
+    if (rc != LCT_OK) return rc;
+    if (dtype != LCT_DTYPE_BF16 && dtype != LCT_DTYPE_F32) return LCT_ERR_UNSUPPORTED;
+    if (cols == 0) return LCT_ERR_INVALID_ARG;
+    if (cols > LCT_VOCAB_MAX_COLS) return LCT_ERR_UNSUPPORTED;
+    const uint64_t size = value_bytes(dtype), t = ids->tokens;
+    const Matrix dy{d_dy, ld_dy, cols, t, size}, out{d_out, ld_out, cols, ids->vocab, size};
+    const Matrix base{d_base, ld_base, cols, d_base ? ids->vocab : 0, size};
+    const uint64_t work = LCT_EMBEDDING_WORK_BYTES(t, ids->vocab, cols), id_bytes = t * (ids->wide ? 8 : 4);
+    const bool in_place = d_base == d_out && ld_base == ld_out;
+    if (!matrix_ok(dy) || !matrix_ok(out) || !matrix_ok(base)) return LCT_ERR_INVALID_ARG;
+    if (!d_work || reinterpret_cast<uintptr_t>(d_work) % 16) return LCT_ERR_INVALID_ARG;
+    if (!apart(out, dy) || (!in_place && !apart(out, base)) || !apart(out, ids->d_ids, id_bytes) ||
+        !apart(out, d_work, work) || !apart(dy, d_work, work) || !apart(base, d_work, work) ||
+        !apart(d_work, work, ids->d_ids, id_bytes))
+        return LCT_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const uint64_t t4 = (t + 3) / 4 * 4;
+    int32_t *w = static_cast<int32_t *>(d_work);
+    SortArgs sort{};
+    sort.ids = ids->d_ids;
+    sort.wide = ids->wide;
+    sort.count = w;
+    sort.key[0] = w + 4;
+    sort.key[1] = sort.key[0] + t4;
+    sort.order[0] = sort.key[1] + t4;
+    sort.order[1] = sort.order[0] + t4;
+    sort.first = sort.order[1] + t4;
+    sort.tokens = static_cast<int32_t>(t);
+    sort.vocab = static_cast<int32_t>(ids->vocab);
+    if (launch_sort_ids(sort, s) != cudaSuccess) return LCT_ERR_CUDA;
+    SegmentArgs g{};
+    g.src = d_dy;
+    g.ld_src = static_cast<int64_t>(ld_dy);
+    g.key = sort.key[0];
+    g.order = sort.order[0];
+    g.first = sort.first;
+    g.count = sort.count;
+    g.scale = scale;
+    g.base = d_base;
+    g.ld_base = static_cast<int64_t>(ld_base);
+    g.out = d_out;
+    g.ld_out = static_cast<int64_t>(ld_out);
+    g.part = reinterpret_cast<float *>(sort.first + (ids->vocab + 3) / 4 * 4);
+    g.cols = static_cast<int32_t>(cols);
+    g.tokens = static_cast<int32_t>(t);
+    g.vocab = static_cast<int32_t>(ids->vocab);
+    const bool aligned = cols * size % 16 == 0 && matrix_al(out) && matrix_al(dy) && matrix_al(base);
+    return launch_segments(g, dtype == LCT_DTYPE_F32, aligned, !in_place, s) == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
+}

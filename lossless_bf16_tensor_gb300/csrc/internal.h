@@ -196,4 +196,71 @@ cudaError_t launch_adapter(const AdapterArgs &a, bool back, cudaStream_t s);
 cudaError_t launch_adapter_grad(const AdapterArgs &a, cudaStream_t s);
 cudaError_t launch_adapter_plan(const PlanArgs &a, cudaStream_t s);
 
+// A matrix of rows in memory, as a call gets it, with values of `size` bytes.
+struct Matrix {
+    const void *p;
+    uint64_t ld, cols, rows, size;
+};
+inline uint64_t matrix_bytes(const Matrix &m) { return m.rows ? m.size * ((m.rows - 1) * m.ld + m.cols) : 0; }
+inline bool matrix_ok(const Matrix &m)
+{
+    return !m.rows || (m.p && reinterpret_cast<uintptr_t>(m.p) % m.size == 0 && m.ld >= m.cols && m.ld <= kMaxN);
+}
+// Whether every row begins at a 16-byte boundary (and TMA's strides hold the distance between rows).
+inline bool matrix_al(const Matrix &m)
+{
+    return !m.rows || (reinterpret_cast<uintptr_t>(m.p) % 16 == 0 &&
+                       ((m.ld * m.size % 16 == 0 && m.ld < 1ull << 36) || m.rows == 1));
+}
+inline bool apart(const void *x, uint64_t xn, const void *p, uint64_t n)
+{
+    const uint64_t xl = reinterpret_cast<uint64_t>(x), pl = reinterpret_cast<uint64_t>(p);
+    return !x || !p || !xn || !n || xl + xn <= pl || pl + n <= xl;
+}
+inline bool apart(const Matrix &m, const void *p, uint64_t n) { return apart(m.p, matrix_bytes(m), p, n); }
+// Whether two matrices share no value: apart in memory, or column slices of rows with one stride that do not meet.
+inline bool apart(const Matrix &x, const Matrix &y)
+{
+    if (!x.rows || !y.rows || apart(x.p, matrix_bytes(x), y.p, matrix_bytes(y))) return true;
+    const uint64_t xl = reinterpret_cast<uint64_t>(x.p), yl = reinterpret_cast<uint64_t>(y.p), ld = x.ld * x.size;
+    if (x.ld != y.ld || x.size != y.size || (xl ^ yl) % x.size) return false;
+    const uint64_t d = yl >= xl ? (yl - xl) % ld : (ld - (xl - yl) % ld) % ld;
+    return d >= x.cols * x.size && d + y.cols * y.size <= ld;
+}
+
+// Ids sorted: key and order [0] are the result, [1] scratch; first[v] (or NULL), where v's begin, -1 without any.
+struct SortArgs {
+    const void *ids;
+    int32_t *key[2], *order[2], *first, *count;
+    int32_t *clear;  // two words that become zero, or NULL
+    int32_t tokens, vocab, bits, passes;  // bits a pass and passes are set by the launcher
+    bool wide;
+};
+struct LookupArgs {
+    const void *ids, *table;
+    void *out;
+    int64_t ld_table, ld_out, row0, rows, vocab, tokens;  // the table's rows are row0 .. row0 + rows of vocab
+    int32_t cols;
+    float scale;
+    bool wide;
+};
+// Sums of the rows of equal ids, in sorted order.
+struct SegmentArgs {
+    const void *src;          // row order[i] (NULL: row i) belongs to key[i]
+    const int32_t *key, *order, *first, *count;
+    const float *coef;        // [i], or NULL: 1
+    const void *base;         // or NULL
+    void *out;                // row key[i]; compact: float32 rows, row first[key[i]]
+    float *part;              // [chunks][2][cols]
+    int64_t ld_src, ld_base, ld_out;
+    float scale;
+    int32_t cols, tokens, vocab, fill_rows;
+    uint32_t chunks, slabs;   // set by the launcher
+    bool compact;
+};
+cudaError_t launch_sort_ids(SortArgs a, cudaStream_t s);
+cudaError_t launch_lookup(const LookupArgs &a, bool wide, bool aligned, cudaStream_t s);  // wide: float32 values
+cudaError_t launch_segments(const SegmentArgs &a, bool wide, bool aligned, bool fill, cudaStream_t s);
+lct_status check_ids(const lct_ids *ids);
+
 }  // namespace lct

@@ -1,0 +1,1122 @@
+// The cross entropy of a projection onto a large vocabulary, and its gradients,
+// a piece of the vocabulary at a time, without keeping logits.  For a token i
+// with target t_i, and c_i the gradient of its loss:
+//
+//   z_iv = x_i W_v,  l_i = log sum_v exp z_iv,  loss_i = l_i - z_{i,t_i}
+//   g_iv = c_i (exp(z_iv - l_i) - [v = t_i]),  dx = g W,  dW = g^T x
+//
+// The four products (z, z again, g W, g^T x) are one kernel, k_product, with four
+// ends.  The first turns its tile of z into each row's maximum and sum of
+// exponentials, which k_loss_merge joins over the tiles and pieces: what leaves
+// the SMs is 16 bytes a token and tile.  The second computes z again and writes
+// g as BF16, for a part of the piece that is bounded (kGradValues), which the
+// other two read.  Tensor cores bound all of them where tokens are many; where
+// they are few, reading W from HBM does.
+//
+// Rounding: products take BF16 and add in float32.  g is rounded to BF16 without
+// its target's entry: that one, c_i (exp(-loss_i) - 1), is as large as all others
+// of its row together, and goes into dx and dW in float32 (dx: in k_loss_finish;
+// dW: sums over the tokens of one target, k_segments, added as dW's tile is
+// written), so that both are rounded once.
+//
+// Tokens without a target are left out of the gradients' products: the others are
+// packed in the order of their targets, which the sums over a target's tokens
+// need anyway.  What stands in the x of such a token reaches nothing.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "../../include/lct.h"
+#include "codec_dev.cuh"
+#include "internal.h"
+#include "rows_dev.cuh"
+#include "tensor_dev.cuh"
+
+namespace lct {
+
+enum Product { kLogits, kSoftmax, kDx, kDw };
+
+struct ProductArgs {
+    int32_t m, n, k;        // rows, columns and depth of the result
+    const int32_t *count;   // tokens that are there (rows, or dW's depth); NULL: as given
+    int32_t *status;        // latched: a wait that ran out
+    int32_t splits;         // kDx: parts of the depth, each with a result of its own
+    bool add;               // kDx: to what is there
+    bool begins;            // kLogits: a call's first product clears the status and the counter behind it
+    const void *ids;        // kLogits: the targets
+    bool wide;
+    int64_t row0;           // the vocabulary's row that column 0 (kDw: row 0) is
+    float2 *part;           // kLogits: [tiles of 128 columns][m], maximum and sum of exponentials
+    float *mine;            // kLogits: the targets' logits
+    const int32_t *target;  // kSoftmax, packed: targets, l and c
+    const float *lse, *share;
+    const float *extra;     // kDw: the targets' sums, row first[v] (-1: none)
+    const int32_t *first;
+    int64_t ld_extra;
+    __nv_bfloat16 *out;     // kDw, rows at any address
+    int64_t ld_out;
+    bool boxes;             // the result is written by boxes (maps.c)
+};
+struct ProductMaps {
+    CUtensorMap a, b, c;
+};
+struct MergeArgs {
+    const float2 *part;     // [slots][tokens]
+    float2 *state;          // [tokens], from piece to piece
+    const float *mine;
+    const void *ids;
+    float *loss, *lse, *total;  // total: sum, mean, 1 / count (or NULL)
+    double *sums;           // a block's, for the total
+    int32_t *counts, *counter;
+    const int32_t *status;
+    int64_t tokens, vocab;
+    int32_t slots, blocks, block0;
+    bool wide, begins, ends;
+};
+struct PackArgs {
+    const __nv_bfloat16 *src;
+    __nv_bfloat16 *dst;
+    const int32_t *order, *count;  // or NULL: all rows, as they are
+    const float *dloss, *scale, *loss, *lse;
+    float *lse_out, *share_out, *coef_out;
+    int64_t ld_src, ld_dst, dloss_stride;
+    int32_t rows, cols;
+};
+struct FinishArgs {
+    const float *part;             // [splits][tokens][ld_part]
+    const int32_t *key, *order, *count, *status;
+    const float *coef;
+    const __nv_bfloat16 *w;        // the vocabulary's matrix, or (gathered) the targets' rows in the packed order
+    const void *ids;
+    __nv_bfloat16 *dx;
+    int64_t ld_part, ld_w, ld_dx, tokens;
+    int32_t splits, cols;
+    bool gathered, wide;
+};
+
+namespace dev {
+
+// --------------------------------------------------------- products by pairs
+
+// A tile of 256 by 256 belongs to two blocks of a cluster, which multiply as
+// one (cta_group::2): each holds 128 rows of A, 128 of the columns of B, and the
+// sums of its rows.  Against a block alone on 128 by 256, each operand byte in
+// shared memory is used twice as often.
+constexpr int kTile = 256, kHalfTile = 128, kDepth = 64;
+constexpr int kStages = 6;
+constexpr uint32_t kOperand = kHalfTile * 128;  // 128 rows (or columns) by 64 of depth
+constexpr uint32_t kStage = 2 * kOperand;
+constexpr int kEndWarps = 8, kFirstEndWarp = 4;
+constexpr int kProductThreads = 32 * (kFirstEndWarp + kEndWarps);
+constexpr uint32_t kStagingAt = kStages * kStage, kStaging = 32 * 128;  // a warp's 32 rows of 128 bytes
+constexpr uint32_t kProductBytes = kStagingAt + kEndWarps * kStaging + 1024;
+constexpr int kGroup = 16;  // tiles of rows that are worked on side by side
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t word, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+// The barrier at this place in both blocks gets an arrival when the products issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+__device__ __forceinline__ void pair_alloc(uint32_t *at, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(at)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_free(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+// A box into this block's shared memory, which tells a barrier of the pair's first block (`bar`: its address in the
+// cluster).
+__device__ __forceinline__ void pair_box(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(m), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void store_box(const CUtensorMap *m, int x, int y, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(m), "r"(x),
+                 "r"(y), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void store_box(const CUtensorMap *m, int x, int y, int z, uint32_t src, bool add)
+{
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                         m),
+                     "r"(x), "r"(y), "r"(z), "r"(src)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m),
+                     "r"(x), "r"(y), "r"(z), "r"(src)
+                     : "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// 32 columns of this lane's row, and the wait for them (one statement: nothing that uses them can come between).
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32])
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// An item of work: a tile, and the steps of depth that it takes.
+struct Item {
+    int tm, tn, split, k0, k1;
+};
+__device__ __forceinline__ Item item_at(int item, int tiles_m, int tiles_n, int splits, int depth)
+{
+    Item w;
+    const int tiles = tiles_m * tiles_n;
+    w.split = item / tiles;
+    const int t = item - w.split * tiles;
+    // groups of kGroup tiles of rows, whose operand stays in L2 while the columns go by
+    const int g = t / (kGroup * tiles_n), in = t - g * kGroup * tiles_n;
+    const int high = min(kGroup, tiles_m - g * kGroup);
+    w.tn = in / high;
+    w.tm = g * kGroup + in - w.tn * high;
+    w.k0 = static_cast<int>(static_cast<int64_t>(depth) * w.split / splits);
+    w.k1 = static_cast<int>(static_cast<int64_t>(depth) * (w.split + 1) / splits);
+    return w;
+}
+
+// Each row's maximum and sum of exponentials of 32 columns joins (m, s).
+__device__ __forceinline__ void join32(const float (&z)[32], float &m, float &s)
+{
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) top = fmaxf(top, z[i]);
+    const float at = top == -INFINITY ? 0.0f : top * kLog2e;
+    float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) a[i & 3] += exp2_fast(fmaf(z[i], kLog2e, -at));
+    s = fmaf(s, exp2_fast(fmaf(m, kLog2e, -at)), (a[0] + a[1]) + (a[2] + a[3]));
+    m = top;
+}
+
+// Warps by what they do: warp 0 loads boxes (TMA), warp 1 of the first block
+// issues the products, warps 4 to 11 turn sums into results, two to each
+// quarter of the rows.  Sums are double-buffered in TMEM, so that a tile's end
+// runs while the next one's products do.
+template <int OP>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    k_product(const __grid_constant__ ProductArgs g, const __grid_constant__ ProductMaps maps)
+{
+    constexpr bool kAcrossA = OP == kDw, kAcrossB = OP == kDx || OP == kDw;
+    constexpr int S = kStages;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[S], freed[S], done[2], drained[2];
+    __shared__ uint32_t tmem_at;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+    if (warp == 0) pair_alloc(&tmem_at, 512);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&freed[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&done[i], 1);
+            mbar_init(&drained[i], 2 * kEndWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1 && lane < (OP == kLogits || (OP == kDw && !g.boxes) ? 2 : 3))
+        fetch_map(lane == 0 ? &maps.a : lane == 1 ? &maps.b : &maps.c);
+    tc_before();
+    cluster_sync();
+    tc_after();
+    const uint32_t tmem = tmem_at;
+    pdl_wait();
+    if (OP == kLogits && g.begins && blockIdx.x == 0 && threadIdx.x == 0) {
+        g.status[0] = 0;
+        g.status[1] = 0;
+    }
+    int m = g.m, k = g.k;
+    if (g.count) {
+        const int there = max(0, *g.count);
+        if (OP == kDw)
+            k = min(k, there);
+        else
+            m = min(m, there);
+    }
+    const int tiles_m = (m + kTile - 1) / kTile, tiles_n = (g.n + kTile - 1) / kTile, depth = (k + kDepth - 1) / kDepth;
+    const int items = tiles_m * tiles_n * g.splits;
+    Waiter waiter;
+    // a warp's lanes give up together
+    auto wait = [&](uint64_t *bar, int parity) {
+        waiter.wait_cluster(bar, parity);
+        waiter.dead = __any_sync(kFull, waiter.dead);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------- boxes
+        int i = 0;
+        for (int item = pair; item < items; item += pairs) {
+            const Item w = item_at(item, tiles_m, tiles_n, g.splits, depth);
+            const int row = w.tm * kTile + rank * kHalfTile, col = w.tn * kTile + rank * kHalfTile;
+            for (int d = w.k0; d < w.k1; ++d, ++i) {
+                const int s = i % S;
+                if (i >= S) wait(&freed[s], (i / S - 1) & 1);
+                if (elect() && !waiter.dead) {
+                    const uint32_t bar = peer_addr(smem_addr(&full[s]), 0), a = base + s * kStage, b = a + kOperand;
+                    if (rank == 0) mbar_expect_tx(&full[s], 2 * kStage);
+                    if (kAcrossA) {
+                        pair_box(a, &maps.a, row, d * kDepth, bar);
+                        pair_box(a + kOperand / 2, &maps.a, row + 64, d * kDepth, bar);
+                    } else {
+                        pair_box(a, &maps.a, d * kDepth, row, bar);
+                    }
+                    if (kAcrossB) {
+                        pair_box(b, &maps.b, col, d * kDepth, bar);
+                        pair_box(b + kOperand / 2, &maps.b, col + 64, d * kDepth, bar);
+                    } else {
+                        pair_box(b, &maps.b, d * kDepth, col, bar);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        // the block does not end before its boxes have been used
+        for (int j = max(0, i - S); j < i; ++j) wait(&freed[j % S], (j / S) & 1);
+    } else if (warp == 1 && rank == 0) {
+        // ---------------------------------------------------------- products
+        constexpr uint32_t word = (1u << 4) | (1u << 7) | (1u << 10) | (kAcrossA ? 1u << 15 : 0u) |
+                                  (kAcrossB ? 1u << 16 : 0u) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+        const uint64_t a0 = operand(base, kAcrossA ? kOperand / 2 : 0);
+        const uint64_t b0 = operand(base + kOperand, kAcrossB ? kOperand / 2 : 0);
+        int i = 0, t = 0;
+        for (int item = pair; item < items; item += pairs) {
+            const Item w = item_at(item, tiles_m, tiles_n, g.splits, depth);
+            if (w.k1 <= w.k0) continue;
+            if (t >= 2) wait(&drained[t & 1], (t / 2 - 1) & 1);
+            const uint32_t sums = tmem + (t & 1) * kTile;
+            for (int d = w.k0; d < w.k1; ++d, ++i) {
+                const int s = i % S;
+                wait(&full[s], (i / S) & 1);
+                tc_after();
+                if (elect() && !waiter.dead) {
+                    const uint64_t a = a0 + s * (kStage >> 4), b = b0 + s * (kStage >> 4);
+#pragma unroll
+                    for (int j = 0; j < kDepth / 16; ++j)
+                        pair_mma(sums, a + j * (kAcrossA ? 128 : 2), b + j * (kAcrossB ? 128 : 2), word, d > w.k0 || j > 0);
+                    pair_commit(&freed[s]);
+                    if (d == w.k1 - 1) pair_commit(&done[t & 1]);
+                }
+                __syncwarp();
+            }
+            ++t;
+        }
+        // every product has ended before the block does
+        for (int j = max(0, t - 2); j < t; ++j) wait(&done[j & 1], (j / 2) & 1);
+    } else if (warp >= kFirstEndWarp) {
+        // -------------------------------------------------------------- ends
+        const int quarter = warp & 3, half = (warp - kFirstEndWarp) / 4;
+        const uint32_t staging = base + kStagingAt + (warp - kFirstEndWarp) * kStaging;
+        int t = 0;
+        for (int item = pair; item < items; item += pairs) {
+            const Item w = item_at(item, tiles_m, tiles_n, g.splits, depth);
+            const bool some = w.k1 > w.k0;
+            if (some) {
+                wait(&done[t & 1], (t / 2) & 1);
+                tc_after();
+            }
+            if (waiter.dead) break;
+            const uint32_t sums = tmem + (t & 1) * kTile + half * kHalfTile + (static_cast<uint32_t>(quarter * 32) << 16);
+            const int row0 = w.tm * kTile + rank * kHalfTile + quarter * 32, row = row0 + lane;
+            const int col0 = w.tn * kTile + half * kHalfTile;
+            auto load = [&](int c, float(&v)[32]) {
+                if (some) {
+                    tmem_load32(sums + c, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                }
+                if (some && c == kHalfTile - 32) {  // the last of them: the next products may take their place
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                         peer_addr(smem_addr(&drained[t & 1]), 0))
+                                     : "memory");
+                }
+            };
+            if (OP == kLogits) {
+                const int64_t id = row < m ? id_at(g.ids, g.wide, row) - g.row0 - col0 : -1;
+                float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < kHalfTile; c += 32) {
+                    float v[32];
+                    load(c, v);
+                    if (col0 + c + 32 > g.n) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (col0 + c + e >= g.n) v[e] = -INFINITY;
+                    }
+                    if (id >= c && id < c + 32 && col0 + id < g.n) {
+                        const int at = static_cast<int>(id) - c;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e == at) g.mine[row] = v[e];
+                    }
+                    join32(v, top, sum);
+                }
+                if (row < m && col0 < g.n) g.part[static_cast<int64_t>(w.tn * 2 + half) * m + row] = make_float2(top, sum);
+            } else if (OP == kDx) {
+#pragma unroll 1
+                for (int c = 0; c < kHalfTile; c += 32) {
+                    float v[32];
+                    load(c, v);
+                    if (lane == 0) bulk_wait_read();  // the last box has left
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        store16(staging + swz(lane, q),
+                                make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                           __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0 && col0 + c < g.n && row0 < m) {
+                        store_box(&maps.c, col0 + c, row0, w.split, staging, g.add);
+                        bulk_commit();
+                    }
+                }
+            } else {
+                int target = -1;
+                float lse = 0.0f, share = 0.0f;
+                const float *extra = nullptr;
+                if (OP == kSoftmax && row < m) {
+                    target = static_cast<int>(g.target[row] - g.row0) - col0;
+                    lse = g.lse[row] * kLog2e;
+                    share = g.share[row];
+                }
+                if (OP == kDw && row < m) {
+                    const int at = g.first[g.row0 + row];
+                    if (at >= 0) extra = g.extra + at * g.ld_extra + col0;
+                }
+#pragma unroll 1
+                for (int c = 0; c < kHalfTile; c += 64) {
+                    uint32_t packed[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v[32];
+                        load(c + 32 * h, v);
+                        if (OP == kSoftmax) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                v[e] = exp2_fast(fmaf(v[e], kLog2e, -lse)) * share;
+                                if (c + 32 * h + e == target || row >= m) v[e] = 0.0f;
+                            }
+                        } else if (extra) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                if (col0 + c + 32 * h + 4 * q >= g.n) break;
+                                const float4 more = *reinterpret_cast<const float4 *>(extra + c + 32 * h + 4 * q);
+                                v[4 * q] += more.x, v[4 * q + 1] += more.y, v[4 * q + 2] += more.z, v[4 * q + 3] += more.w;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) packed[16 * h + e] = pack2(v[2 * e], v[2 * e + 1]);
+                    }
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        store16(staging + swz(lane, q),
+                                make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2], packed[4 * q + 3]));
+                    if (OP == kSoftmax || g.boxes) {
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0 && col0 + c < g.n && row0 < g.m) {
+                            store_box(&maps.c, col0 + c, row0, staging);
+                            bulk_commit();
+                        }
+                    } else {
+                        __syncwarp();
+                        for (int r = 0; r < 32 && row0 + r < m; ++r) {
+                            __nv_bfloat16 *to = g.out + (row0 + r) * g.ld_out + col0 + c;
+#pragma unroll
+                            for (int e = lane; e < 64; e += 32) {
+                                uint16_t x;
+                                asm volatile("ld.shared.u16 %0, [%1];"
+                                             : "=h"(x)
+                                             : "r"(staging + swz(r, e / 8) + (e & 7) * 2)
+                                             : "memory");
+                                if (col0 + c + e < g.n) to[e] = __ushort_as_bfloat16(x);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (some) ++t;
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+    if (waiter.dead) atomicCAS(reinterpret_cast<unsigned int *>(g.status), 0u, static_cast<unsigned int>(LCT_ERR_TIMEOUT));
+    __syncwarp();
+    tc_before();
+    cluster_sync();
+    tc_after();
+    if (warp == 0) pair_free(tmem, 512);
+}
+
+// -------------------------------------------------- the loss from its pieces
+
+constexpr int kMergeTokens = 32, kMergeGroups = 32;
+
+__device__ __forceinline__ void join(float &m, float &s, float2 o)
+{
+    const float top = fmaxf(m, o.x), at = top == -INFINITY ? 0.0f : top;
+    s = s * exp2_fast((m - at) * kLog2e) + o.y * exp2_fast((o.x - at) * kLog2e);
+    m = top;
+}
+
+// Joins the tiles' maxima and sums of 32 tokens a block with the state of the
+// pieces before; after the last piece, the losses.  Their sum (double, in the
+// order of the blocks) is made by the last block to come.
+__global__ void __launch_bounds__(1024) k_loss_merge(const __grid_constant__ MergeArgs g)
+{
+    __shared__ float2 joined[kMergeGroups][kMergeTokens];
+    __shared__ double sums[32];
+    __shared__ int counts[32];
+    __shared__ bool is_last;
+    const int lane = threadIdx.x & 31, group = threadIdx.x / 32;
+    const int64_t token = static_cast<int64_t>(blockIdx.x) * kMergeTokens + lane;
+    pdl_wait();
+    float m = -INFINITY, s = 0.0f;
+    if (token < g.tokens) {
+#pragma unroll 4
+        for (int i = group; i < g.slots; i += kMergeGroups) join(m, s, g.part[static_cast<int64_t>(i) * g.tokens + token]);
+    }
+    joined[group][lane] = make_float2(m, s);
+    __syncthreads();
+    double loss = 0.0;
+    int counted = 0;
+    if (group == 0 && token < g.tokens) {
+        for (int i = 1; i < kMergeGroups; ++i) join(m, s, joined[i][lane]);
+        if (!g.begins) join(m, s, g.state[token]);
+        if (!g.ends) {
+            g.state[token] = make_float2(m, s);
+        } else {
+            const int64_t id = id_at(g.ids, g.wide, token);
+            const float lse = *g.status ? __int_as_float(0x7FC00000) : m + logf(s);
+            const float l = id < 0 ? 0.0f : id >= g.vocab ? __int_as_float(0x7FC00000) : lse - g.mine[token];
+            g.lse[token] = lse;
+            g.loss[token] = l;
+            loss = l;
+            counted = id >= 0;
+        }
+    }
+    if (!g.ends || !g.total) return;
+    if (group == 0) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            loss += __shfl_xor_sync(kFull, loss, o);
+            counted += __shfl_xor_sync(kFull, counted, o);
+        }
+        if (lane == 0) {
+            g.sums[blockIdx.x + g.block0] = loss;
+            g.counts[blockIdx.x + g.block0] = counted;
+            __threadfence();
+            is_last = atomicAdd(g.counter, 1) == g.blocks - 1;
+        }
+    }
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    loss = 0.0;
+    counted = 0;
+    for (int i = threadIdx.x; i < g.blocks; i += blockDim.x) {
+        loss += __ldcg(&g.sums[i]);
+        counted += __ldcg(&g.counts[i]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        loss += __shfl_xor_sync(kFull, loss, o);
+        counted += __shfl_xor_sync(kFull, counted, o);
+    }
+    if (lane == 0) sums[group] = loss, counts[group] = counted;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        loss = 0.0;
+        counted = 0;
+        for (int i = 0; i < 32; ++i) loss += sums[i], counted += counts[i];
+        const int n = max(1, counted);
+        g.total[0] = static_cast<float>(loss);
+        g.total[1] = static_cast<float>(loss / n);
+        g.total[2] = static_cast<float>(1.0 / n);
+    }
+}
+
+// ----------------------------------------------------------- packed tokens
+
+// Row i of dst is row order[i] of src (NULL: row i), for the tokens that are
+// there; rows behind them, as far as a step of depth reaches, are zero.  With
+// order, also what the tokens' ends need.
+template <bool AL>
+__global__ void __launch_bounds__(kRowThreads) k_loss_pack(const __grid_constant__ PackArgs g)
+{
+    pdl_wait();
+    const int64_t i = blockIdx.x;
+    const int slab = blockIdx.y;
+    const int count = g.count ? *g.count : g.rows;
+    if (i >= count + 63) return;  // (rows behind the last are nobody's, and boxes fill them with zeros)
+    Piece<__nv_bfloat16, AL> p;
+    if (i < count) {
+        const int64_t token = g.order ? g.order[i] : i;
+        p.load(g.src + token * g.ld_src, slab, g.cols);
+        if (g.order && slab == 0 && threadIdx.x == 0) {
+            const float c = g.dloss[token * g.dloss_stride] * (g.scale ? *g.scale : 1.0f);
+            g.lse_out[i] = g.lse[token];
+            g.share_out[i] = c;
+            g.coef_out[i] = c * expm1f(-g.loss[token]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < RowPiece<__nv_bfloat16, AL>::kVec; ++e) p.v[e] = __float2bfloat16_rn(0.0f);
+    }
+    p.store(g.dst + i * g.ld_dst, slab, g.cols);
+}
+
+// dx of token order[i]: the parts' sum, and the target's term.  Tokens without a
+// target get zeros, those with an impossible one NaN.
+template <bool AL>
+__global__ void __launch_bounds__(kRowThreads) k_loss_finish(const __grid_constant__ FinishArgs g)
+{
+    using P = RowPiece<__nv_bfloat16, AL>;
+    pdl_wait();
+    const int64_t i = blockIdx.x, token = g.order[i];
+    const int slab = blockIdx.y;
+    Piece<__nv_bfloat16, AL> p;
+    float acc[P::kVec];
+#pragma unroll
+    for (int e = 0; e < P::kVec; ++e) acc[e] = 0.0f;
+    if (*g.status) {
+#pragma unroll
+        for (int e = 0; e < P::kVec; ++e) acc[e] = __int_as_float(0x7FC00000);
+    } else if (i < *g.count) {
+        const float f = g.coef[i];
+        p.load(g.w + (g.gathered ? i : static_cast<int64_t>(g.key[i])) * g.ld_w, slab, g.cols);
+        for (int s = 0; s < g.splits; ++s) {
+            const float *part = g.part + (s * g.tokens + i) * g.ld_part;
+            if (AL) {
+                const int c = P::col(slab, 0);
+                if (c < g.cols) {
+                    const float4 a = *reinterpret_cast<const float4 *>(part + c);
+                    const float4 b = *reinterpret_cast<const float4 *>(part + c + 4);
+                    acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
+                    acc[P::kVec - 4] += b.x, acc[P::kVec - 3] += b.y, acc[P::kVec - 2] += b.z, acc[P::kVec - 1] += b.w;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < P::kVec; ++e)
+                    if (P::col(slab, e) < g.cols) acc[e] += part[P::col(slab, e)];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < P::kVec; ++e) acc[e] = fmaf(f, to_float(p.v[e]), acc[e]);
+    } else if (id_at(g.ids, g.wide, token) >= 0) {
+#pragma unroll
+        for (int e = 0; e < P::kVec; ++e) acc[e] = __int_as_float(0x7FC00000);
+    }
+#pragma unroll
+    for (int e = 0; e < P::kVec; ++e) p.v[e] = __float2bfloat16_rn(acc[e]);
+    p.store(g.dx + token * g.ld_dx, slab, g.cols);
+}
+
+}  // namespace dev
+
+namespace {
+
+// Pairs of blocks that the GPU holds at once, asked for once a device.
+template <int OP>
+cudaError_t pairs_at_once(int *pairs)
+{
+    static int known[64] = {};
+    int device = 0;
+    cudaError_t rc = cudaGetDevice(&device);
+    if (rc != cudaSuccess) return rc;
+    const int at = device & 63;
+    if (!known[at]) {
+        rc = cudaFuncSetAttribute(dev::k_product<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dev::kProductBytes);
+        if (rc != cudaSuccess) return rc;
+        const int n = static_cast<int>(clusters_at_once(dev::k_product<OP>, dev::kProductThreads, dev::kProductBytes, 2));
+        if (n <= 0) return cudaErrorInvalidConfiguration;
+        known[at] = n;
+    }
+    *pairs = known[at];
+    return cudaSuccess;
+}
+
+template <int OP>
+cudaError_t product(const ProductArgs &g, const ProductMaps &maps, cudaStream_t s)
+{
+    int pairs;
+    const cudaError_t rc = pairs_at_once<OP>(&pairs);
+    if (rc != cudaSuccess) return rc;
+    const int64_t items = static_cast<int64_t>((g.m + dev::kTile - 1) / dev::kTile) * ((g.n + dev::kTile - 1) / dev::kTile) *
+                          g.splits;
+    if (items == 0) return cudaSuccess;
+    return launch<true>(dev::k_product<OP>, dim3(2 * static_cast<uint32_t>(std::min<int64_t>(items, pairs))),
+                        dev::kProductThreads, dev::kProductBytes, 2, s, g, maps);
+}
+
+cudaError_t pack(const PackArgs &g, bool aligned, cudaStream_t s)
+{
+    if (g.rows == 0) return cudaSuccess;
+    uint32_t threads, slabs;
+    row_shape(g.cols, aligned ? 8 : 4, &threads, &slabs);
+    return aligned ? launch<true>(dev::k_loss_pack<true>, dim3(g.rows, slabs), threads, 0, 1, s, g)
+                   : launch<true>(dev::k_loss_pack<false>, dim3(g.rows, slabs), threads, 0, 1, s, g);
+}
+
+// The values of g that are there at a time: 256 MB.
+constexpr uint64_t kGradValues = 1ull << 27;
+constexpr uint64_t kPackValues = 1ull << 26;  // of W, where its rows have to be moved to 16-byte boundaries
+constexpr int64_t kMergeChunk = 32768;        // tokens of one product of the forward pass
+
+uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
+
+// Parts of the depth of dx's product, so that few tokens still give every pair work.
+int dx_splits(uint64_t tokens, uint64_t cols)
+{
+    const uint64_t tiles = up(tokens, dev::kTile) / dev::kTile * (up(cols, dev::kTile) / dev::kTile);
+    return static_cast<int>(std::max<uint64_t>(1, 76 / std::max<uint64_t>(tiles, 1)));
+}
+
+// Where things are in d_work.  What lives from piece to piece comes first, and
+// does not depend on a piece's size.
+struct Layout {
+    uint64_t bytes = 0;
+    uint64_t take(uint64_t n)
+    {
+        const uint64_t at = bytes;
+        bytes += up(n, 256);
+        return at;
+    }
+};
+struct ForwardLayout : Layout {
+    uint64_t head, state, mine, sums, counts, x, part, w;
+    uint64_t ld, chunk, piece;  // rows of packed matrices; tokens of a product; rows of W that are moved at a time
+    ForwardLayout(uint64_t tokens, uint64_t cols, uint64_t rows, bool move)
+    {
+        ld = up(cols, 8);
+        chunk = std::min<uint64_t>(tokens, kMergeChunk);
+        piece = move ? std::min(rows, std::max<uint64_t>(256, kPackValues / ld / 256 * 256)) : rows;
+        const uint64_t blocks = up(tokens, dev::kMergeTokens) / dev::kMergeTokens;
+        head = take(16);
+        state = take(8 * tokens);
+        mine = take(4 * tokens);
+        sums = take(8 * blocks);
+        counts = take(4 * blocks);
+        x = take(move ? 2 * tokens * ld : 0);
+        part = take(8 * chunk * (up(piece, dev::kHalfTile) / dev::kHalfTile));
+        w = take(move ? 2 * piece * ld : 0);
+    }
+};
+struct BackwardLayout : Layout {
+    uint64_t head, key[2], order[2], first, lse, share, coef, x, extra, part, target, g, sums, w;
+    uint64_t ld, ld4, piece, ld_g;
+    int splits;
+    BackwardLayout(uint64_t tokens, uint64_t vocab, uint64_t cols, uint64_t rows, bool weight, bool move, bool pieces)
+    {
+        ld = up(cols, 8);
+        ld4 = up(cols, 4);
+        splits = dx_splits(tokens, cols);
+        uint64_t most = std::max<uint64_t>(256, kGradValues / std::max<uint64_t>(1, up(tokens, 256)) / 256 * 256);
+        if (move) most = std::min(most, std::max<uint64_t>(256, kPackValues / ld / 256 * 256));
+        piece = std::min(rows, most);
+        ld_g = up(piece, 64);
+        head = take(16);
+        for (int i = 0; i < 2; ++i) {
+            key[i] = take(4 * tokens);
+            order[i] = take(4 * tokens);
+        }
+        first = take(weight ? 4 * vocab : 0);
+        lse = take(4 * tokens);
+        share = take(4 * tokens);
+        coef = take(4 * tokens);
+        x = take(2 * tokens * ld);
+        extra = take(weight ? 4 * tokens * ld4 : 0);
+        part = take(4 * static_cast<uint64_t>(splits) * tokens * ld4);
+        target = take(pieces ? 2 * tokens * ld : 0);
+        // g takes the place of the partial sums of the targets' terms, which come before it
+        g = take(std::max(2 * tokens * ld_g,
+                          weight ? 8 * (up(tokens, LCT_EMBEDDING_CHUNK) / LCT_EMBEDDING_CHUNK) * cols : 0));
+        w = take(move ? 2 * piece * ld : 0);
+    }
+};
+
+// What both directions check.
+lct_status check_batch(const lct_ids *ids, const uint16_t *d_x, uint64_t ld_x, uint64_t cols, const uint16_t *d_w,
+                       uint64_t ld_w, uint64_t first, uint64_t rows, const void *d_work, Matrix *x, Matrix *w)
+{
+    const lct_status rc = check_ids(ids);
+    if (rc != LCT_OK) return rc;
+    if (cols == 0 || rows == 0 || first > ids->vocab || rows > ids->vocab - first) return LCT_ERR_INVALID_ARG;
+    if (cols > LCT_VOCAB_MAX_COLS) return LCT_ERR_UNSUPPORTED;
+    *x = Matrix{d_x, ld_x, cols, ids->tokens, 2};
+    *w = Matrix{d_w, ld_w, cols, rows, 2};
+    if (!matrix_ok(*x) || !matrix_ok(*w) || !d_work || reinterpret_cast<uintptr_t>(d_work) % 256) return LCT_ERR_INVALID_ARG;
+    return LCT_OK;
+}
+
+template <typename T>
+T *at(void *work, uint64_t offset)
+{
+    return reinterpret_cast<T *>(static_cast<char *>(work) + offset);
+}
+const __nv_bfloat16 *bf16(const uint16_t *p) { return reinterpret_cast<const __nv_bfloat16 *>(p); }
+__nv_bfloat16 *bf16(uint16_t *p) { return reinterpret_cast<__nv_bfloat16 *>(p); }
+
+}  // namespace
+}  // namespace lct
+
+using namespace lct;
+
+extern "C" uint64_t lct_loss_work_bytes(uint64_t tokens, uint64_t vocab, uint64_t cols, uint64_t rows, int32_t flags)
+{
+    const bool move = flags & LCT_LOSS_UNALIGNED;
+    if (flags & LCT_LOSS_BACKWARD)
+        return BackwardLayout(tokens, vocab, cols, rows, flags & LCT_LOSS_WEIGHT, move, rows < vocab).bytes;
+    return ForwardLayout(tokens, cols, rows, move).bytes;
+}
+
+extern "C" lct_status lct_loss_forward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,
+                                       const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows, float *d_loss,
+                                       float *d_lse, float *d_total, void *d_work, uint64_t work_bytes, void *stream)
+{
+    Matrix x, w;
+    const lct_status ok = check_batch(targets, d_x, ld_x, cols, d_w, ld_w, first, rows, d_work, &x, &w);
+    if (ok != LCT_OK) return ok;
+    const uint64_t t = targets->tokens, id_size = targets->wide ? 8 : 4;
+    const bool move = !matrix_al(x) || !matrix_al(w), begins = first == 0, ends = first + rows == targets->vocab;
+    const ForwardLayout l(t, cols, rows, move);
+    if (work_bytes < l.bytes || (t && (!d_loss || !d_lse)) || reinterpret_cast<uintptr_t>(d_loss) % 4 ||
+        reinterpret_cast<uintptr_t>(d_lse) % 4 || reinterpret_cast<uintptr_t>(d_total) % 4)
+        return LCT_ERR_INVALID_ARG;
+    const struct {
+        const void *p;
+        uint64_t n;
+    } out[4] = {{d_loss, 4 * t}, {d_lse, 4 * t}, {d_total, 12}, {d_work, l.bytes}};
+    for (int i = 0; i < 4; ++i) {
+        if (!apart(x, out[i].p, out[i].n) || !apart(w, out[i].p, out[i].n) ||
+            !apart(targets->d_ids, t * id_size, out[i].p, out[i].n))
+            return LCT_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 4; ++j)
+            if (!apart(out[i].p, out[i].n, out[j].p, out[j].n)) return LCT_ERR_INVALID_ARG;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (t == 0) {
+        if (!d_total || !ends) return LCT_OK;
+        // sum and mean of no losses; nobody has a share
+        return cudaMemsetAsync(d_total, 0, 12, s) == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
+    }
+    const __nv_bfloat16 *xp = bf16(d_x);
+    uint64_t ldx = ld_x;
+    if (move) {
+        xp = at<__nv_bfloat16>(d_work, l.x);
+        ldx = l.ld;
+        if (begins) {
+            PackArgs p{};
+            p.src = bf16(d_x);
+            p.ld_src = static_cast<int64_t>(ld_x);
+            p.dst = at<__nv_bfloat16>(d_work, l.x);
+            p.ld_dst = static_cast<int64_t>(l.ld);
+            p.rows = static_cast<int32_t>(t);
+            p.cols = static_cast<int32_t>(cols);
+            if (pack(p, false, s) != cudaSuccess) return LCT_ERR_CUDA;
+        }
+    }
+    for (uint64_t r0 = 0; r0 < rows; r0 += l.piece) {
+        const uint64_t n = std::min(l.piece, rows - r0);
+        const __nv_bfloat16 *wp = bf16(d_w) + r0 * ld_w;
+        uint64_t ldw = ld_w;
+        if (move) {
+            PackArgs p{};
+            p.src = wp;
+            p.ld_src = static_cast<int64_t>(ld_w);
+            p.dst = at<__nv_bfloat16>(d_work, l.w);
+            p.ld_dst = static_cast<int64_t>(l.ld);
+            p.rows = static_cast<int32_t>(n);
+            p.cols = static_cast<int32_t>(cols);
+            if (pack(p, false, s) != cudaSuccess) return LCT_ERR_CUDA;
+            wp = p.dst;
+            ldw = l.ld;
+        }
+        for (uint64_t t0 = 0; t0 < t; t0 += l.chunk) {
+            const uint64_t tn = std::min(l.chunk, t - t0);
+            const void *ids = static_cast<const char *>(targets->d_ids) + t0 * id_size;
+            ProductMaps maps{};
+            if (!box_map(&maps.a, xp + t0 * ldx, cols, tn, ldx, 0, dev::kHalfTile) ||
+                !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kHalfTile))
+                return LCT_ERR_CUDA;
+            ProductArgs g{};
+            g.m = static_cast<int32_t>(tn);
+            g.n = static_cast<int32_t>(n);
+            g.k = static_cast<int32_t>(cols);
+            g.status = at<int32_t>(d_work, l.head);
+            g.splits = 1;
+            g.begins = begins && r0 == 0 && t0 == 0;
+            g.ids = ids;
+            g.wide = targets->wide;
+            g.row0 = static_cast<int64_t>(first + r0);
+            g.part = at<float2>(d_work, l.part);
+            g.mine = at<float>(d_work, l.mine) + t0;
+            if (product<kLogits>(g, maps, s) != cudaSuccess) return LCT_ERR_CUDA;
+            MergeArgs m{};
+            m.part = g.part;
+            m.state = at<float2>(d_work, l.state) + t0;
+            m.mine = g.mine;
+            m.ids = ids;
+            m.wide = targets->wide;
+            m.loss = d_loss + t0;
+            m.lse = d_lse + t0;
+            m.total = d_total;
+            m.sums = at<double>(d_work, l.sums);
+            m.counts = at<int32_t>(d_work, l.counts);
+            m.status = g.status;
+            m.counter = g.status + 1;
+            m.tokens = static_cast<int64_t>(tn);
+            m.vocab = static_cast<int64_t>(targets->vocab);
+            m.slots = static_cast<int32_t>(up(n, dev::kHalfTile) / dev::kHalfTile);
+            m.blocks = static_cast<int32_t>(up(t, dev::kMergeTokens) / dev::kMergeTokens);
+            m.block0 = static_cast<int32_t>(t0 / dev::kMergeTokens);
+            m.begins = begins && r0 == 0;
+            m.ends = ends && r0 + n == rows;
+            if (launch<true>(dev::k_loss_merge, dim3(static_cast<uint32_t>(up(tn, dev::kMergeTokens) / dev::kMergeTokens)), 1024,
+                             0, 1, s, m) != cudaSuccess)
+                return LCT_ERR_CUDA;
+        }
+    }
+    return LCT_OK;
+}
+
+extern "C" lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,
+                                        const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows,
+                                        const float *d_loss, const float *d_lse, const float *d_dloss, uint64_t dloss_stride,
+                                        const float *d_scale, uint16_t *d_dx, uint64_t ld_dx, uint16_t *d_dw, uint64_t ld_dw,
+                                        void *d_work, uint64_t work_bytes, void *stream)
+{
+    Matrix x, w;
+    const lct_status ok = check_batch(targets, d_x, ld_x, cols, d_w, ld_w, first, rows, d_work, &x, &w);
+    if (ok != LCT_OK) return ok;
+    const uint64_t t = targets->tokens, v = targets->vocab, id_bytes = t * (targets->wide ? 8 : 4);
+    const bool move = !matrix_al(x) || !matrix_al(w), begins = first == 0, ends = first + rows == v, pieces = rows < v;
+    const BackwardLayout l(t, v, cols, rows, d_dw != nullptr, move, pieces);
+    const Matrix dx{d_dx, ld_dx, cols, t, 2}, dw{d_dw, ld_dw, cols, d_dw ? rows : 0, 2};
+    if (work_bytes < l.bytes || !matrix_ok(dx) || !matrix_ok(dw) || dloss_stride > 1) return LCT_ERR_INVALID_ARG;
+    if (t && (!d_loss || !d_lse || !d_dloss)) return LCT_ERR_INVALID_ARG;
+    const struct {
+        const void *p;
+        uint64_t n;
+    } in[5] = {{targets->d_ids, id_bytes},
+               {d_loss, 4 * t},
+               {d_lse, 4 * t},
+               {d_dloss, t ? 4 * ((t - 1) * dloss_stride + 1) : 0},
+               {d_scale, 4}};
+    for (int i = 1; i < 5; ++i)
+        if (reinterpret_cast<uintptr_t>(in[i].p) % 4) return LCT_ERR_INVALID_ARG;
+    if (!apart(dx, x) || !apart(dx, w) || !apart(dw, x) || !apart(dw, w) || !apart(dx, dw) || !apart(dx, d_work, l.bytes) ||
+        !apart(dw, d_work, l.bytes) || !apart(x, d_work, l.bytes) || !apart(w, d_work, l.bytes))
+        return LCT_ERR_INVALID_ARG;
+    for (const auto &r : in)
+        if (!apart(dx, r.p, r.n) || !apart(dw, r.p, r.n) || !apart(d_work, l.bytes, r.p, r.n)) return LCT_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (t == 0) {
+        if (!d_dw) return LCT_OK;
+        return cudaMemset2DAsync(d_dw, 2 * ld_dw, 0, 2 * cols, rows, s) == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
+    }
+    int32_t *status = at<int32_t>(d_work, l.head), *count = status + 2;
+    int32_t *key = at<int32_t>(d_work, l.key[0]), *order = at<int32_t>(d_work, l.order[0]);
+    __nv_bfloat16 *xp = at<__nv_bfloat16>(d_work, l.x);
+    const int64_t ld = static_cast<int64_t>(l.ld), ld4 = static_cast<int64_t>(l.ld4);
+    const int32_t tokens = static_cast<int32_t>(t), k = static_cast<int32_t>(cols);
+    if (begins) {
+        SortArgs o{};
+        o.ids = targets->d_ids;
+        o.wide = targets->wide;
+        for (int i = 0; i < 2; ++i) {
+            o.key[i] = at<int32_t>(d_work, l.key[i]);
+            o.order[i] = at<int32_t>(d_work, l.order[i]);
+        }
+        o.first = d_dw ? at<int32_t>(d_work, l.first) : nullptr;
+        o.count = count;
+        o.clear = status;
+        o.tokens = tokens;
+        o.vocab = static_cast<int32_t>(v);
+        if (launch_sort_ids(o, s) != cudaSuccess) return LCT_ERR_CUDA;
+        PackArgs p{};
+        p.src = bf16(d_x);
+        p.ld_src = static_cast<int64_t>(ld_x);
+        p.dst = xp;
+        p.ld_dst = ld;
+        p.order = order;
+        p.count = count;
+        p.dloss = d_dloss;
+        p.dloss_stride = static_cast<int64_t>(dloss_stride);
+        p.scale = d_scale;
+        p.loss = d_loss;
+        p.lse = d_lse;
+        p.lse_out = at<float>(d_work, l.lse);
+        p.share_out = at<float>(d_work, l.share);
+        p.coef_out = at<float>(d_work, l.coef);
+        p.rows = tokens;
+        p.cols = k;
+        if (pack(p, matrix_al(x) && cols % 8 == 0, s) != cudaSuccess) return LCT_ERR_CUDA;
+        if (d_dw) {
+            SegmentArgs e{};
+            e.src = xp;
+            e.ld_src = ld;
+            e.key = key;
+            e.first = o.first;
+            e.count = count;
+            e.coef = p.coef_out;
+            e.out = at<float>(d_work, l.extra);
+            e.ld_out = ld4;
+            e.part = at<float>(d_work, l.g);
+            e.scale = 1.0f;
+            e.cols = k;
+            e.tokens = tokens;
+            e.vocab = static_cast<int32_t>(v);
+            e.compact = true;
+            if (launch_segments(e, false, cols % 8 == 0, false, s) != cudaSuccess) return LCT_ERR_CUDA;
+        }
+    }
+    if (pieces) {  // the targets' rows, as their pieces come
+        LookupArgs u{};
+        u.ids = key;
+        u.table = d_w;
+        u.out = at<__nv_bfloat16>(d_work, l.target);
+        u.ld_table = static_cast<int64_t>(ld_w);
+        u.ld_out = ld;
+        u.row0 = static_cast<int64_t>(first);
+        u.rows = static_cast<int64_t>(rows);
+        u.vocab = static_cast<int64_t>(v);
+        u.tokens = static_cast<int64_t>(t);
+        u.cols = k;
+        u.scale = 1.0f;
+        if (launch_lookup(u, false, matrix_al(w) && cols % 8 == 0, s) != cudaSuccess) return LCT_ERR_CUDA;
+    }
+    const bool dw_boxes = matrix_al(dw);
+    for (uint64_t r0 = 0; r0 < rows; r0 += l.piece) {
+        const uint64_t n = std::min(l.piece, rows - r0);
+        const __nv_bfloat16 *wp = bf16(d_w) + r0 * ld_w;
+        uint64_t ldw = ld_w;
+        if (move) {
+            PackArgs p{};
+            p.src = wp;
+            p.ld_src = static_cast<int64_t>(ld_w);
+            p.dst = at<__nv_bfloat16>(d_work, l.w);
+            p.ld_dst = ld;
+            p.rows = static_cast<int32_t>(n);
+            p.cols = k;
+            if (pack(p, false, s) != cudaSuccess) return LCT_ERR_CUDA;
+            wp = p.dst;
+            ldw = l.ld;
+        }
+        __nv_bfloat16 *gp = at<__nv_bfloat16>(d_work, l.g);
+        ProductMaps maps{};
+        ProductArgs g{};
+        g.m = tokens;
+        g.n = static_cast<int32_t>(n);
+        g.k = k;
+        g.count = count;
+        g.status = status;
+        g.splits = 1;
+        g.row0 = static_cast<int64_t>(first + r0);
+        g.target = key;
+        g.lse = at<float>(d_work, l.lse);
+        g.share = at<float>(d_work, l.share);
+        g.boxes = true;
+        if (!box_map(&maps.a, xp, cols, t, l.ld, 0, dev::kHalfTile) || !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kHalfTile) ||
+            !box_map(&maps.c, gp, n, t, l.ld_g, 0, 32) || product<kSoftmax>(g, maps, s) != cudaSuccess)
+            return LCT_ERR_CUDA;
+        g.n = k;
+        g.k = static_cast<int32_t>(n);
+        g.splits = l.splits;
+        g.add = !(begins && r0 == 0);
+        if (!box_map(&maps.a, gp, n, t, l.ld_g, 0, dev::kHalfTile) || !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kDepth) ||
+            !box_map32(&maps.c, at<float>(d_work, l.part), cols, t, l.ld4, l.splits) ||
+            product<kDx>(g, maps, s) != cudaSuccess)
+            return LCT_ERR_CUDA;
+        if (!d_dw) continue;
+        g.m = static_cast<int32_t>(n);
+        g.k = tokens;
+        g.splits = 1;
+        g.extra = at<float>(d_work, l.extra);
+        g.first = at<int32_t>(d_work, l.first);
+        g.ld_extra = ld4;
+        g.out = bf16(d_dw) + r0 * ld_dw;
+        g.ld_out = static_cast<int64_t>(ld_dw);
+        g.boxes = dw_boxes;
+        if (!box_map(&maps.a, gp, n, t, l.ld_g, 0, dev::kDepth) || !box_map(&maps.b, xp, cols, t, l.ld, 0, dev::kDepth) ||
+            (dw_boxes && !box_map(&maps.c, g.out, cols, n, ld_dw, 0, 32)) || product<kDw>(g, maps, s) != cudaSuccess)
+            return LCT_ERR_CUDA;
+    }
+    if (!ends) return LCT_OK;
+    FinishArgs f{};
+    f.part = at<float>(d_work, l.part);
+    f.ld_part = ld4;
+    f.tokens = static_cast<int64_t>(t);
+    f.splits = l.splits;
+    f.key = key;
+    f.order = order;
+    f.count = count;
+    f.status = status;
+    f.coef = at<float>(d_work, l.coef);
+    f.w = pieces ? at<__nv_bfloat16>(d_work, l.target) : bf16(d_w);
+    f.ld_w = pieces ? ld : static_cast<int64_t>(ld_w);
+    f.gathered = pieces;
+    f.ids = targets->d_ids;
+    f.wide = targets->wide;
+    f.dx = bf16(d_dx);
+    f.ld_dx = static_cast<int64_t>(ld_dx);
+    f.cols = k;
+    const bool al = cols % 8 == 0 && matrix_al(dx) && (pieces || matrix_al(w));
+    uint32_t threads, slabs;
+    row_shape(k, al ? 8 : 4, &threads, &slabs);
+    const cudaError_t rc = al ? launch<true>(dev::k_loss_finish<true>, dim3(tokens, slabs), threads, 0, 1, s, f)
+                              : launch<true>(dev::k_loss_finish<false>, dim3(tokens, slabs), threads, 0, 1, s, f);
+    return rc == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
+}

@@ -253,4 +253,38 @@ inline bool box_map(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same for float32 (planes > 0) and boxes of 32 columns by 32 rows.
+inline bool box_map32(CUtensorMap *m, const float *p, uint64_t cols, uint64_t rows, uint64_t ld, uint64_t planes)
+{
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {cols, rows, planes}, strides[2] = {4 * ld, 4 * ld * rows};
+    const cuuint32_t size[3] = {32, 32, 1}, step[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float *>(p), dims, strides, size, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How many clusters of a size the GPU holds at once (0: none, or an error).
+template <typename... P>
+uint32_t clusters_at_once(void (*kernel)(P...), uint32_t threads, uint32_t smem, uint32_t cluster)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // a size that does not fit is no error of the caller's
+        return 0;
+    }
+    return n > 0 ? static_cast<uint32_t>(n) : 0;
+}
+
 }  // namespace lct
