@@ -479,11 +479,11 @@ lct_status lct_adapter_backward(const lct_adapters *bank, const lct_token_plan *
 #define LCT_VOCAB_MAX (1 << 24)          /* rows of the vocabulary's matrix */
 #define LCT_VOCAB_MAX_COLS (1 << 16)
 #define LCT_VOCAB_MAX_TOKENS (1 << 24)
-#define LCT_EMBEDDING_CHUNK 32           /* sorted tokens that one block adds */
+#define LCT_EMBEDDING_CHUNK(tokens) ((tokens) <= 8192 ? 8 : 32) /* sorted tokens that one block adds */
 /* scratch of lct_embedding_grad */
-#define LCT_EMBEDDING_WORK_BYTES(tokens, vocab, cols)                                                      \
-    (16ull + 64ull * (((uint64_t)(tokens) + 3) / 4) + 16ull * (((uint64_t)(vocab) + 3) / 4) +              \
-     8ull * (((uint64_t)(tokens) + LCT_EMBEDDING_CHUNK - 1) / LCT_EMBEDDING_CHUNK) * (uint64_t)(cols))
+#define LCT_EMBEDDING_WORK_BYTES(tokens, cols)                                                             \
+    (16ull + 64ull * (((uint64_t)(tokens) + 3) / 4) +                                                      \
+     8ull * (((uint64_t)(tokens) + LCT_EMBEDDING_CHUNK(tokens) - 1) / LCT_EMBEDDING_CHUNK(tokens)) * (uint64_t)(cols))
 
 /* A batch's ids: a row of the vocabulary's matrix for each token.  A negative
  * id is none (padding, a token without a target). */

@@ -16,6 +16,8 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/lct.h"
@@ -472,7 +474,7 @@ PyObject *embedding_grad(PyObject *const *a)
     const at::Tensor &out = a[5] == Py_None ? fresh : tensor(a[5], "out must be a tensor or None");
     no_gradient({&dy, &out}, "embedding_grad");
     const Rows outr = rows_of(out, cols, vocab, device, "out", dy.scalar_type());
-    at::Tensor work = make({static_cast<int64_t>(LCT_EMBEDDING_WORK_BYTES(ids.tokens, vocab, cols))}, at::kByte, device);
+    at::Tensor work = make({static_cast<int64_t>(LCT_EMBEDDING_WORK_BYTES(ids.tokens, cols))}, at::kByte, device);
     check(lct_embedding_grad(&ids, dyr.p, dyr.ld, dtype, cols, scale, base.p, base.ld, outr.p, outr.ld, work.data_ptr(),
                              stream_of(device)),
           "lct_embedding_grad");
@@ -512,9 +514,8 @@ LossOperands loss_operands(const at::Tensor &x, const at::Tensor &w, const at::T
     o.unaligned = odd(o.x, o.ids.tokens) || odd(o.w, o.rows);
     return o;
 }
-const at::Tensor &floats(PyObject *o, uint64_t n, int device, const char *what)
+const at::Tensor &floats(const at::Tensor &t, uint64_t n, int device, const char *what)
 {
-    const at::Tensor &t = tensor(o, what);
     if (t.scalar_type() != at::kFloat || !t.is_cuda() || t.get_device() != device || !t.is_contiguous() ||
         static_cast<uint64_t>(t.numel()) != n) {
         PyErr_Format(PyExc_ValueError, "%s: expected contiguous float32, %llu values on CUDA device %d", what,
@@ -524,27 +525,44 @@ const at::Tensor &floats(PyObject *o, uint64_t n, int device, const char *what)
     return t;
 }
 
-// (x, weight, targets, total) -> (loss, lse) or (loss, lse, total)
-PyObject *cross_entropy(PyObject *const *a)
+// x [..., cols] as a matrix whose rows the kernels can read: a copy where its leading dimensions make no single row index,
+// or a row's values do not lie side by side.
+at::Tensor as_rows(const at::Tensor &x, int64_t cols)
 {
-    const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
-    const at::Tensor &targets = tensor(a[2], "targets must be a tensor");
+    at::Tensor r = x.dim() == 2 ? x : x.reshape({-1, cols});
+    return r.stride(1) == 1 && r.stride(0) >= cols ? r : r.contiguous();
+}
+
+enum { MEAN = 0, SUM = 1, NONE = 2 };
+
+struct Forward {
+    at::Tensor loss, lse, total;
+};
+Forward loss_forward(const at::Tensor &x, const at::Tensor &w, const at::Tensor &targets, bool totals)
+{
     const Held zero(PyLong_FromLong(0));
     const LossOperands o = loss_operands(x, w, targets, zero.o, zero.o);
-    no_gradient({&x, &w}, "cross_entropy");
-    const bool totals = a[3] == Py_True;
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(o.device));
-    at::Tensor loss = make(targets.sizes(), at::kFloat, o.device), lse = make(targets.sizes(), at::kFloat, o.device), total;
-    if (totals) total = make({3}, at::kFloat, o.device);
+    Forward f{make(targets.sizes(), at::kFloat, o.device), make(targets.sizes(), at::kFloat, o.device), {}};
+    if (totals) f.total = make({3}, at::kFloat, o.device);
     const uint64_t bytes =
         lct_loss_work_bytes(o.ids.tokens, o.ids.vocab, o.cols, o.rows, o.unaligned ? LCT_LOSS_UNALIGNED : 0);
     at::Tensor work = make({static_cast<int64_t>(bytes)}, at::kByte, o.device);
-    check(lct_loss_forward(&o.ids, o.x.p, o.x.ld, o.cols, o.w.p, o.w.ld, 0, o.rows, static_cast<float *>(loss.data_ptr()),
-                           static_cast<float *>(lse.data_ptr()), totals ? static_cast<float *>(total.data_ptr()) : nullptr,
-                           work.data_ptr(), bytes, stream_of(o.device)),
+    check(lct_loss_forward(&o.ids, o.x.p, o.x.ld, o.cols, o.w.p, o.w.ld, 0, o.rows, static_cast<float *>(f.loss.data_ptr()),
+                           static_cast<float *>(f.lse.data_ptr()),
+                           totals ? static_cast<float *>(f.total.data_ptr()) : nullptr, work.data_ptr(), bytes,
+                           stream_of(o.device)),
           "lct_loss_forward");
-    if (!totals) return tuple_of({THPVariable_Wrap(loss), THPVariable_Wrap(lse)});
-    return tuple_of({THPVariable_Wrap(loss), THPVariable_Wrap(lse), THPVariable_Wrap(total)});
+    return f;
+}
+
+// (x, weight, targets) -> (loss, lse)
+PyObject *cross_entropy(PyObject *const *a)
+{
+    const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
+    no_gradient({&x, &w}, "cross_entropy");
+    const Forward f = loss_forward(x, w, tensor(a[2], "targets must be a tensor"), false);
+    return tuple_of({THPVariable_Wrap(f.loss), THPVariable_Wrap(f.lse)});
 }
 
 // (x, piece, first, vocab, targets, loss, lse, total or None, work) -> None
@@ -552,8 +570,9 @@ PyObject *cross_entropy_piece(PyObject *const *a)
 {
     const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
     const LossOperands o = loss_operands(x, w, tensor(a[4], "targets must be a tensor"), a[2], a[3]);
-    const at::Tensor &loss = floats(a[5], o.ids.tokens, o.device, "loss"), &lse = floats(a[6], o.ids.tokens, o.device, "lse");
-    float *total = a[7] == Py_None ? nullptr : static_cast<float *>(floats(a[7], 3, o.device, "total").data_ptr());
+    const at::Tensor &loss = floats(tensor(a[5], "loss must be a tensor"), o.ids.tokens, o.device, "loss");
+    const at::Tensor &lse = floats(tensor(a[6], "lse must be a tensor"), o.ids.tokens, o.device, "lse");
+    float *total = a[7] == Py_None ? nullptr : static_cast<float *>(floats(tensor(a[7], "total must be a tensor or None"), 3, o.device, "total").data_ptr());
     const at::Tensor &work = tensor(a[8], "work must be a tensor");
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(o.device));
     check(lct_loss_forward(&o.ids, o.x.p, o.x.ld, o.cols, o.w.p, o.w.ld, o.first, o.rows,
@@ -567,41 +586,145 @@ struct Upstream {
     const float *dloss, *scale;
     uint64_t stride;
 };
-// dloss: a value a token, or one for all; scale: a value that all are multiplied by, or None
-Upstream upstream_of(PyObject *dloss, PyObject *scale, uint64_t tokens, int device)
+// dloss: a value a token, or one for all; scale: a value that all are multiplied by, or undefined
+Upstream upstream_of(const at::Tensor &dloss, const at::Tensor &scale, uint64_t tokens, int device)
 {
     Upstream u{};
-    const at::Tensor &t = tensor(dloss, "dloss must be a tensor");
-    u.stride = t.numel() == 1 && tokens != 1 ? 0 : 1;
+    u.stride = dloss.numel() == 1 && tokens != 1 ? 0 : 1;
     u.dloss = static_cast<const float *>(floats(dloss, u.stride ? tokens : 1, device, "dloss").data_ptr());
-    if (scale != Py_None) u.scale = static_cast<const float *>(floats(scale, 1, device, "scale").data_ptr());
+    if (scale.defined()) u.scale = static_cast<const float *>(floats(scale, 1, device, "scale").data_ptr());
     return u;
 }
+at::Tensor maybe(PyObject *o, const char *what) { return o == Py_None ? at::Tensor() : tensor(o, what); }
 
-// (x, weight, targets, loss, lse, dloss, scale or None, weight_grad) -> (dx, dw or None)
-PyObject *cross_entropy_grads(PyObject *const *a)
+struct Backward {
+    at::Tensor dx, dw;
+};
+Backward loss_backward(const at::Tensor &x, const at::Tensor &w, const at::Tensor &targets, const at::Tensor &loss,
+                       const at::Tensor &lse, const at::Tensor &dloss, const at::Tensor &scale, bool weight)
 {
-    const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
     const Held zero(PyLong_FromLong(0));
-    const LossOperands o = loss_operands(x, w, tensor(a[2], "targets must be a tensor"), zero.o, zero.o);
-    const at::Tensor &loss = floats(a[3], o.ids.tokens, o.device, "loss"), &lse = floats(a[4], o.ids.tokens, o.device, "lse");
-    const Upstream u = upstream_of(a[5], a[6], o.ids.tokens, o.device);
-    no_gradient({&x, &w, &loss, &lse}, "cross_entropy_grads");
-    const bool weight = a[7] == Py_True;
+    const LossOperands o = loss_operands(x, w, targets, zero.o, zero.o);
+    floats(loss, o.ids.tokens, o.device, "loss");
+    floats(lse, o.ids.tokens, o.device, "lse");
+    const Upstream u = upstream_of(dloss, scale, o.ids.tokens, o.device);
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(o.device));
-    at::Tensor dx = make(x.sizes(), at::kBFloat16, o.device), dw;
-    if (weight) dw = make(w.sizes(), at::kBFloat16, o.device);
+    Backward b{make(x.sizes(), at::kBFloat16, o.device), {}};
+    if (weight) b.dw = make(w.sizes(), at::kBFloat16, o.device);
     const uint64_t bytes = lct_loss_work_bytes(
         o.ids.tokens, o.ids.vocab, o.cols, o.rows,
         LCT_LOSS_BACKWARD | (weight ? LCT_LOSS_WEIGHT : 0) | (o.unaligned ? LCT_LOSS_UNALIGNED : 0));
     at::Tensor work = make({static_cast<int64_t>(bytes)}, at::kByte, o.device);
     check(lct_loss_backward(&o.ids, o.x.p, o.x.ld, o.cols, o.w.p, o.w.ld, 0, o.rows,
                             static_cast<const float *>(loss.data_ptr()), static_cast<const float *>(lse.data_ptr()), u.dloss,
-                            u.stride, u.scale, static_cast<uint16_t *>(dx.data_ptr()), o.cols,
-                            weight ? static_cast<uint16_t *>(dw.data_ptr()) : nullptr, o.cols, work.data_ptr(), bytes,
+                            u.stride, u.scale, static_cast<uint16_t *>(b.dx.data_ptr()), o.cols,
+                            weight ? static_cast<uint16_t *>(b.dw.data_ptr()) : nullptr, o.cols, work.data_ptr(), bytes,
                             stream_of(o.device)),
           "lct_loss_backward");
-    return tuple_of({THPVariable_Wrap(dx), weight ? THPVariable_Wrap(dw) : Py_NewRef(Py_None)});
+    return b;
+}
+
+// (x, weight, targets, loss, lse, dloss, weight_grad) -> (dx, dw or None)
+PyObject *cross_entropy_grads(PyObject *const *a)
+{
+    const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
+    const at::Tensor &loss = tensor(a[3], "loss must be a tensor"), &lse = tensor(a[4], "lse must be a tensor");
+    const at::Tensor &dloss = tensor(a[5], "dloss must be a tensor");
+    no_gradient({&x, &w, &loss, &lse, &dloss}, "cross_entropy_grads");
+    const Backward b =
+        loss_backward(x, w, tensor(a[2], "targets must be a tensor"), loss, lse, dloss, at::Tensor(), a[6] == Py_True);
+    return tuple_of({THPVariable_Wrap(b.dx), b.dw.defined() ? THPVariable_Wrap(b.dw) : Py_NewRef(Py_None)});
+}
+
+// The mean or sum in a tensor of its own, which shares its memory with the three totals.
+at::Tensor reduced(const Forward &f, int reduction)
+{
+    if (reduction == NONE) return f.loss;
+    at::Tensor r = at::empty({0}, f.total.options());
+    r.set_(f.total.storage(), reduction == MEAN ? 1 : 0, {}, {});
+    return r;
+}
+
+// Under autograd by torch's C++ side: its Python side takes longer than the kernels of a small step.  A Python error that
+// the checks set is handed on as torch's.
+[[noreturn]] void as_torch_error()
+{
+    PyGILState_STATE gil = PyGILState_Ensure();
+    PyObject *type, *value, *trace;
+    PyErr_Fetch(&type, &value, &trace);
+    PyObject *text = value ? PyObject_Str(value) : nullptr;
+    const char *c = text ? PyUnicode_AsUTF8(text) : nullptr;
+    const std::string what = c ? c : "linear_cross_entropy failed";
+    Py_XDECREF(text);
+    Py_XDECREF(type);
+    Py_XDECREF(value);
+    Py_XDECREF(trace);
+    PyErr_Clear();
+    PyGILState_Release(gil);
+    TORCH_CHECK(false, what);
+}
+
+struct LinearCrossEntropy : torch::autograd::Function<LinearCrossEntropy> {
+    static at::Tensor forward(torch::autograd::AutogradContext *ctx, const at::Tensor &x, const at::Tensor &w,
+                              const at::Tensor &targets, int64_t reduction)
+    {
+        const at::Tensor rows = as_rows(x, w.size(1));
+        const Forward f = loss_forward(rows, w, targets, true);
+        ctx->save_for_backward({rows, w, targets, f.loss, f.lse, f.total});
+        ctx->saved_data["reduction"] = reduction;
+        ctx->saved_data["shape"] = x.sizes().vec();
+        // (a token's losses are also saved: autograd has to be able to give the caller a tensor of its own)
+        return reduction == NONE ? f.loss.clone() : reduced(f, static_cast<int>(reduction));
+    }
+    static torch::autograd::variable_list backward(torch::autograd::AutogradContext *ctx, torch::autograd::variable_list dy)
+    {
+        const auto saved = ctx->get_saved_variables();
+        const int64_t reduction = ctx->saved_data["reduction"].toInt();
+        torch::autograd::variable_list grads(4);
+        {
+            const at::AutoGradMode off(false);
+            at::Tensor dloss = dy[0].to(at::kFloat).contiguous();
+            const at::Tensor scale = reduction == MEAN ? saved[5].slice(0, 2, 3) : at::Tensor();
+            Backward b;
+            try {
+                const PyGILState_STATE gil = PyGILState_Ensure();
+                struct Release {
+                    PyGILState_STATE gil;
+                    ~Release() { PyGILState_Release(gil); }
+                } release{gil};
+                b = loss_backward(saved[0], saved[1], saved[2], saved[3], saved[4], dloss, scale, ctx->needs_input_grad(1));
+            } catch (const Raised &) {
+                as_torch_error();
+            }
+            if (ctx->needs_input_grad(0)) grads[0] = b.dx.view(ctx->saved_data["shape"].toIntVector());
+            if (ctx->needs_input_grad(1)) grads[1] = b.dw;
+        }
+        // the gradients' own gradients are not there: asking for them raises
+        if (at::GradMode::is_enabled() && (dy[0].requires_grad() || saved[0].requires_grad() || saved[1].requires_grad())) {
+            torch::autograd::variable_list some;
+            for (const at::Tensor &g : grads)
+                if (g.defined()) some.push_back(g.set_requires_grad(true));
+            const auto error = std::make_shared<torch::autograd::DelayedError>(
+                "linear_cross_entropy is differentiable once", static_cast<int64_t>(some.size()));
+            some = (*error)(std::move(some));
+            size_t i = 0;
+            for (at::Tensor &g : grads)
+                if (g.defined()) g = some[i++];
+        }
+        return grads;
+    }
+};
+
+// (x, weight, targets, reduction) -> loss
+PyObject *linear_cross_entropy(PyObject *const *a)
+{
+    const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
+    const at::Tensor &targets = tensor(a[2], "targets must be a tensor");
+    const int reduction = static_cast<int>(number(a[3]));
+    need(w.dim() == 2 && x.dim() >= 1 && x.size(x.dim() - 1) == w.size(1), "expected x [..., columns] and weight [vocabulary, columns]");
+    if (at::GradMode::is_enabled() && (x.requires_grad() || w.requires_grad()))
+        return THPVariable_Wrap(LinearCrossEntropy::apply(x, w, targets, static_cast<int64_t>(reduction)));
+    return THPVariable_Wrap(reduced(loss_forward(as_rows(x, w.size(1)), w, targets, true), reduction));
 }
 
 // (x, piece, first, vocab, targets, loss, lse, dloss, scale or None, dx, dw's piece or None, work) -> None
@@ -609,8 +732,10 @@ PyObject *cross_entropy_grads_piece(PyObject *const *a)
 {
     const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
     const LossOperands o = loss_operands(x, w, tensor(a[4], "targets must be a tensor"), a[2], a[3]);
-    const at::Tensor &loss = floats(a[5], o.ids.tokens, o.device, "loss"), &lse = floats(a[6], o.ids.tokens, o.device, "lse");
-    const Upstream u = upstream_of(a[7], a[8], o.ids.tokens, o.device);
+    const at::Tensor &loss = floats(tensor(a[5], "loss must be a tensor"), o.ids.tokens, o.device, "loss");
+    const at::Tensor &lse = floats(tensor(a[6], "lse must be a tensor"), o.ids.tokens, o.device, "lse");
+    const at::Tensor scale = maybe(a[8], "scale must be a tensor or None");
+    const Upstream u = upstream_of(tensor(a[7], "dloss must be a tensor"), scale, o.ids.tokens, o.device);
     const Rows dx = rows_of(tensor(a[9], "dx must be a tensor"), o.cols, o.ids.tokens, o.device, "dx");
     Rows dw;
     if (a[10] != Py_None) dw = rows_of(tensor(a[10], "dw must be a tensor or None"), o.cols, o.rows, o.device, "dw");
@@ -670,9 +795,10 @@ PyMethodDef methods[] = {method<grad_norm, 1>("grad_norm"),
                          method<adapter_grads, 12>("adapter_grads"),
                          method<embedding, 6>("embedding"),
                          method<embedding_grad, 6>("embedding_grad"),
-                         method<cross_entropy, 4>("cross_entropy"),
+                         method<cross_entropy, 3>("cross_entropy"),
                          method<cross_entropy_piece, 9>("cross_entropy_piece"),
-                         method<cross_entropy_grads, 8>("cross_entropy_grads"),
+                         method<cross_entropy_grads, 7>("cross_entropy_grads"),
+                         method<linear_cross_entropy, 4>("linear_cross_entropy"),
                          method<cross_entropy_grads_piece, 12>("cross_entropy_grads_piece"),
                          method<loss_work_bytes, 5>("loss_work_bytes"),
                          method<set_error, 1>("set_error"),

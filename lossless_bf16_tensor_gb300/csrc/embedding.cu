@@ -26,12 +26,119 @@ namespace dev {
 
 // --------------------------------------------------------- sorting the ids
 
+// A row of a value, or of a base: a warp's, in 16-byte pieces between its ends.
+__device__ __forceinline__ void fill_row(const FillArgs &f, int64_t r)
+{
+    const int lane = threadIdx.x & 31;
+    uint16_t *row = reinterpret_cast<uint16_t *>(static_cast<char *>(f.out) + r * f.ld_out);
+    const uint16_t *base =
+        f.base ? reinterpret_cast<const uint16_t *>(static_cast<const char *>(f.base) + r * f.ld_base) : nullptr;
+    const int n = static_cast<int>((r == f.rows - 1 ? f.last : f.bytes) / 2);
+    const uint16_t value = static_cast<uint16_t>(f.value);
+    int a = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 2, pieces = 0;
+    if (!base || ((reinterpret_cast<uintptr_t>(base) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0)
+        pieces = max(0, n - a) / 8;
+    if (pieces == 0) a = 0;
+    for (int c = lane; c < a; c += 32) row[c] = base ? base[c] : value;
+    uint4 *q = reinterpret_cast<uint4 *>(row + a);
+    if (base) {
+        const uint4 *b = reinterpret_cast<const uint4 *>(base + a);
+        for (int c0 = lane; c0 < pieces; c0 += 32 * 8) {
+            uint4 v[8];  // asked for together: nobody tells the compiler that the rows are apart
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c0 + 32 * i < pieces) v[i] = b[c0 + 32 * i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c0 + 32 * i < pieces) q[c0 + 32 * i] = v[i];
+        }
+    } else {
+        const uint4 v = make_uint4(f.value, f.value, f.value, f.value);
+#pragma unroll 4
+        for (int c = lane; c < pieces; c += 32) q[c] = v;
+    }
+    for (int c = a + 8 * pieces + lane; c < n; c += 32) row[c] = base ? base[c] : value;
+}
+
+// While the ids are being sorted, the other blocks of the same launch write what
+// needs no order: the last rows, with or without tokens (those with tokens are
+// replaced later), as many as that time allows.
+__device__ __forceinline__ void fill(const FillArgs &f, int64_t warp, int64_t warps)
+{
+    for (int64_t r = f.rows - f.early + warp; r < f.rows; r += warps) fill_row(f, r);
+}
+
+// Ids outside 0 .. vocab - 1 become `vocab` and end up behind the others.
+__device__ __forceinline__ int key_of(const SortArgs &g, int64_t i)
+{
+    const int64_t id = id_at(g.ids, g.wide, i);
+    return id < 0 || id >= g.vocab ? g.vocab : static_cast<int>(id);
+}
+
+// Batches up to 8192 ids: an id's place is the number of smaller ones and of
+// equal ones before it, and 67 million comparisons, 64 ids a block, are done
+// before a cluster has met once.
+constexpr int kRankThreads = 256, kRankIds = 64, kRankMost = 8192;
+__global__ void __launch_bounds__(kRankThreads) k_rank_ids(const __grid_constant__ SortArgs g)
+{
+    extern __shared__ int4 keys4[];
+    __shared__ int found[kRankThreads / kRankIds][kRankIds];
+    __shared__ int there;
+    int *keys = reinterpret_cast<int *>(keys4);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int blocks = (g.tokens + kRankIds - 1) / kRankIds;
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        const int warps = kRankThreads / 32;
+        fill(g.fill, (blockIdx.x - blocks) * static_cast<int64_t>(warps) + threadIdx.x / 32,
+             static_cast<int64_t>(gridDim.x - blocks) * warps);
+        return;
+    }
+    if (g.clear && blockIdx.x == 0 && threadIdx.x < 2) g.clear[threadIdx.x] = 0;
+    if (threadIdx.x == 0) there = 0;
+    const int padded = (g.tokens + 15) & ~15;
+    int valid = 0;
+#pragma unroll 8
+    for (int j = threadIdx.x; j < padded; j += kRankThreads) {
+        const int key = j < g.tokens ? key_of(g, j) : INT32_MAX;
+        keys[j] = key;
+        valid += key < g.vocab;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        valid = __reduce_add_sync(kFull, valid);
+        if ((threadIdx.x & 31) == 0) atomicAdd(&there, valid);
+    }
+    const int mine = threadIdx.x % kRankIds, part = threadIdx.x / kRankIds;
+    const int i0 = blockIdx.x * kRankIds, i = i0 + mine;
+    const int key = i < g.tokens ? keys[i] : 0;
+    // a quarter of the ids: those before the block's, those among them, those behind
+    const int quarter = padded / 4, lo = part * quarter, hi = lo + quarter;
+    auto smaller = [&](int from, int to, int than) {
+        int n = 0;
+#pragma unroll 4
+        for (int j = from; j < to; j += 4) {
+            const int4 k = keys4[j / 4];
+            n += (k.x < than) + (k.y < than) + (k.z < than) + (k.w < than);
+        }
+        return n;
+    };
+    int n = smaller(lo, min(hi, i0), key + 1) + smaller(max(lo, i0 + kRankIds), hi, key);
+    for (int j = max(lo, i0); j < min(hi, i0 + kRankIds); ++j) n += keys[j] < key + (j < i);
+    found[part][mine] = n;
+    __syncthreads();
+    if (part == 0 && i < g.tokens) {
+        const int place = n + found[1][mine] + found[2][mine] + found[3][mine];
+        g.key[0][place] = key;
+        g.order[0][place] = i;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *g.count = there;
+}
+
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortBlocks = 8;
 
-// Stable radix sort of the ids by one cluster: least digit first, a warp
-// counting and placing 32 consecutive ids at a time.  Ids outside 0 .. vocab - 1
-// become `vocab` and end up behind the others.  Then first[v], where v's ids
-// begin (-1: none), and the number of ids that are there.
+// Longer batches: stable radix sort by one cluster, least digit first, a warp
+// counting and placing 32 consecutive ids at a time.
 __global__ void __launch_bounds__(kSortThreads) k_sort_ids(const __grid_constant__ SortArgs g)
 {
     extern __shared__ uint32_t counts[];  // [warps][digits], then the block's totals [digits]
@@ -45,16 +152,19 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_ids(const __grid_constant
     const int64_t lo = static_cast<int64_t>(rank * kSortWarps + warp) * share;
     const int64_t hi = min(lo + share, static_cast<int64_t>(g.tokens));
     pdl_wait();
+    pdl_launch_dependents();
+    if (blockIdx.x >= size) {
+        fill(g.fill, static_cast<int64_t>(blockIdx.x - size) * kSortWarps + warp,
+             static_cast<int64_t>(gridDim.x - size) * kSortWarps);
+        return;
+    }
     if (g.clear && rank == 0 && threadIdx.x < 2) g.clear[threadIdx.x] = 0;
-    if (g.first)
-        for (int v = rank * kSortThreads + threadIdx.x; v < g.vocab; v += size * kSortThreads) g.first[v] = -1;
     for (int pass = 0; pass < g.passes; ++pass) {
         const int to = (g.passes - 1 - pass) & 1, shift = pass * g.bits;
         auto key_at = [&](int64_t i) -> int {
             if (i >= hi) return -1;
             if (pass) return __ldcg(&g.key[to ^ 1][i]);
-            const int64_t id = id_at(g.ids, g.wide, i);
-            return id < 0 || id >= g.vocab ? g.vocab : static_cast<int>(id);
+            return key_of(g, i);
         };
         for (int d = lane; d < digits; d += 32) mine[d] = 0;
         __syncwarp();
@@ -69,11 +179,16 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_ids(const __grid_constant
         // each warp's place within the block's ids of a digit
         for (int d = threadIdx.x; d < digits; d += kSortThreads) {
             uint32_t sum = 0;
+#pragma unroll 1
+            for (int w0 = 0; w0 < kSortWarps; w0 += 16) {
+                uint32_t c[16];
 #pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t c = counts[w * digits + d];
-                counts[w * digits + d] = sum;
-                sum += c;
+                for (int w = 0; w < 16; ++w) c[w] = counts[(w0 + w) * digits + d];
+#pragma unroll
+                for (int w = 0; w < 16; ++w) {
+                    counts[(w0 + w) * digits + d] = sum;
+                    sum += c[w];
+                }
             }
             total[d] = sum;
         }
@@ -118,16 +233,9 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_ids(const __grid_constant
     }
     for (int64_t i = lo + lane; i < hi; i += 32) {
         const int key = __ldcg(&g.key[0][i]), last = i ? __ldcg(&g.key[0][i - 1]) : -1;
-        if (key != last) {
-            if (key < g.vocab) {
-                if (g.first) g.first[key] = static_cast<int>(i);
-            } else {
-                *g.count = static_cast<int>(i);
-            }
-        }
+        if (key != last && key >= g.vocab) *g.count = static_cast<int>(i);
         if (i == g.tokens - 1 && key < g.vocab) *g.count = g.tokens;
     }
-    if (g.tokens == 0 && rank == 0 && threadIdx.x == 0) *g.count = 0;
 }
 
 // ------------------------------------------------------------------ lookup
@@ -142,6 +250,7 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding(const __grid_constant
     Piece<T, AL> p[ROWS];
     int64_t id[ROWS];
     pdl_wait();
+    pdl_launch_dependents();
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) id[r] = i0 + r < g.tokens ? id_at(g.ids, g.wide, i0 + r) : -1;
 #pragma unroll
@@ -170,28 +279,25 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding(const __grid_constant
 
 // ---------------------------------------------------------------- gradient
 
-constexpr int kSegTokens = LCT_EMBEDDING_CHUNK;
+constexpr int kSegTokens = 32;  // of a chunk, at most
 constexpr int kSegAhead = 8;  // rows asked for at a time
 
 // A finished row: scaled, added to its base, rounded once.  Compact sums
 // (float32, unscaled) go to the row of the id's first token instead.
 template <typename T, bool AL>
 __device__ __forceinline__ void finish_row(const SegmentArgs &g, int key, int first, int slab,
-                                           const float (&acc)[RowPiece<T, AL>::kVec])
+                                           const float (&acc)[RowPiece<T, AL>::kVec], const Piece<T, AL> &base)
 {
     using P = RowPiece<T, AL>;
     if (g.compact) {
-        float *row = static_cast<float *>(g.out) + first * g.ld_out;
-#pragma unroll
-        for (int e = 0; e < P::kVec; ++e)
-            if (P::col(slab, e) < g.cols) row[P::col(slab, e)] = acc[e];
+        FloatPiece<T, AL>::store(acc, static_cast<float *>(g.out) + first * g.ld_out, slab, g.cols);
+        if (slab == 0 && threadIdx.x == 0) g.first[key] = first;
         return;
     }
     Piece<T, AL> p;
-    if (g.base) p.load(static_cast<const T *>(g.base) + key * g.ld_base, slab, g.cols);
 #pragma unroll
     for (int e = 0; e < P::kVec; ++e)
-        p.v[e] = from_float<T>(g.base ? fmaf(g.scale, acc[e], to_float(p.v[e])) : g.scale * acc[e]);
+        p.v[e] = from_float<T>(g.base ? fmaf(g.scale, acc[e], to_float(base.v[e])) : g.scale * acc[e]);
     p.store(static_cast<T *>(g.out) + key * g.ld_out, slab, g.cols);
 }
 
@@ -202,48 +308,67 @@ __device__ __forceinline__ float *partial(const SegmentArgs &g, int64_t chunk, i
     return g.part + (chunk * 2 + which) * g.cols;
 }
 
-// Rows without tokens: zero, or their base.
-template <typename T, bool AL>
-__device__ __forceinline__ void fill_rows(const SegmentArgs &g, int64_t block)
+// The first of the sorted ids that is not smaller than v, by a warp: 32 of them
+// are looked at in one trip to memory.
+__device__ __forceinline__ int64_t lower_bound(const int32_t *key, int64_t count, int v)
 {
-    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
-    const int64_t r0 = block * g.fill_rows, r1 = min(r0 + g.fill_rows, static_cast<int64_t>(g.vocab));
-    for (int64_t r = r0 + threadIdx.x / 32; r < r1; r += warps) {
-        if (g.first[r] >= 0) continue;
-        T *row = static_cast<T *>(g.out) + r * g.ld_out;
-        const T *base = g.base ? static_cast<const T *>(g.base) + r * g.ld_base : nullptr;
-        // whole 16-byte pieces between the row's ends, where both rows have them
-        const uint32_t skip = (reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T);
-        constexpr int kPer = 16 / sizeof(T);
-        int a = AL || !skip ? 0 : kPer - static_cast<int>(skip), n = 0;
-        if (AL || !base || ((reinterpret_cast<uintptr_t>(base) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0)
-            n = max(0, g.cols - a) / kPer;
-        if (n == 0) a = 0;
-        for (int c = lane; c < a; c += 32) row[c] = base ? base[c] : from_float<T>(0.0f);
-        uint4 *q = reinterpret_cast<uint4 *>(row + a);
-        const uint4 *b = reinterpret_cast<const uint4 *>(base + a);
-#pragma unroll 4
-        for (int c = lane; c < n; c += 32) q[c] = base ? __ldg(b + c) : make_uint4(0, 0, 0, 0);
-        for (int c = a + n * kPer + lane; c < g.cols; c += 32) row[c] = base ? base[c] : from_float<T>(0.0f);
+    const int lane = threadIdx.x & 31;
+    int64_t lo = 0, n = count;  // the place is lo .. lo + n
+    while (n > 0) {
+        const int64_t step = (n + 31) / 32, at = lo + step * lane;
+        const bool smaller = at < lo + n && key[at] < v;
+        const int below = __popc(__ballot_sync(kFull, smaller));
+        if (below == 0) return lo;
+        const int64_t next = lo + step * (below - 1) + 1;
+        n = min(step - 1, lo + n - next);
+        lo = next;
+    }
+    return lo;
+}
+
+// Rows without tokens, of the vocabulary's kFillRows rows that the block has.
+constexpr int kFillRows = 512;
+__device__ __forceinline__ void fill_rest(const SegmentArgs &g, int64_t block)
+{
+    __shared__ uint32_t have[kFillRows / 32];
+    __shared__ int64_t ends[2];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    const int64_t r0 = block * g.fill_rows, r1 = min(r0 + g.fill_rows, g.fill.rows - g.fill.early), count = *g.count;
+    for (int i = threadIdx.x; i < kFillRows / 32; i += blockDim.x) have[i] = 0;
+    for (int i = warp; i < 2; i += warps) {
+        const int64_t at = lower_bound(g.key, count, static_cast<int>(i ? r1 : r0));
+        if (lane == 0) ends[i] = at;
+    }
+    __syncthreads();
+    for (int64_t i = ends[0] + threadIdx.x; i < ends[1]; i += blockDim.x) {
+        const int r = g.key[i] - static_cast<int>(r0);
+        atomicOr(&have[r / 32], 1u << (r & 31));
+    }
+    __syncthreads();
+    for (int64_t r = r0 + warp; r < r1; r += warps) {
+        const int at = static_cast<int>(r - r0);
+        if (!(have[at / 32] >> (at & 31) & 1)) fill_row(g.fill, r);
     }
 }
 
-// Chunks of sorted tokens by the first blocks, rows without tokens by the rest.
-template <typename T, bool AL>
+// A chunk of sorted tokens and a slab of columns a block; rows without tokens by the blocks behind them.
+template <typename T, bool AL, bool BASE>
 __global__ void __launch_bounds__(kRowThreads) k_segments(const __grid_constant__ SegmentArgs g)
 {
     using P = RowPiece<T, AL>;
     __shared__ int keys[kSegTokens], tokens[kSegTokens];
     __shared__ float coefs[kSegTokens];
     pdl_wait();
-    if (blockIdx.x >= g.chunks * g.slabs) {
-        fill_rows<T, AL>(g, blockIdx.x - g.chunks * g.slabs);
+    pdl_launch_dependents();
+    const uint32_t blocks = g.chunks * g.slabs;
+    if (blockIdx.x >= blocks) {
+        fill_rest(g, blockIdx.x - blocks);
         return;
     }
     const int64_t chunk = blockIdx.x / g.slabs;
     const int slab = blockIdx.x % g.slabs;
-    const int64_t i0 = chunk * kSegTokens;
-    const int n = static_cast<int>(min(static_cast<int64_t>(kSegTokens), *g.count - i0));
+    const int64_t i0 = chunk * g.chunk;
+    const int n = static_cast<int>(min(static_cast<int64_t>(g.chunk), *g.count - i0));
     if (n <= 0) return;
     for (int j = threadIdx.x; j < n; j += blockDim.x) {
         keys[j] = g.key[i0 + j];
@@ -257,10 +382,16 @@ __global__ void __launch_bounds__(kRowThreads) k_segments(const __grid_constant_
 #pragma unroll
     for (int e = 0; e < P::kVec; ++e) acc[e] = 0.0f;
     for (int j0 = 0; j0 < n; j0 += kSegAhead) {
-        Piece<T, AL> p[kSegAhead];
+        Piece<T, AL> p[kSegAhead], base[BASE ? kSegAhead : 1];
 #pragma unroll
-        for (int j = 0; j < kSegAhead; ++j)
-            if (j0 + j < n) p[j].load(static_cast<const T *>(g.src) + tokens[j0 + j] * g.ld_src, slab, g.cols);
+        for (int j = 0; j < kSegAhead; ++j) {
+            const int at = j0 + j;
+            if (at >= n) continue;
+            p[j].load(static_cast<const T *>(g.src) + tokens[at] * g.ld_src, slab, g.cols);
+            // an id's last row: its base is wanted as well
+            if (BASE && (at + 1 == n || keys[at + 1] != keys[at]))
+                base[j].load(static_cast<const T *>(g.base) + keys[at] * g.ld_base, slab, g.cols);
+        }
 #pragma unroll
         for (int j = 0; j < kSegAhead; ++j) {
             const int at = j0 + j;
@@ -270,12 +401,11 @@ __global__ void __launch_bounds__(kRowThreads) k_segments(const __grid_constant_
             for (int e = 0; e < P::kVec; ++e) acc[e] = fmaf(f, to_float(p[j].v[e]), acc[e]);
             if (at + 1 < n && keys[at + 1] == keys[at]) continue;
             if (began < 0 || (at == n - 1 && goes_on)) {
-                float *to = partial(g, chunk, began < 0 ? 0 : 1);
-#pragma unroll
-                for (int e = 0; e < P::kVec; ++e)
-                    if (P::col(slab, e) < g.cols) to[P::col(slab, e)] = acc[e];
+                FloatPiece<T, AL>::store(acc, partial(g, chunk, began < 0 ? 0 : 1), slab, g.cols);
+                // where it began, for the kernel that adds the parts
+                if (g.compact && began >= 0 && slab == 0 && threadIdx.x == 0) g.first[keys[at]] = static_cast<int>(began);
             } else {
-                finish_row<T, AL>(g, keys[at], static_cast<int>(began), slab, acc);
+                finish_row<T, AL>(g, keys[at], static_cast<int>(began), slab, acc, base[BASE ? j : 0]);
             }
             began = i0 + at + 1;
 #pragma unroll
@@ -290,7 +420,8 @@ __global__ void __launch_bounds__(kRowThreads) k_segment_ends(const __grid_const
 {
     using P = RowPiece<T, AL>;
     pdl_wait();
-    const int64_t chunk = blockIdx.x / g.slabs, i0 = chunk * kSegTokens, next = i0 + kSegTokens, count = *g.count;
+    pdl_launch_dependents();
+    const int64_t chunk = blockIdx.x / g.slabs, i0 = chunk * g.chunk, next = i0 + g.chunk, count = *g.count;
     const int slab = blockIdx.x % g.slabs, lane = threadIdx.x & 31;
     if (next >= count) return;
     const int key = g.key[next - 1];
@@ -298,7 +429,7 @@ __global__ void __launch_bounds__(kRowThreads) k_segment_ends(const __grid_const
     // the chunks that the id goes on in
     int64_t more = 0;
     for (;; more += 32) {
-        const int64_t at = next + (more + lane) * kSegTokens;
+        const int64_t at = next + (more + lane) * g.chunk;
         const uint32_t same = __ballot_sync(kFull, at < count && g.key[at] == key);
         if (same != kFull) {
             more += __ffs(~same) - 1;
@@ -306,33 +437,48 @@ __global__ void __launch_bounds__(kRowThreads) k_segment_ends(const __grid_const
         }
     }
     float acc[P::kVec];
-    const float *from = partial(g, chunk, 1);
-#pragma unroll
-    for (int e = 0; e < P::kVec; ++e) acc[e] = P::col(slab, e) < g.cols ? from[P::col(slab, e)] : 0.0f;
-#pragma unroll 4
+    FloatPiece<T, AL>::load(acc, partial(g, chunk, 1), slab, g.cols);
+    Piece<T, AL> base;
+    if (g.base) base.load(static_cast<const T *>(g.base) + key * g.ld_base, slab, g.cols);
+#pragma unroll 8
     for (int64_t c = 1; c <= more; ++c) {
-        from = partial(g, chunk + c, 0);
+        float v[P::kVec];
+        FloatPiece<T, AL>::load(v, partial(g, chunk + c, 0), slab, g.cols);
 #pragma unroll
-        for (int e = 0; e < P::kVec; ++e)
-            if (P::col(slab, e) < g.cols) acc[e] += from[P::col(slab, e)];
+        for (int e = 0; e < P::kVec; ++e) acc[e] += v[e];
     }
     const int first = g.compact ? g.first[key] : 0;
-    finish_row<T, AL>(g, key, first, slab, acc);
+    finish_row<T, AL>(g, key, first, slab, acc, base);
 }
 
 }  // namespace dev
 
 // ------------------------------------------------------------------ launches
 
+// Fill blocks of `bytes_each` at a time, at most `most`.
+static uint32_t fill_blocks(const FillArgs &f, uint64_t bytes_each, uint64_t most)
+{
+    if (!f.out || !f.early) return 0;
+    const uint64_t bytes = static_cast<uint64_t>(f.early) * static_cast<uint64_t>(f.bytes);
+    return static_cast<uint32_t>(std::min(most, (bytes + bytes_each - 1) / bytes_each));
+}
+
 cudaError_t launch_sort_ids(SortArgs g, cudaStream_t s)
 {
+    const uint32_t tokens = static_cast<uint32_t>(g.tokens);
+    if (tokens <= dev::kRankMost) {
+        const uint32_t blocks = (tokens + dev::kRankIds - 1) / dev::kRankIds + fill_blocks(g.fill, 65536, 152 * 6);
+        return blocks ? launch<true>(dev::k_rank_ids, dim3(blocks), dev::kRankThreads, (tokens + 15) / 16 * 64, 1, s, g)
+                      : cudaSuccess;
+    }
     int need = 1;
     while (need < 31 && g.vocab >> need) ++need;  // bits of `vocab`, the largest key
     g.passes = (need + 8) / 9;
     g.bits = (need + g.passes - 1) / g.passes;
     const uint32_t smem = (dev::kSortWarps + 1) * (4u << g.bits);
-    return launch<true>(dev::k_sort_ids, dim3(g.tokens > 4096 ? dev::kSortBlocks : 1), dev::kSortThreads, smem,
-                        g.tokens > 4096 ? dev::kSortBlocks : 1, s, g);
+    const uint32_t fills = fill_blocks(g.fill, 262144, 152 * 2 - dev::kSortBlocks);
+    return launch<true>(dev::k_sort_ids, dim3((fills + dev::kSortBlocks - 1) / dev::kSortBlocks * dev::kSortBlocks + dev::kSortBlocks),
+                        dev::kSortThreads, smem, dev::kSortBlocks, s, g);
 }
 
 namespace {
@@ -349,17 +495,22 @@ cudaError_t lookup(const LookupArgs &g, cudaStream_t s)
 }
 
 template <typename T, bool AL>
-cudaError_t segments(SegmentArgs g, bool fill, cudaStream_t s)
+cudaError_t segments(SegmentArgs g, cudaStream_t s)
 {
     uint32_t threads;
     row_shape(g.cols, dev::RowPiece<T, AL>::kVec, &threads, &g.slabs);
-    g.chunks = (static_cast<uint32_t>(g.tokens) + dev::kSegTokens - 1) / dev::kSegTokens;
-    // a fill block's rows: about 64 KB
-    g.fill_rows = static_cast<int32_t>(std::max<uint64_t>(threads / 32, 65536 / (sizeof(T) * static_cast<uint64_t>(g.cols))));
-    const uint32_t fills = fill ? (static_cast<uint32_t>(g.vocab) + g.fill_rows - 1) / g.fill_rows : 0;
-    cudaError_t rc = cudaSuccess;
-    if (g.chunks * g.slabs + fills)
-        rc = launch<true>(dev::k_segments<T, AL>, dim3(g.chunks * g.slabs + fills), threads, 0, 1, s, g);
+    g.chunk = static_cast<int32_t>(LCT_EMBEDDING_CHUNK(static_cast<uint64_t>(g.tokens)));
+    g.chunks = (static_cast<uint32_t>(g.tokens) + g.chunk - 1) / g.chunk;
+    uint64_t fills = 0;
+    if (g.fill.out) {  // about 64 KB a block
+        g.fill_rows = static_cast<int32_t>(
+            std::min<int64_t>(dev::kFillRows, std::max<int64_t>(threads / 32, 65536 / g.fill.bytes)));
+        fills = (static_cast<uint64_t>(g.fill.rows - g.fill.early) + g.fill_rows - 1) / g.fill_rows;
+    }
+    if (!g.chunks && !fills) return cudaSuccess;
+    const dim3 grid(static_cast<uint32_t>(g.chunks * g.slabs + fills));
+    cudaError_t rc = g.base ? launch<true>(dev::k_segments<T, AL, true>, grid, threads, 0, 1, s, g)
+                            : launch<true>(dev::k_segments<T, AL, false>, grid, threads, 0, 1, s, g);
     if (rc == cudaSuccess && g.chunks > 1)
         rc = launch<true>(dev::k_segment_ends<T, AL>, dim3((g.chunks - 1) * g.slabs), threads, 0, 1, s, g);
     return rc;
@@ -367,10 +518,10 @@ cudaError_t segments(SegmentArgs g, bool fill, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_segments(const SegmentArgs &g, bool wide, bool aligned, bool fill, cudaStream_t s)
+cudaError_t launch_segments(const SegmentArgs &g, bool wide, bool aligned, cudaStream_t s)
 {
-    if (wide) return aligned ? segments<float, true>(g, fill, s) : segments<float, false>(g, fill, s);
-    return aligned ? segments<__nv_bfloat16, true>(g, fill, s) : segments<__nv_bfloat16, false>(g, fill, s);
+    if (wide) return aligned ? segments<float, true>(g, s) : segments<float, false>(g, s);
+    return aligned ? segments<__nv_bfloat16, true>(g, s) : segments<__nv_bfloat16, false>(g, s);
 }
 
 cudaError_t launch_lookup(const LookupArgs &g, bool wide, bool aligned, cudaStream_t s)
@@ -390,6 +541,9 @@ lct_status check_ids(const lct_ids *ids)
 }
 
 namespace {
+
+// Bytes of rows that are written while ids are sorted, by the two ways of that.
+constexpr int64_t kFillShort = 24 << 20, kFillLong = 160 << 20;
 
 uint64_t value_bytes(int32_t dtype) { return dtype == LCT_DTYPE_F32 ? 4 : 2; }
 
@@ -443,7 +597,7 @@ extern "C" lct_status lct_embedding_grad(const lct_ids *ids, const void *d_dy, u
     const uint64_t size = value_bytes(dtype), t = ids->tokens;
     const Matrix dy{d_dy, ld_dy, cols, t, size}, out{d_out, ld_out, cols, ids->vocab, size};
     const Matrix base{d_base, ld_base, cols, d_base ? ids->vocab : 0, size};
-    const uint64_t work = LCT_EMBEDDING_WORK_BYTES(t, ids->vocab, cols), id_bytes = t * (ids->wide ? 8 : 4);
+    const uint64_t work = LCT_EMBEDDING_WORK_BYTES(t, cols), id_bytes = t * (ids->wide ? 8 : 4);
     const bool in_place = d_base == d_out && ld_base == ld_out;
     if (!matrix_ok(dy) || !matrix_ok(out) || !matrix_ok(base)) return LCT_ERR_INVALID_ARG;
     if (!d_work || reinterpret_cast<uintptr_t>(d_work) % 16) return LCT_ERR_INVALID_ARG;
@@ -462,26 +616,36 @@ extern "C" lct_status lct_embedding_grad(const lct_ids *ids, const void *d_dy, u
     sort.key[1] = sort.key[0] + t4;
     sort.order[0] = sort.key[1] + t4;
     sort.order[1] = sort.order[0] + t4;
-    sort.first = sort.order[1] + t4;
     sort.tokens = static_cast<int32_t>(t);
     sort.vocab = static_cast<int32_t>(ids->vocab);
+    if (!in_place) {
+        FillArgs &f = sort.fill;
+        f.out = d_out;
+        f.base = d_base;
+        f.rows = static_cast<int64_t>(ids->vocab);
+        f.bytes = f.last = static_cast<int64_t>(cols * size);
+        f.ld_out = static_cast<int64_t>(ld_out * size);
+        f.ld_base = static_cast<int64_t>(ld_base * size);
+        // what the time of the sort is enough for
+        f.early = t ? std::min<int64_t>(f.rows, (t <= dev::kRankMost ? kFillShort : kFillLong) / f.bytes) : f.rows;
+    }
     if (launch_sort_ids(sort, s) != cudaSuccess) return LCT_ERR_CUDA;
+    if (t == 0) return LCT_OK;  // every row has been written
     SegmentArgs g{};
     g.src = d_dy;
     g.ld_src = static_cast<int64_t>(ld_dy);
     g.key = sort.key[0];
     g.order = sort.order[0];
-    g.first = sort.first;
     g.count = sort.count;
     g.scale = scale;
     g.base = d_base;
     g.ld_base = static_cast<int64_t>(ld_base);
     g.out = d_out;
     g.ld_out = static_cast<int64_t>(ld_out);
-    g.part = reinterpret_cast<float *>(sort.first + (ids->vocab + 3) / 4 * 4);
+    g.part = reinterpret_cast<float *>(sort.order[1] + t4);
+    g.fill = sort.fill;
     g.cols = static_cast<int32_t>(cols);
     g.tokens = static_cast<int32_t>(t);
-    g.vocab = static_cast<int32_t>(ids->vocab);
     const bool aligned = cols * size % 16 == 0 && matrix_al(out) && matrix_al(dy) && matrix_al(base);
-    return launch_segments(g, dtype == LCT_DTYPE_F32, aligned, !in_place, s) == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
+    return launch_segments(g, dtype == LCT_DTYPE_F32, aligned, s) == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
 }

@@ -228,11 +228,20 @@ inline bool apart(const Matrix &x, const Matrix &y)
     return d >= x.cols * x.size && d + y.cols * y.size <= ld;
 }
 
-// Ids sorted: key and order [0] are the result, [1] scratch; first[v] (or NULL), where v's begin, -1 without any.
+// Rows of a value, or of a base, the last `early` of them while ids are sorted.  In bytes.
+struct FillArgs {
+    void *out;                         // NULL: nothing
+    const void *base;                  // or NULL
+    int64_t rows, early, bytes, last;  // the last row may be shorter
+    int64_t ld_out, ld_base;
+    uint32_t value;
+};
+// Ids sorted: key and order [0] are the result, [1] scratch; how many are within the vocabulary.
 struct SortArgs {
     const void *ids;
-    int32_t *key[2], *order[2], *first, *count;
-    int32_t *clear;  // two words that become zero, or NULL
+    int32_t *key[2], *order[2], *count;
+    int32_t *clear;                    // two words that become zero, or NULL
+    FillArgs fill;
     int32_t tokens, vocab, bits, passes;  // bits a pass and passes are set by the launcher
     bool wide;
 };
@@ -247,20 +256,23 @@ struct LookupArgs {
 // Sums of the rows of equal ids, in sorted order.
 struct SegmentArgs {
     const void *src;          // row order[i] (NULL: row i) belongs to key[i]
-    const int32_t *key, *order, *first, *count;
+    const int32_t *key, *order, *count;
+    int32_t *first;           // compact: the row that is key's
     const float *coef;        // [i], or NULL: 1
     const void *base;         // or NULL
-    void *out;                // row key[i]; compact: float32 rows, row first[key[i]]
+    void *out;                // row key[i]; compact: float32 rows, that of the key's first place
     float *part;              // [chunks][2][cols]
     int64_t ld_src, ld_base, ld_out;
     float scale;
-    int32_t cols, tokens, vocab, fill_rows;
-    uint32_t chunks, slabs;   // set by the launcher
+    FillArgs fill;            // rows without tokens, or none
+    int32_t cols, tokens;
+    int32_t chunk, fill_rows; // set by the launcher, as are the next two
+    uint32_t chunks, slabs;
     bool compact;
 };
 cudaError_t launch_sort_ids(SortArgs a, cudaStream_t s);
 cudaError_t launch_lookup(const LookupArgs &a, bool wide, bool aligned, cudaStream_t s);  // wide: float32 values
-cudaError_t launch_segments(const SegmentArgs &a, bool wide, bool aligned, bool fill, cudaStream_t s);
+cudaError_t launch_segments(const SegmentArgs &a, bool wide, bool aligned, cudaStream_t s);
 lct_status check_ids(const lct_ids *ids);
 
 }  // namespace lct

@@ -40,15 +40,17 @@ enum Product { kLogits, kSoftmax, kDx, kDw };
 
 struct ProductArgs {
     int32_t m, n, k;        // rows, columns and depth of the result
+    uint32_t a_rows;        // of a box of A that is not across
     const int32_t *count;   // tokens that are there (rows, or dW's depth); NULL: as given
     int32_t *status;        // latched: a wait that ran out
-    int32_t splits;         // kDx: parts of the depth, each with a result of its own
+    int32_t splits;         // kDx: parts of the depth at most, each with a result of its own
+    int32_t depth, pairs;   // what their number goes by: the same for all pieces
     bool add;               // kDx: to what is there
     bool begins;            // kLogits: a call's first product clears the status and the counter behind it
     const void *ids;        // kLogits: the targets
     bool wide;
     int64_t row0;           // the vocabulary's row that column 0 (kDw: row 0) is
-    float2 *part;           // kLogits: [tiles of 128 columns][m], maximum and sum of exponentials
+    float2 *part;           // kLogits: [units of 64 columns][m], maximum and sum of exponentials
     float *mine;            // kLogits: the targets' logits
     const int32_t *target;  // kSoftmax, packed: targets, l and c
     const float *lse, *share;
@@ -92,7 +94,7 @@ struct FinishArgs {
     const void *ids;
     __nv_bfloat16 *dx;
     int64_t ld_part, ld_w, ld_dx, tokens;
-    int32_t splits, cols;
+    int32_t splits, cols, depth, pairs;  // what dx's product had
     bool gathered, wide;
 };
 
@@ -101,19 +103,34 @@ namespace dev {
 // --------------------------------------------------------- products by pairs
 
 // A tile of 256 by 256 belongs to two blocks of a cluster, which multiply as
-// one (cta_group::2): each holds 128 rows of A, 128 of the columns of B, and the
+// one (cta_group::2): each holds 128 rows of A, half of the columns of B, and the
 // sums of its rows.  Against a block alone on 128 by 256, each operand byte in
 // shared memory is used twice as often.
 constexpr int kTile = 256, kHalfTile = 128, kDepth = 64;
-constexpr int kStages = 6;
+constexpr int kUnit = 64;  // columns that a warp turns into results at a time
 constexpr uint32_t kOperand = kHalfTile * 128;  // 128 rows (or columns) by 64 of depth
 constexpr uint32_t kStage = 2 * kOperand;
-constexpr int kEndWarps = 8, kFirstEndWarp = 4;
-constexpr int kProductThreads = 32 * (kFirstEndWarp + kEndWarps);
-constexpr uint32_t kStagingAt = kStages * kStage, kStaging = 32 * 128;  // a warp's 32 rows of 128 bytes
-constexpr uint32_t kProductBytes = kStagingAt + kEndWarps * kStaging + 1024;
-constexpr int kGroup = 16;  // tiles of rows that are worked on side by side
+constexpr int kFirstEndWarp = 4;
+constexpr uint32_t kStaging = 32 * 128;  // a warp's 32 rows of 128 bytes
+constexpr int kGroup = 16;               // tiles of rows that are worked on side by side
 constexpr float kLog2e = 1.4426950408889634f;
+// Depth of logits that tensor cores add by themselves: their float32 sums drop
+// what does not fit, always towards zero, which over a depth of 4096 makes the
+// losses wrong by 2e-6; each 1024 are added to the rest in registers (5e-7).
+constexpr int kSumSteps = 1024 / kDepth;
+
+// Warps that turn sums into results, four to a unit at a time, and the ring's
+// slots.  Exponentials take long, so that each unit of a tile has its own four;
+// where results leave by boxes, their staging takes the room of a slot.
+template <int OP>
+struct Shape {
+    static constexpr int kGroups = OP == kLogits ? 4 : 2;
+    static constexpr int kEndWarps = 4 * kGroups;
+    static constexpr int kStages = OP == kLogits ? 7 : 6;
+    static constexpr int kThreads = 32 * (kFirstEndWarp + kEndWarps);
+    static constexpr uint32_t kStagingAt = kStages * kStage;
+    static constexpr uint32_t kBytes = kStagingAt + (OP == kLogits ? 0 : kEndWarps * kStaging) + 1024;
+};
 
 __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t word, bool add)
 {
@@ -172,8 +189,8 @@ __device__ __forceinline__ void store_box(const CUtensorMap *m, int x, int y, in
 }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
-// 32 columns of this lane's row, and the wait for them (one statement: nothing that uses them can come between).
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32])
+// Columns of this lane's row, and the wait for them (one statement: nothing that uses them can come between).
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[32])
 {
     uint32_t r[32];
     asm volatile(
@@ -189,6 +206,18 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32])
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[8])
+{
+    uint32_t r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -197,55 +226,84 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// Parts of dx's depth that give the pairs as much to do as can be: tiles go
+// round in turns, and every part costs about three steps more.
+__device__ __forceinline__ int parts_of(int tiles, int depth, int most, int pairs)
+{
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int s = 1; s <= most && s <= max(1, depth / 4); ++s) {
+        const int64_t cost = (static_cast<int64_t>(tiles) * s + pairs - 1) / pairs * ((depth + s - 1) / s + 3);
+        if (cost < least) least = cost, best = s;
+    }
+    return best;
+}
+
 // An item of work: a tile, and the steps of depth that it takes.
 struct Item {
     int tm, tn, split, k0, k1;
 };
-__device__ __forceinline__ Item item_at(int item, int tiles_m, int tiles_n, int splits, int depth)
-{
-    Item w;
-    const int tiles = tiles_m * tiles_n;
-    w.split = item / tiles;
-    const int t = item - w.split * tiles;
-    // groups of kGroup tiles of rows, whose operand stays in L2 while the columns go by
-    const int g = t / (kGroup * tiles_n), in = t - g * kGroup * tiles_n;
-    const int high = min(kGroup, tiles_m - g * kGroup);
-    w.tn = in / high;
-    w.tm = g * kGroup + in - w.tn * high;
-    w.k0 = static_cast<int>(static_cast<int64_t>(depth) * w.split / splits);
-    w.k1 = static_cast<int>(static_cast<int64_t>(depth) * (w.split + 1) / splits);
-    return w;
-}
+// A pair's items: every `pairs`-th tile, in groups of kGroup tiles of rows, whose
+// operand stays in L2 while the columns go by.
+struct Items {
+    int tiles_m, tiles_n, splits, depth, at, end;
+    __device__ __forceinline__ Items(const ProductArgs &g, int m, int k)
+    {
+        tiles_m = (m + kTile - 1) / kTile;
+        tiles_n = (g.n + kTile - 1) / kTile;
+        depth = (k + kDepth - 1) / kDepth;
+        splits = g.splits > 1 ? parts_of(tiles_m * tiles_n, g.depth, g.splits, g.pairs) : 1;
+        at = blockIdx.x / 2;
+        end = tiles_m * tiles_n * splits;
+    }
+    __device__ __forceinline__ bool next(Item &w)
+    {
+        if (at >= end) return false;
+        const int tiles = tiles_m * tiles_n;
+        w.split = at / tiles;
+        const int t = at - w.split * tiles, g = t / (kGroup * tiles_n), in = t - g * kGroup * tiles_n;
+        const int high = min(kGroup, tiles_m - g * kGroup);
+        w.tn = in / high;
+        w.tm = g * kGroup + in - w.tn * high;
+        w.k0 = static_cast<int>(static_cast<int64_t>(depth) * w.split / splits);
+        w.k1 = static_cast<int>(static_cast<int64_t>(depth) * (w.split + 1) / splits);
+        at += gridDim.x / 2;
+        return true;
+    }
+};
 
-// Each row's maximum and sum of exponentials of 32 columns joins (m, s).
-__device__ __forceinline__ void join32(const float (&z)[32], float &m, float &s)
+// Each row's maximum and sum of exponentials of N columns joins (m, s).
+template <int N>
+__device__ __forceinline__ void join_columns(const float (&z)[N], float &m, float &s)
 {
-    float top = m;
+    float t[4] = {m, z[1], z[2], z[3]};
+    t[0] = fmaxf(t[0], z[0]);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) top = fmaxf(top, z[i]);
+    for (int i = 4; i < N; ++i) t[i & 3] = fmaxf(t[i & 3], z[i]);
+    const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
     const float at = top == -INFINITY ? 0.0f : top * kLog2e;
     float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) a[i & 3] += exp2_fast(fmaf(z[i], kLog2e, -at));
+    for (int i = 0; i < N; ++i) a[i & 3] += exp2_fast(fmaf(z[i], kLog2e, -at));
     s = fmaf(s, exp2_fast(fmaf(m, kLog2e, -at)), (a[0] + a[1]) + (a[2] + a[3]));
     m = top;
 }
 
 // Warps by what they do: warp 0 loads boxes (TMA), warp 1 of the first block
-// issues the products, warps 4 to 11 turn sums into results, two to each
+// issues the products, the others turn sums into results, each warp those of a
 // quarter of the rows.  Sums are double-buffered in TMEM, so that a tile's end
 // runs while the next one's products do.
 template <int OP>
-__global__ void __launch_bounds__(kProductThreads, 1)
+__global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     k_product(const __grid_constant__ ProductArgs g, const __grid_constant__ ProductMaps maps)
 {
+    using H = Shape<OP>;
     constexpr bool kAcrossA = OP == kDw, kAcrossB = OP == kDx || OP == kDw;
-    constexpr int S = kStages;
+    constexpr int S = H::kStages;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[S], freed[S], done[2], drained[2];
     __shared__ uint32_t tmem_at;
     const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
     if (warp == 0) pair_alloc(&tmem_at, 512);
@@ -256,7 +314,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&done[i], 1);
-            mbar_init(&drained[i], 2 * kEndWarps);
+            mbar_init(&drained[i], 2 * H::kEndWarps);
         }
         fence_mbar_init();
     }
@@ -267,6 +325,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     tc_after();
     const uint32_t tmem = tmem_at;
     pdl_wait();
+    pdl_launch_dependents();
     if (OP == kLogits && g.begins && blockIdx.x == 0 && threadIdx.x == 0) {
         g.status[0] = 0;
         g.status[1] = 0;
@@ -279,8 +338,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         else
             m = min(m, there);
     }
-    const int tiles_m = (m + kTile - 1) / kTile, tiles_n = (g.n + kTile - 1) / kTile, depth = (k + kDepth - 1) / kDepth;
-    const int items = tiles_m * tiles_n * g.splits;
+    Items items(g, m, k);
+    Item w;
     Waiter waiter;
     // a warp's lanes give up together
     auto wait = [&](uint64_t *bar, int parity) {
@@ -291,19 +350,22 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------------------- boxes
         int i = 0;
-        for (int item = pair; item < items; item += pairs) {
-            const Item w = item_at(item, tiles_m, tiles_n, g.splits, depth);
+        while (items.next(w)) {
             const int row = w.tm * kTile + rank * kHalfTile, col = w.tn * kTile + rank * kHalfTile;
+            // rows of a second block that has none are not fetched: what is there in their place reaches only itself
+            const bool rows = kAcrossA || row < g.m;
+            const uint32_t a_bytes = kAcrossA ? kOperand : g.a_rows * 128;
+            const uint32_t bytes = 2 * kOperand + (kAcrossA || w.tm * kTile + kHalfTile < g.m ? 2 * a_bytes : a_bytes);
             for (int d = w.k0; d < w.k1; ++d, ++i) {
                 const int s = i % S;
                 if (i >= S) wait(&freed[s], (i / S - 1) & 1);
                 if (elect() && !waiter.dead) {
                     const uint32_t bar = peer_addr(smem_addr(&full[s]), 0), a = base + s * kStage, b = a + kOperand;
-                    if (rank == 0) mbar_expect_tx(&full[s], 2 * kStage);
+                    if (rank == 0) mbar_expect_tx(&full[s], bytes);
                     if (kAcrossA) {
                         pair_box(a, &maps.a, row, d * kDepth, bar);
                         pair_box(a + kOperand / 2, &maps.a, row + 64, d * kDepth, bar);
-                    } else {
+                    } else if (rows) {
                         pair_box(a, &maps.a, d * kDepth, row, bar);
                     }
                     if (kAcrossB) {
@@ -325,170 +387,232 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const uint64_t a0 = operand(base, kAcrossA ? kOperand / 2 : 0);
         const uint64_t b0 = operand(base + kOperand, kAcrossB ? kOperand / 2 : 0);
         int i = 0, t = 0;
-        for (int item = pair; item < items; item += pairs) {
-            const Item w = item_at(item, tiles_m, tiles_n, g.splits, depth);
-            if (w.k1 <= w.k0) continue;
-            if (t >= 2) wait(&drained[t & 1], (t / 2 - 1) & 1);
-            const uint32_t sums = tmem + (t & 1) * kTile;
+        while (items.next(w)) {
+            int left = 0;  // steps until these sums are done
+            uint32_t sums = tmem;
+            bool add = false;
             for (int d = w.k0; d < w.k1; ++d, ++i) {
+                if (left == 0) {
+                    left = OP == kLogits ? min(kSumSteps, w.k1 - d) : w.k1 - d;
+                    if (t >= 2) wait(&drained[t & 1], (t / 2 - 1) & 1);
+                    sums = tmem + (t & 1) * kTile;
+                    add = false;
+                }
                 const int s = i % S;
                 wait(&full[s], (i / S) & 1);
                 tc_after();
+                --left;
                 if (elect() && !waiter.dead) {
                     const uint64_t a = a0 + s * (kStage >> 4), b = b0 + s * (kStage >> 4);
 #pragma unroll
                     for (int j = 0; j < kDepth / 16; ++j)
-                        pair_mma(sums, a + j * (kAcrossA ? 128 : 2), b + j * (kAcrossB ? 128 : 2), word, d > w.k0 || j > 0);
+                        pair_mma(sums, a + j * (kAcrossA ? 128 : 2), b + j * (kAcrossB ? 128 : 2), word, add || j > 0);
                     pair_commit(&freed[s]);
-                    if (d == w.k1 - 1) pair_commit(&done[t & 1]);
+                    if (left == 0) pair_commit(&done[t & 1]);
                 }
                 __syncwarp();
+                add = true;
+                if (left == 0) ++t;
             }
-            ++t;
         }
         // every product has ended before the block does
         for (int j = max(0, t - 2); j < t; ++j) wait(&done[j & 1], (j / 2) & 1);
     } else if (warp >= kFirstEndWarp) {
         // -------------------------------------------------------------- ends
-        const int quarter = warp & 3, half = (warp - kFirstEndWarp) / 4;
-        const uint32_t staging = base + kStagingAt + (warp - kFirstEndWarp) * kStaging;
+        const int quarter = warp & 3, group = (warp - kFirstEndWarp) / 4;
+        const uint32_t staging = base + H::kStagingAt + (warp - kFirstEndWarp) * kStaging;
         int t = 0;
-        for (int item = pair; item < items; item += pairs) {
-            const Item w = item_at(item, tiles_m, tiles_n, g.splits, depth);
-            const bool some = w.k1 > w.k0;
-            if (some) {
-                wait(&done[t & 1], (t / 2) & 1);
-                tc_after();
+        // the products after the next may take these sums' place
+        auto arrive = [&] {
+            tc_before();
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                 peer_addr(smem_addr(&drained[t & 1]), 0))
+                             : "memory");
+        };
+        // what a row's results need beside its sums, asked for a tile ahead
+        struct RowInfo {
+            int target;
+            float lse, share;
+            int64_t id;
+        };
+        auto info_of = [&](const Item &of) {
+            RowInfo r = {-1, 0.0f, 0.0f, -1};
+            const int row = of.tm * kTile + rank * kHalfTile + quarter * 32 + lane;
+            if (row < m) {
+                if (OP == kLogits) r.id = id_at(g.ids, g.wide, row);
+                if (OP == kSoftmax) r.target = g.target[row], r.lse = g.lse[row], r.share = g.share[row];
+                if (OP == kDw) r.target = g.first[g.row0 + row];
             }
-            if (waiter.dead) break;
-            const uint32_t sums = tmem + (t & 1) * kTile + half * kHalfTile + (static_cast<uint32_t>(quarter * 32) << 16);
+            return r;
+        };
+        Item ahead;
+        bool more = items.next(ahead);
+        RowInfo info = {}, info_ahead = {};
+        if (more) info_ahead = info_of(ahead);
+        while (more) {
+            w = ahead;
+            info = info_ahead;
+            more = items.next(ahead);
+            if (more) info_ahead = info_of(ahead);
             const int row0 = w.tm * kTile + rank * kHalfTile + quarter * 32, row = row0 + lane;
-            const int col0 = w.tn * kTile + half * kHalfTile;
-            auto load = [&](int c, float(&v)[32]) {
-                if (some) {
-                    tmem_load32(sums + c, v);
-                } else {
+            const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+            if constexpr (OP == kLogits) {
+                // the unit of this warp, its sums over the depth in registers
+                float z[kUnit];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = 0.0f;
-                }
-                if (some && c == kHalfTile - 32) {  // the last of them: the next products may take their place
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                                         peer_addr(smem_addr(&drained[t & 1]), 0))
-                                     : "memory");
-                }
-            };
-            if (OP == kLogits) {
-                const int64_t id = row < m ? id_at(g.ids, g.wide, row) - g.row0 - col0 : -1;
-                float top = -INFINITY, sum = 0.0f;
+                for (int e = 0; e < kUnit; ++e) z[e] = 0.0f;
+                const int col0 = w.tn * kTile + group * kUnit;
 #pragma unroll 1
-                for (int c = 0; c < kHalfTile; c += 32) {
-                    float v[32];
-                    load(c, v);
-                    if (col0 + c + 32 > g.n) {
+                for (int d = w.k0; d < w.k1; d += kSumSteps, ++t) {
+                    wait(&done[t & 1], (t / 2) & 1);
+                    if (waiter.dead) break;
+                    tc_after();
+                    if (col0 < g.n) {
+                        const uint32_t sums = lanes + (t & 1) * kTile + group * kUnit;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (col0 + c + e >= g.n) v[e] = -INFINITY;
-                    }
-                    if (id >= c && id < c + 32 && col0 + id < g.n) {
-                        const int at = static_cast<int>(id) - c;
+                        for (int c = 0; c < kUnit; c += 8) {
+                            float v[8];
+                            tmem_load(sums + c, v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e == at) g.mine[row] = v[e];
-                    }
-                    join32(v, top, sum);
-                }
-                if (row < m && col0 < g.n) g.part[static_cast<int64_t>(w.tn * 2 + half) * m + row] = make_float2(top, sum);
-            } else if (OP == kDx) {
-#pragma unroll 1
-                for (int c = 0; c < kHalfTile; c += 32) {
-                    float v[32];
-                    load(c, v);
-                    if (lane == 0) bulk_wait_read();  // the last box has left
-                    __syncwarp();
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        store16(staging + swz(lane, q),
-                                make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                           __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0 && col0 + c < g.n && row0 < m) {
-                        store_box(&maps.c, col0 + c, row0, w.split, staging, g.add);
-                        bulk_commit();
-                    }
-                }
-            } else {
-                int target = -1;
-                float lse = 0.0f, share = 0.0f;
-                const float *extra = nullptr;
-                if (OP == kSoftmax && row < m) {
-                    target = static_cast<int>(g.target[row] - g.row0) - col0;
-                    lse = g.lse[row] * kLog2e;
-                    share = g.share[row];
-                }
-                if (OP == kDw && row < m) {
-                    const int at = g.first[g.row0 + row];
-                    if (at >= 0) extra = g.extra + at * g.ld_extra + col0;
-                }
-#pragma unroll 1
-                for (int c = 0; c < kHalfTile; c += 64) {
-                    uint32_t packed[32];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float v[32];
-                        load(c + 32 * h, v);
-                        if (OP == kSoftmax) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                v[e] = exp2_fast(fmaf(v[e], kLog2e, -lse)) * share;
-                                if (c + 32 * h + e == target || row >= m) v[e] = 0.0f;
-                            }
-                        } else if (extra) {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                if (col0 + c + 32 * h + 4 * q >= g.n) break;
-                                const float4 more = *reinterpret_cast<const float4 *>(extra + c + 32 * h + 4 * q);
-                                v[4 * q] += more.x, v[4 * q + 1] += more.y, v[4 * q + 2] += more.z, v[4 * q + 3] += more.w;
-                            }
+                            for (int e = 0; e < 8; ++e) z[c + e] += v[e];
                         }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) packed[16 * h + e] = pack2(v[2 * e], v[2 * e + 1]);
                     }
-                    if (lane == 0) bulk_wait_read();
-                    __syncwarp();
+                    arrive();
+                }
+                if (waiter.dead) break;
+                if (col0 >= g.n) continue;
+                int mine = -1;  // the target's column among these
+                if (row < m) {
+                    const int64_t id = info.id - g.row0 - col0;
+                    if (id >= 0 && id < min(kUnit, g.n - col0)) mine = static_cast<int>(id);
+                }
+                float top = -INFINITY, sum = 0.0f;
+                if (col0 + kUnit > g.n) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        store16(staging + swz(lane, q),
-                                make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2], packed[4 * q + 3]));
-                    if (OP == kSoftmax || g.boxes) {
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0 && col0 + c < g.n && row0 < g.m) {
-                            store_box(&maps.c, col0 + c, row0, staging);
-                            bulk_commit();
+                    for (int e = 0; e < kUnit; ++e)
+                        if (col0 + e >= g.n) z[e] = -INFINITY;
+                }
+                if (mine >= 0) {
+#pragma unroll
+                    for (int e = 0; e < kUnit; ++e)
+                        if (e == mine) g.mine[row] = z[e];
+                }
+                join_columns(z, top, sum);
+                if (row < m) g.part[static_cast<int64_t>(col0 / kUnit) * m + row] = make_float2(top, sum);
+            } else {
+                const bool some = w.k1 > w.k0;
+                if (some) {
+                    wait(&done[t & 1], (t / 2) & 1);
+                    tc_after();
+                }
+                if (waiter.dead) break;
+                const uint32_t sums = lanes + (t & 1) * kTile;
+                const int target = static_cast<int>(info.target - g.row0);
+                const float lse = info.lse * kLog2e, share = info.share;
+                const float *extra = nullptr;
+                if (OP == kDw && info.target >= 0) extra = g.extra + info.target * g.ld_extra;
+#pragma unroll 1
+                for (int u = group; u < kTile / kUnit; u += H::kGroups) {
+                    const int col0 = w.tn * kTile + u * kUnit;
+                    const bool last = u + H::kGroups >= kTile / kUnit;
+                    if constexpr (OP == kDx) {
+#pragma unroll 1
+                        for (int c = 0; c < kUnit; c += 32) {
+                            float v[32];
+                            if (some) {
+                                tmem_load(sums + u * kUnit + c, v);
+                                if (last && c == kUnit - 32) arrive();
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                            }
+                            if (lane == 0) bulk_wait_read();  // the last box has left
+                            __syncwarp();
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                store16(staging + swz(lane, q),
+                                        make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                                   __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0 && col0 + c < g.n && row0 < m) {
+                                store_box(&maps.c, col0 + c, row0, w.split, staging, g.add);
+                                bulk_commit();
+                            }
                         }
                     } else {
-                        __syncwarp();
-                        for (int r = 0; r < 32 && row0 + r < m; ++r) {
-                            __nv_bfloat16 *to = g.out + (row0 + r) * g.ld_out + col0 + c;
+                        uint32_t packed[32];
+                        float4 more_of[OP == kDw ? kUnit / 4 : 1];
+                        if (OP == kDw && extra) {
 #pragma unroll
-                            for (int e = lane; e < 64; e += 32) {
-                                uint16_t x;
-                                asm volatile("ld.shared.u16 %0, [%1];"
-                                             : "=h"(x)
-                                             : "r"(staging + swz(r, e / 8) + (e & 7) * 2)
-                                             : "memory");
-                                if (col0 + c + e < g.n) to[e] = __ushort_as_bfloat16(x);
-                            }
+                            for (int q = 0; q < kUnit / 4; ++q)
+                                if (col0 + 4 * q < g.n) more_of[q] = *reinterpret_cast<const float4 *>(extra + col0 + 4 * q);
                         }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float v[32];
+                            if (some) {
+                                tmem_load(sums + u * kUnit + 32 * h, v);
+                                if (last && h == 1) arrive();
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                            }
+                            if (OP == kSoftmax) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = exp2_fast(fmaf(v[e], kLog2e, -lse)) * share;
+                                const int at = target - col0 - 32 * h;
+                                if (row >= m || (at >= 0 && at < 32)) {
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        if (e == at || row >= m) v[e] = 0.0f;
+                                }
+                            } else if (extra) {
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) {
+                                    if (col0 + 32 * h + 4 * q >= g.n) break;
+                                    const float4 add = more_of[OP == kDw ? 8 * h + q : 0];
+                                    v[4 * q] += add.x, v[4 * q + 1] += add.y, v[4 * q + 2] += add.z, v[4 * q + 3] += add.w;
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) packed[16 * h + e] = pack2(v[2 * e], v[2 * e + 1]);
+                        }
+                        if (lane == 0) bulk_wait_read();
                         __syncwarp();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            store16(staging + swz(lane, q),
+                                    make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2], packed[4 * q + 3]));
+                        if (OP == kSoftmax || g.boxes) {
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0 && row0 < g.m && col0 < g.n) {
+                                store_box(&maps.c, col0, row0, staging);
+                                bulk_commit();
+                            }
+                        } else {
+                            __syncwarp();
+                            for (int r = 0; r < 32 && row0 + r < m; ++r) {
+                                __nv_bfloat16 *to = g.out + (row0 + r) * g.ld_out + col0;
+#pragma unroll
+                                for (int e = lane; e < kUnit; e += 32) {
+                                    uint16_t x;
+                                    asm volatile("ld.shared.u16 %0, [%1];"
+                                                 : "=h"(x)
+                                                 : "r"(staging + swz(r, e / 8) + (e & 7) * 2)
+                                                 : "memory");
+                                    if (col0 + e < g.n) to[e] = __ushort_as_bfloat16(x);
+                                }
+                            }
+                            __syncwarp();
+                        }
                     }
                 }
+                if (some) ++t;
             }
-            if (some) ++t;
         }
         if (lane == 0) bulk_wait_all();
     }
@@ -523,6 +647,7 @@ __global__ void __launch_bounds__(1024) k_loss_merge(const __grid_constant__ Mer
     const int lane = threadIdx.x & 31, group = threadIdx.x / 32;
     const int64_t token = static_cast<int64_t>(blockIdx.x) * kMergeTokens + lane;
     pdl_wait();
+    pdl_launch_dependents();
     float m = -INFINITY, s = 0.0f;
     if (token < g.tokens) {
 #pragma unroll 4
@@ -597,6 +722,7 @@ template <bool AL>
 __global__ void __launch_bounds__(kRowThreads) k_loss_pack(const __grid_constant__ PackArgs g)
 {
     pdl_wait();
+    pdl_launch_dependents();
     const int64_t i = blockIdx.x;
     const int slab = blockIdx.y;
     const int count = g.count ? *g.count : g.rows;
@@ -625,6 +751,7 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_finish(const __grid_consta
 {
     using P = RowPiece<__nv_bfloat16, AL>;
     pdl_wait();
+    pdl_launch_dependents();
     const int64_t i = blockIdx.x, token = g.order[i];
     const int slab = blockIdx.y;
     Piece<__nv_bfloat16, AL> p;
@@ -637,21 +764,15 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_finish(const __grid_consta
     } else if (i < *g.count) {
         const float f = g.coef[i];
         p.load(g.w + (g.gathered ? i : static_cast<int64_t>(g.key[i])) * g.ld_w, slab, g.cols);
-        for (int s = 0; s < g.splits; ++s) {
+        const int parts = g.splits > 1 ? parts_of((*g.count + kTile - 1) / kTile * ((g.cols + kTile - 1) / kTile), g.depth,
+                                                  g.splits, g.pairs)
+                                       : 1;
+        for (int s = 0; s < parts; ++s) {
             const float *part = g.part + (s * g.tokens + i) * g.ld_part;
-            if (AL) {
-                const int c = P::col(slab, 0);
-                if (c < g.cols) {
-                    const float4 a = *reinterpret_cast<const float4 *>(part + c);
-                    const float4 b = *reinterpret_cast<const float4 *>(part + c + 4);
-                    acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
-                    acc[P::kVec - 4] += b.x, acc[P::kVec - 3] += b.y, acc[P::kVec - 2] += b.z, acc[P::kVec - 1] += b.w;
-                }
-            } else {
+            float v[P::kVec];
+            FloatPiece<__nv_bfloat16, AL>::load(v, part, slab, g.cols);
 #pragma unroll
-                for (int e = 0; e < P::kVec; ++e)
-                    if (P::col(slab, e) < g.cols) acc[e] += part[P::col(slab, e)];
-            }
+            for (int e = 0; e < P::kVec; ++e) acc[e] += v[e];
         }
 #pragma unroll
         for (int e = 0; e < P::kVec; ++e) acc[e] = fmaf(f, to_float(p.v[e]), acc[e]);
@@ -678,9 +799,9 @@ cudaError_t pairs_at_once(int *pairs)
     if (rc != cudaSuccess) return rc;
     const int at = device & 63;
     if (!known[at]) {
-        rc = cudaFuncSetAttribute(dev::k_product<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dev::kProductBytes);
+        rc = cudaFuncSetAttribute(dev::k_product<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dev::Shape<OP>::kBytes);
         if (rc != cudaSuccess) return rc;
-        const int n = static_cast<int>(clusters_at_once(dev::k_product<OP>, dev::kProductThreads, dev::kProductBytes, 2));
+        const int n = static_cast<int>(clusters_at_once(dev::k_product<OP>, dev::Shape<OP>::kThreads, dev::Shape<OP>::kBytes, 2));
         if (n <= 0) return cudaErrorInvalidConfiguration;
         known[at] = n;
     }
@@ -698,8 +819,11 @@ cudaError_t product(const ProductArgs &g, const ProductMaps &maps, cudaStream_t 
                           g.splits;
     if (items == 0) return cudaSuccess;
     return launch<true>(dev::k_product<OP>, dim3(2 * static_cast<uint32_t>(std::min<int64_t>(items, pairs))),
-                        dev::kProductThreads, dev::kProductBytes, 2, s, g, maps);
+                        dev::Shape<OP>::kThreads, dev::Shape<OP>::kBytes, 2, s, g, maps);
 }
+
+// Rows of A's boxes.  Of few tokens no more is fetched than there is (rows behind them reach only themselves).
+uint32_t a_rows(uint64_t tokens) { return tokens <= 8 ? 8 : tokens <= 32 ? 32 : dev::kHalfTile; }
 
 cudaError_t pack(const PackArgs &g, bool aligned, cudaStream_t s)
 {
@@ -717,11 +841,12 @@ constexpr int64_t kMergeChunk = 32768;        // tokens of one product of the fo
 
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
-// Parts of the depth of dx's product, so that few tokens still give every pair work.
+// Parts of the depth of dx's product, at most, so that few tokens still give every pair work (parts_of chooses): within
+// 256 MB.
 int dx_splits(uint64_t tokens, uint64_t cols)
 {
-    const uint64_t tiles = up(tokens, dev::kTile) / dev::kTile * (up(cols, dev::kTile) / dev::kTile);
-    return static_cast<int>(std::max<uint64_t>(1, 76 / std::max<uint64_t>(tiles, 1)));
+    const uint64_t room = (1ull << 28) / std::max<uint64_t>(1, 4 * tokens * up(cols, 4));
+    return static_cast<int>(std::max<uint64_t>(1, std::min<uint64_t>(16, room)));
 }
 
 // Where things are in d_work.  What lives from piece to piece comes first, and
@@ -750,20 +875,21 @@ struct ForwardLayout : Layout {
         sums = take(8 * blocks);
         counts = take(4 * blocks);
         x = take(move ? 2 * tokens * ld : 0);
-        part = take(8 * chunk * (up(piece, dev::kHalfTile) / dev::kHalfTile));
+        part = take(8 * chunk * (up(piece, dev::kUnit) / dev::kUnit));
         w = take(move ? 2 * piece * ld : 0);
     }
 };
 struct BackwardLayout : Layout {
     uint64_t head, key[2], order[2], first, lse, share, coef, x, extra, part, target, g, sums, w;
     uint64_t ld, ld4, piece, ld_g;
-    int splits;
+    int splits, depth;
     BackwardLayout(uint64_t tokens, uint64_t vocab, uint64_t cols, uint64_t rows, bool weight, bool move, bool pieces)
     {
         ld = up(cols, 8);
         ld4 = up(cols, 4);
         splits = dx_splits(tokens, cols);
         uint64_t most = std::max<uint64_t>(256, kGradValues / std::max<uint64_t>(1, up(tokens, 256)) / 256 * 256);
+        depth = static_cast<int>(up(std::min(vocab, most), dev::kDepth) / dev::kDepth);
         if (move) most = std::min(most, std::max<uint64_t>(256, kPackValues / ld / 256 * 256));
         piece = std::min(rows, most);
         ld_g = up(piece, 64);
@@ -782,7 +908,7 @@ struct BackwardLayout : Layout {
         target = take(pieces ? 2 * tokens * ld : 0);
         // g takes the place of the partial sums of the targets' terms, which come before it
         g = take(std::max(2 * tokens * ld_g,
-                          weight ? 8 * (up(tokens, LCT_EMBEDDING_CHUNK) / LCT_EMBEDDING_CHUNK) * cols : 0));
+                          weight ? 8 * (up(tokens, LCT_EMBEDDING_CHUNK(tokens)) / LCT_EMBEDDING_CHUNK(tokens)) * cols : 0));
         w = take(move ? 2 * piece * ld : 0);
     }
 };
@@ -887,10 +1013,6 @@ extern "C" lct_status lct_loss_forward(const lct_ids *targets, const uint16_t *d
         for (uint64_t t0 = 0; t0 < t; t0 += l.chunk) {
             const uint64_t tn = std::min(l.chunk, t - t0);
             const void *ids = static_cast<const char *>(targets->d_ids) + t0 * id_size;
-            ProductMaps maps{};
-            if (!box_map(&maps.a, xp + t0 * ldx, cols, tn, ldx, 0, dev::kHalfTile) ||
-                !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kHalfTile))
-                return LCT_ERR_CUDA;
             ProductArgs g{};
             g.m = static_cast<int32_t>(tn);
             g.n = static_cast<int32_t>(n);
@@ -903,7 +1025,11 @@ extern "C" lct_status lct_loss_forward(const lct_ids *targets, const uint16_t *d
             g.row0 = static_cast<int64_t>(first + r0);
             g.part = at<float2>(d_work, l.part);
             g.mine = at<float>(d_work, l.mine) + t0;
-            if (product<kLogits>(g, maps, s) != cudaSuccess) return LCT_ERR_CUDA;
+            ProductMaps maps{};
+            g.a_rows = a_rows(tn);
+            if (!box_map(&maps.a, xp + t0 * ldx, cols, tn, ldx, 0, g.a_rows) ||
+                !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kHalfTile) || product<kLogits>(g, maps, s) != cudaSuccess)
+                return LCT_ERR_CUDA;
             MergeArgs m{};
             m.part = g.part;
             m.state = at<float2>(d_work, l.state) + t0;
@@ -919,7 +1045,7 @@ extern "C" lct_status lct_loss_forward(const lct_ids *targets, const uint16_t *d
             m.counter = g.status + 1;
             m.tokens = static_cast<int64_t>(tn);
             m.vocab = static_cast<int64_t>(targets->vocab);
-            m.slots = static_cast<int32_t>(up(n, dev::kHalfTile) / dev::kHalfTile);
+            m.slots = static_cast<int32_t>(up(n, dev::kUnit) / dev::kUnit);
             m.blocks = static_cast<int32_t>(up(t, dev::kMergeTokens) / dev::kMergeTokens);
             m.block0 = static_cast<int32_t>(t0 / dev::kMergeTokens);
             m.begins = begins && r0 == 0;
@@ -980,7 +1106,15 @@ extern "C" lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *
             o.key[i] = at<int32_t>(d_work, l.key[i]);
             o.order[i] = at<int32_t>(d_work, l.order[i]);
         }
-        o.first = d_dw ? at<int32_t>(d_work, l.first) : nullptr;
+        int32_t *sums = at<int32_t>(d_work, l.first);
+        if (d_dw) {  // no row of the vocabulary has a sum yet
+            const int64_t all = static_cast<int64_t>(4 * v);
+            o.fill.out = sums;
+            o.fill.value = 0xFFFFFFFFu;
+            o.fill.bytes = o.fill.ld_out = 4096;
+            o.fill.rows = o.fill.early = (all + 4095) / 4096;
+            o.fill.last = all - (o.fill.rows - 1) * 4096;
+        }
         o.count = count;
         o.clear = status;
         o.tokens = tokens;
@@ -1009,7 +1143,7 @@ extern "C" lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *
             e.src = xp;
             e.ld_src = ld;
             e.key = key;
-            e.first = o.first;
+            e.first = sums;
             e.count = count;
             e.coef = p.coef_out;
             e.out = at<float>(d_work, l.extra);
@@ -1018,9 +1152,8 @@ extern "C" lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *
             e.scale = 1.0f;
             e.cols = k;
             e.tokens = tokens;
-            e.vocab = static_cast<int32_t>(v);
             e.compact = true;
-            if (launch_segments(e, false, cols % 8 == 0, false, s) != cudaSuccess) return LCT_ERR_CUDA;
+            if (launch_segments(e, false, cols % 8 == 0, s) != cudaSuccess) return LCT_ERR_CUDA;
         }
     }
     if (pieces) {  // the targets' rows, as their pieces come
@@ -1039,6 +1172,8 @@ extern "C" lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *
         if (launch_lookup(u, false, matrix_al(w) && cols % 8 == 0, s) != cudaSuccess) return LCT_ERR_CUDA;
     }
     const bool dw_boxes = matrix_al(dw);
+    int pairs;
+    if (pairs_at_once<kDx>(&pairs) != cudaSuccess) return LCT_ERR_CUDA;
     for (uint64_t r0 = 0; r0 < rows; r0 += l.piece) {
         const uint64_t n = std::min(l.piece, rows - r0);
         const __nv_bfloat16 *wp = bf16(d_w) + r0 * ld_w;
@@ -1069,14 +1204,17 @@ extern "C" lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *
         g.lse = at<float>(d_work, l.lse);
         g.share = at<float>(d_work, l.share);
         g.boxes = true;
-        if (!box_map(&maps.a, xp, cols, t, l.ld, 0, dev::kHalfTile) || !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kHalfTile) ||
+        g.a_rows = a_rows(t);
+        if (!box_map(&maps.a, xp, cols, t, l.ld, 0, g.a_rows) || !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kHalfTile) ||
             !box_map(&maps.c, gp, n, t, l.ld_g, 0, 32) || product<kSoftmax>(g, maps, s) != cudaSuccess)
             return LCT_ERR_CUDA;
         g.n = k;
         g.k = static_cast<int32_t>(n);
         g.splits = l.splits;
+        g.depth = l.depth;
+        g.pairs = pairs;
         g.add = !(begins && r0 == 0);
-        if (!box_map(&maps.a, gp, n, t, l.ld_g, 0, dev::kHalfTile) || !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kDepth) ||
+        if (!box_map(&maps.a, gp, n, t, l.ld_g, 0, g.a_rows) || !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kDepth) ||
             !box_map32(&maps.c, at<float>(d_work, l.part), cols, t, l.ld4, l.splits) ||
             product<kDx>(g, maps, s) != cudaSuccess)
             return LCT_ERR_CUDA;
@@ -1100,6 +1238,8 @@ extern "C" lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *
     f.ld_part = ld4;
     f.tokens = static_cast<int64_t>(t);
     f.splits = l.splits;
+    f.depth = l.depth;
+    f.pairs = pairs;
     f.key = key;
     f.order = order;
     f.count = count;

@@ -72,6 +72,39 @@ struct Piece {
     }
 };
 
+// A thread's float32 values that go with a piece, in a row of such that begins at a 16-byte boundary where pieces do.
+template <typename T, bool AL>
+struct FloatPiece {
+    using P = RowPiece<T, AL>;
+    static __device__ __forceinline__ void load(float (&v)[P::kVec], const float *row, int slab, int cols)
+    {
+        if constexpr (AL) {
+            const int c = P::col(slab, 0);
+#pragma unroll
+            for (int e = 0; e < P::kVec; e += 4) {
+                const float4 q = c < cols ? *reinterpret_cast<const float4 *>(row + c + e) : make_float4(0, 0, 0, 0);
+                v[e] = q.x, v[e + 1] = q.y, v[e + 2] = q.z, v[e + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < P::kVec; ++e) v[e] = P::col(slab, e) < cols ? row[P::col(slab, e)] : 0.0f;
+        }
+    }
+    static __device__ __forceinline__ void store(const float (&v)[P::kVec], float *row, int slab, int cols)
+    {
+        if constexpr (AL) {
+            const int c = P::col(slab, 0);
+#pragma unroll
+            for (int e = 0; e < P::kVec; e += 4)
+                if (c < cols) *reinterpret_cast<float4 *>(row + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < P::kVec; ++e)
+                if (P::col(slab, e) < cols) row[P::col(slab, e)] = v[e];
+        }
+    }
+};
+
 }  // namespace dev
 
 // Threads of a block and slabs of a row for `vec` values a thread.

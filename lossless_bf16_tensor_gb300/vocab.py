@@ -77,7 +77,7 @@ def cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor):
     [vocabulary, k] in BF16, rows at any stride; targets int32 or int64.  Keeps no
     logits.  Autograd does not see this call (``linear_cross_entropy`` gives
     gradients)."""
-    return calls.cross_entropy(x, weight, targets, False)
+    return calls.cross_entropy(x, weight, targets)
 
 
 def cross_entropy_grads(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, loss: torch.Tensor,
@@ -85,10 +85,16 @@ def cross_entropy_grads(x: torch.Tensor, weight: torch.Tensor, targets: torch.Te
     """(dx, dw): the gradients of ``cross_entropy``'s loss for dloss, float32, a
     value a token or one for all.  dw is None without `weight_grad` (a frozen
     projection)."""
-    return calls.cross_entropy_grads(x, weight, targets, loss, lse, dloss, None, bool(weight_grad))
+    return calls.cross_entropy_grads(x, weight, targets, loss, lse, dloss, bool(weight_grad))
 
 
 _REDUCTIONS = ("mean", "sum", "none")
+
+
+def _reduction(name):
+    if name not in _REDUCTIONS:
+        raise ValueError("reduction must be one of %s" % (_REDUCTIONS,))
+    return _REDUCTIONS.index(name)
 
 
 def _reduced(reduction, loss, total):
@@ -101,25 +107,6 @@ def _upstream(reduction, dy, total):
     return dy, total[2:] if reduction == "mean" else None
 
 
-class _LinearCrossEntropy(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, weight, targets, reduction):
-        xr = _rows(x, weight.shape[1])
-        loss, lse, total = calls.cross_entropy(xr, weight, targets, True)
-        ctx.save_for_backward(xr, weight, targets, loss, lse, total)
-        ctx.rest = (reduction, x.shape)
-        return _reduced(reduction, loss, total).clone()
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dy):
-        x, weight, targets, loss, lse, total = ctx.saved_tensors
-        reduction, shape = ctx.rest
-        dloss, scale = _upstream(reduction, dy, total)
-        dx, dw = calls.cross_entropy_grads(x, weight, targets, loss, lse, dloss, scale, ctx.needs_input_grad[1])
-        return dx.view(shape) if ctx.needs_input_grad[0] else None, dw, None, None
-
-
 def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                          reduction: str = "mean") -> torch.Tensor:
     """The cross entropy of the projection x W^T against targets, float32: its mean
@@ -127,12 +114,7 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.T
     (reduction "none") each token's.  x [..., k] and weight [vocabulary, k] in
     BF16, at any strides.  Differentiable (once) in x and weight; neither pass
     keeps logits."""
-    if reduction not in _REDUCTIONS:
-        raise ValueError("reduction must be one of %s" % (_REDUCTIONS,))
-    targets = targets.contiguous()
-    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad):
-        return _LinearCrossEntropy.apply(x, weight, targets, reduction)
-    return _reduced(reduction, *calls.cross_entropy(_rows(x, weight.shape[1]), weight, targets, True)[::2])
+    return calls.linear_cross_entropy(x, weight, targets.contiguous(), _reduction(reduction))
 
 
 # ------------------------------------------------------ compressed matrices
@@ -228,8 +210,7 @@ def compressed_cross_entropy(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_c
     decoded a piece at a time (and again in backward): neither the dense weight
     nor the logits are ever there.  Differentiable (once) in x; the weight is
     frozen (``compressed_cross_entropy_grads`` gives its gradient)."""
-    if reduction not in _REDUCTIONS:
-        raise ValueError("reduction must be one of %s" % (_REDUCTIONS,))
+    _reduction(reduction)
     targets = targets.contiguous()
     if torch.is_grad_enabled() and x.requires_grad:
         return _CompressedCrossEntropy.apply(x, targets, w, cb, rows, cols, reduction, tile_blocks)

@@ -196,7 +196,9 @@ def within(got, bound, what):
 
 
 LOSS_CASES = [(1, 1, 1), (1, 2, 8), (1, 5000, 64), (2, 255, 100), (127, 129, 63), (128, 128, 64), (129, 257, 72), (255, 300, 1001),
-              (256, 256, 128), (257, 1000, 200), (300, 70_000, 40), (1000, 513, 2056), (1500, 4000, 96), (33, 3, 4096)]
+              (256, 256, 128), (257, 1000, 200), (300, 70_000, 40), (1000, 513, 2056), (1500, 4000, 96), (33, 3, 4096),
+              # few tokens, whose boxes are low
+              (8, 1000, 512), (9, 333, 264), (16, 5000, 1024), (32, 700, 2048), (3, 40, 8192), (17, 1024, 8), (31, 15, 64), (1, 16, 4096)]
 
 
 @pytest.mark.parametrize("t,v,k", LOSS_CASES)
