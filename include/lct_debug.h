@@ -45,6 +45,22 @@ lct_status lct_debug_adapter_backward_timeout(const lct_adapters *bank, const lc
                                               uint16_t *d_dx_out, uint64_t ld_dx_out, uint16_t *d_da, uint16_t *d_db,
                                               void *d_work, void *stream);
 
+/* lct_loss_forward and lct_loss_backward with kernels whose product warps do
+ * nothing: every wait for a product runs out, after about a second in each
+ * kernel.  Losses (the backward pass: dx) are NaN and d_work's first word is
+ * LCT_ERR_TIMEOUT; the kernels return normally and the CUDA context stays usable.
+ * Errors as for those. */
+lct_status lct_debug_loss_forward_timeout(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,
+                                          const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows,
+                                          float *d_loss, float *d_lse, float *d_total, void *d_work,
+                                          uint64_t work_bytes, void *stream);
+lct_status lct_debug_loss_backward_timeout(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,
+                                           const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows,
+                                           const float *d_loss, const float *d_lse, const float *d_dloss,
+                                           uint64_t dloss_stride, const float *d_scale, uint16_t *d_dx, uint64_t ld_dx,
+                                           uint16_t *d_dw, uint64_t ld_dw, void *d_work, uint64_t work_bytes,
+                                           void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 
 #include "../../include/lct.h"
+#include "../../include/lct_debug.h"
 #include "codec_dev.cuh"
 #include "internal.h"
 #include "rows_dev.cuh"
@@ -60,6 +61,7 @@ struct ProductArgs {
     __nv_bfloat16 *out;     // kDw, rows at any address
     int64_t ld_out;
     bool boxes;             // the result is written by boxes (maps.c)
+    bool stalled;           // a test: no products are made, so that waits run out
 };
 struct ProductMaps {
     CUtensorMap a, b, c;
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
         const uint64_t a0 = operand(base, kAcrossA ? kOperand / 2 : 0);
         const uint64_t b0 = operand(base + kOperand, kAcrossB ? kOperand / 2 : 0);
         int i = 0, t = 0;
-        while (items.next(w)) {
+        while (!g.stalled && items.next(w)) {
             int left = 0;  // steps until these sums are done
             uint32_t sums = tmem;
             bool add = false;
@@ -948,9 +950,11 @@ extern "C" uint64_t lct_loss_work_bytes(uint64_t tokens, uint64_t vocab, uint64_
     return ForwardLayout(tokens, cols, rows, move).bytes;
 }
 
-extern "C" lct_status lct_loss_forward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,
-                                       const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows, float *d_loss,
-                                       float *d_lse, float *d_total, void *d_work, uint64_t work_bytes, void *stream)
+namespace {
+
+lct_status forward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols, const uint16_t *d_w,
+                   uint64_t ld_w, uint64_t first, uint64_t rows, float *d_loss, float *d_lse, float *d_total, void *d_work,
+                   uint64_t work_bytes, bool stalled, void *stream)
 {
     Matrix x, w;
     const lct_status ok = check_batch(targets, d_x, ld_x, cols, d_w, ld_w, first, rows, d_work, &x, &w);
@@ -1018,6 +1022,7 @@ extern "C" lct_status lct_loss_forward(const lct_ids *targets, const uint16_t *d
             g.n = static_cast<int32_t>(n);
             g.k = static_cast<int32_t>(cols);
             g.status = at<int32_t>(d_work, l.head);
+            g.stalled = stalled;
             g.splits = 1;
             g.begins = begins && r0 == 0 && t0 == 0;
             g.ids = ids;
@@ -1058,11 +1063,10 @@ extern "C" lct_status lct_loss_forward(const lct_ids *targets, const uint16_t *d
     return LCT_OK;
 }
 
-extern "C" lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,
-                                        const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows,
-                                        const float *d_loss, const float *d_lse, const float *d_dloss, uint64_t dloss_stride,
-                                        const float *d_scale, uint16_t *d_dx, uint64_t ld_dx, uint16_t *d_dw, uint64_t ld_dw,
-                                        void *d_work, uint64_t work_bytes, void *stream)
+lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols, const uint16_t *d_w,
+                    uint64_t ld_w, uint64_t first, uint64_t rows, const float *d_loss, const float *d_lse,
+                    const float *d_dloss, uint64_t dloss_stride, const float *d_scale, uint16_t *d_dx, uint64_t ld_dx,
+                    uint16_t *d_dw, uint64_t ld_dw, void *d_work, uint64_t work_bytes, bool stalled, void *stream)
 {
     Matrix x, w;
     const lct_status ok = check_batch(targets, d_x, ld_x, cols, d_w, ld_w, first, rows, d_work, &x, &w);
@@ -1198,6 +1202,7 @@ extern "C" lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *
         g.k = k;
         g.count = count;
         g.status = status;
+        g.stalled = stalled;
         g.splits = 1;
         g.row0 = static_cast<int64_t>(first + r0);
         g.target = key;
@@ -1260,3 +1265,28 @@ extern "C" lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *
                               : launch<true>(dev::k_loss_finish<false>, dim3(tokens, slabs), threads, 0, 1, s, f);
     return rc == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
 }
+
+}  // namespace
+
+#define LOSS_FORWARD(name, stalled)                                                                                     \
+    extern "C" lct_status name(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,               \
+                               const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows, float *d_loss,        \
+                               float *d_lse, float *d_total, void *d_work, uint64_t work_bytes, void *stream)           \
+    {                                                                                                                   \
+        return forward(targets, d_x, ld_x, cols, d_w, ld_w, first, rows, d_loss, d_lse, d_total, d_work, work_bytes,    \
+                       stalled, stream);                                                                                \
+    }
+#define LOSS_BACKWARD(name, stalled)                                                                                    \
+    extern "C" lct_status name(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,               \
+                               const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows, const float *d_loss,  \
+                               const float *d_lse, const float *d_dloss, uint64_t dloss_stride, const float *d_scale,   \
+                               uint16_t *d_dx, uint64_t ld_dx, uint16_t *d_dw, uint64_t ld_dw, void *d_work,            \
+                               uint64_t work_bytes, void *stream)                                                       \
+    {                                                                                                                   \
+        return backward(targets, d_x, ld_x, cols, d_w, ld_w, first, rows, d_loss, d_lse, d_dloss, dloss_stride, d_scale, \
+                        d_dx, ld_dx, d_dw, ld_dw, d_work, work_bytes, stalled, stream);                                 \
+    }
+LOSS_FORWARD(lct_loss_forward, false)
+LOSS_BACKWARD(lct_loss_backward, false)
+LOSS_FORWARD(lct_debug_loss_forward_timeout, true)
+LOSS_BACKWARD(lct_debug_loss_backward_timeout, true)
