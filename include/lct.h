@@ -480,10 +480,12 @@ lct_status lct_adapter_backward(const lct_adapters *bank, const lct_token_plan *
 #define LCT_VOCAB_MAX_COLS (1 << 16)
 #define LCT_VOCAB_MAX_TOKENS (1 << 24)
 #define LCT_EMBEDDING_CHUNK(tokens) ((tokens) <= 8192 ? 8 : 32) /* sorted tokens that one block adds */
+#define LCT_EMBEDDING_PART(cols) (((uint64_t)(cols) + 14) / 8 * 8) /* values of a partial sum */
 /* scratch of lct_embedding_grad */
 #define LCT_EMBEDDING_WORK_BYTES(tokens, cols)                                                             \
     (16ull + 64ull * (((uint64_t)(tokens) + 3) / 4) +                                                      \
-     8ull * (((uint64_t)(tokens) + LCT_EMBEDDING_CHUNK(tokens) - 1) / LCT_EMBEDDING_CHUNK(tokens)) * (uint64_t)(cols))
+     8ull * (((uint64_t)(tokens) + LCT_EMBEDDING_CHUNK(tokens) - 1) / LCT_EMBEDDING_CHUNK(tokens)) *                  \
+         LCT_EMBEDDING_PART(cols))
 
 /* A batch's ids: a row of the vocabulary's matrix for each token.  A negative
  * id is none (padding, a token without a target). */
@@ -498,8 +500,9 @@ typedef struct {
  * no counterpart.)  d_table holds rows `first` .. first + rows of the matrix
  * [vocab, cols], ld_table values apart, of `dtype`, which is out's too; tokens
  * of other rows are left as they are, so that a compressed matrix can be decoded
- * and looked up a piece at a time.  Rows at 16-byte boundaries are the fast
- * case.  Errors: LCT_ERR_INVALID_ARG (NULL or misaligned pointers, strides
+ * and looked up a piece at a time.  Rows of whole 16-byte pieces at 16-byte
+ * boundaries are the fast case; of others whole aligned pieces are fetched, what
+ * lies before a row's first value and behind its last one among it.  Errors: LCT_ERR_INVALID_ARG (NULL or misaligned pointers, strides
  * below cols, rows outside the vocabulary, out over another operand),
  * LCT_ERR_UNSUPPORTED (another dtype, a size above the limits), LCT_ERR_CUDA. */
 lct_status lct_embedding(const lct_ids *ids, const void *d_table, uint64_t ld_table, int32_t dtype, uint64_t first,

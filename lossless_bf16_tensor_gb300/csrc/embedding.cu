@@ -26,46 +26,51 @@ namespace dev {
 
 // --------------------------------------------------------- sorting the ids
 
-// A row of a value, or of a base: a warp's, in 16-byte pieces between its ends.
-__device__ __forceinline__ void fill_row(const FillArgs &f, int64_t r)
+// A row of a value, or of a base, in 16-byte pieces of the row between its ends,
+// by `lanes` threads of which this is the lane-th.
+__device__ __forceinline__ void fill_row(const FillArgs &f, int64_t r, int lane, int lanes)
 {
-    const int lane = threadIdx.x & 31;
     uint16_t *row = reinterpret_cast<uint16_t *>(static_cast<char *>(f.out) + r * f.ld_out);
     const uint16_t *base =
         f.base ? reinterpret_cast<const uint16_t *>(static_cast<const char *>(f.base) + r * f.ld_base) : nullptr;
     const int n = static_cast<int>((r == f.rows - 1 ? f.last : f.bytes) / 2);
     const uint16_t value = static_cast<uint16_t>(f.value);
-    int a = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 2, pieces = 0;
-    if (!base || ((reinterpret_cast<uintptr_t>(base) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0)
-        pieces = max(0, n - a) / 8;
-    if (pieces == 0) a = 0;
-    for (int c = lane; c < a; c += 32) row[c] = base ? base[c] : value;
+    const int a = min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 2), pieces = (n - a) / 8;
+    for (int c = lane; c < a; c += lanes) row[c] = base ? base[c] : value;
     uint4 *q = reinterpret_cast<uint4 *>(row + a);
     if (base) {
-        const uint4 *b = reinterpret_cast<const uint4 *>(base + a);
-        for (int c0 = lane; c0 < pieces; c0 += 32 * 8) {
+        for (int c0 = lane; c0 < pieces; c0 += lanes * 8) {
             uint4 v[8];  // asked for together: nobody tells the compiler that the rows are apart
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (c0 + 32 * i < pieces) v[i] = b[c0 + 32 * i];
+                if (c0 + lanes * i < pieces) v[i] = load_any(base + a + 8 * (c0 + lanes * i), 16);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (c0 + 32 * i < pieces) q[c0 + 32 * i] = v[i];
+                if (c0 + lanes * i < pieces) q[c0 + lanes * i] = v[i];
         }
     } else {
         const uint4 v = make_uint4(f.value, f.value, f.value, f.value);
 #pragma unroll 4
-        for (int c = lane; c < pieces; c += 32) q[c] = v;
+        for (int c = lane; c < pieces; c += lanes) q[c] = v;
     }
-    for (int c = a + 8 * pieces + lane; c < n; c += 32) row[c] = base ? base[c] : value;
+    for (int c = a + 8 * pieces + lane; c < n; c += lanes) row[c] = base ? base[c] : value;
+}
+// Threads of a row: a warp, or as many as a short row has pieces.
+__device__ __forceinline__ int fill_lanes(const FillArgs &f)
+{
+    int lanes = 32;
+    while (lanes > 1 && lanes * 16 >= 2 * f.bytes) lanes /= 2;
+    return lanes;
 }
 
 // While the ids are being sorted, the other blocks of the same launch write what
 // needs no order: the last rows, with or without tokens (those with tokens are
 // replaced later), as many as that time allows.
-__device__ __forceinline__ void fill(const FillArgs &f, int64_t warp, int64_t warps)
+__device__ __forceinline__ void fill(const FillArgs &f, int64_t block, int64_t blocks)
 {
-    for (int64_t r = f.rows - f.early + warp; r < f.rows; r += warps) fill_row(f, r);
+    const int lanes = fill_lanes(f), rows = blockDim.x / lanes;  // at a time
+    for (int64_t r = f.rows - f.early + block * rows + threadIdx.x / lanes; r < f.rows; r += blocks * rows)
+        fill_row(f, r, threadIdx.x % lanes, lanes);
 }
 
 // Ids outside 0 .. vocab - 1 become `vocab` and end up behind the others.
@@ -76,27 +81,28 @@ __device__ __forceinline__ int key_of(const SortArgs &g, int64_t i)
 }
 
 // Batches up to 8192 ids: an id's place is the number of smaller ones and of
-// equal ones before it, and 67 million comparisons, 64 ids a block, are done
-// before a cluster has met once.
-constexpr int kRankThreads = 256, kRankIds = 64, kRankMost = 8192;
+// equal ones before it, and 67 million comparisons, IDS ids a block, are done
+// before a cluster has met twice (8192 ids of a narrow table: 8 us, 18 by the sort).
+constexpr int kRankThreads = 1024, kRankMost = 8192;
+template <int IDS>
 __global__ void __launch_bounds__(kRankThreads) k_rank_ids(const __grid_constant__ SortArgs g)
 {
+    constexpr int kParts = kRankThreads / IDS;  // of the ids that each of the block's is compared with
     extern __shared__ int4 keys4[];
-    __shared__ int found[kRankThreads / kRankIds][kRankIds];
+    __shared__ int found[kParts][IDS];
     __shared__ int there;
     int *keys = reinterpret_cast<int *>(keys4);
     pdl_wait();
     pdl_launch_dependents();
-    const int blocks = (g.tokens + kRankIds - 1) / kRankIds;
+    const int blocks = (g.tokens + IDS - 1) / IDS;
     if (static_cast<int>(blockIdx.x) >= blocks) {
-        const int warps = kRankThreads / 32;
-        fill(g.fill, (blockIdx.x - blocks) * static_cast<int64_t>(warps) + threadIdx.x / 32,
-             static_cast<int64_t>(gridDim.x - blocks) * warps);
+        fill(g.fill, blockIdx.x - blocks, gridDim.x - blocks);
         return;
     }
     if (g.clear && blockIdx.x == 0 && threadIdx.x < 2) g.clear[threadIdx.x] = 0;
     if (threadIdx.x == 0) there = 0;
-    const int padded = (g.tokens + 15) & ~15;
+    constexpr int kRound = 4 * kParts;
+    const int padded = (g.tokens + kRound - 1) / kRound * kRound;
     int valid = 0;
 #pragma unroll 8
     for (int j = threadIdx.x; j < padded; j += kRankThreads) {
@@ -109,11 +115,11 @@ __global__ void __launch_bounds__(kRankThreads) k_rank_ids(const __grid_constant
         valid = __reduce_add_sync(kFull, valid);
         if ((threadIdx.x & 31) == 0) atomicAdd(&there, valid);
     }
-    const int mine = threadIdx.x % kRankIds, part = threadIdx.x / kRankIds;
-    const int i0 = blockIdx.x * kRankIds, i = i0 + mine;
+    const int mine = threadIdx.x % IDS, part = threadIdx.x / IDS;
+    const int i0 = blockIdx.x * IDS, i = i0 + mine;
     const int key = i < g.tokens ? keys[i] : 0;
-    // a quarter of the ids: those before the block's, those among them, those behind
-    const int quarter = padded / 4, lo = part * quarter, hi = lo + quarter;
+    // a part of the ids: those before the block's, those among them, those behind
+    const int share = padded / kParts, lo = part * share, hi = lo + share;
     auto smaller = [&](int from, int to, int than) {
         int n = 0;
 #pragma unroll 4
@@ -123,12 +129,14 @@ __global__ void __launch_bounds__(kRankThreads) k_rank_ids(const __grid_constant
         }
         return n;
     };
-    int n = smaller(lo, min(hi, i0), key + 1) + smaller(max(lo, i0 + kRankIds), hi, key);
-    for (int j = max(lo, i0); j < min(hi, i0 + kRankIds); ++j) n += keys[j] < key + (j < i);
+    int n = smaller(lo, min(hi, i0), key + 1) + smaller(max(lo, i0 + IDS), hi, key);
+    for (int j = max(lo, i0); j < min(hi, i0 + IDS); ++j) n += keys[j] < key + (j < i);
     found[part][mine] = n;
     __syncthreads();
     if (part == 0 && i < g.tokens) {
-        const int place = n + found[1][mine] + found[2][mine] + found[3][mine];
+        int place = n;
+#pragma unroll
+        for (int p = 1; p < kParts; ++p) place += found[p][mine];
         g.key[0][place] = key;
         g.order[0][place] = i;
     }
@@ -154,8 +162,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_ids(const __grid_constant
     pdl_wait();
     pdl_launch_dependents();
     if (blockIdx.x >= size) {
-        fill(g.fill, static_cast<int64_t>(blockIdx.x - size) * kSortWarps + warp,
-             static_cast<int64_t>(gridDim.x - size) * kSortWarps);
+        fill(g.fill, blockIdx.x - size, gridDim.x - size);
         return;
     }
     if (g.clear && rank == 0 && threadIdx.x < 2) g.clear[threadIdx.x] = 0;
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_ids(const __grid_constant
 template <typename T, bool AL, int ROWS>
 __global__ void __launch_bounds__(kRowThreads) k_embedding(const __grid_constant__ LookupArgs g)
 {
-    const int slab = blockIdx.y;
+    const int piece = piece_of<T>(blockIdx.y);
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * ROWS;
     Piece<T, AL> p[ROWS];
     int64_t id[ROWS];
@@ -257,11 +264,12 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding(const __grid_constant
     for (int r = 0; r < ROWS; ++r) {
         const int64_t at = id[r] - g.row0;
         if (at >= 0 && at < g.rows) {
-            p[r].load(static_cast<const T *>(g.table) + at * g.ld_table, slab, g.cols);
+            const int c = piece - skip_of_row<T, AL>(static_cast<T *>(g.out) + (i0 + r) * g.ld_out);
+            p[r].load(static_cast<const T *>(g.table) + at * g.ld_table, c, g.cols);
         } else {
             const T fill = from_float<T>(id[r] < 0 ? 0.0f : __int_as_float(0x7FC00000));
 #pragma unroll
-            for (int e = 0; e < RowPiece<T, AL>::kVec; ++e) p[r].v[e] = fill;
+            for (int e = 0; e < kVec<T>; ++e) p[r].v[e] = fill;
         }
     }
 #pragma unroll
@@ -271,9 +279,10 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding(const __grid_constant
         if (i0 + r >= g.tokens || (!there && id[r] >= 0 && id[r] < g.vocab)) continue;  // another piece's row
         if (there && g.scale != 1.0f) {
 #pragma unroll
-            for (int e = 0; e < RowPiece<T, AL>::kVec; ++e) p[r].v[e] = from_float<T>(to_float(p[r].v[e]) * g.scale);
+            for (int e = 0; e < kVec<T>; ++e) p[r].v[e] = from_float<T>(to_float(p[r].v[e]) * g.scale);
         }
-        p[r].store(static_cast<T *>(g.out) + (i0 + r) * g.ld_out, slab, g.cols);
+        T *row = static_cast<T *>(g.out) + (i0 + r) * g.ld_out;
+        p[r].store(row, piece - skip_of_row<T, AL>(row), g.cols);
     }
 }
 
@@ -282,30 +291,36 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding(const __grid_constant
 constexpr int kSegTokens = 32;  // of a chunk, at most
 constexpr int kSegAhead = 8;  // rows asked for at a time
 
+// The row that key's sum goes to, and the column of it at which this thread's piece begins.
+template <typename T, bool AL>
+__device__ __forceinline__ int first_col(const SegmentArgs &g, int key, int piece)
+{
+    return g.compact ? piece : piece - skip_of_row<T, AL>(static_cast<T *>(g.out) + key * g.ld_out);
+}
+
 // A finished row: scaled, added to its base, rounded once.  Compact sums
 // (float32, unscaled) go to the row of the id's first token instead.
 template <typename T, bool AL>
-__device__ __forceinline__ void finish_row(const SegmentArgs &g, int key, int first, int slab,
-                                           const float (&acc)[RowPiece<T, AL>::kVec], const Piece<T, AL> &base)
+__device__ __forceinline__ void finish_row(const SegmentArgs &g, int key, int first, int piece, const float (&acc)[kVec<T>],
+                                           const Piece<T, AL> &base)
 {
-    using P = RowPiece<T, AL>;
     if (g.compact) {
-        FloatPiece<T, AL>::store(acc, static_cast<float *>(g.out) + first * g.ld_out, slab, g.cols);
-        if (slab == 0 && threadIdx.x == 0) g.first[key] = first;
+        if (piece < g.cols) store_floats<T>(acc, static_cast<float *>(g.out) + first * g.ld_out, piece);
+        if (piece == 0) g.first[key] = first;
         return;
     }
     Piece<T, AL> p;
 #pragma unroll
-    for (int e = 0; e < P::kVec; ++e)
+    for (int e = 0; e < kVec<T>; ++e)
         p.v[e] = from_float<T>(g.base ? fmaf(g.scale, acc[e], to_float(base.v[e])) : g.scale * acc[e]);
-    p.store(static_cast<T *>(g.out) + key * g.ld_out, slab, g.cols);
+    p.store(static_cast<T *>(g.out) + key * g.ld_out, first_col<T, AL>(g, key, piece), g.cols);
 }
 
-// Partial sums of an id that crosses chunks, [chunk][2][cols]: of one that began
+// Partial sums of an id that crosses chunks, [chunk][2][pieces' values]: of one that began
 // earlier (0), of one that begins here and goes on (1).
 __device__ __forceinline__ float *partial(const SegmentArgs &g, int64_t chunk, int which)
 {
-    return g.part + (chunk * 2 + which) * g.cols;
+    return g.part + (chunk * 2 + which) * LCT_EMBEDDING_PART(g.cols);
 }
 
 // The first of the sorted ids that is not smaller than v, by a warp: 32 of them
@@ -326,8 +341,8 @@ __device__ __forceinline__ int64_t lower_bound(const int32_t *key, int64_t count
     return lo;
 }
 
-// Rows without tokens, of the vocabulary's kFillRows rows that the block has.
-constexpr int kFillRows = 512;
+// Rows without tokens, of the block's (at most kFillRows).
+constexpr int kFillRows = 4096;
 __device__ __forceinline__ void fill_rest(const SegmentArgs &g, int64_t block)
 {
     __shared__ uint32_t have[kFillRows / 32];
@@ -345,9 +360,10 @@ __device__ __forceinline__ void fill_rest(const SegmentArgs &g, int64_t block)
         atomicOr(&have[r / 32], 1u << (r & 31));
     }
     __syncthreads();
-    for (int64_t r = r0 + warp; r < r1; r += warps) {
+    const int lanes = fill_lanes(g.fill), rows = blockDim.x / lanes;
+    for (int64_t r = r0 + threadIdx.x / lanes; r < r1; r += rows) {
         const int at = static_cast<int>(r - r0);
-        if (!(have[at / 32] >> (at & 31) & 1)) fill_row(g.fill, r);
+        if (!(have[at / 32] >> (at & 31) & 1)) fill_row(g.fill, r, threadIdx.x % lanes, lanes);
     }
 }
 
@@ -355,7 +371,6 @@ __device__ __forceinline__ void fill_rest(const SegmentArgs &g, int64_t block)
 template <typename T, bool AL, bool BASE>
 __global__ void __launch_bounds__(kRowThreads) k_segments(const __grid_constant__ SegmentArgs g)
 {
-    using P = RowPiece<T, AL>;
     __shared__ int keys[kSegTokens], tokens[kSegTokens];
     __shared__ float coefs[kSegTokens];
     pdl_wait();
@@ -366,7 +381,8 @@ __global__ void __launch_bounds__(kRowThreads) k_segments(const __grid_constant_
         return;
     }
     const int64_t chunk = blockIdx.x / g.slabs;
-    const int slab = blockIdx.x % g.slabs;
+    const int piece = piece_of<T>(blockIdx.x % g.slabs);
+    const bool used = piece < g.cols + (AL ? 0 : kVec<T> - 1);
     const int64_t i0 = chunk * g.chunk;
     const int n = static_cast<int>(min(static_cast<int64_t>(g.chunk), *g.count - i0));
     if (n <= 0) return;
@@ -378,38 +394,40 @@ __global__ void __launch_bounds__(kRowThreads) k_segments(const __grid_constant_
     __syncthreads();
     const bool goes_on = i0 + n < *g.count && g.key[i0 + n] == keys[n - 1];
     int64_t began = i0 > 0 && g.key[i0 - 1] == keys[0] ? -1 : i0;  // where the id's tokens begin (-1: in an earlier chunk)
-    float acc[P::kVec];
+    float acc[kVec<T>];
 #pragma unroll
-    for (int e = 0; e < P::kVec; ++e) acc[e] = 0.0f;
-    for (int j0 = 0; j0 < n; j0 += kSegAhead) {
-        Piece<T, AL> p[kSegAhead], base[BASE ? kSegAhead : 1];
+    for (int e = 0; e < kVec<T>; ++e) acc[e] = 0.0f;
+    constexpr int kAhead = AL ? kSegAhead : kSegAhead / 2;  // others take two reads
+    for (int j0 = 0; j0 < n; j0 += kAhead) {
+        Piece<T, AL> p[kAhead], base[BASE ? kAhead : 1];
 #pragma unroll
-        for (int j = 0; j < kSegAhead; ++j) {
+        for (int j = 0; j < kAhead; ++j) {
             const int at = j0 + j;
             if (at >= n) continue;
-            p[j].load(static_cast<const T *>(g.src) + tokens[at] * g.ld_src, slab, g.cols);
+            const int c = first_col<T, AL>(g, keys[at], piece);
+            p[j].load(static_cast<const T *>(g.src) + tokens[at] * g.ld_src, c, g.cols);
             // an id's last row: its base is wanted as well
             if (BASE && (at + 1 == n || keys[at + 1] != keys[at]))
-                base[j].load(static_cast<const T *>(g.base) + keys[at] * g.ld_base, slab, g.cols);
+                base[j].load(static_cast<const T *>(g.base) + keys[at] * g.ld_base, c, g.cols);
         }
 #pragma unroll
-        for (int j = 0; j < kSegAhead; ++j) {
+        for (int j = 0; j < kAhead; ++j) {
             const int at = j0 + j;
             if (at >= n) break;
             const float f = coefs[at];
 #pragma unroll
-            for (int e = 0; e < P::kVec; ++e) acc[e] = fmaf(f, to_float(p[j].v[e]), acc[e]);
+            for (int e = 0; e < kVec<T>; ++e) acc[e] = fmaf(f, to_float(p[j].v[e]), acc[e]);
             if (at + 1 < n && keys[at + 1] == keys[at]) continue;
             if (began < 0 || (at == n - 1 && goes_on)) {
-                FloatPiece<T, AL>::store(acc, partial(g, chunk, began < 0 ? 0 : 1), slab, g.cols);
+                if (used) store_floats<T>(acc, partial(g, chunk, began < 0 ? 0 : 1), piece);
                 // where it began, for the kernel that adds the parts
-                if (g.compact && began >= 0 && slab == 0 && threadIdx.x == 0) g.first[keys[at]] = static_cast<int>(began);
+                if (g.compact && began >= 0 && piece == 0) g.first[keys[at]] = static_cast<int>(began);
             } else {
-                finish_row<T, AL>(g, keys[at], static_cast<int>(began), slab, acc, base[BASE ? j : 0]);
+                finish_row<T, AL>(g, keys[at], static_cast<int>(began), piece, acc, base[BASE ? j : 0]);
             }
             began = i0 + at + 1;
 #pragma unroll
-            for (int e = 0; e < P::kVec; ++e) acc[e] = 0.0f;
+            for (int e = 0; e < kVec<T>; ++e) acc[e] = 0.0f;
         }
     }
 }
@@ -418,11 +436,10 @@ __global__ void __launch_bounds__(kRowThreads) k_segments(const __grid_constant_
 template <typename T, bool AL>
 __global__ void __launch_bounds__(kRowThreads) k_segment_ends(const __grid_constant__ SegmentArgs g)
 {
-    using P = RowPiece<T, AL>;
     pdl_wait();
     pdl_launch_dependents();
     const int64_t chunk = blockIdx.x / g.slabs, i0 = chunk * g.chunk, next = i0 + g.chunk, count = *g.count;
-    const int slab = blockIdx.x % g.slabs, lane = threadIdx.x & 31;
+    const int piece = piece_of<T>(blockIdx.x % g.slabs), lane = threadIdx.x & 31;
     if (next >= count) return;
     const int key = g.key[next - 1];
     if (g.key[next] != key || (i0 > 0 && g.key[i0] == key && g.key[i0 - 1] == key)) return;
@@ -436,19 +453,20 @@ __global__ void __launch_bounds__(kRowThreads) k_segment_ends(const __grid_const
             break;
         }
     }
-    float acc[P::kVec];
-    FloatPiece<T, AL>::load(acc, partial(g, chunk, 1), slab, g.cols);
+    float acc[kVec<T>];
+    if (piece >= g.cols + (AL ? 0 : kVec<T> - 1)) return;
+    load_floats<T>(acc, partial(g, chunk, 1), piece);
     Piece<T, AL> base;
-    if (g.base) base.load(static_cast<const T *>(g.base) + key * g.ld_base, slab, g.cols);
+    if (g.base) base.load(static_cast<const T *>(g.base) + key * g.ld_base, first_col<T, AL>(g, key, piece), g.cols);
 #pragma unroll 8
     for (int64_t c = 1; c <= more; ++c) {
-        float v[P::kVec];
-        FloatPiece<T, AL>::load(v, partial(g, chunk + c, 0), slab, g.cols);
+        float v[kVec<T>];
+        load_floats<T>(v, partial(g, chunk + c, 0), piece);
 #pragma unroll
-        for (int e = 0; e < P::kVec; ++e) acc[e] += v[e];
+        for (int e = 0; e < kVec<T>; ++e) acc[e] += v[e];
     }
     const int first = g.compact ? g.first[key] : 0;
-    finish_row<T, AL>(g, key, first, slab, acc, base);
+    finish_row<T, AL>(g, key, first, piece, acc, base);
 }
 
 }  // namespace dev
@@ -467,9 +485,13 @@ cudaError_t launch_sort_ids(SortArgs g, cudaStream_t s)
 {
     const uint32_t tokens = static_cast<uint32_t>(g.tokens);
     if (tokens <= dev::kRankMost) {
-        const uint32_t blocks = (tokens + dev::kRankIds - 1) / dev::kRankIds + fill_blocks(g.fill, 65536, 152 * 6);
-        return blocks ? launch<true>(dev::k_rank_ids, dim3(blocks), dev::kRankThreads, (tokens + 15) / 16 * 64, 1, s, g)
-                      : cudaSuccess;
+        // as few ids a block as there are SMs for
+        const uint32_t ids = tokens <= 4096 ? 32 : 64;
+        const uint32_t blocks = (tokens + ids - 1) / ids + fill_blocks(g.fill, 131072, 152 * 2);
+        const uint32_t smem = (tokens + 127) / 128 * 512;
+        if (!blocks) return cudaSuccess;
+        return ids == 32 ? launch<true>(dev::k_rank_ids<32>, dim3(blocks), dev::kRankThreads, smem, 1, s, g)
+                         : launch<true>(dev::k_rank_ids<64>, dim3(blocks), dev::kRankThreads, smem, 1, s, g);
     }
     int need = 1;
     while (need < 31 && g.vocab >> need) ++need;  // bits of `vocab`, the largest key
@@ -487,7 +509,7 @@ template <typename T, bool AL>
 cudaError_t lookup(const LookupArgs &g, cudaStream_t s)
 {
     uint32_t threads, slabs;
-    row_shape(g.cols, dev::RowPiece<T, AL>::kVec, &threads, &slabs);
+    row_shape(g.cols, dev::kVec<T>, AL, &threads, &slabs);
     if (g.tokens * static_cast<uint64_t>(slabs) <= 152 * 8)
         return launch<true>(dev::k_embedding<T, AL, 1>, dim3(static_cast<uint32_t>(g.tokens), slabs), threads, 0, 1, s, g);
     return launch<true>(dev::k_embedding<T, AL, 4>, dim3(static_cast<uint32_t>((g.tokens + 3) / 4), slabs), threads, 0, 1, s,
@@ -498,7 +520,7 @@ template <typename T, bool AL>
 cudaError_t segments(SegmentArgs g, cudaStream_t s)
 {
     uint32_t threads;
-    row_shape(g.cols, dev::RowPiece<T, AL>::kVec, &threads, &g.slabs);
+    row_shape(g.cols, dev::kVec<T>, AL, &threads, &g.slabs);
     g.chunk = static_cast<int32_t>(LCT_EMBEDDING_CHUNK(static_cast<uint64_t>(g.tokens)));
     g.chunks = (static_cast<uint32_t>(g.tokens) + g.chunk - 1) / g.chunk;
     uint64_t fills = 0;

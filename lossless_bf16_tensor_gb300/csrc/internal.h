@@ -261,7 +261,7 @@ struct SegmentArgs {
     const float *coef;        // [i], or NULL: 1
     const void *base;         // or NULL
     void *out;                // row key[i]; compact: float32 rows, that of the key's first place
-    float *part;              // [chunks][2][cols]
+    float *part;              // [chunks][2][LCT_EMBEDDING_PART]
     int64_t ld_src, ld_base, ld_out;
     float scale;
     FillArgs fill;            // rows without tokens, or none

@@ -228,14 +228,16 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// Parts of dx's depth that give the pairs as much to do as can be: tiles go
-// round in turns, and every part costs about three steps more.
+// Parts of dx's depth that give the pairs as much to do as can be.  In steps of a
+// pair: tiles go round in turns, in each of which a tile's result takes about
+// six, and what every part has to write and k_loss_finish to read takes 0.3 for
+// each tile.
 __device__ __forceinline__ int parts_of(int tiles, int depth, int most, int pairs)
 {
     int best = 1;
     int64_t least = INT64_MAX;
     for (int s = 1; s <= most && s <= max(1, depth / 4); ++s) {
-        const int64_t cost = (static_cast<int64_t>(tiles) * s + pairs - 1) / pairs * ((depth + s - 1) / s + 3);
+        const int64_t cost = 10 * ((static_cast<int64_t>(tiles) * s + pairs - 1) / pairs * ((depth + s - 1) / s + 6)) + 3ll * s * tiles;
         if (cost < least) least = cost, best = s;
     }
     return best;
@@ -720,30 +722,34 @@ __global__ void __launch_bounds__(1024) k_loss_merge(const __grid_constant__ Mer
 // Row i of dst is row order[i] of src (NULL: row i), for the tokens that are
 // there; rows behind them, as far as a step of depth reaches, are zero.  With
 // order, also what the tokens' ends need.
+constexpr int kPackRows = 4;  // a block's, asked for together
 template <bool AL>
 __global__ void __launch_bounds__(kRowThreads) k_loss_pack(const __grid_constant__ PackArgs g)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t i = blockIdx.x;
-    const int slab = blockIdx.y;
+    const int i0 = blockIdx.x * kPackRows, piece = piece_of<__nv_bfloat16>(blockIdx.y);
     const int count = g.count ? *g.count : g.rows;
-    if (i >= count + 63) return;  // (rows behind the last are nobody's, and boxes fill them with zeros)
-    Piece<__nv_bfloat16, AL> p;
-    if (i < count) {
+    const int end = min(g.rows, count + 63);  // (rows behind the last are nobody's, and boxes fill them with zeros)
+    Piece<__nv_bfloat16, AL> p[kPackRows];
+#pragma unroll
+    for (int r = 0; r < kPackRows; ++r) {
+        const int i = i0 + r;
+        p[r].q = make_uint4(0, 0, 0, 0);
+        if (i >= count) continue;
         const int64_t token = g.order ? g.order[i] : i;
-        p.load(g.src + token * g.ld_src, slab, g.cols);
-        if (g.order && slab == 0 && threadIdx.x == 0) {
+        p[r].load(g.src + token * g.ld_src, piece, g.cols);
+        if (g.order && piece == 0) {
             const float c = g.dloss[token * g.dloss_stride] * (g.scale ? *g.scale : 1.0f);
             g.lse_out[i] = g.lse[token];
             g.share_out[i] = c;
             g.coef_out[i] = c * expm1f(-g.loss[token]);
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < RowPiece<__nv_bfloat16, AL>::kVec; ++e) p.v[e] = __float2bfloat16_rn(0.0f);
     }
-    p.store(g.dst + i * g.ld_dst, slab, g.cols);
+#pragma unroll
+    for (int r = 0; r < kPackRows; ++r)
+        if (i0 + r < end && piece < g.cols)
+            *reinterpret_cast<uint4 *>(g.dst + (i0 + r) * g.ld_dst + piece) = p[r].q;
 }
 
 // dx of token order[i]: the parts' sum, and the target's term.  Tokens without a
@@ -751,40 +757,46 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_pack(const __grid_constant
 template <bool AL>
 __global__ void __launch_bounds__(kRowThreads) k_loss_finish(const __grid_constant__ FinishArgs g)
 {
-    using P = RowPiece<__nv_bfloat16, AL>;
     pdl_wait();
     pdl_launch_dependents();
     const int64_t i = blockIdx.x, token = g.order[i];
-    const int slab = blockIdx.y;
+    __nv_bfloat16 *dx = g.dx + token * g.ld_dx;
+    const int c = piece_of<__nv_bfloat16>(blockIdx.y) - skip_of_row<__nv_bfloat16, AL>(dx);
+    if (c >= g.cols) return;
     Piece<__nv_bfloat16, AL> p;
-    float acc[P::kVec];
+    float acc[kVec<__nv_bfloat16>];
 #pragma unroll
-    for (int e = 0; e < P::kVec; ++e) acc[e] = 0.0f;
+    for (int e = 0; e < kVec<__nv_bfloat16>; ++e) acc[e] = 0.0f;
     if (*g.status) {
 #pragma unroll
-        for (int e = 0; e < P::kVec; ++e) acc[e] = __int_as_float(0x7FC00000);
+        for (int e = 0; e < kVec<__nv_bfloat16>; ++e) acc[e] = __int_as_float(0x7FC00000);
     } else if (i < *g.count) {
         const float f = g.coef[i];
-        p.load(g.w + (g.gathered ? i : static_cast<int64_t>(g.key[i])) * g.ld_w, slab, g.cols);
+        p.load(g.w + (g.gathered ? i : static_cast<int64_t>(g.key[i])) * g.ld_w, c, g.cols);
         const int parts = g.splits > 1 ? parts_of((*g.count + kTile - 1) / kTile * ((g.cols + kTile - 1) / kTile), g.depth,
                                                   g.splits, g.pairs)
                                        : 1;
         for (int s = 0; s < parts; ++s) {
             const float *part = g.part + (s * g.tokens + i) * g.ld_part;
-            float v[P::kVec];
-            FloatPiece<__nv_bfloat16, AL>::load(v, part, slab, g.cols);
+            float v[kVec<__nv_bfloat16>];
+            if (AL) {
+                load_floats<__nv_bfloat16>(v, part, c);
+            } else {
 #pragma unroll
-            for (int e = 0; e < P::kVec; ++e) acc[e] += v[e];
+                for (int e = 0; e < kVec<__nv_bfloat16>; ++e) v[e] = c + e >= 0 && c + e < g.cols ? part[c + e] : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < kVec<__nv_bfloat16>; ++e) acc[e] += v[e];
         }
 #pragma unroll
-        for (int e = 0; e < P::kVec; ++e) acc[e] = fmaf(f, to_float(p.v[e]), acc[e]);
+        for (int e = 0; e < kVec<__nv_bfloat16>; ++e) acc[e] = fmaf(f, to_float(p.v[e]), acc[e]);
     } else if (id_at(g.ids, g.wide, token) >= 0) {
 #pragma unroll
-        for (int e = 0; e < P::kVec; ++e) acc[e] = __int_as_float(0x7FC00000);
+        for (int e = 0; e < kVec<__nv_bfloat16>; ++e) acc[e] = __int_as_float(0x7FC00000);
     }
 #pragma unroll
-    for (int e = 0; e < P::kVec; ++e) p.v[e] = __float2bfloat16_rn(acc[e]);
-    p.store(g.dx + token * g.ld_dx, slab, g.cols);
+    for (int e = 0; e < kVec<__nv_bfloat16>; ++e) p.v[e] = __float2bfloat16_rn(acc[e]);
+    p.store(dx, c, g.cols);
 }
 
 }  // namespace dev
@@ -831,9 +843,10 @@ cudaError_t pack(const PackArgs &g, bool aligned, cudaStream_t s)
 {
     if (g.rows == 0) return cudaSuccess;
     uint32_t threads, slabs;
-    row_shape(g.cols, aligned ? 8 : 4, &threads, &slabs);
-    return aligned ? launch<true>(dev::k_loss_pack<true>, dim3(g.rows, slabs), threads, 0, 1, s, g)
-                   : launch<true>(dev::k_loss_pack<false>, dim3(g.rows, slabs), threads, 0, 1, s, g);
+    row_shape(g.cols, 8, true, &threads, &slabs);
+    const dim3 grid((g.rows + dev::kPackRows - 1) / dev::kPackRows, slabs);
+    return aligned ? launch<true>(dev::k_loss_pack<true>, grid, threads, 0, 1, s, g)
+                   : launch<true>(dev::k_loss_pack<false>, grid, threads, 0, 1, s, g);
 }
 
 // The values of g that are there at a time: 256 MB.
@@ -847,7 +860,7 @@ uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 // 256 MB.
 int dx_splits(uint64_t tokens, uint64_t cols)
 {
-    const uint64_t room = (1ull << 28) / std::max<uint64_t>(1, 4 * tokens * up(cols, 4));
+    const uint64_t room = (1ull << 28) / std::max<uint64_t>(1, 4 * tokens * up(cols, 8));
     return static_cast<int>(std::max<uint64_t>(1, std::min<uint64_t>(16, room)));
 }
 
@@ -883,12 +896,11 @@ struct ForwardLayout : Layout {
 };
 struct BackwardLayout : Layout {
     uint64_t head, key[2], order[2], first, lse, share, coef, x, extra, part, target, g, sums, w;
-    uint64_t ld, ld4, piece, ld_g;
+    uint64_t ld, piece, ld_g;
     int splits, depth;
     BackwardLayout(uint64_t tokens, uint64_t vocab, uint64_t cols, uint64_t rows, bool weight, bool move, bool pieces)
     {
         ld = up(cols, 8);
-        ld4 = up(cols, 4);
         splits = dx_splits(tokens, cols);
         uint64_t most = std::max<uint64_t>(256, kGradValues / std::max<uint64_t>(1, up(tokens, 256)) / 256 * 256);
         depth = static_cast<int>(up(std::min(vocab, most), dev::kDepth) / dev::kDepth);
@@ -905,12 +917,12 @@ struct BackwardLayout : Layout {
         share = take(4 * tokens);
         coef = take(4 * tokens);
         x = take(2 * tokens * ld);
-        extra = take(weight ? 4 * tokens * ld4 : 0);
-        part = take(4 * static_cast<uint64_t>(splits) * tokens * ld4);
+        extra = take(weight ? 4 * tokens * ld : 0);
+        part = take(4 * static_cast<uint64_t>(splits) * tokens * ld);
         target = take(pieces ? 2 * tokens * ld : 0);
         // g takes the place of the partial sums of the targets' terms, which come before it
         g = take(std::max(2 * tokens * ld_g,
-                          weight ? 8 * (up(tokens, LCT_EMBEDDING_CHUNK(tokens)) / LCT_EMBEDDING_CHUNK(tokens)) * cols : 0));
+                          weight ? 8 * (up(tokens, LCT_EMBEDDING_CHUNK(tokens)) / LCT_EMBEDDING_CHUNK(tokens)) * LCT_EMBEDDING_PART(cols) : 0));
         w = take(move ? 2 * piece * ld : 0);
     }
 };
@@ -1100,7 +1112,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
     int32_t *status = at<int32_t>(d_work, l.head), *count = status + 2;
     int32_t *key = at<int32_t>(d_work, l.key[0]), *order = at<int32_t>(d_work, l.order[0]);
     __nv_bfloat16 *xp = at<__nv_bfloat16>(d_work, l.x);
-    const int64_t ld = static_cast<int64_t>(l.ld), ld4 = static_cast<int64_t>(l.ld4);
+    const int64_t ld = static_cast<int64_t>(l.ld);
     const int32_t tokens = static_cast<int32_t>(t), k = static_cast<int32_t>(cols);
     if (begins) {
         SortArgs o{};
@@ -1151,7 +1163,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
             e.count = count;
             e.coef = p.coef_out;
             e.out = at<float>(d_work, l.extra);
-            e.ld_out = ld4;
+            e.ld_out = ld;
             e.part = at<float>(d_work, l.g);
             e.scale = 1.0f;
             e.cols = k;
@@ -1220,7 +1232,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
         g.pairs = pairs;
         g.add = !(begins && r0 == 0);
         if (!box_map(&maps.a, gp, n, t, l.ld_g, 0, g.a_rows) || !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kDepth) ||
-            !box_map32(&maps.c, at<float>(d_work, l.part), cols, t, l.ld4, l.splits) ||
+            !box_map32(&maps.c, at<float>(d_work, l.part), cols, t, l.ld, l.splits) ||
             product<kDx>(g, maps, s) != cudaSuccess)
             return LCT_ERR_CUDA;
         if (!d_dw) continue;
@@ -1229,7 +1241,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
         g.splits = 1;
         g.extra = at<float>(d_work, l.extra);
         g.first = at<int32_t>(d_work, l.first);
-        g.ld_extra = ld4;
+        g.ld_extra = ld;
         g.out = bf16(d_dw) + r0 * ld_dw;
         g.ld_out = static_cast<int64_t>(ld_dw);
         g.boxes = dw_boxes;
@@ -1240,7 +1252,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
     if (!ends) return LCT_OK;
     FinishArgs f{};
     f.part = at<float>(d_work, l.part);
-    f.ld_part = ld4;
+    f.ld_part = ld;
     f.tokens = static_cast<int64_t>(t);
     f.splits = l.splits;
     f.depth = l.depth;
@@ -1260,7 +1272,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
     f.cols = k;
     const bool al = cols % 8 == 0 && matrix_al(dx) && (pieces || matrix_al(w));
     uint32_t threads, slabs;
-    row_shape(k, al ? 8 : 4, &threads, &slabs);
+    row_shape(k, 8, al, &threads, &slabs);
     const cudaError_t rc = al ? launch<true>(dev::k_loss_finish<true>, dim3(tokens, slabs), threads, 0, 1, s, f)
                               : launch<true>(dev::k_loss_finish<false>, dim3(tokens, slabs), threads, 0, 1, s, f);
     return rc == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;

@@ -215,3 +215,35 @@ def test_loss_and_gradients(vocab, t, v, k):
     assert frozen[1] is None and torch.equal(frozen[0], dx)
     again = vocab.cross_entropy_grads(x, w, ids, loss, lse, c)
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("k", [1, 7, 8, 9, 250, 256, 263, 2049, 4100])
+def test_rows_at_any_address(vocab, k, dtype):
+    """Tables, gradients and bases that begin anywhere, rows any distance apart, and what lies around them."""
+    gen = generator(k)
+    t, v = 70, 23
+    ids = make_ids(t, v, gen, 0.2)
+    for i in range(9):
+        ld = k + 9 + i
+        def view(rows, at):  # noqa: E306
+            whole = torch.randn(rows + 2, ld, generator=gen, device="cuda").to(dtype)
+            return whole, whole[1:-1, at:at + k]
+        _, table = view(v, i)
+        whole, out = view(t, (3 * i) % 9)
+        before = whole.clone()
+        want = (table.float() * 1.7).to(dtype)[ids.clamp(min=0)]
+        want[ids < 0] = 0
+        vocab.embedding(ids, table, 1.7, out=out)
+        assert torch.equal(out, want)
+        out.copy_(before[1:-1, (3 * i) % 9:(3 * i) % 9 + k])
+        assert torch.equal(whole, before)
+        _, dy = view(t, i)
+        _, base = view(v, (5 * i) % 9)
+        whole, out = view(v, (2 * i) % 9)
+        before = whole.clone()
+        vocab.embedding_grad(dy, ids, v, 1.7, base=base, out=out)
+        want, off = grad_bound(dy, ids, v, 1.7, base)
+        assert ((out.double() - want).abs() <= off).all()
+        out.copy_(before[1:-1, (2 * i) % 9:(2 * i) % 9 + k])
+        assert torch.equal(whole, before)
