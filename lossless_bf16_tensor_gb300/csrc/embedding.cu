@@ -3,13 +3,15 @@
 //   lookup    out_i = f E[t_i]                         (0 for t_i < 0)
 //   gradient  dE_v = dE0_v + f sum over t_i = v of dy_i
 //
-// Both move rows and compute next to nothing: HBM bounds them.  The gradient
-// reads dy once, in the order of the ids (a stable radix sort of the batch's ids
-// comes first), and writes every row of dE once: sums are held in float32
-// registers, in the tokens' order, so that no atomics are needed and the same
-// inputs give the same bits.  Frequent ids would make one block add thousands of
-// rows; so the sorted tokens are cut into chunks of 32 whatever their ids, and
-// the partial sums of an id that crosses chunks are added by a second kernel.
+// Both move rows and compute next to nothing: HBM bounds them (a lookup of 16,384
+// rows of 8 KB by frequent ids takes 32 us, 8.5 TB/s with what L2 gives again; the
+// gradient of the same batch in a table of 131,072 rows 187 us, 97% of what its
+// 1.2 GB take at a copy's rate).  The gradient reads dy once, in the order of the
+// ids, which are sorted first, and writes every row of dE once: sums are held in
+// float32 registers, in the tokens' order, so that no atomics are needed and the
+// same inputs give the same bits.  Frequent ids would make one block add thousands
+// of rows; so the sorted tokens are cut into chunks of 8 or 32 whatever their ids,
+// and the partial sums of an id that crosses chunks are added by a third kernel.
 #include <algorithm>
 #include <cstdint>
 
@@ -24,7 +26,7 @@
 namespace lct {
 namespace dev {
 
-// --------------------------------------------------------- sorting the ids
+// -------------------------------------------- rows without tokens, sorted ids
 
 // A row of a value, or of a base, in 16-byte pieces of the row between its ends,
 // by `lanes` threads of which this is the lane-th.
@@ -39,13 +41,13 @@ __device__ __forceinline__ void fill_row(const FillArgs &f, int64_t r, int lane,
     for (int c = lane; c < a; c += lanes) row[c] = base ? base[c] : value;
     uint4 *q = reinterpret_cast<uint4 *>(row + a);
     if (base) {
-        for (int c0 = lane; c0 < pieces; c0 += lanes * 8) {
-            uint4 v[8];  // asked for together: nobody tells the compiler that the rows are apart
+        for (int c0 = lane; c0 < pieces; c0 += lanes * 4) {
+            uint4 v[4];  // asked for together: nobody tells the compiler that the rows are apart
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
                 if (c0 + lanes * i < pieces) v[i] = load_any(base + a + 8 * (c0 + lanes * i), 16);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
                 if (c0 + lanes * i < pieces) q[c0 + lanes * i] = v[i];
         }
     } else {
@@ -260,9 +262,24 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding(const __grid_constant
     pdl_launch_dependents();
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) id[r] = i0 + r < g.tokens ? id_at(g.ids, g.wide, i0 + r) : -1;
+    // whole pieces of rows that are all there: no branch between their reads
+    bool inside = !AL;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int c = piece - skip_of_row<T, AL>(static_cast<T *>(g.out) + (i0 + r) * g.ld_out);
+        inside = inside && id[r] >= g.row0 && id[r] < g.row0 + g.rows && c >= 0 && c + kVec<T> <= g.cols;
+    }
+    if (inside) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int c = piece - skip_of_row<T, AL>(static_cast<T *>(g.out) + (i0 + r) * g.ld_out);
+            p[r].q = load_any(static_cast<const T *>(g.table) + (id[r] - g.row0) * g.ld_table + c, 16);
+        }
+    }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         const int64_t at = id[r] - g.row0;
+        if (inside) continue;
         if (at >= 0 && at < g.rows) {
             const int c = piece - skip_of_row<T, AL>(static_cast<T *>(g.out) + (i0 + r) * g.ld_out);
             p[r].load(static_cast<const T *>(g.table) + at * g.ld_table, c, g.cols);
@@ -289,7 +306,9 @@ __global__ void __launch_bounds__(kRowThreads) k_embedding(const __grid_constant
 // ---------------------------------------------------------------- gradient
 
 constexpr int kSegTokens = 32;  // of a chunk, at most
-constexpr int kSegAhead = 8;  // rows asked for at a time
+// Rows asked for at a time.  Eight of them, with their bases, leave so few blocks
+// on an SM that the rows without tokens, which the same launch writes, take 10% longer.
+constexpr int kSegAhead = 4;
 
 // The row that key's sum goes to, and the column of it at which this thread's piece begins.
 template <typename T, bool AL>
@@ -369,7 +388,7 @@ __device__ __forceinline__ void fill_rest(const SegmentArgs &g, int64_t block)
 
 // A chunk of sorted tokens and a slab of columns a block; rows without tokens by the blocks behind them.
 template <typename T, bool AL, bool BASE>
-__global__ void __launch_bounds__(kRowThreads) k_segments(const __grid_constant__ SegmentArgs g)
+__global__ void __launch_bounds__(kRowThreads, 4) k_segments(const __grid_constant__ SegmentArgs g)
 {
     __shared__ int keys[kSegTokens], tokens[kSegTokens];
     __shared__ float coefs[kSegTokens];
@@ -384,16 +403,18 @@ __global__ void __launch_bounds__(kRowThreads) k_segments(const __grid_constant_
     const int piece = piece_of<T>(blockIdx.x % g.slabs);
     const bool used = piece < g.cols + (AL ? 0 : kVec<T> - 1);
     const int64_t i0 = chunk * g.chunk;
-    const int n = static_cast<int>(min(static_cast<int64_t>(g.chunk), *g.count - i0));
-    if (n <= 0) return;
-    for (int j = threadIdx.x; j < n; j += blockDim.x) {
+    const int64_t count = *g.count;
+    for (int j = threadIdx.x; j < g.chunk && i0 + j < g.tokens; j += blockDim.x) {
         keys[j] = g.key[i0 + j];
         tokens[j] = g.order ? g.order[i0 + j] : static_cast<int>(i0 + j);
-        coefs[j] = g.coef ? g.coef[i0 + j] : 1.0f;
+        coefs[j] = g.coef && i0 + j < count ? g.coef[i0 + j] : 1.0f;
     }
+    const int before = i0 > 0 ? g.key[i0 - 1] : -1, behind = i0 + g.chunk < g.tokens ? g.key[i0 + g.chunk] : -1;
     __syncthreads();
-    const bool goes_on = i0 + n < *g.count && g.key[i0 + n] == keys[n - 1];
-    int64_t began = i0 > 0 && g.key[i0 - 1] == keys[0] ? -1 : i0;  // where the id's tokens begin (-1: in an earlier chunk)
+    const int n = static_cast<int>(min(static_cast<int64_t>(g.chunk), count - i0));
+    if (n <= 0) return;
+    const bool goes_on = i0 + n < count && behind == keys[n - 1];
+    int64_t began = before == keys[0] ? -1 : i0;  // where the id's tokens begin (-1: in an earlier chunk)
     float acc[kVec<T>];
 #pragma unroll
     for (int e = 0; e < kVec<T>; ++e) acc[e] = 0.0f;
@@ -438,11 +459,12 @@ __global__ void __launch_bounds__(kRowThreads) k_segment_ends(const __grid_const
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t chunk = blockIdx.x / g.slabs, i0 = chunk * g.chunk, next = i0 + g.chunk, count = *g.count;
+    const int64_t chunk = blockIdx.x / g.slabs, i0 = chunk * g.chunk, next = i0 + g.chunk;
     const int piece = piece_of<T>(blockIdx.x % g.slabs), lane = threadIdx.x & 31;
-    if (next >= count) return;
-    const int key = g.key[next - 1];
-    if (g.key[next] != key || (i0 > 0 && g.key[i0] == key && g.key[i0 - 1] == key)) return;
+    // (there is a chunk behind this one, so that all of these are ids; those behind the last are no row's)
+    const int64_t count = *g.count;
+    const int key = g.key[next - 1], begins = g.key[i0], before = i0 ? g.key[i0 - 1] : -1, goes_on = g.key[next];
+    if (next >= count || goes_on != key || (begins == key && before == key)) return;
     // the chunks that the id goes on in
     int64_t more = 0;
     for (;; more += 32) {
@@ -458,12 +480,18 @@ __global__ void __launch_bounds__(kRowThreads) k_segment_ends(const __grid_const
     load_floats<T>(acc, partial(g, chunk, 1), piece);
     Piece<T, AL> base;
     if (g.base) base.load(static_cast<const T *>(g.base) + key * g.ld_base, first_col<T, AL>(g, key, piece), g.cols);
-#pragma unroll 8
-    for (int64_t c = 1; c <= more; ++c) {
-        float v[kVec<T>];
-        load_floats<T>(v, partial(g, chunk + c, 0), piece);
+    constexpr int kParts = 64 / kVec<T>;  // at a time
+    for (int64_t c0 = 1; c0 <= more; c0 += kParts) {
+        float v[kParts][kVec<T>];
 #pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) acc[e] += v[e];
+        for (int i = 0; i < kParts; ++i)
+            if (c0 + i <= more) load_floats<T>(v[i], partial(g, chunk + c0 + i, 0), piece);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            if (c0 + i > more) break;
+#pragma unroll
+            for (int e = 0; e < kVec<T>; ++e) acc[e] += v[i][e];
+        }
     }
     const int first = g.compact ? g.first[key] : 0;
     finish_row<T, AL>(g, key, first, piece, acc, base);
@@ -486,7 +514,7 @@ cudaError_t launch_sort_ids(SortArgs g, cudaStream_t s)
     const uint32_t tokens = static_cast<uint32_t>(g.tokens);
     if (tokens <= dev::kRankMost) {
         // as few ids a block as there are SMs for
-        const uint32_t ids = tokens <= 4096 ? 32 : 64;
+        const uint32_t ids = tokens <= 152 * 32 ? 32 : 64;
         const uint32_t blocks = (tokens + ids - 1) / ids + fill_blocks(g.fill, 131072, 152 * 2);
         const uint32_t smem = (tokens + 127) / 128 * 512;
         if (!blocks) return cudaSuccess;
@@ -564,8 +592,9 @@ lct_status check_ids(const lct_ids *ids)
 
 namespace {
 
-// Bytes of rows that are written while ids are sorted, by the two ways of that.
-constexpr int64_t kFillShort = 24 << 20, kFillLong = 160 << 20;
+// Bytes of rows that are written while ids are sorted, by the two ways of that (about 8 and 20 us; none: 218 us where
+// 16,384 tokens of 8 KB take 207, 160 MB: 210).
+constexpr int64_t kFillShort = 12 << 20, kFillLong = 100 << 20;
 
 uint64_t value_bytes(int32_t dtype) { return dtype == LCT_DTYPE_F32 ? 4 : 2; }
 

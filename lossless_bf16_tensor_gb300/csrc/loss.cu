@@ -46,6 +46,7 @@ struct ProductArgs {
     int32_t *status;        // latched: a wait that ran out
     int32_t splits;         // kDx: parts of the depth at most, each with a result of its own
     int32_t depth, pairs;   // what their number goes by: the same for all pieces
+    int32_t sum_steps;      // kLogits: steps of depth that tensor cores add by themselves
     bool add;               // kDx: to what is there
     bool begins;            // kLogits: a call's first product clears the status and the counter behind it
     const void *ids;        // kLogits: the targets
@@ -65,6 +66,10 @@ struct ProductArgs {
 };
 struct ProductMaps {
     CUtensorMap a, b, c;
+};
+struct FewArgs {
+    const __nv_bfloat16 *x, *w;
+    int64_t ld_x, ld_w;
 };
 struct MergeArgs {
     const float2 *part;     // [slots][tokens]
@@ -116,11 +121,6 @@ constexpr int kFirstEndWarp = 4;
 constexpr uint32_t kStaging = 32 * 128;  // a warp's 32 rows of 128 bytes
 constexpr int kGroup = 16;               // tiles of rows that are worked on side by side
 constexpr float kLog2e = 1.4426950408889634f;
-// Depth of logits that tensor cores add by themselves: their float32 sums drop
-// what does not fit, always towards zero, which over a depth of 4096 makes the
-// losses wrong by 2e-6; each 1024 are added to the rest in registers (5e-7).
-constexpr int kSumSteps = 1024 / kDepth;
-
 // Warps that turn sums into results, four to a unit at a time, and the ring's
 // slots.  Exponentials take long, so that each unit of a tile has its own four;
 // where results leave by boxes, their staging takes the room of a slot.
@@ -285,11 +285,12 @@ __device__ __forceinline__ void join_columns(const float (&z)[N], float &m, floa
 #pragma unroll
     for (int i = 4; i < N; ++i) t[i & 3] = fmaxf(t[i & 3], z[i]);
     const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-    const float at = top == -INFINITY ? 0.0f : top * kLog2e;
+    // (differences first: the largest has to count as exactly 1 where the others are next to nothing)
+    const float at = top == -INFINITY ? 0.0f : top;
     float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < N; ++i) a[i & 3] += exp2_fast(fmaf(z[i], kLog2e, -at));
-    s = fmaf(s, exp2_fast(fmaf(m, kLog2e, -at)), (a[0] + a[1]) + (a[2] + a[3]));
+    for (int i = 0; i < N; ++i) a[i & 3] += exp2_fast((z[i] - at) * kLog2e);
+    s = fmaf(s, exp2_fast((m - at) * kLog2e), (a[0] + a[1]) + (a[2] + a[3]));
     m = top;
 }
 
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
             bool add = false;
             for (int d = w.k0; d < w.k1; ++d, ++i) {
                 if (left == 0) {
-                    left = OP == kLogits ? min(kSumSteps, w.k1 - d) : w.k1 - d;
+                    left = OP == kLogits ? min(g.sum_steps, w.k1 - d) : w.k1 - d;
                     if (t >= 2) wait(&drained[t & 1], (t / 2 - 1) & 1);
                     sums = tmem + (t & 1) * kTile;
                     add = false;
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
                 for (int e = 0; e < kUnit; ++e) z[e] = 0.0f;
                 const int col0 = w.tn * kTile + group * kUnit;
 #pragma unroll 1
-                for (int d = w.k0; d < w.k1; d += kSumSteps, ++t) {
+                for (int d = w.k0; d < w.k1; d += g.sum_steps, ++t) {
                     wait(&done[t & 1], (t / 2) & 1);
                     if (waiter.dead) break;
                     tc_after();
@@ -639,6 +640,110 @@ __device__ __forceinline__ void join(float &m, float &s, float2 o)
     m = top;
 }
 
+// ------------------------------------------------------------- few tokens
+
+// Logits of up to 4 tokens, which reading W bounds (32,768 rows of 4096, with the
+// merge: 47 us for one token, 5.7 TB/s, 55 for two, 69 for four; by tiles 57 to 60.
+// Eight take 113.)  A warp takes two rows of W at a time, a lane eight columns of
+// 256; x is in shared memory.  Sums are float32 multiply-adds, rounded
+// to nearest: with one token's loss there is nothing that an error averages out
+// over, and tiles would have to add every 64 of depth in registers to be as exact,
+// which takes them three times as long.  W's rows may begin anywhere.
+constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kFewBlocks = 304, kFewMost = 4;
+
+__host__ __device__ constexpr uint32_t few_pitch(uint32_t cols) { return (cols + 255) / 256 * 512; }
+
+// The products of two pairs of BF16 values join two sums.
+__device__ __forceinline__ void add_products(float2 &acc, uint32_t a, uint32_t b)
+{
+    const float2 x = make_float2(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+    const float2 y = make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
+    acc = __ffma2_rn(x, y, acc);
+}
+
+template <int TOKENS, bool AL>
+__global__ void __launch_bounds__(kFewThreads, 2) k_logits_few(const __grid_constant__ ProductArgs g,
+                                                                 const __grid_constant__ FewArgs f)
+{
+    constexpr int ROWS = 2, kSteps = 4;  // of 256 columns, asked for at a time
+    extern __shared__ uint4 raw4[];
+    __shared__ float2 joined[kFewWarps][TOKENS];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t xs = smem_addr(raw4), pitch = few_pitch(g.k);
+    pdl_wait();
+    pdl_launch_dependents();
+    if (g.begins && blockIdx.x == 0 && threadIdx.x < 2) g.status[threadIdx.x] = 0;
+    const int pieces = pitch / 16;
+    for (int i = threadIdx.x; i < TOKENS * pieces; i += kFewThreads) {
+        const int token = i / pieces, c = (i - token * pieces) * 8;
+        Piece<__nv_bfloat16, false> p;
+        p.q = make_uint4(0, 0, 0, 0);
+        if (token < g.m && c < g.k) p.load(f.x + token * f.ld_x, c, g.k);
+        store16(xs + token * pitch + c * 2, p.q);
+    }
+    __syncthreads();
+    const int64_t target = lane < g.m ? id_at(g.ids, g.wide, lane) - g.row0 : -1;  // lane t's results are token t's
+    float top = -INFINITY, sum = 0.0f;
+    for (int row = (blockIdx.x * kFewWarps + warp) * ROWS; row < g.n; row += gridDim.x * kFewWarps * ROWS) {
+        float2 acc[ROWS][TOKENS];  // of even and odd columns
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int t = 0; t < TOKENS; ++t) acc[r][t] = make_float2(0.0f, 0.0f);
+        for (int c0 = 0; c0 < g.k; c0 += 256 * kSteps) {
+            Piece<__nv_bfloat16, AL> w[kSteps][ROWS];
+            auto ask = [&](auto load) {
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r)
+                        load(w[j][r], f.w + min(row + r, g.n - 1) * f.ld_w, c0 + 256 * j + lane * 8);
+            };
+            if (!AL && c0 + 256 * kSteps <= g.k)
+                ask([](auto &p, const __nv_bfloat16 *from, int c) { p.q = load_any(from + c, 16); });
+            else
+                ask([&](auto &p, const __nv_bfloat16 *from, int c) { p.load(from, c, g.k); });
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+                if (c0 + 256 * j >= g.k) break;
+#pragma unroll
+                for (int t = 0; t < TOKENS; ++t) {
+                    const uint4 x = load16(xs + t * pitch + (c0 + 256 * j + lane * 8) * 2);
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) {
+                        add_products(acc[r][t], w[j][r].q.x, x.x);
+                        add_products(acc[r][t], w[j][r].q.y, x.y);
+                        add_products(acc[r][t], w[j][r].q.z, x.z);
+                        add_products(acc[r][t], w[j][r].q.w, x.w);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            float mine = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < TOKENS; ++t) {
+                float z = acc[r][t].x + acc[r][t].y;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+                if (lane == t) mine = z;
+            }
+            if (row + r >= g.n) break;
+            if (target == row + r) g.mine[lane] = mine;
+            const float most = fmaxf(top, mine), at = most == -INFINITY ? 0.0f : most;
+            sum = sum * exp2_fast((top - at) * kLog2e) + exp2_fast((mine - at) * kLog2e);
+            top = most;
+        }
+    }
+    if (lane < TOKENS) joined[warp][lane] = make_float2(top, sum);
+    __syncthreads();
+    if (warp == 0 && lane < g.m) {
+        for (int i = 1; i < kFewWarps; ++i) join(top, sum, joined[i][lane]);
+        g.part[static_cast<int64_t>(blockIdx.x) * g.m + lane] = make_float2(top, sum);
+    }
+}
+
 // Joins the tiles' maxima and sums of 32 tokens a block with the state of the
 // pieces before; after the last piece, the losses.  Their sum (double, in the
 // order of the blocks) is made by the last block to come.
@@ -668,9 +773,10 @@ __global__ void __launch_bounds__(1024) k_loss_merge(const __grid_constant__ Mer
             g.state[token] = make_float2(m, s);
         } else {
             const int64_t id = id_at(g.ids, g.wide, token);
-            const float lse = *g.status ? __int_as_float(0x7FC00000) : m + logf(s);
-            const float l = id < 0 ? 0.0f : id >= g.vocab ? __int_as_float(0x7FC00000) : lse - g.mine[token];
-            g.lse[token] = lse;
+            // the loss of a token that is sure is far smaller than its logits: not by way of lse
+            const float tail = *g.status ? __int_as_float(0x7FC00000) : logf(s);
+            const float l = id < 0 ? 0.0f : id >= g.vocab ? __int_as_float(0x7FC00000) : (m - g.mine[token]) + tail;
+            g.lse[token] = m + tail;
             g.loss[token] = l;
             loss = l;
             counted = id >= 0;
@@ -732,13 +838,21 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_pack(const __grid_constant
     const int count = g.count ? *g.count : g.rows;
     const int end = min(g.rows, count + 63);  // (rows behind the last are nobody's, and boxes fill them with zeros)
     Piece<__nv_bfloat16, AL> p[kPackRows];
+    const bool inside = !AL && piece + 8 <= g.cols && i0 + kPackRows <= count;  // whole pieces of all rows: no branch between
+    if (inside) {
+#pragma unroll
+        for (int r = 0; r < kPackRows; ++r) {
+            const int64_t token = g.order ? g.order[i0 + r] : i0 + r;
+            p[r].q = load_any(g.src + token * g.ld_src + piece, 16);
+        }
+    }
 #pragma unroll
     for (int r = 0; r < kPackRows; ++r) {
         const int i = i0 + r;
-        p[r].q = make_uint4(0, 0, 0, 0);
+        if (!inside) p[r].q = make_uint4(0, 0, 0, 0);
         if (i >= count) continue;
         const int64_t token = g.order ? g.order[i] : i;
-        p[r].load(g.src + token * g.ld_src, piece, g.cols);
+        if (!inside) p[r].load(g.src + token * g.ld_src, piece, g.cols);
         if (g.order && piece == 0) {
             const float c = g.dloss[token * g.dloss_stride] * (g.scale ? *g.scale : 1.0f);
             g.lse_out[i] = g.lse[token];
@@ -836,6 +950,32 @@ cudaError_t product(const ProductArgs &g, const ProductMaps &maps, cudaStream_t 
                         dev::Shape<OP>::kThreads, dev::Shape<OP>::kBytes, 2, s, g, maps);
 }
 
+// Whether a forward pass is one of few tokens: x fits beside another block's.
+bool is_few(uint64_t tokens, uint64_t cols)
+{
+    const uint64_t rows = tokens <= 1 ? 1 : tokens <= 2 ? 2 : 4;
+    return tokens <= dev::kFewMost && rows * dev::few_pitch(static_cast<uint32_t>(cols)) <= 100 * 1024;
+}
+uint32_t few_blocks(uint64_t rows)
+{
+    return static_cast<uint32_t>(std::min<uint64_t>(dev::kFewBlocks, (rows + 2 * dev::kFewWarps - 1) / (2 * dev::kFewWarps)));
+}
+template <int TOKENS>
+cudaError_t few_at(const ProductArgs &g, const FewArgs &f, bool aligned, cudaStream_t s)
+{
+    return launch<true>(aligned ? dev::k_logits_few<TOKENS, true> : dev::k_logits_few<TOKENS, false>,
+                        dim3(few_blocks(g.n)), dev::kFewThreads, TOKENS * dev::few_pitch(g.k), 1, s, g, f);
+}
+cudaError_t few(const ProductArgs &g, const FewArgs &f, bool aligned, cudaStream_t s)
+{
+    return g.m <= 1 ? few_at<1>(g, f, aligned, s) : g.m <= 2 ? few_at<2>(g, f, aligned, s) : few_at<4>(g, f, aligned, s);
+}
+
+// Tensor cores' float32 sums drop what does not fit, always towards zero: over a depth of 4096 a logit of 12 comes out 3e-5
+// too small, and the loss of a token that is sure is wrong by that share.  So each 512 of depth are added to the rest in
+// registers (7e-6; 2 to 3% longer.  256: a quarter longer).
+constexpr int kSumDepth = 512;
+
 // Rows of A's boxes.  Of few tokens no more is fetched than there is (rows behind them reach only themselves).
 uint32_t a_rows(uint64_t tokens) { return tokens <= 8 ? 8 : tokens <= 32 ? 32 : dev::kHalfTile; }
 
@@ -890,7 +1030,8 @@ struct ForwardLayout : Layout {
         sums = take(8 * blocks);
         counts = take(4 * blocks);
         x = take(move ? 2 * tokens * ld : 0);
-        part = take(8 * chunk * (up(piece, dev::kUnit) / dev::kUnit));
+        const uint64_t units = up(piece, dev::kUnit) / dev::kUnit;
+        part = take(8 * chunk * (is_few(tokens, cols) ? std::max<uint64_t>(units, few_blocks(piece)) : units));
         w = take(move ? 2 * piece * ld : 0);
     }
 };
@@ -959,7 +1100,7 @@ extern "C" uint64_t lct_loss_work_bytes(uint64_t tokens, uint64_t vocab, uint64_
     const bool move = flags & LCT_LOSS_UNALIGNED;
     if (flags & LCT_LOSS_BACKWARD)
         return BackwardLayout(tokens, vocab, cols, rows, flags & LCT_LOSS_WEIGHT, move, rows < vocab).bytes;
-    return ForwardLayout(tokens, cols, rows, move).bytes;
+    return ForwardLayout(tokens, cols, rows, move && !is_few(tokens, cols)).bytes;
 }
 
 namespace {
@@ -972,7 +1113,8 @@ lct_status forward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, u
     const lct_status ok = check_batch(targets, d_x, ld_x, cols, d_w, ld_w, first, rows, d_work, &x, &w);
     if (ok != LCT_OK) return ok;
     const uint64_t t = targets->tokens, id_size = targets->wide ? 8 : 4;
-    const bool move = !matrix_al(x) || !matrix_al(w), begins = first == 0, ends = first + rows == targets->vocab;
+    const bool by_few = !stalled && is_few(t, cols), w_al = matrix_al(w) && cols % 8 == 0;
+    const bool move = !by_few && (!matrix_al(x) || !matrix_al(w)), begins = first == 0, ends = first + rows == targets->vocab;
     const ForwardLayout l(t, cols, rows, move);
     if (work_bytes < l.bytes || (t && (!d_loss || !d_lse)) || reinterpret_cast<uintptr_t>(d_loss) % 4 ||
         reinterpret_cast<uintptr_t>(d_lse) % 4 || reinterpret_cast<uintptr_t>(d_total) % 4)
@@ -1042,11 +1184,17 @@ lct_status forward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, u
             g.row0 = static_cast<int64_t>(first + r0);
             g.part = at<float2>(d_work, l.part);
             g.mine = at<float>(d_work, l.mine) + t0;
-            ProductMaps maps{};
-            g.a_rows = a_rows(tn);
-            if (!box_map(&maps.a, xp + t0 * ldx, cols, tn, ldx, 0, g.a_rows) ||
-                !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kHalfTile) || product<kLogits>(g, maps, s) != cudaSuccess)
-                return LCT_ERR_CUDA;
+            if (by_few) {
+                const FewArgs f{xp, wp, static_cast<int64_t>(ldx), static_cast<int64_t>(ldw)};
+                if (few(g, f, w_al, s) != cudaSuccess) return LCT_ERR_CUDA;
+            } else {
+                ProductMaps maps{};
+                g.a_rows = a_rows(tn);
+                g.sum_steps = kSumDepth / dev::kDepth;
+                if (!box_map(&maps.a, xp + t0 * ldx, cols, tn, ldx, 0, g.a_rows) ||
+                    !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kHalfTile) || product<kLogits>(g, maps, s) != cudaSuccess)
+                    return LCT_ERR_CUDA;
+            }
             MergeArgs m{};
             m.part = g.part;
             m.state = at<float2>(d_work, l.state) + t0;
@@ -1062,7 +1210,7 @@ lct_status forward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, u
             m.counter = g.status + 1;
             m.tokens = static_cast<int64_t>(tn);
             m.vocab = static_cast<int64_t>(targets->vocab);
-            m.slots = static_cast<int32_t>(up(n, dev::kUnit) / dev::kUnit);
+            m.slots = by_few ? static_cast<int32_t>(few_blocks(n)) : static_cast<int32_t>(up(n, dev::kUnit) / dev::kUnit);
             m.blocks = static_cast<int32_t>(up(t, dev::kMergeTokens) / dev::kMergeTokens);
             m.block0 = static_cast<int32_t>(t0 / dev::kMergeTokens);
             m.begins = begins && r0 == 0;

@@ -51,8 +51,8 @@ __device__ __forceinline__ uint4 load_any(const void *p, uint32_t bytes)
 {
     const uint32_t s = reinterpret_cast<uintptr_t>(p) & 15;
     const uint4 *a = reinterpret_cast<const uint4 *>(static_cast<const char *>(p) - s);
-    const uint4 x = *a;
-    const uint4 y = s + bytes > 16 ? a[1] : make_uint4(0, 0, 0, 0);
+    // (the second is read in any case, the first again where it holds all: a branch would keep reads from being batched)
+    const uint4 x = a[0], y = a[s + bytes > 16];
     return shift16(x, y, s);
 }
 __device__ __forceinline__ float to_float(float v) { return v; }

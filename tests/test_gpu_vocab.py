@@ -247,3 +247,20 @@ def test_rows_at_any_address(vocab, k, dtype):
         assert ((out.double() - want).abs() <= off).all()
         out.copy_(before[1:-1, (2 * i) % 9:(2 * i) % 9 + k])
         assert torch.equal(whole, before)
+
+
+@pytest.mark.parametrize("t,k", [(1, 4096), (5, 1024), (200, 8192), (300, 4096)])
+def test_losses_of_sure_tokens(vocab, t, k):
+    """Losses far smaller than their logits are as exact as the logits' differences are, not their roundings."""
+    x, w, ids, _ = loss_case(t, 3000, k, seed=30, lean=0.0)
+    x = (x.float() * 0.5 + 3.0 * w[ids].float()).to(BF16)
+    z = x.double() @ w.double().t()
+    want = torch.logsumexp(z, 1) - z.gather(1, ids[:, None])[:, 0]
+    assert float(want.median()) < 0.1
+    loss, lse = vocab.cross_entropy(x, w, ids)
+    # sums of 128 or 512 of depth drop at most 2^-23 of a part's size at each of their steps
+    mass = x.double().abs() @ w.double().abs().t()
+    part = 128 if t <= 256 else 512
+    off = 2 * (part / 16 + 17 + k / part) * 2.0 ** -23 * mass.amax(1)
+    # a loss moves by its own size times what the logits do
+    assert ((loss.double() - want).abs() <= off * want + 2.0 ** -21 * want + 2.0 ** -22).all()
