@@ -6,7 +6,7 @@
 //   g_iv = c_i (exp(z_iv - l_i) - [v = t_i]),  dx = g W,  dW = g^T x
 //
 // The four products (z, z again, g W, g^T x) are one kernel, k_product, with four
-// ends.  The first turns its tile of z into each row's maximum and sum of
+// ends (of up to 4 tokens, z is k_logits_few's).  The first turns its tile of z into each row's maximum and sum of
 // exponentials, which k_loss_merge joins over the tiles and pieces: what leaves
 // the SMs is 16 bytes a token and tile.  The second computes z again and writes
 // g as BF16, for a part of the piece that is bounded (kGradValues), which the
@@ -52,8 +52,8 @@ struct ProductArgs {
     const void *ids;        // kLogits: the targets
     bool wide;
     int64_t row0;           // the vocabulary's row that column 0 (kDw: row 0) is
-    float2 *part;           // kLogits: [units of 64 columns][m], maximum and sum of exponentials
-    float *mine;            // kLogits: the targets' logits
+    float2 *part;           // kLogits: [units of 64 columns][m], maximum (in log 2) and sum of exponentials
+    float *mine;            // kLogits: the targets' logits, in log 2
     const int32_t *target;  // kSoftmax, packed: targets, l and c
     const float *lse, *share;
     const float *extra;     // kDw: the targets' sums, row first[v] (-1: none)
@@ -120,19 +120,13 @@ constexpr uint32_t kStage = 2 * kOperand;
 constexpr int kFirstEndWarp = 4;
 constexpr uint32_t kStaging = 32 * 128;  // a warp's 32 rows of 128 bytes
 constexpr int kGroup = 16;               // tiles of rows that are worked on side by side
-constexpr float kLog2e = 1.4426950408889634f;
-// Warps that turn sums into results, four to a unit at a time, and the ring's
-// slots.  Exponentials take long, so that each unit of a tile has its own four;
-// where results leave by boxes, their staging takes the room of a slot.
-template <int OP>
-struct Shape {
-    static constexpr int kGroups = OP == kLogits ? 4 : 2;
-    static constexpr int kEndWarps = 4 * kGroups;
-    static constexpr int kStages = OP == kLogits ? 7 : 6;
-    static constexpr int kThreads = 32 * (kFirstEndWarp + kEndWarps);
-    static constexpr uint32_t kStagingAt = kStages * kStage;
-    static constexpr uint32_t kBytes = kStagingAt + (OP == kLogits ? 0 : kEndWarps * kStaging) + 1024;
-};
+constexpr float kLog2e = 1.4426950408889634f;  // 1 / log 2
+// Warps that turn sums into results, two for each quarter of the rows.  (Four,
+// for the exponentials of a short depth: 255 columns 8% faster, 1024 and more 3%
+// slower.)  Where results leave by boxes, their staging takes the room of a slot.
+constexpr int kGroups = 2, kEndWarps = 4 * kGroups, kProductThreads = 32 * (kFirstEndWarp + kEndWarps);
+constexpr int kStages = 6;
+constexpr uint32_t kStagingAt = kStages * kStage, kProductBytes = kStagingAt + kEndWarps * kStaging + 1024;
 
 __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t word, bool add)
 {
@@ -276,6 +270,10 @@ struct Items {
     }
 };
 
+// Logits are held in units of log 2, from the sums over depth on: a difference and
+// an exponential of base 2 then have no rounding between them, and the largest
+// counts as exactly 1 where the others are next to nothing.
+
 // Each row's maximum and sum of exponentials of N columns joins (m, s).
 template <int N>
 __device__ __forceinline__ void join_columns(const float (&z)[N], float &m, float &s)
@@ -285,12 +283,11 @@ __device__ __forceinline__ void join_columns(const float (&z)[N], float &m, floa
 #pragma unroll
     for (int i = 4; i < N; ++i) t[i & 3] = fmaxf(t[i & 3], z[i]);
     const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-    // (differences first: the largest has to count as exactly 1 where the others are next to nothing)
     const float at = top == -INFINITY ? 0.0f : top;
     float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < N; ++i) a[i & 3] += exp2_fast((z[i] - at) * kLog2e);
-    s = fmaf(s, exp2_fast((m - at) * kLog2e), (a[0] + a[1]) + (a[2] + a[3]));
+    for (int i = 0; i < N; ++i) a[i & 3] += exp2_fast(z[i] - at);
+    s = fmaf(s, exp2_fast(m - at), (a[0] + a[1]) + (a[2] + a[3]));
     m = top;
 }
 
@@ -299,12 +296,11 @@ __device__ __forceinline__ void join_columns(const float (&z)[N], float &m, floa
 // quarter of the rows.  Sums are double-buffered in TMEM, so that a tile's end
 // runs while the next one's products do.
 template <int OP>
-__global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
+__global__ void __launch_bounds__(kProductThreads, 1)
     k_product(const __grid_constant__ ProductArgs g, const __grid_constant__ ProductMaps maps)
 {
-    using H = Shape<OP>;
     constexpr bool kAcrossA = OP == kDw, kAcrossB = OP == kDx || OP == kDw;
-    constexpr int S = H::kStages;
+    constexpr int S = kStages;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[S], freed[S], done[2], drained[2];
     __shared__ uint32_t tmem_at;
@@ -319,7 +315,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&done[i], 1);
-            mbar_init(&drained[i], 2 * H::kEndWarps);
+            mbar_init(&drained[i], 2 * kEndWarps);
         }
         fence_mbar_init();
     }
@@ -330,7 +326,6 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     tc_after();
     const uint32_t tmem = tmem_at;
     pdl_wait();
-    pdl_launch_dependents();
     if (OP == kLogits && g.begins && blockIdx.x == 0 && threadIdx.x == 0) {
         g.status[0] = 0;
         g.status[1] = 0;
@@ -346,8 +341,9 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     Items items(g, m, k);
     Item w;
     Waiter waiter;
-    // a warp's lanes give up together
-    auto wait = [&](uint64_t *bar, int parity) {
+    auto wait = [&](uint64_t *bar, int parity) { waiter.wait_cluster(bar, parity); };
+    // where the lanes have to give up together (a vote a step would cost the product's warp 3%)
+    auto wait_all = [&](uint64_t *bar, int parity) {
         waiter.wait_cluster(bar, parity);
         waiter.dead = __any_sync(kFull, waiter.dead);
     };
@@ -383,6 +379,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
                 __syncwarp();
             }
         }
+        pdl_launch_dependents();  // (blocks that only wait, from the start, make the product 1 to 2% slower)
         // the block does not end before its boxes have been used
         for (int j = max(0, i - S); j < i; ++j) wait(&freed[j % S], (j / S) & 1);
     } else if (warp == 1 && rank == 0) {
@@ -425,7 +422,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     } else if (warp >= kFirstEndWarp) {
         // -------------------------------------------------------------- ends
         const int quarter = warp & 3, group = (warp - kFirstEndWarp) / 4;
-        const uint32_t staging = base + H::kStagingAt + (warp - kFirstEndWarp) * kStaging;
+        const uint32_t staging = base + kStagingAt + (warp - kFirstEndWarp) * kStaging;
         int t = 0;
         // the products after the next may take these sums' place
         auto arrive = [&] {
@@ -464,52 +461,59 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
             const int row0 = w.tm * kTile + rank * kHalfTile + quarter * 32, row = row0 + lane;
             const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
             if constexpr (OP == kLogits) {
-                // the unit of this warp, its sums over the depth in registers
-                float z[kUnit];
+                // this warp's units, their sums over the depth in registers
+                constexpr int kUnits = kTile / kUnit / kGroups;
+                float z[kUnits][kUnit];
 #pragma unroll
-                for (int e = 0; e < kUnit; ++e) z[e] = 0.0f;
-                const int col0 = w.tn * kTile + group * kUnit;
+                for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                    for (int e = 0; e < kUnit; ++e) z[u][e] = 0.0f;
+                const int first = w.tn * kTile + group * kUnits * kUnit;
 #pragma unroll 1
                 for (int d = w.k0; d < w.k1; d += g.sum_steps, ++t) {
-                    wait(&done[t & 1], (t / 2) & 1);
+                    wait_all(&done[t & 1], (t / 2) & 1);
                     if (waiter.dead) break;
                     tc_after();
-                    if (col0 < g.n) {
-                        const uint32_t sums = lanes + (t & 1) * kTile + group * kUnit;
+                    const uint32_t sums = lanes + (t & 1) * kTile + group * kUnits * kUnit;
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u)
 #pragma unroll
                         for (int c = 0; c < kUnit; c += 8) {
                             float v[8];
-                            tmem_load(sums + c, v);
+                            tmem_load(sums + u * kUnit + c, v);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) z[c + e] += v[e];
+                            for (int e = 0; e < 8; ++e) z[u][c + e] = fmaf(v[e], kLog2e, z[u][c + e]);
                         }
-                    }
                     arrive();
                 }
                 if (waiter.dead) break;
-                if (col0 >= g.n) continue;
-                int mine = -1;  // the target's column among these
-                if (row < m) {
-                    const int64_t id = info.id - g.row0 - col0;
-                    if (id >= 0 && id < min(kUnit, g.n - col0)) mine = static_cast<int>(id);
-                }
-                float top = -INFINITY, sum = 0.0f;
-                if (col0 + kUnit > g.n) {
 #pragma unroll
-                    for (int e = 0; e < kUnit; ++e)
-                        if (col0 + e >= g.n) z[e] = -INFINITY;
-                }
-                if (mine >= 0) {
+                for (int u = 0; u < kUnits; ++u) {
+                    const int col0 = first + u * kUnit;
+                    if (col0 >= g.n) break;
+                    int mine = -1;  // the target's column among these
+                    if (row < m) {
+                        const int64_t id = info.id - g.row0 - col0;
+                        if (id >= 0 && id < min(kUnit, g.n - col0)) mine = static_cast<int>(id);
+                    }
+                    float top = -INFINITY, sum = 0.0f;
+                    if (col0 + kUnit > g.n) {
 #pragma unroll
-                    for (int e = 0; e < kUnit; ++e)
-                        if (e == mine) g.mine[row] = z[e];
+                        for (int e = 0; e < kUnit; ++e)
+                            if (col0 + e >= g.n) z[u][e] = -INFINITY;
+                    }
+                    if (mine >= 0) {
+#pragma unroll
+                        for (int e = 0; e < kUnit; ++e)
+                            if (e == mine) g.mine[row] = z[u][e];
+                    }
+                    join_columns(z[u], top, sum);
+                    if (row < m) g.part[static_cast<int64_t>(col0 / kUnit) * m + row] = make_float2(top, sum);
                 }
-                join_columns(z, top, sum);
-                if (row < m) g.part[static_cast<int64_t>(col0 / kUnit) * m + row] = make_float2(top, sum);
             } else {
                 const bool some = w.k1 > w.k0;
                 if (some) {
-                    wait(&done[t & 1], (t / 2) & 1);
+                    wait_all(&done[t & 1], (t / 2) & 1);
                     tc_after();
                 }
                 if (waiter.dead) break;
@@ -519,9 +523,9 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
                 const float *extra = nullptr;
                 if (OP == kDw && info.target >= 0) extra = g.extra + info.target * g.ld_extra;
 #pragma unroll 1
-                for (int u = group; u < kTile / kUnit; u += H::kGroups) {
+                for (int u = group; u < kTile / kUnit; u += kGroups) {
                     const int col0 = w.tn * kTile + u * kUnit;
-                    const bool last = u + H::kGroups >= kTile / kUnit;
+                    const bool last = u + kGroups >= kTile / kUnit;
                     if constexpr (OP == kDx) {
 #pragma unroll 1
                         for (int c = 0; c < kUnit; c += 32) {
@@ -636,7 +640,7 @@ constexpr int kMergeTokens = 32, kMergeGroups = 32;
 __device__ __forceinline__ void join(float &m, float &s, float2 o)
 {
     const float top = fmaxf(m, o.x), at = top == -INFINITY ? 0.0f : top;
-    s = s * exp2_fast((m - at) * kLog2e) + o.y * exp2_fast((o.x - at) * kLog2e);
+    s = s * exp2_fast(m - at) + o.y * exp2_fast(o.x - at);
     m = top;
 }
 
@@ -727,12 +731,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_logits_few(const __grid_cons
                 float z = acc[r][t].x + acc[r][t].y;
 #pragma unroll
                 for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
-                if (lane == t) mine = z;
+                if (lane == t) mine = z * kLog2e;
             }
             if (row + r >= g.n) break;
             if (target == row + r) g.mine[lane] = mine;
             const float most = fmaxf(top, mine), at = most == -INFINITY ? 0.0f : most;
-            sum = sum * exp2_fast((top - at) * kLog2e) + exp2_fast((mine - at) * kLog2e);
+            sum = sum * exp2_fast(top - at) + exp2_fast(mine - at);
             top = most;
         }
     }
@@ -774,9 +778,10 @@ __global__ void __launch_bounds__(1024) k_loss_merge(const __grid_constant__ Mer
         } else {
             const int64_t id = id_at(g.ids, g.wide, token);
             // the loss of a token that is sure is far smaller than its logits: not by way of lse
+            constexpr float kLn2 = 0.6931471805599453f;
             const float tail = *g.status ? __int_as_float(0x7FC00000) : logf(s);
-            const float l = id < 0 ? 0.0f : id >= g.vocab ? __int_as_float(0x7FC00000) : (m - g.mine[token]) + tail;
-            g.lse[token] = m + tail;
+            const float l = id < 0 ? 0.0f : id >= g.vocab ? __int_as_float(0x7FC00000) : fmaf(m - g.mine[token], kLn2, tail);
+            g.lse[token] = fmaf(m, kLn2, tail);
             g.loss[token] = l;
             loss = l;
             counted = id >= 0;
@@ -927,9 +932,9 @@ cudaError_t pairs_at_once(int *pairs)
     if (rc != cudaSuccess) return rc;
     const int at = device & 63;
     if (!known[at]) {
-        rc = cudaFuncSetAttribute(dev::k_product<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dev::Shape<OP>::kBytes);
+        rc = cudaFuncSetAttribute(dev::k_product<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dev::kProductBytes);
         if (rc != cudaSuccess) return rc;
-        const int n = static_cast<int>(clusters_at_once(dev::k_product<OP>, dev::Shape<OP>::kThreads, dev::Shape<OP>::kBytes, 2));
+        const int n = static_cast<int>(clusters_at_once(dev::k_product<OP>, dev::kProductThreads, dev::kProductBytes, 2));
         if (n <= 0) return cudaErrorInvalidConfiguration;
         known[at] = n;
     }
@@ -947,7 +952,7 @@ cudaError_t product(const ProductArgs &g, const ProductMaps &maps, cudaStream_t 
                           g.splits;
     if (items == 0) return cudaSuccess;
     return launch<true>(dev::k_product<OP>, dim3(2 * static_cast<uint32_t>(std::min<int64_t>(items, pairs))),
-                        dev::Shape<OP>::kThreads, dev::Shape<OP>::kBytes, 2, s, g, maps);
+                        dev::kProductThreads, dev::kProductBytes, 2, s, g, maps);
 }
 
 // Whether a forward pass is one of few tokens: x fits beside another block's.
@@ -972,9 +977,10 @@ cudaError_t few(const ProductArgs &g, const FewArgs &f, bool aligned, cudaStream
 }
 
 // Tensor cores' float32 sums drop what does not fit, always towards zero: over a depth of 4096 a logit of 12 comes out 3e-5
-// too small, and the loss of a token that is sure is wrong by that share.  So each 512 of depth are added to the rest in
-// registers (7e-6; 2 to 3% longer.  256: a quarter longer).
-constexpr int kSumDepth = 512;
+// too small, and the loss of a token that is sure is wrong by that share.  So the sums of every 1024 of depth are added to the
+// rest in registers (the losses of 8192 tokens then are as far from 64 bits as those of float32 products, 6e-7 of their norm),
+// of every 512 where tokens are few: there it costs nothing, with many 3 to 4%.  (256: a quarter longer.)
+uint32_t sum_steps(uint64_t tokens) { return (tokens > 1024 ? 1024 : 512) / dev::kDepth; }
 
 // Rows of A's boxes.  Of few tokens no more is fetched than there is (rows behind them reach only themselves).
 uint32_t a_rows(uint64_t tokens) { return tokens <= 8 ? 8 : tokens <= 32 ? 32 : dev::kHalfTile; }
@@ -1190,7 +1196,7 @@ lct_status forward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, u
             } else {
                 ProductMaps maps{};
                 g.a_rows = a_rows(tn);
-                g.sum_steps = kSumDepth / dev::kDepth;
+                g.sum_steps = static_cast<int32_t>(sum_steps(t));
                 if (!box_map(&maps.a, xp + t0 * ldx, cols, tn, ldx, 0, g.a_rows) ||
                     !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kHalfTile) || product<kLogits>(g, maps, s) != cudaSuccess)
                     return LCT_ERR_CUDA;
