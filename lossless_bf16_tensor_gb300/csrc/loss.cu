@@ -229,10 +229,11 @@ __device__ __forceinline__ float exp2_fast(float x)
 __device__ __forceinline__ int parts_of(int tiles, int depth, int most, int pairs)
 {
     int best = 1;
-    int64_t least = INT64_MAX;
-    for (int s = 1; s <= most && s <= max(1, depth / 4); ++s) {
-        const int64_t cost = 10 * ((static_cast<int64_t>(tiles) * s + pairs - 1) / pairs * ((depth + s - 1) / s + 6)) + 3ll * s * tiles;
-        if (cost < least) least = cost, best = s;
+    uint64_t least = ~0ull;
+    for (uint32_t s = 1; s <= static_cast<uint32_t>(most) && s <= static_cast<uint32_t>(max(1, depth / 4)); ++s) {
+        const uint32_t rounds = (tiles * s + pairs - 1) / pairs, steps = (depth + s - 1) / s;
+        const uint64_t cost = 10ull * rounds * (steps + 6) + 3ull * s * tiles;
+        if (cost < least) least = cost, best = static_cast<int>(s);
     }
     return best;
 }
@@ -753,25 +754,33 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_logits_few(const __grid_cons
 // order of the blocks) is made by the last block to come.
 __global__ void __launch_bounds__(1024) k_loss_merge(const __grid_constant__ MergeArgs g)
 {
-    __shared__ float2 joined[kMergeGroups][kMergeTokens];
+    __shared__ float2 joined[kMergeGroups][kMergeTokens + 1];
     __shared__ double sums[32];
     __shared__ int counts[32];
     __shared__ bool is_last;
     const int lane = threadIdx.x & 31, group = threadIdx.x / 32;
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * kMergeTokens + lane;
+    const int64_t token0 = static_cast<int64_t>(blockIdx.x) * kMergeTokens;
     pdl_wait();
     pdl_launch_dependents();
     float m = -INFINITY, s = 0.0f;
-    if (token < g.tokens) {
+    if (token0 + lane < g.tokens) {
 #pragma unroll 4
-        for (int i = group; i < g.slots; i += kMergeGroups) join(m, s, g.part[static_cast<int64_t>(i) * g.tokens + token]);
+        for (int i = group; i < g.slots; i += kMergeGroups) join(m, s, g.part[static_cast<int64_t>(i) * g.tokens + token0 + lane]);
     }
     joined[group][lane] = make_float2(m, s);
     __syncthreads();
+    // each warp joins the groups of one token
+    const int64_t token = token0 + group;
+    const float2 mine = joined[lane][group];
+    m = mine.x, s = mine.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float2 other = make_float2(__shfl_xor_sync(kFull, m, o), __shfl_xor_sync(kFull, s, o));
+        join(m, s, other);
+    }
     double loss = 0.0;
     int counted = 0;
-    if (group == 0 && token < g.tokens) {
-        for (int i = 1; i < kMergeGroups; ++i) join(m, s, joined[i][lane]);
+    if (lane == 0 && token < g.tokens) {
         if (!g.begins) join(m, s, g.state[token]);
         if (!g.ends) {
             g.state[token] = make_float2(m, s);
@@ -788,7 +797,11 @@ __global__ void __launch_bounds__(1024) k_loss_merge(const __grid_constant__ Mer
         }
     }
     if (!g.ends || !g.total) return;
+    if (lane == 0) sums[group] = loss, counts[group] = counted;
+    __syncthreads();
     if (group == 0) {
+        loss = sums[lane];
+        counted = counts[lane];
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             loss += __shfl_xor_sync(kFull, loss, o);
@@ -833,7 +846,7 @@ __global__ void __launch_bounds__(1024) k_loss_merge(const __grid_constant__ Mer
 // Row i of dst is row order[i] of src (NULL: row i), for the tokens that are
 // there; rows behind them, as far as a step of depth reaches, are zero.  With
 // order, also what the tokens' ends need.
-constexpr int kPackRows = 4;  // a block's, asked for together
+constexpr int kPackRows = 4;  // a block's, asked for together (every block has a warp at least)
 template <bool AL>
 __global__ void __launch_bounds__(kRowThreads) k_loss_pack(const __grid_constant__ PackArgs g)
 {
@@ -841,29 +854,30 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_pack(const __grid_constant
     pdl_launch_dependents();
     const int i0 = blockIdx.x * kPackRows, piece = piece_of<__nv_bfloat16>(blockIdx.y);
     const int count = g.count ? *g.count : g.rows;
+    int64_t token[kPackRows];
+#pragma unroll
+    for (int r = 0; r < kPackRows; ++r) token[r] = g.order && i0 + r < g.rows ? g.order[i0 + r] : i0 + r;
     const int end = min(g.rows, count + 63);  // (rows behind the last are nobody's, and boxes fill them with zeros)
     Piece<__nv_bfloat16, AL> p[kPackRows];
     const bool inside = !AL && piece + 8 <= g.cols && i0 + kPackRows <= count;  // whole pieces of all rows: no branch between
     if (inside) {
 #pragma unroll
-        for (int r = 0; r < kPackRows; ++r) {
-            const int64_t token = g.order ? g.order[i0 + r] : i0 + r;
-            p[r].q = load_any(g.src + token * g.ld_src + piece, 16);
-        }
+        for (int r = 0; r < kPackRows; ++r) p[r].q = load_any(g.src + token[r] * g.ld_src + piece, 16);
     }
 #pragma unroll
     for (int r = 0; r < kPackRows; ++r) {
         const int i = i0 + r;
         if (!inside) p[r].q = make_uint4(0, 0, 0, 0);
         if (i >= count) continue;
-        const int64_t token = g.order ? g.order[i] : i;
-        if (!inside) p[r].load(g.src + token * g.ld_src, piece, g.cols);
-        if (g.order && piece == 0) {
-            const float c = g.dloss[token * g.dloss_stride] * (g.scale ? *g.scale : 1.0f);
-            g.lse_out[i] = g.lse[token];
-            g.share_out[i] = c;
-            g.coef_out[i] = c * expm1f(-g.loss[token]);
-        }
+        if (!inside) p[r].load(g.src + token[r] * g.ld_src, piece, g.cols);
+    }
+    if (g.order && piece < kPackRows * 8 && i0 + piece / 8 < count) {  // the first threads: what goes with a row
+        const int r = piece / 8;
+        const int64_t t = r == 0 ? token[0] : r == 1 ? token[1] : r == 2 ? token[2] : token[3];
+        const float c = g.dloss[t * g.dloss_stride] * (g.scale ? *g.scale : 1.0f);
+        g.lse_out[i0 + r] = g.lse[t];
+        g.share_out[i0 + r] = c;
+        g.coef_out[i0 + r] = c * expm1f(-g.loss[t]);
     }
 #pragma unroll
     for (int r = 0; r < kPackRows; ++r)
@@ -873,49 +887,74 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_pack(const __grid_constant
 
 // dx of token order[i]: the parts' sum, and the target's term.  Tokens without a
 // target get zeros, those with an impossible one NaN.
+constexpr int kFinishRows = 2;  // a block's, asked for together
 template <bool AL>
 __global__ void __launch_bounds__(kRowThreads) k_loss_finish(const __grid_constant__ FinishArgs g)
 {
+    using T = __nv_bfloat16;
+    constexpr int R = kFinishRows;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t i = blockIdx.x, token = g.order[i];
-    __nv_bfloat16 *dx = g.dx + token * g.ld_dx;
-    const int c = piece_of<__nv_bfloat16>(blockIdx.y) - skip_of_row<__nv_bfloat16, AL>(dx);
-    if (c >= g.cols) return;
-    Piece<__nv_bfloat16, AL> p;
-    float acc[kVec<__nv_bfloat16>];
+    const int i0 = blockIdx.x * R, piece = piece_of<T>(blockIdx.y), count = *g.count, status = *g.status;
+    int token[R], key[R];
+    float coef[R];
 #pragma unroll
-    for (int e = 0; e < kVec<__nv_bfloat16>; ++e) acc[e] = 0.0f;
-    if (*g.status) {
+    for (int r = 0; r < R; ++r) {
+        const int i = min(i0 + r, static_cast<int>(g.tokens) - 1);
+        token[r] = g.order[i];
+        key[r] = g.key[i];
+        coef[r] = g.coef[i];
+    }
+    const int parts = g.splits > 1 ? parts_of((count + kTile - 1) / kTile * ((g.cols + kTile - 1) / kTile), g.depth, g.splits,
+                                              g.pairs)
+                                   : 1;
+    T *dx[R];
+    int c[R];
+    bool there[R];
+    Piece<T, AL> w[R];
+    float acc[R][kVec<T>];
 #pragma unroll
-        for (int e = 0; e < kVec<__nv_bfloat16>; ++e) acc[e] = __int_as_float(0x7FC00000);
-    } else if (i < *g.count) {
-        const float f = g.coef[i];
-        p.load(g.w + (g.gathered ? i : static_cast<int64_t>(g.key[i])) * g.ld_w, c, g.cols);
-        const int parts = g.splits > 1 ? parts_of((*g.count + kTile - 1) / kTile * ((g.cols + kTile - 1) / kTile), g.depth,
-                                                  g.splits, g.pairs)
-                                       : 1;
-        for (int s = 0; s < parts; ++s) {
-            const float *part = g.part + (s * g.tokens + i) * g.ld_part;
-            float v[kVec<__nv_bfloat16>];
-            if (AL) {
-                load_floats<__nv_bfloat16>(v, part, c);
-            } else {
+    for (int r = 0; r < R; ++r) {
+        dx[r] = g.dx + token[r] * g.ld_dx;
+        c[r] = piece - skip_of_row<T, AL>(dx[r]);
+        there[r] = i0 + r < count && c[r] < g.cols;
+        if (there[r]) w[r].load(g.w + (g.gathered ? i0 + r : key[r]) * g.ld_w, c[r], g.cols);
+    }
+    auto load_part = [&](float(&v)[kVec<T>], int part, int r) {
+        const float *from = g.part + (part * g.tokens + i0 + r) * g.ld_part;
+        if (AL) {
+            load_floats<T>(v, from, c[r]);
+        } else {
 #pragma unroll
-                for (int e = 0; e < kVec<__nv_bfloat16>; ++e) v[e] = c + e >= 0 && c + e < g.cols ? part[c + e] : 0.0f;
+            for (int e = 0; e < kVec<T>; ++e) v[e] = c[r] + e >= 0 && c[r] + e < g.cols ? from[c[r] + e] : 0.0f;
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (there[r]) load_part(acc[r], 0, r);
+    for (int p = 1; p < parts; ++p)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (there[r]) {
+                float v[kVec<T>];
+                load_part(v, p, r);
+#pragma unroll
+                for (int e = 0; e < kVec<T>; ++e) acc[r][e] += v[e];
             }
 #pragma unroll
-            for (int e = 0; e < kVec<__nv_bfloat16>; ++e) acc[e] += v[e];
+    for (int r = 0; r < R; ++r) {
+        if (i0 + r >= g.tokens || c[r] >= g.cols) continue;
+        Piece<T, AL> out;
+        if (there[r] && !status) {
+#pragma unroll
+            for (int e = 0; e < kVec<T>; ++e) out.v[e] = __float2bfloat16_rn(fmaf(coef[r], to_float(w[r].v[e]), acc[r][e]));
+        } else {
+            const bool wrong = status || id_at(g.ids, g.wide, token[r]) >= 0;
+#pragma unroll
+            for (int e = 0; e < kVec<T>; ++e) out.v[e] = __float2bfloat16_rn(wrong ? __int_as_float(0x7FC00000) : 0.0f);
         }
-#pragma unroll
-        for (int e = 0; e < kVec<__nv_bfloat16>; ++e) acc[e] = fmaf(f, to_float(p.v[e]), acc[e]);
-    } else if (id_at(g.ids, g.wide, token) >= 0) {
-#pragma unroll
-        for (int e = 0; e < kVec<__nv_bfloat16>; ++e) acc[e] = __int_as_float(0x7FC00000);
+        out.store(dx[r], c[r], g.cols);
     }
-#pragma unroll
-    for (int e = 0; e < kVec<__nv_bfloat16>; ++e) p.v[e] = __float2bfloat16_rn(acc[e]);
-    p.store(dx, c, g.cols);
 }
 
 }  // namespace dev
@@ -1427,8 +1466,9 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
     const bool al = cols % 8 == 0 && matrix_al(dx) && (pieces || matrix_al(w));
     uint32_t threads, slabs;
     row_shape(k, 8, al, &threads, &slabs);
-    const cudaError_t rc = al ? launch<true>(dev::k_loss_finish<true>, dim3(tokens, slabs), threads, 0, 1, s, f)
-                              : launch<true>(dev::k_loss_finish<false>, dim3(tokens, slabs), threads, 0, 1, s, f);
+    const dim3 grid((tokens + dev::kFinishRows - 1) / dev::kFinishRows, slabs);
+    const cudaError_t rc = al ? launch<true>(dev::k_loss_finish<true>, grid, threads, 0, 1, s, f)
+                              : launch<true>(dev::k_loss_finish<false>, grid, threads, 0, 1, s, f);
     return rc == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
 }
 
