@@ -342,10 +342,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     Items items(g, m, k);
     Item w;
     Waiter waiter;
-    auto wait = [&](uint64_t *bar, int parity) { waiter.wait_cluster(bar, parity); };
+    // Barriers tell of boxes, products and reads of TMEM that are done, and of no ordinary write: waits order nothing beyond
+    // the block, and arrivals at a peer's barrier nothing at all (a release would wait for the results on their way to memory).
+    auto wait = [&](uint64_t *bar, int parity) { waiter.wait(bar, parity); };
     // where the lanes have to give up together (a vote a step would cost the product's warp 3%)
     auto wait_all = [&](uint64_t *bar, int parity) {
-        waiter.wait_cluster(bar, parity);
+        waiter.wait(bar, parity);
         waiter.dead = __any_sync(kFull, waiter.dead);
     };
 
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             tc_before();
             __syncwarp();
             if (lane == 0)
-                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                                  peer_addr(smem_addr(&drained[t & 1]), 0))
                              : "memory");
         };
