@@ -226,16 +226,18 @@ __device__ __forceinline__ float exp2_fast(float x)
 // pair: tiles go round in turns, in each of which a tile's result takes about
 // six, and what every part has to write and k_loss_finish to read takes 0.3 for
 // each tile.
-__device__ __forceinline__ int parts_of(int tiles, int depth, int most, int pairs)
+__device__ __forceinline__ int parts_of(int tiles, int depth, int most, int pairs)  // by a whole warp
 {
-    int best = 1;
-    uint64_t least = ~0ull;
-    for (uint32_t s = 1; s <= static_cast<uint32_t>(most) && s <= static_cast<uint32_t>(max(1, depth / 4)); ++s) {
+    const uint32_t end = static_cast<uint32_t>(max(1, min(most, depth / 4)));
+    uint64_t best = ~0ull;
+    for (uint32_t s = (threadIdx.x & 31) + 1; s <= end; s += 32) {
         const uint32_t rounds = (tiles * s + pairs - 1) / pairs, steps = (depth + s - 1) / s;
         const uint64_t cost = 10ull * rounds * (steps + 6) + 3ull * s * tiles;
-        if (cost < least) least = cost, best = static_cast<int>(s);
+        best = min(best, cost << 8 | s);  // the fewest of the cheapest
     }
-    return best;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) best = min(best, __shfl_xor_sync(kFull, best, o));
+    return static_cast<int>(best & 255);
 }
 
 // An item of work: a tile, and the steps of depth that it takes.
@@ -890,7 +892,7 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_pack(const __grid_constant
 // dx of token order[i]: the parts' sum, and the target's term.  Tokens without a
 // target get zeros, those with an impossible one NaN.
 constexpr int kFinishRows = 2;  // a block's, asked for together
-template <bool AL>
+template <bool AL, bool PARTS>
 __global__ void __launch_bounds__(kRowThreads) k_loss_finish(const __grid_constant__ FinishArgs g)
 {
     using T = __nv_bfloat16;
@@ -907,9 +909,8 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_finish(const __grid_consta
         key[r] = g.key[i];
         coef[r] = g.coef[i];
     }
-    const int parts = g.splits > 1 ? parts_of((count + kTile - 1) / kTile * ((g.cols + kTile - 1) / kTile), g.depth, g.splits,
-                                              g.pairs)
-                                   : 1;
+    const int parts = PARTS ? parts_of((count + kTile - 1) / kTile * ((g.cols + kTile - 1) / kTile), g.depth, g.splits, g.pairs)
+                            : 1;
     T *dx[R];
     int c[R];
     bool there[R];
@@ -934,15 +935,23 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_finish(const __grid_consta
 #pragma unroll
     for (int r = 0; r < R; ++r)
         if (there[r]) load_part(acc[r], 0, r);
-    for (int p = 1; p < parts; ++p)
+    constexpr int kAhead = 4;  // parts asked for together
+    for (int p0 = 1; p0 < parts; p0 += kAhead) {
+        float v[kAhead][R][kVec<T>];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (there[r]) {
-                float v[kVec<T>];
-                load_part(v, p, r);
+        for (int p = 0; p < kAhead; ++p)
 #pragma unroll
-                for (int e = 0; e < kVec<T>; ++e) acc[r][e] += v[e];
-            }
+            for (int r = 0; r < R; ++r)
+                if (there[r] && p0 + p < parts) load_part(v[p][r], p0 + p, r);
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (there[r] && p0 + p < parts) {
+#pragma unroll
+                    for (int e = 0; e < kVec<T>; ++e) acc[r][e] += v[p][r][e];
+                }
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         if (i0 + r >= g.tokens || c[r] >= g.cols) continue;
@@ -1048,7 +1057,7 @@ uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 int dx_splits(uint64_t tokens, uint64_t cols)
 {
     const uint64_t room = (1ull << 28) / std::max<uint64_t>(1, 4 * tokens * up(cols, 8));
-    return static_cast<int>(std::max<uint64_t>(1, std::min<uint64_t>(16, room)));
+    return static_cast<int>(std::max<uint64_t>(1, std::min<uint64_t>(64, room)));
 }
 
 // Where things are in d_work.  What lives from piece to piece comes first, and
@@ -1469,8 +1478,9 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
     uint32_t threads, slabs;
     row_shape(k, 8, al, &threads, &slabs);
     const dim3 grid((tokens + dev::kFinishRows - 1) / dev::kFinishRows, slabs);
-    const cudaError_t rc = al ? launch<true>(dev::k_loss_finish<true>, grid, threads, 0, 1, s, f)
-                              : launch<true>(dev::k_loss_finish<false>, grid, threads, 0, 1, s, f);
+    const auto kernel = f.splits > 1 ? (al ? dev::k_loss_finish<true, true> : dev::k_loss_finish<false, true>)
+                                     : (al ? dev::k_loss_finish<true, false> : dev::k_loss_finish<false, false>);
+    const cudaError_t rc = launch<true>(kernel, grid, threads, 0, 1, s, f);
     return rc == cudaSuccess ? LCT_OK : LCT_ERR_CUDA;
 }
 
