@@ -2,7 +2,8 @@
 codec, the fused compressed SGD / SGD-with-momentum / AdamW steps, and the
 pieces built on them for training (saved activations kept compressed,
 a linear layer whose weight is decoded tile by tile, low-rank adapters beside
-it, the norm and clipping of gradients).
+it, the norm and clipping of gradients, the lookup and the loss at the two ends
+of a vocabulary's matrix).
 
 The work happens in ``liblct.so`` (CUDA kernels behind a C ABI, declared in
 ``include/lct.h``); ``binding`` is its thin ctypes binding, re-exported here:
@@ -14,7 +15,7 @@ The work happens in ``liblct.so`` (CUDA kernels behind a C ABI, declared in
                                             CompressedTensor)
 
 ``activations.compressed_activations``, ``matmul.compressed_linear``, and what
-``adapters`` and ``grads`` hold are imported from their modules.  The binding is loaded on first attribute access
+``adapters``, ``grads`` and ``vocab`` hold are imported from their modules.  The binding is loaded on first attribute access
 and raises if the library is not built; nothing falls back to the CPU.
 """
 

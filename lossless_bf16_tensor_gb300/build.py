@@ -1,5 +1,5 @@
 """Build liblct.so (the C-ABI library) for sm_103a with nvcc, and _calls.so (the
-Python entry points of its gradient and adapter calls) with the C++ compiler,
+Python entry points of its gradient, adapter and vocabulary calls) with the C++ compiler,
 in-tree.
 
 Each translation unit is compiled in parallel, then linked into one shared

@@ -1,4 +1,4 @@
-"""Loads _calls.so, the Python entry points of the gradient and adapter calls
+"""Loads _calls.so, the Python entry points of the gradient, adapter and vocabulary calls
 (``calls.cpp``).  There is no fallback: importing this fails if the library has
 not been built (``python -m lossless_bf16_tensor_gb300.build``)."""
 from __future__ import annotations

@@ -525,8 +525,8 @@ const at::Tensor &floats(const at::Tensor &t, uint64_t n, int device, const char
     return t;
 }
 
-// x [..., cols] as a matrix whose rows the kernels can read: a copy where its leading dimensions make no single row index,
-// or a row's values do not lie side by side.
+// x [..., cols], or a weight, as a matrix whose rows the kernels can read: a copy where its leading dimensions make no single
+// row index, or a row's values do not lie side by side.
 at::Tensor as_rows(const at::Tensor &x, int64_t cols)
 {
     at::Tensor r = x.dim() == 2 ? x : x.reshape({-1, cols});
@@ -668,9 +668,9 @@ struct LinearCrossEntropy : torch::autograd::Function<LinearCrossEntropy> {
     static at::Tensor forward(torch::autograd::AutogradContext *ctx, const at::Tensor &x, const at::Tensor &w,
                               const at::Tensor &targets, int64_t reduction)
     {
-        const at::Tensor rows = as_rows(x, w.size(1));
-        const Forward f = loss_forward(rows, w, targets, true);
-        ctx->save_for_backward({rows, w, targets, f.loss, f.lse, f.total});
+        const at::Tensor rows = as_rows(x, w.size(1)), weight = as_rows(w, w.size(1));
+        const Forward f = loss_forward(rows, weight, targets, true);
+        ctx->save_for_backward({rows, weight, targets, f.loss, f.lse, f.total});
         ctx->saved_data["reduction"] = reduction;
         ctx->saved_data["shape"] = x.sizes().vec();
         // (a token's losses are also saved: autograd has to be able to give the caller a tensor of its own)
@@ -724,7 +724,7 @@ PyObject *linear_cross_entropy(PyObject *const *a)
     need(w.dim() == 2 && x.dim() >= 1 && x.size(x.dim() - 1) == w.size(1), "expected x [..., columns] and weight [vocabulary, columns]");
     if (at::GradMode::is_enabled() && (x.requires_grad() || w.requires_grad()))
         return THPVariable_Wrap(LinearCrossEntropy::apply(x, w, targets, static_cast<int64_t>(reduction)));
-    return THPVariable_Wrap(reduced(loss_forward(as_rows(x, w.size(1)), w, targets, true), reduction));
+    return THPVariable_Wrap(reduced(loss_forward(as_rows(x, w.size(1)), as_rows(w, w.size(1)), targets, true), reduction));
 }
 
 // (x, piece, first, vocab, targets, loss, lse, dloss, scale or None, dx, dw's piece or None, work) -> None

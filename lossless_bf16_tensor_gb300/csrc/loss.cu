@@ -6,12 +6,14 @@
 //   g_iv = c_i (exp(z_iv - l_i) - [v = t_i]),  dx = g W,  dW = g^T x
 //
 // The four products (z, z again, g W, g^T x) are one kernel, k_product, with four
-// ends (of up to 4 tokens, z is k_logits_few's).  The first turns its tile of z into each row's maximum and sum of
-// exponentials, which k_loss_merge joins over the tiles and pieces: what leaves
-// the SMs is 16 bytes a token and tile.  The second computes z again and writes
-// g as BF16, for a part of the piece that is bounded (kGradValues), which the
-// other two read.  Tensor cores bound all of them where tokens are many; where
-// they are few, reading W from HBM does.
+// ends (of one or two tokens, z is k_logits_few's).  The first turns its tile of z into
+// each row's maximum and sum of exponentials, which k_loss_merge joins over the
+// tiles and pieces: what leaves the SMs is 8 bytes a token and 64 columns.  The
+// second computes z again and writes g as BF16, for a part of the piece that is
+// bounded (kGradValues), which the other two read.  Tensor cores bound all of them
+// where tokens are many (8192 tokens, 32,768 rows of 4096: z 1.04 ms, 2.1 PFLOP/s,
+// 97% of the tensor pipe's cycles; the gradients 3.5 ms); where they are few,
+// reading W from HBM does.
 //
 // Rounding: products take BF16 and add in float32.  g is rounded to BF16 without
 // its target's entry: that one, c_i (exp(-loss_i) - 1), is as large as all others
@@ -651,14 +653,14 @@ __device__ __forceinline__ void join(float &m, float &s, float2 o)
 
 // ------------------------------------------------------------- few tokens
 
-// Logits of up to 4 tokens, which reading W bounds (32,768 rows of 4096, with the
-// merge: 47 us for one token, 5.7 TB/s, 55 for two, 69 for four; by tiles 57 to 60.
-// Eight take 113.)  A warp takes two rows of W at a time, a lane eight columns of
-// 256; x is in shared memory.  Sums are float32 multiply-adds, rounded
-// to nearest: with one token's loss there is nothing that an error averages out
-// over, and tiles would have to add every 64 of depth in registers to be as exact,
-// which takes them three times as long.  W's rows may begin anywhere.
-constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kFewBlocks = 304, kFewMost = 4;
+// Logits of one or two tokens, which reading W bounds (32,768 rows of 4096, with
+// the merge: 46 us for one token, 5.8 TB/s, 55 for two; by tiles 52 for up to
+// 128).  A warp takes two rows of W at a time, a lane eight columns of 256; x is in
+// shared memory.  Sums are float32 multiply-adds, rounded to nearest: with a single
+// token's loss there is nothing that an error averages out over, and tiles would
+// have to add every 64 of depth in registers to be as exact, which takes them three
+// times as long.  W's rows may begin anywhere.
+constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kFewBlocks = 304, kFewMost = 2;
 
 __host__ __device__ constexpr uint32_t few_pitch(uint32_t cols) { return (cols + 255) / 256 * 512; }
 
@@ -1008,7 +1010,7 @@ cudaError_t product(const ProductArgs &g, const ProductMaps &maps, cudaStream_t 
 // Whether a forward pass is one of few tokens: x fits beside another block's.
 bool is_few(uint64_t tokens, uint64_t cols)
 {
-    const uint64_t rows = tokens <= 1 ? 1 : tokens <= 2 ? 2 : 4;
+    const uint64_t rows = tokens <= 1 ? 1 : 2;
     return tokens <= dev::kFewMost && rows * dev::few_pitch(static_cast<uint32_t>(cols)) <= 100 * 1024;
 }
 uint32_t few_blocks(uint64_t rows)
@@ -1023,7 +1025,7 @@ cudaError_t few_at(const ProductArgs &g, const FewArgs &f, bool aligned, cudaStr
 }
 cudaError_t few(const ProductArgs &g, const FewArgs &f, bool aligned, cudaStream_t s)
 {
-    return g.m <= 1 ? few_at<1>(g, f, aligned, s) : g.m <= 2 ? few_at<2>(g, f, aligned, s) : few_at<4>(g, f, aligned, s);
+    return g.m <= 1 ? few_at<1>(g, f, aligned, s) : few_at<2>(g, f, aligned, s);
 }
 
 // Tensor cores' float32 sums drop what does not fit, always towards zero: over a depth of 4096 a logit of 12 comes out 3e-5
@@ -1076,7 +1078,7 @@ struct ForwardLayout : Layout {
     uint64_t ld, chunk, piece;  // rows of packed matrices; tokens of a product; rows of W that are moved at a time
     ForwardLayout(uint64_t tokens, uint64_t cols, uint64_t rows, bool move)
     {
-        ld = up(cols, 8);
+        ld = up(cols, 64);  // whole lines of 128 bytes: boxes of others touch two
         chunk = std::min<uint64_t>(tokens, kMergeChunk);
         piece = move ? std::min(rows, std::max<uint64_t>(256, kPackValues / ld / 256 * 256)) : rows;
         const uint64_t blocks = up(tokens, dev::kMergeTokens) / dev::kMergeTokens;
@@ -1093,11 +1095,12 @@ struct ForwardLayout : Layout {
 };
 struct BackwardLayout : Layout {
     uint64_t head, key[2], order[2], first, lse, share, coef, x, extra, part, target, g, sums, w;
-    uint64_t ld, piece, ld_g;
+    uint64_t ld, ldf, piece, ld_g;  // rows of packed BF16 and of float32 matrices, rows of W at a time, rows of g
     int splits, depth;
     BackwardLayout(uint64_t tokens, uint64_t vocab, uint64_t cols, uint64_t rows, bool weight, bool move, bool pieces)
     {
-        ld = up(cols, 8);
+        ld = up(cols, 64);
+        ldf = up(cols, 8);
         splits = dx_splits(tokens, cols);
         uint64_t most = std::max<uint64_t>(256, kGradValues / std::max<uint64_t>(1, up(tokens, 256)) / 256 * 256);
         depth = static_cast<int>(up(std::min(vocab, most), dev::kDepth) / dev::kDepth);
@@ -1114,8 +1117,8 @@ struct BackwardLayout : Layout {
         share = take(4 * tokens);
         coef = take(4 * tokens);
         x = take(2 * tokens * ld);
-        extra = take(weight ? 4 * tokens * ld : 0);
-        part = take(4 * static_cast<uint64_t>(splits) * tokens * ld);
+        extra = take(weight ? 4 * tokens * ldf : 0);
+        part = take(4 * static_cast<uint64_t>(splits) * tokens * ldf);
         target = take(pieces ? 2 * tokens * ld : 0);
         // g takes the place of the partial sums of the targets' terms, which come before it
         g = take(std::max(2 * tokens * ld_g,
@@ -1316,7 +1319,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
     int32_t *status = at<int32_t>(d_work, l.head), *count = status + 2;
     int32_t *key = at<int32_t>(d_work, l.key[0]), *order = at<int32_t>(d_work, l.order[0]);
     __nv_bfloat16 *xp = at<__nv_bfloat16>(d_work, l.x);
-    const int64_t ld = static_cast<int64_t>(l.ld);
+    const int64_t ld = static_cast<int64_t>(l.ld), ldf = static_cast<int64_t>(l.ldf);
     const int32_t tokens = static_cast<int32_t>(t), k = static_cast<int32_t>(cols);
     if (begins) {
         SortArgs o{};
@@ -1367,7 +1370,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
             e.count = count;
             e.coef = p.coef_out;
             e.out = at<float>(d_work, l.extra);
-            e.ld_out = ld;
+            e.ld_out = ldf;
             e.part = at<float>(d_work, l.g);
             e.scale = 1.0f;
             e.cols = k;
@@ -1436,7 +1439,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
         g.pairs = pairs;
         g.add = !(begins && r0 == 0);
         if (!box_map(&maps.a, gp, n, t, l.ld_g, 0, g.a_rows) || !box_map(&maps.b, wp, cols, n, ldw, 0, dev::kDepth) ||
-            !box_map32(&maps.c, at<float>(d_work, l.part), cols, t, l.ld, l.splits) ||
+            !box_map32(&maps.c, at<float>(d_work, l.part), cols, t, l.ldf, l.splits) ||
             product<kDx>(g, maps, s) != cudaSuccess)
             return LCT_ERR_CUDA;
         if (!d_dw) continue;
@@ -1445,7 +1448,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
         g.splits = 1;
         g.extra = at<float>(d_work, l.extra);
         g.first = at<int32_t>(d_work, l.first);
-        g.ld_extra = ld;
+        g.ld_extra = ldf;
         g.out = bf16(d_dw) + r0 * ld_dw;
         g.ld_out = static_cast<int64_t>(ld_dw);
         g.boxes = dw_boxes;
@@ -1456,7 +1459,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
     if (!ends) return LCT_OK;
     FinishArgs f{};
     f.part = at<float>(d_work, l.part);
-    f.ld_part = ld;
+    f.ld_part = ldf;
     f.tokens = static_cast<int64_t>(t);
     f.splits = l.splits;
     f.depth = l.depth;

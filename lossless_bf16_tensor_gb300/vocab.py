@@ -67,6 +67,8 @@ def embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, rows: int, scale: flo
 def _rows(x, k):
     """x [..., k] as a matrix whose rows the kernels can read: a copy where its leading dimensions make no single row
     index, or a row's values do not lie side by side."""
+    if x.dim() == 0 or x.shape[-1] != k:
+        raise ValueError("expected x [..., %d]" % k)
     rows = x.reshape(-1, k)
     return rows if rows.stride(1) == 1 and rows.stride(0) >= k else rows.contiguous()
 

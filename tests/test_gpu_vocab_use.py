@@ -87,6 +87,38 @@ def test_loss_gradients_against_differences(vocab):
         assert abs(float((got.double() * d).sum()) - want) <= 6 * float((off * d).norm()) + 1e-9
 
 
+def test_operands_at_any_strides(vocab):
+    x, w, ids, _ = loss_case(60, 50, 64, 0.1, seed=31)
+    want_x, want_w = x.clone().requires_grad_(True), w.clone().requires_grad_(True)
+    want = vocab.linear_cross_entropy(want_x, want_w, ids)
+    grads = torch.autograd.grad(want, (want_x, want_w))
+    leaf, weight = x.t().contiguous().requires_grad_(True), w.t().contiguous().requires_grad_(True)
+    wide = torch.stack([ids, ids], 1)
+    loss = vocab.linear_cross_entropy(leaf.t(), weight.t(), wide[:, 0])
+    assert torch.equal(loss.detach(), want.detach())
+    got = torch.autograd.grad(loss, (leaf, weight))
+    assert torch.equal(got[0].t(), grads[0]) and torch.equal(got[1].t(), grads[1])
+    one = x[:1].expand(60, 64).clone()
+    rows = x[:1].expand(60, 64)                       # one row in memory
+    assert torch.equal(vocab.linear_cross_entropy(rows, w, ids), vocab.linear_cross_entropy(one, w, ids))
+
+
+def test_saved_tensors_go_through_hooks(vocab):
+    """What the loss saves for backward is kept compressed like any other saved tensor; a parameter is not copied."""
+    from lossless_bf16_tensor_gb300 import binding as B
+    from lossless_bf16_tensor_gb300.activations import compressed_activations
+    x, w, ids, _ = loss_case(600, 300, 256, 0.1, seed=32)
+    leaf, weight = x.clone().requires_grad_(True), torch.nn.Parameter(w.clone())
+    h = leaf * 1.5
+    want = torch.autograd.grad(vocab.linear_cross_entropy(h, weight, ids), (leaf, weight), retain_graph=True)
+    with compressed_activations(B.lct_codebook_build("gaussian", 2.0)) as kept:
+        loss = vocab.linear_cross_entropy(h, weight, ids)
+    kept.flush()
+    assert kept.stats["compressed"] == 1 and kept.stats["fallback"] == 0
+    got = torch.autograd.grad(loss, (leaf, weight))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_second_derivatives_raise(vocab):
     x, w, ids, _ = loss_case(20, 30, 16, seed=5)
     leaf, weight = x.clone().requires_grad_(True), w.clone().requires_grad_(True)
@@ -275,6 +307,10 @@ def test_compressed_lookup(vocab, rows, cols, tile):
     want = (table.float() * 3.5).to(BF16)[ids.clamp(min=0)]
     want[ids < 0] = 0
     assert torch.equal(vocab.compressed_embedding(ids, ct, cb, rows, cols, 3.5, tile_blocks=tile), want)
+    for call in (lambda: vocab.compressed_embedding(ids, ct, cb, rows + 1, cols),
+                 lambda: vocab.compressed_cross_entropy(table[:333], ct, cb, rows, 2 * cols, ids.view(-1))):
+        with pytest.raises(ValueError):
+            call()
     bad = torch.tensor([rows, -1, rows - 1], device="cuda", dtype=torch.int32)
     got = vocab.compressed_embedding(bad, ct, cb, rows, cols, tile_blocks=tile)
     assert got[0].isnan().all() and not got[1].any() and torch.equal(got[2], table[-1])
