@@ -1055,10 +1055,10 @@ constexpr int64_t kMergeChunk = 32768;        // tokens of one product of the fo
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
 // Parts of the depth of dx's product, at most, so that few tokens still give every pair work (parts_of chooses): within
-// 256 MB.
+// 128 MB.
 int dx_splits(uint64_t tokens, uint64_t cols)
 {
-    const uint64_t room = (1ull << 28) / std::max<uint64_t>(1, 4 * tokens * up(cols, 8));
+    const uint64_t room = (1ull << 27) / std::max<uint64_t>(1, 4 * tokens * up(cols, 8));
     return static_cast<int>(std::max<uint64_t>(1, std::min<uint64_t>(64, room)));
 }
 
@@ -1197,7 +1197,7 @@ lct_status forward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, u
     }
     const __nv_bfloat16 *xp = bf16(d_x);
     uint64_t ldx = ld_x;
-    if (move) {
+    if (move && !matrix_al(x)) {
         xp = at<__nv_bfloat16>(d_work, l.x);
         ldx = l.ld;
         if (begins) {
@@ -1215,7 +1215,7 @@ lct_status forward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, u
         const uint64_t n = std::min(l.piece, rows - r0);
         const __nv_bfloat16 *wp = bf16(d_w) + r0 * ld_w;
         uint64_t ldw = ld_w;
-        if (move) {
+        if (move && !matrix_al(w)) {
             PackArgs p{};
             p.src = wp;
             p.ld_src = static_cast<int64_t>(ld_w);
@@ -1401,7 +1401,7 @@ lct_status backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, 
         const uint64_t n = std::min(l.piece, rows - r0);
         const __nv_bfloat16 *wp = bf16(d_w) + r0 * ld_w;
         uint64_t ldw = ld_w;
-        if (move) {
+        if (!matrix_al(w)) {
             PackArgs p{};
             p.src = wp;
             p.ld_src = static_cast<int64_t>(ld_w);
