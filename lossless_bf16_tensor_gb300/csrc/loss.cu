@@ -1055,10 +1055,10 @@ constexpr int64_t kMergeChunk = 32768;        // tokens of one product of the fo
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
 // Parts of the depth of dx's product, at most, so that few tokens still give every pair work (parts_of chooses): within
-// 128 MB.
+// 256 MB.
 int dx_splits(uint64_t tokens, uint64_t cols)
 {
-    const uint64_t room = (1ull << 27) / std::max<uint64_t>(1, 4 * tokens * up(cols, 8));
+    const uint64_t room = (1ull << 28) / std::max<uint64_t>(1, 4 * tokens * up(cols, 8));
     return static_cast<int>(std::max<uint64_t>(1, std::min<uint64_t>(64, room)));
 }
 
