@@ -5,8 +5,8 @@
 //
 // Both move rows and compute next to nothing: HBM bounds them (a lookup of 16,384
 // rows of 8 KB by frequent ids takes 32 us, 8.5 TB/s with what L2 gives again; the
-// gradient of the same batch in a table of 131,072 rows 187 us, 97% of what its
-// 1.2 GB take at a copy's rate).  The gradient reads dy once, in the order of the
+// gradient of the same batch in a table of 131,072 rows 182 us, what its 1.2 GB
+// take at a copy's rate).  The gradient reads dy once, in the order of the
 // ids, which are sorted first, and writes every row of dE once: sums are held in
 // float32 registers, in the tokens' order, so that no atomics are needed and the
 // same inputs give the same bits.  Frequent ids would make one block add thousands
@@ -552,17 +552,24 @@ cudaError_t segments(SegmentArgs g, cudaStream_t s)
     g.chunk = static_cast<int32_t>(LCT_EMBEDDING_CHUNK(static_cast<uint64_t>(g.tokens)));
     g.chunks = (static_cast<uint32_t>(g.tokens) + g.chunk - 1) / g.chunk;
     uint64_t fills = 0;
-    if (g.fill.out) {  // about 64 KB a block
-        g.fill_rows = static_cast<int32_t>(
-            std::min<int64_t>(dev::kFillRows, std::max<int64_t>(threads / 32, 65536 / g.fill.bytes)));
-        fills = (static_cast<uint64_t>(g.fill.rows - g.fill.early) + g.fill_rows - 1) / g.fill_rows;
+    const uint32_t row_threads = threads;
+    const int64_t rest = g.fill.out ? g.fill.rows - g.fill.early : 0;
+    if (rest) {
+        // The blocks that fill have the threads of the others, 256 bytes each: at least four warps, as short rows' single
+        // one with 64 KB takes 37 us for 131,072 rows of 128 bytes (12), 240 us for a million of 512 (134).  Eight
+        // warps are no faster where tokens are few and leave less room for sums where they are many (20,000 in a million rows
+        // of 126 bytes: 89 us, with four 84).
+        threads = std::max<uint32_t>(threads, 128);
+        g.fill_rows = static_cast<int32_t>(std::min<int64_t>(
+            dev::kFillRows, std::max<int64_t>(threads / 32, 256 * static_cast<int64_t>(threads) / g.fill.bytes)));
+        fills = (static_cast<uint64_t>(rest) + g.fill_rows - 1) / g.fill_rows;
     }
     if (!g.chunks && !fills) return cudaSuccess;
     const dim3 grid(static_cast<uint32_t>(g.chunks * g.slabs + fills));
     cudaError_t rc = g.base ? launch<true>(dev::k_segments<T, AL, true>, grid, threads, 0, 1, s, g)
                             : launch<true>(dev::k_segments<T, AL, false>, grid, threads, 0, 1, s, g);
     if (rc == cudaSuccess && g.chunks > 1)
-        rc = launch<true>(dev::k_segment_ends<T, AL>, dim3((g.chunks - 1) * g.slabs), threads, 0, 1, s, g);
+        rc = launch<true>(dev::k_segment_ends<T, AL>, dim3((g.chunks - 1) * g.slabs), row_threads, 0, 1, s, g);
     return rc;
 }
 
@@ -592,8 +599,9 @@ lct_status check_ids(const lct_ids *ids)
 
 namespace {
 
-// Bytes of rows that are written while ids are sorted, by the two ways of that (about 8 and 20 us; none: 218 us where
-// 16,384 tokens of 8 KB take 207, 160 MB: 210).
+// Bytes of rows that are written while ids are sorted, by the two ways of that (about 8 and 20 us).  Long batches: none
+// makes 16,384 tokens of 8 KB 195 us, 160 MB 184, this 182.  Short ones: a table that is written whole here needs no more
+// blocks (5000 tokens, 10,007 rows of 32 bytes: 20 us, none: 24); of larger ones it changes 1 to 2 us, either way.
 constexpr int64_t kFillShort = 12 << 20, kFillLong = 100 << 20;
 
 uint64_t value_bytes(int32_t dtype) { return dtype == LCT_DTYPE_F32 ? 4 : 2; }

@@ -11,8 +11,8 @@
 // tiles and pieces: what leaves the SMs is 8 bytes a token and 64 columns.  The
 // second computes z again and writes g as BF16, for a part of the piece that is
 // bounded (kGradValues), which the other two read.  Tensor cores bound all of them
-// where tokens are many (8192 tokens, 32,768 rows of 4096: z 1.04 ms, 2.1 PFLOP/s,
-// 97% of the tensor pipe's cycles; the gradients 3.5 ms); where they are few,
+// where tokens are many (8192 tokens, 32,768 rows of 4096: z 1.1 ms, 2.0 PFLOP/s,
+// 98% of the tensor pipe's cycles; the gradients 3.6 to 3.8 ms); where they are few,
 // reading W from HBM does.
 //
 // Rounding: products take BF16 and add in float32.  g is rounded to BF16 without
@@ -654,7 +654,7 @@ __device__ __forceinline__ void join(float &m, float &s, float2 o)
 // ------------------------------------------------------------- few tokens
 
 // Logits of one or two tokens, which reading W bounds (32,768 rows of 4096, with
-// the merge: 46 us for one token, 5.8 TB/s, 55 for two; by tiles 52 for up to
+// the merge: 47 us for one token, 5.7 TB/s, 55 for two; by tiles 53 to 59 for up to
 // 128).  A warp takes two rows of W at a time, a lane eight columns of 256; x is in
 // shared memory.  Sums are float32 multiply-adds, rounded to nearest: with a single
 // token's loss there is nothing that an error averages out over, and tiles would
@@ -1028,10 +1028,10 @@ cudaError_t few(const ProductArgs &g, const FewArgs &f, bool aligned, cudaStream
     return g.m <= 1 ? few_at<1>(g, f, aligned, s) : few_at<2>(g, f, aligned, s);
 }
 
-// Tensor cores' float32 sums drop what does not fit, always towards zero: over a depth of 4096 a logit of 12 comes out 3e-5
-// too small, and the loss of a token that is sure is wrong by that share.  So the sums of every 1024 of depth are added to the
-// rest in registers (the losses of 8192 tokens then are as far from 64 bits as those of float32 products, 6e-7 of their norm),
-// of every 512 where tokens are few: there it costs nothing, with many 3 to 4%.  (256: a quarter longer.)
+// Tensor cores' float32 sums drop what does not fit, always towards zero: over a depth of 4096 a logit of 12 comes out 5e-5
+// too small, and losses of 0.03 are wrong by 4e-5 of their size.  So the sums of every 1024 of depth are added to the rest in
+// registers (1.2e-5, and 9e-6 of such losses, as float32 products have), of every 512 where tokens are few (6e-6, 4e-6): there
+// it costs nothing, with many up to 3%.  (256: 4 to 8%.)
 uint32_t sum_steps(uint64_t tokens) { return (tokens > 1024 ? 1024 : 512) / dev::kDepth; }
 
 // Rows of A's boxes.  Of few tokens no more is fetched than there is (rows behind them reach only themselves).

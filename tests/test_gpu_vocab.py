@@ -105,6 +105,25 @@ def test_lookup_gradient(vocab, t, v, k, none, dtype):
             assert torch.equal(again, got)
 
 
+@pytest.mark.parametrize("t,v,k", [(3, 200_000, 40), (500, 131_072, 64), (5000, 131_072, 256), (20_000, 900_000, 63), (1, 9000, 1001)])
+def test_lookup_gradient_of_tables_too_large_to_write_while_ids_are_sorted(vocab, t, v, k):
+    """Short and long rows that are left to the blocks beside the sums."""
+    gen = generator(t + v)
+    ids = make_ids(t, v, gen, 0.1 if t > 1 else 0.0)
+    ids[0] = v - 1
+    dy = torch.randn(t, k, generator=gen, device="cuda").to(BF16)
+    base = torch.randn(v, k, generator=gen, device="cuda").to(BF16)
+    for scale, b in ((1.0, None), (-3.3, base)):
+        got = vocab.embedding_grad(dy, ids, v, scale, base=b)
+        there = torch.zeros(v, dtype=torch.bool, device="cuda")
+        there[ids[ids >= 0]] = True
+        assert torch.equal(got[~there], b[~there] if b is not None else torch.zeros_like(got[~there]))
+        rows = there.nonzero()[:, 0]
+        place = torch.where(ids < 0, -1, torch.searchsorted(rows, ids.clamp(min=0)))
+        want, off = grad_bound(dy, place, len(rows), scale, b[rows] if b is not None else None)
+        assert ((got[rows].double() - want).abs() <= off).all()
+
+
 def test_lookup_gradient_keeps_its_bits_and_what_is_around(vocab):
     gen = generator(3)
     t, v, k = 3000, 40, 96
