@@ -528,7 +528,8 @@ lct_status lct_embedding_grad(const lct_ids *ids, const void *d_dy, uint64_t ld_
 #define LCT_LOSS_UNALIGNED 4 /* a row of x or of the weight does not begin at a 16-byte boundary */
 
 /* Bytes of scratch (256-byte aligned) of the two calls below for pieces of at
- * most `rows` rows of the vocabulary: one piece (rows = vocab), or several. */
+ * most `rows` rows of the vocabulary: one piece (rows = vocab), or several.  0 for
+ * sizes that the calls refuse. */
 uint64_t lct_loss_work_bytes(uint64_t tokens, uint64_t vocab, uint64_t cols, uint64_t rows, int32_t flags);
 
 /* The cross entropy of a projection onto the vocabulary, which keeps no logits:

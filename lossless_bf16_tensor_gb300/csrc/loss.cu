@@ -1156,6 +1156,8 @@ using namespace lct;
 
 extern "C" uint64_t lct_loss_work_bytes(uint64_t tokens, uint64_t vocab, uint64_t cols, uint64_t rows, int32_t flags)
 {
+    // of what the calls refuse, nothing is worked out
+    if (!cols || cols > LCT_VOCAB_MAX_COLS || tokens > LCT_VOCAB_MAX_TOKENS || vocab > LCT_VOCAB_MAX || rows > vocab) return 0;
     const bool move = flags & LCT_LOSS_UNALIGNED;
     if (flags & LCT_LOSS_BACKWARD)
         return BackwardLayout(tokens, vocab, cols, rows, flags & LCT_LOSS_WEIGHT, move, rows < vocab).bytes;

@@ -113,6 +113,13 @@ def test_scratch_covers_every_piece(lib):
     assert lib.lct_loss_work_bytes(65_536, 262_144, 4096, 262_144, 3) < 4 << 30
 
 
+def test_scratch_of_sizes_that_are_refused(lib):
+    for t, v, k, rows in ((10, 100, 0, 100), (10, 100, 2 ** 16 + 1, 100), (10, 100, 2 ** 64 - 1, 100), (2 ** 24 + 1, 100, 8, 100),
+                          (2 ** 64 - 1, 100, 8, 100), (10, 2 ** 24 + 1, 8, 100), (10, 2 ** 64 - 1, 8, 2 ** 64 - 1), (10, 100, 8, 101)):
+        for flags in range(8):
+            assert lib.lct_loss_work_bytes(t, v, k, rows, flags) == 0
+
+
 def test_python_refusals(lct_lib):
     torch = pytest.importorskip("torch")
     from lossless_bf16_tensor_gb300 import vocab
