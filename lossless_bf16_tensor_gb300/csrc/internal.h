@@ -202,9 +202,11 @@ struct Matrix {
     uint64_t ld, cols, rows, size;
 };
 inline uint64_t matrix_bytes(const Matrix &m) { return m.rows ? m.size * ((m.rows - 1) * m.ld + m.cols) : 0; }
+// (Up to 2^24 rows: their extent is within 64 bits before it is compared.)
 inline bool matrix_ok(const Matrix &m)
 {
-    return !m.rows || (m.p && reinterpret_cast<uintptr_t>(m.p) % m.size == 0 && m.ld >= m.cols && m.ld <= kMaxN);
+    return !m.rows || (m.p && reinterpret_cast<uintptr_t>(m.p) % m.size == 0 && m.ld >= m.cols && m.ld <= kMaxN &&
+                       (m.rows - 1) * m.ld + m.cols <= kMaxN);
 }
 // Whether every row begins at a 16-byte boundary (and TMA's strides hold the distance between rows).
 inline bool matrix_al(const Matrix &m)

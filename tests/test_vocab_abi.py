@@ -113,6 +113,17 @@ def test_scratch_covers_every_piece(lib):
     assert lib.lct_loss_work_bytes(65_536, 262_144, 4096, 262_144, 3) < 4 << 30
 
 
+def test_refusals_of_extents_beyond_any_memory(lib):
+    """2^24 rows 2^40 float32 values apart: their bytes pass 64 bits, where every overlap would be missed."""
+    wide = ids(vocab=2 ** 24)
+    for ld in (2 ** 40, 2 ** 38, 2 ** 30):
+        assert lookup(lib, wide, ldt=ld, dtype=1, rows=2 ** 24) == INVALID
+        assert gradient(lib, wide, ldo=ld, dtype=1) == INVALID
+        assert gradient(lib, wide, base=B, ldb=ld, dtype=1) == INVALID
+        assert forward(lib, wide, ldw=ld, rows=2 ** 24) == INVALID
+        assert backward(lib, wide, lddw=ld, rows=2 ** 24) == INVALID
+
+
 def test_scratch_of_sizes_that_are_refused(lib):
     for t, v, k, rows in ((10, 100, 0, 100), (10, 100, 2 ** 16 + 1, 100), (10, 100, 2 ** 64 - 1, 100), (2 ** 24 + 1, 100, 8, 100),
                           (2 ** 64 - 1, 100, 8, 100), (10, 2 ** 24 + 1, 8, 100), (10, 2 ** 64 - 1, 8, 2 ** 64 - 1), (10, 100, 8, 101)):
