@@ -12,7 +12,7 @@
 // second computes z again and writes g as BF16, for a part of the piece that is
 // bounded (kGradValues), which the other two read.  Tensor cores bound all of them
 // where tokens are many (8192 tokens, 32,768 rows of 4096: z 1.1 ms, 2.0 PFLOP/s,
-// 98% of the tensor pipe's cycles; the gradients 3.6 to 3.8 ms); where they are few,
+// 97% of the tensor pipe's cycles; the gradients 3.6 to 3.8 ms); where they are few,
 // reading W from HBM does.
 //
 // Rounding: products take BF16 and add in float32.  g is rounded to BF16 without
@@ -654,8 +654,8 @@ __device__ __forceinline__ void join(float &m, float &s, float2 o)
 // ------------------------------------------------------------- few tokens
 
 // Logits of one or two tokens, which reading W bounds (32,768 rows of 4096, with
-// the merge: 47 us for one token, 5.7 TB/s, 55 for two; by tiles 53 to 59 for up to
-// 128).  A warp takes two rows of W at a time, a lane eight columns of 256; x is in
+// the merge: 47 us for one token, 5.7 TB/s, 55 for two; by tiles 53 to 62 for up to
+// 256).  A warp takes two rows of W at a time, a lane eight columns of 256; x is in
 // shared memory.  Sums are float32 multiply-adds, rounded to nearest: with a single
 // token's loss there is nothing that an error averages out over, and tiles would
 // have to add every 64 of depth in registers to be as exact, which takes them three

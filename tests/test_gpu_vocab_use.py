@@ -465,6 +465,57 @@ def test_a_captured_training_step(vocab):
         assert torch.equal(loss.detach(), value) and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_two_streams_at_once(vocab):
+    """Eager calls of two streams, each with its own products of pairs, in flight together."""
+    cases = [loss_case(1000, 9000, 256, 0.2, seed=21), loss_case(700, 12_000, 512, 0.1, seed=22)]
+
+    def everything(x, w, ids, c):
+        loss, lse = vocab.cross_entropy(x, w, ids)
+        dx, dw = vocab.cross_entropy_grads(x, w, ids, loss, lse, c)
+        return loss, lse, dx, vocab.embedding_grad(dx, ids, w.shape[0], 2.0, base=dw)
+
+    want = [everything(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cases], [[], []]
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(everything(*cases[i]))
+    torch.cuda.synchronize()
+    for i, w in enumerate(want):
+        assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, w))
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+def test_a_loss_that_is_changed_in_place(vocab, reduction):
+    """As where gradients accumulate over several batches: the backward pass reads nothing of what the caller owns."""
+    x, w, ids, _ = loss_case(90, 200, 64, 0.2, seed=23)
+    leaf = x.clone().requires_grad_(True)
+    (want,) = torch.autograd.grad((vocab.linear_cross_entropy(leaf, w, ids, reduction) * 0.25).sum(), leaf)
+    loss = vocab.linear_cross_entropy(leaf, w, ids, reduction)
+    loss *= 0.25
+    (got,) = torch.autograd.grad(loss.sum(), leaf)
+    assert torch.equal(got, want)
+
+
+def test_smallest_shapes(vocab):
+    from lossless_bf16_tensor_gb300.binding import LctError
+    x, w, ids, _ = loss_case(1, 50, 64, seed=24)
+    whole = vocab.linear_cross_entropy(x, w, ids)
+    leaf = x[0].clone().requires_grad_(True)
+    one = vocab.linear_cross_entropy(leaf, w, ids[0])             # a token without a batch
+    assert one.shape == () and torch.equal(one.detach(), whole)
+    assert torch.autograd.grad(one, leaf)[0].shape == (64,)
+    assert vocab.embedding(ids[0], w).shape == (64,)
+    none = torch.zeros(0, 5, 64, device="cuda", dtype=BF16, requires_grad=True)
+    loss = vocab.linear_cross_entropy(none, w, torch.zeros(0, 5, device="cuda", dtype=torch.long))
+    assert float(loss.detach()) == 0 and torch.autograd.grad(loss, none)[0].shape == (0, 5, 64)
+    with pytest.raises(LctError):                                 # nothing to project: the C call refuses it
+        vocab.cross_entropy(x[:, :0], w[:, :0], ids)
+    with pytest.raises(LctError):
+        vocab.embedding(ids, w[:, :0])
+
+
 # ------------------------------------------------------- pieces, long batches
 
 def test_many_tokens_in_several_products(vocab):
