@@ -563,7 +563,9 @@ lct_status lct_loss_forward(const lct_ids *targets, const uint16_t *d_x, uint64_
  * dW, whatever its x holds; one with an impossible target has dx NaN and adds
  * nothing.  Pieces as in the forward pass (d_dw NULL for all or none); d_dx is
  * written by the last one's call.  Sums are added in an order that depends on the
- * targets alone: the same bits every time.  A wait that ran out makes dx NaN.
+ * targets alone: the same bits every time.  A wait that ran out on the device
+ * leaves LCT_ERR_TIMEOUT in d_work's first word and makes dx NaN, and so the
+ * rows of dW that its piece had not finished by then and those of later pieces.
  * Errors as lct_loss_forward. */
 lct_status lct_loss_backward(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,
                              const uint16_t *d_w, uint64_t ld_w, uint64_t first, uint64_t rows, const float *d_loss,

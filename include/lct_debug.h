@@ -47,7 +47,7 @@ lct_status lct_debug_adapter_backward_timeout(const lct_adapters *bank, const lc
 
 /* lct_loss_forward and lct_loss_backward with kernels whose product warps do
  * nothing: every wait for a product runs out, after about a second in each
- * kernel.  Losses (the backward pass: dx) are NaN and d_work's first word is
+ * kernel.  Losses (the backward pass: dx and dW) are NaN and d_work's first word is
  * LCT_ERR_TIMEOUT; the kernels return normally and the CUDA context stays usable.
  * Errors as for those. */
 lct_status lct_debug_loss_forward_timeout(const lct_ids *targets, const uint16_t *d_x, uint64_t ld_x, uint64_t cols,

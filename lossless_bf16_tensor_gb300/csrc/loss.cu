@@ -61,7 +61,7 @@ struct ProductArgs {
     const float *extra;     // kDw: the targets' sums, row first[v] (-1: none)
     const int32_t *first;
     int64_t ld_extra;
-    __nv_bfloat16 *out;     // kDw, rows at any address
+    __nv_bfloat16 *out;     // kDw, for rows at any address and where a wait ran out
     int64_t ld_out;
     bool boxes;             // the result is written by boxes (maps.c)
     bool stalled;           // a test: no products are made, so that waits run out
@@ -296,6 +296,14 @@ __device__ __forceinline__ void join_columns(const float (&z)[N], float &m, floa
     m = top;
 }
 
+// dW's values of 32 rows by a unit of columns where a wait ran out: no number that could pass for a gradient.
+__device__ __forceinline__ void store_nan(const ProductArgs &g, int row0, int m, int col0)
+{
+    for (int r = row0; r < min(row0 + 32, m); ++r)
+        for (int c = col0 + static_cast<int>(threadIdx.x & 31); c < min(col0 + kUnit, g.n); c += 32)
+            g.out[r * g.ld_out + c] = __ushort_as_bfloat16(0x7FFF);
+}
+
 // Warps by what they do: warp 0 loads boxes (TMA), warp 1 of the first block
 // issues the products, the others turn sums into results, each warp those of a
 // quarter of the rows.  Sums are double-buffered in TMEM, so that a tile's end
@@ -343,6 +351,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         else
             m = min(m, there);
     }
+    // g is not what it should be: no products, and dW says so
+    const bool failed = OP == kDw && *g.status;
     Items items(g, m, k);
     Item w;
     Waiter waiter;
@@ -358,7 +368,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------------------- boxes
         int i = 0;
-        while (items.next(w)) {
+        while (!failed && items.next(w)) {
             const int row = w.tm * kTile + rank * kHalfTile, col = w.tn * kTile + rank * kHalfTile;
             // rows of a second block that has none are not fetched: what is there in their place reaches only itself
             const bool rows = kAcrossA || row < g.m;
@@ -396,7 +406,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const uint64_t a0 = operand(base, kAcrossA ? kOperand / 2 : 0);
         const uint64_t b0 = operand(base + kOperand, kAcrossB ? kOperand / 2 : 0);
         int i = 0, t = 0;
-        while (!g.stalled && items.next(w)) {
+        while (!g.stalled && !failed && items.next(w)) {
             int left = 0;  // steps until these sums are done
             uint32_t sums = tmem;
             bool add = false;
@@ -456,6 +466,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             }
             return r;
         };
+        waiter.dead = failed;
         Item ahead;
         bool more = items.next(ahead);
         RowInfo info = {}, info_ahead = {};
@@ -522,6 +533,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (some) {
                     wait_all(&done[t & 1], (t / 2) & 1);
                     tc_after();
+                }
+                if (OP == kDw && waiter.dead) {
+                    for (int u = group; u < kTile / kUnit; u += kGroups) store_nan(g, row0, m, w.tn * kTile + u * kUnit);
+                    continue;
                 }
                 if (waiter.dead) break;
                 const uint32_t sums = lanes + (t & 1) * kTile;
