@@ -699,8 +699,9 @@ struct LinearCrossEntropy : torch::autograd::Function<LinearCrossEntropy> {
             if (ctx->needs_input_grad(0)) grads[0] = b.dx.view(ctx->saved_data["shape"].toIntVector());
             if (ctx->needs_input_grad(1)) grads[1] = b.dw;
         }
-        // the gradients' own gradients are not there: asking for them raises
-        if (at::GradMode::is_enabled() && (dy[0].requires_grad() || saved[0].requires_grad() || saved[1].requires_grad())) {
+        // The gradients' own gradients are not there: asking for them raises.  They depend on the operands whatever the
+        // saved ones (which may be copies that autograd has not seen) and the upstream say.
+        if (at::GradMode::is_enabled()) {
             torch::autograd::variable_list some;
             for (const at::Tensor &g : grads)
                 if (g.defined()) some.push_back(g.set_requires_grad(true));

@@ -22,6 +22,7 @@ from torch.autograd.function import once_differentiable
 from . import binding as B
 from .calls import calls
 from .matmul import default_tile_blocks, tile_rows
+from .once import once
 
 _BACKWARD, _WEIGHT, _UNALIGNED = 1, 2, 4  # LCT_LOSS_*
 
@@ -196,13 +197,13 @@ class _CompressedCrossEntropy(torch.autograd.Function):
         return _reduced(reduction, loss, total).clone()
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dy):
         x, targets, loss, lse, total = ctx.saved_tensors
         w, cb, rows, cols, reduction, tile_blocks, shape = ctx.rest
-        dloss, scale = _upstream(reduction, dy, total)
-        dx, _ = _compressed_backward(x, w, cb, rows, cols, targets, loss, lse, dloss, scale, False, tile_blocks)
-        return (dx.view(shape),) + (None,) * 7
+        with torch.no_grad():
+            dloss, scale = _upstream(reduction, dy, total)
+            dx, _ = _compressed_backward(x, w, cb, rows, cols, targets, loss, lse, dloss, scale, False, tile_blocks)
+        return once("compressed_cross_entropy", dx.view(shape)) + (None,) * 7
 
 
 def compressed_cross_entropy(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_codebook, rows: int, cols: int,
