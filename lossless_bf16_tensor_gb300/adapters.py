@@ -13,11 +13,11 @@ current stream, and nothing synchronises.
 from __future__ import annotations
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import binding as B
 from .calls import calls
 from .matmul import compressed_linear, compressed_linear_input_grad
+from .once import once
 
 
 class AdapterBank:
@@ -107,7 +107,6 @@ class _AdapterLinear(torch.autograd.Function):
         return out
 
     @staticmethod
-    @once_differentiable  # the gradients' own gradients are not there: asking for them raises
     def backward(ctx, dy):
         x, xa = ctx.saved_tensors
         operands, versions, w, cb, n, k = ctx.rest
@@ -115,10 +114,12 @@ class _AdapterLinear(torch.autograd.Function):
             if then != now:
                 raise RuntimeError("adapter_linear: %s was modified in place between forward and backward "
                                    "(version %s, now %s)" % (name, then, now))
-        dy = dy.contiguous()
-        dx = compressed_linear_input_grad(dy, w, cb, n, k) if ctx.needs_input_grad[0] else None
-        dx, da, db = calls.adapter_grads(*operands, dy, x, xa, dx, dx)
-        return dx, da, db, None, None, None, None
+        with torch.no_grad():
+            dy = dy.contiguous()
+            dx = compressed_linear_input_grad(dy, w, cb, n, k) if ctx.needs_input_grad[0] else None
+            dx, da, db = calls.adapter_grads(*operands, dy, x, xa, dx, dx)
+        # the gradients' own gradients are not there: asking for them raises
+        return once("adapter_linear", dx, da, db) + (None,) * 4
 
 
 def adapter_linear(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_codebook, bank: AdapterBank,
