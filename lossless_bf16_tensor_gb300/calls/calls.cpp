@@ -467,8 +467,11 @@ PyObject *embedding_grad(PyObject *const *a)
     const float scale = static_cast<float>(real(a[3]));
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
     Rows base;
-    if (a[4] != Py_None)
-        base = rows_of(tensor(a[4], "base must be a tensor or None"), cols, vocab, device, "base", dy.scalar_type());
+    if (a[4] != Py_None) {
+        const at::Tensor &b = tensor(a[4], "base must be a tensor or None");
+        no_gradient({&b}, "embedding_grad");
+        base = rows_of(b, cols, vocab, device, "base", dy.scalar_type());
+    }
     at::Tensor fresh;
     if (a[5] == Py_None) fresh = make({static_cast<int64_t>(vocab), static_cast<int64_t>(cols)}, dy.scalar_type(), device);
     const at::Tensor &out = a[5] == Py_None ? fresh : tensor(a[5], "out must be a tensor or None");

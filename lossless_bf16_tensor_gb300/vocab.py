@@ -59,7 +59,8 @@ def embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, rows: int, scale: flo
     """base + scale * (the sum of dy over the tokens of each row), [rows, columns]
     in dy's type: the dense gradient of ``embedding``.  base None is zero.  `out`
     may be base itself, whose rows without tokens are then left alone; by
-    default it is a new tensor."""
+    default it is a new tensor.  Autograd does not see this call: it raises where
+    dy, base or out requires a gradient and gradients are enabled."""
     return calls.embedding_grad(dy, tokens.contiguous(), rows, scale, base, out)
 
 
