@@ -14,6 +14,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
@@ -68,6 +69,29 @@ void wrote(const at::Tensor &t)
 }
 
 void *stream_of(int device) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream(); }
+
+// Forward-mode tangents are gradients that none of the calls gives.
+void no_tangent(std::initializer_list<const at::Tensor *> operands, const char *what)
+{
+    if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return;
+    for (const at::Tensor *t : operands)
+        if (t->_fw_grad(0).defined()) {
+            PyErr_Format(PyExc_RuntimeError, "%s has no forward-mode derivative, but an operand carries a tangent", what);
+            throw Raised{};
+        }
+}
+// Autograd does not see what a call does with these.
+void no_gradient(std::initializer_list<const at::Tensor *> operands, const char *what)
+{
+    if (at::GradMode::is_enabled())
+        for (const at::Tensor *t : operands)
+            if (t->requires_grad()) {
+                PyErr_Format(PyExc_RuntimeError,
+                             "%s gives no gradients, but an operand requires one: call it under torch.no_grad()", what);
+                throw Raised{};
+            }
+    no_tangent(operands, what);
+}
 
 // ---------------------------------------------------------------- gradients
 
@@ -330,6 +354,7 @@ PyObject *adapter_apply(PyObject *const *a)
                                                     "adapter_linear, or call it under torch.no_grad()");
                 throw Raised{};
             }
+    no_tangent({&x, &y, &out, &tensor(a[0], "a"), &tensor(a[1], "b"), &tensor(a[2], "scale")}, "adapter_apply");
     at::Tensor xa;
     if (keep) xa = make({static_cast<int64_t>(plan.tokens), static_cast<int64_t>(bank.rank)}, at::kFloat, device);
     check(lct_adapter_forward(&bank, &plan, xr.p, xr.ld, yr.p, yr.ld, outr.p, outr.ld,
@@ -412,17 +437,6 @@ double real(PyObject *o)
     if (PyErr_Occurred()) throw Raised{};
     return v;
 }
-void no_gradient(std::initializer_list<const at::Tensor *> operands, const char *what)
-{
-    if (!at::GradMode::is_enabled()) return;
-    for (const at::Tensor *t : operands)
-        if (t->requires_grad()) {
-            PyErr_Format(PyExc_RuntimeError,
-                         "%s gives no gradients, but an operand requires one: call it under torch.no_grad()", what);
-            throw Raised{};
-        }
-}
-
 // (ids, table, first, vocab, scale, out or None) -> out; the table's rows are `first` .. of vocab (0: all of them)
 PyObject *embedding(PyObject *const *a)
 {
@@ -444,7 +458,7 @@ PyObject *embedding(PyObject *const *a)
         fresh = make(shape, table.scalar_type(), device);
     }
     const at::Tensor &out = a[5] == Py_None ? fresh : tensor(a[5], "out must be a tensor or None");
-    no_gradient({&table, &out}, "embedding into out");
+    no_gradient({&table, &out}, a[5] == Py_None ? "embedding" : "embedding into out");
     const Rows outr = rows_of(out, cols, ids.tokens, device, "out", table.scalar_type());
     check(lct_embedding(&ids, tr.p, tr.ld, dtype, first, rows, cols, scale, outr.p, outr.ld, stream_of(device)),
           "lct_embedding");
@@ -572,6 +586,7 @@ PyObject *cross_entropy(PyObject *const *a)
 PyObject *cross_entropy_piece(PyObject *const *a)
 {
     const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
+    no_tangent({&x}, "compressed_cross_entropy");
     const LossOperands o = loss_operands(x, w, tensor(a[4], "targets must be a tensor"), a[2], a[3]);
     const at::Tensor &loss = floats(tensor(a[5], "loss must be a tensor"), o.ids.tokens, o.device, "loss");
     const at::Tensor &lse = floats(tensor(a[6], "lse must be a tensor"), o.ids.tokens, o.device, "lse");
@@ -725,6 +740,7 @@ PyObject *linear_cross_entropy(PyObject *const *a)
     const at::Tensor &x = tensor(a[0], "x must be a tensor"), &w = tensor(a[1], "weight must be a tensor");
     const at::Tensor &targets = tensor(a[2], "targets must be a tensor");
     const int reduction = static_cast<int>(number(a[3]));
+    no_tangent({&x, &w}, "linear_cross_entropy");
     need(w.dim() == 2 && x.dim() >= 1 && x.size(x.dim() - 1) == w.size(1), "expected x [..., columns] and weight [vocabulary, columns]");
     if (at::GradMode::is_enabled() && (x.requires_grad() || w.requires_grad()))
         return THPVariable_Wrap(LinearCrossEntropy::apply(x, w, targets, static_cast<int64_t>(reduction)));

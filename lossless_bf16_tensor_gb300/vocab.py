@@ -10,7 +10,8 @@ vocabulary, both with gradients, for dense and for compressed matrices.
     dx, dw = compressed_cross_entropy_grads(...)                       # dw: the dense gradient of the fused steps
 
 A negative id is none: a row of zeros, a loss of 0, no gradients, not counted in
-the mean.  An id of the vocabulary's size or more gives NaN.  Only orchestration
+the mean.  An id of the vocabulary's size or more gives NaN.  Forward-mode
+derivatives are not there: operands that carry a tangent are refused.  Only orchestration
 lives here: everything runs in liblct's kernels, on the current stream, and
 nothing synchronises.
 """
