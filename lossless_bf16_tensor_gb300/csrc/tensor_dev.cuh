@@ -202,12 +202,19 @@ struct Waiter {
 
 }  // namespace dev
 
+// What a kernel may have of dynamic shared memory, asked for before a launch that takes more than 32 KB.  It is a
+// property of the kernel and not of the launch: where the sizes of a call choose how much is taken, another thread's
+// smaller launch in between would lower it again.  So it is the same for all of them.  (Static shared memory, here
+// below 10 KB, comes on top.)
+constexpr uint32_t kSharedMost = 200 * 1024;
+
 template <bool DEPENDENT = false, typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), dim3 grid, uint32_t threads, uint32_t smem, uint32_t cluster, cudaStream_t s,
                    A... args)
 {
     if (smem > 32 * 1024) {  // above what every kernel may have
-        const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    smem < kSharedMost ? kSharedMost : smem);
         if (rc != cudaSuccess) return rc;
     }
     cudaLaunchConfig_t cfg = {};
