@@ -529,7 +529,13 @@ lct_status lct_embedding_grad(const lct_ids *ids, const void *d_dy, uint64_t ld_
 
 /* Bytes of scratch (256-byte aligned) of the two calls below for pieces of at
  * most `rows` rows of the vocabulary: one piece (rows = vocab), or several.  0 for
- * sizes that the calls refuse. */
+ * sizes that the calls refuse.  The forward pass takes at most 256 MB and a few
+ * words a token; the backward pass, for g and for dx's sums, at most 256 MB each
+ * (512 bytes a token, or as much as a float32 dx, where that is more), a copy of
+ * x, and with the weight's gradient another in float32 and a word for each row of
+ * the vocabulary.  Neither grows with tokens times vocab.  Rows that have
+ * to be copied to 16-byte boundaries add a copy of x (forward) and 128 MB or 256
+ * rows of the weight; several pieces one of the targets' rows. */
 uint64_t lct_loss_work_bytes(uint64_t tokens, uint64_t vocab, uint64_t cols, uint64_t rows, int32_t flags);
 
 /* The cross entropy of a projection onto the vocabulary, which keeps no logits:

@@ -1062,15 +1062,19 @@ cudaError_t pack(const PackArgs &g, bool aligned, cudaStream_t s)
                    : launch<true>(dev::k_loss_pack<false>, grid, threads, 0, 1, s, g);
 }
 
-// The values of g that are there at a time: 256 MB.
+// The values of g that are there at a time: 256 MB (above 2^19 tokens, which pass that with 256 columns: 256 columns).
 constexpr uint64_t kGradValues = 1ull << 27;
 constexpr uint64_t kPackValues = 1ull << 26;  // of W, where its rows have to be moved to 16-byte boundaries
-constexpr int64_t kMergeChunk = 32768;        // tokens of one product of the forward pass
+// The tiles' maxima and sums, 8 bytes a token and 64 columns, within 256 MB: of so many tokens at most, fewer where the
+// vocabulary is large (262,144 rows: 8192), but at no fewer than 2048, with fewer rows at a time (above 2^20) instead: each
+// product of the forward pass reads its part of W once.
+constexpr uint64_t kMergeChunk = 32768, kMergeLeast = 2048, kMergeParts = 1ull << 25;
 
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
 // Parts of the depth of dx's product, at most, so that few tokens still give every pair work (parts_of chooses): within
-// 256 MB.
+// 256 MB, where one of float32 [tokens, cols] is not more.  They are reserved whatever parts_of, which knows the
+// tokens that have a target, will use (1000 x 10,007 x 1024: 64 of 4 MB, of which 4 to 10 are).
 int dx_splits(uint64_t tokens, uint64_t cols)
 {
     const uint64_t room = (1ull << 28) / std::max<uint64_t>(1, 4 * tokens * up(cols, 8));
@@ -1094,8 +1098,13 @@ struct ForwardLayout : Layout {
     ForwardLayout(uint64_t tokens, uint64_t cols, uint64_t rows, bool move)
     {
         ld = up(cols, 64);  // whole lines of 128 bytes: boxes of others touch two
-        chunk = std::min<uint64_t>(tokens, kMergeChunk);
         piece = move ? std::min(rows, std::max<uint64_t>(256, kPackValues / ld / 256 * 256)) : rows;
+        chunk = std::min(tokens, kMergeChunk);
+        const auto units_of = [](uint64_t n) { return up(n, dev::kUnit) / dev::kUnit; };
+        if (chunk * units_of(piece) > kMergeParts) {
+            chunk = std::min(chunk, std::max(kMergeLeast, kMergeParts / units_of(piece) / 256 * 256));
+            piece = std::min(piece, kMergeParts / chunk * dev::kUnit / 256 * 256);
+        }
         const uint64_t blocks = up(tokens, dev::kMergeTokens) / dev::kMergeTokens;
         head = take(16);
         state = take(8 * tokens);
@@ -1103,7 +1112,7 @@ struct ForwardLayout : Layout {
         sums = take(8 * blocks);
         counts = take(4 * blocks);
         x = take(move ? 2 * tokens * ld : 0);
-        const uint64_t units = up(piece, dev::kUnit) / dev::kUnit;
+        const uint64_t units = units_of(piece);
         part = take(8 * chunk * (is_few(tokens, cols) ? std::max<uint64_t>(units, few_blocks(piece)) : units));
         w = take(move ? 2 * piece * ld : 0);
     }
