@@ -11,15 +11,25 @@
 // tiles and pieces: what leaves the SMs is 8 bytes a token and 64 columns.  The
 // second computes z again and writes g as BF16, for a part of the piece that is
 // bounded (kGradValues), which the other two read.  Tensor cores bound all of them
-// where tokens are many (8192 tokens, 32,768 rows of 4096: z 1.1 ms, 2.0 PFLOP/s,
-// 97% of the tensor pipe's cycles; the gradients 3.6 to 3.8 ms); where they are few,
-// reading W from HBM does.
+// where tokens are many (8192 tokens, 32,768 rows of 4096, in calls: z 1.19 to 1.23 ms,
+// 1.8 PFLOP/s, 97% of the tensor pipe's cycles; the gradients 3.8 to 4.1 ms); where they
+// are few, reading W from HBM does.
 //
 // Rounding: products take BF16 and add in float32.  g is rounded to BF16 without
 // its target's entry: that one, c_i (exp(-loss_i) - 1), is as large as all others
 // of its row together, and goes into dx and dW in float32 (dx: in k_loss_finish;
 // dW: sums over the tokens of one target, k_segments, added as dW's tile is
-// written), so that both are rounded once.
+// written), so that both are rounded once.  What g's rounding leaves: rows of dW
+// that are nobody's target are 2.3e-3 off (2-norm; 1.66e-3 with one rounding), all
+// others and dx 1.66e-3.  g in float32 would double what its products read, each of which
+// would become several, of BF16 parts.
+//
+// The logits of the backward pass are summed over the whole depth by the tensor
+// cores, which drop what does not fit, towards zero (sum_steps says what the forward
+// pass does against that).  g comes out smaller by the same share for all of a row but
+// its target: 1e-4 of it for logits of 12 and 4e-4 of 50, 4096 deep, below the 1.7e-3
+// of its rounding; as much as that only for logits of 200 at 4096 or 50 at 16,384 (2.2e-3
+// and 1.2e-3).
 //
 // Tokens without a target are left out of the gradients' products: the others are
 // packed in the order of their targets, which the sums over a target's tokens
@@ -358,6 +368,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     Waiter waiter;
     // Barriers tell of boxes, products and reads of TMEM that are done, and of no ordinary write: waits order nothing beyond
     // the block, and arrivals at a peer's barrier nothing at all (a release would wait for the results on their way to memory).
+    // Sums that are handed back are in registers by then: tcgen05.wait::ld comes before the arrival, and a fence between.
     auto wait = [&](uint64_t *bar, int parity) { waiter.wait(bar, parity); };
     // where the lanes have to give up together (a vote a step would cost the product's warp 3%)
     auto wait_all = [&](uint64_t *bar, int parity) {

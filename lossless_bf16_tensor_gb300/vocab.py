@@ -79,9 +79,9 @@ def _rows(x, k):
 def cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor):
     """(loss, lse), float32 in the shape of the targets: lse = log sum_v exp(x W_v)
     and loss = lse - x W_target (0 without a target).  x [..., k] and weight
-    [vocabulary, k] in BF16, rows at any stride; targets int32 or int64.  Keeps no
-    logits.  Autograd does not see this call (``linear_cross_entropy`` gives
-    gradients)."""
+    [vocabulary, k] in BF16, rows at any one stride; targets int32 or int64,
+    contiguous.  Keeps no logits.  Autograd does not see this call
+    (``linear_cross_entropy`` gives gradients, and takes operands at any strides)."""
     return calls.cross_entropy(x, weight, targets)
 
 
@@ -212,9 +212,10 @@ def compressed_cross_entropy(x: torch.Tensor, w: B.CompressedTensor, cb: B.lct_c
                              targets: torch.Tensor, reduction: str = "mean",
                              tile_blocks: int | None = None) -> torch.Tensor:
     """``linear_cross_entropy`` on a compressed weight [rows, cols], which is
-    decoded a piece at a time (and again in backward): neither the dense weight
-    nor the logits are ever there.  Differentiable (once) in x; the weight is
-    frozen (``compressed_cross_entropy_grads`` gives its gradient)."""
+    decoded a piece at a time (and again in backward, until when it has to stay as
+    it is): neither the dense weight nor the logits are ever there.  Differentiable
+    (once) in x; the weight is frozen (``compressed_cross_entropy_grads`` gives its
+    gradient)."""
     _reduction(reduction)
     targets = targets.contiguous()
     if torch.is_grad_enabled() and x.requires_grad:
