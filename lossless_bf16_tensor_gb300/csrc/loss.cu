@@ -1112,10 +1112,11 @@ struct ForwardLayout : Layout {
         piece = move ? std::min(rows, std::max<uint64_t>(256, kPackValues / ld / 256 * 256)) : rows;
         chunk = std::min(tokens, kMergeChunk);
         const auto units_of = [](uint64_t n) { return up(n, dev::kUnit) / dev::kUnit; };
-        if (chunk * units_of(piece) > kMergeParts) {
+        // (what is reserved does not fall where rows grow: a smaller piece has to find room in a larger one's)
+        const uint64_t parts = std::min(kMergeParts, chunk * units_of(piece));
+        if (chunk * units_of(piece) > kMergeParts)
             chunk = std::min(chunk, std::max(kMergeLeast, kMergeParts / units_of(piece) / 256 * 256));
-            piece = std::min(piece, kMergeParts / chunk * dev::kUnit / 256 * 256);
-        }
+        if (chunk * units_of(piece) > kMergeParts) piece = kMergeParts / chunk * dev::kUnit / 256 * 256;
         const uint64_t blocks = up(tokens, dev::kMergeTokens) / dev::kMergeTokens;
         head = take(16);
         state = take(8 * tokens);
@@ -1123,8 +1124,7 @@ struct ForwardLayout : Layout {
         sums = take(8 * blocks);
         counts = take(4 * blocks);
         x = take(move ? 2 * tokens * ld : 0);
-        const uint64_t units = units_of(piece);
-        part = take(8 * chunk * (is_few(tokens, cols) ? std::max<uint64_t>(units, few_blocks(piece)) : units));
+        part = take(8 * (is_few(tokens, cols) ? std::max(parts, chunk * few_blocks(piece)) : parts));
         w = take(move ? 2 * piece * ld : 0);
     }
 };

@@ -46,3 +46,20 @@ def test_parts_of_tokens_and_rows(vocab, t, v):
         for some in (slice(0, 8192), slice(8192, t), slice(4000, 5000 + 1024)):
             one = vocab.cross_entropy(x[some], w, ids[some])
             assert torch.equal(one[0], loss[some]) and torch.equal(one[1], lse[some])
+
+
+def test_a_smaller_last_piece(vocab):
+    """Scratch for the first of two pieces is enough for the second, whose 64 rows less let more tokens be done at a time."""
+    t, k, first, rest = 9000, 8, 262_208, 262_144
+    v = first + rest
+    x, w, ids, _ = loss_case(t, v, k, 0.1, seed=81)
+    want = vocab.cross_entropy(x, w, ids)
+    work = torch.empty(vocab.calls.loss_work_bytes(t, v, k, first, 0), dtype=torch.uint8, device="cuda")
+    loss, lse, total = (torch.zeros(n, device="cuda") for n in (t, t, 3))
+    vocab.calls.cross_entropy_piece(x, w[:first], 0, v, ids, loss, lse, total, work)
+    vocab.calls.cross_entropy_piece(x, w[first:], first, v, ids, loss, lse, total, work)
+    # the same products; exponentials and sums, joined in another order, are off as in the test above, here on both sides
+    off = 2 * (2.0 ** -20 + 2.0 ** -22 * 2 * want[1].abs())
+    assert ((lse - want[1]).abs() <= off).all()
+    assert ((loss - want[0]).abs() <= off + 2.0 ** -22 * want[0].abs()).all()
+    assert torch.equal(loss[ids < 0], want[0][ids < 0])

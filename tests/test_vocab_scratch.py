@@ -1,5 +1,5 @@
 """What the loss's scratch is bounded by (no GPU)."""
-
+import random
 import pytest
 
 from test_vocab_abi import UNSUPPORTED, backward, forward, gradient, lib, lookup  # noqa: F401
@@ -43,3 +43,17 @@ def test_columns_beyond_the_limit(lib):  # noqa: F811
     assert gradient(lib, cols=wide, ldd=2 ** 17, ldo=2 ** 17) == UNSUPPORTED
     assert forward(lib, cols=wide, ldx=2 ** 17, ldw=2 ** 17) == UNSUPPORTED
     assert backward(lib, cols=wide, ldx=2 ** 17, ldw=2 ** 17, ldd=2 ** 17, lddw=2 ** 17) == UNSUPPORTED
+
+
+def test_forward_of_smaller_pieces(lib):  # noqa: F811
+    """Scratch for pieces of at most some rows is enough for every smaller one: the last of a matrix is."""
+    rng = random.Random(1)
+    v = 2 ** 24
+    for t in (1, 2, 777, 2048, 2500, 10_000, 32_768, 100_000):
+        for _ in range(300):
+            rows = int(2 ** rng.uniform(0, 24))
+            less = rng.choice([rows - 1, rows - 64, rows - 256, rows // 2, rng.randint(1, rows), rows // 64 * 64])
+            if less < 1:
+                continue
+            for flags in (0, 4):
+                assert lib.lct_loss_work_bytes(t, v, 64, less, flags) <= lib.lct_loss_work_bytes(t, v, 64, rows, flags), (t, rows, less)
