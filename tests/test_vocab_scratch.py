@@ -1,5 +1,6 @@
 """What the loss's scratch is bounded by (no GPU)."""
 import random
+
 import pytest
 
 from test_vocab_abi import UNSUPPORTED, backward, forward, gradient, lib, lookup  # noqa: F401
